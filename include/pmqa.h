@@ -360,6 +360,129 @@ int pmqa_sparse_mla_merge(const void *outs, const float *lses, int32_t parts, in
                           int32_t heads, void *out, float *lse, pmqa_stream_t stream);
 
 /*
+ * A paged K/V cache held in 8 bits, and four operators on it: append a step's
+ * new tokens, attend to the cached ones, add up the attention weight that each
+ * cached token received, and keep the tokens with the most of it in fewer
+ * blocks. It serves the layers (or models) that keep ordinary keys and values
+ * beside the indexed latent cache of the sparse layers; the source pages have no
+ * counterpart.
+ *
+ *   k_cache, v_cache  fp8 e4m3fn [num_blocks, kv_heads, block_size, head_dim],
+ *                 contiguous, 16-byte aligned: a block holds block_size
+ *                 consecutive tokens of one request
+ *   k_scale, v_scale  fp32 [num_blocks, kv_heads]: one scale per block and head;
+ *                 a cached value is its code times its scale
+ *   block_tables  int32 [bs, max_blocks_per_seq], row-major; only the first
+ *                 ceil(ctx_i / block_size) entries of row i are read
+ *   context_lens  int32 [bs]: ctx_i, tokens of request i, this call's new ones
+ *                 included
+ *   row_begin     int32 [bs + 1], not decreasing, within [0, rows]: request i
+ *                 has the n_i = row_begin[i + 1] - row_begin[i] <= max_rows rows
+ *                 from row_begin[i] on; its row j sits at slot
+ *                 ctx_i - n_i + j and sees the slots t <= ctx_i - n_i + j.
+ *                 Rows of no request are neither read nor written. Unused by
+ *                 pmqa_cache_evict (as are rows and max_rows).
+ * head_dim must be 64 or 128, block_size at most 1024, kv_heads at most 65535
+ * (PMQA_ERR_UNSUPPORTED otherwise). A context outside [0, block_size *
+ * max_blocks_per_seq], or rows that break the rules above, are clamped and set
+ * PMQA_DEV_BAD_CONTEXT; a table entry outside [0, num_blocks) sets
+ * PMQA_DEV_BAD_BLOCK_ID, and its tokens are left out (not written by append,
+ * not attended to or weighed, zeros where evict would have moved them).
+ *
+ * Every call takes a workspace of pmqa_cache_workspace_bytes() bytes, 256-byte
+ * aligned, its status word zero before the first use (pmqa_workspace_init).
+ */
+typedef struct pmqa_cache_problem {
+    void *k_cache;
+    void *v_cache;
+    float *k_scale;
+    float *v_scale;
+    const int32_t *block_tables;
+    const int32_t *context_lens;
+    const int32_t *row_begin;
+    int32_t bs;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t block_size;
+    int32_t max_blocks_per_seq;
+    int32_t rows;
+    int32_t max_rows;
+    int64_t num_blocks;
+} pmqa_cache_problem;
+
+/* About 17 MB, whatever the problem. */
+size_t pmqa_cache_workspace_bytes(void);
+
+/*
+ * Quantise a call's new tokens into their blocks. k, v: bf16 [rows, kv_heads,
+ * head_dim], 16-byte aligned, already rotated where the model rotates. With
+ * e(a) = 2^ceil(log2(a / 448)), at least 2^-100, the new scale of a touched
+ * block and head (keys and values apart) is
+ *   s' = max(s, e(a)) if the block holds earlier tokens of the request, else e(a),
+ * a the largest finite |value| the call writes there; where s' != s the earlier
+ * codes c become rne(c s / s'), and a new value x is stored as rne(x / s'),
+ * saturated at 448 (NaN stays NaN). Slots behind ctx_i and blocks without a new
+ * token are left as they were. A block that receives tokens must belong to one
+ * request only. New rows whose slot would be negative (n_i > ctx_i) are dropped
+ * and set PMQA_DEV_BAD_CONTEXT. One kernel launch.
+ */
+int pmqa_cache_append(const pmqa_cache_problem *p, const void *k, const void *v, void *ws,
+                      size_t ws_bytes, pmqa_stream_t stream);
+
+/*
+ * Attention of every row to the slots that it sees, query head hq with kv head
+ * h = hq / (heads / kv_heads):
+ *   s_t = sm_scale * q . k_t,  out = sum_t softmax(s)_t v_t,  lse = ln sum_t exp(s_t)
+ *   q    bf16 [rows, heads, head_dim], 16-byte aligned
+ *   out  bf16 [rows, heads, head_dim], 16-byte aligned
+ *   lse  fp32 [rows, heads] or NULL
+ * heads must be a multiple of kv_heads, at most 128 times kv_heads, and
+ * max_rows * heads < 2^31. A row that sees no slot gives out = 0 and lse = -inf.
+ * sm_scale must be finite.
+ */
+int pmqa_cache_attention(const pmqa_cache_problem *p, const void *q, int32_t heads, float sm_scale,
+                         void *out, float *lse, void *ws, size_t ws_bytes, pmqa_stream_t stream);
+
+/*
+ * The weight each cached token received: for t < ctx_i (and t < mass_width)
+ *   mass_out[i][h][t] = mass_in[i][h][t] + sum of exp(sm_scale * q_(j,hq) . k_t - lse[j][hq])
+ * over request i's rows j that see t and the query heads hq of kv head h; other
+ * entries are not written. q, heads and sm_scale as in the attention call whose
+ * lse this is; v_cache and v_scale are not read and may be NULL.
+ *   mass_in   fp32 [bs, kv_heads, mass_width] or NULL (zeros); may be mass_out
+ *   mass_out  fp32 [bs, kv_heads, mass_width]
+ */
+int pmqa_cache_weigh(const pmqa_cache_problem *p, const void *q, int32_t heads, float sm_scale,
+                     const float *lse, const float *mass_in, float *mass_out, int64_t mass_width,
+                     void *ws, size_t ws_bytes, pmqa_stream_t stream);
+
+/*
+ * Keep min(ctx_i, keep) tokens of every request and kv head, each head its own,
+ * in new blocks. A request with ctx_i <= keep keeps all; otherwise its first
+ * `sinks` and last `recent` tokens stay, and of those between, the
+ * keep - sinks - recent with the largest mass (equal masses: the lower slot;
+ * NaN lowest). Their order is kept, so token n of the new context is slot
+ * kept[i][h][n] of the old one.
+ *   mass        fp32 [bs, kv_heads, mass_width]; ctx_i must not exceed mass_width
+ *   new_tables  int32 [bs, new_blocks_per_seq], new_blocks_per_seq * block_size >=
+ *               keep: the blocks that receive the kept tokens, in the same pools;
+ *               the first ceil(min(ctx_i, keep) / block_size) of row i are used.
+ *               None of them may be in use by block_tables or listed twice
+ *   kept        int32 [bs, kv_heads, keep]: old slots in rising order, then -1
+ *   lens_out    int32 [bs]: min(ctx_i, keep); not context_lens itself
+ *   mass_out    fp32 [bs, kv_heads, mass_width] or NULL: the kept tokens' masses,
+ *               then zeros; must not overlap mass
+ * A new block's scale is e(largest |code * scale| moved there) (see append), its
+ * codes rounded to it; slots past the new length are left as they were. Masks by
+ * slot keep their meaning after it: a request's last `recent` tokens are still
+ * its last. sinks + recent <= keep. Two kernel launches.
+ */
+int pmqa_cache_evict(const pmqa_cache_problem *p, const float *mass, int64_t mass_width, int32_t keep,
+                     int32_t sinks, int32_t recent, const int32_t *new_tables,
+                     int32_t new_blocks_per_seq, int32_t *kept, int32_t *lens_out, float *mass_out,
+                     void *ws, size_t ws_bytes, pmqa_stream_t stream);
+
+/*
  * Measurement aid beside the decode path (computes nothing of the method): reads
  * the rows rows[0..n) of a pool of fixed-pitch rows, each as its 16-byte aligned
  * window (144 bytes for row_pitch 132, the token row of the KV cache; 576 bytes

@@ -1,8 +1,9 @@
 """Build libpmqa.so in-tree with nvcc for sm_103a (GB300).
 
-Twelve translation units compile in parallel (the C ABI, the allocation-free
-entry point, the sparse MLA decode, the row-gather probe, and the decode and the
-prefill kernel once per supported head count) and link into one shared library
+The translation units compile in parallel (the C ABI, the allocation-free
+entry point, the sparse MLA decode, the operators on the 8-bit K/V cache, the
+row-gather probe, and the decode and the prefill kernel once per supported head
+count) and link into one shared library
 with the CUDA runtime linked statically, so the library loads on a machine
 without a GPU too.
 """
@@ -36,6 +37,8 @@ def _sources():
              ("pmqa_noalloc", os.path.join(CSRC, "pmqa_noalloc.cu"), []),
              ("pmqa_mla", os.path.join(CSRC, "pmqa_mla.cu"), []),
              ("pmqa_gather_probe", os.path.join(CSRC, "pmqa_gather_probe.cu"), [])]
+    for name in ("", "_append", "_attn", "_weigh", "_evict"):
+        units.append((f"pmqa_cache{name}", os.path.join(CSRC, f"pmqa_cache{name}.cu"), []))
     for h in HEADS:
         units.append((f"pmqa_main_h{h}", os.path.join(CSRC, "pmqa_main_inst.cu"),
                       [f"-DPMQA_HEADS={h}"]))

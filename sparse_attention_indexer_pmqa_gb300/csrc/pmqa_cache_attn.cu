@@ -1,0 +1,631 @@
+// pmqa_cache_attn.cu -- attention over the paged 8-bit K/V cache for requests
+// with few query rows (decode, speculative verify), and the kernel that joins
+// split contexts.
+//
+// For query row j of request i and query head hq (kv head h = hq / group):
+//   x_t = sm_scale log2(e) ks_t (q . K_t),  p_t = 2^(x_t - m),  l = sum p_t,
+//   out = sum_t p_t vs_t V_t / l,           lse = (m + log2 l) ln 2,
+// one pass over the tokens with a running m (a row's maximum, moved only when a
+// token exceeds it by more than 2^8).
+//
+// Bound by HBM: each token and kv head costs 2 D bytes and 4 D flops per query
+// row, so with R rows per kv head the arithmetic is 2 R flops a byte; at R <=
+// 32 that is far below the ridge. The layout follows from that:
+//   * the items (request, kv head, block of 8 NT rows, tile of 64 tokens) are
+//     flattened and split evenly over the CTAs, so contexts of any mix of
+//     lengths finish together; a context cut between CTAs leaves (O, m, l)
+//     parts in the workspace and the second kernel joins them;
+//   * every warp takes 16 of a tile's 64 tokens through its own ring of
+//     cp.async stages and never waits for another warp inside a context;
+//   * products run as S^T = K Q^T and O^T = V^T P^T, so the 16 rows of the
+//     m16n8k16 shape are tokens (then value columns) and the 8 columns are
+//     query rows: a group of 8 wastes nothing, the softmax weights of a thread
+//     stay in its registers (one movmatrix makes the second product's
+//     operand), and O costs 32 registers per 8 rows at D = 128;
+//   * e4m3 to f16 is exact; q is scaled by a power of two per row so that its
+//     largest value lies in [2^14, 2^15) (bf16 values within 2^-31 of it
+//     exactly representable in f16); p is rounded to f16 (2^-12 relative), the
+//     only rounding before the bf16 output; sums, m, l and O are fp32.
+#include <algorithm>
+#include <cmath>
+
+#include "pmqa_cache_host.cuh"
+
+namespace pmqa {
+namespace cache {
+
+constexpr int kAttnWarps = 4;
+constexpr int kAttnThreads = 32 * kAttnWarps;
+constexpr int kWarpTokens = 16;
+constexpr int kAttnTile = kAttnWarps * kWarpTokens;
+constexpr float kSlack = 8.0f;    // p <= 2^8 before the maximum moves
+constexpr int kLeastTiles = 2;    // fewest tiles a CTA takes (small problems)
+
+struct AttnArgs {
+    View c;
+    const uint16_t *q;   // bf16 [rows, heads, D]
+    uint16_t *out;       // bf16 [rows, heads, D]
+    float *lse;          // [rows, heads] or null
+    float scale_log2;    // sm_scale log2(e)
+    int heads, group;
+    int least, most;     // requests with least <= n group <= most are this kernel's
+    int4 *meta;          // per CTA: (i, h, b, 2 parts + (slot & 1)) of the context it leaves open
+    float *ml;           // [2 CTAs][8 NT][2]
+    float *part;         // [2 CTAs][8 NT][D]
+};
+
+// A warp's stage: 16 K rows, 16 V rows, 16 + 16 scales, the mask of tokens
+// that exist. 16-byte chunk c of row r is stored at a place that spreads both
+// access patterns (8 tokens x 4 chunks for K, 4 tokens x 2 chunks for V) over
+// all banks.
+template <int D>
+struct Stage {
+    static constexpr uint32_t kRows = kWarpTokens * D;
+    static constexpr uint32_t kOffKs = 2 * kRows, kOffVs = kOffKs + 64, kOffMask = kOffVs + 64;
+    static constexpr uint32_t kBytes = kOffMask + 16;
+    __device__ static __forceinline__ uint32_t at(int r, int c)
+    {
+        if constexpr (D == 128)
+            return (uint32_t)(r * 128 + ((c ^ ((((r >> 1) & 3) << 1) ^ ((r & 1) << 2))) << 4));
+        else
+            return (uint32_t)((r >> 1) * 128 + (((((r & 1) << 2) | c) ^ (((r >> 1) & 3) << 1)) << 4));
+    }
+};
+
+template <int D, int NT>
+struct AttnShape {
+    static constexpr int kStages = 3;
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kPitch = D + 4;  // floats per row of the merge buffer
+    static constexpr uint32_t kRing = kAttnWarps * kStages * Stage<D>::kBytes;
+    static constexpr uint32_t kOffMerge = kRing;
+    static constexpr uint32_t kOffMl = kOffMerge + kAttnWarps * 8 * kPitch * 4;
+    static constexpr uint32_t kSmem = kOffMl + kAttnWarps * kRows * 8;
+    static constexpr int kOcc = NT == 1 ? 3 : NT == 2 ? 3 : 2;
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
+    cache_attn_kernel(const __grid_constant__ AttnArgs a)
+{
+    using Sh = AttnShape<D, NT>;
+    using St = Stage<D>;
+    constexpr int S = Sh::kStages;
+    constexpr int ROWS = Sh::kRows;
+    constexpr int KS = D / 16;   // k steps of the first product
+    constexpr int MT = D / 16;   // 16-column tiles of the second
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+    const View &c = a.c;
+    const int G = a.group;
+    griddep_launch_dependents();
+
+    Range rg;
+    Walk w;
+    find_range<kAttnTile, ROWS, kAttnThreads>(c, G, a.least, a.most, kLeastTiles, rg, w);
+    if (rg.x0 >= rg.x1) {
+        if (tid == 0)
+            a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+        return;
+    }
+    const long long n_items = rg.x1 - rg.x0;
+    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * S) * St::kBytes;
+    float *const merge = reinterpret_cast<float *>(smem + Sh::kOffMerge);
+    float2 *const mls = reinterpret_cast<float2 *>(smem + Sh::kOffMl);
+
+    // tokens of request q that some row of row block b sees
+    auto seen_end = [&](const Request &q, int b) {
+        const int last = min(q.n - 1, (b * ROWS + ROWS - 1) / G);
+        return max(0, q.ctx - q.n + last + 1);
+    };
+
+    // ---------------------------------------------------------- producer state
+    // `pw` is the item whose table entry is loaded (pend_*); its copies are
+    // issued one step later.
+    Walk pw = w;
+    long long p_left = n_items;  // items not yet looked up
+    int pend_page = -1, pend_tok = 0, pend_h = 0;
+    bool pend_in = false;        // this lane's token is one that a row sees
+    auto look_up = [&]() {
+        pend_in = false;
+        if (p_left > 0) {
+            pend_tok = pw.t * kAttnTile + warp * kWarpTokens + (lane & 15);
+            pend_h = pw.h;
+            pend_in = pend_tok < seen_end(pw.q, pw.b);
+            if (pend_in)
+                pend_page = __ldg(c.bt + (long long)pw.i * c.W + c.page_of(pend_tok));
+            --p_left;
+            if (p_left > 0)
+                pw.template next<kAttnTile, ROWS>(c, G, a.least, a.most);
+        }
+    };
+    int p_slot = 0;
+    auto issue = [&]() {
+        const uint32_t st = ring + (uint32_t)p_slot * St::kBytes;
+        if (++p_slot == S)
+            p_slot = 0;
+        bool ok = pend_in;
+        if (ok && (pend_page < 0 || (long long)pend_page >= c.nb)) {
+            atomicOr(c.status, (uint32_t)PMQA_DEV_BAD_BLOCK_ID);
+            ok = false;
+        }
+        const uint32_t mask = __ballot_sync(kFull, ok) & 0xFFFFu;
+        if (lane == 0)
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(st + St::kOffMask), "r"(mask) : "memory");
+        if (mask) {
+            const long long phys = ok ? (long long)pend_page * c.H + pend_h : 0;
+            const long long row = ok ? (phys * c.P + (pend_tok - c.page_of(pend_tok) * c.P)) * D : 0;
+            const uint32_t sdst = st + (lane < 16 ? St::kOffKs : St::kOffVs) + (uint32_t)(lane & 15) * 4u;
+            if (ok)
+                cp_async_4(sdst, (lane < 16 ? c.ks : c.vs) + phys);
+            else
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(sdst), "r"(0) : "memory");
+            constexpr int CH = D / 16, PER = 32 / CH;  // chunks a row, rows an instruction
+            const int ch = lane % CH;
+#pragma unroll
+            for (int k = 0; k < kWarpTokens / PER; ++k) {
+                const int r = k * PER + lane / CH;
+                const long long src = __shfl_sync(kFull, row, r) + ch * 16;
+                const uint32_t nb = (mask >> r) & 1u ? 16u : 0u;
+                cp_async_16(st + St::at(r, ch), c.k + src, nb);
+                cp_async_16(st + St::kRows + St::at(r, ch), c.v + src, nb);
+            }
+        }
+        cp_async_commit();
+    };
+
+    look_up();
+#pragma unroll 1
+    for (int s = 0; s < S - 1; ++s) {
+        issue();
+        look_up();
+    }
+
+    // ---------------------------------------------------------- consumer state
+    float acc[NT][MT][4];
+    uint32_t qb[NT][KS][2];
+    float m[NT][2], l[NT][2], rc[NT][2];
+    int lim[NT][2];               // last slot that the row sees, -1 for padding
+    float vref = 0.0f, vinv = 0.0f, vtop = 0.0f;
+    int seg = -1, end = 0, c_slot = 0;
+    long long x = rg.x0;
+    int4 open = make_int4(0, 0, 0, 0);
+    bool fresh = true;
+#pragma unroll 1
+    for (;;) {
+        if (fresh) {
+            fresh = false;
+            ++seg;
+            end = seen_end(w.q, w.b);
+            vref = vinv = vtop = 0.0f;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                // this thread's part of query row g of the block: 16 dims of each 64
+                const int R = w.b * ROWS + nt * 8 + g;
+                const bool has = R < w.q.n * G;
+                const uint16_t *src =
+                    a.q + ((long long)(w.q.r0 + R / G) * a.heads + w.h * G + R % G) * D + 16 * t4;
+                uint4 u[D / 32];
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k)
+                    u[k] = has ? __ldg(reinterpret_cast<const uint4 *>(src + (k >> 1) * 64 + (k & 1) * 8))
+                               : make_uint4(0, 0, 0, 0);
+                float top = 0.0f;
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k) {
+                    const uint32_t e[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+#pragma unroll
+                    for (int z = 0; z < 4; ++z)
+                        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(e[z] << 16)),
+                                               fabsf(__uint_as_float(e[z] & 0xFFFF0000u))));
+                }
+                top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+                const int e2 = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 120);
+                const float up = __uint_as_float((uint32_t)(14 - e2 + 127) << 23);
+                const float down = __uint_as_float((uint32_t)(e2 - 14 + 127) << 23);
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k) {
+                    const uint32_t e[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        // dims 8 (k & 1) + 2 z of this thread's 16: k step (k >> 1) * 4 + (k & 1) * 2 + z / 2
+                        const float lo = __uint_as_float(e[z] << 16) * up;
+                        const float hi = __uint_as_float(e[z] & 0xFFFF0000u) * up;
+                        qb[nt][(k >> 1) * 4 + (k & 1) * 2 + (z >> 1)][z & 1] = pack_f16x2(lo, hi);
+                    }
+                }
+                const float mine = a.scale_log2 * down;
+                rc[nt][0] = __shfl_sync(kFull, mine, 8 * t4);
+                rc[nt][1] = __shfl_sync(kFull, mine, 8 * t4 + 4);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int Re = w.b * ROWS + nt * 8 + 2 * t4 + e;
+                    lim[nt][e] = Re < w.q.n * G ? w.q.ctx - w.q.n + Re / G : -1;
+                    m[nt][e] = -INFINITY;
+                    l[nt][e] = 0.0f;
+                }
+#pragma unroll
+                for (int j = 0; j < MT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        acc[nt][j][e] = 0.0f;
+            }
+        }
+        cp_async_wait_group<S - 2>();
+        __syncwarp();
+        issue();
+        look_up();
+        const uint32_t st = ring + (uint32_t)c_slot * St::kBytes;
+        if (++c_slot == S)
+            c_slot = 0;
+        const int base = w.t * kAttnTile + warp * kWarpTokens;
+        const uint32_t mask = base < end ? lds32(st + St::kOffMask) : 0u;
+        if (mask) {
+            float s[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    s[nt][e] = 0.0f;
+#pragma unroll
+            for (int half = 0; half < D / 64; ++half) {
+                const uint4 ka = lds128(st + St::at(g, half * 4 + t4));
+                const uint4 kb = lds128(st + St::at(g + 8, half * 4 + t4));
+                const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    uint32_t a0, a1, a2, a3;
+                    e4m3x4_to_f16x2(wa[z], a0, a2);
+                    e4m3x4_to_f16x2(wb[z], a1, a3);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma_f16(s[nt], a0, a1, a2, a3, qb[nt][half * 4 + z][0], qb[nt][half * 4 + z][1]);
+                }
+            }
+            const float ks0 = __uint_as_float(lds32(st + St::kOffKs + 4u * g));
+            const float ks1 = __uint_as_float(lds32(st + St::kOffKs + 4u * g + 32u));
+            const float vs0 = __uint_as_float(lds32(st + St::kOffVs + 4u * g));
+            const float vs1 = __uint_as_float(lds32(st + St::kOffVs + 4u * g + 32u));
+            // every row sees every token of the chunk (no mask to apply)
+            const bool whole = mask == 0xFFFFu && base + 15 <= w.q.ctx - w.q.n;
+            bool exceed = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                s[nt][0] *= ks0 * rc[nt][0];
+                s[nt][1] *= ks0 * rc[nt][1];
+                s[nt][2] *= ks1 * rc[nt][0];
+                s[nt][3] *= ks1 * rc[nt][1];
+                if (!whole) {
+                    const bool k0 = (mask >> g) & 1u, k1 = (mask >> (g + 8)) & 1u;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        if (!k0 || base + g > lim[nt][e])
+                            s[nt][e] = -INFINITY;
+                        if (!k1 || base + g + 8 > lim[nt][e])
+                            s[nt][2 + e] = -INFINITY;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    exceed |= fmaxf(s[nt][e], s[nt][2 + e]) > m[nt][e] + kSlack;
+            }
+            if (__any_sync(kFull, exceed)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float top = fmaxf(s[nt][e], s[nt][2 + e]);
+                        top = fmaxf(top, __shfl_xor_sync(kFull, top, 4));
+                        top = fmaxf(top, __shfl_xor_sync(kFull, top, 8));
+                        top = fmaxf(top, __shfl_xor_sync(kFull, top, 16));
+                        if (top > m[nt][e]) {
+                            const float alpha = ex2_approx(m[nt][e] - top);
+                            m[nt][e] = top;
+                            l[nt][e] *= alpha;
+#pragma unroll
+                            for (int j = 0; j < MT; ++j) {
+                                acc[nt][j][e] *= alpha;
+                                acc[nt][j][2 + e] *= alpha;
+                            }
+                        }
+                    }
+            }
+            // O is held in units of vref; p takes the token's scale over vref.
+            // vref moves when the chunk's largest scale leaves [2^-5, 2^5] vref
+            // (not to scales under 2^-60 of the largest seen: blocks of zeros).
+            float vmax = fmaxf(fabsf(vs0), fabsf(vs1));
+            vmax = fmaxf(vmax, __shfl_xor_sync(kFull, vmax, 4));
+            vmax = fmaxf(vmax, __shfl_xor_sync(kFull, vmax, 8));
+            vmax = fmaxf(vmax, __shfl_xor_sync(kFull, vmax, 16));
+            if (!(vmax <= 32.0f * vref && 32.0f * vmax >= vref) && vmax > 1e-36f &&
+                vmax >= vtop * 8.6736174e-19f) {
+                const float f = vref / vmax;
+                vref = vmax;
+                vinv = 1.0f / vmax;
+                vtop = fmaxf(vtop, vmax);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < MT; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            acc[nt][j][e] *= f;
+            }
+            const float rv0 = vs0 * vinv, rv1 = vs1 * vinv;
+            uint32_t pb[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float m0 = m[nt][0] == -INFINITY ? 0.0f : m[nt][0];
+                const float m1 = m[nt][1] == -INFINITY ? 0.0f : m[nt][1];
+                const float p0 = ex2_approx(s[nt][0] - m0), p1 = ex2_approx(s[nt][1] - m1);
+                const float p2 = ex2_approx(s[nt][2] - m0), p3 = ex2_approx(s[nt][3] - m1);
+                l[nt][0] += p0 + p2;
+                l[nt][1] += p1 + p3;
+                pb[nt][0] = transpose8x8(pack_f16x2(p0 * rv0, p1 * rv0));
+                pb[nt][1] = transpose8x8(pack_f16x2(p2 * rv1, p3 * rv1));
+            }
+            // value columns: D = 128, thread g holds dims 16 g .. 16 g + 15; D = 64, 8 g .. 8 g + 7
+            constexpr int VW = D / 32;  // 32-bit words per token and thread
+            uint32_t v[4][VW];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int r = 2 * t4 + (k & 1) + (k >> 1) * 8;
+                if constexpr (D == 128) {
+                    const uint4 u = lds128(st + St::kRows + St::at(r, g));
+                    v[k][0] = u.x;
+                    v[k][1] = u.y;
+                    v[k][2] = u.z;
+                    v[k][3] = u.w;
+                } else {
+                    const uint32_t ad = st + St::kRows + St::at(r, g >> 1) + (uint32_t)(g & 1) * 8u;
+                    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[k][0]), "=r"(v[k][1]) : "r"(ad));
+                }
+            }
+#pragma unroll
+            for (int z = 0; z < VW; ++z) {
+                uint32_t f[2][2], h[2][2];
+                e4m3x4_to_f16x2(__byte_perm(v[0][z], v[1][z], 0x5140), f[0][0], f[0][1]);
+                e4m3x4_to_f16x2(__byte_perm(v[2][z], v[3][z], 0x5140), h[0][0], h[0][1]);
+                e4m3x4_to_f16x2(__byte_perm(v[0][z], v[1][z], 0x7362), f[1][0], f[1][1]);
+                e4m3x4_to_f16x2(__byte_perm(v[2][z], v[3][z], 0x7362), h[1][0], h[1][1]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+                        mma_f16(acc[nt][2 * z + y], f[y][0], f[y][1], h[y][0], h[y][1], pb[nt][0], pb[nt][1]);
+            }
+        }
+        ++x;
+        if (w.t + 1 < w.T && x < rg.x1) {
+            ++w.t;
+            continue;
+        }
+
+        // ------------------------------------------- the end of a context (or of this CTA's part)
+        // thread (g, t4) holds rows 2 t4, 2 t4 + 1 of each 8 and D / 8 value columns from g D / 8
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float sum = l[nt][e];
+                sum += __shfl_xor_sync(kFull, sum, 4);
+                sum += __shfl_xor_sync(kFull, sum, 8);
+                sum += __shfl_xor_sync(kFull, sum, 16);
+                if (g == 0)
+                    mls[warp * ROWS + nt * 8 + 2 * t4 + e] = make_float2(m[nt][e], sum);
+            }
+        __syncthreads();
+        const bool starts = x - rg.x0 > w.t;  // the context's first tile was this CTA's too
+        const bool ends = w.t + 1 == w.T;
+        const int slot = 2 * (int)blockIdx.x + (seg > 0 ? 1 : 0);
+        const bool split = !(starts && ends);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int row = nt * 8 + 2 * t4 + e;
+                float M = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < kAttnWarps; ++k)
+                    M = fmaxf(M, mls[k * ROWS + row].x);
+                const float f = m[nt][e] == -INFINITY ? 0.0f : ex2_approx(m[nt][e] - M) * vref;
+                float *dst = merge + (warp * 8 + 2 * t4 + e) * Sh::kPitch + g * (D / 8);
+                // a NaN sum keeps its NaN: weight 0 is only for a warp without tokens
+#pragma unroll
+                for (int j = 0; j < MT; j += 2)
+                    *reinterpret_cast<float4 *>(dst + 2 * j) =
+                        make_float4(acc[nt][j][e] * f, acc[nt][j][2 + e] * f, acc[nt][j + 1][e] * f,
+                                    acc[nt][j + 1][2 + e] * f);
+            }
+            __syncthreads();
+            constexpr int TPR = D / 4;                    // threads per row
+            constexpr int RPP = kAttnThreads / TPR;       // rows per pass
+#pragma unroll
+            for (int r8 = tid / TPR; r8 < 8; r8 += RPP) {
+                const int row = nt * 8 + r8, col = (tid % TPR) * 4;
+                float M = -INFINITY, L = 0.0f;
+#pragma unroll
+                for (int k = 0; k < kAttnWarps; ++k)
+                    M = fmaxf(M, mls[k * ROWS + row].x);
+                float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int k = 0; k < kAttnWarps; ++k) {
+                    const float2 q2 = mls[k * ROWS + row];
+                    L += q2.x == -INFINITY ? q2.y : q2.y * ex2_approx(q2.x - M);
+                    const float4 u = *reinterpret_cast<const float4 *>(merge + (k * 8 + r8) * Sh::kPitch + col);
+                    o.x += u.x;
+                    o.y += u.y;
+                    o.z += u.z;
+                    o.w += u.w;
+                }
+                if (split) {
+                    __stcg(reinterpret_cast<float4 *>(a.part + ((long long)slot * ROWS + row) * D + col), o);
+                    if (col == 0)
+                        __stcg(reinterpret_cast<float2 *>(a.ml + ((long long)slot * ROWS + row) * 2),
+                               make_float2(M, L));
+                } else {
+                    const int R = w.b * ROWS + row;
+                    if (R < w.q.n * G) {
+                        const long long rh = (long long)(w.q.r0 + R / G) * a.heads + w.h * G + R % G;
+                        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+                        uint2 b;
+                        b.x = __bfloat16_as_ushort(__float2bfloat16_rn(o.x * inv)) |
+                              (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(o.y * inv)) << 16;
+                        b.y = __bfloat16_as_ushort(__float2bfloat16_rn(o.z * inv)) |
+                              (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(o.w * inv)) << 16;
+                        *reinterpret_cast<uint2 *>(a.out + rh * D + col) = b;
+                        if (a.lse && col == 0)
+                            a.lse[rh] = L == 0.0f ? -INFINITY : (M == -INFINITY ? L : (M + log2f(L)) * kLn2);
+                    }
+                }
+            }
+            __syncthreads();
+        }
+        if (starts && !ends) {
+            // this CTA is the first of several: it names the parts for the joining kernel
+            const long long last = x - 1 + (w.T - 1 - w.t);
+            const long long want = (rg.total + kLeastTiles - 1) / kLeastTiles;
+            const long long C = want < (long long)gridDim.x ? want : (long long)gridDim.x;
+            const int cta = (int)(((last + 1) * C - 1) / rg.total);
+            open = make_int4(w.i, w.h, w.b, 2 * (cta - (int)blockIdx.x + 1) + (slot & 1));
+        }
+        if (x >= rg.x1)
+            break;
+        fresh = true;
+        w.template next<kAttnTile, ROWS>(c, G, a.least, a.most);
+    }
+    cp_async_wait_all();
+    if (tid == 0)
+        a.meta[blockIdx.x] = open;
+}
+
+// Joins the parts of the contexts that the first kernel cut: block (c, y) takes
+// 4 rows of the context that CTA c began and left open. Each row's weights
+// 2^(m_k - M) are worked out once, then every thread adds its 4 columns over
+// the parts.
+template <int D, int NT>
+__global__ void __launch_bounds__(D) cache_attn_join_kernel(const __grid_constant__ AttnArgs a)
+{
+    constexpr int ROWS = 8 * NT;
+    __shared__ float s_w[4][kMaxCtas];
+    __shared__ float s_M[4], s_L[4];
+    griddep_wait();
+    const int4 meta = a.meta[blockIdx.x];
+    const int parts = meta.w >> 1;
+    if (parts == 0)
+        return;
+    const int h = meta.y, b = meta.z;
+    const Request q = load_request(a.c, meta.x, false);
+    const int R0 = b * ROWS + (int)blockIdx.y * 4;
+    if (R0 >= q.n * a.group)
+        return;
+    // part k in the first slot of CTA c + k, part 0 where CTA c put it
+    auto slot_of = [&](int k) { return 2 * ((int)blockIdx.x + k) + (k == 0 ? meta.w & 1 : 0); };
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int r = warp; r < 4; r += D / 32) {
+        const int row = (int)blockIdx.y * 4 + r;
+        float M = -INFINITY;
+        for (int k = lane; k < parts; k += 32)
+            M = fmaxf(M, a.ml[((long long)slot_of(k) * ROWS + row) * 2]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+        float L = 0.0f;
+        for (int k = lane; k < parts; k += 32) {
+            const float2 p = *reinterpret_cast<const float2 *>(a.ml + ((long long)slot_of(k) * ROWS + row) * 2);
+            const float f = p.x == -INFINITY ? (p.y == 0.0f ? 0.0f : 1.0f) : ex2_approx(p.x - M);
+            s_w[r][k] = f;
+            L += f * p.y;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            L += __shfl_xor_sync(kFull, L, o);
+        if (lane == 0) {
+            s_M[r] = M;
+            s_L[r] = L;
+        }
+    }
+    __syncthreads();
+    const int r = threadIdx.x / (D / 4), col = (threadIdx.x % (D / 4)) * 4;
+    const int row = (int)blockIdx.y * 4 + r, R = R0 + r;
+    if (R >= q.n * a.group)
+        return;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int k = 0; k < parts; ++k) {
+        const float f = s_w[r][k];
+        const float4 u = *reinterpret_cast<const float4 *>(a.part + ((long long)slot_of(k) * ROWS + row) * D + col);
+        o.x += f * u.x;
+        o.y += f * u.y;
+        o.z += f * u.z;
+        o.w += f * u.w;
+    }
+    const float M = s_M[r], L = s_L[r], inv = L == 0.0f ? 0.0f : 1.0f / L;
+    const long long rh = (long long)(q.r0 + R / a.group) * a.heads + h * a.group + R % a.group;
+    uint2 bb;
+    bb.x = __bfloat16_as_ushort(__float2bfloat16_rn(o.x * inv)) |
+           (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(o.y * inv)) << 16;
+    bb.y = __bfloat16_as_ushort(__float2bfloat16_rn(o.z * inv)) |
+           (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(o.w * inv)) << 16;
+    *reinterpret_cast<uint2 *>(a.out + rh * D + col) = bb;
+    if (a.lse && col == 0)
+        a.lse[rh] = L == 0.0f ? -INFINITY : (M == -INFINITY ? L : (M + log2f(L)) * kLn2);
+}
+
+template <int D, int NT>
+static cudaError_t launch_rows(AttnArgs &a, uint8_t *ws, int sms, cudaStream_t st)
+{
+    using Sh = AttnShape<D, NT>;
+    const int grid = std::min(sms * Sh::kOcc, kMaxCtas);
+    a.meta = reinterpret_cast<int4 *>(ws + kStatusBytes);
+    a.ml = reinterpret_cast<float *>(ws + kStatusBytes + kMaxCtas * sizeof(int4));
+    a.part = a.ml + (size_t)2 * kMaxCtas * 32 * 2;
+    cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<D, NT>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::kSmem);
+    if (e != cudaSuccess)
+        return e;
+    cache_attn_kernel<D, NT><<<grid, kAttnThreads, Sh::kSmem, st>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = st;
+    cfg.gridDim = dim3((unsigned)grid, 2 * NT);
+    cfg.blockDim = dim3(D);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<D, NT>, a);
+}
+
+// Requests with least <= rows * group <= most.
+cudaError_t launch_attn_rows(AttnCall &q, int least, int most, int sms, cudaStream_t st)
+{
+    AttnArgs a{};
+    a.c = q.c;
+    a.q = static_cast<const uint16_t *>(q.q);
+    a.out = static_cast<uint16_t *>(q.out);
+    a.lse = q.lse;
+    a.scale_log2 = q.sm_scale * kLog2e;
+    a.heads = q.heads;
+    a.group = q.heads / q.c.H;
+    a.least = least;
+    a.most = most;
+    // 8, 16 or 32 rows a block: what the longest request needs, or (when longer
+    // ones go elsewhere or take several blocks) what one row of every head needs
+    const long long need = (long long)q.c.max_rows * a.group;
+    const int rows = need <= 32 ? (int)need : a.group;
+    if (q.c.D == 128)
+        return rows <= 8 ? launch_rows<128, 1>(a, q.ws, sms, st)
+               : rows <= 16 ? launch_rows<128, 2>(a, q.ws, sms, st)
+                            : launch_rows<128, 4>(a, q.ws, sms, st);
+    return rows <= 8 ? launch_rows<64, 1>(a, q.ws, sms, st)
+           : rows <= 16 ? launch_rows<64, 2>(a, q.ws, sms, st)
+                        : launch_rows<64, 4>(a, q.ws, sms, st);
+}
+
+}  // namespace cache
+}  // namespace pmqa

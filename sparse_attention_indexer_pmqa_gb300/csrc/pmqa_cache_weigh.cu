@@ -1,0 +1,303 @@
+// pmqa_cache_weigh.cu -- the attention weight that each cached token receives
+// from a call's query rows, added to a running total per request and kv head:
+//   mass_out[i][h][t] = mass_in[i][h][t] +
+//       sum over rows j and heads hq of kv head h that see t of
+//       exp(sm_scale q_(j,hq) . k_t - lse[j][hq]).
+//
+// Reads K once (D bytes per token and kv head) and nothing of V; every token
+// belongs to one warp, so there are no atomics and the sums are the same on
+// every run. Products run as S = K Q^T (tokens are the 16 rows of the
+// m16n8k16 shape, query rows the 8 columns): a thread adds the weights of its
+// own query rows in registers and four threads join theirs by two shuffles.
+#include <algorithm>
+#include <cmath>
+
+#include "pmqa_cache_host.cuh"
+
+namespace pmqa {
+namespace cache {
+
+constexpr int kWeighWarps = 4;
+constexpr int kWeighThreads = 32 * kWeighWarps;
+constexpr int kWeighTile = 16 * kWeighWarps;
+constexpr int kWeighStages = 4;
+
+struct WeighArgs {
+    View c;
+    const uint16_t *q;
+    const float *lse;      // [rows, heads]
+    const float *mass_in;  // [bs, H, width] or null
+    float *mass_out;
+    long long width;
+    float scale_log2;
+    int heads, group;
+    int least, most;
+};
+
+template <int D>
+struct WeighStage {
+    static constexpr uint32_t kRows = 16 * D;
+    static constexpr uint32_t kOffKs = kRows, kOffMass = kOffKs + 64, kOffMask = kOffMass + 64;
+    static constexpr uint32_t kBytes = kOffMask + 16;
+    __device__ static __forceinline__ uint32_t at(int r, int c)
+    {
+        if constexpr (D == 128)
+            return (uint32_t)(r * 128 + ((c ^ ((((r >> 1) & 3) << 1) ^ ((r & 1) << 2))) << 4));
+        else
+            return (uint32_t)((r >> 1) * 128 + (((((r & 1) << 2) | c) ^ (((r >> 1) & 3) << 1)) << 4));
+    }
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kWeighThreads, NT == 4 ? 3 : 4)
+    cache_weigh_kernel(const __grid_constant__ WeighArgs a)
+{
+    using St = WeighStage<D>;
+    constexpr int S = kWeighStages;
+    constexpr int ROWS = 8 * NT;
+    constexpr int KS = D / 16;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+    const View &c = a.c;
+    const int G = a.group;
+    Range rg;
+    Walk w;
+    find_range<kWeighTile, 0, kWeighThreads>(c, G, a.least, a.most, 1, rg, w);
+    if (rg.x0 >= rg.x1)
+        return;
+    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * S) * St::kBytes;
+
+    Walk pw = w;
+    long long p_left = rg.x1 - rg.x0;
+    int pend_page = -1, pend_tok = 0, pend_h = 0, pend_i = 0;
+    bool pend_in = false;
+    auto look_up = [&]() {
+        pend_in = false;
+        if (p_left > 0) {
+            pend_tok = pw.t * kWeighTile + warp * 16 + (lane & 15);
+            pend_h = pw.h;
+            pend_i = pw.i;
+            pend_in = pend_tok < pw.q.ctx && pend_tok < a.width;
+            if (pend_in)
+                pend_page = __ldg(c.bt + (long long)pw.i * c.W + c.page_of(pend_tok));
+            --p_left;
+            if (p_left > 0)
+                pw.template next<kWeighTile, 0>(c, G, a.least, a.most);
+        }
+    };
+    int p_slot = 0;
+    auto issue = [&]() {
+        const uint32_t st = ring + (uint32_t)p_slot * St::kBytes;
+        if (++p_slot == S)
+            p_slot = 0;
+        bool ok = pend_in;
+        if (ok && (pend_page < 0 || (long long)pend_page >= c.nb)) {
+            atomicOr(c.status, (uint32_t)PMQA_DEV_BAD_BLOCK_ID);
+            ok = false;
+        }
+        const uint32_t mask = __ballot_sync(kFull, ok) & 0xFFFFu;
+        const uint32_t here = __ballot_sync(kFull, pend_in) & 0xFFFFu;
+        if (lane == 0)
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(st + St::kOffMask), "r"(mask) : "memory");
+        if (here) {
+            const long long phys = ok ? (long long)pend_page * c.H + pend_h : 0;
+            const long long row = ok ? (phys * c.P + (pend_tok - c.page_of(pend_tok) * c.P)) * D : 0;
+            if (lane < 16) {
+                if (ok)
+                    cp_async_4(st + St::kOffKs + (uint32_t)lane * 4u, c.ks + phys);
+            } else if (pend_in && a.mass_in) {
+                cp_async_4(st + St::kOffMass + (uint32_t)(lane & 15) * 4u,
+                           a.mass_in + ((long long)pend_i * c.H + pend_h) * a.width + pend_tok);
+            }
+            constexpr int CH = D / 16, PER = 32 / CH;
+            const int ch = lane % CH;
+#pragma unroll
+            for (int k = 0; k < 16 / PER; ++k) {
+                const int r = k * PER + lane / CH;
+                const long long src = __shfl_sync(kFull, row, r) + ch * 16;
+                cp_async_16(st + St::at(r, ch), c.k + src, (mask >> r) & 1u ? 16u : 0u);
+            }
+        }
+        cp_async_commit();
+    };
+    look_up();
+#pragma unroll 1
+    for (int s = 0; s < S - 1; ++s) {
+        issue();
+        look_up();
+    }
+
+    uint32_t qb[NT][KS][2];
+    float rc[NT][2], rl[NT][2];  // scale and lse (base 2) of rows 2 t4, 2 t4 + 1 of each 8
+    int lim[NT][2];
+    // block b of 8 NT query rows of the current request and head into registers
+    auto load_rows = [&](int b) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int R = b * ROWS + nt * 8 + g;
+            const bool has = R < w.q.n * G;
+            const uint16_t *src =
+                a.q + ((long long)(w.q.r0 + R / G) * a.heads + w.h * G + R % G) * D + 16 * t4;
+            uint4 u[D / 32];
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k)
+                u[k] = has ? __ldg(reinterpret_cast<const uint4 *>(src + (k >> 1) * 64 + (k & 1) * 8))
+                           : make_uint4(0, 0, 0, 0);
+            float top = 0.0f;
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+                const uint32_t e[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+#pragma unroll
+                for (int z = 0; z < 4; ++z)
+                    top = fmaxf(top, fmaxf(fabsf(__uint_as_float(e[z] << 16)),
+                                           fabsf(__uint_as_float(e[z] & 0xFFFF0000u))));
+            }
+            top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+            const int e2 = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 120);
+            const float up = __uint_as_float((uint32_t)(14 - e2 + 127) << 23);
+            const float down = __uint_as_float((uint32_t)(e2 - 14 + 127) << 23);
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+                const uint32_t e[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    const float lo = __uint_as_float(e[z] << 16) * up;
+                    const float hi = __uint_as_float(e[z] & 0xFFFF0000u) * up;
+                    qb[nt][(k >> 1) * 4 + (k & 1) * 2 + (z >> 1)][z & 1] = pack_f16x2(lo, hi);
+                }
+            }
+            const float mine = a.scale_log2 * down;
+            rc[nt][0] = __shfl_sync(kFull, mine, 8 * t4);
+            rc[nt][1] = __shfl_sync(kFull, mine, 8 * t4 + 4);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int Re = b * ROWS + nt * 8 + 2 * t4 + e;
+                const bool row = Re < w.q.n * G;
+                lim[nt][e] = row ? w.q.ctx - w.q.n + Re / G : -1;
+                rl[nt][e] = row ? __ldg(a.lse + (long long)(w.q.r0 + Re / G) * a.heads + w.h * G + Re % G) * kLog2e
+                                : 0.0f;
+            }
+        }
+    };
+    int c_slot = 0;
+    bool fresh = true;
+    int blocks = 0;
+#pragma unroll 1
+    for (long long x = rg.x0; x < rg.x1;) {
+        if (fresh) {
+            blocks = (w.q.n * G + ROWS - 1) / ROWS;
+            if (blocks > 0)
+                load_rows(0);
+            fresh = false;
+        }
+        cp_async_wait_group<S - 2>();
+        __syncwarp();
+        issue();
+        look_up();
+        const uint32_t st = ring + (uint32_t)c_slot * St::kBytes;
+        if (++c_slot == S)
+            c_slot = 0;
+        const int base = w.t * kWeighTile + warp * 16;
+        if (base < w.q.ctx) {
+            const uint32_t mask = lds32(st + St::kOffMask);
+            uint32_t ka[KS][4];
+#pragma unroll
+            for (int half = 0; half < D / 64; ++half) {
+                const uint4 u0 = lds128(st + St::at(g, half * 4 + t4));
+                const uint4 u1 = lds128(st + St::at(g + 8, half * 4 + t4));
+                const uint32_t wa[4] = {u0.x, u0.y, u0.z, u0.w}, wb[4] = {u1.x, u1.y, u1.z, u1.w};
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    e4m3x4_to_f16x2(wa[z], ka[half * 4 + z][0], ka[half * 4 + z][2]);
+                    e4m3x4_to_f16x2(wb[z], ka[half * 4 + z][1], ka[half * 4 + z][3]);
+                }
+            }
+            const float ks0 = __uint_as_float(lds32(st + St::kOffKs + 4u * g));
+            const float ks1 = __uint_as_float(lds32(st + St::kOffKs + 4u * g + 32u));
+            const bool k0 = (mask >> g) & 1u, k1 = (mask >> (g + 8)) & 1u;
+            float sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll 1
+            for (int b = 0; b < blocks; ++b) {
+                if (b > 0)
+                    load_rows(b);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int k = 0; k < KS; ++k)
+                        mma_f16(s, ka[k][0], ka[k][1], ka[k][2], ka[k][3], qb[nt][k][0], qb[nt][k][1]);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float w0 = ex2_approx(s[e] * (ks0 * rc[nt][e]) - rl[nt][e]);
+                        const float w1 = ex2_approx(s[2 + e] * (ks1 * rc[nt][e]) - rl[nt][e]);
+                        sum0 += k0 && base + g <= lim[nt][e] ? w0 : 0.0f;
+                        sum1 += k1 && base + g + 8 <= lim[nt][e] ? w1 : 0.0f;
+                    }
+                }
+            }
+            if (blocks > 1)
+                load_rows(0);
+            sum0 += __shfl_xor_sync(kFull, sum0, 1);
+            sum0 += __shfl_xor_sync(kFull, sum0, 2);
+            sum1 += __shfl_xor_sync(kFull, sum1, 1);
+            sum1 += __shfl_xor_sync(kFull, sum1, 2);
+            if (t4 < 2) {
+                const int t = base + g + 8 * t4;
+                if (t < w.q.ctx && t < a.width) {
+                    const float had =
+                        a.mass_in ? __uint_as_float(lds32(st + St::kOffMass + 4u * (uint32_t)(g + 8 * t4))) : 0.0f;
+                    a.mass_out[((long long)w.i * c.H + w.h) * a.width + t] = had + (t4 ? sum1 : sum0);
+                }
+            }
+        }
+        ++x;
+        if (w.t + 1 < w.T) {
+            ++w.t;
+        } else if (x < rg.x1) {
+            w.template next<kWeighTile, 0>(c, G, a.least, a.most);
+            fresh = true;
+        }
+    }
+    cp_async_wait_all();
+}
+
+template <int D, int NT>
+static cudaError_t launch(const WeighArgs &a, int sms, cudaStream_t st)
+{
+    const int smem = (int)(kWeighWarps * kWeighStages * WeighStage<D>::kBytes);
+    cudaError_t e = cudaFuncSetAttribute(cache_weigh_kernel<D, NT>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess)
+        return e;
+    cache_weigh_kernel<D, NT><<<sms * (NT == 4 ? 3 : 4), kWeighThreads, smem, st>>>(a);
+    return cudaGetLastError();
+}
+
+// Requests with least <= rows * group <= most.
+cudaError_t launch_weigh_rows(const WeighCall &q, int least, int most, int sms, cudaStream_t st)
+{
+    WeighArgs a{};
+    a.c = q.c;
+    a.q = static_cast<const uint16_t *>(q.q);
+    a.lse = q.lse;
+    a.mass_in = q.mass_in;
+    a.mass_out = q.mass_out;
+    a.width = q.width;
+    a.scale_log2 = q.sm_scale * kLog2e;
+    a.heads = q.heads;
+    a.group = q.heads / q.c.H;
+    a.least = least;
+    a.most = most;
+    const long long need = std::min<long long>((long long)q.c.max_rows * a.group, most);
+    if (q.c.D == 128)
+        return need <= 8 ? launch<128, 1>(a, sms, st)
+               : need <= 16 ? launch<128, 2>(a, sms, st)
+                            : launch<128, 4>(a, sms, st);
+    return need <= 8 ? launch<64, 1>(a, sms, st)
+           : need <= 16 ? launch<64, 2>(a, sms, st)
+                        : launch<64, 4>(a, sms, st);
+}
+
+}  // namespace cache
+}  // namespace pmqa

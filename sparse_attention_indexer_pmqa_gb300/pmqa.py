@@ -40,6 +40,8 @@ EXPORTED = (
     "pmqa_logits_topk_range",
     "pmqa_mqa_logits", "pmqa_topk_merge", "pmqa_sparse_mla_workspace_bytes",
     "pmqa_sparse_mla_decode", "pmqa_sparse_mla_decode_range", "pmqa_sparse_mla_merge",
+    "pmqa_cache_workspace_bytes", "pmqa_cache_append", "pmqa_cache_attention",
+    "pmqa_cache_weigh", "pmqa_cache_evict",
     "pmqa_gather_probe", "pmqa_read_device_status", "pmqa_status_string", "pmqa_version",
 )
 
@@ -110,6 +112,28 @@ class MlaProblem(ctypes.Structure):
     ]
 
 
+class CacheProblem(ctypes.Structure):
+    """Mirror of struct pmqa_cache_problem."""
+
+    _fields_ = [
+        ("k_cache", ctypes.c_void_p),
+        ("v_cache", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("block_tables", ctypes.c_void_p),
+        ("context_lens", ctypes.c_void_p),
+        ("row_begin", ctypes.c_void_p),
+        ("bs", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("block_size", ctypes.c_int32),
+        ("max_blocks_per_seq", ctypes.c_int32),
+        ("rows", ctypes.c_int32),
+        ("max_rows", ctypes.c_int32),
+        ("num_blocks", ctypes.c_int64),
+    ]
+
+
 _lib = None
 
 
@@ -131,6 +155,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
     PP = ctypes.POINTER(Problem)
     PM = ctypes.POINTER(MqaProblem)
     PL = ctypes.POINTER(MlaProblem)
+    PC = ctypes.POINTER(CacheProblem)
+    F32 = ctypes.c_float
     sig = {
         "pmqa_workspace_bytes": ([I32, I32, I32, I32, ctypes.c_int], SZ),
         "pmqa_workspace_init": ([V, SZ, V], ctypes.c_int),
@@ -146,6 +172,12 @@ def load(path: str | None = None) -> ctypes.CDLL:
         "pmqa_sparse_mla_decode": ([PL, V, V, V, SZ, V], ctypes.c_int),
         "pmqa_sparse_mla_decode_range": ([PL, V, V, V, V, V, SZ, V], ctypes.c_int),
         "pmqa_sparse_mla_merge": ([V, V, I32, I32, I32, V, V, V], ctypes.c_int),
+        "pmqa_cache_workspace_bytes": ([], SZ),
+        "pmqa_cache_append": ([PC, V, V, V, SZ, V], ctypes.c_int),
+        "pmqa_cache_attention": ([PC, V, I32, F32, V, V, V, SZ, V], ctypes.c_int),
+        "pmqa_cache_weigh": ([PC, V, I32, F32, V, V, V, I64, V, SZ, V], ctypes.c_int),
+        "pmqa_cache_evict": ([PC, V, I64, I32, I32, I32, V, I32, V, V, V, V, SZ, V],
+                             ctypes.c_int),
         "pmqa_gather_probe": ([V, ctypes.c_uint64, V, I64, I32, I32, V, V], ctypes.c_int),
         "pmqa_read_device_status": ([V, V], ctypes.c_int),
         "pmqa_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -155,7 +187,6 @@ def load(path: str | None = None) -> ctypes.CDLL:
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = res
-    del I64
     _lib = lib
     return lib
 
@@ -452,6 +483,172 @@ def pmqa_sparse_mla_merge(outs, lses, *, out=None, lse=None, stream=None):
     _check(load().pmqa_sparse_mla_merge(_ptr(outs), _ptr(lses), parts, rows, heads, _ptr(out),
                                         _ptr(lse), _stream(stream)), "pmqa_sparse_mla_merge")
     return out, lse
+
+
+def make_cache_problem(k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                       row_begin=None, rows: int = 0, max_rows: int = 0) -> CacheProblem:
+    """Fill a pmqa_cache_problem from tensors shaped as in the C header (the
+    pools as float8_e4m3fn or uint8; v_cache and v_scale may be None where the
+    call does not read values)."""
+    import torch
+
+    num_blocks, kv_heads, block_size, head_dim = k_cache.shape
+    bs = block_tables.shape[0]
+    dev = k_cache.device
+    for pool, scale in ((k_cache, k_scale), (v_cache, v_scale)):
+        if pool is None:
+            continue
+        assert pool.shape == k_cache.shape and pool.element_size() == 1 and pool.is_contiguous()
+        assert scale.shape == (num_blocks, kv_heads) and scale.dtype == torch.float32
+        assert scale.is_contiguous() and pool.device == dev == scale.device
+    for t in (block_tables, context_lens) if row_begin is None else (block_tables, context_lens,
+                                                                     row_begin):
+        assert t.dtype == torch.int32 and t.is_contiguous() and t.device == dev and t.is_cuda
+    assert context_lens.shape == (bs,) and (row_begin is None or row_begin.shape == (bs + 1,))
+    return CacheProblem(
+        k_cache=k_cache.data_ptr(), v_cache=0 if v_cache is None else v_cache.data_ptr(),
+        k_scale=k_scale.data_ptr(), v_scale=0 if v_cache is None else v_scale.data_ptr(),
+        block_tables=block_tables.data_ptr(), context_lens=context_lens.data_ptr(),
+        row_begin=0 if row_begin is None else row_begin.data_ptr(), bs=bs, kv_heads=kv_heads,
+        head_dim=head_dim, block_size=block_size, max_blocks_per_seq=block_tables.shape[1],
+        rows=rows, max_rows=max_rows, num_blocks=num_blocks)
+
+
+def pmqa_cache_workspace_bytes() -> int:
+    return int(load().pmqa_cache_workspace_bytes())
+
+
+def cache_workspace(device=None, stream=None):
+    """A zero-initialised workspace for the pmqa_cache_* calls."""
+    import torch
+
+    ws = torch.empty(pmqa_cache_workspace_bytes(), dtype=torch.uint8, device=device or "cuda")
+    with torch.cuda.device(ws.device):
+        pmqa_workspace_init(ws, stream=stream)
+    return ws
+
+
+def _cache_call(name: str, p: CacheProblem, device, stream, ws, *args) -> None:
+    """Call a pmqa_cache_* function with the problem's device current (its
+    stream unless one is given)."""
+    import torch
+
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _cache_call(name, p, device, stream, ws, *args)
+    if ws is None:
+        ws = cache_workspace(device, stream)
+    assert ws.device == device and ws.is_contiguous()
+    rc = getattr(load(), name)(ctypes.byref(p), *args, ws.data_ptr(),
+                               ws.numel() * ws.element_size(), _stream(stream))
+    if rc != PMQA_OK:
+        raise PmqaError(rc, name)
+
+
+def _rows(t, device, dtype) -> None:
+    assert t.device == device and t.dtype == dtype and t.is_contiguous()
+
+
+def pmqa_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                      row_begin, max_rows: int, *, ws=None, stream=None) -> None:
+    """Quantise new tokens k, v (bf16 [rows, kv_heads, head_dim]) into the
+    cache's blocks, updating the pools and their scales in place."""
+    import torch
+
+    p = make_cache_problem(k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                           row_begin, k.shape[0], max_rows)
+    for t in (k, v):
+        _rows(t, k_cache.device, torch.bfloat16)
+        assert t.shape == (p.rows, p.kv_heads, p.head_dim)
+    _cache_call("pmqa_cache_append", p, k_cache.device, stream, ws, k.data_ptr(), v.data_ptr())
+
+
+def pmqa_cache_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                         row_begin, max_rows: int, sm_scale: float, *, out=None, lse=None,
+                         want_lse: bool = False, ws=None, stream=None):
+    """Attention of q (bf16 [rows, heads, head_dim]) to the cached tokens: bf16
+    out of q's shape (and fp32 lse [rows, heads] when asked for or given)."""
+    import torch
+
+    p = make_cache_problem(k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                           row_begin, q.shape[0], max_rows)
+    rows, heads, _ = q.shape
+    _rows(q, k_cache.device, torch.bfloat16)
+    assert q.shape[2] == p.head_dim
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _rows(out, q.device, torch.bfloat16)
+        assert out.shape == q.shape
+    if lse is None and want_lse:
+        lse = torch.empty((rows, heads), dtype=torch.float32, device=q.device)
+    elif lse is not None:
+        _rows(lse, q.device, torch.float32)
+        assert lse.shape == (rows, heads)
+    _cache_call("pmqa_cache_attention", p, q.device, stream, ws, q.data_ptr(), heads, sm_scale,
+                out.data_ptr(), 0 if lse is None else lse.data_ptr())
+    return (out, lse) if lse is not None else out
+
+
+def pmqa_cache_weigh(q, k_cache, k_scale, block_tables, context_lens, row_begin, max_rows: int,
+                     sm_scale: float, lse, mass_in=None, *, mass_out=None, mass_width=None,
+                     ws=None, stream=None):
+    """mass_in (fp32 [bs, kv_heads, mass_width], None for zeros) plus the
+    attention weight that each cached token receives from the rows of q, whose
+    log-sum-exp `lse` the attention call returned. Only entries of cached tokens
+    are written to mass_out (which may be mass_in); a new one starts as a copy
+    of mass_in, or as zeros."""
+    import torch
+
+    p = make_cache_problem(k_cache, None, k_scale, None, block_tables, context_lens, row_begin,
+                           q.shape[0], max_rows)
+    rows, heads, _ = q.shape
+    _rows(q, k_cache.device, torch.bfloat16)
+    _rows(lse, q.device, torch.float32)
+    assert q.shape[2] == p.head_dim and lse.shape == (rows, heads)
+    if mass_out is None:
+        if mass_in is not None:
+            mass_out = mass_in.clone()
+        else:
+            width = mass_width or p.block_size * p.max_blocks_per_seq
+            mass_out = torch.zeros((p.bs, p.kv_heads, width), dtype=torch.float32, device=q.device)
+    for t in (mass_out,) if mass_in is None else (mass_out, mass_in):
+        _rows(t, q.device, torch.float32)
+        assert t.shape == (p.bs, p.kv_heads, mass_out.shape[2])
+    _cache_call("pmqa_cache_weigh", p, q.device, stream, ws, q.data_ptr(), heads, sm_scale,
+                lse.data_ptr(), 0 if mass_in is None else mass_in.data_ptr(),
+                mass_out.data_ptr(), mass_out.shape[2])
+    return mass_out
+
+
+def pmqa_cache_evict(k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, mass,
+                     keep: int, sinks: int, recent: int, new_tables, *, kept=None, lens_out=None,
+                     mass_out=None, ws=None, stream=None):
+    """Keep at most `keep` tokens per request and kv head (the first `sinks`,
+    the last `recent`, and those with the most mass) in the blocks of
+    new_tables; returns (kept [bs, kv_heads, keep], lens_out [bs], mass_out)."""
+    import torch
+
+    p = make_cache_problem(k_cache, v_cache, k_scale, v_scale, block_tables, context_lens)
+    dev = k_cache.device
+    _rows(mass, dev, torch.float32)
+    _rows(new_tables, dev, torch.int32)
+    assert mass.shape[:2] == (p.bs, p.kv_heads) and new_tables.shape[0] == p.bs
+    if kept is None:
+        kept = torch.empty((p.bs, p.kv_heads, keep), dtype=torch.int32, device=dev)
+    if lens_out is None:
+        lens_out = torch.empty_like(context_lens)
+    if mass_out is None:
+        mass_out = torch.empty_like(mass)
+    _rows(kept, dev, torch.int32)
+    _rows(lens_out, dev, torch.int32)
+    _rows(mass_out, dev, torch.float32)
+    assert kept.shape == (p.bs, p.kv_heads, keep) and lens_out.shape == (p.bs,)
+    assert mass_out.shape == mass.shape
+    _cache_call("pmqa_cache_evict", p, dev, stream, ws, mass.data_ptr(), mass.shape[2], keep,
+                sinks, recent, new_tables.data_ptr(), new_tables.shape[1], kept.data_ptr(),
+                lens_out.data_ptr(), mass_out.data_ptr())
+    return kept, lens_out, mass_out
 
 
 def pmqa_gather_probe(pool, rows, row_pitch, method, *, out=None, stream=None):
