@@ -81,12 +81,20 @@ View view(const pmqa_cache_problem *p, void *ws)
     return c;
 }
 
+// SMs of the current device (looked up once per device: a property of it).
 int sm_count(int *n)
 {
+    static std::atomic<int> known[64];
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    if (cudaGetDevice(&dev) != cudaSuccess)
         return PMQA_ERR_CUDA;
+    *n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (*n > 0)
+        return PMQA_OK;
+    if (cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return PMQA_ERR_CUDA;
+    if (dev < 64)
+        known[dev].store(*n, std::memory_order_relaxed);
     return PMQA_OK;
 }
 

@@ -581,8 +581,8 @@ static cudaError_t launch_rows(AttnArgs &a, uint8_t *ws, int sms, cudaStream_t s
     a.meta = reinterpret_cast<int4 *>(ws + kStatusBytes);
     a.ml = reinterpret_cast<float *>(ws + kStatusBytes + kMaxCtas * sizeof(int4));
     a.part = a.ml + (size_t)2 * kMaxCtas * 32 * 2;
-    cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<D, NT>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::kSmem);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(cache_attn_kernel<D, NT>, (int)Sh::kSmem, done);
     if (e != cudaSuccess)
         return e;
     cache_attn_kernel<D, NT><<<grid, kAttnThreads, Sh::kSmem, st>>>(a);

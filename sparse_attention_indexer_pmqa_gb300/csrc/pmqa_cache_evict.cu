@@ -395,8 +395,8 @@ cudaError_t launch_evict(const EvictCall &q, int sms, cudaStream_t st)
     const long long chunk = ((std::min<long long>(q.width, 0x7FFFFF00ll) + cs - 1) / cs + 1023) & ~1023ll;
     a.key_cap = (int)std::min<long long>(chunk, kKeysMax);
     const int smem = a.key_cap * 4;
-    cudaError_t e = cudaFuncSetAttribute(cache_evict_select_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(cache_evict_select_kernel, kKeysMax * 4, done);
     if (e != cudaSuccess)
         return e;
     if (pairs * cs > 0x7FFFFFFFll)

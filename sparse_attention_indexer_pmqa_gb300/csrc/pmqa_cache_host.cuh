@@ -2,10 +2,31 @@
 // C ABI hands to the kernels' translation units.
 #pragma once
 
+#include <atomic>
+
 #include "pmqa_cache.cuh"
 
 namespace pmqa {
 namespace cache {
+
+// The kernel's shared-memory limit, raised once per device and kernel (a
+// property of the loaded code; setting it costs several microseconds of host
+// time, more than the launch). `done` is one word per kernel, a bit per device.
+template <typename K>
+inline cudaError_t allow_smem(K *kernel, int bytes, std::atomic<uint64_t> &done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+    if (bit & done.load(std::memory_order_relaxed))
+        return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess)
+        done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 struct AttnCall {
     View c;

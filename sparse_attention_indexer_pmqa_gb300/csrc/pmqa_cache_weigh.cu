@@ -266,8 +266,8 @@ template <int D, int NT>
 static cudaError_t launch(const WeighArgs &a, int sms, cudaStream_t st)
 {
     const int smem = (int)(kWeighWarps * kWeighStages * WeighStage<D>::kBytes);
-    cudaError_t e = cudaFuncSetAttribute(cache_weigh_kernel<D, NT>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(cache_weigh_kernel<D, NT>, smem, done);
     if (e != cudaSuccess)
         return e;
     cache_weigh_kernel<D, NT><<<sms * (NT == 4 ? 3 : 4), kWeighThreads, smem, st>>>(a);

@@ -135,6 +135,7 @@ class CacheProblem(ctypes.Structure):
 
 
 _lib = None
+_dtypes = ()  # torch's float32, int32, bfloat16 (torch is imported on first use)
 
 
 def library_path() -> str:
@@ -490,28 +491,30 @@ def make_cache_problem(k_cache, v_cache, k_scale, v_scale, block_tables, context
     """Fill a pmqa_cache_problem from tensors shaped as in the C header (the
     pools as float8_e4m3fn or uint8; v_cache and v_scale may be None where the
     call does not read values)."""
-    import torch
+    global _dtypes
+    if not _dtypes:
+        import torch
 
+        _dtypes = (torch.float32, torch.int32, torch.bfloat16)
     num_blocks, kv_heads, block_size, head_dim = k_cache.shape
-    bs = block_tables.shape[0]
-    dev = k_cache.device
-    for pool, scale in ((k_cache, k_scale), (v_cache, v_scale)):
-        if pool is None:
-            continue
-        assert pool.shape == k_cache.shape and pool.element_size() == 1 and pool.is_contiguous()
-        assert scale.shape == (num_blocks, kv_heads) and scale.dtype == torch.float32
-        assert scale.is_contiguous() and pool.device == dev == scale.device
-    for t in (block_tables, context_lens) if row_begin is None else (block_tables, context_lens,
-                                                                     row_begin):
-        assert t.dtype == torch.int32 and t.is_contiguous() and t.device == dev and t.is_cuda
-    assert context_lens.shape == (bs,) and (row_begin is None or row_begin.shape == (bs + 1,))
+    bs, width = block_tables.shape
+    dev = k_cache.get_device()
+    f32, i32 = _dtypes[:2]
+    assert dev >= 0 and k_cache.element_size() == 1 and k_cache.is_contiguous()
+    _like(k_scale, dev, f32, (num_blocks, kv_heads))
+    if v_cache is not None:
+        assert v_cache.element_size() == 1
+        _like(v_cache, dev, v_cache.dtype, (num_blocks, kv_heads, block_size, head_dim))
+        _like(v_scale, dev, f32, (num_blocks, kv_heads))
+    _like(block_tables, dev, i32, (bs, width))
+    _like(context_lens, dev, i32, (bs,))
+    if row_begin is not None:
+        _like(row_begin, dev, i32, (bs + 1,))
     return CacheProblem(
-        k_cache=k_cache.data_ptr(), v_cache=0 if v_cache is None else v_cache.data_ptr(),
-        k_scale=k_scale.data_ptr(), v_scale=0 if v_cache is None else v_scale.data_ptr(),
-        block_tables=block_tables.data_ptr(), context_lens=context_lens.data_ptr(),
-        row_begin=0 if row_begin is None else row_begin.data_ptr(), bs=bs, kv_heads=kv_heads,
-        head_dim=head_dim, block_size=block_size, max_blocks_per_seq=block_tables.shape[1],
-        rows=rows, max_rows=max_rows, num_blocks=num_blocks)
+        k_cache.data_ptr(), None if v_cache is None else v_cache.data_ptr(), k_scale.data_ptr(),
+        None if v_cache is None else v_scale.data_ptr(), block_tables.data_ptr(),
+        context_lens.data_ptr(), None if row_begin is None else row_begin.data_ptr(),
+        bs, kv_heads, head_dim, block_size, width, rows, max_rows, num_blocks)
 
 
 def pmqa_cache_workspace_bytes() -> int:
@@ -528,39 +531,42 @@ def cache_workspace(device=None, stream=None):
     return ws
 
 
-def _cache_call(name: str, p: CacheProblem, device, stream, ws, *args) -> None:
-    """Call a pmqa_cache_* function with the problem's device current (its
-    stream unless one is given)."""
+def _like(t, dev: int, dtype, shape) -> None:
+    """What every operand of a pmqa_cache_* call must be: on the cache's
+    device, of the documented type and shape, contiguous."""
+    assert t.get_device() == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous(), \
+        f"expected a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}"
+
+
+def _cache_call(name: str, p: CacheProblem, dev: int, stream, ws, *args) -> None:
+    """Call a pmqa_cache_* function with device `dev` current, on its current
+    stream unless one is given."""
     import torch
 
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _cache_call(name, p, device, stream, ws, *args)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _cache_call(name, p, dev, stream, ws, *args)
     if ws is None:
-        ws = cache_workspace(device, stream)
-    assert ws.device == device and ws.is_contiguous()
-    rc = getattr(load(), name)(ctypes.byref(p), *args, ws.data_ptr(),
-                               ws.numel() * ws.element_size(), _stream(stream))
+        ws = cache_workspace(torch.device("cuda", dev), stream)
+    assert ws.get_device() == dev and ws.is_contiguous()
+    s = torch.cuda.current_stream(dev) if stream is None else stream
+    rc = getattr(_lib or load(), name)(ctypes.byref(p), *args, ws.data_ptr(), ws.nbytes,
+                                       s.cuda_stream)
     if rc != PMQA_OK:
         raise PmqaError(rc, name)
-
-
-def _rows(t, device, dtype) -> None:
-    assert t.device == device and t.dtype == dtype and t.is_contiguous()
 
 
 def pmqa_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
                       row_begin, max_rows: int, *, ws=None, stream=None) -> None:
     """Quantise new tokens k, v (bf16 [rows, kv_heads, head_dim]) into the
     cache's blocks, updating the pools and their scales in place."""
-    import torch
-
     p = make_cache_problem(k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
                            row_begin, k.shape[0], max_rows)
-    for t in (k, v):
-        _rows(t, k_cache.device, torch.bfloat16)
-        assert t.shape == (p.rows, p.kv_heads, p.head_dim)
-    _cache_call("pmqa_cache_append", p, k_cache.device, stream, ws, k.data_ptr(), v.data_ptr())
+    dev, bf16 = k_cache.get_device(), _dtypes[2]
+    shape = (p.rows, p.kv_heads, p.head_dim)
+    _like(k, dev, bf16, shape)
+    _like(v, dev, bf16, shape)
+    _cache_call("pmqa_cache_append", p, dev, stream, ws, k.data_ptr(), v.data_ptr())
 
 
 def pmqa_cache_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
@@ -568,26 +574,24 @@ def pmqa_cache_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, co
                          want_lse: bool = False, ws=None, stream=None):
     """Attention of q (bf16 [rows, heads, head_dim]) to the cached tokens: bf16
     out of q's shape (and fp32 lse [rows, heads] when asked for or given)."""
-    import torch
-
+    rows, heads, head_dim = q.shape
     p = make_cache_problem(k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
-                           row_begin, q.shape[0], max_rows)
-    rows, heads, _ = q.shape
-    _rows(q, k_cache.device, torch.bfloat16)
-    assert q.shape[2] == p.head_dim
+                           row_begin, rows, max_rows)
+    dev = k_cache.get_device()
+    f32, _, bf16 = _dtypes
+    shape = (rows, heads, p.head_dim)
+    _like(q, dev, bf16, shape)
     if out is None:
-        out = torch.empty_like(q)
+        out = q.new_empty(shape)
     else:
-        _rows(out, q.device, torch.bfloat16)
-        assert out.shape == q.shape
-    if lse is None and want_lse:
-        lse = torch.empty((rows, heads), dtype=torch.float32, device=q.device)
-    elif lse is not None:
-        _rows(lse, q.device, torch.float32)
-        assert lse.shape == (rows, heads)
-    _cache_call("pmqa_cache_attention", p, q.device, stream, ws, q.data_ptr(), heads, sm_scale,
-                out.data_ptr(), 0 if lse is None else lse.data_ptr())
-    return (out, lse) if lse is not None else out
+        _like(out, dev, bf16, shape)
+    if lse is None:
+        lse = q.new_empty((rows, heads), dtype=f32) if want_lse else None
+    else:
+        _like(lse, dev, f32, (rows, heads))
+    _cache_call("pmqa_cache_attention", p, dev, stream, ws, q.data_ptr(), heads, sm_scale,
+                out.data_ptr(), None if lse is None else lse.data_ptr())
+    return out if lse is None else (out, lse)
 
 
 def pmqa_cache_weigh(q, k_cache, k_scale, block_tables, context_lens, row_begin, max_rows: int,
@@ -598,26 +602,26 @@ def pmqa_cache_weigh(q, k_cache, k_scale, block_tables, context_lens, row_begin,
     log-sum-exp `lse` the attention call returned. Only entries of cached tokens
     are written to mass_out (which may be mass_in); a new one starts as a copy
     of mass_in, or as zeros."""
-    import torch
-
-    p = make_cache_problem(k_cache, None, k_scale, None, block_tables, context_lens, row_begin,
-                           q.shape[0], max_rows)
     rows, heads, _ = q.shape
-    _rows(q, k_cache.device, torch.bfloat16)
-    _rows(lse, q.device, torch.float32)
-    assert q.shape[2] == p.head_dim and lse.shape == (rows, heads)
+    p = make_cache_problem(k_cache, None, k_scale, None, block_tables, context_lens, row_begin,
+                           rows, max_rows)
+    dev = k_cache.get_device()
+    f32, _, bf16 = _dtypes
+    _like(q, dev, bf16, (rows, heads, p.head_dim))
+    _like(lse, dev, f32, (rows, heads))
     if mass_out is None:
         if mass_in is not None:
             mass_out = mass_in.clone()
         else:
             width = mass_width or p.block_size * p.max_blocks_per_seq
-            mass_out = torch.zeros((p.bs, p.kv_heads, width), dtype=torch.float32, device=q.device)
-    for t in (mass_out,) if mass_in is None else (mass_out, mass_in):
-        _rows(t, q.device, torch.float32)
-        assert t.shape == (p.bs, p.kv_heads, mass_out.shape[2])
-    _cache_call("pmqa_cache_weigh", p, q.device, stream, ws, q.data_ptr(), heads, sm_scale,
-                lse.data_ptr(), 0 if mass_in is None else mass_in.data_ptr(),
-                mass_out.data_ptr(), mass_out.shape[2])
+            mass_out = q.new_zeros((p.bs, p.kv_heads, width), dtype=f32)
+    shape = (p.bs, p.kv_heads, mass_out.shape[-1])
+    _like(mass_out, dev, f32, shape)
+    if mass_in is not None:
+        _like(mass_in, dev, f32, shape)
+    _cache_call("pmqa_cache_weigh", p, dev, stream, ws, q.data_ptr(), heads, sm_scale,
+                lse.data_ptr(), None if mass_in is None else mass_in.data_ptr(),
+                mass_out.data_ptr(), shape[2])
     return mass_out
 
 
@@ -627,26 +631,26 @@ def pmqa_cache_evict(k_cache, v_cache, k_scale, v_scale, block_tables, context_l
     """Keep at most `keep` tokens per request and kv head (the first `sinks`,
     the last `recent`, and those with the most mass) in the blocks of
     new_tables; returns (kept [bs, kv_heads, keep], lens_out [bs], mass_out)."""
-    import torch
-
     p = make_cache_problem(k_cache, v_cache, k_scale, v_scale, block_tables, context_lens)
-    dev = k_cache.device
-    _rows(mass, dev, torch.float32)
-    _rows(new_tables, dev, torch.int32)
-    assert mass.shape[:2] == (p.bs, p.kv_heads) and new_tables.shape[0] == p.bs
+    dev = k_cache.get_device()
+    f32, i32, _ = _dtypes
+    wide, list_shape = (p.bs, p.kv_heads, mass.shape[-1]), (p.bs, p.kv_heads, max(keep, 0))
+    _like(mass, dev, f32, wide)
+    _like(new_tables, dev, i32, (p.bs, new_tables.shape[-1]))
     if kept is None:
-        kept = torch.empty((p.bs, p.kv_heads, keep), dtype=torch.int32, device=dev)
+        kept = mass.new_empty(list_shape, dtype=i32)
+    else:
+        _like(kept, dev, i32, list_shape)
     if lens_out is None:
-        lens_out = torch.empty_like(context_lens)
+        lens_out = mass.new_empty((p.bs,), dtype=i32)
+    else:
+        _like(lens_out, dev, i32, (p.bs,))
     if mass_out is None:
-        mass_out = torch.empty_like(mass)
-    _rows(kept, dev, torch.int32)
-    _rows(lens_out, dev, torch.int32)
-    _rows(mass_out, dev, torch.float32)
-    assert kept.shape == (p.bs, p.kv_heads, keep) and lens_out.shape == (p.bs,)
-    assert mass_out.shape == mass.shape
-    _cache_call("pmqa_cache_evict", p, dev, stream, ws, mass.data_ptr(), mass.shape[2], keep,
-                sinks, recent, new_tables.data_ptr(), new_tables.shape[1], kept.data_ptr(),
+        mass_out = mass.new_empty(wide)
+    else:
+        _like(mass_out, dev, f32, wide)
+    _cache_call("pmqa_cache_evict", p, dev, stream, ws, mass.data_ptr(), wide[2], keep, sinks,
+                recent, new_tables.data_ptr(), new_tables.shape[1], kept.data_ptr(),
                 lens_out.data_ptr(), mass_out.data_ptr())
     return kept, lens_out, mass_out
 
