@@ -143,7 +143,15 @@ extern "C" int pmqa_cache_attention(const pmqa_cache_problem *p, const void *q, 
     if ((rc = sm_count(&sms)) != PMQA_OK)
         return rc;
     AttnCall a{view(p, ws), q, out, lse, sm_scale, heads, static_cast<uint8_t *>(ws)};
-    return code_of(launch_attn_rows(a, 1, 0x7FFFFFFF, sms, cuda(stream)));
+    // requests with up to kShortRows packed rows split their context over the
+    // GPU; longer ones keep the tensor cores busy with their rows
+    const long long most = (long long)p->max_rows * (heads / p->kv_heads);
+    cudaError_t e = cudaSuccess;
+    if (most > kShortRows)
+        e = launch_attn_prompt(a, kShortRows + 1, cuda(stream));
+    if (e == cudaSuccess)
+        e = launch_attn_rows(a, 1, kShortRows, sms, cuda(stream));
+    return code_of(e);
 }
 
 extern "C" int pmqa_cache_weigh(const pmqa_cache_problem *p, const void *q, int32_t heads,

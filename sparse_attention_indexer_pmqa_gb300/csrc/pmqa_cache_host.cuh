@@ -28,6 +28,8 @@ inline cudaError_t allow_smem(K *kernel, int bytes, std::atomic<uint64_t> &done)
     return e;
 }
 
+constexpr int kShortRows = 32;  // packed rows (rows * group) of the short-row kernels
+
 struct AttnCall {
     View c;
     const void *q;
@@ -63,6 +65,7 @@ struct EvictCall {
 
 cudaError_t launch_append(const View &c, const void *k, const void *v, cudaStream_t st);
 cudaError_t launch_attn_rows(AttnCall &q, int least, int most, int sms, cudaStream_t st);
+cudaError_t launch_attn_prompt(AttnCall &q, int least, cudaStream_t st);
 cudaError_t launch_weigh_rows(const WeighCall &q, int least, int most, int sms, cudaStream_t st);
 cudaError_t launch_evict(const EvictCall &q, int sms, cudaStream_t st);
 

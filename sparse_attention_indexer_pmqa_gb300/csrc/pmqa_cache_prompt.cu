@@ -1,0 +1,643 @@
+// pmqa_cache_prompt.cu -- attention over the paged 8-bit K/V cache for requests
+// with many query rows (prompts, prompt chunks) on the 5th-generation tensor
+// cores.
+//
+// Rows of one request and kv head are packed as R = j * group + g (query token
+// j, head g of the group), 256 of them to a CTA in two tiles of 128. With the
+// tokens in tiles of 128:
+//   S = Q K^T    kind::f8f6f4 on the cached codes as they are: q, scaled by a
+//                power of two per row, is the sum of two e4m3 terms, exact for
+//                bf16 values within 2^-10 of their row's largest and off by at
+//                most 2^-18 of it below that; both terms add into one
+//                accumulator, at the cost of one bf16 product;
+//   p = 2^(x - m), x = S ks_t c_row, masked by slot; running m and l per row,
+//                one thread per row; P is written as f16 over the columns that
+//                held S;
+//   O += P V     kind::f16 with P from tensor memory and V as f16: the codes
+//                converted (exactly) and scaled by vs_t / vref, vref the largest
+//                block scale so far, so that O needs no factor per token.
+// Roles of a CTA's 16 warps: 0-3 and 4-7 are the softmax (and the final output)
+// of the two row tiles, 8-11 look up the blocks, copy K and V rows (cp.async)
+// into the operand layouts and convert V, warp 12 issues the products. While
+// one tile's softmax runs the tensor cores work for the other.
+//
+// Bound by the tensor cores: 4 D flops per visible (row, head, token) at the
+// bf16 rate, 512 cycles per 128 x 128 x 128 product and tile against about 4.2
+// issue slots per score, 1100 cycles for both tiles.
+#include <algorithm>
+#include <cmath>
+
+#include "pmqa_cache_host.cuh"
+
+namespace pmqa {
+namespace cache {
+
+constexpr int kPrRows = 256;      // packed rows per CTA (two tiles of 128)
+constexpr int kPrTok = 128;       // tokens per tile
+constexpr int kPrThreads = 512;
+constexpr int kKStages = 3, kVStages = 2, kMeta = 4;
+constexpr uint32_t kTileBytes = 128 * 128;           // 128 rows of 128 bytes
+constexpr float kPrSlack = 8.0f;                     // p <= 2^8 before the maximum moves
+constexpr float kVUp = 64.0f;                        // V is held times 64 / vref in f16
+
+// shared memory: operands (1024-byte aligned), then per-tile values, barriers
+constexpr uint32_t kPrOffQ = 0;                                   // [tile][hi, lo]
+constexpr uint32_t kPrOffK = kPrOffQ + 4 * kTileBytes;
+constexpr uint32_t kPrOffRaw = kPrOffK + kKStages * kTileBytes;   // V codes, 2 slots
+constexpr uint32_t kPrOffV = kPrOffRaw + 2 * kTileBytes;          // V f16, 2 slots of 32 KB
+constexpr uint32_t kPrOffKs = kPrOffV + kVStages * 2 * kTileBytes;  // [kMeta][128] fp32
+constexpr uint32_t kPrOffVs = kPrOffKs + kMeta * 512;             // [kMeta][128] fp32
+constexpr uint32_t kPrOffTile = kPrOffVs + kMeta * 512;           // [kMeta]: mask words 4, vfac, vref, 2 spare
+constexpr uint32_t kPrOffRed = kPrOffTile + kMeta * 32;           // [4] fp32
+constexpr uint32_t kPrOffBar = kPrOffRed + 16;
+enum {
+    kBKFull = 0,                  // [3] K rows landed: 128 cp.async arrivals
+    kBKEmpty = kBKFull + 3,       // [3] scores done with the stage: MMA commit
+    kBVFull = kBKEmpty + 3,       // [2] V converted, factors written: 4 warps
+    kBVEmpty = kBVFull + 2,       // [2] output update done with the slot: MMA commit
+    kBSFull = kBVEmpty + 2,       // [2 tiles] scores in TMEM: MMA commit
+    kBPFull = kBSFull + 2,        // [2 tiles] P written, O rescaled: 4 warps
+    kBODone = kBPFull + 2,        // every product done: MMA commit
+    kBQ = kBODone + 1,            // Q operands written: 8 warps
+    kBCount = kBQ + 1
+};
+constexpr uint32_t kPrOffMisc = kPrOffBar + kBCount * 8;
+constexpr uint32_t kPrSmem = kPrOffMisc + 16;
+static_assert(kPrSmem <= 232448, "shared memory budget");
+
+struct PromptArgs {
+    View c;
+    const uint16_t *q;
+    uint16_t *out;
+    float *lse;
+    float scale_log2;
+    int heads, group;
+    int least;        // requests with at least this many packed rows
+    long long slots;  // row-block slots over all requests (upper bound)
+};
+
+// First row-block slot of request i (see the append kernel's first_slot).
+__device__ __forceinline__ long long first_block(const PromptArgs &a, int i)
+{
+    return (long long)max(__ldg(a.c.row_begin + i), 0) * a.group / kPrRows + i;
+}
+
+// Byte of (row r, 16-byte chunk c) in a 128-byte-row operand, 128-byte swizzle.
+__device__ __forceinline__ uint32_t sw128(int r, int c)
+{
+    return (uint32_t)(r * 128) + (uint32_t)((c ^ (r & 7)) << 4);
+}
+
+// D[tmem] (+)= A[tmem] * B[smem], f16 inputs, fp32 accumulation, one CTA.
+__device__ __forceinline__ void umma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
+                                            uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// 16 consecutive TMEM columns of this thread's lane from registers.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __grid_constant__ PromptArgs a)
+{
+    constexpr int CH = D / 16;  // 16-byte chunks of a cached row
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sbase = smem_u32(smem);
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(kFull, tid >> 5, 0);
+    const View &c = a.c;
+    const int G = a.group;
+
+    // ------------------------------------------------------------ which rows
+    // slots run from the last to the first: a request's last rows see the most tokens
+    const long long item = (long long)gridDim.x - 1 - blockIdx.x;
+    const long long slot = item / c.H;
+    const int h = (int)(item - slot * c.H);
+    int lo = 0, len = c.bs;
+    while (len > 1) {
+        const int step = (len + 31) >> 5;
+        const int at = lo + lane * step;
+        const uint32_t le = __ballot_sync(kFull, lane * step < len && first_block(a, at) <= slot);
+        const int k = max(__popc(le) - 1, 0);
+        lo += k * step;
+        len = min(step, len - k * step);
+    }
+    const int req = lo;
+    const Request q = load_request(c, req, h == 0 && tid == 0);
+    const long long nth = slot - first_block(a, req);
+    const int rows_all = q.n * G;
+    if (rows_all < a.least || nth < 0 || nth * kPrRows >= rows_all)
+        return;  // the same for the whole CTA
+    const int R0 = (int)nth * kPrRows;
+    const int nrow = min(kPrRows, rows_all - R0);
+    const bool two = nrow > 128;
+    const int first_tok = q.ctx - q.n;  // slot of query token 0
+    const int end = max(0, first_tok + (R0 + nrow - 1) / G + 1);  // tokens that some row sees
+    const int T = (end + kPrTok - 1) / kPrTok;
+
+    if (sbase & 1023u) {
+        if (tid == 0)
+            atomicOr(c.status, (uint32_t)PMQA_DEV_INTERNAL);
+        return;
+    }
+    uint64_t *const bar = reinterpret_cast<uint64_t *>(smem + kPrOffBar);
+    uint32_t *const misc = reinterpret_cast<uint32_t *>(smem + kPrOffMisc);
+    volatile int *const abort_flag = reinterpret_cast<volatile int *>(misc + 1);
+    if (tid == 0) {
+        for (int s = 0; s < kKStages; ++s) {
+            mbar_init(&bar[kBKFull + s], 128);
+            mbar_init(&bar[kBKEmpty + s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&bar[kBVFull + s], 4);
+            mbar_init(&bar[kBVEmpty + s], 1);
+            mbar_init(&bar[kBSFull + s], 1);
+            mbar_init(&bar[kBPFull + s], 4);
+        }
+        mbar_init(&bar[kBODone], 1);
+        mbar_init(&bar[kBQ], 8);
+        misc[1] = 0;
+        mbar_init_fence();
+    }
+    if (warp == 12)
+        tmem_alloc(misc, 512);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = misc[0];
+    // columns: S (then P) of tile 0, 1 at 0, 128; O of tile 0, 1 at 256, 384
+    auto fail = [&]() {
+        atomicOr(c.status, (uint32_t)PMQA_DEV_TIMEOUT);
+        *abort_flag = 1;
+    };
+
+    if (warp < 8) {
+        // -------------------------------------------------------- softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");  // 2 x 160 + 2 x 96 = 4 x 128
+        const int tile = warp >> 2;
+        const int row = (warp & 3) * 32 + lane;     // TMEM lane
+        const int R = R0 + tile * 128 + row;
+        const bool has = tile * 128 + row < nrow;
+        const int j = R / G, g = R - j * G;
+        const long long rh = (long long)(q.r0 + j) * a.heads + h * G + g;
+        const int lim = has ? first_tok + j : 0x7FFFFFFF;  // last slot that the row sees
+        float rc;
+        {
+            // the row's q as two e4m3 terms, K-major in the 128-byte swizzle
+            const uint4 *src = reinterpret_cast<const uint4 *>(a.q + rh * D);
+            uint4 u[D / 8];
+#pragma unroll
+            for (int k = 0; k < D / 8; ++k)
+                u[k] = has ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
+            float top = 0.0f;
+#pragma unroll
+            for (int k = 0; k < D / 8; ++k) {
+                const uint32_t e[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+#pragma unroll
+                for (int z = 0; z < 4; ++z)
+                    top = fmaxf(top, fmaxf(fabsf(__uint_as_float(e[z] << 16)),
+                                           fabsf(__uint_as_float(e[z] & 0xFFFF0000u))));
+            }
+            const int e2 = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 120);
+            // a negative scale goes into q, so that c_row >= 0 keeps the order of the scores
+            const float up = copysignf(__uint_as_float((uint32_t)(7 - e2 + 127) << 23), a.scale_log2);
+            rc = fabsf(a.scale_log2) * __uint_as_float((uint32_t)(e2 - 7 + 127) << 23);
+            const uint32_t qd = sbase + kPrOffQ + (uint32_t)tile * 2 * kTileBytes;
+            // an infinite or NaN q would saturate: its scores become NaN through c_row
+            if (!(top < INFINITY))
+                rc = __int_as_float(0x7FFFFFFF);
+            bool nan = false;
+#pragma unroll
+            for (int k = 0; k < D / 8; k += 2) {
+                uint32_t hi[4], lw[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const uint4 &uu = u[k + (y >> 1)];
+                    const uint32_t e0 = (y & 1) ? uu.z : uu.x, e1 = (y & 1) ? uu.w : uu.y;
+                    const float f0 = __uint_as_float(e0 << 16) * up, f1 = __uint_as_float(e0 & 0xFFFF0000u) * up;
+                    const float f2 = __uint_as_float(e1 << 16) * up, f3 = __uint_as_float(e1 & 0xFFFF0000u) * up;
+                    nan |= f0 != f0 || f1 != f1 || f2 != f2 || f3 != f3;
+                    hi[y] = f32x4_to_e4m3x4(f0, f1, f2, f3);
+                    float h0, h1, h2, h3;
+                    e4m3x2_to_f32x2(hi[y] & 0xFFFFu, h0, h1);
+                    e4m3x2_to_f32x2(hi[y] >> 16, h2, h3);
+                    lw[y] = f32x4_to_e4m3x4(f0 - h0, f1 - h1, f2 - h2, f3 - h3);
+                }
+                sts128(qd + sw128(row, k >> 1), hi[0], hi[1], hi[2], hi[3]);
+                sts128(qd + kTileBytes + sw128(row, k >> 1), lw[0], lw[1], lw[2], lw[3]);
+            }
+            if (nan)
+                rc = __int_as_float(0x7FFFFFFF);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&bar[kBQ]);
+        }
+        float m = -INFINITY, l = 0.0f, vref = 0.0f;
+        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + (uint32_t)tile * 128u + lane_off;
+        const uint32_t tO = tmem + 256u + (uint32_t)tile * 128u + lane_off;
+        bool ok = true;
+        if (tile == 0 || two) {
+            for (int t = 0; t < T; ++t) {
+                const uint32_t vph = (uint32_t)(t >> 1) & 1u;
+                ok = ok && mbar_wait(&bar[kBSFull + tile], (uint32_t)t & 1u, abort_flag) &&
+                     mbar_wait(&bar[kBVFull + (t & 1)], vph, abort_flag);
+                if (!__all_sync(kFull, ok)) {
+                    ok = false;
+                    fail();
+                    break;
+                }
+                tc_fence_after_sync();
+                const float4 *const ksp = reinterpret_cast<const float4 *>(smem + kPrOffKs + (t % kMeta) * 512);
+                const uint4 mw = lds128(sbase + kPrOffTile + (uint32_t)(t % kMeta) * 32u);
+                const uint32_t mb = sbase + kPrOffTile + (uint32_t)(t % kMeta) * 32u + 16u;
+                const float vfac = __uint_as_float(lds32(mb));
+                vref = __uint_as_float(lds32(mb + 4u));
+                const int base = t * kPrTok;
+                // nothing of the tile is masked for any row of this warp
+                const bool whole = (mw.x & mw.y & mw.z & mw.w) == 0xFFFFFFFFu &&
+                                   __all_sync(kFull, base + kPrTok - 1 <= lim);
+                const uint32_t msk[4] = {mw.x, mw.y, mw.z, mw.w};
+                // first pass: the row's largest x of the tile
+                float top = -INFINITY;
+#pragma unroll
+                for (int cc = 0; cc < 4; ++cc) {
+                    uint32_t s[32];
+                    tmem_ld32(tS + 32u * cc, s);
+                    tmem_ld_wait();
+                    reg_fence_cols<32>(s);
+#pragma unroll
+                    for (int z = 0; z < 8; ++z) {
+                        const float4 k4 = ksp[8 * cc + z];
+                        float y0, y1, y2, y3;
+                        fmul2(y0, y1, __uint_as_float(s[4 * z]), __uint_as_float(s[4 * z + 1]), k4.x, k4.y);
+                        fmul2(y2, y3, __uint_as_float(s[4 * z + 2]), __uint_as_float(s[4 * z + 3]), k4.z, k4.w);
+                        if (!whole) {
+                            const int b0 = 4 * z;
+                            y0 = (msk[cc] >> b0 & 1u) && base + 32 * cc + b0 <= lim ? y0 : -INFINITY;
+                            y1 = (msk[cc] >> (b0 + 1) & 1u) && base + 32 * cc + b0 + 1 <= lim ? y1 : -INFINITY;
+                            y2 = (msk[cc] >> (b0 + 2) & 1u) && base + 32 * cc + b0 + 2 <= lim ? y2 : -INFINITY;
+                            y3 = (msk[cc] >> (b0 + 3) & 1u) && base + 32 * cc + b0 + 3 <= lim ? y3 : -INFINITY;
+                        }
+                        top = fmaxf(top, fmaxf(fmaxf(y0, y1), fmaxf(y2, y3)));
+                    }
+                }
+                top *= rc;
+                float alpha = vfac;
+                if (top > m + kPrSlack) {
+                    alpha *= ex2_approx(m - top);
+                    l *= ex2_approx(m - top);
+                    m = top;
+                }
+                if (t > 0 && __any_sync(kFull, alpha != 1.0f)) {
+                    // O holds tiles before this one: PV of tile t - 1 is done (SFull)
+#pragma unroll 1
+                    for (int cc = 0; cc < D / 32; ++cc) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + 32u * cc, o);
+                        tmem_ld_wait();
+                        reg_fence_cols<32>(o);
+#pragma unroll
+                        for (int z = 0; z < 32; ++z)
+                            o[z] = __float_as_uint(__uint_as_float(o[z]) * alpha);
+                        tmem_st32(tO + 32u * cc, o);
+                    }
+                }
+                const float ms = m == -INFINITY ? 0.0f : -m;
+                float l0 = 0.0f, l1 = 0.0f;
+#pragma unroll
+                for (int cc = 0; cc < 4; ++cc) {
+                    uint32_t s[32], p[16];
+                    tmem_ld32(tS + 32u * cc, s);
+                    tmem_ld_wait();
+                    reg_fence_cols<32>(s);
+#pragma unroll
+                    for (int z = 0; z < 8; ++z) {
+                        const float4 k4 = ksp[8 * cc + z];
+                        float y0, y1, y2, y3;
+                        fmul2(y0, y1, __uint_as_float(s[4 * z]), __uint_as_float(s[4 * z + 1]), k4.x, k4.y);
+                        fmul2(y2, y3, __uint_as_float(s[4 * z + 2]), __uint_as_float(s[4 * z + 3]), k4.z, k4.w);
+                        float x0 = ms, x1 = ms, x2 = ms, x3 = ms;
+                        ffma2(x0, x1, y0, y1, rc, rc);
+                        ffma2(x2, x3, y2, y3, rc, rc);
+                        if (!whole) {
+                            const int b0 = 4 * z;
+                            x0 = (msk[cc] >> b0 & 1u) && base + 32 * cc + b0 <= lim ? x0 : -INFINITY;
+                            x1 = (msk[cc] >> (b0 + 1) & 1u) && base + 32 * cc + b0 + 1 <= lim ? x1 : -INFINITY;
+                            x2 = (msk[cc] >> (b0 + 2) & 1u) && base + 32 * cc + b0 + 2 <= lim ? x2 : -INFINITY;
+                            x3 = (msk[cc] >> (b0 + 3) & 1u) && base + 32 * cc + b0 + 3 <= lim ? x3 : -INFINITY;
+                        }
+                        x0 = ex2_approx(x0);
+                        x1 = ex2_approx(x1);
+                        x2 = ex2_approx(x2);
+                        x3 = ex2_approx(x3);
+                        fadd2(l0, l1, x0, x1);
+                        fadd2(l0, l1, x2, x3);
+                        p[2 * z] = pack_f16x2(x0, x1);
+                        p[2 * z + 1] = pack_f16x2(x2, x3);
+                    }
+                    tmem_st16(tS + 16u * cc, p);
+                }
+                l += l0 + l1;
+                tmem_st_wait();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&bar[kBPFull + tile]);
+            }
+            // -------------------------------------------------------- output
+            ok = ok && mbar_wait(&bar[kBODone], 0u, abort_flag);
+            if (__all_sync(kFull, ok)) {
+                tc_fence_after_sync();
+                const float f = l == 0.0f ? 0.0f : vref * (1.0f / kVUp) / l;
+#pragma unroll 1
+                for (int cc = 0; cc < D / 32; ++cc) {
+                    uint32_t o[32];
+                    if (T > 0) {
+                        tmem_ld32(tO + 32u * cc, o);
+                        tmem_ld_wait();
+                        reg_fence_cols<32>(o);
+                    }
+                    if (has) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(a.out + rh * D + 32 * cc);
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            uint32_t b[4];
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) {
+                                const float f0 = l == 0.0f ? 0.0f : __uint_as_float(o[8 * z + 2 * y]) * f;
+                                const float f1 = l == 0.0f ? 0.0f : __uint_as_float(o[8 * z + 2 * y + 1]) * f;
+                                b[y] = __bfloat16_as_ushort(__float2bfloat16_rn(f0)) |
+                                       (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(f1)) << 16;
+                            }
+                            dst[z] = make_uint4(b[0], b[1], b[2], b[3]);
+                        }
+                    }
+                }
+                if (has && a.lse)
+                    a.lse[rh] = l == 0.0f ? -INFINITY : (m == -INFINITY ? l : (m + log2f(l)) * kLn2);
+            } else {
+                fail();
+            }
+        }
+    } else if (warp < 12) {
+        // -------------------------------------------------------- loader
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        // thread = token of a tile for the look-ups; a warp copies its 32 rows
+        const int lt = tid - 256, lw = lt >> 5;
+        const int32_t *const bt = c.bt + (long long)req * c.W;
+        struct Row {
+            long long phys;  // block * H + h, -1 for none
+            int off;         // row within the block
+        };
+        auto look_up = [&](int t) -> int {
+            const int tok = t * kPrTok + lt;
+            return t < T && tok < end ? __ldg(bt + c.page_of(tok)) : -1;
+        };
+        auto row_of = [&](int t, int page) -> Row {
+            const int tok = t * kPrTok + lt;
+            Row r{-1, 0};
+            if (t < T && tok < end) {
+                if (page < 0 || (long long)page >= c.nb) {
+                    atomicOr(c.status, (uint32_t)PMQA_DEV_BAD_BLOCK_ID);
+                } else {
+                    r.phys = (long long)page * c.H + h;
+                    r.off = tok - c.page_of(tok) * c.P;
+                }
+            }
+            return r;
+        };
+        // K rows, both scales and the mask of tile t; V codes of tile t
+        auto copy_rows = [&](const uint8_t *pool, uint32_t dst, const Row &r, bool swz) {
+            const long long byte = r.phys < 0 ? -1 : (r.phys * c.P + r.off) * D;
+            constexpr int PER = 32 / CH;
+            const int ch = lane % CH;
+#pragma unroll
+            for (int k = 0; k < 32 / PER; ++k) {
+                const int rr = k * PER + lane / CH;
+                const long long src = __shfl_sync(kFull, byte, rr);
+                const int rt = lw * 32 + rr;
+                cp_async_16(dst + (swz ? sw128(rt, ch) : (uint32_t)(rt * 128 + ch * 16)),
+                            pool + (src < 0 ? 0 : src) + ch * 16, src < 0 ? 0u : 16u);
+            }
+        };
+        auto load_k = [&](int t, const Row &r) {
+            const uint32_t ks = sbase + kPrOffKs + (uint32_t)(t % kMeta) * 512u + (uint32_t)lt * 4u;
+            const uint32_t vs = sbase + kPrOffVs + (uint32_t)(t % kMeta) * 512u + (uint32_t)lt * 4u;
+            const uint32_t mask = __ballot_sync(kFull, r.phys >= 0);
+            if (lane == 0)
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(sbase + kPrOffTile + (uint32_t)(t % kMeta) * 32u + (uint32_t)lw * 4u), "r"(mask) : "memory");
+            if (r.phys >= 0) {
+                cp_async_4(ks, c.ks + r.phys);
+                cp_async_4(vs, c.vs + r.phys);
+            } else {
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(ks), "r"(0) : "memory");
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(vs), "r"(0) : "memory");
+            }
+            copy_rows(c.k, sbase + kPrOffK + (uint32_t)(t % kKStages) * kTileBytes, r, true);
+        };
+        // K runs two tiles ahead of the conversion, V codes one
+        int pg0 = look_up(0), pg1 = look_up(1), pg2 = look_up(2);
+        Row r0 = row_of(0, pg0), r1 = row_of(1, pg1);
+        if (T > 0) {
+            load_k(0, r0);
+            cp_async_arrive_noinc(&bar[kBKFull + 0]);
+            copy_rows(c.v, sbase + kPrOffRaw, r0, false);
+        }
+        cp_async_commit();
+        if (T > 1) {
+            load_k(1, r1);
+            cp_async_arrive_noinc(&bar[kBKFull + 1]);
+        }
+        cp_async_commit();
+        float vref = 0.0f;
+        bool ok = true;
+        for (int t = 0; t < T; ++t) {
+            const int pg3 = look_up(t + 3);
+            const Row r2 = row_of(t + 2, pg2);
+            if (t + 2 < T) {
+                const int st = (t + 2) % kKStages;
+                ok = ok && mbar_wait(&bar[kBKEmpty + st], ((uint32_t)((t + 2) / kKStages) & 1u) ^ 1u, abort_flag);
+                if (__all_sync(kFull, ok)) {
+                    load_k(t + 2, r2);
+                    cp_async_arrive_noinc(&bar[kBKFull + st]);
+                } else {
+                    ok = false;
+                }
+            }
+            cp_async_commit();
+            // all but the K rows just issued: V codes and scales of tile t
+            cp_async_wait_group<1>();
+            ok = ok && mbar_wait(&bar[kBVEmpty + (t & 1)], ((uint32_t)(t >> 1) & 1u) ^ 1u, abort_flag);
+            float *const red = reinterpret_cast<float *>(smem + kPrOffRed);
+            if (!named_bar_and(1, 128, ok)) {
+                fail();
+                break;
+            }
+            // every thread is done with tile t - 1's codes: their slot takes tile t + 1's
+            if (t + 1 < T)
+                copy_rows(c.v, sbase + kPrOffRaw + (uint32_t)((t + 1) & 1) * kTileBytes, r1, false);
+            cp_async_commit();
+            r1 = r2;
+            pg2 = pg3;
+            // vref: the largest |scale| so far
+            float vmax = fabsf(__uint_as_float(lds32(sbase + kPrOffVs + (uint32_t)(t % kMeta) * 512u + (uint32_t)lt * 4u)));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                vmax = fmaxf(vmax, __shfl_xor_sync(kFull, vmax, o));
+            if (lane == 0)
+                red[lw] = vmax;
+            named_bar_sync(1, 128);
+            vmax = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+            const float vnew = vmax > vref && vmax > 1e-36f ? vmax : vref;
+            const float vfac = vnew > vref ? vref / vnew : 1.0f;
+            vref = vnew;
+            const float vinv = vref > 0.0f ? kVUp / vref : 0.0f;
+            if (lt == 0)
+                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(sbase + kPrOffTile + (uint32_t)(t % kMeta) * 32u + 16u),
+                             "r"(__float_as_uint(vfac)), "r"(__float_as_uint(vref)) : "memory");
+            const uint32_t raw = sbase + kPrOffRaw + (uint32_t)(t & 1) * kTileBytes;
+            const uint32_t vd = sbase + kPrOffV + (uint32_t)(t & 1) * 2 * kTileBytes;
+            const uint32_t vsb = sbase + kPrOffVs + (uint32_t)(t % kMeta) * 512u;
+            const int ch = lt % CH;
+#pragma unroll
+            for (int k = 0; k < CH; ++k) {
+                const int tok = k * (128 / CH) + lt / CH;
+                const uint4 u = lds128(raw + (uint32_t)(tok * 128 + ch * 16));
+                const float f = __uint_as_float(lds32(vsb + (uint32_t)tok * 4u)) * vinv;
+                const uint32_t f2 = pack_f16x2(f, f);
+                uint32_t o[8];
+                e4m3x4_to_f16x2(u.x, o[0], o[1]);
+                e4m3x4_to_f16x2(u.y, o[2], o[3]);
+                e4m3x4_to_f16x2(u.z, o[4], o[5]);
+                e4m3x4_to_f16x2(u.w, o[6], o[7]);
+#pragma unroll
+                for (int y = 0; y < 8; ++y)
+                    asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(o[y]) : "r"(f2));
+                // value columns 16 ch .. 16 ch + 15: chunks 2 ch, 2 ch + 1 of 8 columns each
+                const uint32_t blk = vd + (uint32_t)(ch >> 2) * kTileBytes;
+                const int c0 = (2 * ch) & 7;
+                sts128(blk + sw128(tok, c0), o[0], o[1], o[2], o[3]);
+                sts128(blk + sw128(tok, c0 + 1), o[4], o[5], o[6], o[7]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&bar[kBVFull + (t & 1)]);
+        }
+        cp_async_wait_all();
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        if (warp == 12 && lane == 0) {
+        // -------------------------------------------------------- products
+        constexpr uint32_t idq = idesc_e4m3_f32(128, 128);
+        constexpr uint32_t idv = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | (8u << 24);
+        const int tiles = two ? 2 : 1;
+        auto scores = [&](int t, int tile) {
+            const uint32_t qd = sbase + kPrOffQ + (uint32_t)tile * 2 * kTileBytes;
+            const uint64_t kd = sw128_kmajor_desc(sbase + kPrOffK + (uint32_t)(t % kKStages) * kTileBytes);
+#pragma unroll
+            for (int term = 0; term < 2; ++term) {
+                const uint64_t ad = sw128_kmajor_desc(qd + (uint32_t)term * kTileBytes);
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k)
+                    umma_e4m3(tmem + (uint32_t)tile * 128u, ad + 2u * k, kd + 2u * k, idq, (term | k) ? 1u : 0u);
+            }
+            umma_commit(&bar[kBSFull + tile]);
+        };
+        bool ok = T == 0 || (mbar_wait(&bar[kBQ], 0u, abort_flag) && mbar_wait(&bar[kBKFull], 0u, abort_flag));
+        if (ok && T > 0) {
+            fence_proxy_async_smem();
+            tc_fence_after_sync();
+            for (int tile = 0; tile < tiles; ++tile)
+                scores(0, tile);
+            umma_commit(&bar[kBKEmpty]);
+        }
+        for (int t = 0; ok && t < T; ++t) {
+            const bool more = t + 1 < T;
+            ok = mbar_wait(&bar[kBVFull + (t & 1)], (uint32_t)(t >> 1) & 1u, abort_flag);
+            if (more)
+                ok = ok && mbar_wait(&bar[kBKFull + (t + 1) % kKStages], (uint32_t)((t + 1) / kKStages) & 1u, abort_flag);
+            if (!ok)
+                break;
+            fence_proxy_async_smem();
+            for (int tile = 0; ok && tile < tiles; ++tile) {
+                ok = mbar_wait(&bar[kBPFull + tile], (uint32_t)t & 1u, abort_flag);
+                if (!ok)
+                    break;
+                tc_fence_after_sync();
+                const uint32_t vd = sbase + kPrOffV + (uint32_t)(t & 1) * 2 * kTileBytes;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    umma_f16_ts(tmem + 256u + (uint32_t)tile * 128u, tmem + (uint32_t)tile * 128u + 8u * k,
+                                sw128_mnmajor_desc(vd + (uint32_t)k * 2048u, kTileBytes, 1024u), idv,
+                                (t | k) ? 1u : 0u);
+                if (tile == tiles - 1)
+                    umma_commit(&bar[kBVEmpty + (t & 1)]);
+                if (more)
+                    scores(t + 1, tile);
+                if (more && tile == tiles - 1)
+                    umma_commit(&bar[kBKEmpty + (t + 1) % kKStages]);
+            }
+        }
+        if (!ok)
+            fail();
+        umma_commit(&bar[kBODone]);
+        if (!mbar_wait(&bar[kBODone], 0u, nullptr))
+            atomicOr(c.status, (uint32_t)PMQA_DEV_TIMEOUT);
+        }
+    }
+    __syncwarp();
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 12) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Requests with at least `least` packed rows (rows * group).
+cudaError_t launch_attn_prompt(AttnCall &q, int least, cudaStream_t st)
+{
+    PromptArgs a{};
+    a.c = q.c;
+    a.q = static_cast<const uint16_t *>(q.q);
+    a.out = static_cast<uint16_t *>(q.out);
+    a.lse = q.lse;
+    a.scale_log2 = q.sm_scale * kLog2e;
+    a.heads = q.heads;
+    a.group = q.heads / q.c.H;
+    a.least = least;
+    a.slots = (long long)q.c.rows * a.group / kPrRows + q.c.bs;
+    const long long grid = a.slots * q.c.H;
+    if (grid > 0x7FFFFFFFll)
+        return cudaErrorInvalidConfiguration;
+    static std::atomic<uint64_t> done64{0}, done128{0};
+    cudaError_t e = q.c.D == 128 ? allow_smem(cache_prompt_kernel<128>, (int)kPrSmem, done128)
+                                 : allow_smem(cache_prompt_kernel<64>, (int)kPrSmem, done64);
+    if (e != cudaSuccess)
+        return e;
+    if (q.c.D == 128)
+        cache_prompt_kernel<128><<<(unsigned)grid, kPrThreads, kPrSmem, st>>>(a);
+    else
+        cache_prompt_kernel<64><<<(unsigned)grid, kPrThreads, kPrSmem, st>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace cache
+}  // namespace pmqa
