@@ -35,7 +35,7 @@ namespace cache {
 constexpr int kPrRows = 256;      // packed rows per CTA (two tiles of 128)
 constexpr int kPrTok = 128;       // tokens per tile
 constexpr int kPrThreads = 512;
-constexpr int kKStages = 3, kVStages = 2, kMeta = 4;
+constexpr int kKStages = 2, kRawSlots = 3, kVStages = 2, kMeta = 4;
 constexpr uint32_t kTileBytes = 128 * 128;           // 128 rows of 128 bytes
 constexpr float kPrSlack = 8.0f;                     // p <= 2^8 before the maximum moves
 constexpr float kVUp = 64.0f;                        // V is held times 64 / vref in f16
@@ -43,17 +43,17 @@ constexpr float kVUp = 64.0f;                        // V is held times 64 / vre
 // shared memory: operands (1024-byte aligned), then per-tile values, barriers
 constexpr uint32_t kPrOffQ = 0;                                   // [tile][hi, lo]
 constexpr uint32_t kPrOffK = kPrOffQ + 4 * kTileBytes;
-constexpr uint32_t kPrOffRaw = kPrOffK + kKStages * kTileBytes;   // V codes, 2 slots
-constexpr uint32_t kPrOffV = kPrOffRaw + 2 * kTileBytes;          // V f16, 2 slots of 32 KB
+constexpr uint32_t kPrOffRaw = kPrOffK + kKStages * kTileBytes;   // V codes, 3 slots
+constexpr uint32_t kPrOffV = kPrOffRaw + kRawSlots * kTileBytes;          // V f16, 2 slots of 32 KB
 constexpr uint32_t kPrOffKs = kPrOffV + kVStages * 2 * kTileBytes;  // [kMeta][128] fp32
 constexpr uint32_t kPrOffVs = kPrOffKs + kMeta * 512;             // [kMeta][128] fp32
 constexpr uint32_t kPrOffTile = kPrOffVs + kMeta * 512;           // [kMeta]: mask words 4, vfac, vref, 2 spare
 constexpr uint32_t kPrOffRed = kPrOffTile + kMeta * 32;           // [4] fp32
 constexpr uint32_t kPrOffBar = kPrOffRed + 16;
 enum {
-    kBKFull = 0,                  // [3] K rows landed: 128 cp.async arrivals
-    kBKEmpty = kBKFull + 3,       // [3] scores done with the stage: MMA commit
-    kBVFull = kBKEmpty + 3,       // [2] V converted, factors written: 4 warps
+    kBKFull = 0,                  // [2] K rows landed: 128 cp.async arrivals
+    kBKEmpty = kBKFull + kKStages,  // [2] scores done with the stage: MMA commit
+    kBVFull = kBKEmpty + kKStages,       // [2] V converted, factors written: 4 warps
     kBVEmpty = kBVFull + 2,       // [2] output update done with the slot: MMA commit
     kBSFull = kBVEmpty + 2,       // [2 tiles] scores in TMEM: MMA commit
     kBPFull = kBSFull + 2,        // [2 tiles] P written, O rescaled: 4 warps
@@ -109,6 +109,88 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r)
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
+}
+
+// Four scores times their tokens' scales; MASK: -inf for a token that does not
+// exist (bits of `have`) or lies behind the row's last slot `lim`.
+template <bool MASK>
+__device__ __forceinline__ void scaled4(const uint32_t *s, const float4 &k, uint32_t have, int col, int lim,
+                                        float (&y)[4])
+{
+    fmul2(y[0], y[1], __uint_as_float(s[0]), __uint_as_float(s[1]), k.x, k.y);
+    fmul2(y[2], y[3], __uint_as_float(s[2]), __uint_as_float(s[3]), k.z, k.w);
+    if constexpr (MASK) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            y[e] = (have >> e & 1u) && col + e <= lim ? y[e] : -INFINITY;
+    }
+}
+
+// The largest scaled score of this thread's row (128 columns from tS). The
+// loops over column chunks stay rolled: unrolled, the two passes and their
+// masked forms outgrow the instruction cache (882 us against 580 on 6415 rows
+// of 32 heads).
+template <bool MASK>
+__device__ __forceinline__ float row_max(uint32_t tS, const float4 *ks, uint32_t tb, int lim)
+{
+    float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll 1
+    for (int cc = 0; cc < 4; ++cc) {
+        uint32_t s[32];
+        tmem_ld32(tS + 32u * cc, s);
+        const uint32_t have = MASK ? lds32(tb + 4u * cc) : 0u;
+        tmem_ld_wait();
+        reg_fence_cols<32>(s);
+#pragma unroll
+        for (int z = 0; z < 8; ++z) {
+            float y[4];
+            scaled4<MASK>(s + 4 * z, ks[8 * cc + z], have >> (4 * z), 32 * cc + 4 * z, lim, y);
+            t0 = fmaxf(t0, fmaxf(y[0], y[1]));
+            t1 = fmaxf(t1, fmaxf(y[2], y[3]));
+        }
+    }
+    return fmaxf(t0, t1);
+}
+
+// p = 2^(y rc + ms) of the row's columns, written as f16 pairs from column tS
+// on (chunk cc's 16 columns lie within scores already read); returns their sum.
+template <bool MASK>
+__device__ __forceinline__ float weights(uint32_t tS, const float4 *ks, uint32_t tb, int lim, float rc, float ms)
+{
+    float l0 = 0.0f, l1 = 0.0f;
+#pragma unroll 1
+    for (int cc = 0; cc < 4; ++cc) {
+        uint32_t s[32], p[16];
+        tmem_ld32(tS + 32u * cc, s);
+        const uint32_t have = MASK ? lds32(tb + 4u * cc) : 0u;
+        tmem_ld_wait();
+        reg_fence_cols<32>(s);
+#pragma unroll
+        for (int z = 0; z < 8; ++z) {
+            float y[4], x0 = ms, x1 = ms, x2 = ms, x3 = ms;
+            scaled4<false>(s + 4 * z, ks[8 * cc + z], 0u, 0, 0, y);
+            ffma2(x0, x1, y[0], y[1], rc, rc);
+            ffma2(x2, x3, y[2], y[3], rc, rc);
+            if constexpr (MASK) {
+                // after the product: c_row may be 0
+                const int col = 32 * cc + 4 * z;
+                x0 = (have >> (4 * z) & 1u) && col <= lim ? x0 : -INFINITY;
+                x1 = (have >> (4 * z + 1) & 1u) && col + 1 <= lim ? x1 : -INFINITY;
+                x2 = (have >> (4 * z + 2) & 1u) && col + 2 <= lim ? x2 : -INFINITY;
+                x3 = (have >> (4 * z + 3) & 1u) && col + 3 <= lim ? x3 : -INFINITY;
+            }
+            x0 = ex2_approx(x0);
+            x1 = ex2_approx(x1);
+            x2 = ex2_approx(x2);
+            x3 = ex2_approx(x3);
+            fadd2(l0, l1, x0, x1);
+            fadd2(l0, l1, x2, x3);
+            p[2 * z] = pack_f16x2(x0, x1);
+            p[2 * z + 1] = pack_f16x2(x2, x3);
+        }
+        tmem_st16(tS + 16u * cc, p);
+    }
+    return l0 + l1;
 }
 
 template <int D>
@@ -264,39 +346,16 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
                 }
                 tc_fence_after_sync();
                 const float4 *const ksp = reinterpret_cast<const float4 *>(smem + kPrOffKs + (t % kMeta) * 512);
-                const uint4 mw = lds128(sbase + kPrOffTile + (uint32_t)(t % kMeta) * 32u);
-                const uint32_t mb = sbase + kPrOffTile + (uint32_t)(t % kMeta) * 32u + 16u;
-                const float vfac = __uint_as_float(lds32(mb));
-                vref = __uint_as_float(lds32(mb + 4u));
+                const uint32_t tb = sbase + kPrOffTile + (uint32_t)(t % kMeta) * 32u;
+                const uint4 mw = lds128(tb);
+                const float vfac = __uint_as_float(lds32(tb + 16u));
+                vref = __uint_as_float(lds32(tb + 20u));
                 const int base = t * kPrTok;
                 // nothing of the tile is masked for any row of this warp
                 const bool whole = (mw.x & mw.y & mw.z & mw.w) == 0xFFFFFFFFu &&
                                    __all_sync(kFull, base + kPrTok - 1 <= lim);
-                const uint32_t msk[4] = {mw.x, mw.y, mw.z, mw.w};
-                // first pass: the row's largest x of the tile
-                float top = -INFINITY;
-#pragma unroll
-                for (int cc = 0; cc < 4; ++cc) {
-                    uint32_t s[32];
-                    tmem_ld32(tS + 32u * cc, s);
-                    tmem_ld_wait();
-                    reg_fence_cols<32>(s);
-#pragma unroll
-                    for (int z = 0; z < 8; ++z) {
-                        const float4 k4 = ksp[8 * cc + z];
-                        float y0, y1, y2, y3;
-                        fmul2(y0, y1, __uint_as_float(s[4 * z]), __uint_as_float(s[4 * z + 1]), k4.x, k4.y);
-                        fmul2(y2, y3, __uint_as_float(s[4 * z + 2]), __uint_as_float(s[4 * z + 3]), k4.z, k4.w);
-                        if (!whole) {
-                            const int b0 = 4 * z;
-                            y0 = (msk[cc] >> b0 & 1u) && base + 32 * cc + b0 <= lim ? y0 : -INFINITY;
-                            y1 = (msk[cc] >> (b0 + 1) & 1u) && base + 32 * cc + b0 + 1 <= lim ? y1 : -INFINITY;
-                            y2 = (msk[cc] >> (b0 + 2) & 1u) && base + 32 * cc + b0 + 2 <= lim ? y2 : -INFINITY;
-                            y3 = (msk[cc] >> (b0 + 3) & 1u) && base + 32 * cc + b0 + 3 <= lim ? y3 : -INFINITY;
-                        }
-                        top = fmaxf(top, fmaxf(fmaxf(y0, y1), fmaxf(y2, y3)));
-                    }
-                }
+                // first pass: the row's largest score of the tile
+                float top = whole ? row_max<false>(tS, ksp, tb, lim - base) : row_max<true>(tS, ksp, tb, lim - base);
                 top *= rc;
                 float alpha = vfac;
                 if (top > m + kPrSlack) {
@@ -318,42 +377,10 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
                         tmem_st32(tO + 32u * cc, o);
                     }
                 }
+                // second pass: the weights, as f16, over the columns that held the scores
                 const float ms = m == -INFINITY ? 0.0f : -m;
-                float l0 = 0.0f, l1 = 0.0f;
-#pragma unroll
-                for (int cc = 0; cc < 4; ++cc) {
-                    uint32_t s[32], p[16];
-                    tmem_ld32(tS + 32u * cc, s);
-                    tmem_ld_wait();
-                    reg_fence_cols<32>(s);
-#pragma unroll
-                    for (int z = 0; z < 8; ++z) {
-                        const float4 k4 = ksp[8 * cc + z];
-                        float y0, y1, y2, y3;
-                        fmul2(y0, y1, __uint_as_float(s[4 * z]), __uint_as_float(s[4 * z + 1]), k4.x, k4.y);
-                        fmul2(y2, y3, __uint_as_float(s[4 * z + 2]), __uint_as_float(s[4 * z + 3]), k4.z, k4.w);
-                        float x0 = ms, x1 = ms, x2 = ms, x3 = ms;
-                        ffma2(x0, x1, y0, y1, rc, rc);
-                        ffma2(x2, x3, y2, y3, rc, rc);
-                        if (!whole) {
-                            const int b0 = 4 * z;
-                            x0 = (msk[cc] >> b0 & 1u) && base + 32 * cc + b0 <= lim ? x0 : -INFINITY;
-                            x1 = (msk[cc] >> (b0 + 1) & 1u) && base + 32 * cc + b0 + 1 <= lim ? x1 : -INFINITY;
-                            x2 = (msk[cc] >> (b0 + 2) & 1u) && base + 32 * cc + b0 + 2 <= lim ? x2 : -INFINITY;
-                            x3 = (msk[cc] >> (b0 + 3) & 1u) && base + 32 * cc + b0 + 3 <= lim ? x3 : -INFINITY;
-                        }
-                        x0 = ex2_approx(x0);
-                        x1 = ex2_approx(x1);
-                        x2 = ex2_approx(x2);
-                        x3 = ex2_approx(x3);
-                        fadd2(l0, l1, x0, x1);
-                        fadd2(l0, l1, x2, x3);
-                        p[2 * z] = pack_f16x2(x0, x1);
-                        p[2 * z + 1] = pack_f16x2(x2, x3);
-                    }
-                    tmem_st16(tS + 16u * cc, p);
-                }
-                l += l0 + l1;
+                l += whole ? weights<false>(tS, ksp, tb, lim - base, rc, ms)
+                           : weights<true>(tS, ksp, tb, lim - base, rc, ms);
                 tmem_st_wait();
                 tc_fence_before_sync();
                 __syncwarp();
@@ -451,50 +478,46 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
             }
             copy_rows(c.k, sbase + kPrOffK + (uint32_t)(t % kKStages) * kTileBytes, r, true);
         };
-        // K runs two tiles ahead of the conversion, V codes one
-        int pg0 = look_up(0), pg1 = look_up(1), pg2 = look_up(2);
-        Row r0 = row_of(0, pg0), r1 = row_of(1, pg1);
-        if (T > 0) {
-            load_k(0, r0);
-            cp_async_arrive_noinc(&bar[kBKFull + 0]);
-            copy_rows(c.v, sbase + kPrOffRaw, r0, false);
+        // both run two tiles ahead of the conversion; a tile's scales come with its K rows
+        int pg2 = look_up(2);
+        {
+            const Row r0 = row_of(0, look_up(0)), r1 = row_of(1, look_up(1));
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const Row &r = t ? r1 : r0;
+                if (t < T)
+                    copy_rows(c.v, sbase + kPrOffRaw + (uint32_t)t * kTileBytes, r, false);
+                cp_async_commit();
+                if (t < T) {
+                    load_k(t, r);
+                    cp_async_arrive_noinc(&bar[kBKFull + t]);
+                }
+                cp_async_commit();
+            }
         }
-        cp_async_commit();
-        if (T > 1) {
-            load_k(1, r1);
-            cp_async_arrive_noinc(&bar[kBKFull + 1]);
-        }
-        cp_async_commit();
         float vref = 0.0f;
         bool ok = true;
+        float *const red = reinterpret_cast<float *>(smem + kPrOffRed);
+        int raw_slot = 0;
         for (int t = 0; t < T; ++t) {
             const int pg3 = look_up(t + 3);
             const Row r2 = row_of(t + 2, pg2);
-            if (t + 2 < T) {
-                const int st = (t + 2) % kKStages;
-                ok = ok && mbar_wait(&bar[kBKEmpty + st], ((uint32_t)((t + 2) / kKStages) & 1u) ^ 1u, abort_flag);
-                if (__all_sync(kFull, ok)) {
-                    load_k(t + 2, r2);
-                    cp_async_arrive_noinc(&bar[kBKFull + st]);
-                } else {
-                    ok = false;
-                }
-            }
-            cp_async_commit();
-            // all but the K rows just issued: V codes and scales of tile t
-            cp_async_wait_group<1>();
+            pg2 = pg3;
+            // all but tile t + 1's two groups: V codes and scales of tile t
+            cp_async_wait_group<2>();
             ok = ok && mbar_wait(&bar[kBVEmpty + (t & 1)], ((uint32_t)(t >> 1) & 1u) ^ 1u, abort_flag);
-            float *const red = reinterpret_cast<float *>(smem + kPrOffRed);
             if (!named_bar_and(1, 128, ok)) {
                 fail();
                 break;
             }
-            // every thread is done with tile t - 1's codes: their slot takes tile t + 1's
-            if (t + 1 < T)
-                copy_rows(c.v, sbase + kPrOffRaw + (uint32_t)((t + 1) & 1) * kTileBytes, r1, false);
+            const uint32_t raw = sbase + kPrOffRaw + (uint32_t)raw_slot * kTileBytes;
+            // every thread is done with tile t - 1's codes: their slot takes tile t + 2's
+            if (t + 2 < T)
+                copy_rows(c.v, sbase + kPrOffRaw + (uint32_t)(raw_slot == 0 ? 2 : raw_slot - 1) * kTileBytes, r2,
+                          false);
             cp_async_commit();
-            r1 = r2;
-            pg2 = pg3;
+            if (++raw_slot == kRawSlots)
+                raw_slot = 0;
             // vref: the largest |scale| so far
             float vmax = fabsf(__uint_as_float(lds32(sbase + kPrOffVs + (uint32_t)(t % kMeta) * 512u + (uint32_t)lt * 4u)));
 #pragma unroll
@@ -511,7 +534,6 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
             if (lt == 0)
                 asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(sbase + kPrOffTile + (uint32_t)(t % kMeta) * 32u + 16u),
                              "r"(__float_as_uint(vfac)), "r"(__float_as_uint(vref)) : "memory");
-            const uint32_t raw = sbase + kPrOffRaw + (uint32_t)(t & 1) * kTileBytes;
             const uint32_t vd = sbase + kPrOffV + (uint32_t)(t & 1) * 2 * kTileBytes;
             const uint32_t vsb = sbase + kPrOffVs + (uint32_t)(t % kMeta) * 512u;
             const int ch = lt % CH;
@@ -539,6 +561,16 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&bar[kBVFull + (t & 1)]);
+            if (t + 2 < T) {
+                const int st = t % kKStages;  // freed by the scores of tile t
+                ok = mbar_wait(&bar[kBKEmpty + st], (uint32_t)(t / kKStages) & 1u, abort_flag);
+                ok = __all_sync(kFull, ok);
+                if (ok) {
+                    load_k(t + 2, r2);
+                    cp_async_arrive_noinc(&bar[kBKFull + st]);
+                }
+            }
+            cp_async_commit();
         }
         cp_async_wait_all();
     } else {
