@@ -47,7 +47,7 @@ constexpr uint32_t kPrOffRaw = kPrOffK + kKStages * kTileBytes;   // V codes, 3 
 constexpr uint32_t kPrOffV = kPrOffRaw + kRawSlots * kTileBytes;          // V f16, 2 slots of 32 KB
 constexpr uint32_t kPrOffKs = kPrOffV + kVStages * 2 * kTileBytes;  // [kMeta][128] fp32
 constexpr uint32_t kPrOffVs = kPrOffKs + kMeta * 512;             // [kMeta][128] fp32
-constexpr uint32_t kPrOffTile = kPrOffVs + kMeta * 512;           // [kMeta]: mask words 4, vfac, vref, 2 spare
+constexpr uint32_t kPrOffTile = kPrOffVs + kMeta * 512;           // [kMeta]: 4 mask words, vfac, vref, 4 bytes: even scales
 constexpr uint32_t kPrOffRed = kPrOffTile + kMeta * 32;           // [4] fp32
 constexpr uint32_t kPrOffBar = kPrOffRed + 16;
 enum {
@@ -111,82 +111,121 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r)
         : "memory");
 }
 
-// Four scores times their tokens' scales; MASK: -inf for a token that does not
-// exist (bits of `have`) or lies behind the row's last slot `lim`.
-template <bool MASK>
-__device__ __forceinline__ void scaled4(const uint32_t *s, const float4 &k, uint32_t have, int col, int lim,
-                                        float (&y)[4])
+// How the scores of a tile are read. kEven: every token counts and each 32 of
+// them share one scale that is not negative (a block that covers them, or equal
+// scales); kWhole: every token counts, a scale each; kMasked: tokens that do not
+// exist (mask words) or lie behind the row's last slot `lim` are -inf.
+enum { kEven, kWhole, kMasked };
+
+__device__ __forceinline__ float max3(float a, float b, float c)
 {
-    fmul2(y[0], y[1], __uint_as_float(s[0]), __uint_as_float(s[1]), k.x, k.y);
-    fmul2(y[2], y[3], __uint_as_float(s[2]), __uint_as_float(s[3]), k.z, k.w);
-    if constexpr (MASK) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            y[e] = (have >> e & 1u) && col + e <= lim ? y[e] : -INFINITY;
-    }
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// (d0, d1) = (a0, a1) * b + c with b and c pairs held in 64 bits.
+__device__ __forceinline__ void ffma2_to(float &d0, float &d1, float a0, float a1, uint64_t b, uint64_t c)
+{
+    asm("{\n\t.reg .b64 ra, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\t"
+        "fma.rn.f32x2 rd, ra, %4, %5;\n\t"
+        "mov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "l"(b), "l"(c));
+}
+
+__device__ __forceinline__ uint64_t pair(float x)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(x));
+    return r;
 }
 
 // The largest scaled score of this thread's row (128 columns from tS). The
 // loops over column chunks stay rolled: unrolled, the two passes and their
-// masked forms outgrow the instruction cache (882 us against 580 on 6415 rows
-// of 32 heads).
-template <bool MASK>
-__device__ __forceinline__ float row_max(uint32_t tS, const float4 *ks, uint32_t tb, int lim)
+// three forms outgrow the instruction cache (882 us against 543 on 6415 rows of
+// 32 heads).
+template <int HOW>
+__device__ __forceinline__ float row_max(uint32_t tS, const float *ks, uint32_t tb, int lim)
 {
-    float t0 = -INFINITY, t1 = -INFINITY;
+    float top = -INFINITY;
 #pragma unroll 1
     for (int cc = 0; cc < 4; ++cc) {
-        uint32_t s[32];
-        tmem_ld32(tS + 32u * cc, s);
-        const uint32_t have = MASK ? lds32(tb + 4u * cc) : 0u;
+        uint32_t r[32];
+        tmem_ld32(tS + 32u * cc, r);
+        const uint32_t have = HOW == kMasked ? lds32(tb + 4u * cc) : 0u;
+        const float kc = HOW == kEven ? ks[32 * cc] : 0.0f;
         tmem_ld_wait();
-        reg_fence_cols<32>(s);
+        reg_fence_cols<32>(r);
+        float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
-        for (int z = 0; z < 8; ++z) {
+        for (int z = 0; z < 32; z += 4) {
             float y[4];
-            scaled4<MASK>(s + 4 * z, ks[8 * cc + z], have >> (4 * z), 32 * cc + 4 * z, lim, y);
-            t0 = fmaxf(t0, fmaxf(y[0], y[1]));
-            t1 = fmaxf(t1, fmaxf(y[2], y[3]));
+            if constexpr (HOW == kEven) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    y[e] = __uint_as_float(r[z + e]);
+            } else {
+                const float4 k = *reinterpret_cast<const float4 *>(ks + 32 * cc + z);
+                fmul2(y[0], y[1], __uint_as_float(r[z]), __uint_as_float(r[z + 1]), k.x, k.y);
+                fmul2(y[2], y[3], __uint_as_float(r[z + 2]), __uint_as_float(r[z + 3]), k.z, k.w);
+            }
+            if constexpr (HOW == kMasked) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    y[e] = (have >> (z + e) & 1u) && 32 * cc + z + e <= lim ? y[e] : -INFINITY;
+            }
+            t0 = max3(t0, y[0], y[1]);
+            t1 = max3(t1, y[2], y[3]);
         }
+        const float t = fmaxf(t0, t1);
+        top = fmaxf(top, HOW == kEven ? t * kc : t);
     }
-    return fmaxf(t0, t1);
+    return top;
 }
 
 // p = 2^(y rc + ms) of the row's columns, written as f16 pairs from column tS
 // on (chunk cc's 16 columns lie within scores already read); returns their sum.
-template <bool MASK>
-__device__ __forceinline__ float weights(uint32_t tS, const float4 *ks, uint32_t tb, int lim, float rc, float ms)
+template <int HOW>
+__device__ __forceinline__ float weights(uint32_t tS, const float *ks, uint32_t tb, int lim, float rc, float ms)
 {
     float l0 = 0.0f, l1 = 0.0f;
+    const uint64_t m2 = pair(ms);
+    uint64_t r2 = pair(rc);
 #pragma unroll 1
     for (int cc = 0; cc < 4; ++cc) {
-        uint32_t s[32], p[16];
-        tmem_ld32(tS + 32u * cc, s);
-        const uint32_t have = MASK ? lds32(tb + 4u * cc) : 0u;
+        uint32_t r[32], p[16];
+        tmem_ld32(tS + 32u * cc, r);
+        const uint32_t have = HOW == kMasked ? lds32(tb + 4u * cc) : 0u;
+        if constexpr (HOW == kEven)
+            r2 = pair(ks[32 * cc] * rc);
         tmem_ld_wait();
-        reg_fence_cols<32>(s);
+        reg_fence_cols<32>(r);
 #pragma unroll
-        for (int z = 0; z < 8; ++z) {
-            float y[4], x0 = ms, x1 = ms, x2 = ms, x3 = ms;
-            scaled4<false>(s + 4 * z, ks[8 * cc + z], 0u, 0, 0, y);
-            ffma2(x0, x1, y[0], y[1], rc, rc);
-            ffma2(x2, x3, y[2], y[3], rc, rc);
-            if constexpr (MASK) {
-                // after the product: c_row may be 0
-                const int col = 32 * cc + 4 * z;
-                x0 = (have >> (4 * z) & 1u) && col <= lim ? x0 : -INFINITY;
-                x1 = (have >> (4 * z + 1) & 1u) && col + 1 <= lim ? x1 : -INFINITY;
-                x2 = (have >> (4 * z + 2) & 1u) && col + 2 <= lim ? x2 : -INFINITY;
-                x3 = (have >> (4 * z + 3) & 1u) && col + 3 <= lim ? x3 : -INFINITY;
+        for (int z = 0; z < 32; z += 4) {
+            float y[4], x[4];
+            if constexpr (HOW == kEven) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    y[e] = __uint_as_float(r[z + e]);
+            } else {
+                const float4 k = *reinterpret_cast<const float4 *>(ks + 32 * cc + z);
+                fmul2(y[0], y[1], __uint_as_float(r[z]), __uint_as_float(r[z + 1]), k.x, k.y);
+                fmul2(y[2], y[3], __uint_as_float(r[z + 2]), __uint_as_float(r[z + 3]), k.z, k.w);
             }
-            x0 = ex2_approx(x0);
-            x1 = ex2_approx(x1);
-            x2 = ex2_approx(x2);
-            x3 = ex2_approx(x3);
-            fadd2(l0, l1, x0, x1);
-            fadd2(l0, l1, x2, x3);
-            p[2 * z] = pack_f16x2(x0, x1);
-            p[2 * z + 1] = pack_f16x2(x2, x3);
+            ffma2_to(x[0], x[1], y[0], y[1], r2, m2);
+            ffma2_to(x[2], x[3], y[2], y[3], r2, m2);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (HOW == kMasked)  // after the product: c_row may be 0
+                    x[e] = (have >> (z + e) & 1u) && 32 * cc + z + e <= lim ? x[e] : -INFINITY;
+                x[e] = ex2_approx(x[e]);
+            }
+            fadd2(l0, l1, x[0], x[1]);
+            fadd2(l0, l1, x[2], x[3]);
+            p[z / 2] = pack_f16x2(x[0], x[1]);
+            p[z / 2 + 1] = pack_f16x2(x[2], x[3]);
         }
         tmem_st16(tS + 16u * cc, p);
     }
@@ -345,17 +384,21 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
                     break;
                 }
                 tc_fence_after_sync();
-                const float4 *const ksp = reinterpret_cast<const float4 *>(smem + kPrOffKs + (t % kMeta) * 512);
+                const float *const ksp = reinterpret_cast<const float *>(smem + kPrOffKs + (t % kMeta) * 512);
                 const uint32_t tb = sbase + kPrOffTile + (uint32_t)(t % kMeta) * 32u;
                 const uint4 mw = lds128(tb);
                 const float vfac = __uint_as_float(lds32(tb + 16u));
                 vref = __uint_as_float(lds32(tb + 20u));
-                const int base = t * kPrTok;
+                const uint32_t even = lds32(tb + 24u);
+                const int base = t * kPrTok, past = lim - base;
                 // nothing of the tile is masked for any row of this warp
                 const bool whole = (mw.x & mw.y & mw.z & mw.w) == 0xFFFFFFFFu &&
-                                   __all_sync(kFull, base + kPrTok - 1 <= lim);
+                                   __all_sync(kFull, past >= kPrTok - 1);
+                const int how = !whole ? kMasked : even == 0x01010101u ? kEven : kWhole;
                 // first pass: the row's largest score of the tile
-                float top = whole ? row_max<false>(tS, ksp, tb, lim - base) : row_max<true>(tS, ksp, tb, lim - base);
+                float top = how == kEven    ? row_max<kEven>(tS, ksp, tb, past)
+                            : how == kWhole ? row_max<kWhole>(tS, ksp, tb, past)
+                                            : row_max<kMasked>(tS, ksp, tb, past);
                 top *= rc;
                 float alpha = vfac;
                 if (top > m + kPrSlack) {
@@ -379,8 +422,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
                 }
                 // second pass: the weights, as f16, over the columns that held the scores
                 const float ms = m == -INFINITY ? 0.0f : -m;
-                l += whole ? weights<false>(tS, ksp, tb, lim - base, rc, ms)
-                           : weights<true>(tS, ksp, tb, lim - base, rc, ms);
+                l += how == kEven    ? weights<kEven>(tS, ksp, tb, past, rc, ms)
+                     : how == kWhole ? weights<kWhole>(tS, ksp, tb, past, rc, ms)
+                                     : weights<kMasked>(tS, ksp, tb, past, rc, ms);
                 tmem_st_wait();
                 tc_fence_before_sync();
                 __syncwarp();
@@ -523,8 +567,13 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1)
                 vmax = fmaxf(vmax, __shfl_xor_sync(kFull, vmax, o));
-            if (lane == 0)
+            // do the warp's 32 tokens share one key scale that is not negative?
+            const float kmine = __uint_as_float(lds32(sbase + kPrOffKs + (uint32_t)(t % kMeta) * 512u + (uint32_t)lt * 4u));
+            const bool even = __all_sync(kFull, kmine >= 0.0f && kmine == __shfl_sync(kFull, kmine, 0));
+            if (lane == 0) {
                 red[lw] = vmax;
+                asm volatile("st.shared.u8 [%0], %1;" ::"r"(sbase + kPrOffTile + (uint32_t)(t % kMeta) * 32u + 24u + (uint32_t)lw), "r"(even ? 1u : 0u) : "memory");
+            }
             named_bar_sync(1, 128);
             vmax = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
             const float vnew = vmax > vref && vmax > 1e-36f ? vmax : vref;
