@@ -37,7 +37,6 @@ constexpr int kPrTok = 128;       // tokens per tile
 constexpr int kPrThreads = 512;
 constexpr int kKStages = 2, kRawSlots = 3, kVStages = 2, kMeta = 4;
 constexpr uint32_t kTileBytes = 128 * 128;           // 128 rows of 128 bytes
-constexpr float kPrSlack = 8.0f;                     // p <= 2^8 before the maximum moves
 constexpr float kVUp = 64.0f;                        // V is held times 64 / vref in f16
 
 // shared memory: operands (1024-byte aligned), then per-tile values, barriers
@@ -185,34 +184,37 @@ __device__ __forceinline__ float row_max(uint32_t tS, const float *ks, uint32_t 
     return top;
 }
 
-// p = 2^(y rc + ms) of the row's columns, written as f16 pairs from column tS
-// on (chunk cc's 16 columns lie within scores already read); returns their sum.
+// p = 2^(y rc + ms) of the row's 128 columns as f16 pairs; returns their sum.
+// The next 32 columns load while these are worked on.
 template <int HOW>
-__device__ __forceinline__ float weights(uint32_t tS, const float *ks, uint32_t tb, int lim, float rc, float ms)
+__device__ __forceinline__ float weights(uint32_t tS, const float *ks, uint32_t tb, int lim, float rc, float ms,
+                                         uint32_t (&p)[64])
 {
     float l0 = 0.0f, l1 = 0.0f;
     const uint64_t m2 = pair(ms);
     uint64_t r2 = pair(rc);
-#pragma unroll 1
+    uint32_t r[2][32];
+    tmem_ld32(tS, r[0]);
+#pragma unroll
     for (int cc = 0; cc < 4; ++cc) {
-        uint32_t r[32], p[16];
-        tmem_ld32(tS + 32u * cc, r);
         const uint32_t have = HOW == kMasked ? lds32(tb + 4u * cc) : 0u;
         if constexpr (HOW == kEven)
             r2 = pair(ks[32 * cc] * rc);
         tmem_ld_wait();
-        reg_fence_cols<32>(r);
+        reg_fence_cols<32>(r[cc & 1]);
+        if (cc < 3)
+            tmem_ld32(tS + 32u * (cc + 1), r[(cc + 1) & 1]);
 #pragma unroll
         for (int z = 0; z < 32; z += 4) {
             float y[4], x[4];
             if constexpr (HOW == kEven) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    y[e] = __uint_as_float(r[z + e]);
+                    y[e] = __uint_as_float(r[cc & 1][z + e]);
             } else {
                 const float4 k = *reinterpret_cast<const float4 *>(ks + 32 * cc + z);
-                fmul2(y[0], y[1], __uint_as_float(r[z]), __uint_as_float(r[z + 1]), k.x, k.y);
-                fmul2(y[2], y[3], __uint_as_float(r[z + 2]), __uint_as_float(r[z + 3]), k.z, k.w);
+                fmul2(y[0], y[1], __uint_as_float(r[cc & 1][z]), __uint_as_float(r[cc & 1][z + 1]), k.x, k.y);
+                fmul2(y[2], y[3], __uint_as_float(r[cc & 1][z + 2]), __uint_as_float(r[cc & 1][z + 3]), k.z, k.w);
             }
             ffma2_to(x[0], x[1], y[0], y[1], r2, m2);
             ffma2_to(x[2], x[3], y[2], y[3], r2, m2);
@@ -224,10 +226,9 @@ __device__ __forceinline__ float weights(uint32_t tS, const float *ks, uint32_t 
             }
             fadd2(l0, l1, x[0], x[1]);
             fadd2(l0, l1, x[2], x[3]);
-            p[z / 2] = pack_f16x2(x[0], x[1]);
-            p[z / 2 + 1] = pack_f16x2(x[2], x[3]);
+            p[16 * cc + z / 2] = pack_f16x2(x[0], x[1]);
+            p[16 * cc + z / 2 + 1] = pack_f16x2(x[2], x[3]);
         }
-        tmem_st16(tS + 16u * cc, p);
     }
     return l0 + l1;
 }
@@ -308,7 +309,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
 
     if (warp < 8) {
         // -------------------------------------------------------- softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");  // 2 x 160 + 2 x 96 = 4 x 128
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");  // 2 x 176 + 2 x 80 = 4 x 128
         const int tile = warp >> 2;
         const int row = (warp & 3) * 32 + lane;     // TMEM lane
         const int R = R0 + tile * 128 + row;
@@ -395,17 +396,37 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
                 const bool whole = (mw.x & mw.y & mw.z & mw.w) == 0xFFFFFFFFu &&
                                    __all_sync(kFull, past >= kPrTok - 1);
                 const int how = !whole ? kMasked : even == 0x01010101u ? kEven : kWhole;
-                // first pass: the row's largest score of the tile
-                float top = how == kEven    ? row_max<kEven>(tS, ksp, tb, past)
-                            : how == kWhole ? row_max<kWhole>(tS, ksp, tb, past)
-                                            : row_max<kMasked>(tS, ksp, tb, past);
-                top *= rc;
-                float alpha = vfac;
-                if (top > m + kPrSlack) {
-                    alpha *= ex2_approx(m - top);
-                    l *= ex2_approx(m - top);
-                    m = top;
+                // m is the largest score of the first tile that the row saw, and
+                // moves again only when a tile's weights sum to more than 2^15:
+                // till then every p fits f16, so the scores are read once and
+                // the tile's maximum is not taken.
+                float alpha = vfac, sum;
+                uint32_t p[64];
+                bool fix = __any_sync(kFull, m == -INFINITY);
+#pragma unroll 1
+                for (int round = 0;; ++round) {
+                    if (fix) {
+                        const float top = rc * (how == kMasked ? row_max<kMasked>(tS, ksp, tb, past)
+                                                               : row_max<kWhole>(tS, ksp, tb, past));
+                        if (top > m && (round > 0 || m == -INFINITY)) {
+                            const float f = ex2_approx(m - top);
+                            alpha *= f;
+                            l *= f;
+                            m = top;
+                        }
+                    }
+                    const float ms = m == -INFINITY ? 0.0f : -m;
+                    sum = how == kEven    ? weights<kEven>(tS, ksp, tb, past, rc, ms, p)
+                          : how == kWhole ? weights<kWhole>(tS, ksp, tb, past, rc, ms, p)
+                                          : weights<kMasked>(tS, ksp, tb, past, rc, ms, p);
+                    fix = __any_sync(kFull, sum > 32768.0f);
+                    if (!fix || round > 0)
+                        break;
                 }
+                l += sum;
+#pragma unroll
+                for (int cc = 0; cc < 4; ++cc)
+                    tmem_st16(tS + 16u * cc, p + 16 * cc);
                 if (t > 0 && __any_sync(kFull, alpha != 1.0f)) {
                     // O holds tiles before this one: PV of tile t - 1 is done (SFull)
 #pragma unroll 1
@@ -420,11 +441,6 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
                         tmem_st32(tO + 32u * cc, o);
                     }
                 }
-                // second pass: the weights, as f16, over the columns that held the scores
-                const float ms = m == -INFINITY ? 0.0f : -m;
-                l += how == kEven    ? weights<kEven>(tS, ksp, tb, past, rc, ms)
-                     : how == kWhole ? weights<kWhole>(tS, ksp, tb, past, rc, ms)
-                                     : weights<kMasked>(tS, ksp, tb, past, rc, ms);
                 tmem_st_wait();
                 tc_fence_before_sync();
                 __syncwarp();
@@ -468,7 +484,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
         }
     } else if (warp < 12) {
         // -------------------------------------------------------- loader
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         // thread = token of a tile for the look-ups; a warp copies its 32 rows
         const int lt = tid - 256, lw = lt >> 5;
         const int32_t *const bt = c.bt + (long long)req * c.W;
@@ -623,7 +639,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
         }
         cp_async_wait_all();
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         if (warp == 12 && lane == 0) {
         // -------------------------------------------------------- products
         constexpr uint32_t idq = idesc_e4m3_f32(128, 128);
