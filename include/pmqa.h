@@ -382,8 +382,8 @@ int pmqa_sparse_mla_merge(const void *outs, const float *lses, int32_t parts, in
  *                 ctx_i - n_i + j and sees the slots t <= ctx_i - n_i + j.
  *                 Rows of no request are neither read nor written. Unused by
  *                 pmqa_cache_evict (as are rows and max_rows).
- * head_dim must be 64 or 128, block_size at most 1024, kv_heads at most 65535
- * (PMQA_ERR_UNSUPPORTED otherwise). A context outside [0, block_size *
+ * head_dim must be 64 or 128, block_size at most 1024, kv_heads at most 65535,
+ * num_blocks * kv_heads * block_size < 2^32 - 1 (PMQA_ERR_UNSUPPORTED otherwise). A context outside [0, block_size *
  * max_blocks_per_seq], or rows that break the rules above, are clamped and set
  * PMQA_DEV_BAD_CONTEXT; a table entry outside [0, num_blocks) sets
  * PMQA_DEV_BAD_BLOCK_ID, and its tokens are left out (not written by append,

@@ -32,6 +32,9 @@ int check(const pmqa_cache_problem *p, int need, const void *ws, size_t ws_bytes
         return PMQA_ERR_INVALID_ARG;
     if ((p->head_dim != 64 && p->head_dim != 128) || p->block_size > kMaxBlock || p->kv_heads > 65535)
         return PMQA_ERR_UNSUPPORTED;
+    // rows of a pool are counted in 32 bits
+    if (p->num_blocks > 0xFFFFFFFEll / ((long long)p->kv_heads * p->block_size))
+        return PMQA_ERR_UNSUPPORTED;
     if (!ws || !aligned(ws, 256))
         return PMQA_ERR_INVALID_ARG;
     if (ws_bytes < kWorkspace)

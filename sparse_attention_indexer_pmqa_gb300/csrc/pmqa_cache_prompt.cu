@@ -17,8 +17,8 @@
 //                converted (exactly) and scaled by vs_t / vref, vref the largest
 //                block scale so far, so that O needs no factor per token.
 // Roles of a CTA's 16 warps: 0-3 and 4-7 are the softmax (and the final output)
-// of the two row tiles, 8-11 look up the blocks, copy K and V rows (cp.async)
-// into the operand layouts and convert V, warp 12 issues the products. While
+// of the two row tiles, 8-11 convert V, 12 issues the products, 13 and 14 look up
+// the blocks and copy K and V rows (cp.async). While
 // one tile's softmax runs the tensor cores work for the other.
 //
 // Bound by the tensor cores: 4 D flops per visible (row, head, token) at the
@@ -47,18 +47,20 @@ constexpr uint32_t kPrOffV = kPrOffRaw + kRawSlots * kTileBytes;          // V f
 constexpr uint32_t kPrOffKs = kPrOffV + kVStages * 2 * kTileBytes;  // [kMeta][128] fp32
 constexpr uint32_t kPrOffVs = kPrOffKs + kMeta * 512;             // [kMeta][128] fp32
 constexpr uint32_t kPrOffTile = kPrOffVs + kMeta * 512;           // [kMeta]: 4 mask words, vfac, vref, 4 bytes: even scales
-constexpr uint32_t kPrOffRed = kPrOffTile + kMeta * 32;           // [4] fp32
-constexpr uint32_t kPrOffBar = kPrOffRed + 16;
+constexpr uint32_t kPrOffRed = kPrOffTile + kMeta * 32;           // [2][4] fp32
+constexpr uint32_t kPrOffBar = kPrOffRed + 32;
 enum {
-    kBKFull = 0,                  // [2] K rows landed: 128 cp.async arrivals
-    kBKEmpty = kBKFull + kKStages,  // [2] scores done with the stage: MMA commit
+    kBKFull = 0,                  // [2] K rows, scales, mask landed: 32 cp.async arrivals and lane 0's own
+    kBKEmpty = kBKFull + kKStages,  // [2] scores done with the stage (MMA commit), its scales read (4 warps)
     kBVFull = kBKEmpty + kKStages,       // [2] V converted, factors written: 4 warps
     kBVEmpty = kBVFull + 2,       // [2] output update done with the slot: MMA commit
     kBSFull = kBVEmpty + 2,       // [2 tiles] scores in TMEM: MMA commit
     kBPFull = kBSFull + 2,        // [2 tiles] P written, O rescaled: 4 warps
     kBODone = kBPFull + 2,        // every product done: MMA commit
     kBQ = kBODone + 1,            // Q operands written: 8 warps
-    kBCount = kBQ + 1
+    kBRawFull = kBQ + 1,          // [3] V codes landed: 32 cp.async arrivals and lane 0's own
+    kBRawEmpty = kBRawFull + kRawSlots,  // [3] V codes converted: 4 warps
+    kBCount = kBRawEmpty + kRawSlots
 };
 constexpr uint32_t kPrOffMisc = kPrOffBar + kBCount * 8;
 constexpr uint32_t kPrSmem = kPrOffMisc + 16;
@@ -281,8 +283,12 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
     volatile int *const abort_flag = reinterpret_cast<volatile int *>(misc + 1);
     if (tid == 0) {
         for (int s = 0; s < kKStages; ++s) {
-            mbar_init(&bar[kBKFull + s], 128);
-            mbar_init(&bar[kBKEmpty + s], 1);
+            mbar_init(&bar[kBKFull + s], 33);
+            mbar_init(&bar[kBKEmpty + s], 5);
+        }
+        for (int s = 0; s < kRawSlots; ++s) {
+            mbar_init(&bar[kBRawFull + s], 33);
+            mbar_init(&bar[kBRawEmpty + s], 4);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bar[kBVFull + s], 4);
@@ -483,161 +489,93 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
             }
         }
     } else if (warp < 12) {
-        // -------------------------------------------------------- loader
+        // -------------------------------------------------------- V conversion
         asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-        // thread = token of a tile for the look-ups; a warp copies its 32 rows
         const int lt = tid - 256, lw = lt >> 5;
-        const int32_t *const bt = c.bt + (long long)req * c.W;
-        struct Row {
-            long long phys;  // block * H + h, -1 for none
-            int off;         // row within the block
-        };
-        auto look_up = [&](int t) -> int {
-            const int tok = t * kPrTok + lt;
-            return t < T && tok < end ? __ldg(bt + c.page_of(tok)) : -1;
-        };
-        auto row_of = [&](int t, int page) -> Row {
-            const int tok = t * kPrTok + lt;
-            Row r{-1, 0};
-            if (t < T && tok < end) {
-                if (page < 0 || (long long)page >= c.nb) {
-                    atomicOr(c.status, (uint32_t)PMQA_DEV_BAD_BLOCK_ID);
-                } else {
-                    r.phys = (long long)page * c.H + h;
-                    r.off = tok - c.page_of(tok) * c.P;
-                }
-            }
-            return r;
-        };
-        // K rows, both scales and the mask of tile t; V codes of tile t
-        auto copy_rows = [&](const uint8_t *pool, uint32_t dst, const Row &r, bool swz) {
-            const long long byte = r.phys < 0 ? -1 : (r.phys * c.P + r.off) * D;
-            constexpr int PER = 32 / CH;
-            const int ch = lane % CH;
-#pragma unroll
-            for (int k = 0; k < 32 / PER; ++k) {
-                const int rr = k * PER + lane / CH;
-                const long long src = __shfl_sync(kFull, byte, rr);
-                const int rt = lw * 32 + rr;
-                cp_async_16(dst + (swz ? sw128(rt, ch) : (uint32_t)(rt * 128 + ch * 16)),
-                            pool + (src < 0 ? 0 : src) + ch * 16, src < 0 ? 0u : 16u);
-            }
-        };
-        auto load_k = [&](int t, const Row &r) {
-            const uint32_t ks = sbase + kPrOffKs + (uint32_t)(t % kMeta) * 512u + (uint32_t)lt * 4u;
-            const uint32_t vs = sbase + kPrOffVs + (uint32_t)(t % kMeta) * 512u + (uint32_t)lt * 4u;
-            const uint32_t mask = __ballot_sync(kFull, r.phys >= 0);
-            if (lane == 0)
-                asm volatile("st.shared.b32 [%0], %1;" ::"r"(sbase + kPrOffTile + (uint32_t)(t % kMeta) * 32u + (uint32_t)lw * 4u), "r"(mask) : "memory");
-            if (r.phys >= 0) {
-                cp_async_4(ks, c.ks + r.phys);
-                cp_async_4(vs, c.vs + r.phys);
-            } else {
-                asm volatile("st.shared.b32 [%0], %1;" ::"r"(ks), "r"(0) : "memory");
-                asm volatile("st.shared.b32 [%0], %1;" ::"r"(vs), "r"(0) : "memory");
-            }
-            copy_rows(c.k, sbase + kPrOffK + (uint32_t)(t % kKStages) * kTileBytes, r, true);
-        };
-        // both run two tiles ahead of the conversion; a tile's scales come with its K rows
-        int pg2 = look_up(2);
-        {
-            const Row r0 = row_of(0, look_up(0)), r1 = row_of(1, look_up(1));
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const Row &r = t ? r1 : r0;
-                if (t < T)
-                    copy_rows(c.v, sbase + kPrOffRaw + (uint32_t)t * kTileBytes, r, false);
-                cp_async_commit();
-                if (t < T) {
-                    load_k(t, r);
-                    cp_async_arrive_noinc(&bar[kBKFull + t]);
-                }
-                cp_async_commit();
-            }
-        }
+        float *const red = reinterpret_cast<float *>(smem + kPrOffRed);
         float vref = 0.0f;
         bool ok = true;
-        float *const red = reinterpret_cast<float *>(smem + kPrOffRed);
         int raw_slot = 0;
+        uint32_t raw_ph = 0;
         for (int t = 0; t < T; ++t) {
-            const int pg3 = look_up(t + 3);
-            const Row r2 = row_of(t + 2, pg2);
-            pg2 = pg3;
-            // all but tile t + 1's two groups: V codes and scales of tile t
-            cp_async_wait_group<2>();
-            ok = ok && mbar_wait(&bar[kBVEmpty + (t & 1)], ((uint32_t)(t >> 1) & 1u) ^ 1u, abort_flag);
+            ok = ok && mbar_wait(&bar[kBKFull + t % kKStages], (uint32_t)(t / kKStages) & 1u, abort_flag) &&
+                 mbar_wait(&bar[kBRawFull + raw_slot], raw_ph, abort_flag) &&
+                 mbar_wait(&bar[kBVEmpty + (t & 1)], ((uint32_t)(t >> 1) & 1u) ^ 1u, abort_flag);
+            const float *const ksp = reinterpret_cast<const float *>(smem + kPrOffKs + (t % kMeta) * 512);
+            const float *const vsp = reinterpret_cast<const float *>(smem + kPrOffVs + (t % kMeta) * 512);
+            const uint32_t tb = sbase + kPrOffTile + (uint32_t)(t % kMeta) * 32u;
+            // vref: the largest |scale| so far; and do the warp's 32 tokens share one
+            // key scale that is not negative?
+            const float kmine = ksp[lt];
+            float vmax = fabsf(vsp[lt]);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                vmax = fmaxf(vmax, __shfl_xor_sync(kFull, vmax, o));
+            const bool even = __all_sync(kFull, kmine >= 0.0f && kmine == __shfl_sync(kFull, kmine, 0));
+            if (lane == 0) {
+                red[4 * (t & 1) + lw] = vmax;
+                asm volatile("st.shared.u8 [%0], %1;" ::"r"(tb + 24u + (uint32_t)lw), "r"(even ? 1u : 0u) : "memory");
+            }
             if (!named_bar_and(1, 128, ok)) {
                 fail();
                 break;
             }
-            const uint32_t raw = sbase + kPrOffRaw + (uint32_t)raw_slot * kTileBytes;
-            // every thread is done with tile t - 1's codes: their slot takes tile t + 2's
-            if (t + 2 < T)
-                copy_rows(c.v, sbase + kPrOffRaw + (uint32_t)(raw_slot == 0 ? 2 : raw_slot - 1) * kTileBytes, r2,
-                          false);
-            cp_async_commit();
-            if (++raw_slot == kRawSlots)
-                raw_slot = 0;
-            // vref: the largest |scale| so far
-            float vmax = fabsf(__uint_as_float(lds32(sbase + kPrOffVs + (uint32_t)(t % kMeta) * 512u + (uint32_t)lt * 4u)));
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                vmax = fmaxf(vmax, __shfl_xor_sync(kFull, vmax, o));
-            // do the warp's 32 tokens share one key scale that is not negative?
-            const float kmine = __uint_as_float(lds32(sbase + kPrOffKs + (uint32_t)(t % kMeta) * 512u + (uint32_t)lt * 4u));
-            const bool even = __all_sync(kFull, kmine >= 0.0f && kmine == __shfl_sync(kFull, kmine, 0));
-            if (lane == 0) {
-                red[lw] = vmax;
-                asm volatile("st.shared.u8 [%0], %1;" ::"r"(sbase + kPrOffTile + (uint32_t)(t % kMeta) * 32u + 24u + (uint32_t)lw), "r"(even ? 1u : 0u) : "memory");
-            }
-            named_bar_sync(1, 128);
-            vmax = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+            const float4 r4 = *reinterpret_cast<const float4 *>(red + 4 * (t & 1));
+            vmax = fmaxf(fmaxf(r4.x, r4.y), fmaxf(r4.z, r4.w));
             const float vnew = vmax > vref && vmax > 1e-36f ? vmax : vref;
             const float vfac = vnew > vref ? vref / vnew : 1.0f;
             vref = vnew;
             const float vinv = vref > 0.0f ? kVUp / vref : 0.0f;
             if (lt == 0)
-                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(sbase + kPrOffTile + (uint32_t)(t % kMeta) * 32u + 16u),
-                             "r"(__float_as_uint(vfac)), "r"(__float_as_uint(vref)) : "memory");
-            const uint32_t vd = sbase + kPrOffV + (uint32_t)(t & 1) * 2 * kTileBytes;
-            const uint32_t vsb = sbase + kPrOffVs + (uint32_t)(t % kMeta) * 512u;
-            const int ch = lt % CH;
+                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(tb + 16u), "r"(__float_as_uint(vfac)),
+                             "r"(__float_as_uint(vref)) : "memory");
+            const uint8_t *const raw = smem + kPrOffRaw + raw_slot * kTileBytes;
+            uint8_t *const vd = smem + kPrOffV + (t & 1) * 2 * kTileBytes;
+            // a thread converts 16 codes of a token at a time; the lanes of the upper
+            // value columns take the neighbouring token, which spreads the stores
+            // of both column blocks over all banks
+            const int ch = lt % CH, flip = D == 128 ? ch >> 2 : 0;
 #pragma unroll
-            for (int k = 0; k < CH; ++k) {
-                const int tok = k * (128 / CH) + lt / CH;
-                const uint4 u = lds128(raw + (uint32_t)(tok * 128 + ch * 16));
-                const float f = __uint_as_float(lds32(vsb + (uint32_t)tok * 4u)) * vinv;
-                const uint32_t f2 = pack_f16x2(f, f);
-                uint32_t o[8];
-                e4m3x4_to_f16x2(u.x, o[0], o[1]);
-                e4m3x4_to_f16x2(u.y, o[2], o[3]);
-                e4m3x4_to_f16x2(u.z, o[4], o[5]);
-                e4m3x4_to_f16x2(u.w, o[6], o[7]);
+            for (int k0 = 0; k0 < CH; k0 += 4) {
+                uint4 u[4];
+                float f[4];
 #pragma unroll
-                for (int y = 0; y < 8; ++y)
-                    asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(o[y]) : "r"(f2));
-                // value columns 16 ch .. 16 ch + 15: chunks 2 ch, 2 ch + 1 of 8 columns each
-                const uint32_t blk = vd + (uint32_t)(ch >> 2) * kTileBytes;
-                const int c0 = (2 * ch) & 7;
-                sts128(blk + sw128(tok, c0), o[0], o[1], o[2], o[3]);
-                sts128(blk + sw128(tok, c0 + 1), o[4], o[5], o[6], o[7]);
+                for (int k = 0; k < 4; ++k) {
+                    const int tok = ((k0 + k) * (128 / CH) + lt / CH) ^ flip;
+                    u[k] = *reinterpret_cast<const uint4 *>(raw + tok * 128 + ch * 16);
+                    f[k] = vsp[tok] * vinv;
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int tok = ((k0 + k) * (128 / CH) + lt / CH) ^ flip;
+                    const uint32_t f2 = pack_f16x2(f[k], f[k]);
+                    uint32_t o[8];
+                    e4m3x4_to_f16x2(u[k].x, o[0], o[1]);
+                    e4m3x4_to_f16x2(u[k].y, o[2], o[3]);
+                    e4m3x4_to_f16x2(u[k].z, o[4], o[5]);
+                    e4m3x4_to_f16x2(u[k].w, o[6], o[7]);
+#pragma unroll
+                    for (int y = 0; y < 8; ++y)
+                        asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(o[y]) : "r"(f2));
+                    // value columns 16 ch .. 16 ch + 15: chunks 2 ch, 2 ch + 1 of 8 columns each
+                    uint8_t *const blk = vd + (ch >> 2) * kTileBytes;
+                    const int c0 = (2 * ch) & 7;
+                    *reinterpret_cast<uint4 *>(blk + sw128(tok, c0)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4 *>(blk + sw128(tok, c0 + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+                }
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0)
+            if (lane == 0) {
                 mbar_arrive(&bar[kBVFull + (t & 1)]);
-            if (t + 2 < T) {
-                const int st = t % kKStages;  // freed by the scores of tile t
-                ok = mbar_wait(&bar[kBKEmpty + st], (uint32_t)(t / kKStages) & 1u, abort_flag);
-                ok = __all_sync(kFull, ok);
-                if (ok) {
-                    load_k(t + 2, r2);
-                    cp_async_arrive_noinc(&bar[kBKFull + st]);
-                }
+                mbar_arrive(&bar[kBRawEmpty + raw_slot]);
+                mbar_arrive(&bar[kBKEmpty + t % kKStages]);
             }
-            cp_async_commit();
+            if (++raw_slot == kRawSlots) {
+                raw_slot = 0;
+                raw_ph ^= 1u;
+            }
         }
-        cp_async_wait_all();
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         if (warp == 12 && lane == 0) {
@@ -697,6 +635,91 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
         umma_commit(&bar[kBODone]);
         if (!mbar_wait(&bar[kBODone], 0u, nullptr))
             atomicOr(c.status, (uint32_t)PMQA_DEV_TIMEOUT);
+        } else if (warp == 13 || warp == 14) {
+            // ---------------------------------------------------- loaders
+            // warp 13: K rows, both scales and the mask; warp 14: V codes. A lane
+            // looks up tokens lane, lane + 32, ... of the tile, one tile ahead.
+            const bool is_k = warp == 13;
+            const uint8_t *const pool = is_k ? c.k : c.v;
+            const int32_t *const bt = c.bt + (long long)req * c.W;
+            constexpr uint32_t kNone = 0xFFFFFFFFu;
+            constexpr int PER = 32 / CH;  // rows an instruction copies
+            const int ch = lane % CH;
+            int page[4];
+            auto look_up = [&](int t) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int tok = t * kPrTok + 32 * k + lane;
+                    page[k] = t < T && tok < end ? __ldg(bt + c.page_of(tok)) : -1;
+                }
+            };
+            look_up(0);
+            bool ok = true;
+            int slot_i = 0;
+            uint32_t ph = 1;
+            const int slots = is_k ? kKStages : kRawSlots;
+            for (int t = 0; t < T; ++t) {
+                uint32_t phys[4], row[4];  // block * H + h, and row of the pool
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int tok = t * kPrTok + 32 * k + lane;
+                    phys[k] = row[k] = kNone;
+                    if (tok < end) {
+                        if (page[k] < 0 || (long long)page[k] >= c.nb) {
+                            atomicOr(c.status, (uint32_t)PMQA_DEV_BAD_BLOCK_ID);
+                        } else {
+                            phys[k] = (uint32_t)page[k] * (uint32_t)c.H + (uint32_t)h;
+                            row[k] = phys[k] * (uint32_t)c.P + (uint32_t)(tok - c.page_of(tok) * c.P);
+                        }
+                    }
+                }
+                look_up(t + 1);
+                ok = mbar_wait(&bar[(is_k ? kBKEmpty : kBRawEmpty) + slot_i], ph, abort_flag);
+                ok = __all_sync(kFull, ok);
+                if (!ok) {
+                    fail();
+                    break;
+                }
+                const uint32_t dst = sbase + (is_k ? kPrOffK : kPrOffRaw) + (uint32_t)slot_i * kTileBytes;
+                if (is_k) {
+                    const uint32_t meta = (uint32_t)(t % kMeta);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t at = meta * 512u + (uint32_t)(32 * k + lane) * 4u;
+                        const uint32_t mask = __ballot_sync(kFull, phys[k] != kNone);
+                        if (lane == 0)
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(sbase + kPrOffTile + meta * 32u + 4u * k),
+                                         "r"(mask) : "memory");
+                        if (phys[k] != kNone) {
+                            cp_async_4(sbase + kPrOffKs + at, c.ks + phys[k]);
+                            cp_async_4(sbase + kPrOffVs + at, c.vs + phys[k]);
+                        } else {
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(sbase + kPrOffKs + at), "r"(0) : "memory");
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(sbase + kPrOffVs + at), "r"(0) : "memory");
+                        }
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int y = 0; y < CH; ++y) {
+                        const int rr = y * PER + lane / CH, rt = 32 * k + rr;
+                        const uint32_t src = __shfl_sync(kFull, row[k], rr);
+                        cp_async_16(dst + (is_k ? sw128(rt, ch) : (uint32_t)(rt * 128 + ch * 16)),
+                                    pool + (src == kNone ? 0ull : (unsigned long long)src * D) + ch * 16,
+                                    src == kNone ? 0u : 16u);
+                    }
+                uint64_t *const full = &bar[(is_k ? kBKFull : kBRawFull) + slot_i];
+                cp_async_arrive_noinc(full);
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(full);  // releases the plain stores (masks, zero scales)
+                if (++slot_i == slots) {
+                    slot_i = 0;
+                    ph ^= 1u;
+                }
+            }
+            cp_async_wait_all();
         }
     }
     __syncwarp();
