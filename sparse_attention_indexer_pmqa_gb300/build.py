@@ -37,7 +37,7 @@ def _sources():
              ("pmqa_noalloc", os.path.join(CSRC, "pmqa_noalloc.cu"), []),
              ("pmqa_mla", os.path.join(CSRC, "pmqa_mla.cu"), []),
              ("pmqa_gather_probe", os.path.join(CSRC, "pmqa_gather_probe.cu"), [])]
-    for name in ("", "_append", "_attn", "_prompt", "_weigh", "_evict"):
+    for name in ("", "_append", "_attn", "_prompt", "_weigh", "_window", "_evict"):
         units.append((f"pmqa_cache{name}", os.path.join(CSRC, f"pmqa_cache{name}.cu"), []))
     for h in HEADS:
         units.append((f"pmqa_main_h{h}", os.path.join(CSRC, "pmqa_main_inst.cu"),

@@ -178,7 +178,13 @@ extern "C" int pmqa_cache_weigh(const pmqa_cache_problem *p, const void *q, int3
     if ((rc = sm_count(&sms)) != PMQA_OK)
         return rc;
     WeighCall a{view(p, ws), q, lse, mass_in, mass_out, mass_width, sm_scale, heads};
-    return code_of(launch_weigh_rows(a, 0, 0x7FFFFFFF, sms, cuda(stream)));
+    const long long most = (long long)p->max_rows * (heads / p->kv_heads);
+    cudaError_t e = cudaSuccess;
+    if (most > kShortRows)
+        e = launch_weigh_window(a, kShortRows + 1, sms, cuda(stream));
+    if (e == cudaSuccess)
+        e = launch_weigh_rows(a, 0, kShortRows, sms, cuda(stream));
+    return code_of(e);
 }
 
 extern "C" int pmqa_cache_evict(const pmqa_cache_problem *p, const float *mass, int64_t mass_width,

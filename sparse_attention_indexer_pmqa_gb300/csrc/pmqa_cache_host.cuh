@@ -67,6 +67,7 @@ cudaError_t launch_append(const View &c, const void *k, const void *v, cudaStrea
 cudaError_t launch_attn_rows(AttnCall &q, int least, int most, int sms, cudaStream_t st);
 cudaError_t launch_attn_prompt(AttnCall &q, int least, cudaStream_t st);
 cudaError_t launch_weigh_rows(const WeighCall &q, int least, int most, int sms, cudaStream_t st);
+cudaError_t launch_weigh_window(const WeighCall &q, int least, int sms, cudaStream_t st);
 cudaError_t launch_evict(const EvictCall &q, int sms, cudaStream_t st);
 
 }  // namespace cache
