@@ -31,9 +31,8 @@ namespace cache {
 constexpr int kSelThr = 1024;
 constexpr int kSelWarps = kSelThr / 32;
 constexpr int kBins = 2048;
-constexpr int kKeysMax = 48 * 1024;  // keys of a CTA's slice kept in shared memory (192 KB)
+constexpr int kKeysMax = 20 * 1024;  // keys of a CTA's slice kept in shared memory (80 KB: two CTAs per SM)
 constexpr int kMoveThreads = 128;
-constexpr int kMoveHold = 8;         // 16-byte pieces of rows that a thread keeps in registers
 
 struct EvictArgs {
     View c;
@@ -250,7 +249,10 @@ __global__ void __launch_bounds__(kSelThr) cache_evict_select_kernel(const __gri
     cl.sync();  // no CTA leaves while others read its shared memory
 }
 
-template <int D, int WARPS>
+// HOLD: 16-byte pieces of rows that a thread keeps in registers. The three
+// dependent look-ups of a row (kept slot, block, data) are made for all HOLD
+// rows at a time.
+template <int D, int WARPS, int HOLD>
 __global__ void __launch_bounds__(kMoveThreads) cache_evict_move_kernel(const __grid_constant__ EvictArgs a)
 {
     constexpr int UNITS = kMoveThreads / (32 * WARPS);
@@ -285,49 +287,53 @@ __global__ void __launch_bounds__(kMoveThreads) cache_evict_move_kernel(const __
     const int32_t *const kept = a.kept + y * a.keep + p0;
     const int col = (ut % TPR) * 16, r0 = ut / TPR;
     float top = 0.0f;
-    auto fetch = [&](int r, uint4 &x, float &s) {
-        const int t = __ldcg(kept + r);
-        const int b_old = c.page_of(t);
-        const int page = __ldg(c.bt + (long long)i * c.W + b_old);
-        if (page < 0 || (long long)page >= c.nb) {
+    uint4 x[HOLD];
+    float s[HOLD];
+    // rows rb + k RPP of the new block: codes and scales (zeros for none)
+    auto fetch = [&](int rb) {
+        int t[HOLD], page[HOLD];
+#pragma unroll
+        for (int k = 0; k < HOLD; ++k)
+            t[k] = rb + k * RPP < n ? __ldcg(kept + rb + k * RPP) : -1;
+#pragma unroll
+        for (int k = 0; k < HOLD; ++k)
+            page[k] = t[k] >= 0 ? __ldg(c.bt + (long long)i * c.W + c.page_of(t[k])) : 0;
+        bool bad = false;
+#pragma unroll
+        for (int k = 0; k < HOLD; ++k) {
+            const bool ok = t[k] >= 0 && page[k] >= 0 && (long long)page[k] < c.nb;
+            bad |= t[k] >= 0 && !ok;
+            x[k] = make_uint4(0, 0, 0, 0);
+            s[k] = 0.0f;
+            if (ok) {
+                const long long phys = (long long)page[k] * c.H + h;
+                x[k] = __ldg(reinterpret_cast<const uint4 *>(
+                    pool + (phys * c.P + (t[k] - c.page_of(t[k]) * c.P)) * D + col));
+                s[k] = __ldg(scale + phys);
+            }
+        }
+        if (bad)
             atomicOr(c.status, (uint32_t)PMQA_DEV_BAD_BLOCK_ID);
-            x = make_uint4(0, 0, 0, 0);
-            s = 0.0f;
-            return;
-        }
-        const long long phys = (long long)page * c.H + h;
-        x = __ldg(reinterpret_cast<const uint4 *>(pool + (phys * c.P + (t - b_old * c.P)) * D + col));
-        s = __ldg(scale + phys);
     };
-    auto widen = [&](const uint4 &x, float s) {
-        const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+    auto widen = [&]() {
 #pragma unroll
-        for (int z = 0; z < 4; ++z) {
-            float f0, f1, f2, f3;
-            e4m3x2_to_f32x2(e[z] & 0xFFFFu, f0, f1);
-            e4m3x2_to_f32x2(e[z] >> 16, f2, f3);
-            const float m = fmaxf(fmaxf(fabsf(f0), fabsf(f1)), fmaxf(fabsf(f2), fabsf(f3))) * s;
-            top = fmaxf(top, m < INFINITY ? m : 0.0f);
+        for (int k = 0; k < HOLD; ++k) {
+            const uint32_t e[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                float f0, f1, f2, f3;
+                e4m3x2_to_f32x2(e[z] & 0xFFFFu, f0, f1);
+                e4m3x2_to_f32x2(e[z] >> 16, f2, f3);
+                const float m = fmaxf(fmaxf(fabsf(f0), fabsf(f1)), fmaxf(fabsf(f2), fabsf(f3))) * s[k];
+                top = fmaxf(top, m < INFINITY ? m : 0.0f);
+            }
         }
     };
-    uint4 x[kMoveHold];
-    float s[kMoveHold];
-#pragma unroll
-    for (int k = 0; k < kMoveHold; ++k) {
-        const int r = r0 + k * RPP;
-        x[k] = make_uint4(0, 0, 0, 0);
-        s[k] = 0.0f;
-        if (r < n)
-            fetch(r, x[k], s[k]);
-    }
-#pragma unroll
-    for (int k = 0; k < kMoveHold; ++k)
-        widen(x[k], s[k]);
-    for (int r = r0 + kMoveHold * RPP; r < n; r += RPP) {
-        uint4 z;
-        float sz;
-        fetch(r, z, sz);
-        widen(z, sz);
+    // blocks longer than the registers hold are read twice: for the maximum, and to move
+    const bool once = n <= HOLD * RPP;
+    for (int rb = r0; rb < n; rb += HOLD * RPP) {
+        fetch(rb);
+        widen();
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
@@ -345,28 +351,51 @@ __global__ void __launch_bounds__(kMoveThreads) cache_evict_move_kernel(const __
     uint8_t *const dst = (is_v ? c.v : c.k) + dphys * c.P * D;
     if (ut == 0)
         scale[dphys] = sn;
-    auto put = [&](int r, const uint4 &xr, float sr) {
-        const uint32_t e[4] = {xr.x, xr.y, xr.z, xr.w};
-        uint32_t o[4];
+    for (int rb = r0; rb < n; rb += HOLD * RPP) {
+        if (!once)
+            fetch(rb);
 #pragma unroll
-        for (int z = 0; z < 4; ++z) {
-            float f0, f1, f2, f3;
-            e4m3x2_to_f32x2(e[z] & 0xFFFFu, f0, f1);
-            e4m3x2_to_f32x2(e[z] >> 16, f2, f3);
-            o[z] = f32x4_to_e4m3x4(f0 * sr * inv, f1 * sr * inv, f2 * sr * inv, f3 * sr * inv);
+        for (int k = 0; k < HOLD; ++k) {
+            const int r = rb + k * RPP;
+            if (r >= n)
+                break;
+            const uint32_t e[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+            uint32_t o[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                float f0, f1, f2, f3;
+                e4m3x2_to_f32x2(e[z] & 0xFFFFu, f0, f1);
+                e4m3x2_to_f32x2(e[z] >> 16, f2, f3);
+                o[z] = f32x4_to_e4m3x4(f0 * s[k] * inv, f1 * s[k] * inv, f2 * s[k] * inv, f3 * s[k] * inv);
+            }
+            *reinterpret_cast<uint4 *>(dst + (long long)r * D + col) = make_uint4(o[0], o[1], o[2], o[3]);
         }
-        *reinterpret_cast<uint4 *>(dst + (long long)r * D + col) = make_uint4(o[0], o[1], o[2], o[3]);
-    };
-#pragma unroll
-    for (int k = 0; k < kMoveHold; ++k)
-        if (r0 + k * RPP < n)
-            put(r0 + k * RPP, x[k], s[k]);
-    for (int r = r0 + kMoveHold * RPP; r < n; r += RPP) {
-        uint4 z;
-        float sz;
-        fetch(r, z, sz);
-        put(r, z, sz);
     }
+}
+
+template <int D>
+static cudaError_t launch_move(const EvictArgs &a, long long pairs, cudaStream_t st)
+{
+    // a warp's pass covers 512 / D rows: up to 4 passes of one warp, else of four warps
+    const int P = a.c.P, pass = 512 / D;
+    const bool one = P <= 4 * pass;
+    const long long units = pairs * a.pages * 2;
+    const long long grid = one ? (units + 3) / 4 : units;
+    if (grid > 0x7FFFFFFFll)
+        return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = st;
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kMoveThreads);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (one)
+        return cudaLaunchKernelEx(&cfg, cache_evict_move_kernel<D, 1, 4>, a);
+    return P <= 16 * pass ? cudaLaunchKernelEx(&cfg, cache_evict_move_kernel<D, 4, 4>, a)
+                          : cudaLaunchKernelEx(&cfg, cache_evict_move_kernel<D, 4, 8>, a);
 }
 
 cudaError_t launch_evict(const EvictCall &q, int sms, cudaStream_t st)
@@ -386,10 +415,10 @@ cudaError_t launch_evict(const EvictCall &q, int sms, cudaStream_t st)
     a.pages = (q.keep + q.c.P - 1) / q.c.P;
     const long long pairs = (long long)q.c.bs * q.c.H;
     // CTAs per cluster: enough for the longest row's keys to stay in shared
-    // memory, and (few pairs) enough to use the GPU; 8 is the portable most
+    // memory, and (few pairs) enough to use the GPU, two to an SM; 8 is the portable most
     int cs = 1;
     while (cs < 8 && (q.width > (long long)cs * kKeysMax ||
-                      (pairs * cs * 2 <= sms && q.width > (long long)cs * 4096)))
+                      (pairs * cs <= sms && q.width > (long long)cs * 4096)))
         cs *= 2;
     a.cs = cs;
     const long long chunk = ((std::min<long long>(q.width, 0x7FFFFF00ll) + cs - 1) / cs + 1023) & ~1023ll;
@@ -416,25 +445,7 @@ cudaError_t launch_evict(const EvictCall &q, int sms, cudaStream_t st)
     e = cudaLaunchKernelEx(&cfg, cache_evict_select_kernel, a);
     if (e != cudaSuccess)
         return e;
-    // one warp holds kMoveHold * 512 / D rows; four warps share longer blocks
-    const bool wide = q.c.P > kMoveHold * 512 / q.c.D;
-    const long long units = pairs * a.pages * 2;
-    const long long grid = wide ? units : (units + 3) / 4;
-    if (grid > 0x7FFFFFFFll)
-        return cudaErrorInvalidConfiguration;
-    cfg = {};
-    cfg.stream = st;
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kMoveThreads);
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (q.c.D == 128)
-        return wide ? cudaLaunchKernelEx(&cfg, cache_evict_move_kernel<128, 4>, a)
-                    : cudaLaunchKernelEx(&cfg, cache_evict_move_kernel<128, 1>, a);
-    return wide ? cudaLaunchKernelEx(&cfg, cache_evict_move_kernel<64, 4>, a)
-                : cudaLaunchKernelEx(&cfg, cache_evict_move_kernel<64, 1>, a);
+    return q.c.D == 128 ? launch_move<128>(a, pairs, st) : launch_move<64>(a, pairs, st);
 }
 
 }  // namespace cache
