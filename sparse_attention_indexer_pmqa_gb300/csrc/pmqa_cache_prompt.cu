@@ -511,7 +511,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1)
                 vmax = fmaxf(vmax, __shfl_xor_sync(kFull, vmax, o));
-            const bool even = __all_sync(kFull, kmine >= 0.0f && kmine == __shfl_sync(kFull, kmine, 0));
+            const float klead = __shfl_sync(kFull, kmine, 0);
+            const bool even = __all_sync(kFull, kmine >= 0.0f && kmine == klead);
             if (lane == 0) {
                 red[4 * (t & 1) + lw] = vmax;
                 asm volatile("st.shared.u8 [%0], %1;" ::"r"(tb + 24u + (uint32_t)lw), "r"(even ? 1u : 0u) : "memory");
