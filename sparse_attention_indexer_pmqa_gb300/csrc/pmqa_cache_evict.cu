@@ -31,7 +31,7 @@ namespace cache {
 constexpr int kSelThr = 1024;
 constexpr int kSelWarps = kSelThr / 32;
 constexpr int kBins = 2048;
-constexpr int kKeysMax = 20 * 1024;  // keys of a CTA's slice kept in shared memory (80 KB: two CTAs per SM)
+constexpr int kKeysMax = 48 * 1024;  // keys of a CTA's slice kept in shared memory (192 KB)
 constexpr int kMoveThreads = 128;
 
 struct EvictArgs {
@@ -55,6 +55,22 @@ __device__ __forceinline__ uint32_t mass_key(float x)
         return 0u;
     const uint32_t b = __float_as_uint(x + 0.0f);
     return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+// One more key in `bin` of a histogram, for every lane with `in`: the lanes that
+// share the first one's bin (masses pile up at zero) add up first.
+__device__ __forceinline__ void count_key(uint32_t *hist, uint32_t bin, bool in, int lane)
+{
+    const uint32_t act = __ballot_sync(kFull, in);
+    if (act == 0)
+        return;
+    const int lead = __ffs(act) - 1;
+    const uint32_t first = __shfl_sync(kFull, bin, lead);
+    const uint32_t same = __ballot_sync(kFull, in && bin == first);
+    if (lane == lead)
+        atomicAdd(&hist[bin], (uint32_t)__popc(same));
+    else if (in && !(same >> lane & 1u))
+        atomicAdd(&hist[bin], 1u);
 }
 
 __global__ void __launch_bounds__(kSelThr) cache_evict_select_kernel(const __grid_constant__ EvictArgs a)
@@ -120,13 +136,10 @@ __global__ void __launch_bounds__(kSelThr) cache_evict_select_kernel(const __gri
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const int t = t0 + k * kSelThr + tid;
-            if (t >= hi)
-                continue;
             const uint32_t key = mass_key(f[k]);
-            if (t - lo < a.key_cap)
+            if (t < hi && t - lo < a.key_cap)
                 keys[t - lo] = key;
-            if (t >= mid0 && t < mid1)
-                atomicAdd(&hist[0][key >> 21], 1u);
+            count_key(hist[0], key >> 21, t < hi && t >= mid0 && t < mid1, lane);
         }
     }
     uint32_t want = (uint32_t)(a.keep - a.sinks - a.recent);  // rank (from the top) of the last kept key
@@ -176,12 +189,10 @@ __global__ void __launch_bounds__(kSelThr) cache_evict_select_kernel(const __gri
         const int nshift = pass == 0 ? 10 : 0;
         const uint32_t nmask = pass == 0 ? 2047u : 1023u;
         const int ms = shift;
-        for (int t = lo + tid; t < hi; t += kSelThr) {
-            if (t < mid0 || t >= mid1)
-                continue;
-            const uint32_t key = key_of(t);
-            if ((key >> ms) == (prefix >> ms))
-                atomicAdd(&hn[(key >> nshift) & nmask], 1u);
+        for (int t = lo + tid; t - tid < hi; t += kSelThr) {
+            const bool mid = t < hi && t >= mid0 && t < mid1;
+            const uint32_t key = mid ? key_of(t) : 0u;
+            count_key(hn, (key >> nshift) & nmask, mid && (key >> ms) == (prefix >> ms), lane);
         }
         if (pass == 0) {
             // pass 2 counts into hist[0] again: clear it once every CTA has read it
@@ -415,7 +426,7 @@ cudaError_t launch_evict(const EvictCall &q, int sms, cudaStream_t st)
     a.pages = (q.keep + q.c.P - 1) / q.c.P;
     const long long pairs = (long long)q.c.bs * q.c.H;
     // CTAs per cluster: enough for the longest row's keys to stay in shared
-    // memory, and (few pairs) enough to use the GPU, two to an SM; 8 is the portable most
+    // memory, and (few pairs) enough to use the GPU; 8 is the portable most
     int cs = 1;
     while (cs < 8 && (q.width > (long long)cs * kKeysMax ||
                       (pairs * cs <= sms && q.width > (long long)cs * 4096)))
