@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
             a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
         return;
     }
-    const long long n_items = rg.x1 - rg.x0;
+    const long long n_items = min(rg.x1 - rg.x0, 0x7FFFFFFFll);  // a CTA never has more
     const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * S) * St::kBytes;
     float *const merge = reinterpret_cast<float *>(smem + Sh::kOffMerge);
     float2 *const mls = reinterpret_cast<float2 *>(smem + Sh::kOffMl);
@@ -123,29 +123,40 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
     // `pw` is the item whose table entry is loaded (pend_*); its copies are
     // issued one step later.
     Walk pw = w;
-    long long p_left = n_items;  // items not yet looked up
-    int pend_page = -1, pend_tok = 0, pend_h = 0;
-    bool pend_in = false;        // this lane's token is one that a row sees
+    int p_left = (int)n_items;  // items not yet looked up
+    int p_end = seen_end(pw.q, pw.b);
+    int pend_page = -1, pend_off = 0, pend_h = 0;
+    bool pend_in = false;       // this lane's token is one that a row sees
     auto look_up = [&]() {
         pend_in = false;
         if (p_left > 0) {
-            pend_tok = pw.t * kAttnTile + warp * kWarpTokens + (lane & 15);
+            const int tok = pw.t * kAttnTile + warp * kWarpTokens + (lane & 15);
+            pend_in = tok < p_end;
+            const int pg = c.page_of(tok);
+            pend_off = tok - pg * c.P;
             pend_h = pw.h;
-            pend_in = pend_tok < seen_end(pw.q, pw.b);
             if (pend_in)
-                pend_page = __ldg(c.bt + (long long)pw.i * c.W + c.page_of(pend_tok));
-            --p_left;
-            if (p_left > 0)
-                pw.template next<kAttnTile, ROWS>(c, G, a.least, a.most);
+                pend_page = __ldg(c.bt + (long long)pw.i * c.W + pg);
+            if (--p_left > 0) {
+                if (pw.t + 1 < pw.T) {
+                    ++pw.t;
+                } else {
+                    pw.template next<kAttnTile, ROWS>(c, G, a.least, a.most);
+                    p_end = seen_end(pw.q, pw.b);
+                }
+            }
         }
     };
+    constexpr int CH = D / 16, PER = 32 / CH;  // chunks a row, rows an instruction
+    const int ch = lane % CH;
+    const bool one_block = (c.P & (kWarpTokens - 1)) == 0;  // 16 tokens never leave a block
     int p_slot = 0;
     auto issue = [&]() {
         const uint32_t st = ring + (uint32_t)p_slot * St::kBytes;
         if (++p_slot == S)
             p_slot = 0;
         bool ok = pend_in;
-        if (ok && (pend_page < 0 || (long long)pend_page >= c.nb)) {
+        if (ok && (uint32_t)pend_page >= (uint32_t)min(c.nb, 0x7FFFFFFFll)) {
             atomicOr(c.status, (uint32_t)PMQA_DEV_BAD_BLOCK_ID);
             ok = false;
         }
@@ -153,22 +164,35 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
         if (lane == 0)
             asm volatile("st.shared.b32 [%0], %1;" ::"r"(st + St::kOffMask), "r"(mask) : "memory");
         if (mask) {
-            const long long phys = ok ? (long long)pend_page * c.H + pend_h : 0;
-            const long long row = ok ? (phys * c.P + (pend_tok - c.page_of(pend_tok) * c.P)) * D : 0;
+            // block * H + head, and the row of the pool (both below 2^32)
+            const uint32_t phys = ok ? (uint32_t)pend_page * (uint32_t)c.H + (uint32_t)pend_h : 0u;
+            const uint32_t row = phys * (uint32_t)c.P + (uint32_t)pend_off;
             const uint32_t sdst = st + (lane < 16 ? St::kOffKs : St::kOffVs) + (uint32_t)(lane & 15) * 4u;
             if (ok)
                 cp_async_4(sdst, (lane < 16 ? c.ks : c.vs) + phys);
             else
                 asm volatile("st.shared.b32 [%0], %1;" ::"r"(sdst), "r"(0) : "memory");
-            constexpr int CH = D / 16, PER = 32 / CH;  // chunks a row, rows an instruction
-            const int ch = lane % CH;
+            if (one_block) {
+                // token 0 exists (a block's tokens exist up to some one): 16 rows on end
+                const uint64_t src = (uint64_t)__shfl_sync(kFull, row, 0) * D + (uint32_t)lane * 16u;
+                const uint8_t *const ks = c.k + src, *const vs = c.v + src;
 #pragma unroll
-            for (int k = 0; k < kWarpTokens / PER; ++k) {
-                const int r = k * PER + lane / CH;
-                const long long src = __shfl_sync(kFull, row, r) + ch * 16;
-                const uint32_t nb = (mask >> r) & 1u ? 16u : 0u;
-                cp_async_16(st + St::at(r, ch), c.k + src, nb);
-                cp_async_16(st + St::kRows + St::at(r, ch), c.v + src, nb);
+                for (int k = 0; k < kWarpTokens / PER; ++k) {
+                    const int r = k * PER + lane / CH;
+                    const uint32_t nb = (mask >> r) & 1u ? 16u : 0u;
+                    cp_async_16(st + St::at(r, ch), ks + k * 512, nb);
+                    cp_async_16(st + St::kRows + St::at(r, ch), vs + k * 512, nb);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < kWarpTokens / PER; ++k) {
+                    const int r = k * PER + lane / CH;
+                    const uint32_t nb = (mask >> r) & 1u ? 16u : 0u;
+                    const uint32_t rr = __shfl_sync(kFull, row, r);
+                    const uint64_t src = (uint64_t)(nb ? rr : 0u) * D + (uint32_t)ch * 16u;
+                    cp_async_16(st + St::at(r, ch), c.k + src, nb);
+                    cp_async_16(st + St::kRows + St::at(r, ch), c.v + src, nb);
+                }
             }
         }
         cp_async_commit();
@@ -335,22 +359,23 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
             // vref moves when the chunk's largest scale leaves [2^-5, 2^5] vref
             // (not to scales under 2^-60 of the largest seen: blocks of zeros).
             float vmax = fmaxf(fabsf(vs0), fabsf(vs1));
-            vmax = fmaxf(vmax, __shfl_xor_sync(kFull, vmax, 4));
-            vmax = fmaxf(vmax, __shfl_xor_sync(kFull, vmax, 8));
-            vmax = fmaxf(vmax, __shfl_xor_sync(kFull, vmax, 16));
-            if (!(vmax <= 32.0f * vref && 32.0f * vmax >= vref) && vmax > 1e-36f &&
-                vmax >= vtop * 8.6736174e-19f) {
-                const float f = vref / vmax;
-                vref = vmax;
-                vinv = 1.0f / vmax;
-                vtop = fmaxf(vtop, vmax);
+            if (__any_sync(kFull, vmax > 32.0f * vref) || __all_sync(kFull, 32.0f * vmax < vref)) {
+                vmax = fmaxf(vmax, __shfl_xor_sync(kFull, vmax, 4));
+                vmax = fmaxf(vmax, __shfl_xor_sync(kFull, vmax, 8));
+                vmax = fmaxf(vmax, __shfl_xor_sync(kFull, vmax, 16));
+                if (vmax > 1e-36f && vmax >= vtop * 8.6736174e-19f) {
+                    const float f = vref / vmax;
+                    vref = vmax;
+                    vinv = 1.0f / vmax;
+                    vtop = fmaxf(vtop, vmax);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int j = 0; j < MT; ++j)
+                        for (int j = 0; j < MT; ++j)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            acc[nt][j][e] *= f;
+                            for (int e = 0; e < 4; ++e)
+                                acc[nt][j][e] *= f;
+                }
             }
             const float rv0 = vs0 * vinv, rv1 = vs1 * vinv;
             uint32_t pb[NT][2];
