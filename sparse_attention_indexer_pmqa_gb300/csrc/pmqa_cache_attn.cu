@@ -40,6 +40,7 @@ constexpr int kWarpTokens = 16;
 constexpr int kAttnTile = kAttnWarps * kWarpTokens;
 constexpr float kSlack = 8.0f;    // p <= 2^8 before the maximum moves
 constexpr int kLeastTiles = 2;    // fewest tiles a CTA takes (small problems)
+constexpr int kWholeTokens = 1024;
 
 struct AttnArgs {
     View c;
@@ -49,6 +50,7 @@ struct AttnArgs {
     float scale_log2;    // sm_scale log2(e)
     int heads, group;
     int least, most;     // requests with least <= n group <= most are this kernel's
+    int whole;           // contexts are short: none is cut between CTAs
     int4 *meta;          // per CTA: (i, h, b, 2 parts + (slot & 1)) of the context it leaves open
     float *ml;           // [2 CTAs][8 NT][2]
     float *part;         // [2 CTAs][8 NT][D]
@@ -108,7 +110,19 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
             a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
         return;
     }
-    const long long n_items = min(rg.x1 - rg.x0, 0x7FFFFFFFll);  // a CTA never has more
+    long long x = rg.x0;
+    if (a.whole && w.t > 0) {
+        // uncut: a context belongs to the CTA whose range holds its first tile
+        x += w.T - w.t;
+        w.t = w.T - 1;
+        if (x < rg.x1)
+            w.template next<kAttnTile, ROWS>(c, G, a.least, a.most);
+    }
+    if (x >= rg.x1) {
+        if (tid == 0)
+            a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+        return;
+    }
     const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * S) * St::kBytes;
     float *const merge = reinterpret_cast<float *>(smem + Sh::kOffMerge);
     float2 *const mls = reinterpret_cast<float2 *>(smem + Sh::kOffMl);
@@ -123,13 +137,14 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
     // `pw` is the item whose table entry is loaded (pend_*); its copies are
     // issued one step later.
     Walk pw = w;
-    int p_left = (int)n_items;  // items not yet looked up
+    long long p_x = x;          // its index
+    bool p_more = true;         // it is one of this CTA's
     int p_end = seen_end(pw.q, pw.b);
     int pend_page = -1, pend_off = 0, pend_h = 0;
     bool pend_in = false;       // this lane's token is one that a row sees
     auto look_up = [&]() {
         pend_in = false;
-        if (p_left > 0) {
+        if (p_more) {
             const int tok = pw.t * kAttnTile + warp * kWarpTokens + (lane & 15);
             pend_in = tok < p_end;
             const int pg = c.page_of(tok);
@@ -137,10 +152,13 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
             pend_h = pw.h;
             if (pend_in)
                 pend_page = __ldg(c.bt + (long long)pw.i * c.W + pg);
-            if (--p_left > 0) {
-                if (pw.t + 1 < pw.T) {
-                    ++pw.t;
-                } else {
+            ++p_x;
+            if (pw.t + 1 < pw.T) {
+                ++pw.t;
+                p_more = p_x < rg.x1 || a.whole;
+            } else {
+                p_more = p_x < rg.x1;
+                if (p_more) {
                     pw.template next<kAttnTile, ROWS>(c, G, a.least, a.most);
                     p_end = seen_end(pw.q, pw.b);
                 }
@@ -212,7 +230,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
     int lim[NT][2];               // last slot that the row sees, -1 for padding
     float vref = 0.0f, vinv = 0.0f, vtop = 0.0f;
     int seg = -1, end = 0, c_slot = 0;
-    long long x = rg.x0;
+    const long long x_first = x;
     int4 open = make_int4(0, 0, 0, 0);
     bool fresh = true;
 #pragma unroll 1
@@ -422,7 +440,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
             }
         }
         ++x;
-        if (w.t + 1 < w.T && x < rg.x1) {
+        if (w.t + 1 < w.T && (x < rg.x1 || a.whole)) {
             ++w.t;
             continue;
         }
@@ -441,7 +459,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
                     mls[warp * ROWS + nt * 8 + 2 * t4 + e] = make_float2(m[nt][e], sum);
             }
         __syncthreads();
-        const bool starts = x - rg.x0 > w.t;  // the context's first tile was this CTA's too
+        const bool starts = x - x_first > w.t;  // the context's first tile was this CTA's too
         const bool ends = w.t + 1 == w.T;
         const int slot = 2 * (int)blockIdx.x + (seg > 0 ? 1 : 0);
         const bool split = !(starts && ends);
@@ -623,6 +641,8 @@ static cudaError_t launch_rows(AttnArgs &a, uint8_t *ws, int sms, cudaStream_t s
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    if (a.whole)
+        return cudaSuccess;
     return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<D, NT>, a);
 }
 
@@ -639,6 +659,9 @@ cudaError_t launch_attn_rows(AttnCall &q, int least, int most, int sms, cudaStre
     a.group = q.heads / q.c.H;
     a.least = least;
     a.most = most;
+    // A table of at most kWholeTokens tokens: one CTA reads a context sooner than
+    // a second launch joins its parts
+    a.whole = (long long)q.c.P * q.c.W <= kWholeTokens;
     // 8, 16 or 32 rows a block: what the longest request needs, or (when longer
     // ones go elsewhere or take several blocks) what one row of every head needs
     const long long need = (long long)q.c.max_rows * a.group;
