@@ -78,7 +78,7 @@ View view(const pmqa_cache_problem *p, void *ws)
     c.W = p->max_blocks_per_seq;
     c.rows = p->rows;
     c.max_rows = p->max_rows;
-    c.p_shift = (c.P & (c.P - 1)) == 0 ? __builtin_ctz((unsigned)c.P) : -1;
+    c.p_inv = c.P == 1 ? 0xFFFFFFFFu : (uint32_t)((1ull << 32) / (uint32_t)c.P);
     c.nb = p->num_blocks;
     c.status = static_cast<uint32_t *>(ws);
     return c;

@@ -32,11 +32,16 @@ struct View {
     const int32_t *ctx;       // [bs]
     const int32_t *row_begin; // [bs + 1] or null
     int bs, H, D, P, W, rows, max_rows;
-    int p_shift;              // log2(P) when P is a power of two, else -1
+    uint32_t p_inv;           // min(2^32 - 1, floor(2^32 / P))
     long long nb;
     uint32_t *status;
 
-    __device__ __forceinline__ int page_of(int t) const { return p_shift >= 0 ? t >> p_shift : t / P; }
+    // t / P for t >= 0: the product is below the quotient by less than 1
+    __device__ __forceinline__ int page_of(int t) const
+    {
+        const int q = (int)__umulhi((uint32_t)t, p_inv);
+        return q + ((uint32_t)(q + 1) * (uint32_t)P <= (uint32_t)t ? 1 : 0);
+    }
 };
 
 // A request's rows and context, clamped to what the arrays can hold; what had
