@@ -82,7 +82,11 @@ struct AttnShape {
     static constexpr uint32_t kRing = kAttnWarps * kStages * Stage<D>::kBytes;
     static constexpr uint32_t kOffMerge = kRing;
     static constexpr uint32_t kOffMl = kOffMerge + kAttnWarps * 8 * kPitch * 4;
-    static constexpr uint32_t kSmem = kOffMl + kAttnWarps * kRows * 8;
+    static constexpr uint32_t kOffQ = kOffMl + kAttnWarps * kRows * 8;
+    // 32 rows: q's operand in shared memory (a copy per warp), the registers go to O
+    static constexpr bool kQShared = NT == 4;
+    static constexpr uint32_t kQWarp = (D / 16) * NT * 32 * 8;
+    static constexpr uint32_t kSmem = kOffQ + (kQShared ? kAttnWarps * kQWarp : 0u);
     static constexpr int kOcc = NT == 1 ? 3 : NT == 2 ? 3 : 2;
 };
 
@@ -225,7 +229,9 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
 
     // ---------------------------------------------------------- consumer state
     float acc[NT][MT][4];
-    uint32_t qb[NT][KS][2];
+    constexpr int NQ = Sh::kQShared ? 1 : NT;
+    uint32_t qb[NQ][KS][2];
+    uint2 *const qsm = reinterpret_cast<uint2 *>(smem + Sh::kOffQ + (Sh::kQShared ? warp * Sh::kQWarp : 0u)) + lane;
     float m[NT][2], l[NT][2], rc[NT][2];
     int lim[NT][2];               // last slot that the row sees, -1 for padding
     float vref = 0.0f, vinv = 0.0f, vtop = 0.0f;
@@ -274,8 +280,13 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
                         // dims 8 (k & 1) + 2 z of this thread's 16: k step (k >> 1) * 4 + (k & 1) * 2 + z / 2
                         const float lo = __uint_as_float(e[z] << 16) * up;
                         const float hi = __uint_as_float(e[z] & 0xFFFF0000u) * up;
-                        qb[nt][(k >> 1) * 4 + (k & 1) * 2 + (z >> 1)][z & 1] = pack_f16x2(lo, hi);
+                        qb[Sh::kQShared ? 0 : nt][(k >> 1) * 4 + (k & 1) * 2 + (z >> 1)][z & 1] = pack_f16x2(lo, hi);
                     }
+                }
+                if constexpr (Sh::kQShared) {
+#pragma unroll
+                    for (int k = 0; k < KS; ++k)
+                        qsm[(nt * KS + k) * 32] = make_uint2(qb[0][k][0], qb[0][k][1]);
                 }
                 const float mine = a.scale_log2 * down;
                 rc[nt][0] = __shfl_sync(kFull, mine, 8 * t4);
@@ -321,8 +332,14 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
                     e4m3x4_to_f16x2(wa[z], a0, a2);
                     e4m3x4_to_f16x2(wb[z], a1, a3);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma_f16(s[nt], a0, a1, a2, a3, qb[nt][half * 4 + z][0], qb[nt][half * 4 + z][1]);
+                    for (int nt = 0; nt < NT; ++nt) {
+                        if constexpr (Sh::kQShared) {
+                            const uint2 b = qsm[(nt * KS + half * 4 + z) * 32];
+                            mma_f16(s[nt], a0, a1, a2, a3, b.x, b.y);
+                        } else {
+                            mma_f16(s[nt], a0, a1, a2, a3, qb[nt][half * 4 + z][0], qb[nt][half * 4 + z][1]);
+                        }
+                    }
                 }
             }
             const float ks0 = __uint_as_float(lds32(st + St::kOffKs + 4u * g));

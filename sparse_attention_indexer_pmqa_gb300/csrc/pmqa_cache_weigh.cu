@@ -68,30 +68,38 @@ __global__ void __launch_bounds__(kWeighThreads, NT == 4 ? 3 : 4)
     const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * S) * St::kBytes;
 
     Walk pw = w;
-    long long p_left = rg.x1 - rg.x0;
-    int pend_page = -1, pend_tok = 0, pend_h = 0, pend_i = 0;
+    long long p_x = rg.x0;
+    int pend_page = -1, pend_off = 0, pend_tok = 0, pend_h = 0, pend_i = 0;
     bool pend_in = false;
     auto look_up = [&]() {
         pend_in = false;
-        if (p_left > 0) {
+        if (p_x < rg.x1) {
             pend_tok = pw.t * kWeighTile + warp * 16 + (lane & 15);
             pend_h = pw.h;
             pend_i = pw.i;
             pend_in = pend_tok < pw.q.ctx && pend_tok < a.width;
+            const int pg = c.page_of(pend_tok);
+            pend_off = pend_tok - pg * c.P;
             if (pend_in)
-                pend_page = __ldg(c.bt + (long long)pw.i * c.W + c.page_of(pend_tok));
-            --p_left;
-            if (p_left > 0)
-                pw.template next<kWeighTile, 0>(c, G, a.least, a.most);
+                pend_page = __ldg(c.bt + (long long)pw.i * c.W + pg);
+            if (++p_x < rg.x1) {
+                if (pw.t + 1 < pw.T)
+                    ++pw.t;
+                else
+                    pw.template next<kWeighTile, 0>(c, G, a.least, a.most);
+            }
         }
     };
+    constexpr int CH = D / 16, PER = 32 / CH;
+    const int ch = lane % CH;
+    const bool one_block = (c.P & 15) == 0;  // 16 tokens never leave a block
     int p_slot = 0;
     auto issue = [&]() {
         const uint32_t st = ring + (uint32_t)p_slot * St::kBytes;
         if (++p_slot == S)
             p_slot = 0;
         bool ok = pend_in;
-        if (ok && (pend_page < 0 || (long long)pend_page >= c.nb)) {
+        if (ok && (uint32_t)pend_page >= (uint32_t)min(c.nb, 0x7FFFFFFFll)) {
             atomicOr(c.status, (uint32_t)PMQA_DEV_BAD_BLOCK_ID);
             ok = false;
         }
@@ -100,8 +108,8 @@ __global__ void __launch_bounds__(kWeighThreads, NT == 4 ? 3 : 4)
         if (lane == 0)
             asm volatile("st.shared.b32 [%0], %1;" ::"r"(st + St::kOffMask), "r"(mask) : "memory");
         if (here) {
-            const long long phys = ok ? (long long)pend_page * c.H + pend_h : 0;
-            const long long row = ok ? (phys * c.P + (pend_tok - c.page_of(pend_tok) * c.P)) * D : 0;
+            const uint32_t phys = ok ? (uint32_t)pend_page * (uint32_t)c.H + (uint32_t)pend_h : 0u;
+            const uint32_t row = phys * (uint32_t)c.P + (uint32_t)pend_off;
             if (lane < 16) {
                 if (ok)
                     cp_async_4(st + St::kOffKs + (uint32_t)lane * 4u, c.ks + phys);
@@ -109,13 +117,19 @@ __global__ void __launch_bounds__(kWeighThreads, NT == 4 ? 3 : 4)
                 cp_async_4(st + St::kOffMass + (uint32_t)(lane & 15) * 4u,
                            a.mass_in + ((long long)pend_i * c.H + pend_h) * a.width + pend_tok);
             }
-            constexpr int CH = D / 16, PER = 32 / CH;
-            const int ch = lane % CH;
+            // 16 tokens of one block follow one another (token 0 exists if any does)
+            const uint8_t *const lead =
+                c.k + (uint64_t)(mask ? __shfl_sync(kFull, row, 0) : 0u) * D + (uint32_t)lane * 16u;
 #pragma unroll
             for (int k = 0; k < 16 / PER; ++k) {
                 const int r = k * PER + lane / CH;
-                const long long src = __shfl_sync(kFull, row, r) + ch * 16;
-                cp_async_16(st + St::at(r, ch), c.k + src, (mask >> r) & 1u ? 16u : 0u);
+                const uint32_t nb = (mask >> r) & 1u ? 16u : 0u;
+                const uint8_t *src = lead + k * 512;
+                if (!one_block) {
+                    const uint32_t rr = __shfl_sync(kFull, row, r);
+                    src = c.k + (uint64_t)(nb ? rr : 0u) * D + (uint32_t)ch * 16u;
+                }
+                cp_async_16(st + St::at(r, ch), nb ? src : c.k, nb);
             }
         }
         cp_async_commit();
