@@ -19,7 +19,8 @@ namespace cache {
 
 constexpr int kWeighWarps = 4;
 constexpr int kWeighThreads = 32 * kWeighWarps;
-constexpr int kWeighTile = 16 * kWeighWarps;
+constexpr int kWarpTok = 32;
+constexpr int kWeighTile = kWarpTok * kWeighWarps;
 constexpr int kWeighStages = 4;
 
 struct WeighArgs {
@@ -36,8 +37,8 @@ struct WeighArgs {
 
 template <int D>
 struct WeighStage {
-    static constexpr uint32_t kRows = 16 * D;
-    static constexpr uint32_t kOffKs = kRows, kOffMass = kOffKs + 64, kOffMask = kOffMass + 64;
+    static constexpr uint32_t kRows = kWarpTok * D;
+    static constexpr uint32_t kOffKs = kRows, kOffMass = kOffKs + 128, kOffMask = kOffMass + 128;
     static constexpr uint32_t kBytes = kOffMask + 16;
     __device__ static __forceinline__ uint32_t at(int r, int c)
     {
@@ -49,12 +50,11 @@ struct WeighStage {
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kWeighThreads, NT == 4 ? 3 : 4)
+__global__ void __launch_bounds__(kWeighThreads, 3)
     cache_weigh_kernel(const __grid_constant__ WeighArgs a)
 {
     using St = WeighStage<D>;
     constexpr int S = kWeighStages;
-    constexpr int ROWS = 8 * NT;
     constexpr int KS = D / 16;
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kWeighThreads, NT == 4 ? 3 : 4)
     auto look_up = [&]() {
         pend_in = false;
         if (p_x < rg.x1) {
-            pend_tok = pw.t * kWeighTile + warp * 16 + (lane & 15);
+            pend_tok = pw.t * kWeighTile + warp * kWarpTok + lane;
             pend_h = pw.h;
             pend_i = pw.i;
             pend_in = pend_tok < pw.q.ctx && pend_tok < a.width;
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kWeighThreads, NT == 4 ? 3 : 4)
     };
     constexpr int CH = D / 16, PER = 32 / CH;
     const int ch = lane % CH;
-    const bool one_block = (c.P & 15) == 0;  // 16 tokens never leave a block
+    const bool one_block = (c.P & (kWarpTok - 1)) == 0;  // 32 tokens never leave a block
     int p_slot = 0;
     auto issue = [&]() {
         const uint32_t st = ring + (uint32_t)p_slot * St::kBytes;
@@ -103,25 +103,23 @@ __global__ void __launch_bounds__(kWeighThreads, NT == 4 ? 3 : 4)
             atomicOr(c.status, (uint32_t)PMQA_DEV_BAD_BLOCK_ID);
             ok = false;
         }
-        const uint32_t mask = __ballot_sync(kFull, ok) & 0xFFFFu;
-        const uint32_t here = __ballot_sync(kFull, pend_in) & 0xFFFFu;
+        const uint32_t mask = __ballot_sync(kFull, ok);
+        const uint32_t here = __ballot_sync(kFull, pend_in);
         if (lane == 0)
             asm volatile("st.shared.b32 [%0], %1;" ::"r"(st + St::kOffMask), "r"(mask) : "memory");
         if (here) {
             const uint32_t phys = ok ? (uint32_t)pend_page * (uint32_t)c.H + (uint32_t)pend_h : 0u;
             const uint32_t row = phys * (uint32_t)c.P + (uint32_t)pend_off;
-            if (lane < 16) {
-                if (ok)
-                    cp_async_4(st + St::kOffKs + (uint32_t)lane * 4u, c.ks + phys);
-            } else if (pend_in && a.mass_in) {
-                cp_async_4(st + St::kOffMass + (uint32_t)(lane & 15) * 4u,
+            if (ok)
+                cp_async_4(st + St::kOffKs + (uint32_t)lane * 4u, c.ks + phys);
+            if (pend_in && a.mass_in)
+                cp_async_4(st + St::kOffMass + (uint32_t)lane * 4u,
                            a.mass_in + ((long long)pend_i * c.H + pend_h) * a.width + pend_tok);
-            }
-            // 16 tokens of one block follow one another (token 0 exists if any does)
+            // 32 tokens of one block follow one another (token 0 exists if any does)
             const uint8_t *const lead =
                 c.k + (uint64_t)(mask ? __shfl_sync(kFull, row, 0) : 0u) * D + (uint32_t)lane * 16u;
 #pragma unroll
-            for (int k = 0; k < 16 / PER; ++k) {
+            for (int k = 0; k < kWarpTok / PER; ++k) {
                 const int r = k * PER + lane / CH;
                 const uint32_t nb = (mask >> r) & 1u ? 16u : 0u;
                 const uint8_t *src = lead + k * 512;
@@ -144,11 +142,11 @@ __global__ void __launch_bounds__(kWeighThreads, NT == 4 ? 3 : 4)
     uint32_t qb[NT][KS][2];
     float rc[NT][2], rl[NT][2];  // scale and lse (base 2) of rows 2 t4, 2 t4 + 1 of each 8
     int lim[NT][2];
-    // block b of 8 NT query rows of the current request and head into registers
-    auto load_rows = [&](int b) {
+    // the query rows of the current request and head into registers (at most 8 NT of them)
+    auto load_rows = [&]() {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int R = b * ROWS + nt * 8 + g;
+            const int R = nt * 8 + g;
             const bool has = R < w.q.n * G;
             const uint16_t *src =
                 a.q + ((long long)(w.q.r0 + R / G) * a.heads + w.h * G + R % G) * D + 16 * t4;
@@ -186,23 +184,20 @@ __global__ void __launch_bounds__(kWeighThreads, NT == 4 ? 3 : 4)
             rc[nt][1] = __shfl_sync(kFull, mine, 8 * t4 + 4);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int Re = b * ROWS + nt * 8 + 2 * t4 + e;
+                const int Re = nt * 8 + 2 * t4 + e;
                 const bool row = Re < w.q.n * G;
                 lim[nt][e] = row ? w.q.ctx - w.q.n + Re / G : -1;
                 rl[nt][e] = row ? __ldg(a.lse + (long long)(w.q.r0 + Re / G) * a.heads + w.h * G + Re % G) * kLog2e
-                                : 0.0f;
+                                : INFINITY;
             }
         }
     };
     int c_slot = 0;
     bool fresh = true;
-    int blocks = 0;
 #pragma unroll 1
     for (long long x = rg.x0; x < rg.x1;) {
         if (fresh) {
-            blocks = (w.q.n * G + ROWS - 1) / ROWS;
-            if (blocks > 0)
-                load_rows(0);
+            load_rows();
             fresh = false;
         }
         cp_async_wait_group<S - 2>();
@@ -212,57 +207,60 @@ __global__ void __launch_bounds__(kWeighThreads, NT == 4 ? 3 : 4)
         const uint32_t st = ring + (uint32_t)c_slot * St::kBytes;
         if (++c_slot == S)
             c_slot = 0;
-        const int base = w.t * kWeighTile + warp * 16;
+        const int base = w.t * kWeighTile + warp * kWarpTok;
         if (base < w.q.ctx) {
             const uint32_t mask = lds32(st + St::kOffMask);
-            uint32_t ka[KS][4];
+            float s[2][NT][4];
 #pragma unroll
-            for (int half = 0; half < D / 64; ++half) {
-                const uint4 u0 = lds128(st + St::at(g, half * 4 + t4));
-                const uint4 u1 = lds128(st + St::at(g + 8, half * 4 + t4));
-                const uint32_t wa[4] = {u0.x, u0.y, u0.z, u0.w}, wb[4] = {u1.x, u1.y, u1.z, u1.w};
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    e4m3x4_to_f16x2(wa[z], ka[half * 4 + z][0], ka[half * 4 + z][2]);
-                    e4m3x4_to_f16x2(wb[z], ka[half * 4 + z][1], ka[half * 4 + z][3]);
-                }
-            }
-            const float ks0 = __uint_as_float(lds32(st + St::kOffKs + 4u * g));
-            const float ks1 = __uint_as_float(lds32(st + St::kOffKs + 4u * g + 32u));
-            const bool k0 = (mask >> g) & 1u, k1 = (mask >> (g + 8)) & 1u;
-            float sum0 = 0.0f, sum1 = 0.0f;
-#pragma unroll 1
-            for (int b = 0; b < blocks; ++b) {
-                if (b > 0)
-                    load_rows(b);
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    for (int e = 0; e < 4; ++e)
+                        s[u][nt][e] = 0.0f;
 #pragma unroll
-                    for (int k = 0; k < KS; ++k)
-                        mma_f16(s, ka[k][0], ka[k][1], ka[k][2], ka[k][3], qb[nt][k][0], qb[nt][k][1]);
+            for (int half = 0; half < D / 64; ++half)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float w0 = ex2_approx(s[e] * (ks0 * rc[nt][e]) - rl[nt][e]);
-                        const float w1 = ex2_approx(s[2 + e] * (ks1 * rc[nt][e]) - rl[nt][e]);
-                        sum0 += k0 && base + g <= lim[nt][e] ? w0 : 0.0f;
-                        sum1 += k1 && base + g + 8 <= lim[nt][e] ? w1 : 0.0f;
+                for (int u = 0; u < 2; ++u) {
+                    const uint4 u0 = lds128(st + St::at(g + 16 * u, half * 4 + t4));
+                    const uint4 u1 = lds128(st + St::at(g + 16 * u + 8, half * 4 + t4));
+                    const uint32_t wa[4] = {u0.x, u0.y, u0.z, u0.w}, wb[4] = {u1.x, u1.y, u1.z, u1.w};
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        uint32_t a0, a1, a2, a3;
+                        e4m3x4_to_f16x2(wa[z], a0, a2);
+                        e4m3x4_to_f16x2(wb[z], a1, a3);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma_f16(s[u][nt], a0, a1, a2, a3, qb[nt][half * 4 + z][0], qb[nt][half * 4 + z][1]);
                     }
                 }
+            // every row sees every token of the chunk (rows that do not exist weigh 0)
+            const bool whole = mask == kFull && base + kWarpTok - 1 <= w.q.ctx - w.q.n;
+            float sum[4];  // of tokens g, g + 8, g + 16, g + 24
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int tok = g + 8 * v;
+                const float ks = __uint_as_float(lds32(st + St::kOffKs + 4u * (uint32_t)tok));
+                const bool have = (mask >> tok) & 1u;
+                float t = 0.0f;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float y = ex2_approx(s[v >> 1][nt][2 * (v & 1) + e] * (ks * rc[nt][e]) - rl[nt][e]);
+                        t += whole || (have && base + tok <= lim[nt][e]) ? y : 0.0f;
+                    }
+                t += __shfl_xor_sync(kFull, t, 1);
+                sum[v] = t + __shfl_xor_sync(kFull, t, 2);
             }
-            if (blocks > 1)
-                load_rows(0);
-            sum0 += __shfl_xor_sync(kFull, sum0, 1);
-            sum0 += __shfl_xor_sync(kFull, sum0, 2);
-            sum1 += __shfl_xor_sync(kFull, sum1, 1);
-            sum1 += __shfl_xor_sync(kFull, sum1, 2);
-            if (t4 < 2) {
-                const int t = base + g + 8 * t4;
-                if (t < w.q.ctx && t < a.width) {
-                    const float had =
-                        a.mass_in ? __uint_as_float(lds32(st + St::kOffMass + 4u * (uint32_t)(g + 8 * t4))) : 0.0f;
-                    a.mass_out[((long long)w.i * c.H + w.h) * a.width + t] = had + (t4 ? sum1 : sum0);
-                }
+            // lane (g, t4) writes token g + 8 t4
+            const int tok = g + 8 * t4, slot = base + tok;
+            if (slot < w.q.ctx && slot < a.width) {
+                const float got = t4 == 0 ? sum[0] : t4 == 1 ? sum[1] : t4 == 2 ? sum[2] : sum[3];
+                const float had =
+                    a.mass_in ? __uint_as_float(lds32(st + St::kOffMass + 4u * (uint32_t)tok)) : 0.0f;
+                a.mass_out[((long long)w.i * c.H + w.h) * a.width + slot] = had + got;
             }
         }
         ++x;
@@ -284,7 +282,7 @@ static cudaError_t launch(const WeighArgs &a, int sms, cudaStream_t st)
     cudaError_t e = allow_smem(cache_weigh_kernel<D, NT>, smem, done);
     if (e != cudaSuccess)
         return e;
-    cache_weigh_kernel<D, NT><<<sms * (NT == 4 ? 3 : 4), kWeighThreads, smem, st>>>(a);
+    cache_weigh_kernel<D, NT><<<sms * 3, kWeighThreads, smem, st>>>(a);
     return cudaGetLastError();
 }
 
