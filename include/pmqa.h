@@ -380,8 +380,8 @@ int pmqa_sparse_mla_merge(const void *outs, const float *lses, int32_t parts, in
  *                 has the n_i = row_begin[i + 1] - row_begin[i] <= max_rows rows
  *                 from row_begin[i] on; its row j sits at slot
  *                 ctx_i - n_i + j and sees the slots t <= ctx_i - n_i + j.
- *                 Rows of no request are neither read nor written. Unused by
- *                 pmqa_cache_evict (as are rows and max_rows).
+ *                 Rows of no request are neither read nor written; max_rows is at
+ *                 least 1. Unused by pmqa_cache_evict (as are rows and max_rows).
  * head_dim must be 64 or 128, block_size at most 1024, kv_heads at most 65535,
  * num_blocks * kv_heads * block_size < 2^32 - 1 (PMQA_ERR_UNSUPPORTED otherwise). A context outside [0, block_size *
  * max_blocks_per_seq], or rows that break the rules above, are clamped and set
@@ -438,7 +438,11 @@ int pmqa_cache_append(const pmqa_cache_problem *p, const void *k, const void *v,
  *   lse  fp32 [rows, heads] or NULL
  * heads must be a multiple of kv_heads, at most 128 times kv_heads, and
  * max_rows * heads < 2^31. A row that sees no slot gives out = 0 and lse = -inf.
- * sm_scale must be finite.
+ * sm_scale must be finite. A NaN among a block's values (v) makes that column NaN
+ * for every row of the request that the block's other tokens reach, rows that do
+ * not see the NaN's token among them; a NaN key reaches only the rows that see it.
+ * One kernel launch where block_size * max_blocks_per_seq <= 640, else two, and
+ * one more where max_rows * heads / kv_heads > 32.
  */
 int pmqa_cache_attention(const pmqa_cache_problem *p, const void *q, int32_t heads, float sm_scale,
                          void *out, float *lse, void *ws, size_t ws_bytes, pmqa_stream_t stream);
@@ -451,6 +455,8 @@ int pmqa_cache_attention(const pmqa_cache_problem *p, const void *q, int32_t hea
  * lse this is; v_cache and v_scale are not read and may be NULL.
  *   mass_in   fp32 [bs, kv_heads, mass_width] or NULL (zeros); may be mass_out
  *   mass_out  fp32 [bs, kv_heads, mass_width]
+ * Every sum is formed in one order: equal calls give equal bits. One kernel
+ * launch, two where max_rows * heads / kv_heads > 32.
  */
 int pmqa_cache_weigh(const pmqa_cache_problem *p, const void *q, int32_t heads, float sm_scale,
                      const float *lse, const float *mass_in, float *mass_out, int64_t mass_width,

@@ -99,8 +99,8 @@ def _scores(p, i):
     # fp32 accumulation of D products, each sum off by at most one unit of 2^-23 of
     # the absolute products' sum; q split or scaled loses at most 2^-17 of its
     # row's largest value per element; three fp32 multiplications of the score
-    mag = torch.einsum("nhgd,htd->hgnt", q.abs(), k.abs()) * p.sm
-    top = torch.einsum("nhg,ht->hgnt", q.abs().amax(-1), k.abs().sum(-1)) * p.sm
+    mag = torch.einsum("nhgd,htd->hgnt", q.abs(), k.abs()) * abs(p.sm)
+    top = torch.einsum("nhg,ht->hgnt", q.abs().amax(-1), k.abs().sum(-1)) * abs(p.sm)
     err = mag * (p.D + 4) * 2.0 ** -23 + top * 2.0 ** -17
     j = torch.arange(n)[:, None]
     late = torch.arange(c)[None, :] > c - n + j
@@ -158,10 +158,12 @@ def weigh(p, lse, mass_in):
         r0 = int(p.rb[i])
         l = lse[r0:r0 + n].double().reshape(n, p.H, p.G).permute(1, 2, 0)[..., None]
         w = torch.where(torch.isinf(s), torch.zeros_like(s), (s - l).exp())
-        # the exponent's error, 2^-20 for the exponential and lse in base 2, and the fp32 sum
+        # the exponent's error, 2^-20 for the exponential and lse in base 2, the fp32
+        # sum, and 2^-126 where a weight below the normal range is taken for 0
         d = w * (err + 2.0 ** -18 + l.abs().nan_to_num(0, 0, 0) * 2.0 ** -22)
         out[i, :, :c] += w.sum((1, 2))[:, :c]
         tol[i, :, :c] = d.sum((1, 2))[:, :c] + out[i, :, :c].abs() * (n * p.G + 2) * 2.0 ** -24
+        tol[i, :, :c] += n * p.G * 2.0 ** -126
     return out, tol
 
 
