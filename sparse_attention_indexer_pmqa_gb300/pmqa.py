@@ -581,6 +581,8 @@ def pmqa_cache_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, co
                          want_lse: bool = False, ws=None, stream=None):
     """Attention of q (bf16 [rows, heads, head_dim]) to the cached tokens: bf16
     out of q's shape (and fp32 lse [rows, heads] when asked for or given)."""
+    import torch
+
     rows, heads, head_dim = q.shape
     p = make_cache_problem(k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
                            row_begin, rows, max_rows)
@@ -590,11 +592,11 @@ def pmqa_cache_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, co
     assert head_dim == p.head_dim
     _like(q, dev, bf16, n)
     if out is None:
-        out = q.new_empty((rows, heads, head_dim))
+        out = torch.empty_like(q)
     else:
         _like(out, dev, bf16, n)
     if lse is None:
-        lse = q.new_empty((rows, heads), dtype=f32) if want_lse else None
+        lse = torch.empty((rows, heads), dtype=f32, device=q.device) if want_lse else None
     else:
         _like(lse, dev, f32, rows * heads)
     _cache_call("pmqa_cache_attention", p, dev, stream, ws, q.data_ptr(), heads, sm_scale,
@@ -641,6 +643,8 @@ def pmqa_cache_evict(k_cache, v_cache, k_scale, v_scale, block_tables, context_l
     """Keep at most `keep` tokens per request and kv head (the first `sinks`,
     the last `recent`, and those with the most mass) in the blocks of
     new_tables; returns (kept [bs, kv_heads, keep], lens_out [bs], mass_out)."""
+    import torch
+
     p = make_cache_problem(k_cache, v_cache, k_scale, v_scale, block_tables, context_lens)
     dev = k_cache.get_device()
     f32, i32 = _torch()[:2]
@@ -648,15 +652,15 @@ def pmqa_cache_evict(k_cache, v_cache, k_scale, v_scale, block_tables, context_l
     _like(mass, dev, f32, pairs * width)
     _like(new_tables, dev, i32, p.bs * new_tables.shape[-1])
     if kept is None:
-        kept = mass.new_empty((p.bs, p.kv_heads, max(keep, 0)), dtype=i32)
+        kept = torch.empty((p.bs, p.kv_heads, max(keep, 0)), dtype=i32, device=mass.device)
     else:
         _like(kept, dev, i32, pairs * keep)
     if lens_out is None:
-        lens_out = mass.new_empty((p.bs,), dtype=i32)
+        lens_out = torch.empty_like(context_lens)
     else:
         _like(lens_out, dev, i32, p.bs)
     if mass_out is None:
-        mass_out = mass.new_empty((p.bs, p.kv_heads, width))
+        mass_out = torch.empty_like(mass)
     else:
         _like(mass_out, dev, f32, pairs * width)
     _cache_call("pmqa_cache_evict", p, dev, stream, ws, mass.data_ptr(), width, keep, sinks,
