@@ -443,6 +443,7 @@ int pmqa_cache_append(const pmqa_cache_problem *p, const void *k, const void *v,
  * not see the NaN's token among them; a NaN key reaches only the rows that see it.
  * One kernel launch where block_size * max_blocks_per_seq <= 640, else two, and
  * one more where max_rows * heads / kv_heads > 32.
+ * Every sum is formed in one order: equal calls give equal bits.
  */
 int pmqa_cache_attention(const pmqa_cache_problem *p, const void *q, int32_t heads, float sm_scale,
                          void *out, float *lse, void *ws, size_t ws_bytes, pmqa_stream_t stream);

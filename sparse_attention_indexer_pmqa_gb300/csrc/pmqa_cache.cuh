@@ -182,38 +182,52 @@ struct Walk {
 // What every CTA finds out at its start: its item range and the first item.
 struct Range {
     long long x0, x1, total;
+    long long C;       // CTAs that take items
     int i;             // request of item x0
     long long before;  // items before request i
 };
 
 // Called by all THREADS threads of the CTA. Two passes over the requests: the
 // number of items, then the request that holds item x0. `least_items`: no CTA
-// takes fewer items than this while there are any left.
+// takes fewer items than this while there are any left; `join_cost`: what it costs
+// to join one more part of a (request, head, row block), in items (0: nothing).
+// With T items and k CTAs each such context takes T / k + k join_cost, least at
+// k = sqrt(T / join_cost): so many CTAs per context at most, on average.
 template <int TILE, int ROWS, int THREADS>
 __device__ __forceinline__ void find_range(const View &a, int group, int least, int most,
-                                           int least_items, Range &out, Walk &w)
+                                           int least_items, float join_cost, Range &out,
+                                           Walk &w)
 {
-    __shared__ long long s_sum[THREADS / 32];
+    __shared__ long long s_sum[THREADS / 32], s_pairs[THREADS / 32];
     __shared__ Range s_range;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    long long mine = 0;
+    long long sum = 0, pairs = 0;
     int T, B;
     for (int i = tid; i < a.bs; i += THREADS) {
         const Request q = load_request(a, i, blockIdx.x == 0);
-        mine += Walk::items<TILE, ROWS>(a, q, group, least, most, T, B);
+        sum += Walk::items<TILE, ROWS>(a, q, group, least, most, T, B);
+        pairs += (long long)a.H * B;
     }
-    long long sum = mine;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
+    for (int o = 16; o > 0; o >>= 1) {
         sum += __shfl_xor_sync(kFull, sum, o);
-    if (lane == 0)
+        pairs += __shfl_xor_sync(kFull, pairs, o);
+    }
+    if (lane == 0) {
         s_sum[warp] = sum;
+        s_pairs[warp] = pairs;
+    }
     __syncthreads();
     long long total = 0;
+    pairs = 0;
 #pragma unroll
-    for (int k = 0; k < THREADS / 32; ++k)
+    for (int k = 0; k < THREADS / 32; ++k) {
         total += s_sum[k];
-    const long long want = (total + least_items - 1) / least_items;
+        pairs += s_pairs[k];
+    }
+    long long want = (total + least_items - 1) / least_items;
+    if (join_cost > 0.0f)
+        want = min(want, max(pairs, (long long)sqrtf((float)total * (float)pairs / join_cost)));
     const long long C = want < (long long)gridDim.x ? want : (long long)gridDim.x;
     const long long c = blockIdx.x;
     const long long x0 = c < C ? c * total / C : total, x1 = c < C ? (c + 1) * total / C : total;
@@ -256,6 +270,7 @@ __device__ __forceinline__ void find_range(const View &a, int group, int least, 
     out.x0 = x0;
     out.x1 = x1;
     out.total = total;
+    out.C = C;
     if (x0 < x1) {
         out.i = s_range.i;
         out.before = s_range.before;

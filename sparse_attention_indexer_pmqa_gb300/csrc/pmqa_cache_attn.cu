@@ -40,6 +40,9 @@ constexpr int kWarpTokens = 16;
 constexpr int kAttnTile = kAttnWarps * kWarpTokens;
 constexpr float kSlack = 8.0f;    // p <= 2^8 before the maximum moves
 constexpr int kLeastTiles = 2;    // fewest tiles a CTA takes (small problems)
+// Joining one more part, in tiles: with it 60000 tokens of one kv head take 27 us,
+// cut over every CTA 70. (With 32 rows the bound would cost the main loop registers.)
+constexpr float kJoinCost = 0.15f;
 constexpr int kWholeTokens = 640;
 
 struct AttnArgs {
@@ -108,7 +111,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
 
     Range rg;
     Walk w;
-    find_range<kAttnTile, ROWS, kAttnThreads>(c, G, a.least, a.most, kLeastTiles, rg, w);
+    find_range<kAttnTile, ROWS, kAttnThreads>(c, G, a.least, a.most, kLeastTiles, NT == 4 ? 0.0f : kJoinCost, rg, w);
     if (rg.x0 >= rg.x1) {
         if (tid == 0)
             a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
@@ -545,9 +548,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
         if (starts && !ends) {
             // this CTA is the first of several: it names the parts for the joining kernel
             const long long last = x - 1 + (w.T - 1 - w.t);
-            const long long want = (rg.total + kLeastTiles - 1) / kLeastTiles;
-            const long long C = want < (long long)gridDim.x ? want : (long long)gridDim.x;
-            const int cta = (int)(((last + 1) * C - 1) / rg.total);
+            const int cta = (int)(((last + 1) * rg.C - 1) / rg.total);
             open = make_int4(w.i, w.h, w.b, 2 * (cta - (int)blockIdx.x + 1) + (slot & 1));
         }
         if (x >= rg.x1)
@@ -678,7 +679,9 @@ cudaError_t launch_attn_rows(AttnCall &q, int least, int most, int sms, cudaStre
     a.most = most;
     // A table of at most kWholeTokens tokens: uncut, one CTA reads 500 tokens in
     // 11.4 us (990 in 17.6); cut and joined, 10 us and a second launch, which
-    // costs the host about 5 us
+    // costs the host about 4 us. (The CTA that writes the last part as the joining
+    // one saves that launch, but 4000 tokens then take 18 us instead of 15, and
+    // 60000 take 58 instead of 38.)
     a.whole = (long long)q.c.P * q.c.W <= kWholeTokens;
     // 8, 16 or 32 rows a block: what the longest request needs, or (when longer
     // ones go elsewhere or take several blocks) what one row of every head needs

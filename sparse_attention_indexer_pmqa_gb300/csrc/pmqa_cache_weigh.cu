@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(kWeighThreads, 3)
     const int G = a.group;
     Range rg;
     Walk w;
-    find_range<kWeighTile, 0, kWeighThreads>(c, G, a.least, a.most, 1, rg, w);
+    find_range<kWeighTile, 0, kWeighThreads>(c, G, a.least, a.most, 1, 0.0f, rg, w);
     if (rg.x0 >= rg.x1)
         return;
     const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * S) * St::kBytes;
