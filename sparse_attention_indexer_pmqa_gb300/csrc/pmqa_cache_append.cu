@@ -106,13 +106,11 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const __gr
 
     const int col = (ut % TPR) * 8, r0 = ut / TPR;
     uint4 x[kHold];
-    float top = 0.0f;
+    // the largest |value|, as the larger of two bf16 patterns without their signs
+    uint32_t big = 0;
     auto widen = [&](const uint4 &w) {
-        const uint32_t e[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int z = 0; z < 4; ++z)
-            top = fmaxf(top, fmaxf(finite_abs(__uint_as_float(e[z] << 16)),
-                                   finite_abs(__uint_as_float(e[z] & 0xFFFF0000u))));
+        big = __vmaxu2(big, __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                                     __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu)));
     };
 #pragma unroll
     for (int k = 0; k < kHold; ++k) {
@@ -125,6 +123,19 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const __gr
     // rows beyond what the registers hold: read here for the maximum, and again below
     for (int r = r0 + kHold * RPP; r < nrow; r += RPP)
         widen(__ldg(reinterpret_cast<const uint4 *>(src + r * pitch + col)));
+    float top = fmaxf(__uint_as_float(big << 16), __uint_as_float(big & 0xFFFF0000u));
+    if (big << 16 >= 0x7F800000u || big >= 0x7F800000u) {
+        // a NaN or an infinity among them: the largest of the others (rare)
+        top = 0.0f;
+        for (int r = r0; r < nrow; r += RPP) {
+            const uint4 w = __ldg(reinterpret_cast<const uint4 *>(src + r * pitch + col));
+            const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+                top = fmaxf(top, fmaxf(finite_abs(__uint_as_float(e[z] << 16)),
+                                       finite_abs(__uint_as_float(e[z] & 0xFFFF0000u))));
+        }
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
@@ -168,8 +179,8 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const __gr
         }
         if (pow2) {
 #pragma unroll
-            for (int z = 0; z < 8; ++z)
-                f[z] *= inv;
+            for (int z = 0; z < 8; z += 2)
+                fmul2(f[z], f[z + 1], f[z], f[z + 1], inv, inv);
         } else {
             // a scale that append did not make: the nearest code of x / s itself
 #pragma unroll
