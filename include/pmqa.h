@@ -383,8 +383,9 @@ int pmqa_sparse_mla_merge(const void *outs, const float *lses, int32_t parts, in
  *                 Rows of no request are neither read nor written; max_rows is at
  *                 least 1. Unused by pmqa_cache_evict (as are rows and max_rows).
  * head_dim must be 64 or 128, block_size at most 1024, kv_heads at most 65535,
- * num_blocks * kv_heads * block_size < 2^32 - 1 (PMQA_ERR_UNSUPPORTED otherwise). A context outside [0, block_size *
- * max_blocks_per_seq], or rows that break the rules above, are clamped and set
+ * num_blocks * kv_heads * block_size < 2^32 - 1 (PMQA_ERR_UNSUPPORTED otherwise).
+ * A context outside [0, block_size * max_blocks_per_seq] or above 2^31 - 2^16, or
+ * rows that break the rules above, are clamped and set
  * PMQA_DEV_BAD_CONTEXT; a table entry outside [0, num_blocks) sets
  * PMQA_DEV_BAD_BLOCK_ID, and its tokens are left out (not written by append,
  * not attended to or weighed, zeros where evict would have moved them).
@@ -438,11 +439,14 @@ int pmqa_cache_append(const pmqa_cache_problem *p, const void *k, const void *v,
  *   lse  fp32 [rows, heads] or NULL
  * heads must be a multiple of kv_heads, at most 128 times kv_heads, and
  * max_rows * heads < 2^31. A row that sees no slot gives out = 0 and lse = -inf.
- * sm_scale must be finite. A NaN among a block's values (v) makes that column NaN
+ * sm_scale must be finite (times log2(e) too). A NaN among a block's values (v) makes that column NaN
  * for every row of the request that the block's other tokens reach, rows that do
  * not see the NaN's token among them; a NaN key reaches only the rows that see it.
+ * Requests of more than 32 rows n_i * heads / kv_heads hold their values in units
+ * of the largest block scale met so far, to 2^-31 of it at worst.
  * One kernel launch where block_size * max_blocks_per_seq <= 640, else two, and
- * one more where max_rows * heads / kv_heads > 32.
+ * one more where max_rows * heads / kv_heads > 32 (that one alone where
+ * heads / kv_heads > 32).
  * Every sum is formed in one order: equal calls give equal bits.
  */
 int pmqa_cache_attention(const pmqa_cache_problem *p, const void *q, int32_t heads, float sm_scale,

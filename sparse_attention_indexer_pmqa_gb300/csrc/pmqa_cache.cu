@@ -54,7 +54,7 @@ int check(const pmqa_cache_problem *p, int need, const void *ws, size_t ws_bytes
 // heads query heads over the cache's kv heads
 int check_heads(const pmqa_cache_problem *p, int32_t heads, float sm_scale)
 {
-    if (heads < 1 || heads % p->kv_heads != 0 || !std::isfinite(sm_scale))
+    if (heads < 1 || heads % p->kv_heads != 0 || !std::isfinite(sm_scale * kLog2e))
         return PMQA_ERR_INVALID_ARG;
     if (heads / p->kv_heads > kMaxGroup || (long long)p->max_rows * heads > 0x7FFFFFFFll)
         return PMQA_ERR_UNSUPPORTED;
@@ -152,7 +152,7 @@ extern "C" int pmqa_cache_attention(const pmqa_cache_problem *p, const void *q, 
     cudaError_t e = cudaSuccess;
     if (most > kShortRows)
         e = launch_attn_prompt(a, kShortRows + 1, cuda(stream));
-    if (e == cudaSuccess)
+    if (e == cudaSuccess && heads / p->kv_heads <= kShortRows)
         e = launch_attn_rows(a, 1, kShortRows, sms, cuda(stream));
     return code_of(e);
 }

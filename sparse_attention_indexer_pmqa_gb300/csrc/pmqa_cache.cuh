@@ -21,6 +21,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kMaxGroup = 128;       // query heads per kv head
 constexpr int kMaxBlock = 1024;      // tokens per block
+constexpr int kMaxContext = 0x7FFF0000;  // slots rounded up to tiles stay in 32 bits
 constexpr int kMaxCtas = 512;        // CTAs of the short-row attention (workspace parts: 2 each)
 constexpr size_t kStatusBytes = 256;
 
@@ -54,7 +55,7 @@ __device__ __forceinline__ int clamp_ctx(const View &a, int i, bool tell)
 {
     const int c = __ldg(a.ctx + i);
     const long long cap = (long long)a.P * a.W;
-    const int hi = cap < 0x7FFFFF00ll ? (int)cap : 0x7FFFFF00;
+    const int hi = cap < kMaxContext ? (int)cap : kMaxContext;
     if (tell && (c < 0 || c > hi))
         atomicOr(a.status, (uint32_t)PMQA_DEV_BAD_CONTEXT);
     return min(max(c, 0), hi);

@@ -102,10 +102,10 @@ __global__ void __launch_bounds__(kSelThr) cache_evict_select_kernel(const __gri
         a.lens_out[i] = len;
     // what lies behind the kept tokens
     const int all = a.cs * kSelThr, at = rank * kSelThr + tid;
-    for (int p = len + at; p < a.keep; p += all)
+    for (long long p = (long long)len + at; p < a.keep; p += all)
         kept[p] = -1;
     if (mass_out)
-        for (long long p = len + at; p < a.width; p += all)
+        for (long long p = (long long)len + at; p < a.width; p += all)
             mass_out[p] = 0.0f;
     if (ctx <= a.keep) {
         for (int p = at; p < ctx; p += all) {
@@ -284,12 +284,15 @@ __global__ void __launch_bounds__(kMoveThreads) cache_evict_move_kernel(const __
     const int ctx = min((long long)clamp_ctx(c, i, false), a.width);
     const int len = min(ctx, a.keep);
     const int p0 = b * c.P, n = min(c.P, len - p0);
-    if (n <= 0)
+    if (n <= 0) {
+        griddep_wait();  // all CTAs wait: this grid must not end before the selection does
         return;
+    }
     const int dpage = __ldg(a.new_bt + (long long)i * a.new_w + b);
     if (dpage < 0 || (long long)dpage >= c.nb) {
         if (ut == 0)
             atomicOr(c.status, (uint32_t)PMQA_DEV_BAD_BLOCK_ID);
+        griddep_wait();
         return;
     }
     griddep_wait();  // the kept lists are complete

@@ -139,6 +139,7 @@ def test_head_checks(lib, call):
     assert call(lib, p, heads=2 * 129) == UNS
     assert call(lib, p, sm=math.inf) == INV
     assert call(lib, p, sm=math.nan) == INV
+    assert call(lib, p, sm=3.0e38) == INV  # infinite in base 2
     assert call(lib, problem(rows=1 << 28, max_rows=1 << 28), heads=8) == UNS
 
 
