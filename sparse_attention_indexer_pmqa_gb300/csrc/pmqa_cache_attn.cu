@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
                 }
                 top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
-                const int e2 = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 120);
+                const int e2 = min(max((int)(__float_as_uint(top) >> 23) - 127, -112), 127);
                 const float up = __uint_as_float((uint32_t)(14 - e2 + 127) << 23);
                 const float down = __uint_as_float((uint32_t)(e2 - 14 + 127) << 23);
 #pragma unroll

@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
                     top = fmaxf(top, fmaxf(fabsf(__uint_as_float(e[z] << 16)),
                                            fabsf(__uint_as_float(e[z] & 0xFFFF0000u))));
             }
-            const int e2 = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 120);
+            const int e2 = min(max((int)(__float_as_uint(top) >> 23) - 127, -119), 127);
             // a negative scale goes into q, so that c_row >= 0 keeps the order of the scores
             const float up = copysignf(__uint_as_float((uint32_t)(7 - e2 + 127) << 23), a.scale_log2);
             rc = fabsf(a.scale_log2) * __uint_as_float((uint32_t)(e2 - 7 + 127) << 23);

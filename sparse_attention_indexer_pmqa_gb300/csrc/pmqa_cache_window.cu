@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kWnThreads, 1) cache_window_kernel(const __gri
                             top = fmaxf(top, fmaxf(fabsf(f0), fabsf(f1)));
                         }
                     }
-                    const int e2 = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 120);
+                    const int e2 = min(max((int)(__float_as_uint(top) >> 23) - 127, -119), 127);
                     const float up = __uint_as_float((uint32_t)(7 - e2 + 127) << 23);
                     const uint32_t qd = sbase + kWnOffQ + (uint32_t)(row >> 7) * 2 * kWnTile;
 #pragma unroll 2

@@ -9,6 +9,7 @@ the library's kernels. There is no CPU path: if the library is missing,
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 from . import build as _build
@@ -546,6 +547,20 @@ def _like(t, dev: int, dtype, numel: int) -> None:
         f"cuda:{dev}, got {tuple(t.shape)} {t.dtype} on {t.device}"
 
 
+def _on_stream(fn):
+    """With a `stream`, everything that the call allocates, fills or copies is
+    that stream's too."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        import torch
+
+        with torch.cuda.stream(stream):
+            return fn(*args, stream=stream, **kw)
+    return call
+
+
 def _cache_call(name: str, p: CacheProblem, dev: int, stream, ws, *args) -> None:
     """Call a pmqa_cache_* function with device `dev` current, on its current
     stream unless one is given."""
@@ -564,6 +579,7 @@ def _cache_call(name: str, p: CacheProblem, dev: int, stream, ws, *args) -> None
         raise PmqaError(rc, name)
 
 
+@_on_stream
 def pmqa_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
                       row_begin, max_rows: int, *, ws=None, stream=None) -> None:
     """Quantise new tokens k, v (bf16 [rows, kv_heads, head_dim]) into the
@@ -576,6 +592,7 @@ def pmqa_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_tables, co
     _cache_call("pmqa_cache_append", p, dev, stream, ws, k.data_ptr(), v.data_ptr())
 
 
+@_on_stream
 def pmqa_cache_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
                          row_begin, max_rows: int, sm_scale: float, *, out=None, lse=None,
                          want_lse: bool = False, ws=None, stream=None):
@@ -604,6 +621,7 @@ def pmqa_cache_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, co
     return out if lse is None else (out, lse)
 
 
+@_on_stream
 def pmqa_cache_weigh(q, k_cache, k_scale, block_tables, context_lens, row_begin, max_rows: int,
                      sm_scale: float, lse, mass_in=None, *, mass_out=None, mass_width=None,
                      ws=None, stream=None):
@@ -637,6 +655,7 @@ def pmqa_cache_weigh(q, k_cache, k_scale, block_tables, context_lens, row_begin,
     return mass_out
 
 
+@_on_stream
 def pmqa_cache_evict(k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, mass,
                      keep: int, sinks: int, recent: int, new_tables, *, kept=None, lens_out=None,
                      mass_out=None, ws=None, stream=None):

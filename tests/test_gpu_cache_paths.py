@@ -317,6 +317,47 @@ def test_other_stream_and_graph(cuda_lib):
     status_is(lib, ws)
 
 
+def test_a_given_stream_also_allocates_and_fills(cuda_lib):
+    """With stream=, zeros and copies made by the call are that stream's: work
+    that is late on the current stream does not undo the result."""
+    lib = cuda_lib
+    p = ref.make([2, 40], [70, 60], kv_heads=2, group=2, head_dim=64, block=16, seed=16)
+    d, q, rb = cuda(p), p.q.cuda(), p.rb.cuda()
+    had = torch.rand((2, 2, 96), device="cuda")
+    out, lse = attend(lib, p, d)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(50_000_000)  # about 25 ms on the current stream
+    args = (q, d[0], d[2], d[4], d[5], rb, p.max_rows, p.sm, lse)
+    a = lib.pmqa_cache_weigh(*args, mass_width=96, stream=side)
+    b = lib.pmqa_cache_weigh(*args, had, stream=side)
+    again = lib.pmqa_cache_attention(q, *d, rb, p.max_rows, p.sm, stream=side)
+    torch.cuda.synchronize()
+    for got, start in ((a, torch.zeros_like(had)), (b, had)):
+        want, tol = ref.weigh(p, lse.cpu(), start.cpu())
+        check(got.cpu(), torch.where(torch.isnan(want), start.cpu().double(), want), tol)
+    assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows", [1, 12, 40])
+@pytest.mark.parametrize("power", [122, -112])
+def test_queries_at_the_ends_of_the_range(cuda_lib, rows, D, power):
+    """q of 2^122 (up to 2^125) or 2^-112 under a score scale that undoes it; a power
+    of two in q is exact, so the tolerances are those of ordinary values."""
+    p = ref.make([rows, 1], [rows + 90, 33], kv_heads=2, group=2, head_dim=D, block=16, seed=17)
+    p.q = (p.q.float() * 2.0 ** power).to(torch.bfloat16)
+    p.sm *= 2.0 ** -power
+    out, lse = attend(cuda_lib, p)
+    matches(p, out, lse)
+    d = cuda(p)
+    width = p.bt.shape[1] * 16
+    mass = cuda_lib.pmqa_cache_weigh(p.q.cuda(), d[0], d[2], d[4], d[5], p.rb.cuda(), p.max_rows,
+                                     p.sm, lse)
+    want, tol = ref.weigh(p, lse.cpu(), torch.zeros((2, 2, width)))
+    check(mass.cpu(), want.nan_to_num(0.0), tol)
+
+
 def test_the_same_call_gives_the_same_bits(cuda_lib):
     p = ref.make([1, 4, 90], [3000, 900, 700], kv_heads=2, group=4, head_dim=128, block=32, seed=16)
     d = cuda(p)
