@@ -153,7 +153,7 @@ extern "C" int pmqa_cache_attention(const pmqa_cache_problem *p, const void *q, 
     if (most > kShortRows)
         e = launch_attn_prompt(a, kShortRows + 1, cuda(stream));
     if (e == cudaSuccess && heads / p->kv_heads <= kShortRows)
-        e = launch_attn_rows(a, 1, kShortRows, sms, cuda(stream));
+        e = launch_attn_rows(a, 1, kShortRows, sms, most > kShortRows, cuda(stream));
     return code_of(e);
 }
 
@@ -183,7 +183,7 @@ extern "C" int pmqa_cache_weigh(const pmqa_cache_problem *p, const void *q, int3
     if (most > kShortRows)
         e = launch_weigh_window(a, kShortRows + 1, sms, cuda(stream));
     if (e == cudaSuccess)
-        e = launch_weigh_rows(a, 0, kShortRows, sms, cuda(stream));
+        e = launch_weigh_rows(a, 0, kShortRows, sms, most > kShortRows, cuda(stream));
     return code_of(e);
 }
 

@@ -115,6 +115,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
     if (rg.x0 >= rg.x1) {
         if (tid == 0)
             a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+        griddep_wait();
         return;
     }
     long long x = rg.x0;
@@ -128,6 +129,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
     if (x >= rg.x1) {
         if (tid == 0)
             a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+        griddep_wait();
         return;
     }
     const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * S) * St::kBytes;
@@ -559,6 +561,8 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
     cp_async_wait_all();
     if (tid == 0)
         a.meta[blockIdx.x] = open;
+    // behind the many-row kernel this one starts early; it ends after it
+    griddep_wait();
 }
 
 // Joins the parts of the contexts that the first kernel cut: block (c, y) takes
@@ -635,7 +639,7 @@ __global__ void __launch_bounds__(D) cache_attn_join_kernel(const __grid_constan
 }
 
 template <int D, int NT>
-static cudaError_t launch_rows(AttnArgs &a, uint8_t *ws, int sms, cudaStream_t st)
+static cudaError_t launch_rows(AttnArgs &a, uint8_t *ws, int sms, bool early, cudaStream_t st)
 {
     using Sh = AttnShape<D, NT>;
     const int grid = std::min(sms * Sh::kOcc, kMaxCtas);
@@ -646,26 +650,15 @@ static cudaError_t launch_rows(AttnArgs &a, uint8_t *ws, int sms, cudaStream_t s
     cudaError_t e = allow_smem(cache_attn_kernel<D, NT>, (int)Sh::kSmem, done);
     if (e != cudaSuccess)
         return e;
-    cache_attn_kernel<D, NT><<<grid, kAttnThreads, Sh::kSmem, st>>>(a);
-    e = cudaGetLastError();
-    if (e != cudaSuccess)
+    e = launch_early(cache_attn_kernel<D, NT>, dim3((unsigned)grid), kAttnThreads, Sh::kSmem, early, st, a);
+    if (e != cudaSuccess || a.whole)
         return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.stream = st;
-    cfg.gridDim = dim3((unsigned)grid, 2 * NT);
-    cfg.blockDim = dim3(D);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (a.whole)
-        return cudaSuccess;
-    return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<D, NT>, a);
+    return launch_early(cache_attn_join_kernel<D, NT>, dim3((unsigned)grid, 2 * NT), D, 0, true, st, a);
 }
 
-// Requests with least <= rows * group <= most.
-cudaError_t launch_attn_rows(AttnCall &q, int least, int most, int sms, cudaStream_t st)
+// Requests with least <= rows * group <= most. early: the kernel before this one
+// in the stream is the many-row kernel of the same call.
+cudaError_t launch_attn_rows(AttnCall &q, int least, int most, int sms, bool early, cudaStream_t st)
 {
     AttnArgs a{};
     a.c = q.c;
@@ -688,12 +681,12 @@ cudaError_t launch_attn_rows(AttnCall &q, int least, int most, int sms, cudaStre
     const long long need = (long long)q.c.max_rows * a.group;
     const int rows = need <= 32 ? (int)need : a.group;
     if (q.c.D == 128)
-        return rows <= 8 ? launch_rows<128, 1>(a, q.ws, sms, st)
-               : rows <= 16 ? launch_rows<128, 2>(a, q.ws, sms, st)
-                            : launch_rows<128, 4>(a, q.ws, sms, st);
-    return rows <= 8 ? launch_rows<64, 1>(a, q.ws, sms, st)
-           : rows <= 16 ? launch_rows<64, 2>(a, q.ws, sms, st)
-                        : launch_rows<64, 4>(a, q.ws, sms, st);
+        return rows <= 8 ? launch_rows<128, 1>(a, q.ws, sms, early, st)
+               : rows <= 16 ? launch_rows<128, 2>(a, q.ws, sms, early, st)
+                            : launch_rows<128, 4>(a, q.ws, sms, early, st);
+    return rows <= 8 ? launch_rows<64, 1>(a, q.ws, sms, early, st)
+           : rows <= 16 ? launch_rows<64, 2>(a, q.ws, sms, early, st)
+                        : launch_rows<64, 4>(a, q.ws, sms, early, st);
 }
 
 }  // namespace cache

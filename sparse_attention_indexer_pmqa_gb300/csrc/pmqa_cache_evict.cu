@@ -73,7 +73,7 @@ __device__ __forceinline__ void count_key(uint32_t *hist, uint32_t bin, bool in,
         atomicAdd(&hist[bin], 1u);
 }
 
-__global__ void __launch_bounds__(kSelThr) cache_evict_select_kernel(const __grid_constant__ EvictArgs a)
+__global__ void __launch_bounds__(kSelThr, 1) cache_evict_select_kernel(const __grid_constant__ EvictArgs a)
 {
     extern __shared__ uint32_t keys[];
     __shared__ uint32_t hist[2][kBins];
@@ -397,19 +397,11 @@ static cudaError_t launch_move(const EvictArgs &a, long long pairs, cudaStream_t
     const long long grid = one ? (units + 3) / 4 : units;
     if (grid > 0x7FFFFFFFll)
         return cudaErrorInvalidConfiguration;
-    cudaLaunchConfig_t cfg = {};
-    cfg.stream = st;
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kMoveThreads);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    const dim3 g((unsigned)grid);
     if (one)
-        return cudaLaunchKernelEx(&cfg, cache_evict_move_kernel<D, 1, 4>, a);
-    return P <= 16 * pass ? cudaLaunchKernelEx(&cfg, cache_evict_move_kernel<D, 4, 4>, a)
-                          : cudaLaunchKernelEx(&cfg, cache_evict_move_kernel<D, 4, 8>, a);
+        return launch_early(cache_evict_move_kernel<D, 1, 4>, g, kMoveThreads, 0, true, st, a);
+    return P <= 16 * pass ? launch_early(cache_evict_move_kernel<D, 4, 4>, g, kMoveThreads, 0, true, st, a)
+                          : launch_early(cache_evict_move_kernel<D, 4, 8>, g, kMoveThreads, 0, true, st, a);
 }
 
 cudaError_t launch_evict(const EvictCall &q, int sms, cudaStream_t st)

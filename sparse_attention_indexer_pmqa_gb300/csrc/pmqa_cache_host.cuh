@@ -28,6 +28,26 @@ inline cudaError_t allow_smem(K *kernel, int bytes, std::atomic<uint64_t> &done)
     return e;
 }
 
+// A launch that, where `early`, may start once every CTA of the kernel before it
+// has started: it waits for that kernel (griddep_wait) before it needs what it
+// wrote, and in any case before it ends.
+template <typename A>
+inline cudaError_t launch_early(void (*kernel)(A), dim3 grid, int threads, size_t smem, bool early,
+                                cudaStream_t st, const A &a)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = st;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = early ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
 constexpr int kShortRows = 32;  // packed rows (rows * group) of the short-row kernels
 
 struct AttnCall {
@@ -64,9 +84,9 @@ struct EvictCall {
 };
 
 cudaError_t launch_append(const View &c, const void *k, const void *v, cudaStream_t st);
-cudaError_t launch_attn_rows(AttnCall &q, int least, int most, int sms, cudaStream_t st);
+cudaError_t launch_attn_rows(AttnCall &q, int least, int most, int sms, bool early, cudaStream_t st);
 cudaError_t launch_attn_prompt(AttnCall &q, int least, cudaStream_t st);
-cudaError_t launch_weigh_rows(const WeighCall &q, int least, int most, int sms, cudaStream_t st);
+cudaError_t launch_weigh_rows(const WeighCall &q, int least, int most, int sms, bool early, cudaStream_t st);
 cudaError_t launch_weigh_window(const WeighCall &q, int least, int sms, cudaStream_t st);
 cudaError_t launch_evict(const EvictCall &q, int sms, cudaStream_t st);
 

@@ -245,6 +245,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
     const int warp = __shfl_sync(kFull, tid >> 5, 0);
     const View &c = a.c;
     const int G = a.group;
+    griddep_launch_dependents();  // the few-row kernel fills the SMs that run out of rows
 
     // ------------------------------------------------------------ which rows
     // slots run from the last to the first: a request's last rows see the most tokens

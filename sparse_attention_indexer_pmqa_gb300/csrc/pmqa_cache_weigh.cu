@@ -63,8 +63,10 @@ __global__ void __launch_bounds__(kWeighThreads, 3)
     Range rg;
     Walk w;
     find_range<kWeighTile, 0, kWeighThreads>(c, G, a.least, a.most, 1, 0.0f, rg, w);
-    if (rg.x0 >= rg.x1)
+    if (rg.x0 >= rg.x1) {
+        griddep_wait();
         return;
+    }
     const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * S) * St::kBytes;
 
     Walk pw = w;
@@ -272,22 +274,23 @@ __global__ void __launch_bounds__(kWeighThreads, 3)
         }
     }
     cp_async_wait_all();
+    griddep_wait();  // this kernel may start before the many-row one is done; it ends after it
 }
 
 template <int D, int NT>
-static cudaError_t launch(const WeighArgs &a, int sms, cudaStream_t st)
+static cudaError_t launch(const WeighArgs &a, int sms, bool early, cudaStream_t st)
 {
     const int smem = (int)(kWeighWarps * kWeighStages * WeighStage<D>::kBytes);
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(cache_weigh_kernel<D, NT>, smem, done);
     if (e != cudaSuccess)
         return e;
-    cache_weigh_kernel<D, NT><<<sms * 3, kWeighThreads, smem, st>>>(a);
-    return cudaGetLastError();
+    return launch_early(cache_weigh_kernel<D, NT>, dim3(3u * (unsigned)sms), kWeighThreads, smem, early, st, a);
 }
 
-// Requests with least <= rows * group <= most.
-cudaError_t launch_weigh_rows(const WeighCall &q, int least, int most, int sms, cudaStream_t st)
+// Requests with least <= rows * group <= most. early: the kernel before this one
+// in the stream is the many-row kernel of the same call.
+cudaError_t launch_weigh_rows(const WeighCall &q, int least, int most, int sms, bool early, cudaStream_t st)
 {
     WeighArgs a{};
     a.c = q.c;
@@ -303,12 +306,12 @@ cudaError_t launch_weigh_rows(const WeighCall &q, int least, int most, int sms, 
     a.most = most;
     const long long need = std::min<long long>((long long)q.c.max_rows * a.group, most);
     if (q.c.D == 128)
-        return need <= 8 ? launch<128, 1>(a, sms, st)
-               : need <= 16 ? launch<128, 2>(a, sms, st)
-                            : launch<128, 4>(a, sms, st);
-    return need <= 8 ? launch<64, 1>(a, sms, st)
-           : need <= 16 ? launch<64, 2>(a, sms, st)
-                        : launch<64, 4>(a, sms, st);
+        return need <= 8 ? launch<128, 1>(a, sms, early, st)
+               : need <= 16 ? launch<128, 2>(a, sms, early, st)
+                            : launch<128, 4>(a, sms, early, st);
+    return need <= 8 ? launch<64, 1>(a, sms, early, st)
+           : need <= 16 ? launch<64, 2>(a, sms, early, st)
+                        : launch<64, 4>(a, sms, early, st);
 }
 
 }  // namespace cache

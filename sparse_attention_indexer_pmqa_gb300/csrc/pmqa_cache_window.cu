@@ -80,6 +80,7 @@ __global__ void __launch_bounds__(kWnThreads, 1) cache_window_kernel(const __gri
     uint64_t *const bar = reinterpret_cast<uint64_t *>(smem + kWnOffBar);
     uint32_t *const misc = reinterpret_cast<uint32_t *>(smem + kWnOffMisc);
     volatile int *const abort_flag = reinterpret_cast<volatile int *>(misc + 1);
+    griddep_launch_dependents();  // the few-row kernel fills the SMs that run out of tiles
     if (sbase & 1023u) {
         if (tid == 0)
             atomicOr(c.status, (uint32_t)PMQA_DEV_INTERNAL);
