@@ -139,13 +139,15 @@ __device__ __forceinline__ uint32_t f32x4_to_e4m3x4(float a, float b, float c, f
 // max(1, ceil(ctx_i / TILE)) and B_i = ceil(n_i * group / ROWS); a request with
 // fewer than `least` or more than `most` query rows (n_i * group) has none.
 // With ROWS = 0 the rows are not cut (B_i = 1) and T_i = ceil(ctx_i / TILE).
+// PAD more items without work follow each context's tiles: what loading its rows
+// and writing its result costs, so that CTAs with many short contexts get less.
 // CTA c of C takes the items [c N / C, (c + 1) N / C).
 struct Walk {
     int i, h, b, t;       // current item
     int T, B;             // tiles and row blocks of request i
     Request q;
 
-    template <int TILE, int ROWS>
+    template <int TILE, int ROWS, int PAD>
     __device__ __forceinline__ static long long items(const View &a, const Request &q, int group,
                                                       int least, int most, int &T, int &B)
     {
@@ -155,11 +157,11 @@ struct Walk {
             B = in ? (q.n * group + ROWS - 1) / ROWS : 0;
         else
             B = in ? 1 : 0;
-        return (long long)a.H * B * T;
+        return (long long)a.H * B * (T > 0 ? T + PAD : 0);
     }
 
     // Step to the next item; false past the last request.
-    template <int TILE, int ROWS>
+    template <int TILE, int ROWS, int PAD>
     __device__ __forceinline__ bool next(const View &a, int group, int least, int most)
     {
         if (++t < T)
@@ -173,7 +175,7 @@ struct Walk {
         h = 0;
         while (++i < a.bs) {
             q = load_request(a, i, false);
-            if (items<TILE, ROWS>(a, q, group, least, most, T, B) > 0)
+            if (items<TILE, ROWS, PAD>(a, q, group, least, most, T, B) > 0)
                 return true;
         }
         return false;
@@ -194,7 +196,7 @@ struct Range {
 // to join one more part of a (request, head, row block), in items (0: nothing).
 // With T items and k CTAs each such context takes T / k + k join_cost, least at
 // k = sqrt(T / join_cost): so many CTAs per context at most, on average.
-template <int TILE, int ROWS, int THREADS>
+template <int TILE, int ROWS, int PAD, int THREADS>
 __device__ __forceinline__ void find_range(const View &a, int group, int least, int most,
                                            int least_items, float join_cost, Range &out,
                                            Walk &w)
@@ -206,7 +208,7 @@ __device__ __forceinline__ void find_range(const View &a, int group, int least, 
     int T, B;
     for (int i = tid; i < a.bs; i += THREADS) {
         const Request q = load_request(a, i, blockIdx.x == 0);
-        sum += Walk::items<TILE, ROWS>(a, q, group, least, most, T, B);
+        sum += Walk::items<TILE, ROWS, PAD>(a, q, group, least, most, T, B);
         pairs += (long long)a.H * B;
     }
 #pragma unroll
@@ -238,7 +240,7 @@ __device__ __forceinline__ void find_range(const View &a, int group, int least, 
         long long n = 0;
         if (i < a.bs) {
             const Request q = load_request(a, i, false);
-            n = Walk::items<TILE, ROWS>(a, q, group, least, most, T, B);
+            n = Walk::items<TILE, ROWS, PAD>(a, q, group, least, most, T, B);
         }
         long long inc = n;
 #pragma unroll
@@ -277,10 +279,10 @@ __device__ __forceinline__ void find_range(const View &a, int group, int least, 
         out.before = s_range.before;
         w.i = out.i;
         w.q = load_request(a, w.i, false);
-        Walk::items<TILE, ROWS>(a, w.q, group, least, most, w.T, w.B);
+        Walk::items<TILE, ROWS, PAD>(a, w.q, group, least, most, w.T, w.B);
         long long y = x0 - out.before;
-        w.t = (int)(y % w.T);
-        y /= w.T;
+        w.t = (int)(y % (w.T + PAD));  // T and above: behind the tiles
+        y /= w.T + PAD;
         w.b = (int)(y % w.B);
         w.h = (int)(y / w.B);
     }

@@ -11,12 +11,13 @@
 // Bound by HBM: each token and kv head costs 2 D bytes and 4 D flops per query
 // row, so with R rows per kv head the arithmetic is 2 R flops a byte; at R <=
 // 32 that is far below the ridge. The layout follows from that:
-//   * the items (request, kv head, block of 8 NT rows, tile of 64 tokens) are
+//   * the items (request, kv head, block of 8 NT rows, tile of tokens) are
 //     flattened and split evenly over the CTAs, so contexts of any mix of
 //     lengths finish together; a context cut between CTAs leaves (O, m, l)
 //     parts in the workspace and the second kernel joins them;
-//   * every warp takes 16 of a tile's 64 tokens through its own ring of
-//     cp.async stages and never waits for another warp inside a context;
+//   * every warp takes 16 of a tile's 64 tokens (32 of 128 at D = 64: 55 us instead
+//     of 71 for 32 contexts of 8 k tokens) through its own ring of cp.async stages
+//     and never waits for another warp inside a context;
 //   * products run as S^T = K Q^T and O^T = V^T P^T, so the 16 rows of the
 //     m16n8k16 shape are tokens (then value columns) and the 8 columns are
 //     query rows: a group of 8 wastes nothing, the softmax weights of a thread
@@ -36,8 +37,6 @@ namespace cache {
 
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * kAttnWarps;
-constexpr int kWarpTokens = 16;
-constexpr int kAttnTile = kAttnWarps * kWarpTokens;
 constexpr float kSlack = 8.0f;    // p <= 2^8 before the maximum moves
 constexpr int kLeastTiles = 2;    // fewest tiles a CTA takes (small problems)
 // Joining one more part, in tiles: with it 60000 tokens of one kv head take 27 us,
@@ -65,8 +64,9 @@ struct AttnArgs {
 // all banks.
 template <int D>
 struct Stage {
-    static constexpr uint32_t kRows = kWarpTokens * D;
-    static constexpr uint32_t kOffKs = 2 * kRows, kOffVs = kOffKs + 64, kOffMask = kOffVs + 64;
+    static constexpr int kTok = D == 64 ? 32 : 16;
+    static constexpr uint32_t kRows = kTok * D;
+    static constexpr uint32_t kOffKs = 2 * kRows, kOffVs = kOffKs + 4 * kTok, kOffMask = kOffVs + 4 * kTok;
     static constexpr uint32_t kBytes = kOffMask + 16;
     __device__ static __forceinline__ uint32_t at(int r, int c)
     {
@@ -81,6 +81,10 @@ template <int D, int NT>
 struct AttnShape {
     static constexpr int kStages = 3;
     static constexpr int kRows = 8 * NT;
+    // What a context's start and end cost, in tiles: 16 requests of 1 to 4096 tokens
+    // and 8 kv heads take 23 us with it, 31 without. (It costs the kernel of 32 rows
+    // registers: 197 us instead of 187 for 32 requests of 32 k tokens and 2 heads.)
+    static constexpr int kPad = NT == 4 ? 0 : 2;
     static constexpr int kPitch = D + 4;  // floats per row of the merge buffer
     static constexpr uint32_t kRing = kAttnWarps * kStages * Stage<D>::kBytes;
     static constexpr uint32_t kOffMerge = kRing;
@@ -103,6 +107,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
     constexpr int ROWS = Sh::kRows;
     constexpr int KS = D / 16;   // k steps of the first product
     constexpr int MT = D / 16;   // 16-column tiles of the second
+    constexpr int TOK = St::kTok, U = TOK / 16, TILE = kAttnWarps * TOK;
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const View &c = a.c;
@@ -111,7 +116,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
 
     Range rg;
     Walk w;
-    find_range<kAttnTile, ROWS, kAttnThreads>(c, G, a.least, a.most, kLeastTiles, NT == 4 ? 0.0f : kJoinCost, rg, w);
+    find_range<TILE, ROWS, Sh::kPad, kAttnThreads>(c, G, a.least, a.most, kLeastTiles, NT == 4 ? 0.0f : kJoinCost, rg, w);
     if (rg.x0 >= rg.x1) {
         if (tid == 0)
             a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
@@ -119,12 +124,13 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
         return;
     }
     long long x = rg.x0;
-    if (a.whole && w.t > 0) {
-        // uncut: a context belongs to the CTA whose range holds its first tile
-        x += w.T - w.t;
+    if (w.t >= w.T || (a.whole && w.t > 0)) {
+        // the range starts behind a context's tiles; or (uncut) a context belongs to
+        // the CTA whose range holds its first tile
+        x += w.T + Sh::kPad - w.t;
         w.t = w.T - 1;
         if (x < rg.x1)
-            w.template next<kAttnTile, ROWS>(c, G, a.least, a.most);
+            w.template next<TILE, ROWS, Sh::kPad>(c, G, a.least, a.most);
     }
     if (x >= rg.x1) {
         if (tid == 0)
@@ -154,7 +160,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
     auto look_up = [&]() {
         pend_in = false;
         if (p_more) {
-            const int tok = pw.t * kAttnTile + warp * kWarpTokens + (lane & 15);
+            const int tok = pw.t * TILE + warp * TOK + (lane & (TOK - 1));
             pend_in = tok < p_end;
             const int pg = c.page_of(tok);
             pend_off = tok - pg * c.P;
@@ -166,9 +172,10 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
                 ++pw.t;
                 p_more = p_x < rg.x1 || a.whole;
             } else {
+                p_x += Sh::kPad;
                 p_more = p_x < rg.x1;
                 if (p_more) {
-                    pw.template next<kAttnTile, ROWS>(c, G, a.least, a.most);
+                    pw.template next<TILE, ROWS, Sh::kPad>(c, G, a.least, a.most);
                     p_end = seen_end(pw.q, pw.b);
                 }
             }
@@ -176,7 +183,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
     };
     constexpr int CH = D / 16, PER = 32 / CH;  // chunks a row, rows an instruction
     const int ch = lane % CH;
-    const bool one_block = (c.P & (kWarpTokens - 1)) == 0;  // 16 tokens never leave a block
+    const bool one_block = (c.P & 15) == 0;  // 16 tokens never leave a block
     int p_slot = 0;
     auto issue = [&]() {
         const uint32_t st = ring + (uint32_t)p_slot * St::kBytes;
@@ -187,32 +194,40 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
             atomicOr(c.status, (uint32_t)PMQA_DEV_BAD_BLOCK_ID);
             ok = false;
         }
-        const uint32_t mask = __ballot_sync(kFull, ok) & 0xFFFFu;
+        const uint32_t mask = __ballot_sync(kFull, ok) & (kFull >> (32 - TOK));
         if (lane == 0)
             asm volatile("st.shared.b32 [%0], %1;" ::"r"(st + St::kOffMask), "r"(mask) : "memory");
         if (mask) {
             // block * H + head, and the row of the pool (both below 2^32)
             const uint32_t phys = ok ? (uint32_t)pend_page * (uint32_t)c.H + (uint32_t)pend_h : 0u;
             const uint32_t row = phys * (uint32_t)c.P + (uint32_t)pend_off;
-            const uint32_t sdst = st + (lane < 16 ? St::kOffKs : St::kOffVs) + (uint32_t)(lane & 15) * 4u;
-            if (ok)
-                cp_async_4(sdst, (lane < 16 ? c.ks : c.vs) + phys);
-            else
-                asm volatile("st.shared.b32 [%0], %1;" ::"r"(sdst), "r"(0) : "memory");
-            if (one_block) {
-                // token 0 exists (a block's tokens exist up to some one): 16 rows on end
-                const uint64_t src = (uint64_t)__shfl_sync(kFull, row, 0) * D + (uint32_t)lane * 16u;
-                const uint8_t *const ks = c.k + src, *const vs = c.v + src;
 #pragma unroll
-                for (int k = 0; k < kWarpTokens / PER; ++k) {
-                    const int r = k * PER + lane / CH;
-                    const uint32_t nb = (mask >> r) & 1u ? 16u : 0u;
-                    cp_async_16(st + St::at(r, ch), ks + k * 512, nb);
-                    cp_async_16(st + St::kRows + St::at(r, ch), vs + k * 512, nb);
+            for (int pool = 0; pool < U; ++pool) {  // 16 tokens: the lower lanes K, the upper ones V
+                const bool is_k = U == 1 ? lane < 16 : pool == 0;
+                const uint32_t sdst =
+                    st + (is_k ? St::kOffKs : St::kOffVs) + (uint32_t)(lane & (TOK - 1)) * 4u;
+                if (ok)
+                    cp_async_4(sdst, (is_k ? c.ks : c.vs) + phys);
+                else
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(sdst), "r"(0) : "memory");
+            }
+            if (one_block) {
+                // of 16 tokens the first exists if any does: rows on end from its own
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const uint64_t src = (uint64_t)__shfl_sync(kFull, row, 16 * u) * D + (uint32_t)lane * 16u;
+                    const uint8_t *const ks = c.k + src, *const vs = c.v + src;
+#pragma unroll
+                    for (int k = 0; k < 16 / PER; ++k) {
+                        const int r = 16 * u + k * PER + lane / CH;
+                        const uint32_t nb = (mask >> r) & 1u ? 16u : 0u;
+                        cp_async_16(st + St::at(r, ch), ks + k * 512, nb);
+                        cp_async_16(st + St::kRows + St::at(r, ch), vs + k * 512, nb);
+                    }
                 }
             } else {
 #pragma unroll
-                for (int k = 0; k < kWarpTokens / PER; ++k) {
+                for (int k = 0; k < TOK / PER; ++k) {
                     const int r = k * PER + lane / CH;
                     const uint32_t nb = (mask >> r) & 1u ? 16u : 0u;
                     const uint32_t rr = __shfl_sync(kFull, row, r);
@@ -317,69 +332,90 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
         const uint32_t st = ring + (uint32_t)c_slot * St::kBytes;
         if (++c_slot == S)
             c_slot = 0;
-        const int base = w.t * kAttnTile + warp * kWarpTokens;
+        const int base = w.t * TILE + warp * TOK;
         const uint32_t mask = base < end ? lds32(st + St::kOffMask) : 0u;
         if (mask) {
-            float s[NT][4];
+            float s[U][NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    s[nt][e] = 0.0f;
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int half = 0; half < D / 64; ++half) {
-                const uint4 ka = lds128(st + St::at(g, half * 4 + t4));
-                const uint4 kb = lds128(st + St::at(g + 8, half * 4 + t4));
-                const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+                    for (int e = 0; e < 4; ++e)
+                        s[u][nt][e] = 0.0f;
 #pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    uint32_t a0, a1, a2, a3;
-                    e4m3x4_to_f16x2(wa[z], a0, a2);
-                    e4m3x4_to_f16x2(wb[z], a1, a3);
+            for (int half = 0; half < D / 64; ++half)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        if constexpr (Sh::kQShared) {
-                            const uint2 b = qsm[(nt * KS + half * 4 + z) * 32];
-                            mma_f16(s[nt], a0, a1, a2, a3, b.x, b.y);
-                        } else {
-                            mma_f16(s[nt], a0, a1, a2, a3, qb[nt][half * 4 + z][0], qb[nt][half * 4 + z][1]);
+                for (int u = 0; u < U; ++u) {
+                    const uint4 ka = lds128(st + St::at(16 * u + g, half * 4 + t4));
+                    const uint4 kb = lds128(st + St::at(16 * u + g + 8, half * 4 + t4));
+                    const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        uint32_t a0, a1, a2, a3;
+                        e4m3x4_to_f16x2(wa[z], a0, a2);
+                        e4m3x4_to_f16x2(wb[z], a1, a3);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            if constexpr (Sh::kQShared) {
+                                const uint2 b = qsm[(nt * KS + half * 4 + z) * 32];
+                                mma_f16(s[u][nt], a0, a1, a2, a3, b.x, b.y);
+                            } else {
+                                mma_f16(s[u][nt], a0, a1, a2, a3, qb[nt][half * 4 + z][0], qb[nt][half * 4 + z][1]);
+                            }
                         }
                     }
                 }
-            }
-            const float ks0 = __uint_as_float(lds32(st + St::kOffKs + 4u * g));
-            const float ks1 = __uint_as_float(lds32(st + St::kOffKs + 4u * g + 32u));
-            const float vs0 = __uint_as_float(lds32(st + St::kOffVs + 4u * g));
-            const float vs1 = __uint_as_float(lds32(st + St::kOffVs + 4u * g + 32u));
+            // scales of tokens 16 u + g and 16 u + g + 8
+            float ks[U][2], vs[U][2], vmax = 0.0f;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const uint32_t at = st + 4u * (uint32_t)(16 * u + 8 * y + g);
+                    ks[u][y] = __uint_as_float(lds32(at + St::kOffKs));
+                    vs[u][y] = __uint_as_float(lds32(at + St::kOffVs));
+                    vmax = fmaxf(vmax, fabsf(vs[u][y]));
+                }
             // every row sees every token of the chunk (no mask to apply)
-            const bool whole = mask == 0xFFFFu && base + 15 <= w.q.ctx - w.q.n;
+            const bool whole = mask == kFull >> (32 - TOK) && base + TOK - 1 <= w.q.ctx - w.q.n;
             bool exceed = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                s[nt][0] *= ks0 * rc[nt][0];
-                s[nt][1] *= ks0 * rc[nt][1];
-                s[nt][2] *= ks1 * rc[nt][0];
-                s[nt][3] *= ks1 * rc[nt][1];
-                if (!whole) {
-                    const bool k0 = (mask >> g) & 1u, k1 = (mask >> (g + 8)) & 1u;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        if (!k0 || base + g > lim[nt][e])
-                            s[nt][e] = -INFINITY;
-                        if (!k1 || base + g + 8 > lim[nt][e])
-                            s[nt][2 + e] = -INFINITY;
+                for (int u = 0; u < U; ++u) {
+                    s[u][nt][0] *= ks[u][0] * rc[nt][0];
+                    s[u][nt][1] *= ks[u][0] * rc[nt][1];
+                    s[u][nt][2] *= ks[u][1] * rc[nt][0];
+                    s[u][nt][3] *= ks[u][1] * rc[nt][1];
+                    if (!whole) {
+                        const int r = 16 * u + g;
+                        const bool k0 = (mask >> r) & 1u, k1 = (mask >> (r + 8)) & 1u;
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            if (!k0 || base + r > lim[nt][e])
+                                s[u][nt][e] = -INFINITY;
+                            if (!k1 || base + r + 8 > lim[nt][e])
+                                s[u][nt][2 + e] = -INFINITY;
+                        }
                     }
                 }
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    exceed |= fmaxf(s[nt][e], s[nt][2 + e]) > m[nt][e] + kSlack;
+                for (int e = 0; e < 2; ++e) {
+                    float top = fmaxf(s[0][nt][e], s[0][nt][2 + e]);
+                    if constexpr (U == 2)
+                        top = fmaxf(top, fmaxf(s[U - 1][nt][e], s[U - 1][nt][2 + e]));
+                    exceed |= top > m[nt][e] + kSlack;
+                }
             }
             if (__any_sync(kFull, exceed)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float top = fmaxf(s[nt][e], s[nt][2 + e]);
+                        float top = fmaxf(s[0][nt][e], s[0][nt][2 + e]);
+                        if constexpr (U == 2)
+                            top = fmaxf(top, fmaxf(s[U - 1][nt][e], s[U - 1][nt][2 + e]));
                         top = fmaxf(top, __shfl_xor_sync(kFull, top, 4));
                         top = fmaxf(top, __shfl_xor_sync(kFull, top, 8));
                         top = fmaxf(top, __shfl_xor_sync(kFull, top, 16));
@@ -398,7 +434,6 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
             // O is held in units of vref; p takes the token's scale over vref.
             // vref moves when the chunk's largest scale leaves [2^-5, 2^5] vref
             // (not to scales under 2^-60 of the largest seen: blocks of zeros).
-            float vmax = fmaxf(fabsf(vs0), fabsf(vs1));
             if (__any_sync(kFull, vmax > 32.0f * vref) || __all_sync(kFull, 32.0f * vmax < vref)) {
                 vmax = fmaxf(vmax, __shfl_xor_sync(kFull, vmax, 4));
                 vmax = fmaxf(vmax, __shfl_xor_sync(kFull, vmax, 8));
@@ -417,48 +452,55 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
                                 acc[nt][j][e] *= f;
                 }
             }
-            const float rv0 = vs0 * vinv, rv1 = vs1 * vinv;
-            uint32_t pb[NT][2];
+            uint32_t pb[U][NT][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float m0 = m[nt][0] == -INFINITY ? 0.0f : m[nt][0];
-                const float m1 = m[nt][1] == -INFINITY ? 0.0f : m[nt][1];
-                const float p0 = ex2_approx(s[nt][0] - m0), p1 = ex2_approx(s[nt][1] - m1);
-                const float p2 = ex2_approx(s[nt][2] - m0), p3 = ex2_approx(s[nt][3] - m1);
-                l[nt][0] += p0 + p2;
-                l[nt][1] += p1 + p3;
-                pb[nt][0] = transpose8x8(pack_f16x2(p0 * rv0, p1 * rv0));
-                pb[nt][1] = transpose8x8(pack_f16x2(p2 * rv1, p3 * rv1));
+            for (int u = 0; u < U; ++u) {
+                const float rv0 = vs[u][0] * vinv, rv1 = vs[u][1] * vinv;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float m0 = m[nt][0] == -INFINITY ? 0.0f : m[nt][0];
+                    const float m1 = m[nt][1] == -INFINITY ? 0.0f : m[nt][1];
+                    const float p0 = ex2_approx(s[u][nt][0] - m0), p1 = ex2_approx(s[u][nt][1] - m1);
+                    const float p2 = ex2_approx(s[u][nt][2] - m0), p3 = ex2_approx(s[u][nt][3] - m1);
+                    l[nt][0] += p0 + p2;
+                    l[nt][1] += p1 + p3;
+                    pb[u][nt][0] = transpose8x8(pack_f16x2(p0 * rv0, p1 * rv0));
+                    pb[u][nt][1] = transpose8x8(pack_f16x2(p2 * rv1, p3 * rv1));
+                }
             }
             // value columns: D = 128, thread g holds dims 16 g .. 16 g + 15; D = 64, 8 g .. 8 g + 7
             constexpr int VW = D / 32;  // 32-bit words per token and thread
-            uint32_t v[4][VW];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int r = 2 * t4 + (k & 1) + (k >> 1) * 8;
-                if constexpr (D == 128) {
-                    const uint4 u = lds128(st + St::kRows + St::at(r, g));
-                    v[k][0] = u.x;
-                    v[k][1] = u.y;
-                    v[k][2] = u.z;
-                    v[k][3] = u.w;
-                } else {
-                    const uint32_t ad = st + St::kRows + St::at(r, g >> 1) + (uint32_t)(g & 1) * 8u;
-                    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[k][0]), "=r"(v[k][1]) : "r"(ad));
+            for (int u = 0; u < U; ++u) {
+                uint32_t v[4][VW];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int r = 16 * u + 2 * t4 + (k & 1) + (k >> 1) * 8;
+                    if constexpr (D == 128) {
+                        const uint4 y = lds128(st + St::kRows + St::at(r, g));
+                        v[k][0] = y.x;
+                        v[k][1] = y.y;
+                        v[k][2] = y.z;
+                        v[k][3] = y.w;
+                    } else {
+                        const uint32_t ad = st + St::kRows + St::at(r, g >> 1) + (uint32_t)(g & 1) * 8u;
+                        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[k][0]), "=r"(v[k][1]) : "r"(ad));
+                    }
                 }
-            }
 #pragma unroll
-            for (int z = 0; z < VW; ++z) {
-                uint32_t f[2][2], h[2][2];
-                e4m3x4_to_f16x2(__byte_perm(v[0][z], v[1][z], 0x5140), f[0][0], f[0][1]);
-                e4m3x4_to_f16x2(__byte_perm(v[2][z], v[3][z], 0x5140), h[0][0], h[0][1]);
-                e4m3x4_to_f16x2(__byte_perm(v[0][z], v[1][z], 0x7362), f[1][0], f[1][1]);
-                e4m3x4_to_f16x2(__byte_perm(v[2][z], v[3][z], 0x7362), h[1][0], h[1][1]);
+                for (int z = 0; z < VW; ++z) {
+                    uint32_t f[2][2], h[2][2];
+                    e4m3x4_to_f16x2(__byte_perm(v[0][z], v[1][z], 0x5140), f[0][0], f[0][1]);
+                    e4m3x4_to_f16x2(__byte_perm(v[2][z], v[3][z], 0x5140), h[0][0], h[0][1]);
+                    e4m3x4_to_f16x2(__byte_perm(v[0][z], v[1][z], 0x7362), f[1][0], f[1][1]);
+                    e4m3x4_to_f16x2(__byte_perm(v[2][z], v[3][z], 0x7362), h[1][0], h[1][1]);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int y = 0; y < 2; ++y)
-                        mma_f16(acc[nt][2 * z + y], f[y][0], f[y][1], h[y][0], h[y][1], pb[nt][0], pb[nt][1]);
+                        for (int y = 0; y < 2; ++y)
+                            mma_f16(acc[nt][2 * z + y], f[y][0], f[y][1], h[y][0], h[y][1], pb[u][nt][0],
+                                    pb[u][nt][1]);
+                }
             }
         }
         ++x;
@@ -553,10 +595,11 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
             const int cta = (int)(((last + 1) * rg.C - 1) / rg.total);
             open = make_int4(w.i, w.h, w.b, 2 * (cta - (int)blockIdx.x + 1) + (slot & 1));
         }
+        x += Sh::kPad;
         if (x >= rg.x1)
             break;
         fresh = true;
-        w.template next<kAttnTile, ROWS>(c, G, a.least, a.most);
+        w.template next<TILE, ROWS, Sh::kPad>(c, G, a.least, a.most);
     }
     cp_async_wait_all();
     if (tid == 0)

@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(kWeighThreads, 3)
     const int G = a.group;
     Range rg;
     Walk w;
-    find_range<kWeighTile, 0, kWeighThreads>(c, G, a.least, a.most, 1, 0.0f, rg, w);
+    find_range<kWeighTile, 0, 0, kWeighThreads>(c, G, a.least, a.most, 1, 0.0f, rg, w);
     if (rg.x0 >= rg.x1) {
         griddep_wait();
         return;
@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kWeighThreads, 3)
                 if (pw.t + 1 < pw.T)
                     ++pw.t;
                 else
-                    pw.template next<kWeighTile, 0>(c, G, a.least, a.most);
+                    pw.template next<kWeighTile, 0, 0>(c, G, a.least, a.most);
             }
         }
     };
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kWeighThreads, 3)
         if (w.t + 1 < w.T) {
             ++w.t;
         } else if (x < rg.x1) {
-            w.template next<kWeighTile, 0>(c, G, a.least, a.most);
+            w.template next<kWeighTile, 0, 0>(c, G, a.least, a.most);
             fresh = true;
         }
     }
