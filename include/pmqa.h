@@ -411,7 +411,7 @@ typedef struct pmqa_cache_problem {
     int64_t num_blocks;
 } pmqa_cache_problem;
 
-/* About 17 MB, whatever the problem. */
+/* About 32 MB, whatever the problem. */
 size_t pmqa_cache_workspace_bytes(void);
 
 /*
@@ -445,7 +445,7 @@ int pmqa_cache_append(const pmqa_cache_problem *p, const void *k, const void *v,
  * Requests of more than 32 rows n_i * heads / kv_heads hold their values in units
  * of the largest block scale met so far, to 2^-31 of it at worst.
  * One kernel launch where block_size * max_blocks_per_seq <= 640, else two, and
- * one more where max_rows * heads / kv_heads > 32 (that one alone where
+ * one or two more where max_rows * heads / kv_heads > 32 (those alone where
  * heads / kv_heads > 32).
  * Every sum is formed in one order: equal calls give equal bits.
  */

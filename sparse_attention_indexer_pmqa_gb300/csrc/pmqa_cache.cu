@@ -1,6 +1,7 @@
 // pmqa_cache.cu -- C ABI of the operators on the paged 8-bit K/V cache
 // (include/pmqa.h): argument checks, the device view of a problem, the choice
 // of kernels. No allocation, no synchronisation, no state between calls.
+#include <algorithm>
 #include <cmath>
 
 #include "pmqa_cache_host.cuh"
@@ -9,9 +10,6 @@ using namespace pmqa;
 using namespace pmqa::cache;
 
 namespace {
-
-// status | open contexts, one per CTA | (m, l) and O of two parts per CTA, 32 rows of 128
-constexpr size_t kWorkspace = kStatusBytes + kMaxCtas * 16 + (size_t)2 * kMaxCtas * 32 * (2 + 128) * 4;
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -150,10 +148,16 @@ extern "C" int pmqa_cache_attention(const pmqa_cache_problem *p, const void *q, 
     // GPU; longer ones keep the tensor cores busy with their rows
     const long long most = (long long)p->max_rows * (heads / p->kv_heads);
     cudaError_t e = cudaSuccess;
+    // fewer row blocks than SMs: their contexts are cut too
+    const int ctas = std::min(sms, kMaxParts);
+    const long long blocks = (long long)p->rows * (heads / p->kv_heads) / kPromptRows * p->kv_heads;
+    const int parts = most > kShortRows && blocks < ctas ? ctas : 0;
     if (most > kShortRows)
-        e = launch_attn_prompt(a, kShortRows + 1, cuda(stream));
+        e = launch_attn_prompt(a, kShortRows + 1, parts, cuda(stream));
     if (e == cudaSuccess && heads / p->kv_heads <= kShortRows)
         e = launch_attn_rows(a, 1, kShortRows, sms, most > kShortRows, cuda(stream));
+    if (e == cudaSuccess && parts > 0)
+        e = launch_attn_join(a, parts, cuda(stream));
     return code_of(e);
 }
 

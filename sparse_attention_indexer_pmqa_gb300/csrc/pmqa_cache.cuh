@@ -23,6 +23,9 @@ constexpr int kMaxGroup = 128;       // query heads per kv head
 constexpr int kMaxBlock = 1024;      // tokens per block
 constexpr int kMaxContext = 0x7FFF0000;  // slots rounded up to tiles stay in 32 bits
 constexpr int kMaxCtas = 512;        // CTAs of the short-row attention (workspace parts: 2 each)
+constexpr int kMaxWide = 320;        // the same with 32 rows a block (8 and 16: kMaxCtas)
+constexpr int kPromptRows = 256;     // packed rows per CTA of the many-row attention
+constexpr int kMaxParts = 160;       // its CTAs where contexts are cut (workspace parts: 1 each)
 constexpr size_t kStatusBytes = 256;
 
 // Device view of a pmqa_cache_problem.

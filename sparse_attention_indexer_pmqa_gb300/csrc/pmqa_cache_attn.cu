@@ -608,14 +608,13 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
     griddep_wait();
 }
 
-// Joins the parts of the contexts that the first kernel cut: block (c, y) takes
-// 4 rows of the context that CTA c began and left open. Each row's weights
-// 2^(m_k - M) are worked out once, then every thread adds its 4 columns over
-// the parts.
-template <int D, int NT>
+// Joins the parts of the contexts that a kernel cut: block (c, y) takes 4 rows at a
+// time of the context that CTA c began and left open. Each row's weights 2^(m_k - M)
+// are worked out once, then every thread adds its 4 columns over the parts. ROWS:
+// rows of a part; SLOTS: parts that a CTA may leave.
+template <int D, int ROWS, int SLOTS>
 __global__ void __launch_bounds__(D) cache_attn_join_kernel(const __grid_constant__ AttnArgs a)
 {
-    constexpr int ROWS = 8 * NT;
     __shared__ float s_w[4][kMaxCtas];
     __shared__ float s_M[4], s_L[4];
     griddep_wait();
@@ -625,70 +624,71 @@ __global__ void __launch_bounds__(D) cache_attn_join_kernel(const __grid_constan
         return;
     const int h = meta.y, b = meta.z;
     const Request q = load_request(a.c, meta.x, false);
-    const int R0 = b * ROWS + (int)blockIdx.y * 4;
-    if (R0 >= q.n * a.group)
-        return;
     // part k in the first slot of CTA c + k, part 0 where CTA c put it
-    auto slot_of = [&](int k) { return 2 * ((int)blockIdx.x + k) + (k == 0 ? meta.w & 1 : 0); };
+    auto slot_of = [&](int k) { return SLOTS * ((int)blockIdx.x + k) + (k == 0 ? meta.w & 1 : 0); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int r = warp; r < 4; r += D / 32) {
-        const int row = (int)blockIdx.y * 4 + r;
-        float M = -INFINITY;
-        for (int k = lane; k < parts; k += 32)
-            M = fmaxf(M, a.ml[((long long)slot_of(k) * ROWS + row) * 2]);
+    for (int y = (int)blockIdx.y * 4; y < ROWS && b * ROWS + y < q.n * a.group; y += 4 * (int)gridDim.y) {
+        for (int r = warp; r < 4; r += D / 32) {
+            const int row = y + r;
+            float M = -INFINITY;
+            for (int k = lane; k < parts; k += 32)
+                M = fmaxf(M, a.ml[((long long)slot_of(k) * ROWS + row) * 2]);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-        float L = 0.0f;
-        for (int k = lane; k < parts; k += 32) {
-            const float2 p = *reinterpret_cast<const float2 *>(a.ml + ((long long)slot_of(k) * ROWS + row) * 2);
-            const float f = p.x == -INFINITY ? (p.y == 0.0f ? 0.0f : 1.0f) : ex2_approx(p.x - M);
-            s_w[r][k] = f;
-            L += f * p.y;
-        }
+            for (int o = 16; o > 0; o >>= 1)
+                M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+            float L = 0.0f;
+            for (int k = lane; k < parts; k += 32) {
+                const float2 p = *reinterpret_cast<const float2 *>(a.ml + ((long long)slot_of(k) * ROWS + row) * 2);
+                const float f = p.x == -INFINITY ? (p.y == 0.0f ? 0.0f : 1.0f) : ex2_approx(p.x - M);
+                s_w[r][k] = f;
+                L += f * p.y;
+            }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            L += __shfl_xor_sync(kFull, L, o);
-        if (lane == 0) {
-            s_M[r] = M;
-            s_L[r] = L;
+            for (int o = 16; o > 0; o >>= 1)
+                L += __shfl_xor_sync(kFull, L, o);
+            if (lane == 0) {
+                s_M[r] = M;
+                s_L[r] = L;
+            }
         }
-    }
-    __syncthreads();
-    const int r = threadIdx.x / (D / 4), col = (threadIdx.x % (D / 4)) * 4;
-    const int row = (int)blockIdx.y * 4 + r, R = R0 + r;
-    if (R >= q.n * a.group)
-        return;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        __syncthreads();
+        const int r = threadIdx.x / (D / 4), col = (threadIdx.x % (D / 4)) * 4;
+        const int row = y + r, R = b * ROWS + row;
+        if (R < q.n * a.group) {
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-    for (int k = 0; k < parts; ++k) {
-        const float f = s_w[r][k];
-        const float4 u = *reinterpret_cast<const float4 *>(a.part + ((long long)slot_of(k) * ROWS + row) * D + col);
-        o.x += f * u.x;
-        o.y += f * u.y;
-        o.z += f * u.z;
-        o.w += f * u.w;
+            for (int k = 0; k < parts; ++k) {
+                const float f = s_w[r][k];
+                const float4 u =
+                    *reinterpret_cast<const float4 *>(a.part + ((long long)slot_of(k) * ROWS + row) * D + col);
+                o.x += f * u.x;
+                o.y += f * u.y;
+                o.z += f * u.z;
+                o.w += f * u.w;
+            }
+            const float M = s_M[r], L = s_L[r], inv = L == 0.0f ? 0.0f : 1.0f / L;
+            const long long rh = (long long)(q.r0 + R / a.group) * a.heads + h * a.group + R % a.group;
+            uint2 bb;
+            bb.x = __bfloat16_as_ushort(__float2bfloat16_rn(o.x * inv)) |
+                   (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(o.y * inv)) << 16;
+            bb.y = __bfloat16_as_ushort(__float2bfloat16_rn(o.z * inv)) |
+                   (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(o.w * inv)) << 16;
+            *reinterpret_cast<uint2 *>(a.out + rh * D + col) = bb;
+            if (a.lse && col == 0)
+                a.lse[rh] = L == 0.0f ? -INFINITY : (M == -INFINITY ? L : (M + log2f(L)) * kLn2);
+        }
+        __syncthreads();
     }
-    const float M = s_M[r], L = s_L[r], inv = L == 0.0f ? 0.0f : 1.0f / L;
-    const long long rh = (long long)(q.r0 + R / a.group) * a.heads + h * a.group + R % a.group;
-    uint2 bb;
-    bb.x = __bfloat16_as_ushort(__float2bfloat16_rn(o.x * inv)) |
-           (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(o.y * inv)) << 16;
-    bb.y = __bfloat16_as_ushort(__float2bfloat16_rn(o.z * inv)) |
-           (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(o.w * inv)) << 16;
-    *reinterpret_cast<uint2 *>(a.out + rh * D + col) = bb;
-    if (a.lse && col == 0)
-        a.lse[rh] = L == 0.0f ? -INFINITY : (M == -INFINITY ? L : (M + log2f(L)) * kLn2);
 }
 
 template <int D, int NT>
 static cudaError_t launch_rows(AttnArgs &a, uint8_t *ws, int sms, bool early, cudaStream_t st)
 {
     using Sh = AttnShape<D, NT>;
-    const int grid = std::min(sms * Sh::kOcc, kMaxCtas);
-    a.meta = reinterpret_cast<int4 *>(ws + kStatusBytes);
-    a.ml = reinterpret_cast<float *>(ws + kStatusBytes + kMaxCtas * sizeof(int4));
-    a.part = a.ml + (size_t)2 * kMaxCtas * 32 * 2;
+    const int grid = std::min(sms * Sh::kOcc, NT == 4 ? kMaxWide : kMaxCtas);
+    a.meta = reinterpret_cast<int4 *>(ws + kWsMeta);
+    a.ml = reinterpret_cast<float *>(ws + kWsMl);
+    a.part = reinterpret_cast<float *>(ws + kWsPart);
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(cache_attn_kernel<D, NT>, (int)Sh::kSmem, done);
     if (e != cudaSuccess)
@@ -696,12 +696,10 @@ static cudaError_t launch_rows(AttnArgs &a, uint8_t *ws, int sms, bool early, cu
     e = launch_early(cache_attn_kernel<D, NT>, dim3((unsigned)grid), kAttnThreads, Sh::kSmem, early, st, a);
     if (e != cudaSuccess || a.whole)
         return e;
-    return launch_early(cache_attn_join_kernel<D, NT>, dim3((unsigned)grid, 2 * NT), D, 0, true, st, a);
+    return launch_early(cache_attn_join_kernel<D, Sh::kRows, 2>, dim3((unsigned)grid, 2 * NT), D, 0, true, st, a);
 }
 
-// Requests with least <= rows * group <= most. early: the kernel before this one
-// in the stream is the many-row kernel of the same call.
-cudaError_t launch_attn_rows(AttnCall &q, int least, int most, int sms, bool early, cudaStream_t st)
+static AttnArgs arguments(const AttnCall &q)
 {
     AttnArgs a{};
     a.c = q.c;
@@ -711,6 +709,28 @@ cudaError_t launch_attn_rows(AttnCall &q, int least, int most, int sms, bool ear
     a.scale_log2 = q.sm_scale * kLog2e;
     a.heads = q.heads;
     a.group = q.heads / q.c.H;
+    return a;
+}
+
+// Joins what the many-row kernel cut (`parts` as in its launch). Every kernel
+// between the two ends after that one.
+cudaError_t launch_attn_join(AttnCall &q, int parts, cudaStream_t st)
+{
+    AttnArgs a = arguments(q);
+    a.meta = reinterpret_cast<int4 *>(q.ws + kWsPromptMeta);
+    a.ml = reinterpret_cast<float *>(q.ws + kWsPromptMl);
+    a.part = reinterpret_cast<float *>(q.ws + kWsPromptPart);
+    const dim3 grid((unsigned)parts, 16);
+    return q.c.D == 128
+               ? launch_early(cache_attn_join_kernel<128, kPromptRows, 1>, grid, 128, 0, true, st, a)
+               : launch_early(cache_attn_join_kernel<64, kPromptRows, 1>, grid, 64, 0, true, st, a);
+}
+
+// Requests with least <= rows * group <= most. early: the kernel before this one
+// in the stream is the many-row kernel of the same call.
+cudaError_t launch_attn_rows(AttnCall &q, int least, int most, int sms, bool early, cudaStream_t st)
+{
+    AttnArgs a = arguments(q);
     a.least = least;
     a.most = most;
     // A table of at most kWholeTokens tokens: uncut, one CTA reads 500 tokens in

@@ -50,6 +50,19 @@ inline cudaError_t launch_early(void (*kernel)(A), dim3 grid, int threads, size_
 
 constexpr int kShortRows = 32;  // packed rows (rows * group) of the short-row kernels
 
+// Workspace: status | open contexts, one per CTA | (m, l) and O of two parts per CTA,
+// 32 rows of 128 (or 16 rows and more CTAs) | the same of the many-row kernel, one
+// part of 256 rows per CTA
+constexpr size_t kPartRows = (size_t)2 * kMaxWide * 32;
+static_assert(kPartRows >= (size_t)2 * kMaxCtas * 16, "parts of 16 rows");
+constexpr size_t kWsMeta = kStatusBytes;
+constexpr size_t kWsMl = kWsMeta + kMaxCtas * 16;
+constexpr size_t kWsPart = kWsMl + kPartRows * 2 * 4;
+constexpr size_t kWsPromptMeta = kWsPart + kPartRows * 128 * 4;
+constexpr size_t kWsPromptMl = kWsPromptMeta + kMaxParts * 16;
+constexpr size_t kWsPromptPart = kWsPromptMl + (size_t)kMaxParts * kPromptRows * 2 * 4;
+constexpr size_t kWorkspace = kWsPromptPart + (size_t)kMaxParts * kPromptRows * 128 * 4;
+
 struct AttnCall {
     View c;
     const void *q;
@@ -85,7 +98,8 @@ struct EvictCall {
 
 cudaError_t launch_append(const View &c, const void *k, const void *v, cudaStream_t st);
 cudaError_t launch_attn_rows(AttnCall &q, int least, int most, int sms, bool early, cudaStream_t st);
-cudaError_t launch_attn_prompt(AttnCall &q, int least, cudaStream_t st);
+cudaError_t launch_attn_prompt(AttnCall &q, int least, int parts, cudaStream_t st);
+cudaError_t launch_attn_join(AttnCall &q, int parts, cudaStream_t st);
 cudaError_t launch_weigh_rows(const WeighCall &q, int least, int most, int sms, bool early, cudaStream_t st);
 cudaError_t launch_weigh_window(const WeighCall &q, int least, int sms, cudaStream_t st);
 cudaError_t launch_evict(const EvictCall &q, int sms, cudaStream_t st);

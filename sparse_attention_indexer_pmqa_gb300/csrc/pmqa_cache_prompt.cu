@@ -32,7 +32,8 @@
 namespace pmqa {
 namespace cache {
 
-constexpr int kPrRows = 256;      // packed rows per CTA (two tiles of 128)
+constexpr int kPrRows = kPromptRows;  // packed rows per CTA (two tiles of 128)
+constexpr int kLeastPart = 4;     // token tiles: a context is not cut finer
 constexpr int kPrTok = 128;       // tokens per tile
 constexpr int kPrThreads = 512;
 constexpr int kKStages = 2, kRawSlots = 3, kVStages = 2, kMeta = 4;
@@ -75,7 +76,113 @@ struct PromptArgs {
     int heads, group;
     int least;        // requests with at least this many packed rows
     long long slots;  // row-block slots over all requests (upper bound)
+    int parts;        // CTAs that contexts may be cut over, 0: they are not cut
+    int4 *meta;       // [parts]: (request, head, row block, 2 parts) of the context that the CTA begins
+    float *ml;        // [parts][256][2]
+    float *part;      // [parts][256][D]
 };
+
+// What a CTA works on: row block `nth` of a request and head, part `part` of the
+// `parts` that its context is cut into, `chunk` token tiles each.
+struct Piece {
+    int req, h, nth, part, parts, chunk;
+};
+
+// With fewer row blocks N than CTAs C, contexts are cut into pieces of
+// chunk = ceil(tiles / (C - N)) tiles: at most tiles / chunk + N <= C of them.
+// Called by the whole CTA; false: there are row blocks enough, nothing is cut.
+__device__ __forceinline__ bool find_piece(const PromptArgs &a, Piece &o)
+{
+    constexpr int WARPS = kPrThreads / 32;
+    __shared__ long long s_n[WARPS], s_t[WARPS];
+    __shared__ int s_req;
+    __shared__ long long s_at;
+    const View &c = a.c;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    auto shape = [&](int i, int &B, int &T) {
+        const Request q = load_request(c, i, false);
+        const int rows = q.n * a.group;
+        B = rows >= a.least ? (rows + kPrRows - 1) / kPrRows : 0;
+        T = max(1, (q.ctx + kPrTok - 1) / kPrTok);
+    };
+    long long n = 0, t = 0;
+    int B, T;
+    for (int i = tid; i < c.bs; i += kPrThreads) {
+        shape(i, B, T);
+        n += (long long)c.H * B;
+        t += (long long)c.H * B * T;
+    }
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) {
+        n += __shfl_xor_sync(kFull, n, k);
+        t += __shfl_xor_sync(kFull, t, k);
+    }
+    if (lane == 0) {
+        s_n[warp] = n;
+        s_t[warp] = t;
+    }
+    __syncthreads();
+    n = t = 0;
+#pragma unroll
+    for (int k = 0; k < WARPS; ++k) {
+        n += s_n[k];
+        t += s_t[k];
+    }
+    if (n >= a.parts)
+        return false;
+    const long long u = blockIdx.x, room = a.parts - n;
+    const int chunk = (int)max((long long)kLeastPart, (t + room - 1) / room);
+    o.parts = 0;
+    o.chunk = chunk;
+    if (tid == 0)
+        s_req = -1;
+    long long base = 0;
+    for (int i0 = 0; u < a.parts && i0 < c.bs; i0 += kPrThreads) {
+        const int i = i0 + tid;
+        long long mine = 0;
+        if (i < c.bs) {
+            shape(i, B, T);
+            mine = (long long)c.H * B * ((T + chunk - 1) / chunk);
+        }
+        long long inc = mine;
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) {
+            const long long y = __shfl_up_sync(kFull, inc, k);
+            if (lane >= k)
+                inc += y;
+        }
+        __syncthreads();
+        if (lane == 31)
+            s_n[warp] = inc;
+        __syncthreads();
+        long long lo = base + inc - mine, all = 0;
+#pragma unroll
+        for (int k = 0; k < WARPS; ++k) {
+            if (k < warp)
+                lo += s_n[k];
+            all += s_n[k];
+        }
+        if (lo <= u && u < lo + mine) {
+            s_req = i;
+            s_at = u - lo;
+        }
+        base += all;
+        if (base > u)
+            break;  // the same for every thread
+    }
+    __syncthreads();
+    if (s_req < 0)
+        return true;  // no piece for this CTA (parts = 0)
+    o.req = s_req;
+    shape(o.req, B, T);
+    o.parts = (T + chunk - 1) / chunk;
+    long long y = s_at;
+    o.part = (int)(y % o.parts);
+    y /= o.parts;
+    o.nth = (int)(y % B);
+    o.h = (int)(y / B);
+    return true;
+}
 
 // First row-block slot of request i (see the append kernel's first_slot).
 __device__ __forceinline__ long long first_block(const PromptArgs &a, int i)
@@ -248,31 +355,43 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
     griddep_launch_dependents();  // the few-row kernel fills the SMs that run out of rows
 
     // ------------------------------------------------------------ which rows
-    // slots run from the last to the first: a request's last rows see the most tokens
-    const long long item = (long long)gridDim.x - 1 - blockIdx.x;
-    const long long slot = item / c.H;
-    const int h = (int)(item - slot * c.H);
-    int lo = 0, len = c.bs;
-    while (len > 1) {
-        const int step = (len + 31) >> 5;
-        const int at = lo + lane * step;
-        const uint32_t le = __ballot_sync(kFull, lane * step < len && first_block(a, at) <= slot);
-        const int k = max(__popc(le) - 1, 0);
-        lo += k * step;
-        len = min(step, len - k * step);
+    Piece pc{0, 0, 0, 0, 1, 0};
+    const bool cut = a.parts > 0 && find_piece(a, pc);
+    if (!cut) {
+        // slots run from the last to the first: a request's last rows see the most tokens
+        const long long item = a.slots * c.H - 1 - blockIdx.x;
+        const long long slot = max(item, 0ll) / c.H;
+        int lo = 0, len = c.bs;
+        while (len > 1) {
+            const int step = (len + 31) >> 5;
+            const int at = lo + lane * step;
+            const uint32_t le = __ballot_sync(kFull, lane * step < len && first_block(a, at) <= slot);
+            const int k = max(__popc(le) - 1, 0);
+            lo += k * step;
+            len = min(step, len - k * step);
+        }
+        const long long nth = slot - first_block(a, lo);
+        const bool mine = item >= 0 && nth >= 0 && nth * kPrRows < 0x7FFFFFFFll;
+        pc = Piece{lo, (int)(max(item, 0ll) - slot * c.H), mine ? (int)nth : 0, 0, mine ? 1 : 0, 0};
     }
-    const int req = lo;
-    const Request q = load_request(c, req, h == 0 && tid == 0);
-    const long long nth = slot - first_block(a, req);
-    const int rows_all = q.n * G;
-    if (rows_all < a.least || nth < 0 || nth * kPrRows >= rows_all)
+    if (a.parts > 0 && tid == 0 && blockIdx.x < a.parts)
+        a.meta[blockIdx.x] = pc.parts > 1 && pc.part == 0 ? make_int4(pc.req, pc.h, pc.nth, 2 * pc.parts)
+                                                          : make_int4(0, 0, 0, 0);
+    if (pc.parts == 0)
         return;  // the same for the whole CTA
-    const int R0 = (int)nth * kPrRows;
+    const int req = pc.req, h = pc.h;
+    const Request q = load_request(c, req, h == 0 && tid == 0);
+    const int rows_all = q.n * G;
+    if (rows_all < a.least || (long long)pc.nth * kPrRows >= rows_all)
+        return;
+    const int R0 = pc.nth * kPrRows;
     const int nrow = min(kPrRows, rows_all - R0);
     const bool two = nrow > 128;
     const int first_tok = q.ctx - q.n;  // slot of query token 0
     const int end = max(0, first_tok + (R0 + nrow - 1) / G + 1);  // tokens that some row sees
-    const int T = (end + kPrTok - 1) / kPrTok;
+    const int tiles = (end + kPrTok - 1) / kPrTok;
+    const int t_0 = pc.part * pc.chunk;  // the piece's first tile, and its number of them
+    const int T = pc.parts > 1 ? max(0, min(tiles - t_0, pc.chunk)) : tiles;
 
     if (sbase & 1023u) {
         if (tid == 0)
@@ -398,7 +517,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
                 const float vfac = __uint_as_float(lds32(tb + 16u));
                 vref = __uint_as_float(lds32(tb + 20u));
                 const uint32_t even = lds32(tb + 24u);
-                const int base = t * kPrTok, past = lim - base;
+                const int past = lim - (t_0 + t) * kPrTok;
                 // nothing of the tile is masked for any row of this warp
                 const bool whole = (mw.x & mw.y & mw.z & mw.w) == 0xFFFFFFFFu &&
                                    __all_sync(kFull, past >= kPrTok - 1);
@@ -458,7 +577,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
             ok = ok && mbar_wait(&bar[kBODone], 0u, abort_flag);
             if (__all_sync(kFull, ok)) {
                 tc_fence_after_sync();
-                const float f = l == 0.0f ? 0.0f : vref * (1.0f / kVUp) / l;
+                const float f = l == 0.0f ? 0.0f : vref * (1.0f / kVUp) / (pc.parts > 1 ? 1.0f : l);
+                const long long at = (long long)blockIdx.x * kPrRows + tile * 128 + row;  // of a part
 #pragma unroll 1
                 for (int cc = 0; cc < D / 32; ++cc) {
                     uint32_t o[32];
@@ -467,7 +587,17 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
                         tmem_ld_wait();
                         reg_fence_cols<32>(o);
                     }
-                    if (has) {
+                    if (has && pc.parts > 1) {
+                        float4 *dst = reinterpret_cast<float4 *>(a.part + at * D + 32 * cc);
+#pragma unroll
+                        for (int z = 0; z < 8; ++z) {
+                            float y[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                y[e] = l == 0.0f ? 0.0f : __uint_as_float(o[4 * z + e]) * f;
+                            dst[z] = make_float4(y[0], y[1], y[2], y[3]);
+                        }
+                    } else if (has) {
                         uint4 *dst = reinterpret_cast<uint4 *>(a.out + rh * D + 32 * cc);
 #pragma unroll
                         for (int z = 0; z < 4; ++z) {
@@ -483,7 +613,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
                         }
                     }
                 }
-                if (has && a.lse)
+                if (has && pc.parts > 1)
+                    *reinterpret_cast<float2 *>(a.ml + at * 2) = make_float2(m, l);
+                else if (has && a.lse)
                     a.lse[rh] = l == 0.0f ? -INFINITY : (m == -INFINITY ? l : (m + log2f(l)) * kLn2);
             } else {
                 fail();
@@ -651,7 +783,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
             auto look_up = [&](int t) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const int tok = t * kPrTok + 32 * k + lane;
+                    const int tok = (t_0 + t) * kPrTok + 32 * k + lane;
                     page[k] = t < T && tok < end ? __ldg(bt + c.page_of(tok)) : -1;
                 }
             };
@@ -664,7 +796,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
                 uint32_t phys[4], row[4];  // block * H + h, and row of the pool
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const int tok = t * kPrTok + 32 * k + lane;
+                    const int tok = (t_0 + t) * kPrTok + 32 * k + lane;
                     phys[k] = row[k] = kNone;
                     if (tok < end) {
                         if (page[k] < 0 || (long long)page[k] >= c.nb) {
@@ -734,7 +866,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
 }
 
 // Requests with at least `least` packed rows (rows * group).
-cudaError_t launch_attn_prompt(AttnCall &q, int least, cudaStream_t st)
+// parts: CTAs that contexts may be cut over (launch_attn_join follows), or 0.
+cudaError_t launch_attn_prompt(AttnCall &q, int least, int parts, cudaStream_t st)
 {
     PromptArgs a{};
     a.c = q.c;
@@ -746,7 +879,11 @@ cudaError_t launch_attn_prompt(AttnCall &q, int least, cudaStream_t st)
     a.group = q.heads / q.c.H;
     a.least = least;
     a.slots = (long long)q.c.rows * a.group / kPrRows + q.c.bs;
-    const long long grid = a.slots * q.c.H;
+    a.parts = parts;
+    a.meta = reinterpret_cast<int4 *>(q.ws + kWsPromptMeta);
+    a.ml = reinterpret_cast<float *>(q.ws + kWsPromptMl);
+    a.part = reinterpret_cast<float *>(q.ws + kWsPromptPart);
+    const long long grid = a.slots * q.c.H + parts;
     if (grid > 0x7FFFFFFFll)
         return cudaErrorInvalidConfiguration;
     static std::atomic<uint64_t> done64{0}, done128{0};

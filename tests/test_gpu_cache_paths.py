@@ -381,6 +381,46 @@ def test_long_contexts_are_cut_and_joined(cuda_lib):
         matches(p, out, lse)
 
 
+@pytest.mark.parametrize("rows,ctx,H,G,D,P", [
+    ([40], [5000], 1, 1, 128, 64),                       # one row block over many CTAs
+    ([5, 1, 5], [3100, 700, 2049], 2, 8, 64, 48),        # beside a request of few rows
+    ([300, 33], [300, 4000], 1, 2, 128, 16),             # blocks that see only the first pieces
+    ([9, 12, 7, 11], [513, 1025, 9, 0], 3, 5, 128, 24),  # pieces of few tokens, an empty context
+    ([2, 1], [1500, 900], 1, 40, 64, 32),                # more query heads than the few-row kernel takes
+    ([70, 60], [60, 2000], 1, 1, 64, 8),                 # rows before slot 0
+])
+def test_many_rows_of_few_requests_are_cut_and_joined(cuda_lib, rows, ctx, H, G, D, P):
+    p = ref.make(rows, ctx, kv_heads=H, group=G, head_dim=D, block=P, seed=21, lead=2, tail=1)
+    ws = cuda_lib.cache_workspace()
+    out, lse = attend(cuda_lib, p, ws=ws)
+    matches(p, out, lse)
+    again, lse2 = attend(cuda_lib, p, ws=ws)
+    r0, r1 = int(p.rb[0]), int(p.rb[-1])
+    assert torch.equal(out[r0:r1], again[r0:r1]) and torch.equal(lse[r0:r1], lse2[r0:r1])
+    status_is(cuda_lib, ws)
+
+
+def test_cut_contexts_with_a_bad_block_and_a_nan_key(cuda_lib):
+    """A key that is NaN reaches the rows that see it and no other piece's; a table
+    entry outside the pool is left out of its piece."""
+    p = ref.make([50, 40], [3000, 2500], kv_heads=1, group=1, head_dim=128, block=32, seed=22)
+    p.kc[p.bt[0, 2980 // 32].long(), 0, 2980 % 32, 5] = ref.NAN8  # rows 30 and later see it
+    ws = cuda_lib.cache_workspace()
+    d = cuda(p)
+    out, lse = attend(cuda_lib, p, d, ws)
+    assert torch.all(torch.isnan(lse[30:50])) and torch.all(torch.isnan(out[30:50]))
+    want, want_l, tol, ltol = ref.attention(p)
+    for a, b in ((0, 30), (50, 90)):
+        check(out.cpu()[a:b], want[a:b], tol[a:b])
+        check(lse.cpu()[a:b], want_l[a:b], ltol[a:b])
+    status_is(cuda_lib, ws)
+    d[4] = d[4].clone()
+    d[4][1, 40] = p.kc.shape[0]
+    again, _ = attend(cuda_lib, p, d, ws)
+    status_is(cuda_lib, ws, cuda_lib.PMQA_DEV_BAD_BLOCK_ID)
+    assert torch.equal(again[:30], out[:30]) and torch.isfinite(again[50:].float()).all()
+
+
 def test_evict_longer_than_a_cluster_holds(cuda_lib):
     """More masses than eight CTAs keep in shared memory, ties across the border."""
     ctx, P, keep = 420000, 1024, 3000
