@@ -11,13 +11,16 @@
 // Bound by HBM: each token and kv head costs 2 D bytes and 4 D flops per query
 // row, so with R rows per kv head the arithmetic is 2 R flops a byte; at R <=
 // 32 that is far below the ridge. The layout follows from that:
-//   * the items (request, kv head, block of 8 NT rows, tile of tokens) are
+//   * the items (request, kv head, block of 8 NT rows, tile of 128 tokens) are
 //     flattened and split evenly over the CTAs, so contexts of any mix of
 //     lengths finish together; a context cut between CTAs leaves (O, m, l)
 //     parts in the workspace and the second kernel joins them;
-//   * every warp takes 16 of a tile's 64 tokens (32 of 128 at D = 64: 55 us instead
-//     of 71 for 32 contexts of 8 k tokens) through its own ring of cp.async stages
-//     and never waits for another warp inside a context;
+//   * every warp takes 32 of a tile's 128 tokens through its own ring of cp.async
+//     stages and never waits for another warp inside a context. Two blocks of 16
+//     tokens in flight hide the products' latency better than more warps do (16
+//     tokens, and three CTAs per SM where registers allow: 127 us instead of 102
+//     for 32 contexts of 32 k tokens, 2 kv heads and 16 rows; 188 instead of 154
+//     with 32 rows; 96 instead of 94 with 8);
 //   * products run as S^T = K Q^T and O^T = V^T P^T, so the 16 rows of the
 //     m16n8k16 shape are tokens (then value columns) and the 8 columns are
 //     query rows: a group of 8 wastes nothing, the softmax weights of a thread
@@ -37,10 +40,14 @@ namespace cache {
 
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * kAttnWarps;
+constexpr int kTok = 32;  // tokens of a warp's step
+constexpr int kTile = kAttnWarps * kTok;
 constexpr float kSlack = 8.0f;    // p <= 2^8 before the maximum moves
+constexpr int kPad = 2;           // what a context's start and end cost, in tiles: 16 requests
+                                  // of 1 to 4096 tokens take 22 us with it, 31 without
 constexpr int kLeastTiles = 2;    // fewest tiles a CTA takes (small problems)
-// Joining one more part, in tiles: with it 60000 tokens of one kv head take 27 us,
-// cut over every CTA 70. (With 32 rows the bound would cost the main loop registers.)
+// Joining one more part, in tiles: with it 60000 tokens of one kv head take 25 us (8
+// rows) and 37 us (32), cut over every CTA 70 and 54.
 constexpr float kJoinCost = 0.15f;
 constexpr int kWholeTokens = 640;
 
@@ -58,13 +65,12 @@ struct AttnArgs {
     float *part;         // [2 CTAs][8 NT][D]
 };
 
-// A warp's stage: 16 K rows, 16 V rows, 16 + 16 scales, the mask of tokens
+// A warp's stage: 32 K rows, 32 V rows, 32 + 32 scales, the mask of tokens
 // that exist. 16-byte chunk c of row r is stored at a place that spreads both
 // access patterns (8 tokens x 4 chunks for K, 4 tokens x 2 chunks for V) over
 // all banks.
 template <int D>
 struct Stage {
-    static constexpr int kTok = D == 64 ? 32 : 16;
     static constexpr uint32_t kRows = kTok * D;
     static constexpr uint32_t kOffKs = 2 * kRows, kOffVs = kOffKs + 4 * kTok, kOffMask = kOffVs + 4 * kTok;
     static constexpr uint32_t kBytes = kOffMask + 16;
@@ -79,22 +85,19 @@ struct Stage {
 
 template <int D, int NT>
 struct AttnShape {
-    static constexpr int kStages = 3;
+    static constexpr int kStages = D == 64 ? 3 : 2;  // what leaves room for kOcc CTAs per SM
     static constexpr int kRows = 8 * NT;
-    // What a context's start and end cost, in tiles: 16 requests of 1 to 4096 tokens
-    // and 8 kv heads take 23 us with it, 31 without. (It costs the kernel of 32 rows
-    // registers: 197 us instead of 187 for 32 requests of 32 k tokens and 2 heads.)
-    static constexpr int kPad = NT == 4 ? 0 : 2;
     static constexpr int kPitch = D + 4;  // floats per row of the merge buffer
     static constexpr uint32_t kRing = kAttnWarps * kStages * Stage<D>::kBytes;
     static constexpr uint32_t kOffMerge = kRing;
     static constexpr uint32_t kOffMl = kOffMerge + kAttnWarps * 8 * kPitch * 4;
     static constexpr uint32_t kOffQ = kOffMl + kAttnWarps * kRows * 8;
-    // 32 rows: q's operand in shared memory (a copy per warp), the registers go to O
+    // 32 rows: q's operand in shared memory, the registers go to O. Every warp writes
+    // the same values there; a context's end has all of them wait for one another.
     static constexpr bool kQShared = NT == 4;
-    static constexpr uint32_t kQWarp = (D / 16) * NT * 32 * 8;
-    static constexpr uint32_t kSmem = kOffQ + (kQShared ? kAttnWarps * kQWarp : 0u);
-    static constexpr int kOcc = NT == 1 ? 3 : NT == 2 ? 3 : 2;
+    static constexpr uint32_t kOffRows = kOffQ + (kQShared ? (D / 16) * NT * 32 * 8 : 0u);
+    static constexpr uint32_t kSmem = kOffRows + (kQShared ? kRows * 8 : 0u);  // a factor, a last slot
+    static constexpr int kOcc = D == 64 && NT < 4 ? 3 : 2;
 };
 
 template <int D, int NT>
@@ -107,7 +110,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
     constexpr int ROWS = Sh::kRows;
     constexpr int KS = D / 16;   // k steps of the first product
     constexpr int MT = D / 16;   // 16-column tiles of the second
-    constexpr int TOK = St::kTok, U = TOK / 16, TILE = kAttnWarps * TOK;
+    constexpr int U = kTok / 16;  // m16 blocks of a step
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const View &c = a.c;
@@ -116,7 +119,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
 
     Range rg;
     Walk w;
-    find_range<TILE, ROWS, Sh::kPad, kAttnThreads>(c, G, a.least, a.most, kLeastTiles, NT == 4 ? 0.0f : kJoinCost, rg, w);
+    find_range<kTile, ROWS, kPad, kAttnThreads>(c, G, a.least, a.most, kLeastTiles, kJoinCost, rg, w);
     if (rg.x0 >= rg.x1) {
         if (tid == 0)
             a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
@@ -127,10 +130,10 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
     if (w.t >= w.T || (a.whole && w.t > 0)) {
         // the range starts behind a context's tiles; or (uncut) a context belongs to
         // the CTA whose range holds its first tile
-        x += w.T + Sh::kPad - w.t;
+        x += w.T + kPad - w.t;
         w.t = w.T - 1;
         if (x < rg.x1)
-            w.template next<TILE, ROWS, Sh::kPad>(c, G, a.least, a.most);
+            w.template next<kTile, ROWS, kPad>(c, G, a.least, a.most);
     }
     if (x >= rg.x1) {
         if (tid == 0)
@@ -160,7 +163,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
     auto look_up = [&]() {
         pend_in = false;
         if (p_more) {
-            const int tok = pw.t * TILE + warp * TOK + (lane & (TOK - 1));
+            const int tok = pw.t * kTile + warp * kTok + lane;
             pend_in = tok < p_end;
             const int pg = c.page_of(tok);
             pend_off = tok - pg * c.P;
@@ -172,10 +175,10 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
                 ++pw.t;
                 p_more = p_x < rg.x1 || a.whole;
             } else {
-                p_x += Sh::kPad;
+                p_x += kPad;
                 p_more = p_x < rg.x1;
                 if (p_more) {
-                    pw.template next<TILE, ROWS, Sh::kPad>(c, G, a.least, a.most);
+                    pw.template next<kTile, ROWS, kPad>(c, G, a.least, a.most);
                     p_end = seen_end(pw.q, pw.b);
                 }
             }
@@ -194,22 +197,20 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
             atomicOr(c.status, (uint32_t)PMQA_DEV_BAD_BLOCK_ID);
             ok = false;
         }
-        const uint32_t mask = __ballot_sync(kFull, ok) & (kFull >> (32 - TOK));
+        const uint32_t mask = __ballot_sync(kFull, ok);
         if (lane == 0)
             asm volatile("st.shared.b32 [%0], %1;" ::"r"(st + St::kOffMask), "r"(mask) : "memory");
         if (mask) {
             // block * H + head, and the row of the pool (both below 2^32)
             const uint32_t phys = ok ? (uint32_t)pend_page * (uint32_t)c.H + (uint32_t)pend_h : 0u;
             const uint32_t row = phys * (uint32_t)c.P + (uint32_t)pend_off;
-#pragma unroll
-            for (int pool = 0; pool < U; ++pool) {  // 16 tokens: the lower lanes K, the upper ones V
-                const bool is_k = U == 1 ? lane < 16 : pool == 0;
-                const uint32_t sdst =
-                    st + (is_k ? St::kOffKs : St::kOffVs) + (uint32_t)(lane & (TOK - 1)) * 4u;
-                if (ok)
-                    cp_async_4(sdst, (is_k ? c.ks : c.vs) + phys);
-                else
-                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(sdst), "r"(0) : "memory");
+            const uint32_t sdst = st + (uint32_t)lane * 4u;
+            if (ok) {
+                cp_async_4(sdst + St::kOffKs, c.ks + phys);
+                cp_async_4(sdst + St::kOffVs, c.vs + phys);
+            } else {
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(sdst + St::kOffKs), "r"(0) : "memory");
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(sdst + St::kOffVs), "r"(0) : "memory");
             }
             if (one_block) {
                 // of 16 tokens the first exists if any does: rows on end from its own
@@ -227,7 +228,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
                 }
             } else {
 #pragma unroll
-                for (int k = 0; k < TOK / PER; ++k) {
+                for (int k = 0; k < kTok / PER; ++k) {
                     const int r = k * PER + lane / CH;
                     const uint32_t nb = (mask >> r) & 1u ? 16u : 0u;
                     const uint32_t rr = __shfl_sync(kFull, row, r);
@@ -251,9 +252,11 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
     float acc[NT][MT][4];
     constexpr int NQ = Sh::kQShared ? 1 : NT;
     uint32_t qb[NQ][KS][2];
-    uint2 *const qsm = reinterpret_cast<uint2 *>(smem + Sh::kOffQ + (Sh::kQShared ? warp * Sh::kQWarp : 0u)) + lane;
-    float m[NT][2], l[NT][2], rc[NT][2];
-    int lim[NT][2];               // last slot that the row sees, -1 for padding
+    uint2 *const qsm = reinterpret_cast<uint2 *>(smem + Sh::kOffQ) + lane;
+    float m[NT][2], l[NT][2], rc[NQ][2];
+    int lim[NQ][2];               // last slot that the row sees, -1 for padding
+    float2 *const rows_c = reinterpret_cast<float2 *>(smem + Sh::kOffRows);
+    int2 *const rows_lim = reinterpret_cast<int2 *>(rows_c + ROWS / 2);
     float vref = 0.0f, vinv = 0.0f, vtop = 0.0f;
     int seg = -1, end = 0, c_slot = 0;
     const long long x_first = x;
@@ -309,12 +312,13 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
                         qsm[(nt * KS + k) * 32] = make_uint2(qb[0][k][0], qb[0][k][1]);
                 }
                 const float mine = a.scale_log2 * down;
-                rc[nt][0] = __shfl_sync(kFull, mine, 8 * t4);
-                rc[nt][1] = __shfl_sync(kFull, mine, 8 * t4 + 4);
+                constexpr auto at = [](int k) { return Sh::kQShared ? 0 : k; };
+                rc[at(nt)][0] = __shfl_sync(kFull, mine, 8 * t4);
+                rc[at(nt)][1] = __shfl_sync(kFull, mine, 8 * t4 + 4);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int Re = w.b * ROWS + nt * 8 + 2 * t4 + e;
-                    lim[nt][e] = Re < w.q.n * G ? w.q.ctx - w.q.n + Re / G : -1;
+                    lim[at(nt)][e] = Re < w.q.n * G ? w.q.ctx - w.q.n + Re / G : -1;
                     m[nt][e] = -INFINITY;
                     l[nt][e] = 0.0f;
                 }
@@ -323,6 +327,10 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         acc[nt][j][e] = 0.0f;
+                if constexpr (Sh::kQShared) {
+                    rows_c[nt * 4 + t4] = make_float2(rc[0][0], rc[0][1]);
+                    rows_lim[nt * 4 + t4] = make_int2(lim[0][0], lim[0][1]);
+                }
             }
         }
         cp_async_wait_group<S - 2>();
@@ -332,7 +340,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
         const uint32_t st = ring + (uint32_t)c_slot * St::kBytes;
         if (++c_slot == S)
             c_slot = 0;
-        const int base = w.t * TILE + warp * TOK;
+        const int base = w.t * kTile + warp * kTok;
         const uint32_t mask = base < end ? lds32(st + St::kOffMask) : 0u;
         if (mask) {
             float s[U][NT][4];
@@ -378,24 +386,28 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
                     vmax = fmaxf(vmax, fabsf(vs[u][y]));
                 }
             // every row sees every token of the chunk (no mask to apply)
-            const bool whole = mask == kFull >> (32 - TOK) && base + TOK - 1 <= w.q.ctx - w.q.n;
+            const bool whole = mask == kFull && base + kTok - 1 <= w.q.ctx - w.q.n;
             bool exceed = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
+                const float2 f = Sh::kQShared ? rows_c[nt * 4 + t4]
+                                              : make_float2(rc[nt % NQ][0], rc[nt % NQ][1]);
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    s[u][nt][0] *= ks[u][0] * rc[nt][0];
-                    s[u][nt][1] *= ks[u][0] * rc[nt][1];
-                    s[u][nt][2] *= ks[u][1] * rc[nt][0];
-                    s[u][nt][3] *= ks[u][1] * rc[nt][1];
+                    s[u][nt][0] *= ks[u][0] * f.x;
+                    s[u][nt][1] *= ks[u][0] * f.y;
+                    s[u][nt][2] *= ks[u][1] * f.x;
+                    s[u][nt][3] *= ks[u][1] * f.y;
                     if (!whole) {
+                        const int2 end2 = Sh::kQShared ? rows_lim[nt * 4 + t4]
+                                                       : make_int2(lim[nt % NQ][0], lim[nt % NQ][1]);
                         const int r = 16 * u + g;
                         const bool k0 = (mask >> r) & 1u, k1 = (mask >> (r + 8)) & 1u;
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            if (!k0 || base + r > lim[nt][e])
+                            if (!k0 || base + r > (e ? end2.y : end2.x))
                                 s[u][nt][e] = -INFINITY;
-                            if (!k1 || base + r + 8 > lim[nt][e])
+                            if (!k1 || base + r + 8 > (e ? end2.y : end2.x))
                                 s[u][nt][2 + e] = -INFINITY;
                         }
                     }
@@ -403,8 +415,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     float top = fmaxf(s[0][nt][e], s[0][nt][2 + e]);
-                    if constexpr (U == 2)
-                        top = fmaxf(top, fmaxf(s[U - 1][nt][e], s[U - 1][nt][2 + e]));
+                                            top = fmaxf(top, fmaxf(s[U - 1][nt][e], s[U - 1][nt][2 + e]));
                     exceed |= top > m[nt][e] + kSlack;
                 }
             }
@@ -414,8 +425,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         float top = fmaxf(s[0][nt][e], s[0][nt][2 + e]);
-                        if constexpr (U == 2)
-                            top = fmaxf(top, fmaxf(s[U - 1][nt][e], s[U - 1][nt][2 + e]));
+                                                    top = fmaxf(top, fmaxf(s[U - 1][nt][e], s[U - 1][nt][2 + e]));
                         top = fmaxf(top, __shfl_xor_sync(kFull, top, 4));
                         top = fmaxf(top, __shfl_xor_sync(kFull, top, 8));
                         top = fmaxf(top, __shfl_xor_sync(kFull, top, 16));
@@ -595,11 +605,11 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
             const int cta = (int)(((last + 1) * rg.C - 1) / rg.total);
             open = make_int4(w.i, w.h, w.b, 2 * (cta - (int)blockIdx.x + 1) + (slot & 1));
         }
-        x += Sh::kPad;
+        x += kPad;
         if (x >= rg.x1)
             break;
         fresh = true;
-        w.template next<TILE, ROWS, Sh::kPad>(c, G, a.least, a.most);
+        w.template next<kTile, ROWS, kPad>(c, G, a.least, a.most);
     }
     cp_async_wait_all();
     if (tid == 0)
@@ -734,8 +744,8 @@ cudaError_t launch_attn_rows(AttnCall &q, int least, int most, int sms, bool ear
     a.least = least;
     a.most = most;
     // A table of at most kWholeTokens tokens: uncut, one CTA reads 500 tokens in
-    // 11.4 us (990 in 17.6); cut and joined, 10 us and a second launch, which
-    // costs the host about 4 us. (The CTA that writes the last part as the joining
+    // 9.7 us and 640 in 11.0; cut and joined, 9.9 and 10.4 us and a second launch,
+    // which costs the host about 4 us. (The CTA that writes the last part as the joining
     // one saves that launch, but 4000 tokens then take 18 us instead of 15, and
     // 60000 take 58 instead of 38.)
     a.whole = (long long)q.c.P * q.c.W <= kWholeTokens;
