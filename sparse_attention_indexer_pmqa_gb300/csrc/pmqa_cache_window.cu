@@ -15,8 +15,10 @@
 // by the tensor cores (D / 32 * 2 products of 66 cycles per tile and 128 rows)
 // and the exponentials (one per token and row, about 3.5 issue slots), 1050 and
 // 900 cycles a tile of 256 rows; four warpgroups hide the latencies. Windows of 64
-// rows of 4 requests of 16 to 32 k tokens (32 query heads over 8) take 77 us, 33 % of
-// the measured bf16 rate counted for one product. K comes row by row: tensor copies
+// rows of 4 requests of 16 to 32 k tokens (32 query heads over 8) take 74 us, 34 % of
+// the measured bf16 rate counted for one product: a row tile's scores, sums and
+// hand-back follow one another, and four warps a scheduler overlap them at 44 % of
+// the issue slots. K comes row by row: tensor copies
 // of whole blocks were no faster (89 us against 86).
 #include <algorithm>
 #include <cmath>
@@ -43,9 +45,9 @@ constexpr uint32_t kWnOffBar = kWnOffMin + 32;
 enum {
     kWKFull = 0,                       // [4] K rows landed: 32 cp.async arrivals and lane 0's own
     kWKEmpty = kWKFull + kWnStages,    // [4] products done (commit), scales read (8 warps)
-    kWSFull = kWKEmpty + kWnStages,    // [2] scores of a buffer: commit
-    kWSEmpty = kWSFull + 2,            // [2] scores read: 8 warps
-    kWDrain = kWSEmpty + 2,            // every product done, before the columns are freed: commit
+    kWSFull = kWKEmpty + kWnStages,    // [2 buffers][2 row tiles] scores: commit
+    kWSEmpty = kWSFull + 4,            // [2][2] scores read: 4 warps
+    kWDrain = kWSEmpty + 4,            // every product done, before the columns are freed: commit
     kWCount = kWDrain + 1
 };
 constexpr uint32_t kWnOffMisc = kWnOffBar + kWCount * 8;
@@ -122,9 +124,9 @@ __global__ void __launch_bounds__(kWnThreads, 1) cache_window_kernel(const __gri
             mbar_init(&bar[kWKFull + s], 33);
             mbar_init(&bar[kWKEmpty + s], 9);
         }
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < 4; ++s) {
             mbar_init(&bar[kWSFull + s], 1);
-            mbar_init(&bar[kWSEmpty + s], 8);
+            mbar_init(&bar[kWSEmpty + s], 4);
         }
         mbar_init(&bar[kWDrain], 1);
         misc[1] = 0;
@@ -252,7 +254,7 @@ __global__ void __launch_bounds__(kWnThreads, 1) cache_window_kernel(const __gri
                         if ((k & 1) != b)
                             continue;
                         const int st = k % kWnStages;
-                        ok = ok && mbar_wait(&bar[kWSFull + b], (uint32_t)(k >> 1) & 1u, abort_flag) &&
+                        ok = ok && mbar_wait(&bar[kWSFull + 2 * b + r], (uint32_t)(k >> 1) & 1u, abort_flag) &&
                              mbar_wait(&bar[kWKFull + st], (uint32_t)(k / kWnStages) & 1u, abort_flag);
                         ok = __all_sync(kFull, ok);
                         if (!ok)
@@ -273,41 +275,48 @@ __global__ void __launch_bounds__(kWnThreads, 1) cache_window_kernel(const __gri
                         if (ok && (r == 0 || two)) {
                             tc_fence_after_sync();
                             const bool whole = __all_sync(kFull, slot <= low);
+// 16 columns are worked on while the next 16 load
+                            uint32_t v[2][16];
+                            tmem_ld16(tS, v[0]);
 #pragma unroll 1
-                            for (int cc = 0; cc < 4; ++cc) {
-                                uint32_t v[32];
-                                tmem_ld32(tS + 32u * cc, v);
-                                tmem_ld_wait();
-                                reg_fence_cols<32>(v);
+                            for (int cc = 0; cc < 8; cc += 2) {
 #pragma unroll
-                                for (int z = 0; z < 32; z += 4) {
-                                    const float4 c4 = *reinterpret_cast<const float4 *>(rc + 32 * cc + z);
-                                    const float4 l4 = *reinterpret_cast<const float4 *>(nl + 32 * cc + z);
-                                    float y0, y1, y2, y3, w0 = l4.x, w1 = l4.y, w2 = l4.z, w3 = l4.w;
-                                    fmul2(y0, y1, __uint_as_float(v[z]), __uint_as_float(v[z + 1]), c4.x, c4.y);
-                                    fmul2(y2, y3, __uint_as_float(v[z + 2]), __uint_as_float(v[z + 3]), c4.z, c4.w);
-                                    ffma2(w0, w1, y0, y1, ks, ks);
-                                    ffma2(w2, w3, y2, y3, ks, ks);
-                                    w0 = ex2_approx(w0);
-                                    w1 = ex2_approx(w1);
-                                    w2 = ex2_approx(w2);
-                                    w3 = ex2_approx(w3);
-                                    if (!whole) {
-                                        const int4 e = *reinterpret_cast<const int4 *>(last + 32 * cc + z);
-                                        w0 = slot <= e.x ? w0 : 0.0f;
-                                        w1 = slot <= e.y ? w1 : 0.0f;
-                                        w2 = slot <= e.z ? w2 : 0.0f;
-                                        w3 = slot <= e.w ? w3 : 0.0f;
+                                for (int y = 0; y < 2; ++y) {
+                                    const int col = 16 * (cc + y);
+                                    tmem_ld_wait();
+                                    reg_fence_cols<16>(v[y]);
+                                    if (y == 0 || cc < 6)
+                                        tmem_ld16(tS + (uint32_t)(col + 16), v[y ^ 1]);
+#pragma unroll
+                                    for (int z = 0; z < 16; z += 4) {
+                                        const float4 c4 = *reinterpret_cast<const float4 *>(rc + col + z);
+                                        const float4 l4 = *reinterpret_cast<const float4 *>(nl + col + z);
+                                        float y0, y1, y2, y3, w0 = l4.x, w1 = l4.y, w2 = l4.z, w3 = l4.w;
+                                        fmul2(y0, y1, __uint_as_float(v[y][z]), __uint_as_float(v[y][z + 1]), c4.x, c4.y);
+                                        fmul2(y2, y3, __uint_as_float(v[y][z + 2]), __uint_as_float(v[y][z + 3]), c4.z, c4.w);
+                                        ffma2(w0, w1, y0, y1, ks, ks);
+                                        ffma2(w2, w3, y2, y3, ks, ks);
+                                        w0 = ex2_approx(w0);
+                                        w1 = ex2_approx(w1);
+                                        w2 = ex2_approx(w2);
+                                        w3 = ex2_approx(w3);
+                                        if (!whole) {
+                                            const int4 e = *reinterpret_cast<const int4 *>(last + col + z);
+                                            w0 = slot <= e.x ? w0 : 0.0f;
+                                            w1 = slot <= e.y ? w1 : 0.0f;
+                                            w2 = slot <= e.z ? w2 : 0.0f;
+                                            w3 = slot <= e.w ? w3 : 0.0f;
+                                        }
+                                        fadd2(s0, s1, w0, w1);
+                                        fadd2(s0, s1, w2, w3);
                                     }
-                                    fadd2(s0, s1, w0, w1);
-                                    fadd2(s0, s1, w2, w3);
                                 }
                             }
                             tc_fence_before_sync();
                         }
                         __syncwarp();
                         if (lane == 0) {
-                            mbar_arrive(&bar[kWSEmpty + b]);
+                            mbar_arrive(&bar[kWSEmpty + 2 * b + r]);
                             mbar_arrive(&bar[kWKEmpty + st]);
                         }
                         const float sum = have ? s0 + s1 : 0.0f;
@@ -327,22 +336,29 @@ __global__ void __launch_bounds__(kWnThreads, 1) cache_window_kernel(const __gri
                         const uint32_t id = idesc_e4m3_f32(128, 128);
                         for (int t = t0; ok && t < t1; ++t) {
                             const int k = n + (t - t0), st = k % kWnStages, b = k & 1;
-                            ok = mbar_wait(&bar[kWKFull + st], (uint32_t)(k / kWnStages) & 1u, abort_flag) &&
-                                 mbar_wait(&bar[kWSEmpty + b], ((uint32_t)(k >> 1) & 1u) ^ 1u, abort_flag);
+                            ok = mbar_wait(&bar[kWKFull + st], (uint32_t)(k / kWnStages) & 1u, abort_flag);
                             if (!ok)
                                 break;
                             fence_proxy_async_smem();
-                            tc_fence_after_sync();
                             const uint64_t kd = sw128_kmajor_desc(sbase + kWnOffK + (uint32_t)st * kWnTile);
-                            for (int r = 0; r < (two ? 2 : 1); ++r) {
+#pragma unroll 1
+                            for (int r = 0; ok && r < 2; ++r) {
+                                ok = mbar_wait(&bar[kWSEmpty + 2 * b + r], ((uint32_t)(k >> 1) & 1u) ^ 1u, abort_flag);
+                                if (!ok)
+                                    break;
+                                tc_fence_after_sync();
                                 const uint64_t qd = sw128_kmajor_desc(sbase + kWnOffQ + (uint32_t)r * 2 * kWnTile);
+                                if (r == 0 || two) {
 #pragma unroll
-                                for (int z = 0; z < D / 16; ++z)
-                                    umma_e4m3(tmem + 256u * b + 128u * r, kd + 2u * (z % (D / 32)),
-                                              qd + (uint64_t)((z / (D / 32)) * (kWnTile >> 4)) + 2u * (z % (D / 32)),
-                                              id, z ? 1u : 0u);
+                                    for (int z = 0; z < D / 16; ++z)
+                                        umma_e4m3(tmem + 256u * b + 128u * r, kd + 2u * (z % (D / 32)),
+                                                  qd + (uint64_t)((z / (D / 32)) * (kWnTile >> 4)) + 2u * (z % (D / 32)),
+                                                  id, z ? 1u : 0u);
+                                }
+                                umma_commit(&bar[kWSFull + 2 * b + r]);
                             }
-                            umma_commit(&bar[kWSFull + b]);
+                            if (!ok)
+                                break;
                             umma_commit(&bar[kWKEmpty + st]);
                         }
                         if (!ok)
