@@ -24,7 +24,7 @@
 // Bound by the tensor cores: 4 D flops per visible (row, head, token) at the
 // bf16 rate, 512 cycles per 128 x 128 x 128 product and tile against about 4.2
 // issue slots per score, 1100 cycles for both tiles. 6415 rows of 32 heads over 8
-// behind 2 to 8 k tokens take 422 us, 930 TFLOP/s (48 % of the measured bf16 rate;
+// behind 2 to 8 k tokens take 418 us, 940 TFLOP/s (49 % of the measured bf16 rate;
 // the tensor pipe is active 45 % of the time): the rest are the gaps between a
 // tile's softmax and its products, instruction fetches (the code is larger than
 // the innermost cache) and the uneven lengths of the items.
@@ -41,6 +41,7 @@ namespace pmqa {
 namespace cache {
 
 constexpr int kPrRows = kPromptRows;  // packed rows per CTA (two tiles of 128)
+constexpr int kRankedRequests = 128;  // so many at most are put in order: each CTA goes over them about 8 times
 constexpr int kLeastPart = 4;     // token tiles (about 9 us): a context is not cut finer
 constexpr int kPrTok = 128;       // tokens per tile
 constexpr int kPrThreads = 512;
@@ -196,6 +197,81 @@ __device__ __forceinline__ bool find_piece(const PromptArgs &a, Piece &o)
 __device__ __forceinline__ long long first_block(const PromptArgs &a, int i)
 {
     return (long long)max(__ldg(a.c.row_begin + i), 0) * a.group / kPrRows + i;
+}
+
+// Row blocks of request i that see at least x token tiles (its last ones): some row
+// of the block must see slot 128 (x - 1).
+__device__ __forceinline__ int blocks_from(const PromptArgs &a, int i, int x)
+{
+    const Request q = load_request(a.c, i, false);
+    const int rows = q.n * a.group, B = rows >= a.least ? (rows + kPrRows - 1) / kPrRows : 0;
+    const long long j = (long long)(x - 1) * kPrTok - (q.ctx - q.n);  // the first row that sees it
+    if (x <= 0 || j <= 0)
+        return B;
+    return j * a.group >= rows ? 0 : B - (int)(j * a.group / kPrRows);
+}
+
+// The u-th row block in the order of falling length (then by request, block, head):
+// a long one started late is waited for (two prompts among decoding requests: 69 us,
+// in the order of the rows 73; by one warp, whose result the others read: in every
+// warp it costs the loops below registers, 482 us instead of 427 on 6415 rows of 32
+// heads). Called by a whole warp; false: u is past the last.
+__device__ __forceinline__ bool ranked_block(const PromptArgs &a, long long u, Piece &o)
+{
+    const View &c = a.c;
+    const int lane = threadIdx.x & 31;
+    auto count = [&](int x) {
+        long long n = 0;
+        for (int i = lane; i < c.bs; i += 32)
+            n += blocks_from(a, i, x);
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1)
+            n += __shfl_xor_sync(kFull, n, k);
+        return n * c.H;
+    };
+    if (u >= count(0))
+        return false;
+    int lo = 0, hi = 0;  // count(lo) > u >= count(hi)
+    for (int i = lane; i < c.bs; i += 32)
+        hi = max(hi, clamp_ctx(c, i, false));
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1)
+        hi = max(hi, __shfl_xor_sync(kFull, hi, k));
+    hi = (hi + kPrTok - 1) / kPrTok + 1;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (count(mid) > u)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    long long at = u - count(hi);  // among the blocks of `lo` tiles
+    for (int i0 = 0; i0 < c.bs; i0 += 32) {
+        const int i = i0 + lane;
+        const int from = i < c.bs ? blocks_from(a, i, lo) : 0;
+        const int mine = i < c.bs ? (from - blocks_from(a, i, hi)) * c.H : 0;
+        int inc = mine;
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) {
+            const int y = __shfl_up_sync(kFull, inc, k);
+            if (lane >= k)
+                inc += y;
+        }
+        const uint32_t over = __ballot_sync(kFull, inc > at);
+        if (over) {
+            const int who = __ffs(over) - 1;
+            const int first = __shfl_sync(kFull, inc - mine, who);
+            o.req = i0 + who;
+            const int k = (int)at - first;
+            o.nth = blocks_from(a, o.req, 0) - __shfl_sync(kFull, from, who) + k / c.H;
+            o.h = k % c.H;
+            o.part = 0;
+            o.parts = 1;
+            return true;
+        }
+        at -= __shfl_sync(kFull, inc, 31);
+    }
+    return false;
 }
 
 // Byte of (row r, 16-byte chunk c) in a 128-byte-row operand, 128-byte swizzle.
@@ -365,7 +441,20 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
     // ------------------------------------------------------------ which rows
     Piece pc{0, 0, 0, 0, 1, 0};
     const bool cut = a.parts > 0 && find_piece(a, pc);
-    if (!cut) {
+    if (!cut && c.bs <= kRankedRequests) {
+        __shared__ int s_pc[4];
+        if (warp == 0) {
+            const bool any = ranked_block(a, blockIdx.x, pc);
+            if (lane == 0) {
+                s_pc[0] = pc.req;
+                s_pc[1] = pc.h;
+                s_pc[2] = pc.nth;
+                s_pc[3] = any ? 1 : 0;
+            }
+        }
+        __syncthreads();
+        pc = Piece{s_pc[0], s_pc[1], s_pc[2], 0, s_pc[3], 0};
+    } else if (!cut) {
         // slots run from the last to the first: a request's last rows see the most tokens
         const long long item = a.slots * c.H - 1 - blockIdx.x;
         const long long slot = max(item, 0ll) / c.H;
@@ -841,16 +930,18 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
                         }
                     }
                 }
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
+#pragma unroll 1
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t mine = k & 2 ? (k & 1 ? row[3] : row[2]) : k & 1 ? row[1] : row[0];
 #pragma unroll
                     for (int y = 0; y < CH; ++y) {
                         const int rr = y * PER + lane / CH, rt = 32 * k + rr;
-                        const uint32_t src = __shfl_sync(kFull, row[k], rr);
+                        const uint32_t src = __shfl_sync(kFull, mine, rr);
                         cp_async_16(dst + (is_k ? sw128(rt, ch) : (uint32_t)(rt * 128 + ch * 16)),
                                     pool + (src == kNone ? 0ull : (unsigned long long)src * D) + ch * 16,
                                     src == kNone ? 0u : 16u);
                     }
+                }
                 uint64_t *const full = &bar[(is_k ? kBKFull : kBRawFull) + slot_i];
                 cp_async_arrive_noinc(full);
                 __syncwarp();

@@ -400,6 +400,18 @@ def test_many_rows_of_few_requests_are_cut_and_joined(cuda_lib, rows, ctx, H, G,
     status_is(cuda_lib, ws)
 
 
+@pytest.mark.parametrize("bs", [128, 140])
+def test_many_requests_with_many_rows(cuda_lib, bs):
+    """More row blocks than SMs, in order of length (up to 128 requests) or of rows."""
+    rows = [40 if i % 3 else 1 for i in range(bs)]
+    ctx = [max(n, (53 * i) % 400) for i, n in enumerate(rows)]
+    p = ref.make(rows, ctx, kv_heads=2, group=2, head_dim=64, block=16, seed=23)
+    ws = cuda_lib.cache_workspace()
+    out, lse = attend(cuda_lib, p, ws=ws)
+    matches(p, out, lse)
+    status_is(cuda_lib, ws)
+
+
 def test_cut_contexts_with_a_bad_block_and_a_nan_key(cuda_lib):
     """A key that is NaN reaches the rows that see it and no other piece's; a table
     entry outside the pool is left out of its piece."""
