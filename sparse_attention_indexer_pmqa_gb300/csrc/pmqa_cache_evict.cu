@@ -18,10 +18,11 @@
 // block's power-of-two scale, and writes the codes rounded to it. Bound by
 // HBM: 2 D bytes in and out per kept token and head.
 //
-// 16 requests of 2 to 64 k tokens and 8 kv heads cut to 4096 tokens: selection 71
-// us (bound by the latencies of its passes over shared memory: two CTAs per SM, of
-// 512 or 1024 threads, take 82 to 97), the move 25 us behind it. One request of 1500
-// tokens: 12 and 9 us.
+// 16 requests of 2 to 64 k tokens and 8 kv heads cut to 4096 tokens: selection 55
+// us (of a CTA's 27: 9 for the masses and the first histogram, 10 for the other
+// passes and their joins, 8 for the places; smaller CTAs, two of them per SM, take
+// 1.1 to 1.4 times as long), the move 25 us behind it. One request of 1500 tokens:
+// 12 and 9 us.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -51,6 +52,7 @@ struct EvictArgs {
     int cs;        // CTAs per cluster
     int key_cap;   // keys of a slice that fit the shared memory given
     int pages;     // new blocks per request (upper bound)
+    int ranked;    // requests are taken in the order of falling length
 };
 
 // Larger floats get larger keys; both zeros the same one; NaN the lowest.
@@ -90,9 +92,26 @@ __global__ void __launch_bounds__(kSelThr, 1) cache_evict_select_kernel(const __
     const View &c = a.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = (int)cl.block_rank();
-    const long long pair = blockIdx.x / a.cs;
-    const int i = (int)(pair / c.H);
+    long long pair = blockIdx.x / a.cs;
+    int i = (int)(pair / c.H);
     griddep_launch_dependents();
+    if (a.ranked) {
+        // the request with i longer ones (of equal ones, the first come first)
+        __shared__ int s_req;
+        if (tid < c.bs) {
+            const int mine = __ldg(c.ctx + tid);
+            int before = 0;
+            for (int j = 0; j < c.bs; ++j) {
+                const int other = __ldg(c.ctx + j);
+                before += other > mine || (other == mine && j < tid);
+            }
+            if (before == i)
+                s_req = tid;
+        }
+        __syncthreads();
+        pair += (long long)(s_req - i) * c.H;
+        i = s_req;
+    }
     int ctx = clamp_ctx(c, i, rank == 0 && tid == 0 && pair % c.H == 0);
     if (ctx > a.width) {
         if (rank == 0 && tid == 0)
@@ -432,6 +451,9 @@ cudaError_t launch_evict(const EvictCall &q, int sms, cudaStream_t st)
                       (pairs * cs <= sms && q.width > (long long)cs * 4096)))
         cs *= 2;
     a.cs = cs;
+    // more CTAs than SMs: long requests start first (the batch above: 55 us instead of
+    // 70), unless ranking them would take longer than it gains
+    a.ranked = pairs * cs > sms && q.c.bs <= 128;
     const long long chunk = ((std::min<long long>(q.width, 0x7FFFFF00ll) + cs - 1) / cs + 1023) & ~1023ll;
     a.key_cap = (int)std::min<long long>(chunk, kKeysMax);
     const int smem = a.key_cap * 4;

@@ -433,6 +433,27 @@ def test_cut_contexts_with_a_bad_block_and_a_nan_key(cuda_lib):
     assert torch.equal(again[:30], out[:30]) and torch.isfinite(again[50:].float()).all()
 
 
+@pytest.mark.parametrize("bs", [40, 140])
+def test_evict_of_many_requests(cuda_lib, bs):
+    """More lists than SMs: taken in the order of their length (up to 128 requests) or
+    of their number; equal lengths, empty requests and ones that keep everything."""
+    keep, P, H = 20, 8, 4
+    ctx = [(37 * i) % 90 if i % 5 else 70 for i in range(bs)]
+    p = ref.make([0] * bs, ctx, kv_heads=H, group=1, head_dim=64, block=P, seed=24, poison=False,
+                 spare=3 * bs)
+    new = p.free[:3 * bs].reshape(bs, 3).contiguous()
+    mass = torch.rand((bs, H, 96), generator=p.gen).mul(8).round()  # many ties
+    want = ref.evict(p, mass, keep, 2, 5, new)
+    d = cuda(p)
+    ws = cuda_lib.cache_workspace()
+    kept, lens, out = cuda_lib.pmqa_cache_evict(*d, mass.cuda(), keep, 2, 5, new.cuda(), ws=ws)
+    assert torch.equal(kept.cpu(), want[0]) and torch.equal(lens.cpu(), want[1])
+    assert torch.equal(out.cpu(), want[2])
+    for got, w in zip((d[0], d[2], d[1], d[3]), want[3:]):
+        assert torch.equal(got.cpu(), w)
+    status_is(cuda_lib, ws)
+
+
 def test_evict_longer_than_a_cluster_holds(cuda_lib):
     """More masses than eight CTAs keep in shared memory, ties across the border."""
     ctx, P, keep = 420000, 1024, 3000
