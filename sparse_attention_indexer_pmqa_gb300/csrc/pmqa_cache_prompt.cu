@@ -24,7 +24,7 @@
 // Bound by the tensor cores: 4 D flops per visible (row, head, token) at the
 // bf16 rate, 512 cycles per 128 x 128 x 128 product and tile against about 4.2
 // issue slots per score, 1100 cycles for both tiles. 6415 rows of 32 heads over 8
-// behind 2 to 8 k tokens take 418 us, 940 TFLOP/s (49 % of the measured bf16 rate;
+// behind 2 to 8 k tokens take 414 us, 950 TFLOP/s (49 % of the measured bf16 rate;
 // the tensor pipe is active 45 % of the time): the rest are the gaps between a
 // tile's softmax and its products, instruction fetches (the code is larger than
 // the innermost cache) and the uneven lengths of the items.
@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
 
     if (warp < 8) {
         // -------------------------------------------------------- softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");  // 2 x 176 + 2 x 80 = 4 x 128
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");  // 2 x 192 + 2 x 64 = 4 x 128
         const int tile = warp >> 2;
         const int row = (warp & 3) * 32 + lane;     // TMEM lane
         const int R = R0 + tile * 128 + row;
@@ -720,7 +720,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
         }
     } else if (warp < 12) {
         // -------------------------------------------------------- V conversion
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         const int lt = tid - 256, lw = lt >> 5;
         float *const red = reinterpret_cast<float *>(smem + kPrOffRed);
         float vref = 0.0f;
@@ -808,7 +808,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
             }
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == 12 && lane == 0) {
         // -------------------------------------------------------- products
         constexpr uint32_t idq = idesc_e4m3_f32(128, 128);
