@@ -424,8 +424,10 @@ size_t pmqa_cache_workspace_bytes(void);
  * codes c become rne(c s / s'), and a new value x is stored as rne(x / s'),
  * saturated at 448 (NaN stays NaN). Slots behind ctx_i and blocks without a new
  * token are left as they were. A block that receives tokens must belong to one
- * request only. New rows whose slot would be negative (n_i > ctx_i) are dropped
- * and set PMQA_DEV_BAD_CONTEXT. One kernel launch.
+ * request only. Lengths out of range drop rows and move none: row j's slot is
+ * ctx_i - n_i + j from the lengths as given, and rows whose slot is negative or
+ * behind the table's last, rows past the first max_rows and rows outside [0, rows) are
+ * not written (PMQA_DEV_BAD_CONTEXT). One kernel launch.
  */
 int pmqa_cache_append(const pmqa_cache_problem *p, const void *k, const void *v, void *ws,
                       size_t ws_bytes, pmqa_stream_t stream);

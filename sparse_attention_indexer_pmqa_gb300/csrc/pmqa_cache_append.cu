@@ -82,15 +82,23 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const __gr
     const Request q = load_request(c, i, u == 2 * slot * c.H && ut == 0);
     if (q.n == 0 || kth < 0)
         return;
-    const int first = q.ctx - q.n;  // slot of the first new row
+    // A row's slot comes from the lengths as they are given: rows that the arrays or
+    // the table have no place for are dropped, and no other row moves over tokens
+    // that are already there.
+    const int rb = __ldg(c.row_begin + i);
+    const long long given = (long long)__ldg(c.row_begin + i + 1) - rb;
+    const long long first = (long long)__ldg(c.ctx + i) - given + (q.r0 - (long long)rb);  // slot of row r0
+    const long long cap = min((long long)c.P * c.W, (long long)kMaxContext);
+    const long long from = max(first, 0ll), to = min(first + q.n, cap);  // slots written
     if (first < 0 && ut == 0)
         atomicOr(c.status, (uint32_t)PMQA_DEV_BAD_CONTEXT);  // rows before slot 0 are not kept
-    const int b0 = c.page_of(max(first, 0));
-    const long long bl = b0 + kth;
-    if (bl * c.P >= q.ctx)
+    if (from >= to)
         return;
-    const int b = (int)bl, lo = max(max(first, 0), b * c.P);
-    const int hi = (int)min((long long)q.ctx, (bl + 1) * c.P);
+    const long long bl = c.page_of((int)from) + kth;
+    if (bl * c.P >= to)
+        return;
+    const int b = (int)bl, lo = (int)max(from, bl * c.P);
+    const int hi = (int)min(to, (bl + 1) * c.P);
     const int held = lo - b * c.P, nrow = hi - lo;
     const int page = __ldg(c.bt + (long long)i * c.W + b);
     if (page < 0 || (long long)page >= c.nb) {

@@ -1,0 +1,101 @@
+"""Inputs at the edges of what the cache operators' documentation allows: lengths and
+rows past their arrays, requests without rows, the largest `keep`, streams."""
+
+import pytest
+import torch
+
+from tests import cache_ref as ref
+from tests.test_gpu_cache import cuda
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------- rows past their arrays
+
+def appended(lib, p, ctx, rb, max_rows):
+    """Both pools and scales after an append with these lengths, and the status."""
+    ws = lib.cache_workspace()
+    d = cuda(p)
+    d[5] = torch.tensor(ctx, dtype=torch.int32, device="cuda")
+    lib.pmqa_cache_append(p.k_new.cuda(), p.v_new.cuda(), *d,
+                          torch.tensor(rb, dtype=torch.int32, device="cuda"), max_rows, ws=ws)
+    return [d[i].cpu() for i in (0, 2, 1, 3)], lib.pmqa_read_device_status(ws)
+
+
+def full_table(n, block):
+    """Two requests, the first with all of its table's blocks in use, and n new rows."""
+    p = ref.make([n, min(n, 2)], [4 * block, 30], kv_heads=2, group=1, head_dim=128, block=block,
+                 seed=51, poison=False)
+    p.bt = p.bt[:, :4].contiguous()
+    return p
+
+
+def only(p, runs):
+    """Leave each request the `count` new rows from `first` on."""
+    keep = torch.cat([torch.arange(first, first + count) for first, count in runs])
+    p.k_new, p.v_new = p.k_new[keep], p.v_new[keep]
+    p.rows = [count for _, count in runs]
+    p.rb = torch.tensor([0, runs[0][1], runs[0][1] + runs[1][1]], dtype=torch.int32)
+
+
+@pytest.mark.parametrize("n,block", [(1, 16), (3, 16), (150, 64), (40, 8)])
+@pytest.mark.parametrize("past", [1, 2, 1000, 2 ** 31 - 1])
+def test_rows_past_the_table_are_dropped(cuda_lib, n, block, past):
+    """A length past the table: rows whose slots the table has go there, the others
+    nowhere, and no earlier token is overwritten."""
+    p = full_table(n, block)
+    cap = 4 * block
+    ctx = min(cap + past, 2 ** 31 - 1)
+    got, status = appended(cuda_lib, p, [ctx, 30], p.rb.tolist(), n)
+    assert status == cuda_lib.PMQA_DEV_BAD_CONTEXT
+    kept = max(0, n - (ctx - cap))
+    p.ctx = torch.tensor([cap if kept else 0, 30], dtype=torch.int32)
+    only(p, [(0, kept), (n, p.rows[1])])
+    for g, w in zip(got, ref.append(p)):
+        assert torch.equal(g, w)
+
+
+@pytest.mark.parametrize("max_rows", [1, 2, 100])
+def test_rows_past_max_rows_are_dropped(cuda_lib, max_rows):
+    """More rows than max_rows: the first ones go to their own slots."""
+    n, ctx = 130, 250
+    p = full_table(n, 64)
+    got, status = appended(cuda_lib, p, [ctx, 30], p.rb.tolist(), max_rows)
+    assert status == cuda_lib.PMQA_DEV_BAD_CONTEXT
+    m1, m2 = min(n, max_rows), min(2, max_rows)
+    p.ctx = torch.tensor([ctx - n + m1, 30 - 2 + m2], dtype=torch.int32)
+    only(p, [(0, m1), (n, m2)])
+    for g, w in zip(got, ref.append(p)):
+        assert torch.equal(g, w)
+
+
+@pytest.mark.parametrize("max_rows", [1, 40])
+def test_rows_outside_the_call_are_dropped(cuda_lib, max_rows):
+    """row_begin outside [0, rows]: rows that exist keep their slots."""
+    # request 0 begins three rows before the first; request 1 ends past the last
+    p = full_table(1, 16)
+    got, status = appended(cuda_lib, p, [60, 30], [-3, 1, 60], max_rows)
+    assert status == cuda_lib.PMQA_DEV_BAD_CONTEXT
+    p.ctx = torch.tensor([60, 0], dtype=torch.int32)  # request 1's row would be slot 30 - 59
+    only(p, [(0, 1), (1, 0)])
+    for g, w in zip(got, ref.append(p)):
+        assert torch.equal(g, w)
+    p = full_table(3, 16)
+    got, status = appended(cuda_lib, p, [60, 30], [0, 3, 8], max_rows)
+    assert status == cuda_lib.PMQA_DEV_BAD_CONTEXT
+    m = [min(3, max_rows), min(2, max_rows)]
+    p.ctx = torch.tensor([60 - 3 + m[0], 30 - 5 + m[1]], dtype=torch.int32)
+    only(p, [(0, m[0]), (3, m[1])])
+    for g, w in zip(got, ref.append(p)):
+        assert torch.equal(g, w)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_a_negative_length_appends_nothing(cuda_lib, n):
+    p = full_table(n, 16)
+    got, status = appended(cuda_lib, p, [-7, 30], p.rb.tolist(), max(n, 2))
+    assert status == cuda_lib.PMQA_DEV_BAD_CONTEXT
+    p.ctx = torch.tensor([0, 30], dtype=torch.int32)
+    only(p, [(0, 0), (n, p.rows[1])])
+    for g, w in zip(got, ref.append(p)):
+        assert torch.equal(g, w)
