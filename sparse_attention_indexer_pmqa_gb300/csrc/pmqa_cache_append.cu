@@ -155,6 +155,8 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const __gr
 #pragma unroll
         for (int k = 0; k < WARPS; ++k)
             top = fmaxf(top, s_top[k]);
+    } else {
+        __syncwarp();  // every lane has read the old scale
     }
     float s = pow2_scale(top);
     if (held > 0)
