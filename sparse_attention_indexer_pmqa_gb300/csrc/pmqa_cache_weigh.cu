@@ -87,6 +87,7 @@ __global__ void __launch_bounds__(kWeighThreads, 3)
     long long p_x = rg.x0;
     int pend_page = -1, pend_off = 0, pend_tok = 0, pend_h = 0, pend_i = 0;
     bool pend_in = false;
+    bool pend_rows = false;  // the request has rows; otherwise its keys are not read
     auto look_up = [&]() {
         pend_in = false;
         if (p_x < rg.x1) {
@@ -94,6 +95,7 @@ __global__ void __launch_bounds__(kWeighThreads, 3)
             pend_h = pw.h;
             pend_i = pw.i;
             pend_in = pend_tok < pw.q.ctx && pend_tok < a.width;
+            pend_rows = pw.q.n > 0;
             const int pg = c.page_of(pend_tok);
             pend_off = pend_tok - pg * c.P;
             if (pend_in)
@@ -121,6 +123,8 @@ __global__ void __launch_bounds__(kWeighThreads, 3)
             atomicOr(c.status, (uint32_t)PMQA_DEV_BAD_BLOCK_ID);
             ok = false;
         }
+        // no mask bit for a token that no row sees: its weight is 0 whatever its key is
+        ok = ok && pend_rows;
         const uint32_t mask = __ballot_sync(kFull, ok);
         const uint32_t here = __ballot_sync(kFull, pend_in);
         if (lane == 0)

@@ -1,11 +1,13 @@
 """Inputs at the edges of what the cache operators' documentation allows: lengths and
 rows past their arrays, requests without rows, the largest `keep`, streams."""
 
+import math
+
 import pytest
 import torch
 
 from tests import cache_ref as ref
-from tests.test_gpu_cache import cuda
+from tests.test_gpu_cache import cuda, status_is
 
 pytestmark = pytest.mark.gpu
 
@@ -99,3 +101,34 @@ def test_a_negative_length_appends_nothing(cuda_lib, n):
     only(p, [(0, 0), (n, p.rows[1])])
     for g, w in zip(got, ref.append(p)):
         assert torch.equal(g, w)
+
+
+# ------------------------------------------------------------- requests without rows
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,G", [(1, 4), (2, 8), (40, 1)])
+@pytest.mark.parametrize("bad", ["codes", "scales", "both"])
+def test_weigh_of_a_request_without_rows(cuda_lib, bad, n, G, D):
+    """A sum over no rows adds nothing, whatever the cached keys are."""
+    p = ref.make([0, n], [150, 100], kv_heads=2, group=G, head_dim=D, block=16, seed=52)
+    if bad != "scales":
+        p.kc[p.bt[0, :9].long()] = ref.NAN8
+    if bad != "codes":
+        p.ks[p.bt[0, :9].long()] = math.nan
+    _, lse, _, _ = ref.attention(p)
+    width = p.bt.shape[1] * 16
+    mass = torch.rand((2, 2, width), generator=p.gen)
+    kc, _, ks, _, bt, ctx = cuda(p)
+    ws = cuda_lib.cache_workspace()
+    args = (p.q.cuda(), kc, ks, bt, ctx, p.rb.cuda(), p.max_rows, p.sm, lse.float().cuda())
+    got = cuda_lib.pmqa_cache_weigh(*args, mass.cuda(), mass_out=torch.zeros_like(mass).cuda(),
+                                    ws=ws).cpu()
+    fresh = cuda_lib.pmqa_cache_weigh(*args, ws=ws).cpu()
+    status_is(cuda_lib, ws)
+    assert torch.equal(got[0, :, :150], mass[0, :, :150]) and torch.all(got[0, :, 150:] == 0.0)
+    assert torch.all(fresh[0] == 0.0)
+    # a table entry outside the pool is still reported
+    bt[0, 1] = -1
+    got = cuda_lib.pmqa_cache_weigh(*args, mass.cuda(), ws=ws).cpu()
+    status_is(cuda_lib, ws, cuda_lib.PMQA_DEV_BAD_BLOCK_ID)
+    assert torch.equal(got[0], mass[0])
