@@ -437,6 +437,12 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
     const View &c = a.c;
     const int G = a.group;
     griddep_launch_dependents();  // the few-row kernel fills the SMs that run out of rows
+    if (G > kShortRows && blockIdx.x == 0) {
+        // no few-row kernel follows: report what had to be clamped here, for requests
+        // without a row block too
+        for (int i = tid; i < c.bs; i += kPrThreads)
+            load_request(c, i, true);
+    }
 
     // ------------------------------------------------------------ which rows
     Piece pc{0, 0, 0, 0, 1, 0};

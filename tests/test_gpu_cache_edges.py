@@ -8,6 +8,7 @@ import torch
 
 from tests import cache_ref as ref
 from tests.test_gpu_cache import cuda, status_is
+from tests.test_gpu_cache_paths import attend, matches
 
 pytestmark = pytest.mark.gpu
 
@@ -132,3 +133,37 @@ def test_weigh_of_a_request_without_rows(cuda_lib, bad, n, G, D):
     got = cuda_lib.pmqa_cache_weigh(*args, mass.cuda(), ws=ws).cpu()
     status_is(cuda_lib, ws, cuda_lib.PMQA_DEV_BAD_BLOCK_ID)
     assert torch.equal(got[0], mass[0])
+
+
+# ------------------------------------------------------------- clamps of requests without rows
+
+@pytest.mark.parametrize("G", [2, 40])
+@pytest.mark.parametrize("rows,ctx,rb", [
+    ([0, 1], [10 ** 6, 30], [0, 0, 1]),   # a context past its table
+    ([0, 1], [-1, 30], [0, 0, 1]),
+    ([1, 0], [30, 20], [0, 1, 0]),        # row_begin falls
+    ([1, 0], [30, 20], [0, 1, 9]),        # and runs past the rows
+])
+def test_clamps_are_reported_for_requests_without_rows(cuda_lib, rows, ctx, rb, G):
+    """Whatever the heads per kv head: a request that no kernel works on is looked at."""
+    p = ref.make(rows, [30, 30], kv_heads=1, group=G, head_dim=64, block=16, seed=53)
+    ws = cuda_lib.cache_workspace()
+    d = cuda(p)
+    d[5] = torch.tensor(ctx, dtype=torch.int32, device="cuda")
+    out, lse = cuda_lib.pmqa_cache_attention(p.q.cuda(), *d, torch.tensor(rb, dtype=torch.int32).cuda(),
+                                             1, p.sm, want_lse=True, ws=ws)
+    status_is(cuda_lib, ws, cuda_lib.PMQA_DEV_BAD_CONTEXT)
+    matches(p, out, lse)
+
+
+@pytest.mark.parametrize("extra,H", [(100, 2), (200, 1)])
+def test_clamps_are_reported_where_nothing_is_cut(cuda_lib, extra, H):
+    """More row blocks than SMs, in order of length (up to 128 requests) or of rows."""
+    p = ref.make([0] + [1] * extra, [30] * (1 + extra), kv_heads=H, group=40, head_dim=64, block=16,
+                 seed=54)
+    ws = cuda_lib.cache_workspace()
+    d = cuda(p)
+    d[5][0] = 10 ** 6
+    out, lse = attend(cuda_lib, p, d, ws)
+    status_is(cuda_lib, ws, cuda_lib.PMQA_DEV_BAD_CONTEXT)
+    matches(p, out, lse)
