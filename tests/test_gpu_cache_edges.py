@@ -167,3 +167,15 @@ def test_clamps_are_reported_where_nothing_is_cut(cuda_lib, extra, H):
     out, lse = attend(cuda_lib, p, d, ws)
     status_is(cuda_lib, ws, cuda_lib.PMQA_DEV_BAD_CONTEXT)
     matches(p, out, lse)
+
+
+@pytest.mark.parametrize("P", [1, 16])
+def test_append_reports_rows_that_fall(cuda_lib, P):
+    """row_begin that falls in the middle: that request has no rows, and is reported."""
+    p = ref.make([5, 0, 1], [30, 30, 30], kv_heads=2, group=1, head_dim=64, block=P, seed=56,
+                 poison=False)
+    got, status = appended(cuda_lib, p, [30, 30, 30], [0, 5, 3, 4], 5)
+    assert status == cuda_lib.PMQA_DEV_BAD_CONTEXT
+    p.k_new[5], p.v_new[5] = p.k_new[3], p.v_new[3]
+    for g, w in zip(got, ref.append(p)):
+        assert torch.equal(g, w)
