@@ -442,7 +442,10 @@ cudaError_t launch_evict(const EvictCall &q, int sms, cudaStream_t st)
     a.kept = q.kept;
     a.lens_out = q.lens_out;
     a.mass_out = q.mass_out;
-    a.pages = (q.keep + q.c.P - 1) / q.c.P;
+    // new blocks that a request can fill: of `keep` tokens, or of its longest context
+    // (keep may be up to 2^31 - 1)
+    const long long most = std::min({(long long)q.keep, (long long)q.c.P * q.c.W, (long long)kMaxContext});
+    a.pages = (int)((most + q.c.P - 1) / q.c.P);
     const long long pairs = (long long)q.c.bs * q.c.H;
     // CTAs per cluster: enough for the longest row's keys to stay in shared
     // memory, and (few pairs) enough to use the GPU; 8 is the portable most

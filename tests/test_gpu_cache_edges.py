@@ -179,3 +179,24 @@ def test_append_reports_rows_that_fall(cuda_lib, P):
     p.k_new[5], p.v_new[5] = p.k_new[3], p.v_new[3]
     for g, w in zip(got, ref.append(p)):
         assert torch.equal(g, w)
+
+
+# ------------------------------------------------------------- the largest keep
+
+def test_evict_with_the_largest_keep(cuda_lib):
+    """keep = 2^31 - 1: nothing is dropped, everything moves."""
+    keep, P, c = 2 ** 31 - 1, 1024, 1500
+    p = ref.make([1], [c], kv_heads=1, group=1, head_dim=64, block=P, seed=55, spare=2, poison=False)
+    new = torch.full((1, -(-keep // P)), -1, dtype=torch.int32)
+    new[0, :2] = p.free[:2]
+    mass = torch.rand((1, 1, c), generator=p.gen)
+    d = cuda(p)
+    ws = cuda_lib.cache_workspace()
+    kept, lens, out = cuda_lib.pmqa_cache_evict(*d, mass.cuda(), keep, 4, 8, new.cuda(), ws=ws)
+    status_is(cuda_lib, ws)
+    assert int(lens[0]) == c and torch.equal(out.cpu(), mass)
+    assert torch.equal(kept[0, 0, :c].cpu(), torch.arange(c, dtype=torch.int32))
+    assert bool((kept[0, 0, c:] == -1).all())
+    want = ref.evict(p, mass, c, 4, 8, new[:, :2])
+    for got, w in zip((d[0], d[2], d[1], d[3]), want[3:]):
+        assert torch.equal(got.cpu(), w)
