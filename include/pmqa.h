@@ -460,7 +460,8 @@ int pmqa_cache_attention(const pmqa_cache_problem *p, const void *q, int32_t hea
  * over request i's rows j that see t and the query heads hq of kv head h; other
  * entries are not written. q, heads and sm_scale as in the attention call whose
  * lse this is; v_cache and v_scale are not read and may be NULL.
- *   mass_in   fp32 [bs, kv_heads, mass_width] or NULL (zeros); may be mass_out
+ *   mass_in   fp32 [bs, kv_heads, mass_width] or NULL (zeros); may be mass_out, but
+ *             must not overlap it otherwise
  *   mass_out  fp32 [bs, kv_heads, mass_width]
  * Every sum is formed in one order: equal calls give equal bits. One kernel
  * launch, two where max_rows * heads / kv_heads > 32.

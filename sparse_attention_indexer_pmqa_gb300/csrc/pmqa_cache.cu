@@ -13,6 +13,13 @@ namespace {
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// `an` bytes from a and `bn` from b share some
+bool overlap(const void *a, long long an, const void *b, long long bn)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + (unsigned long long)bn && y < x + (unsigned long long)an;
+}
+
 bool missing(const void *p, uintptr_t a) { return !p || !aligned(p, a); }
 
 enum { kNeedRows = 1, kNeedValues = 2 };
@@ -177,6 +184,10 @@ extern "C" int pmqa_cache_weigh(const pmqa_cache_problem *p, const void *q, int3
         return PMQA_OK;
     if (missing(mass_out, 4) || (mass_in && !aligned(mass_in, 4)) ||
         (p->rows > 0 && (missing(q, 16) || missing(lse, 4))))
+        return PMQA_ERR_INVALID_ARG;
+    // in place or apart: shifted, sums would be read as other tokens' earlier masses
+    const long long n = 4ll * p->bs * p->kv_heads * mass_width;
+    if (mass_in && mass_in != mass_out && overlap(mass_in, n, mass_out, n))
         return PMQA_ERR_INVALID_ARG;
     int sms = 0;
     if ((rc = sm_count(&sms)) != PMQA_OK)
