@@ -483,7 +483,7 @@ int pmqa_cache_weigh(const pmqa_cache_problem *p, const void *q, int32_t heads, 
  *               the first ceil(min(ctx_i, keep) / block_size) of row i are used.
  *               None of them may be in use by block_tables or listed twice
  *   kept        int32 [bs, kv_heads, keep]: old slots in rising order, then -1
- *   lens_out    int32 [bs]: min(ctx_i, keep); not context_lens itself
+ *   lens_out    int32 [bs]: min(ctx_i, keep); must not overlap context_lens
  *   mass_out    fp32 [bs, kv_heads, mass_width] or NULL: the kept tokens' masses,
  *               then zeros; must not overlap mass
  * A new block's scale is e(largest |code * scale| moved there) (see append), its

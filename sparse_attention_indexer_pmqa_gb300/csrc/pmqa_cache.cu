@@ -217,14 +217,13 @@ extern "C" int pmqa_cache_evict(const pmqa_cache_problem *p, const float *mass, 
     if (p->bs == 0)
         return PMQA_OK;
     if (missing(mass, 4) || missing(new_tables, 4) || missing(kept, 4) || missing(lens_out, 4) ||
-        (mass_out && !aligned(mass_out, 4)) || lens_out == p->context_lens)
+        (mass_out && !aligned(mass_out, 4)))
         return PMQA_ERR_INVALID_ARG;
-    if (mass_out) {
-        // the masses are read while the kept ones are written
-        const long long n = (long long)p->bs * p->kv_heads * mass_width;
-        if (mass_out < mass + n && mass < mass_out + n)
-            return PMQA_ERR_INVALID_ARG;
-    }
+    // lengths and masses are read while the new ones are written
+    const long long n = 4ll * p->bs * p->kv_heads * mass_width;
+    if (overlap(lens_out, 4ll * p->bs, p->context_lens, 4ll * p->bs) ||
+        (mass_out && overlap(mass_out, n, mass, n)))
+        return PMQA_ERR_INVALID_ARG;
     int sms = 0;
     if ((rc = sm_count(&sms)) != PMQA_OK)
         return rc;

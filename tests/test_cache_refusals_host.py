@@ -6,7 +6,7 @@ import ctypes
 import pytest
 
 from sparse_attention_indexer_pmqa_gb300 import build, pmqa
-from tests.test_cache_host import INV, problem, weigh
+from tests.test_cache_host import INV, evict, problem, weigh
 
 
 @pytest.fixture(scope="module")
@@ -26,3 +26,11 @@ def test_weigh_refuses_masses_that_overlap_in_part(lib):
     size = 4 * 2 * 2 * 128
     for shift in (4, -4, size - 4, 4 - size):
         assert weigh(lib, p, had=at(0x30000 + shift), out=at(0x30000)) == INV
+
+
+def test_evict_refuses_lengths_that_overlap_in_part(lib):
+    """lens_out is written while context_lens is read: one word in common is refused
+    as the whole is."""
+    p = problem()  # 2 requests
+    for shift in (0, 4, -4):
+        assert evict(lib, p, lens=at(p.context_lens + shift)) == INV
