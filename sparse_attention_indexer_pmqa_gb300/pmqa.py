@@ -492,20 +492,22 @@ def make_cache_problem(k_cache, v_cache, k_scale, v_scale, block_tables, context
     """Fill a pmqa_cache_problem from tensors shaped as in the C header (the
     pools as float8_e4m3fn or uint8; v_cache and v_scale may be None where the
     call does not read values)."""
-    num_blocks, kv_heads, block_size, head_dim = k_cache.shape
+    num_blocks, kv_heads, block_size, head_dim = pool = k_cache.shape
     bs, width = block_tables.shape
     dev = k_cache.get_device()
     f32, i32 = _torch()[:2]
-    n = num_blocks * kv_heads
-    assert dev >= 0 and k_cache.element_size() == 1 and k_cache.is_contiguous()
-    _like(k_scale, dev, f32, n)
+    code = k_cache.dtype
+    if code not in _torch()[5]:
+        raise AssertionError(f"expected float8_e4m3fn (or uint8) pools, got {code}")
+    _like(k_cache, dev, code, pool)
+    _like(k_scale, dev, f32, (num_blocks, kv_heads))
     if v_cache is not None:
-        _like(v_cache, dev, k_cache.dtype, n * block_size * head_dim)
-        _like(v_scale, dev, f32, n)
-    _like(block_tables, dev, i32, bs * width)
-    _like(context_lens, dev, i32, bs)
+        _like(v_cache, dev, code, pool)
+        _like(v_scale, dev, f32, (num_blocks, kv_heads))
+    _like(block_tables, dev, i32, (bs, width))
+    _like(context_lens, dev, i32, (bs,))
     if row_begin is not None:
-        _like(row_begin, dev, i32, bs + 1)
+        _like(row_begin, dev, i32, (bs + 1,))
     return CacheProblem(
         k_cache.data_ptr(), None if v_cache is None else v_cache.data_ptr(), k_scale.data_ptr(),
         None if v_cache is None else v_scale.data_ptr(), block_tables.data_ptr(),
@@ -528,23 +530,24 @@ def cache_workspace(device=None, stream=None):
 
 
 def _torch():
-    """torch's float32, int32 and bfloat16, and the calls that name the current
-    device and its stream's handle (torch is imported on first use)."""
+    """torch's float32, int32 and bfloat16, the calls that name the current device
+    and its stream's handle, and the pools' types (torch is imported on first use)."""
     global _torch_names
     if not _torch_names:
         import torch
 
         _torch_names = (torch.float32, torch.int32, torch.bfloat16, torch._C._cuda_getDevice,
-                        torch._C._cuda_getCurrentRawStream)
+                        torch._C._cuda_getCurrentRawStream,
+                        (torch.float8_e4m3fn, torch.uint8))
     return _torch_names
 
 
-def _like(t, dev: int, dtype, numel: int) -> None:
+def _like(t, dev: int, dtype, shape) -> None:
     """What every operand of a pmqa_cache_* call must be: on the cache's
-    device, of the documented type and size, contiguous."""
-    assert t.get_device() == dev and t.dtype is dtype and t.numel() == numel \
-        and t.is_contiguous(), f"expected a contiguous {dtype} tensor of {numel} elements on " \
-        f"cuda:{dev}, got {tuple(t.shape)} {t.dtype} on {t.device}"
+    device, of the documented type and shape, contiguous."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise AssertionError(f"expected a contiguous {dtype} tensor of shape {tuple(shape)} on the "
+                             f"cache's device ({dev}), got {tuple(t.shape)} {t.dtype} on {t.device}")
 
 
 def _on_stream(fn):
@@ -564,7 +567,9 @@ def _on_stream(fn):
 def _cache_call(name: str, p: CacheProblem, dev: int, stream, ws, *args) -> None:
     """Call a pmqa_cache_* function with device `dev` current, on its current
     stream unless one is given."""
-    _, _, _, current_device, raw_stream = _torch()
+    if dev < 0:
+        raise AssertionError("the pmqa_cache_* calls take cuda tensors")
+    current_device, raw_stream = _torch()[3:5]
     if dev != current_device():
         import torch
 
@@ -572,7 +577,8 @@ def _cache_call(name: str, p: CacheProblem, dev: int, stream, ws, *args) -> None
             return _cache_call(name, p, dev, stream, ws, *args)
     if ws is None:
         ws = cache_workspace(f"cuda:{dev}", stream)
-    assert ws.get_device() == dev and ws.is_contiguous()
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise AssertionError("expected a contiguous workspace on the cache's device")
     rc = getattr(_lib or load(), name)(p, *args, ws.data_ptr(), ws.nbytes,
                                        raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc != PMQA_OK:
@@ -586,9 +592,9 @@ def pmqa_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_tables, co
     cache's blocks, updating the pools and their scales in place."""
     p = make_cache_problem(k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
                            row_begin, k.shape[0], max_rows)
-    dev, bf16, n = k_cache.get_device(), _torch()[2], p.rows * p.kv_heads * p.head_dim
-    _like(k, dev, bf16, n)
-    _like(v, dev, bf16, n)
+    dev, bf16, shape = k_cache.get_device(), _torch()[2], (p.rows, p.kv_heads, p.head_dim)
+    _like(k, dev, bf16, shape)
+    _like(v, dev, bf16, shape)
     _cache_call("pmqa_cache_append", p, dev, stream, ws, k.data_ptr(), v.data_ptr())
 
 
@@ -600,22 +606,21 @@ def pmqa_cache_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, co
     out of q's shape (and fp32 lse [rows, heads] when asked for or given)."""
     import torch
 
-    rows, heads, head_dim = q.shape
+    rows, heads = q.shape[:2]
     p = make_cache_problem(k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
                            row_begin, rows, max_rows)
     dev = k_cache.get_device()
     f32, _, bf16 = _torch()[:3]
-    n = rows * heads * p.head_dim
-    assert head_dim == p.head_dim
-    _like(q, dev, bf16, n)
+    shape = (rows, heads, p.head_dim)
+    _like(q, dev, bf16, shape)
     if out is None:
         out = torch.empty_like(q)
     else:
-        _like(out, dev, bf16, n)
+        _like(out, dev, bf16, shape)
     if lse is None:
         lse = torch.empty((rows, heads), dtype=f32, device=q.device) if want_lse else None
     else:
-        _like(lse, dev, f32, rows * heads)
+        _like(lse, dev, f32, (rows, heads))
     _cache_call("pmqa_cache_attention", p, dev, stream, ws, q.data_ptr(), heads, sm_scale,
                 out.data_ptr(), None if lse is None else lse.data_ptr())
     return out if lse is None else (out, lse)
@@ -630,25 +635,24 @@ def pmqa_cache_weigh(q, k_cache, k_scale, block_tables, context_lens, row_begin,
     log-sum-exp `lse` the attention call returned. Only entries of cached tokens
     are written to mass_out (which may be mass_in); a new one starts as a copy
     of mass_in, or as zeros."""
-    rows, heads, head_dim = q.shape
+    rows, heads = q.shape[:2]
     p = make_cache_problem(k_cache, None, k_scale, None, block_tables, context_lens, row_begin,
                            rows, max_rows)
     dev = k_cache.get_device()
     f32, _, bf16 = _torch()[:3]
-    assert head_dim == p.head_dim
-    _like(q, dev, bf16, rows * heads * head_dim)
-    _like(lse, dev, f32, rows * heads)
-    if mass_out is None:
-        if mass_in is not None:
-            mass_out = mass_in.clone()
-        else:
-            width = mass_width or p.block_size * p.max_blocks_per_seq
-            mass_out = q.new_zeros((p.bs, p.kv_heads, width), dtype=f32)
-    width = mass_out.shape[-1]
-    _like(mass_out, dev, f32, p.bs * p.kv_heads * width)
+    _like(q, dev, bf16, (rows, heads, p.head_dim))
+    _like(lse, dev, f32, (rows, heads))
+    given = mass_in if mass_out is None else mass_out
+    if given is not None and mass_width not in (None, given.shape[-1]):
+        raise AssertionError(f"mass_width {mass_width} beside masses of {given.shape[-1]}")
+    width = given.shape[-1] if given is not None else mass_width or p.block_size * p.max_blocks_per_seq
+    shape = (p.bs, p.kv_heads, width)
     if mass_in is not None:
-        _like(mass_in, dev, f32, p.bs * p.kv_heads * width)
-        assert mass_in.shape[-1] == width
+        _like(mass_in, dev, f32, shape)
+    if mass_out is None:
+        mass_out = q.new_zeros(shape, dtype=f32) if mass_in is None else mass_in.clone()
+    else:
+        _like(mass_out, dev, f32, shape)
     _cache_call("pmqa_cache_weigh", p, dev, stream, ws, q.data_ptr(), heads, sm_scale,
                 lse.data_ptr(), None if mass_in is None else mass_in.data_ptr(),
                 mass_out.data_ptr(), width)
@@ -667,21 +671,21 @@ def pmqa_cache_evict(k_cache, v_cache, k_scale, v_scale, block_tables, context_l
     p = make_cache_problem(k_cache, v_cache, k_scale, v_scale, block_tables, context_lens)
     dev = k_cache.get_device()
     f32, i32 = _torch()[:2]
-    width, pairs = mass.shape[-1], p.bs * p.kv_heads
-    _like(mass, dev, f32, pairs * width)
-    _like(new_tables, dev, i32, p.bs * new_tables.shape[-1])
+    width, pairs = mass.shape[-1], (p.bs, p.kv_heads)
+    _like(mass, dev, f32, (*pairs, width))
+    _like(new_tables, dev, i32, (p.bs, new_tables.shape[-1]))
     if kept is None:
-        kept = torch.empty((p.bs, p.kv_heads, max(keep, 0)), dtype=i32, device=mass.device)
+        kept = torch.empty((*pairs, max(keep, 0)), dtype=i32, device=mass.device)
     else:
-        _like(kept, dev, i32, pairs * keep)
+        _like(kept, dev, i32, (*pairs, keep))
     if lens_out is None:
         lens_out = torch.empty_like(context_lens)
     else:
-        _like(lens_out, dev, i32, p.bs)
+        _like(lens_out, dev, i32, (p.bs,))
     if mass_out is None:
         mass_out = torch.empty_like(mass)
     else:
-        _like(mass_out, dev, f32, pairs * width)
+        _like(mass_out, dev, f32, (*pairs, width))
     _cache_call("pmqa_cache_evict", p, dev, stream, ws, mass.data_ptr(), width, keep, sinks,
                 recent, new_tables.data_ptr(), new_tables.shape[-1], kept.data_ptr(),
                 lens_out.data_ptr(), mass_out.data_ptr())
