@@ -520,12 +520,14 @@ def pmqa_cache_workspace_bytes() -> int:
 
 
 def cache_workspace(device=None, stream=None):
-    """A zero-initialised workspace for the pmqa_cache_* calls."""
+    """A zero-initialised workspace for the pmqa_cache_* calls. With a `stream` the
+    memory is that stream's too: it may be in use on the current one."""
     import torch
 
-    ws = torch.empty(pmqa_cache_workspace_bytes(), dtype=torch.uint8, device=device or "cuda")
-    with torch.cuda.device(ws.device):
-        pmqa_workspace_init(ws, stream=stream)
+    with torch.cuda.stream(stream):
+        ws = torch.empty(pmqa_cache_workspace_bytes(), dtype=torch.uint8, device=device or "cuda")
+        with torch.cuda.device(ws.device):
+            pmqa_workspace_init(ws, stream=stream)
     return ws
 
 

@@ -200,3 +200,20 @@ def test_evict_with_the_largest_keep(cuda_lib):
     want = ref.evict(p, mass, c, 4, 8, new[:, :2])
     for got, w in zip((d[0], d[2], d[1], d[3]), want[3:]):
         assert torch.equal(got.cpu(), w)
+
+
+# ------------------------------------------------------------- a workspace made on a stream
+
+def test_a_workspace_made_on_a_stream_is_that_streams(cuda_lib):
+    """Memory that the current stream still reads is not handed to another stream."""
+    n = cuda_lib.pmqa_cache_workspace_bytes()
+    side = torch.cuda.Stream()
+    x = torch.full((n,), 7, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda._sleep(50_000_000)  # about 25 ms on the current stream
+    y = x + 0
+    del x
+    ws = cuda_lib.cache_workspace(stream=side)
+    torch.cuda.synchronize()
+    assert bool((y == 7).all())
+    assert cuda_lib.pmqa_read_device_status(ws, stream=side) == 0
