@@ -2,6 +2,8 @@
 they are a small part of the outputs, and results with a part lost, counted twice
 or left out lie outside them (mistakes planted in the plain form)."""
 
+import math
+
 import pytest
 import torch
 
@@ -36,9 +38,9 @@ def test_bounds_are_a_small_part_of_the_output(case):
     cb.matches(p, out.to(torch.bfloat16), lse.float())
 
 
-def refused(p, out, lse):
+def refused(p, out, lse, **kw):
     try:
-        cb.matches(p, out.to(torch.bfloat16), lse.float())
+        cb.matches(p, out.to(torch.bfloat16), lse.float(), **kw)
     except AssertionError:
         return True
     return False
@@ -63,3 +65,23 @@ def test_a_lost_part_lies_outside_the_bounds(case):
         p.vc = kept
         assert refused(p, less, lse)
         assert refused(p, 2 * out - less, lse)
+
+
+def test_left_out_tokens():
+    """Tokens of a block that is left out: the others' slots stay what they are."""
+    p = make(([3], [50], 1, 2, 64, 16), seed=33)
+    gone = torch.zeros((1, 64), dtype=torch.bool)
+    gone[0, 16:32] = True
+    out, lse, _, _, _ = cb.attention(p, gone=gone)
+    k, _ = ref.tokens(p.kc, p.ks, p.bt, 0, 50, 16)
+    v, _ = ref.tokens(p.vc, p.vs, p.bt, 0, 50, 16)
+    for j in range(3):
+        seen = [t for t in range(48 + j) if not 16 <= t < 32]
+        for g in range(2):
+            s = (k[0, seen] @ p.q[j, g].double()) * p.sm
+            torch.testing.assert_close(out[j, g], torch.softmax(s, 0) @ v[0, seen])
+            torch.testing.assert_close(lse[j, g], torch.logsumexp(s, 0))
+    # counted with score 0 and no value, as zero-filled tokens would be, they show
+    full = torch.logaddexp(lse, torch.full_like(lse, math.log(16.0)))
+    assert not refused(p, out, lse, gone=gone)
+    assert refused(p, out * (lse - full).exp()[..., None], full, gone=gone)

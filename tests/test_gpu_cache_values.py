@@ -1,10 +1,11 @@
 """Values of the cache operators inside bounds that stay a small part of them."""
 
 import pytest
+import torch
 
 from tests import cache_bounds as cb
 from tests import cache_ref as ref
-from tests.test_gpu_cache import status_is
+from tests.test_gpu_cache import cuda, status_is
 from tests.test_gpu_cache_paths import attend
 
 pytestmark = pytest.mark.gpu
@@ -34,3 +35,26 @@ def test_values_of_long_contexts(cuda_lib, case, flat):
     out, lse = attend(cuda_lib, p, ws=ws)
     status_is(cuda_lib, ws)
     cb.matches(p, out, lse)
+
+
+# ------------------------------------------------------------- blocks left out
+
+@pytest.mark.parametrize("rows,ctx,bad", [
+    ([60, 1], [150, 20], 1),           # many rows, uncut or in few pieces
+    ([50, 40], [3000, 2500], 40),      # cut over the SMs
+    ([33] * 150, [70] * 150, 0),       # more row blocks than SMs
+    ([2, 1], [150, 20], 2),            # few rows
+    ([1], [4000], 60),                 # few rows, cut
+])
+def test_tokens_of_a_bad_block_take_no_part(cuda_lib, rows, ctx, bad):
+    """Their weight is in no sum: not as tokens of score 0 either."""
+    p = ref.make(rows, ctx, kv_heads=2, group=1, head_dim=128, block=32, seed=42, poison=False)
+    ws = cuda_lib.cache_workspace()
+    d = cuda(p)
+    d[4] = d[4].clone()
+    d[4][0, bad] = p.kc.shape[0]
+    gone = torch.zeros((p.bs, p.bt.shape[1] * 32), dtype=torch.bool)
+    gone[0, 32 * bad:32 * bad + 32] = True
+    out, lse = attend(cuda_lib, p, d, ws)
+    status_is(cuda_lib, ws, cuda_lib.PMQA_DEV_BAD_BLOCK_ID)
+    cb.matches(p, out, lse, gone=gone)
