@@ -444,7 +444,10 @@ int pmqa_cache_append(const pmqa_cache_problem *p, const void *k, const void *v,
  * sm_scale must be finite (times log2(e) too). A NaN among a block's values (v) makes that column NaN
  * for every row of the request that the block's other tokens reach, rows that do
  * not see the NaN's token among them; a NaN key reaches only the rows that see it.
- * Requests of more than 32 rows n_i * heads / kv_heads hold their values in units
+ * Requests of more than 32 rows n_i * heads / kv_heads take q as the sum of two 8-bit
+ * terms, exact where a value is at least 2^-13 of its row's largest and off by at
+ * most 2^-21 of that below (fewer rows: exact from 2^-31 on); weigh does the same.
+ * They hold their values in units
  * of the largest block scale met so far, to 2^-31 of it at worst.
  * One kernel launch where block_size * max_blocks_per_seq <= 640, else two, and
  * one or two more where max_rows * heads / kv_heads > 32 (those alone where

@@ -135,6 +135,33 @@ __device__ __forceinline__ uint32_t f32x4_to_e4m3x4(float a, float b, float c, f
     return f32x2_to_e4m3x2(a, b) | (f32x2_to_e4m3x2(c, d) << 16);
 }
 
+// A bf16 value of at most 2^8 as the sum of an e4m3 and an e5m2 value, for products of
+// kind::f8f6f4 (where the two operands may have different types). The first leaves a
+// remainder of at most 8 units of the value's last bit while the value is 2^-6 or more:
+// three bits, which e5m2 has, down to 2^-16. Below, where e4m3's step stays 2^-9,
+// the remainder of at most 2^-10 is off by up to 2^-14. With the largest value of a row
+// scaled into [2^7, 2^8): exact for values from 2^-13 of it on, off by at most 2^-21
+// of it below. (A second e4m3 value of the same cost ends at 2^-9 and 2^-17.)
+__device__ __forceinline__ uint32_t f32x4_to_e5m2x4(float a, float b, float c, float d)
+{
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    return lo | (uint32_t)hi << 16;
+}
+
+__device__ __forceinline__ void split_terms(float a, float b, float c, float d, uint32_t &first, uint32_t &second)
+{
+    first = f32x4_to_e4m3x4(a, b, c, d);
+    float h0, h1, h2, h3;
+    e4m3x2_to_f32x2(first & 0xFFFFu, h0, h1);
+    e4m3x2_to_f32x2(first >> 16, h2, h3);
+    second = f32x4_to_e5m2x4(a - h0, b - h1, c - h2, d - h3);
+}
+
+// Instruction descriptor of kind::f8f6f4, bits 7-9 and 10-12: the type of A and of B.
+constexpr uint32_t kIdescAE5m2 = 1u << 7, kIdescBE5m2 = 1u << 10;
+
 // ------------------------------------------------------------- walk over items
 //
 // Item = (request i, kv head h, row block b, tile t of TILE tokens), in that

@@ -6,10 +6,10 @@
 // j, head g of the group), 256 of them to a CTA in two tiles of 128. With the
 // tokens in tiles of 128:
 //   S = Q K^T    kind::f8f6f4 on the cached codes as they are: q, scaled by a
-//                power of two per row, is the sum of two e4m3 terms, exact for
-//                bf16 values within 2^-10 of their row's largest and off by at
-//                most 2^-18 of it below that; both terms add into one
-//                accumulator, at the cost of one bf16 product;
+//                power of two per row, is the sum of an e4m3 and an e5m2 term,
+//                exact for bf16 values from 2^-13 of their row's largest on and
+//                off by at most 2^-21 of it below that (split_terms); both terms add
+//                into one accumulator, at the cost of one bf16 product;
 //   p = 2^(x - m), x = S ks_t c_row, masked by slot; running m and l per row,
 //                one thread per row; P is written as f16 over the columns that
 //                held S;
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
         const int lim = has ? first_tok + j : 0x7FFFFFFF;  // last slot that the row sees
         float rc;
         {
-            // the row's q as two e4m3 terms, K-major in the 128-byte swizzle
+            // the row's q as two terms, K-major in the 128-byte swizzle
             const uint4 *src = reinterpret_cast<const uint4 *>(a.q + rh * D);
             uint4 u[D / 8];
 #pragma unroll
@@ -586,11 +586,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
                     const float f0 = __uint_as_float(e0 << 16) * up, f1 = __uint_as_float(e0 & 0xFFFF0000u) * up;
                     const float f2 = __uint_as_float(e1 << 16) * up, f3 = __uint_as_float(e1 & 0xFFFF0000u) * up;
                     nan |= f0 != f0 || f1 != f1 || f2 != f2 || f3 != f3;
-                    hi[y] = f32x4_to_e4m3x4(f0, f1, f2, f3);
-                    float h0, h1, h2, h3;
-                    e4m3x2_to_f32x2(hi[y] & 0xFFFFu, h0, h1);
-                    e4m3x2_to_f32x2(hi[y] >> 16, h2, h3);
-                    lw[y] = f32x4_to_e4m3x4(f0 - h0, f1 - h1, f2 - h2, f3 - h3);
+                    split_terms(f0, f1, f2, f3, hi[y], lw[y]);
                 }
                 sts128(qd + sw128(row, k >> 1), hi[0], hi[1], hi[2], hi[3]);
                 sts128(qd + kTileBytes + sw128(row, k >> 1), lw[0], lw[1], lw[2], lw[3]);
@@ -832,7 +828,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
                 const uint64_t ad = sw128_kmajor_desc(qd + (uint32_t)term * kTileBytes);
 #pragma unroll
                 for (int k = 0; k < D / 32; ++k)
-                    umma_e4m3(tmem + (uint32_t)tile * 128u, ad + 2u * k, kd + 2u * k, idq, (term | k) ? 1u : 0u);
+                    umma_e4m3(tmem + (uint32_t)tile * 128u, ad + 2u * k, kd + 2u * k, term ? idq | kIdescAE5m2 : idq,
+                              (term | k) ? 1u : 0u);
             }
             umma_commit(&bar[kBSFull + tile]);
         };

@@ -3,9 +3,10 @@
 // chunk, or of an observation window before an eviction.
 //
 // S^T = K Q^T on the tensor cores (kind::f8f6f4): the cached codes as they are
-// are the M = 128 tokens, q (two e4m3 terms, exact for bf16 values within 2^-10
-// of their row's largest) the N = 128 packed rows R = j * group + g. A thread
-// then owns one token and adds the weights of its 128 columns in registers,
+// are the M = 128 tokens, q (an e4m3 and an e5m2 term, exact for bf16 values from
+// 2^-13 of their row's largest on: split_terms) the N = 128 packed rows
+// R = j * group + g. A thread then owns one token and adds the weights of its 128
+// columns in registers,
 //   w_t = sum_R 2^(S ks_t c_R - lse_R log2 e),
 // so there is no reduction over lanes and no atomic.
 //
@@ -207,11 +208,7 @@ __global__ void __launch_bounds__(kWnThreads, 1) cache_window_kernel(const __gri
                             const uint32_t e0 = (z & 1) ? uu.z : uu.x, e1 = (z & 1) ? uu.w : uu.y;
                             const float f0 = __uint_as_float(e0 << 16) * up, f1 = __uint_as_float(e0 & 0xFFFF0000u) * up;
                             const float f2 = __uint_as_float(e1 << 16) * up, f3 = __uint_as_float(e1 & 0xFFFF0000u) * up;
-                            hi[z] = f32x4_to_e4m3x4(f0, f1, f2, f3);
-                            float h0, h1, h2, h3;
-                            e4m3x2_to_f32x2(hi[z] & 0xFFFFu, h0, h1);
-                            e4m3x2_to_f32x2(hi[z] >> 16, h2, h3);
-                            lw[z] = f32x4_to_e4m3x4(f0 - h0, f1 - h1, f2 - h2, f3 - h3);
+                            split_terms(f0, f1, f2, f3, hi[z], lw[z]);
                         }
                         sts128(qd + wn_sw128(row & 127, k >> 1), hi[0], hi[1], hi[2], hi[3]);
                         sts128(qd + kWnTile + wn_sw128(row & 127, k >> 1), lw[0], lw[1], lw[2], lw[3]);
@@ -353,7 +350,7 @@ __global__ void __launch_bounds__(kWnThreads, 1) cache_window_kernel(const __gri
                                     for (int z = 0; z < D / 16; ++z)
                                         umma_e4m3(tmem + 256u * b + 128u * r, kd + 2u * (z % (D / 32)),
                                                   qd + (uint64_t)((z / (D / 32)) * (kWnTile >> 4)) + 2u * (z % (D / 32)),
-                                                  id, z ? 1u : 0u);
+                                                  z < D / 32 ? id : id | kIdescBE5m2, z ? 1u : 0u);
                                 }
                                 umma_commit(&bar[kWSFull + 2 * b + r]);
                             }

@@ -58,3 +58,42 @@ def test_tokens_of_a_bad_block_take_no_part(cuda_lib, rows, ctx, bad):
     out, lse = attend(cuda_lib, p, d, ws)
     status_is(cuda_lib, ws, cuda_lib.PMQA_DEV_BAD_BLOCK_ID)
     cb.matches(p, out, lse, gone=gone)
+
+
+# ------------------------------------------------------------- queries with a large channel
+
+def large_channel(rows, ctx, D, power, seed):
+    """Queries with one channel of 2^power that meets zeros, the others 1 to 2 with all
+    eight bits of their significands in use, and keys of 1 and -1: every product and
+    sum of products is exact in fp32."""
+    p = ref.make(rows, ctx, kv_heads=2, group=2, head_dim=D, block=16, seed=seed, poison=False)
+    g = p.gen
+    p.kc = torch.where(torch.rand(p.kc.shape, generator=g) < 0.5, 0x38, 0xB8).to(torch.uint8)
+    p.kc[..., 5] = 0
+    p.ks = torch.ones_like(p.ks)
+    sign = torch.where(torch.rand(p.q.shape, generator=g) < 0.5, 1.0, -1.0)
+    q = sign * (128 + torch.randint(0, 128, p.q.shape, generator=g)) / 128.0
+    q[..., 5] = 2.0 ** power
+    p.q = q.to(torch.bfloat16)
+    assert torch.equal(p.q.float(), q)
+    return p
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows", [2, 40])
+@pytest.mark.parametrize("power,split", [(6, 0.0), (10, 0.0), (13, 0.0), (16, 2.0 ** -21)])
+def test_queries_with_a_large_channel(cuda_lib, rows, D, power, split):
+    """Values of 2^-13 of their row's largest and more keep every bit, for many rows as
+    for few; smaller ones are off by 2^-21 of it at most."""
+    p = large_channel([rows, 1], [rows + 70, 40], D, power, seed=43)
+    split = split if rows == 40 else 0.0
+    ws = cuda_lib.cache_workspace()
+    out, lse = attend(cuda_lib, p, ws=ws)
+    cb.matches(p, out, lse, split=split)
+    mass = cuda_lib.pmqa_cache_weigh(p.q.cuda(), *[t.cuda() for t in (p.kc, p.ks, p.bt, p.ctx, p.rb)],
+                                     p.max_rows, p.sm, lse, ws=ws)
+    want, tol = cb.weigh(p, lse.cpu(), torch.zeros(mass.shape), split=split)
+    held = ~torch.isnan(want)
+    over = (mass.double().cpu()[held] - want[held]).abs() - tol[held]
+    assert float(over.max()) <= 0.0, float(over.max())
+    status_is(cuda_lib, ws)
