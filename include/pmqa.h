@@ -447,8 +447,11 @@ int pmqa_cache_append(const pmqa_cache_problem *p, const void *k, const void *v,
  * Requests of more than 32 rows n_i * heads / kv_heads take q as the sum of two 8-bit
  * terms, exact where a value is at least 2^-13 of its row's largest and off by at
  * most 2^-21 of that below (fewer rows: exact from 2^-31 on); weigh does the same.
- * They hold their values in units
- * of the largest block scale met so far, to 2^-31 of it at worst.
+ * They hold their values (code * scale) to 2^-31 of the largest block scale met so
+ * far; by 2^-11 of themselves where two scales' quotient is no power of two. Fewer
+ * rows hold the weight times the scale, to 2^-25 (2^-11 of itself above 2^-14) of the
+ * largest scale among 32 tokens, or of one up to 32 times as large. Value scales
+ * below 1e-36 count as 0.
  * One kernel launch where block_size * max_blocks_per_seq <= 640, else two, and
  * one or two more where max_rows * heads / kv_heads > 32 (those alone where
  * heads / kv_heads > 32).

@@ -14,8 +14,10 @@
 //                one thread per row; P is written as f16 over the columns that
 //                held S;
 //   O += P V     kind::f16 with P from tensor memory and V as f16: the codes
-//                converted (exactly) and scaled by vs_t / vref, vref the largest
-//                block scale so far, so that O needs no factor per token.
+//                times vs_t / vref, vref the largest block scale so far, so that O
+//                needs no factor per token. Power-of-two scales make that exact down
+//                to 2^-30 vref; others, and smaller ones, are multiplied in fp32 and
+//                rounded once, by 2^-11 of the value or 2^-31 of vref.
 // Roles of a CTA's 16 warps: 0-3 and 4-7 are the softmax (and the final output)
 // of the two row tiles, 8-11 convert V, 12 issues the products, 13 and 14 look up
 // the blocks and copy K and V rows (cp.async). While
@@ -57,8 +59,8 @@ constexpr uint32_t kPrOffV = kPrOffRaw + kRawSlots * kTileBytes;          // V f
 constexpr uint32_t kPrOffKs = kPrOffV + kVStages * 2 * kTileBytes;  // [kMeta][128] fp32
 constexpr uint32_t kPrOffVs = kPrOffKs + kMeta * 512;             // [kMeta][128] fp32
 constexpr uint32_t kPrOffTile = kPrOffVs + kMeta * 512;           // [kMeta]: 4 mask words, vfac, vref, 4 bytes: even scales
-constexpr uint32_t kPrOffRed = kPrOffTile + kMeta * 32;           // [2][4] fp32
-constexpr uint32_t kPrOffBar = kPrOffRed + 32;
+constexpr uint32_t kPrOffRed = kPrOffTile + kMeta * 32;           // [2][largest, smallest][4] fp32
+constexpr uint32_t kPrOffBar = kPrOffRed + 64;
 enum {
     kBKFull = 0,                  // [2] K rows, scales, mask landed: 32 cp.async arrivals and lane 0's own
     kBKEmpty = kBKFull + kKStages,  // [2] scores done with the stage (MMA commit), its scales read (4 warps)
@@ -301,6 +303,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r)
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
+}
+
+__device__ __forceinline__ uint32_t scale_f16x2(uint32_t x, float f)
+{
+    return pack_f16x2(__half2float(__ushort_as_half((unsigned short)(x & 0xFFFFu))) * f,
+                      __half2float(__ushort_as_half((unsigned short)(x >> 16))) * f);
 }
 
 // How the scores of a tile are read. kEven: every token counts and each 32 of
@@ -743,22 +751,27 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
             // vref: the largest |scale| so far; and do the warp's 32 tokens share one
             // key scale that is not negative?
             const float kmine = ksp[lt];
-            float vmax = fabsf(vsp[lt]);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                vmax = fmaxf(vmax, __shfl_xor_sync(kFull, vmax, o));
+            // the largest and the smallest scale but 0 of the warp's 32 (a NaN counts as 0), as bits
+            uint32_t vbits = __float_as_uint(vsp[lt]) & 0x7FFFFFFFu;
+            vbits = vbits > 0x7F800000u ? 0u : vbits;
+            const uint32_t top = __reduce_max_sync(kFull, vbits);
+            const uint32_t least = __reduce_min_sync(kFull, vbits ? vbits : 0x7F800000u);
+            const bool pow2 = __all_sync(kFull, (vbits & 0x7FFFFFu) == 0);
             const float klead = __shfl_sync(kFull, kmine, 0);
             const bool even = __all_sync(kFull, kmine >= 0.0f && kmine == klead);
             if (lane == 0) {
-                red[4 * (t & 1) + lw] = vmax;
+                red[8 * (t & 1) + lw] = __uint_as_float(top);
+                red[8 * (t & 1) + 4 + lw] = pow2 ? __uint_as_float(least) : 0.0f;
                 asm volatile("st.shared.u8 [%0], %1;" ::"r"(tb + 24u + (uint32_t)lw), "r"(even ? 1u : 0u) : "memory");
             }
             if (!named_bar_and(1, 128, ok)) {
                 fail();
                 break;
             }
-            const float4 r4 = *reinterpret_cast<const float4 *>(red + 4 * (t & 1));
-            vmax = fmaxf(fmaxf(r4.x, r4.y), fmaxf(r4.z, r4.w));
+            const float4 r4 = *reinterpret_cast<const float4 *>(red + 8 * (t & 1));
+            const float4 s4 = *reinterpret_cast<const float4 *>(red + 8 * (t & 1) + 4);
+            const float vmax = fmaxf(fmaxf(r4.x, r4.y), fmaxf(r4.z, r4.w));
+            const float vmin = fminf(fminf(s4.x, s4.y), fminf(s4.z, s4.w));
             const float vnew = vmax > vref && vmax > 1e-36f ? vmax : vref;
             const float vfac = vnew > vref ? vref / vnew : 1.0f;
             vref = vnew;
@@ -772,33 +785,50 @@ __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __gri
             // value columns take the neighbouring token, which spreads the stores
             // of both column blocks over all banks
             const int ch = lt % CH, flip = D == 128 ? ch >> 2 : 0;
-#pragma unroll
-            for (int k0 = 0; k0 < CH; k0 += 4) {
-                uint4 u[4];
-                float f[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int tok = ((k0 + k) * (128 / CH) + lt / CH) ^ flip;
-                    u[k] = *reinterpret_cast<const uint4 *>(raw + tok * 128 + ch * 16);
-                    f[k] = vsp[tok] * vinv;
+            if (vmin < vref * 0x1p-30f || (__float_as_uint(vref) & 0x7FFFFFu) != 0) {
+                // factors that f16 does not hold (a quotient that is no power of two, or too
+                // small a one): products in fp32, rounded once. The choice is the tile's, the
+                // loop rolled: 0.3 % on 6415 rows of 32 heads (unrolled 1.5 %, a choice per
+                // token 4 to 7 %, for the instructions that are fetched or passed over).
+#pragma unroll 1
+                for (int k = 0; k < 4 * CH; ++k) {
+                    // four codes of a thread's 16, of its k / 4-th token
+                    const int tok = ((k >> 2) * (128 / CH) + lt / CH) ^ flip, col = 16 * ch + 4 * (k & 3);
+                    const float f = vsp[tok] * vinv;
+                    uint32_t lo, hi;
+                    e4m3x4_to_f16x2(*reinterpret_cast<const uint32_t *>(raw + tok * 128 + col), lo, hi);
+                    *reinterpret_cast<uint2 *>(vd + (col >> 6) * kTileBytes + sw128(tok, (col & 63) >> 3) + 2 * (col & 4)) =
+                        make_uint2(scale_f16x2(lo, f), scale_f16x2(hi, f));
                 }
+            } else {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int tok = ((k0 + k) * (128 / CH) + lt / CH) ^ flip;
-                    const uint32_t f2 = pack_f16x2(f[k], f[k]);
-                    uint32_t o[8];
-                    e4m3x4_to_f16x2(u[k].x, o[0], o[1]);
-                    e4m3x4_to_f16x2(u[k].y, o[2], o[3]);
-                    e4m3x4_to_f16x2(u[k].z, o[4], o[5]);
-                    e4m3x4_to_f16x2(u[k].w, o[6], o[7]);
+                for (int k0 = 0; k0 < CH; k0 += 4) {
+                    uint4 u[4];
+                    float f[4];
 #pragma unroll
-                    for (int y = 0; y < 8; ++y)
-                        asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(o[y]) : "r"(f2));
-                    // value columns 16 ch .. 16 ch + 15: chunks 2 ch, 2 ch + 1 of 8 columns each
-                    uint8_t *const blk = vd + (ch >> 2) * kTileBytes;
-                    const int c0 = (2 * ch) & 7;
-                    *reinterpret_cast<uint4 *>(blk + sw128(tok, c0)) = make_uint4(o[0], o[1], o[2], o[3]);
-                    *reinterpret_cast<uint4 *>(blk + sw128(tok, c0 + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+                    for (int k = 0; k < 4; ++k) {
+                        const int tok = ((k0 + k) * (128 / CH) + lt / CH) ^ flip;
+                        u[k] = *reinterpret_cast<const uint4 *>(raw + tok * 128 + ch * 16);
+                        f[k] = vsp[tok] * vinv;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int tok = ((k0 + k) * (128 / CH) + lt / CH) ^ flip;
+                        const uint32_t f2 = pack_f16x2(f[k], f[k]);
+                        uint32_t o[8];
+                        e4m3x4_to_f16x2(u[k].x, o[0], o[1]);
+                        e4m3x4_to_f16x2(u[k].y, o[2], o[3]);
+                        e4m3x4_to_f16x2(u[k].z, o[4], o[5]);
+                        e4m3x4_to_f16x2(u[k].w, o[6], o[7]);
+#pragma unroll
+                        for (int y = 0; y < 8; ++y)
+                            asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(o[y]) : "r"(f2));
+                        // value columns 16 ch .. 16 ch + 15: chunks 2 ch, 2 ch + 1 of 8 columns each
+                        uint8_t *const blk = vd + (ch >> 2) * kTileBytes;
+                        const int c0 = (2 * ch) & 7;
+                        *reinterpret_cast<uint4 *>(blk + sw128(tok, c0)) = make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4 *>(blk + sw128(tok, c0 + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+                    }
                 }
             }
             fence_proxy_async_smem();

@@ -97,3 +97,22 @@ def test_queries_with_a_large_channel(cuda_lib, rows, D, power, split):
     over = (mass.double().cpu()[held] - want[held]).abs() - tol[held]
     assert float(over.max()) <= 0.0, float(over.max())
     status_is(cuda_lib, ws)
+
+
+# ------------------------------------------------------------- scales far apart
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("power", [-12, -20, -25, -28, -32])
+@pytest.mark.parametrize("scales", ["pow2", "any"])
+def test_value_scales_far_apart(cuda_lib, scales, power, D):
+    """The last block's values are 2^-power times as large as the others': rows that do
+    not see it keep theirs, to 2^-31 of the largest scale."""
+    p = ref.make([40], [304], kv_heads=2, group=1, head_dim=D, block=16, seed=44, poison=False,
+                 scales=scales)
+    p.vs[p.bt[0, :18].long()] *= 2.0 ** power
+    ws = cuda_lib.cache_workspace()
+    out, lse = attend(cuda_lib, p, ws=ws)
+    status_is(cuda_lib, ws)
+    want, _, tol, _, _ = cb.attention(p)
+    assert float((tol[:24] / want[:24].abs().mean()).max()) < 0.5  # the bound says something
+    cb.matches(p, out, lse)
