@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     float top = fmaxf(s[0][nt][e], s[0][nt][2 + e]);
-                                            top = fmaxf(top, fmaxf(s[U - 1][nt][e], s[U - 1][nt][2 + e]));
+                    top = fmaxf(top, fmaxf(s[U - 1][nt][e], s[U - 1][nt][2 + e]));
                     exceed |= top > m[nt][e] + kSlack;
                 }
             }
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         float top = fmaxf(s[0][nt][e], s[0][nt][2 + e]);
-                                                    top = fmaxf(top, fmaxf(s[U - 1][nt][e], s[U - 1][nt][2 + e]));
+                        top = fmaxf(top, fmaxf(s[U - 1][nt][e], s[U - 1][nt][2 + e]));
                         top = fmaxf(top, __shfl_xor_sync(kFull, top, 4));
                         top = fmaxf(top, __shfl_xor_sync(kFull, top, 8));
                         top = fmaxf(top, __shfl_xor_sync(kFull, top, 16));

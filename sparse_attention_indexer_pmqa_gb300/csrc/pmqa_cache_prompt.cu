@@ -342,35 +342,29 @@ __device__ __forceinline__ uint64_t pair(float x)
     return r;
 }
 
-// The largest scaled score of this thread's row (128 columns from tS). The
-// loops over column chunks stay rolled: unrolled, the two passes and their
-// three forms outgrow the instruction cache (882 us against 543, before later steps, on 6415 rows of
-// 32 heads).
+// The largest scaled score of this thread's row (128 columns from tS), of tokens with a
+// scale each or masked. The loops over column chunks stay rolled: unrolled, the two passes
+// and their forms outgrow the instruction cache (882 us against 543, before later steps, on
+// 6415 rows of 32 heads).
 template <int HOW>
 __device__ __forceinline__ float row_max(uint32_t tS, const float *ks, uint32_t tb, int lim)
 {
+    static_assert(HOW != kEven, "equal scales are read as single ones");
     float top = -INFINITY;
 #pragma unroll 1
     for (int cc = 0; cc < 4; ++cc) {
         uint32_t r[32];
         tmem_ld32(tS + 32u * cc, r);
         const uint32_t have = HOW == kMasked ? lds32(tb + 4u * cc) : 0u;
-        const float kc = HOW == kEven ? ks[32 * cc] : 0.0f;
         tmem_ld_wait();
         reg_fence_cols<32>(r);
         float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
         for (int z = 0; z < 32; z += 4) {
             float y[4];
-            if constexpr (HOW == kEven) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    y[e] = __uint_as_float(r[z + e]);
-            } else {
-                const float4 k = *reinterpret_cast<const float4 *>(ks + 32 * cc + z);
-                fmul2(y[0], y[1], __uint_as_float(r[z]), __uint_as_float(r[z + 1]), k.x, k.y);
-                fmul2(y[2], y[3], __uint_as_float(r[z + 2]), __uint_as_float(r[z + 3]), k.z, k.w);
-            }
+            const float4 k = *reinterpret_cast<const float4 *>(ks + 32 * cc + z);
+            fmul2(y[0], y[1], __uint_as_float(r[z]), __uint_as_float(r[z + 1]), k.x, k.y);
+            fmul2(y[2], y[3], __uint_as_float(r[z + 2]), __uint_as_float(r[z + 3]), k.z, k.w);
             if constexpr (HOW == kMasked) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -379,8 +373,7 @@ __device__ __forceinline__ float row_max(uint32_t tS, const float *ks, uint32_t 
             t0 = max3(t0, y[0], y[1]);
             t1 = max3(t1, y[2], y[3]);
         }
-        const float t = fmaxf(t0, t1);
-        top = fmaxf(top, HOW == kEven ? t * kc : t);
+        top = fmaxf(top, fmaxf(t0, t1));
     }
     return top;
 }

@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kWnThreads, 1) cache_window_kernel(const __gri
                         if (ok && (r == 0 || two)) {
                             tc_fence_after_sync();
                             const bool whole = __all_sync(kFull, slot <= low);
-// 16 columns are worked on while the next 16 load
+                            // 16 columns are worked on while the next 16 load
                             uint32_t v[2][16];
                             tmem_ld16(tS, v[0]);
 #pragma unroll 1
