@@ -54,12 +54,10 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const __gr
     const View &c = a.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int ut = tid % (32 * WARPS);  // thread within the unit
-    if (!a.single && blockIdx.x == gridDim.x - 1) {
-        // where row_begin falls, the search below may pass a request over: the last CTA,
-        // whose slots are seldom in use, reports for all of them
-        for (int i = tid; i < c.bs; i += kAppendThreads)
-            load_request(c, i, true);
-    }
+    // where row_begin falls, the search below may pass a request over: the last CTA,
+    // whose slots are seldom in use, reports for all of them
+    if (!a.single && blockIdx.x == gridDim.x - 1)
+        report_requests(c);
     const long long u = (long long)blockIdx.x * UNITS + warp / WARPS;
     const long long n_units = (long long)a.slots * c.H * 2;
     if (u >= n_units)

@@ -427,14 +427,6 @@ __device__ __forceinline__ float weights(uint32_t tS, const float *ks, uint32_t 
     return l0 + l1;
 }
 
-// Reports what has to be clamped, for requests without a row block too. Not inlined: the
-// loop in the kernel's body makes it spill (6415 rows of 32 heads: 479 us instead of 414).
-__device__ __noinline__ void report_requests(const View &c)
-{
-    for (int i = threadIdx.x; i < c.bs; i += kPrThreads)
-        load_request(c, i, true);
-}
-
 template <int D>
 __global__ void __launch_bounds__(kPrThreads, 1) cache_prompt_kernel(const __grid_constant__ PromptArgs a)
 {
