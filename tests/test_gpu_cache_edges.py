@@ -217,3 +217,67 @@ def test_a_workspace_made_on_a_stream_is_that_streams(cuda_lib):
     torch.cuda.synchronize()
     assert bool((y == 7).all())
     assert cuda_lib.pmqa_read_device_status(ws, stream=side) == 0
+
+
+# ------------------------------------------------------------- sizes that no other test has
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("P", [1, 5, 7, 100, 1024])
+def test_many_rows_with_blocks_of_any_size(cuda_lib, P, D):
+    """Blocks that end inside a tile, one token long and longer than a tile."""
+    p = ref.make([45, 300, 2], [333, 300, 150], kv_heads=2, group=2, head_dim=D, block=P, seed=57)
+    ws = cuda_lib.cache_workspace()
+    d = cuda(p)
+    out, lse = attend(cuda_lib, p, d, ws)
+    matches(p, out, lse)
+    mass = cuda_lib.pmqa_cache_weigh(p.q.cuda(), d[0], d[2], d[4], d[5], p.rb.cuda(), p.max_rows, p.sm,
+                                     lse, ws=ws).cpu()
+    want, tol = ref.weigh(p, lse.cpu(), torch.zeros(mass.shape))
+    held = ~torch.isnan(want)
+    assert bool(((mass.double() - want).abs() <= tol)[held].all())
+    status_is(cuda_lib, ws)
+
+
+@pytest.mark.parametrize("rows", [1, 3, 80])
+@pytest.mark.parametrize("width", [1, 70, 129])
+def test_masses_narrower_than_the_context(cuda_lib, width, rows):
+    """Tokens past mass_width are weighed by no one and written nowhere."""
+    p = ref.make([rows, 1], [150, 60], kv_heads=2, group=4, head_dim=128, block=16, seed=58)
+    _, lse, _, _ = ref.attention(p)
+    mass = torch.rand((2, 2, width), generator=p.gen)
+    wide = torch.rand((2, 2, 160), generator=p.gen)
+    wide[..., :width] = mass
+    kc, _, ks, _, bt, ctx = cuda(p)
+    args = (p.q.cuda(), kc, ks, bt, ctx, p.rb.cuda(), p.max_rows, p.sm, lse.float().cuda())
+    ws = cuda_lib.cache_workspace()
+    got = cuda_lib.pmqa_cache_weigh(*args, mass.cuda(), ws=ws)
+    full = cuda_lib.pmqa_cache_weigh(*args, wide.cuda(), ws=ws)
+    assert torch.equal(got, full[..., :width])
+    status_is(cuda_lib, ws)
+
+
+@pytest.mark.parametrize("H,G", [(40, 1), (1, 24), (16, 8)])
+def test_head_counts(cuda_lib, H, G):
+    p = ref.make([1, 60, 3], [200, 140, 9], kv_heads=H, group=G, head_dim=64, block=32, seed=59)
+    ws = cuda_lib.cache_workspace()
+    out, lse = attend(cuda_lib, p, ws=ws)
+    matches(p, out, lse)
+    status_is(cuda_lib, ws)
+
+
+def test_rows_of_no_request_may_hold_anything(cuda_lib):
+    """NaN queries and new tokens in front of, between and behind the requests' rows."""
+    p = ref.make([2, 50], [80, 90], kv_heads=2, group=4, head_dim=128, block=16, seed=60, lead=5,
+                 tail=6, poison=False)
+    for t in (p.q, p.k_new, p.v_new):
+        t[:5], t[57:] = math.nan, math.nan
+    want = ref.append(p)
+    d = cuda(p)
+    ws = cuda_lib.cache_workspace()
+    cuda_lib.pmqa_cache_append(p.k_new.cuda(), p.v_new.cuda(), *d, p.rb.cuda(), 50, ws=ws)
+    for g, w in zip((d[0], d[2], d[1], d[3]), want):
+        assert torch.equal(g.cpu(), w)
+    p.kc, p.ks, p.vc, p.vs = want
+    out, lse = attend(cuda_lib, p, d, ws)
+    matches(p, out, lse)
+    status_is(cuda_lib, ws)
