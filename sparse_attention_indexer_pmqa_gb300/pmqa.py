@@ -495,11 +495,10 @@ def make_cache_problem(k_cache, v_cache, k_scale, v_scale, block_tables, context
     num_blocks, kv_heads, block_size, head_dim = pool = k_cache.shape
     bs, width = block_tables.shape
     dev = k_cache.get_device()
-    f32, i32 = _torch()[:2]
+    f32, i32, _, _, _, codes = _torch()
     code = k_cache.dtype
-    if code not in _torch()[5]:
-        raise AssertionError(f"expected float8_e4m3fn (or uint8) pools, got {code}")
-    _like(k_cache, dev, code, pool)
+    if code not in codes or not k_cache.is_contiguous():
+        raise AssertionError(f"expected contiguous float8_e4m3fn (or uint8) pools, got {code}")
     _like(k_scale, dev, f32, (num_blocks, kv_heads))
     if v_cache is not None:
         _like(v_cache, dev, code, pool)

@@ -81,6 +81,7 @@ def test_binding_refuses_other_types_and_shapes(lib, call):
     values = call != "weigh"
     for t in (torch.float8_e5m2, torch.int8, torch.bool):
         refuses("float8_e4m3fn", k_cache=p.kc.view(t), **(dict(v_cache=p.vc.view(t)) if values else {}))
+    refuses("contiguous", k_cache=p.kc.transpose(1, 2))
     refuses("shape", k_scale=p.ks.reshape(2, -1).contiguous())
     refuses("shape", block_tables=p.bt.reshape(1, -1))
     refuses("shape", context_lens=p.ctx[:1])
