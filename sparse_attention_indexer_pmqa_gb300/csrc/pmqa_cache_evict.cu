@@ -15,14 +15,16 @@
 //
 // Move. A unit (request, head, new block, pool) gathers its rows through the
 // kept list and the old table, takes the largest |code * scale| for the new
-// block's power-of-two scale, and writes the codes rounded to it. Bound by
-// HBM: 2 D bytes in and out per kept token and head.
+// block's power-of-two scale, and writes the codes rounded to it: 2 D bytes in
+// and out per kept token and head.
 //
-// 16 requests of 2 to 64 k tokens and 8 kv heads cut to 4096 tokens: selection 55
-// us (of a CTA's 27: 9 for the masses and the first histogram, 10 for the other
-// passes and their joins, 8 for the places; smaller CTAs, two of them per SM, take
-// 1.1 to 1.4 times as long), the move 25 us behind it. One request of 1500 tokens:
-// 12 and 9 us.
+// 16 requests of 2 to 64 k tokens and 8 kv heads cut to 4096 tokens take 115 us back to
+// back. The selection takes 57 us in one cold launch (of a CTA's 27: 9 for the masses and
+// the first histogram, 10 for the other passes and their joins, 8 for the places; smaller
+// CTAs, two of them per SM, take 1.1 to 1.4 times as long), bound by the instructions and
+// latencies of its passes at 56 % of the issue slots. The move takes 65 us at 3.5 TB/s:
+// the look-ups and conversions of a row bind it, at 87 % of the issue slots. One request of
+// 1500 tokens: 13.5 us back to back.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -454,8 +456,8 @@ cudaError_t launch_evict(const EvictCall &q, int sms, cudaStream_t st)
                       (pairs * cs <= sms && q.width > (long long)cs * 4096)))
         cs *= 2;
     a.cs = cs;
-    // more CTAs than SMs: long requests start first (the batch above: 55 us instead of
-    // 70), unless ranking them would take longer than it gains
+    // more CTAs than SMs: long requests start first (selection of the batch above: 55 us
+    // instead of 70), unless ranking them would take longer than it gains
     a.ranked = pairs * cs > sms && q.c.bs <= 128;
     const long long chunk = ((std::min<long long>(q.width, 0x7FFFFF00ll) + cs - 1) / cs + 1023) & ~1023ll;
     a.key_cap = (int)std::min<long long>(chunk, kKeysMax);

@@ -26,8 +26,8 @@
 // Bound by the tensor cores: 4 D flops per visible (row, head, token) at the
 // bf16 rate, 512 cycles per 128 x 128 x 128 product and tile against about 4.2
 // issue slots per score, 1100 cycles for both tiles. 6415 rows of 32 heads over 8
-// behind 2 to 8 k tokens take 414 us, 950 TFLOP/s (49 % of the measured bf16 rate;
-// the tensor pipe is active 45 % of the time): the rest are the gaps between a
+// behind 2 to 8 k tokens take 415 us, 950 TFLOP/s (49 % of the measured bf16 rate;
+// the tensor pipe is active 43 % of the time): the rest are the gaps between a
 // tile's softmax and its products, instruction fetches (the code is larger than
 // the innermost cache) and the uneven lengths of the items.
 //

@@ -12,14 +12,13 @@
 //
 // A CTA keeps 256 packed rows of one (request, kv head) as operands and streams
 // token tiles past them; more rows are further rounds over the same tiles. Tiles
-// of all requests are split evenly over the CTAs, weighted by their rounds. Bound
-// by the tensor cores (D / 32 * 2 products of 66 cycles per tile and 128 rows)
-// and the exponentials (one per token and row, about 3.5 issue slots), 1050 and
-// 900 cycles a tile of 256 rows; four warpgroups hide the latencies. Windows of 64
-// rows of 4 requests of 16 to 32 k tokens (32 query heads over 8) take 74 us, 34 % of
-// the measured bf16 rate counted for one product: a row tile's scores, sums and
-// hand-back follow one another, and four warps a scheduler overlap them at 44 % of
-// the issue slots. K comes row by row: tensor copies
+// of all requests are split evenly over the CTAs, weighted by their rounds. A tile of
+// 256 rows takes about 3200 cycles: its products 1050 (D / 32 * 2 of 66 cycles per 128
+// rows), the weights 1560 issue slots of each scheduler (6.1 instructions a score and
+// lane, all of the kernel's counted). Windows of 64 rows of 4 requests of 16 to 32 k
+// tokens (32 query heads over 8) take 75 us, 33 % of the measured bf16 rate counted for
+// one product: a row tile's scores, sums and hand-back follow one another, and four warps
+// a scheduler overlap them at 49 % of the issue slots. K comes row by row: tensor copies
 // of whole blocks were no faster (89 us against 86).
 #include <algorithm>
 #include <cmath>
