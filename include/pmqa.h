@@ -391,7 +391,8 @@ int pmqa_sparse_mla_merge(const void *outs, const float *lses, int32_t parts, in
  * not attended to or weighed, zeros where evict would have moved them).
  *
  * Every call takes a workspace of pmqa_cache_workspace_bytes() bytes, 256-byte
- * aligned, its status word zero before the first use (pmqa_workspace_init).
+ * aligned, its status word zero before the first use (pmqa_workspace_init). Outputs
+ * overlap no input and no other output unless a call says so.
  */
 typedef struct pmqa_cache_problem {
     void *k_cache;
@@ -441,7 +442,8 @@ int pmqa_cache_append(const pmqa_cache_problem *p, const void *k, const void *v,
  *   lse  fp32 [rows, heads] or NULL
  * heads must be a multiple of kv_heads, at most 128 times kv_heads, and
  * max_rows * heads < 2^31. A row that sees no slot gives out = 0 and lse = -inf.
- * sm_scale must be finite (times log2(e) too). A NaN among a block's values (v) makes that column NaN
+ * sm_scale must be finite (times log2(e) too). A row of q with an infinite or NaN value
+ * gives NaN. A NaN among a block's values (v) makes that column NaN
  * for every row of the request that the block's other tokens reach, rows that do
  * not see the NaN's token among them; a NaN key reaches only the rows that see it.
  * Requests of more than 32 rows n_i * heads / kv_heads take q as the sum of two 8-bit

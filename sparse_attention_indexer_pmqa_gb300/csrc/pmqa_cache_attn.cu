@@ -315,7 +315,8 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::kOcc)
                     for (int k = 0; k < KS; ++k)
                         qsm[(nt * KS + k) * 32] = make_uint2(qb[0][k][0], qb[0][k][1]);
                 }
-                const float mine = a.scale_log2 * down;
+                // an infinite value would leave its row the tokens of score -inf: NaN instead
+                const float mine = top < INFINITY ? a.scale_log2 * down : __int_as_float(0x7FFFFFFF);
                 constexpr auto at = [](int k) { return Sh::kQShared ? 0 : k; };
                 rc[at(nt)][0] = __shfl_sync(kFull, mine, 8 * t4);
                 rc[at(nt)][1] = __shfl_sync(kFull, mine, 8 * t4 + 4);

@@ -201,7 +201,8 @@ __global__ void __launch_bounds__(kWeighThreads, 3)
                     qb[nt][(k >> 1) * 4 + (k & 1) * 2 + (z >> 1)][z & 1] = pack_f16x2(lo, hi);
                 }
             }
-            const float mine = a.scale_log2 * down;
+            // an infinite value would leave its row the tokens of score -inf: NaN instead
+            const float mine = top < INFINITY ? a.scale_log2 * down : __int_as_float(0x7FFFFFFF);
             rc[nt][0] = __shfl_sync(kFull, mine, 8 * t4);
             rc[nt][1] = __shfl_sync(kFull, mine, 8 * t4 + 4);
 #pragma unroll

@@ -281,3 +281,31 @@ def test_rows_of_no_request_may_hold_anything(cuda_lib):
     out, lse = attend(cuda_lib, p, d, ws)
     matches(p, out, lse)
     status_is(cuda_lib, ws)
+
+
+# ------------------------------------------------------------- infinite queries
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows,G", [(1, 4), (3, 8), (40, 1)])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_an_infinite_query_makes_its_row_nan(cuda_lib, bad, rows, G, D):
+    """For few rows as for many, also where every score would be -inf; no other row changes."""
+    p = ref.make([rows, 1], [90, 40], kv_heads=2, group=G, head_dim=D, block=16, seed=61, poison=False)
+    p.kc[..., 7] = 0xB8  # -1 for every token
+    ws = cuda_lib.cache_workspace()
+    d = cuda(p)
+    out, lse = attend(cuda_lib, p, d, ws)
+    args = (d[0], d[2], d[4], d[5], p.rb.cuda(), p.max_rows, p.sm)
+    mass = cuda_lib.pmqa_cache_weigh(p.q.cuda(), *args, lse, ws=ws)
+    j = rows - 1
+    p.q[j, 0, 7] = bad
+    got, got_l = attend(cuda_lib, p, d, ws)
+    assert bool(torch.isnan(got[j, 0]).all()) and bool(torch.isnan(got_l[j, 0]))
+    same = torch.ones(p.q.shape[:2], dtype=torch.bool)
+    same[j, 0] = False
+    assert torch.equal(got.cpu()[same], out.cpu()[same])
+    assert torch.equal(got_l.cpu()[same], lse.cpu()[same])
+    weighed = cuda_lib.pmqa_cache_weigh(p.q.cuda(), *args, lse, ws=ws)
+    assert bool(torch.isnan(weighed[0, 0, :90]).all())
+    assert torch.equal(weighed[0, 1], mass[0, 1]) and torch.equal(weighed[1], mass[1])
+    status_is(cuda_lib, ws)
