@@ -505,6 +505,238 @@ int pmqa_cache_evict(const pmqa_cache_problem *p, const float *mass, int64_t mas
                      void *ws, size_t ws_bytes, pmqa_stream_t stream);
 
 /*
+ * Around the sparse-MLA step: what rotates queries and keys, what writes the
+ * indexer's cache and the latent cache with the step's queries beside them, what
+ * gives cached indexer keys back, and the attention that reads all of a latent
+ * cache. The source pages start from caches and queries that exist; these calls
+ * make them from a model's projections (bf16).
+ *
+ * Rows of a step, and where their tokens lie in a paged cache of num_blocks
+ * blocks of block_size tokens:
+ *   block_tables  int32 [bs, max_blocks_per_seq], row-major
+ *   context_lens  int32 [bs]: ctx_i, tokens of request i, this step's included
+ *   row_begin     int32 [bs + 1], not decreasing, within [0, rows]: request i has
+ *                 the n_i = row_begin[i + 1] - row_begin[i] <= max_rows rows from
+ *                 row_begin[i] on; its row j is the token at slot ctx_i - n_i + j.
+ *                 Rows of no request are neither read nor written
+ * bs * max_blocks_per_seq < 2^31 and num_blocks * block_size < 2^32 - 1
+ * (PMQA_ERR_UNSUPPORTED otherwise). Lengths that break the rules, and rows whose
+ * slot is negative or behind the table's last, set PMQA_DEV_BAD_CONTEXT; a table
+ * entry outside [0, num_blocks) sets PMQA_DEV_BAD_BLOCK_ID.
+ */
+typedef struct pmqa_paged_rows {
+    const int32_t *block_tables;
+    const int32_t *context_lens;
+    const int32_t *row_begin;
+    int32_t bs;
+    int32_t block_size;
+    int32_t max_blocks_per_seq;
+    int32_t rows;
+    int32_t max_rows;
+    int64_t num_blocks;
+} pmqa_paged_rows;
+
+/*
+ * Rotary positions. Of each head the values begin .. begin + dim are rotated in
+ * dim / 2 pairs: pair i is (x_i, x_{i + dim/2}), or (x_{2i}, x_{2i+1}) with
+ * `interleaved`, and with theta = position * inv_freq[i]
+ *   a' = scale * (a cos theta - b sin theta),  b' = scale * (b cos theta + a sin theta)
+ * The angle is formed modulo a turn in 64-bit fixed point: no accuracy is lost at
+ * far positions. Negative positions turn back.
+ *   inv_freq   fp64 [dim / 2], device: radians per position (pmqa_rope_frequencies)
+ *   positions  int32 [rows], or NULL where a call has slots: the row's slot
+ * dim a multiple of 16 (0: nothing is rotated, the pointers are not used), begin a
+ * multiple of 8, begin + dim at most the head's width, scale finite.
+ */
+typedef struct pmqa_rotary {
+    const double *inv_freq;
+    const int32_t *positions;
+    int32_t dim;
+    int32_t begin;
+    int32_t interleaved;
+    float scale;
+} pmqa_rotary;
+
+/*
+ * Frequencies base^(-2 i / dim), i < dim / 2, for contexts `factor` (>= 1) times as
+ * long as the `trained` positions, written to host memory, and the scale that
+ * belongs to them:
+ *   PMQA_ROPE_PLAIN   as they are (factor and trained unused); scale 1
+ *   PMQA_ROPE_LINEAR  all divided by factor; scale 1
+ *   PMQA_ROPE_PARTS   divided where a pair turns fewer than slow_turns times over the
+ *                     trained positions, kept where more than fast_turns times, and
+ *                     between the two weighted linearly in i (the ends rounded
+ *                     outwards to whole i); scale 0.1 ln(factor) + 1
+ * A host function: no device work. dim even and positive, base > 1; for PARTS
+ * trained >= 1 and 0 < slow_turns < fast_turns.
+ */
+enum { PMQA_ROPE_PLAIN = 0, PMQA_ROPE_LINEAR = 1, PMQA_ROPE_PARTS = 2 };
+int pmqa_rope_frequencies(int32_t dim, double base, int kind, double factor, double trained,
+                          double slow_turns, double fast_turns, double *inv_freq, float *scale);
+
+/*
+ * Heads of bf16 values to rotate: element d of head h of row r at
+ * x + r * x_row + h * x_head + d (strides in elements, multiples of 8), the result
+ * at out likewise; both 16-byte aligned. out may be x (with the same strides: the
+ * values outside the rotated part are then not touched), and overlaps it
+ * otherwise nowhere; two results never share an element.
+ */
+typedef struct pmqa_heads {
+    const void *x;
+    void *out;
+    int64_t x_row;
+    int64_t x_head;
+    int64_t out_row;
+    int64_t out_head;
+    int32_t heads;
+    int32_t head_dim;
+} pmqa_heads;
+
+/*
+ * Rotate the heads of a, and of b unless NULL (queries and keys of one step), at
+ * rotary->positions; values outside the rotated part are copied. Products and
+ * sums in fp32, one rounding to bf16. head_dim a multiple of 8, at most 1024. One
+ * kernel launch.
+ */
+int pmqa_rope(const pmqa_rotary *rotary, int32_t rows, const pmqa_heads *a, const pmqa_heads *b,
+              pmqa_stream_t stream);
+
+/*
+ * Normalisation of a row before it is rotated or quantised, in fp32:
+ *   PMQA_NORM_LAYER  (x - mean) / sqrt(var + eps)     PMQA_NORM_RMS  x / sqrt(mean(x^2) + eps)
+ * times weight, plus bias (fp32, 16-byte aligned, of the row's width, NULL for 1 and
+ * 0; unused with PMQA_NORM_NONE). eps >= 0 and finite.
+ */
+enum { PMQA_NORM_NONE = 0, PMQA_NORM_LAYER = 1, PMQA_NORM_RMS = 2 };
+typedef struct pmqa_norm {
+    int32_t kind;
+    float eps;
+    const float *weight;
+    const float *bias;
+} pmqa_norm;
+
+/*
+ * The indexer's inputs of a step, from the projections.
+ *   keys     k: bf16 [rows, 128], row r at k + r * k_row. Normalised (norm),
+ *            rotated, and written to the row's slot of kv_cache (pmqa_problem) as 128
+ *            codes rne(k' / s) and the fp32 scale s = max(a, 2^-100) / 448, a the
+ *            largest finite |k'|; infinite values saturate, NaN stays NaN
+ *   queries  q: bf16 [rows, heads, 128], head h of row r at q + r * q_row + h * q_head;
+ *            rotated and quantised alike, each head with its own scale s, which goes
+ *            into the head's weight:
+ *              weights_out[r][h] = weights[r][h] * s * weight_scale
+ *            so that q_out and weights_out are what pmqa_logits, pmqa_logits_topk and
+ *            pmqa_mqa_logits take. weights: fp32 (bf16 with weights_bf16) [rows,
+ *            heads], row r at weights + r * weights_row
+ *   q_out    fp8 [rows, heads, 128], weights_out fp32 [rows, heads]
+ * k or q may be NULL: then there is no key to write, or there are no queries (and
+ * weights, q_out and weights_out are not used). k, q and their strides: 16-byte
+ * aligned, multiples of 8 elements; q_out 8-byte aligned. weights_out may be
+ * weights (fp32, weights_row = heads); outputs overlap nothing else.
+ */
+typedef struct pmqa_index_rows {
+    const void *k;
+    const void *q;
+    const void *weights;
+    void *q_out;
+    float *weights_out;
+    int64_t k_row;
+    int64_t q_row;
+    int64_t q_head;
+    int64_t weights_row;
+    int32_t heads;
+    int32_t weights_bf16;
+    float weight_scale;
+} pmqa_index_rows;
+
+/*
+ * kv_cache: uint8 [num_blocks, block_size, 132], 4-byte aligned. A slot that
+ * receives a key belongs to one request only; other slots are left as they were.
+ * Rows past their request's first max_rows are not processed; a row without a slot
+ * writes no key. norm and rotary may be NULL (none). ws: any workspace of this
+ * library (256 bytes are enough); only its status word is used. One kernel launch.
+ */
+int pmqa_index_append(const pmqa_paged_rows *p, void *kv_cache, const pmqa_index_rows *x,
+                      const pmqa_norm *norm, const pmqa_rotary *rotary, void *ws, size_t ws_bytes,
+                      pmqa_stream_t stream);
+
+/*
+ * Cached indexer keys as contiguous rows, the form that pmqa_mqa_logits takes: row
+ * row_begin[i] + j is the token at slot start[i] + j of request i (start: int32
+ * [bs], or NULL for zeros); p->context_lens and p->max_rows are not used, rows of no
+ * request are left as they were, rows without a slot or with a bad table entry give
+ * zeros (a code and a scale of 0).
+ *   k        fp8 [rows, 128], 16-byte aligned
+ *   k_scale  fp32 [rows]
+ * One kernel launch; ws as for pmqa_index_append.
+ */
+int pmqa_index_read(const pmqa_paged_rows *p, const void *kv_cache, const int32_t *start, void *k,
+                    float *k_scale, void *ws, size_t ws_bytes, pmqa_stream_t stream);
+
+/*
+ * The latent rows and queries of a step, in the form of pmqa_sparse_mla_decode and
+ * pmqa_latent_attention: a row is 512 latent values and 64 rotary ones.
+ *   keys     c: bf16 [rows, 512] (row r at c + r * c_row), normalised (norm), and k_pe:
+ *            bf16 [rows, 64] (stride pe_row), rotated; written to the row's slot of
+ *            the latent cache as rne(x / kv_scale), saturated at 448 (NaN stays NaN)
+ *   queries  q_c: bf16 [rows, heads, 512] (the query carried into the latent space)
+ *            and q_pe: bf16 [rows, heads, 64], rotated; q_out: fp8 [rows, heads, 576],
+ *            rne(x / q_scale), saturated
+ * (x / scale is x times the scale's fp32 reciprocal.) c or q_c may be NULL, as in
+ * pmqa_index_append. Strides in elements, multiples of 8; inputs 16-byte, outputs
+ * 8-byte aligned; the scales finite, with finite reciprocals.
+ */
+typedef struct pmqa_latent_rows {
+    const void *c;
+    const void *k_pe;
+    const void *q_c;
+    const void *q_pe;
+    void *q_out;
+    int64_t c_row;
+    int64_t pe_row;
+    int64_t q_c_row;
+    int64_t q_c_head;
+    int64_t q_pe_row;
+    int64_t q_pe_head;
+    int32_t heads;
+    float kv_scale;
+    float q_scale;
+} pmqa_latent_rows;
+
+/* kv_cache: fp8 [num_blocks, block_size, 576], 8-byte aligned. The rest as for
+   pmqa_index_append. */
+int pmqa_latent_append(const pmqa_paged_rows *p, void *kv_cache, const pmqa_latent_rows *x,
+                       const pmqa_norm *norm, const pmqa_rotary *rotary, void *ws, size_t ws_bytes,
+                       pmqa_stream_t stream);
+
+/* About 41 MB, whatever the problem. */
+size_t pmqa_latent_workspace_bytes(void);
+
+/*
+ * Attention of every row to all the cached tokens that it sees, the slots t <=
+ * ctx_i - n_i + j: the dense form of pmqa_sparse_mla_decode, for any number of
+ * heads and for prompts.
+ *   s_t = sm_scale * (q_scale * q_h) . (kv_scale * kv_t),  out = sum_t softmax(s)_t v_t,
+ *   v_t = kv_scale * kv_t[0..511],  lse = ln sum_t exp(s_t)
+ *   q         fp8 e4m3fn [rows, heads, 576], 16-byte aligned
+ *   kv_cache  fp8 e4m3fn [num_blocks, block_size, 576], 16-byte aligned
+ *   out       bf16 [rows, heads, 512], 16-byte aligned; lse fp32 [rows, heads] or NULL
+ * heads 1 to 128, rows * heads < 2^31, |sm_scale * q_scale * kv_scale| * log2(e) at
+ * most 1e20 (PMQA_ERR_UNSUPPORTED otherwise); all of them finite. A row that sees no token gives out = 0 and
+ * lse = -inf; tokens behind a bad table entry are not attended to. A NaN among a
+ * token's values makes the rows that see it NaN, and no other row.
+ * The weights are held as two fp8 terms, to 2^-8 of each and 2^-14 of the row's
+ * largest (2^-10 of 2^4); they are summed in fp32, unrounded.
+ * ws: pmqa_latent_workspace_bytes() bytes, 256-byte aligned, its status word zero
+ * before the first use (pmqa_workspace_init). One kernel launch where block_size *
+ * max_blocks_per_seq <= 512, else two. Every sum is formed in one order: equal
+ * calls give equal bits.
+ */
+int pmqa_latent_attention(const pmqa_paged_rows *p, const void *q, const void *kv_cache,
+                          int32_t heads, float q_scale, float kv_scale, float sm_scale, void *out,
+                          float *lse, void *ws, size_t ws_bytes, pmqa_stream_t stream);
+
+/*
  * Measurement aid beside the decode path (computes nothing of the method): reads
  * the rows rows[0..n) of a pool of fixed-pitch rows, each as its 16-byte aligned
  * window (144 bytes for row_pitch 132, the token row of the KV cache; 576 bytes

@@ -36,6 +36,10 @@ def _sources():
     units = [("pmqa_api", os.path.join(CSRC, "pmqa_api.cu"), []),
              ("pmqa_noalloc", os.path.join(CSRC, "pmqa_noalloc.cu"), []),
              ("pmqa_mla", os.path.join(CSRC, "pmqa_mla.cu"), []),
+             ("pmqa_rope", os.path.join(CSRC, "pmqa_rope.cu"), []),
+             ("pmqa_index_rows", os.path.join(CSRC, "pmqa_index_rows.cu"), []),
+             ("pmqa_latent_rows", os.path.join(CSRC, "pmqa_latent_rows.cu"), []),
+             ("pmqa_latent_attn", os.path.join(CSRC, "pmqa_latent_attn.cu"), []),
              ("pmqa_gather_probe", os.path.join(CSRC, "pmqa_gather_probe.cu"), [])]
     for name in ("", "_append", "_attn", "_prompt", "_weigh", "_window", "_evict"):
         units.append((f"pmqa_cache{name}", os.path.join(CSRC, f"pmqa_cache{name}.cu"), []))

@@ -11,17 +11,6 @@ using namespace pmqa::cache;
 
 namespace {
 
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// `an` bytes from a and `bn` from b share some
-bool overlap(const void *a, long long an, const void *b, long long bn)
-{
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + (unsigned long long)bn && y < x + (unsigned long long)an;
-}
-
-bool missing(const void *p, uintptr_t a) { return !p || !aligned(p, a); }
-
 enum { kNeedRows = 1, kNeedValues = 2 };
 
 // Sizes first, then what is out of the kernels' range, then (when there is
@@ -88,32 +77,6 @@ View view(const pmqa_cache_problem *p, void *ws)
     c.status = static_cast<uint32_t *>(ws);
     return c;
 }
-
-// SMs of the current device (looked up once per device: a property of it).
-int sm_count(int *n)
-{
-    static std::atomic<int> known[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess)
-        return PMQA_ERR_CUDA;
-    *n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
-    if (*n > 0)
-        return PMQA_OK;
-    if (cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return PMQA_ERR_CUDA;
-    if (dev < 64)
-        known[dev].store(*n, std::memory_order_relaxed);
-    return PMQA_OK;
-}
-
-int code_of(cudaError_t e)
-{
-    return e == cudaSuccess                    ? PMQA_OK
-           : e == cudaErrorInvalidConfiguration ? PMQA_ERR_UNSUPPORTED
-                                                : PMQA_ERR_CUDA;
-}
-
-cudaStream_t cuda(pmqa_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
 }  // namespace
 

@@ -1,5 +1,6 @@
-// pmqa_cache_host.cuh -- host side of the cache operators: the calls that the
-// C ABI hands to the kernels' translation units.
+// pmqa_cache_host.cuh -- host side of the cache operators: argument checks and
+// launch helpers (shared with the calls on paged rows), and the calls that the C
+// ABI hands to the kernels' translation units.
 #pragma once
 
 #include <atomic>
@@ -8,6 +9,45 @@
 
 namespace pmqa {
 namespace cache {
+
+// ------------------------------------------------------------- arguments
+
+inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// `an` bytes from a and `bn` from b share some
+inline bool overlap(const void *a, long long an, const void *b, long long bn)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + (unsigned long long)bn && y < x + (unsigned long long)an;
+}
+
+inline bool missing(const void *p, uintptr_t a) { return !p || !aligned(p, a); }
+
+// SMs of the current device (looked up once per device: a property of it).
+inline int sm_count(int *n)
+{
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess)
+        return PMQA_ERR_CUDA;
+    *n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (*n > 0)
+        return PMQA_OK;
+    if (cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return PMQA_ERR_CUDA;
+    if (dev < 64)
+        known[dev].store(*n, std::memory_order_relaxed);
+    return PMQA_OK;
+}
+
+inline int code_of(cudaError_t e)
+{
+    return e == cudaSuccess                    ? PMQA_OK
+           : e == cudaErrorInvalidConfiguration ? PMQA_ERR_UNSUPPORTED
+                                                : PMQA_ERR_CUDA;
+}
+
+inline cudaStream_t cuda(pmqa_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
 // The kernel's shared-memory limit, raised once per device and kernel (a
 // property of the loaded code; setting it costs several microseconds of host

@@ -1,0 +1,322 @@
+// pmqa_index_rows.cu -- the indexer's cache written and read back:
+// pmqa_index_append, pmqa_index_read.
+//
+// Append: per row one key (layer or RMS norm, rotary, one fp32 scale, 132 bytes into
+// the row's slot) and `heads` queries (rotary, a scale each, which goes into the
+// head's weight). Bound by memory: 384 bytes a query head, about 30 instructions of
+// half a warp. Half a warp holds one vector of 128 values, eight a lane (16-byte
+// loads); rotated pairs meet by shuffles of the packed inputs. A CTA takes one row, or
+// four where rows are many, and forms their angles once for all heads.
+//
+// Read: a warp moves 32 rows (8 where there are few), whose places its lanes look up;
+// rows of 132 bytes are aligned to 4 bytes only, so a lane moves one word of each row.
+#include <algorithm>
+
+#include "pmqa_paged.cuh"
+
+namespace pmqa {
+namespace paged {
+
+constexpr int kDimI = 128;       // values of a key or of a query head
+constexpr int kRowI = 132;       // bytes of a cached row
+constexpr int kIndexThreads = 256;
+constexpr float kLeast = 0x1p-100f;
+
+struct IndexArgs {
+    View c;
+    Rotary r;
+    Norm n;
+    uint8_t *kv;
+    const uint16_t *k, *q;
+    const void *w;
+    uint8_t *q_out;
+    float *w_out;
+    long long k_row, q_row, q_head, w_row;
+    int heads, w_bf16;
+    float w_scale;
+};
+
+__device__ __forceinline__ float half_sum(uint32_t mask, float x)
+{
+#pragma unroll
+    for (int k = 8; k > 0; k >>= 1)
+        x += __shfl_xor_sync(mask, x, k);
+    return x;
+}
+
+__device__ __forceinline__ float half_max(uint32_t mask, float x)
+{
+#pragma unroll
+    for (int k = 8; k > 0; k >>= 1)
+        x = fmaxf(x, __shfl_xor_sync(mask, x, k));
+    return x;
+}
+
+// The largest finite |y| of the half warp's 128 values, at least 2^-100.
+__device__ __forceinline__ float largest(uint32_t mask, const float (&y)[8])
+{
+    float top = kLeast;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        top = fmaxf(top, fabsf(y[e]));
+    top = half_max(mask, top);
+    if (top == INFINITY) {
+        top = kLeast;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            top = fmaxf(top, fabsf(y[e]) < INFINITY ? fabsf(y[e]) : 0.0f);
+        top = half_max(mask, top);
+    }
+    return top;
+}
+
+template <int ROWS>
+__global__ void __launch_bounds__(kIndexThreads) index_append_kernel(const __grid_constant__ IndexArgs a)
+{
+    __shared__ RowTable<ROWS, kDimI> t;
+    const int tid = threadIdx.x, lane = tid & 31, at = lane & 15;
+    const uint32_t mask = 0xFFFFu << (lane & 16);
+    const int row0 = blockIdx.x * ROWS;
+    if (blockIdx.x == 0 && blockIdx.y == 0)
+        cache::report_requests(a.c);
+    load_turns(t, a.r);
+    load_rows(t, a.c, a.r, row0, a.k != nullptr);
+
+    // vectors of a row: its heads, then its key
+    const int heads = a.heads, all = heads + (a.k ? 1 : 0);
+    const int total = ROWS * all, step = kIndexThreads / 16 * gridDim.y;
+    constexpr int AHEAD = 4;
+    int row_now = -1;
+    Turn turn;
+    for (int v0 = (int)blockIdx.y * (kIndexThreads / 16) + (tid >> 4); v0 < total; v0 += AHEAD * step) {
+        uint4 u[AHEAD];
+        int row[AHEAD], h[AHEAD];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            const int v = v0 + k * step;
+            row[k] = ROWS == 1 ? 0 : v / all;
+            h[k] = v - row[k] * all;
+            const bool key = h[k] == heads;
+            u[k] = make_uint4(0, 0, 0, 0);
+            if (v >= total || !t.place[row[k]].valid) {
+                row[k] = -1;
+                continue;
+            }
+            const long long r = row0 + row[k];
+            u[k] = load_once((key ? a.k + r * a.k_row : a.q + r * a.q_row + h[k] * a.q_head) + 8 * at);
+        }
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            if (row[k] < 0)
+                continue;
+            const long long r = row0 + row[k];
+            const bool key = h[k] == heads;
+            if (row[k] != row_now) {
+                row_now = row[k];
+                turn.load(a.r, t.cs[row_now], at);
+            }
+            float y[8], other[8];
+            unpack8(u[k], y);
+            if (key && a.n.kind != PMQA_NORM_NONE) {
+                if (a.n.kind == PMQA_NORM_LAYER) {
+                    float s = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        s += y[e];
+                    const float mean = half_sum(mask, s) * (1.0f / kDimI);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        y[e] -= mean;
+                }
+                float s = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    s += y[e] * y[e];
+                const float f = rsqrtf(half_sum(mask, s) * (1.0f / kDimI) + a.n.eps);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    y[e] = y[e] * f * (a.n.weight ? __ldg(a.n.weight + 8 * at + e) : 1.0f) +
+                           (a.n.bias ? __ldg(a.n.bias + 8 * at + e) : 0.0f);
+                if (a.r.dim && !a.r.interleaved) {
+                    const int from = (lane + turn.partner) & 31;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        other[e] = __shfl_sync(mask, y[e], from);
+                }
+            } else if (a.r.dim && !a.r.interleaved) {
+                const int from = (lane + turn.partner) & 31;
+                const uint4 p = make_uint4(__shfl_sync(mask, u[k].x, from), __shfl_sync(mask, u[k].y, from),
+                                           __shfl_sync(mask, u[k].z, from), __shfl_sync(mask, u[k].w, from));
+                unpack8(p, other);
+            }
+            turn.apply(a.r.interleaved, y, other);
+            const float top = largest(mask, y);
+            const uint2 code = codes8(y, 448.0f / top);
+            if (key) {
+                const uint32_t dst = t.place[row[k]].row;
+                if (dst != kNoRow) {
+                    uint32_t *const p = reinterpret_cast<uint32_t *>(a.kv + (unsigned long long)dst * kRowI);
+                    p[2 * at] = code.x;
+                    p[2 * at + 1] = code.y;
+                    if (at == 0)
+                        p[kDimI / 4] = __float_as_uint(top / 448.0f);
+                }
+            } else {
+                const long long o = r * heads + h[k];
+                *reinterpret_cast<uint2 *>(a.q_out + o * kDimI + 8 * at) = code;
+                if (at == 0) {
+                    const long long iw = r * a.w_row + h[k];
+                    const float w = a.w_bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t *>(a.w)[iw] << 16)
+                                             : static_cast<const float *>(a.w)[iw];
+                    a.w_out[o] = w * (top / 448.0f) * a.w_scale;
+                }
+            }
+        }
+    }
+}
+
+struct ReadArgs {
+    View c;
+    const uint8_t *kv;
+    const int32_t *start;
+    uint8_t *k;
+    float *s;
+};
+
+template <int ROWS>
+__global__ void __launch_bounds__(128) index_read_kernel(const __grid_constant__ ReadArgs a)
+{
+    const int lane = threadIdx.x & 31;
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < a.c.bs; i += 128) {
+            const int b = __ldg(a.c.row_begin + i), e = __ldg(a.c.row_begin + i + 1);
+            if (b < 0 || e < b || e > a.c.rows)
+                atomicOr(a.c.status, (uint32_t)PMQA_DEV_BAD_CONTEXT);
+        }
+    const long long first = ((long long)blockIdx.x * 4 + (threadIdx.x >> 5)) * ROWS;
+    if (first >= a.c.rows)
+        return;
+    // lane k looks up row first + k
+    const long long r = first + lane;
+    uint32_t src = kNoRow;
+    bool mine = false;
+    int i = request_of(a.c, (int)first);
+    if (lane < ROWS && r < a.c.rows) {
+        // the rows behind may belong to later requests
+        while (i + 1 < a.c.bs && __ldg(a.c.row_begin + i + 1) <= r)
+            ++i;
+        const int b = __ldg(a.c.row_begin + i);
+        mine = r >= b && r < __ldg(a.c.row_begin + i + 1);
+        if (mine)
+            src = pool_row(a.c, i, (a.start ? (long long)__ldg(a.start + i) : 0ll) + (r - b));
+    }
+    const uint32_t *const pool = reinterpret_cast<const uint32_t *>(a.kv);
+    uint32_t *const out = reinterpret_cast<uint32_t *>(a.k);
+    const uint32_t owned = __ballot_sync(kFull, mine);
+    uint32_t scale = 0;
+    if (src != kNoRow)
+        scale = __ldg(pool + (unsigned long long)src * (kRowI / 4) + kDimI / 4);
+    constexpr int AHEAD = 8;
+#pragma unroll
+    for (int k0 = 0; k0 < ROWS; k0 += AHEAD) {
+        uint32_t w[AHEAD];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            const uint32_t row = __shfl_sync(kFull, src, k0 + k);
+            w[k] = row == kNoRow ? 0u : __ldcs(pool + (unsigned long long)row * (kRowI / 4) + lane);
+        }
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+            if (owned >> (k0 + k) & 1u)
+                out[(first + k0 + k) * (kDimI / 4) + lane] = w[k];
+    }
+    if (mine)
+        a.s[r] = __uint_as_float(scale);
+}
+
+}  // namespace paged
+}  // namespace pmqa
+
+using namespace pmqa;
+using namespace pmqa::paged;
+
+extern "C" int pmqa_index_append(const pmqa_paged_rows *p, void *kv_cache, const pmqa_index_rows *x,
+                                 const pmqa_norm *norm, const pmqa_rotary *rotary, void *ws, size_t ws_bytes,
+                                 pmqa_stream_t stream)
+{
+    int rc = check_rows(p, true, ws, ws_bytes, cache::kStatusBytes);
+    if (rc != PMQA_OK)
+        return rc;
+    IndexArgs a{};
+    if (!x || (rc = check_norm(norm, &a.n)) != PMQA_OK || (rc = check_rotary(rotary, kDimI, false, &a.r)) != PMQA_OK)
+        return x ? rc : PMQA_ERR_INVALID_ARG;
+    if (x->q && (x->heads < 1 || !std::isfinite(x->weight_scale) || x->weights_row < 0))
+        return PMQA_ERR_INVALID_ARG;
+    if (x->q && (long long)x->heads * p->rows > 0x7FFFFFFFll)
+        return PMQA_ERR_UNSUPPORTED;
+    if (p->bs == 0 || p->rows == 0 || (!x->k && !x->q))
+        return PMQA_OK;
+    if (x->k && (cache::missing(kv_cache, 4) || bad_rows(x->k, 16, x->k_row)))
+        return PMQA_ERR_INVALID_ARG;
+    if (x->q) {
+        const long long n = (long long)p->rows * x->heads;
+        if (bad_rows(x->q, 16, x->q_row, x->q_head) || cache::missing(x->q_out, 8) ||
+            cache::missing(x->weights, x->weights_bf16 ? 2 : 4) || cache::missing(x->weights_out, 4))
+            return PMQA_ERR_INVALID_ARG;
+        // weights in place, or apart
+        const long long in = ((p->rows - 1ll) * x->weights_row + x->heads) * (x->weights_bf16 ? 2 : 4);
+        const bool same = x->weights == x->weights_out && !x->weights_bf16 &&
+                          (x->weights_row == x->heads || p->rows == 1);
+        if (!same && cache::overlap(x->weights, in, x->weights_out, 4 * n))
+            return PMQA_ERR_INVALID_ARG;
+    }
+    a.c = view(p, ws);
+    a.kv = static_cast<uint8_t *>(kv_cache);
+    a.k = static_cast<const uint16_t *>(x->k);
+    a.q = static_cast<const uint16_t *>(x->q);
+    a.w = x->weights;
+    a.q_out = static_cast<uint8_t *>(x->q_out);
+    a.w_out = x->weights_out;
+    a.k_row = x->k_row;
+    a.q_row = x->q_row;
+    a.q_head = x->q_head;
+    a.w_row = x->weights_row;
+    a.heads = x->q ? x->heads : 0;
+    a.w_bf16 = x->weights_bf16 ? 1 : 0;
+    a.w_scale = x->weight_scale;
+    int sms = 0;
+    if ((rc = cache::sm_count(&sms)) != PMQA_OK)
+        return rc;
+    const int rows = p->rows;
+    const cudaStream_t st = cache::cuda(stream);
+    if (rows >= 16 * sms)
+        index_append_kernel<4><<<(rows + 3) / 4, kIndexThreads, 0, st>>>(a);
+    else
+        // few rows: a row's vectors over several CTAs, as many as there are SMs for
+        index_append_kernel<1><<<dim3(rows, std::max(1, std::min((a.heads + 16) / 16, sms / rows))), kIndexThreads, 0, st>>>(a);
+    return cache::code_of(cudaGetLastError());
+}
+
+extern "C" int pmqa_index_read(const pmqa_paged_rows *p, const void *kv_cache, const int32_t *start, void *k,
+                               float *k_scale, void *ws, size_t ws_bytes, pmqa_stream_t stream)
+{
+    int rc = check_rows(p, false, ws, ws_bytes, cache::kStatusBytes);
+    if (rc != PMQA_OK)
+        return rc;
+    if (p->bs == 0 || p->rows == 0)
+        return PMQA_OK;
+    if (cache::missing(kv_cache, 4) || !cache::aligned(start, 4) || cache::missing(k, 16) ||
+        cache::missing(k_scale, 4))
+        return PMQA_ERR_INVALID_ARG;
+    ReadArgs a{view(p, ws), static_cast<const uint8_t *>(kv_cache), start, static_cast<uint8_t *>(k), k_scale};
+    int sms = 0;
+    if ((rc = cache::sm_count(&sms)) != PMQA_OK)
+        return rc;
+    const long long rows = p->rows;
+    const cudaStream_t st = cache::cuda(stream);
+    if (rows >= 32ll * 32 * sms)
+        index_read_kernel<32><<<(unsigned)((rows + 127) / 128), 128, 0, st>>>(a);
+    else
+        index_read_kernel<8><<<(unsigned)((rows + 31) / 32), 128, 0, st>>>(a);
+    return cache::code_of(cudaGetLastError());
+}

@@ -1,0 +1,1020 @@
+// pmqa_latent_attn.cu -- attention of every row to all the tokens that it sees of
+// the latent cache, and its C ABI (pmqa_latent_attention).
+//
+//   out[r][h] = sum_t softmax_t(sm_scale * q_h . k_t) * v_t,   v_t = k_t[0..511]
+//
+// Rows of one request are packed as (query token, head), up to N = 16, 32 or 64 to
+// a block. A CTA walks the token tiles (128 tokens) of its blocks:
+//   * four warps look up the tokens in the block table and copy the latent rows (576
+//     bytes) by cp.async straight into the operand layout (pmqa_latent.cuh);
+//   * one thread issues S^T = K Q^T (kind::f8f6f4, M = 128 tokens, N packed rows,
+//     K = 576) into TMEM;
+//   * the softmax threads, one per token and 32 packed rows, form p = 2^(x - m + 4)
+//     with a row maximum m that moves only when a weight passes 2^8, and write p as
+//     two e4m3 terms, p_hi = e4m3(p) and p_lo = e4m3(p - p_hi);
+//   * the thread issues O^T += V^T P^T (M = 128 value columns, four blocks, K = 128
+//     tokens) from the SAME tile as an MN-major operand. With N = 64 both terms add
+//     into one accumulator (the products cost 576 + 2 * 512 fp8 multiplications a
+//     row and token); with fewer rows the terms are N more columns, p_lo times 16,
+//     since there the cost is the read of V.
+// The flattened sequence of (block, tile) is split evenly over the CTAs; a block
+// that is cut leaves its parts (O, m, l) in the workspace and a second kernel joins
+// them. Where a query token has more than 64 heads, neighbouring CTAs take its heads
+// and walk the same tokens at the same time, so that the second finds them in L2.
+//
+// A NaN in a token's row makes all its scores NaN. Where some rows do not see the
+// token, its thread sets the row's values to zero before they are multiplied by
+// the weights (0 for those rows, and for the others a NaN in the sum l, which makes
+// all of their output NaN).
+#include <algorithm>
+#include <cmath>
+
+#include "pmqa_latent.cuh"
+#include "pmqa_paged.cuh"
+
+namespace pmqa {
+namespace latent {
+
+using cache::Request;
+using cache::View;
+using namespace mla;
+
+constexpr uint32_t kFull = cache::kFull;
+constexpr int kTile = 128;      // tokens per tile
+constexpr int kMaxHeads = 128;
+constexpr int kMaxCtas = 160;   // workspace parts: 2 per CTA
+constexpr int kPad = 2;         // tiles' worth of starting and ending a block
+constexpr int kLeast = 2;       // fewest tiles that a CTA takes
+constexpr int kWhole = 512;     // tables of up to so many tokens: blocks are not cut
+constexpr float kBase = 4.0f;   // p = 2^(x - m + kBase)
+constexpr float kTop = 8.0f;    // m moves when a p passes 2^kTop
+constexpr float kUnseen = 1e30f;   // kBase - m of a row that has seen no score: above every |x|
+constexpr double kMaxFactor = 1e20;  // |c_log2|: times a product of two rows (1.2e8) well below kUnseen
+
+constexpr size_t kWsMeta = cache::kStatusBytes;
+constexpr size_t kWsMl = kWsMeta + kMaxCtas * 16;
+constexpr size_t kWsPart = kWsMl + (size_t)2 * kMaxCtas * 64 * 2 * 4;
+constexpr size_t kWorkspace = kWsPart + (size_t)2 * kMaxCtas * 64 * kVDim * 4;
+
+struct Args {
+    View c;
+    const uint8_t *q;   // [rows, heads, 576]
+    const uint8_t *kv;  // [num_blocks * P, 576]
+    uint16_t *out;
+    float *lse;
+    float c_log2;       // sm_scale * q_scale * kv_scale * log2(e)
+    float kv_scale;
+    int heads;
+    int toks;           // query tokens of a block (a power of two; 1 where hb > 1)
+    int hb;             // blocks of a query token (CTAs that walk the same tokens)
+    int ranges;         // parts that the sequence is cut into at most
+    int whole;          // blocks are not cut
+    int4 *meta;         // [ranges]: (request, unit, parts, 0) of the unit cut at the range's end
+    float *ml;          // [2 ranges hb][N][2]
+    float *part;        // [2 ranges hb][N][512]
+};
+
+// ------------------------------------------------------------- the sequence
+//
+// Request i has units u < U_i = ceil(n_i / toks) of `toks` query tokens; unit u has
+// the tiles up to the slot of its last token, whether or not that token exists:
+//   T = floor((ctx - n + toks u + toks - 1) / 128) + 1 = floor((f + u) / w) + 1,
+// f = ceil((ctx - n) / toks), w = 128 / toks. kPad places without work follow each
+// unit's tiles.
+
+struct Req {
+    Request q;
+    int f, U;
+};
+
+__device__ __forceinline__ Req load_req(const Args &a, int i, bool tell)
+{
+    Req r;
+    r.q = cache::load_request(a.c, i, tell);
+    r.U = (r.q.n + a.toks - 1) / a.toks;
+    r.f = (max(r.q.ctx - r.q.n, 0) + a.toks - 1) / a.toks;
+    return r;
+}
+
+// sum of floor(y / w) over y < x
+__device__ __forceinline__ long long floor_sum(long long x, int w)
+{
+    const long long q = x / w;
+    return (long long)w * (q * (q - 1) / 2) + q * (x - q * w);
+}
+
+// places of the first u units
+__device__ __forceinline__ long long places(const Args &a, const Req &r, int u)
+{
+    const int w = kTile / a.toks;
+    return floor_sum((long long)r.f + u, w) - floor_sum(r.f, w) + (long long)u * (1 + kPad);
+}
+
+// Where a role is: unit u of request i, tile t of T, at place x of the sequence.
+struct Cursor {
+    Req r;
+    int i, u, t, T;
+    long long x;
+
+    __device__ __forceinline__ void set_unit(const Args &a) { T = (r.f + u) / (kTile / a.toks) + 1; }
+
+    // the next unit; false past the last
+    __device__ __forceinline__ bool next_unit(const Args &a)
+    {
+        x += T + kPad - t;
+        t = 0;
+        ++u;
+        while (u >= r.U) {
+            if (++i >= a.c.bs)
+                return false;
+            r = load_req(a, i, false);
+            u = 0;
+        }
+        set_unit(a);
+        return true;
+    }
+};
+
+struct Range {
+    long long x0, x1, total;
+    int C;       // ranges with work
+    Cursor at;   // place x0
+    int any;
+};
+
+__device__ __forceinline__ long long range_start(long long total, int C, long long b)
+{
+    return b * total / C;
+}
+
+__device__ __forceinline__ int range_of(long long total, int C, long long x)
+{
+    return (int)(((x + 1) * (long long)C - 1) / total);
+}
+
+// Called by the whole CTA; the result is in s_range after the last barrier.
+template <int THREADS>
+__device__ __forceinline__ void find_range(const Args &a, int g, Range *s_range)
+{
+    __shared__ long long s_sum[THREADS / 32], s_units[THREADS / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    long long sum = 0, units = 0;
+    for (int i = tid; i < a.c.bs; i += THREADS) {
+        const Req r = load_req(a, i, blockIdx.x == 0);
+        sum += places(a, r, r.U);
+        units += r.U;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        sum += __shfl_xor_sync(kFull, sum, o);
+        units += __shfl_xor_sync(kFull, units, o);
+    }
+    if (lane == 0) {
+        s_sum[warp] = sum;
+        s_units[warp] = units;
+    }
+    if (tid == 0)
+        s_range->any = 0;
+    __syncthreads();
+    long long total = 0;
+    units = 0;
+    for (int k = 0; k < THREADS / 32; ++k) {
+        total += s_sum[k];
+        units += s_units[k];
+    }
+    // no more ranges than keep kLeast tiles each
+    const int C = (int)min((long long)a.ranges, max(units > 0 ? 1ll : 0ll, (total - units * kPad) / kLeast));
+    const long long x0 = g < C ? range_start(total, C, g) : total;
+    const long long x1 = g < C ? range_start(total, C, g + 1) : total;
+    long long base = 0;
+    for (int i0 = 0; x0 < x1 && i0 < a.c.bs; i0 += THREADS) {
+        const int i = i0 + tid;
+        long long n = 0;
+        Req r{};
+        if (i < a.c.bs) {
+            r = load_req(a, i, false);
+            n = places(a, r, r.U);
+        }
+        long long inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(kFull, inc, o);
+            if (lane >= o)
+                inc += y;
+        }
+        __syncthreads();
+        if (lane == 31)
+            s_sum[warp] = inc;
+        __syncthreads();
+        long long lo = base + inc - n, all = 0;
+        for (int k = 0; k < THREADS / 32; ++k) {
+            if (k < warp)
+                lo += s_sum[k];
+            all += s_sum[k];
+        }
+        if (n > 0 && lo <= x0 && x0 < lo + n) {
+            // the unit that holds place x0
+            const long long y = x0 - lo;
+            int ua = 0, ub = r.U;
+            while (ub - ua > 1) {
+                const int mid = ua + (ub - ua) / 2;
+                if (places(a, r, mid) <= y)
+                    ua = mid;
+                else
+                    ub = mid;
+            }
+            Cursor c;
+            c.r = r;
+            c.i = i;
+            c.u = ua;
+            c.t = (int)(y - places(a, r, ua));
+            c.x = x0;
+            c.set_unit(a);
+            // behind the tiles, or (whole) inside a unit: the next one
+            bool any = true;
+            if (c.t >= c.T || (a.whole && c.t > 0))
+                any = c.next_unit(a);
+            s_range->at = c;
+            s_range->any = any && c.x < x1;
+        }
+        base += all;
+        if (base > x0)
+            break;  // the same for every thread
+    }
+    if (tid == 0) {
+        s_range->x0 = x0;
+        s_range->x1 = x1;
+        s_range->total = total;
+        s_range->C = C;
+    }
+    __syncthreads();
+}
+
+// The next tile of a range; false at its end.
+__device__ __forceinline__ bool next_tile(const Args &a, Cursor &c, long long x1)
+{
+    ++c.t;
+    ++c.x;
+    if (c.t < c.T)
+        return a.whole || c.x < x1;
+    return c.next_unit(a) && c.x < x1;
+}
+
+// ------------------------------------------------------------- one block of rows
+
+// The packed rows of a unit that CTA `hs` of its range takes.
+struct Block {
+    long long first;  // row of q and out, in heads
+    int rows;         // packed rows
+    int last;         // last slot that the first row sees
+    int end;          // slots that some row sees
+};
+
+__device__ __forceinline__ Block block_of(const Args &a, const Cursor &c, int hs, int N)
+{
+    Block b;
+    const int j0 = c.u * a.toks;
+    const int n = min(a.toks, c.r.q.n - j0);
+    const int h0 = hs * N;
+    b.rows = a.hb > 1 ? min(N, a.heads - h0) : n * a.heads;
+    b.first = ((long long)c.r.q.r0 + j0) * a.heads + h0;
+    b.last = c.r.q.ctx - c.r.q.n + j0;
+    b.end = min(c.r.q.ctx, max(0, b.last + n));
+    return b;
+}
+
+// ------------------------------------------------------------- kernel
+
+template <int N>
+struct Cfg {
+    static constexpr int kGroups = N == 64 ? 2 : 1;       // softmax warpgroups
+    static constexpr int kRowsG = N / kGroups;            // packed rows of each
+    static constexpr int kStages = N == 16 ? 3 : 2;       // value ring
+    static constexpr int kThreads = 128 + 128 * kGroups + 32;
+    static constexpr int kMmaWarp = 4 + 4 * kGroups;
+    static constexpr int kOCols = N == 64 ? 64 : 2 * N;   // output columns of a value block
+    static constexpr float kLo = N == 64 ? 1.0f : 16.0f;  // p_lo holds kLo (p - p_hi)
+    // P: a row of 64 bytes per token, two terms of N rows. N = 64: a buffer of 128 rows for
+    // each term; N = 16: both stages share a row, 32 bytes each.
+    static constexpr uint32_t kPTerm = 128u * 64u;
+    static constexpr uint32_t kPStage = N == 64 ? 2 * kPTerm : N == 32 ? kPTerm : 32u;
+    static constexpr uint32_t kPBytes = N == 16 ? kPTerm : 2 * kPStage;
+    static constexpr uint32_t kColS = 0;                  // 2 x N score columns
+    static constexpr uint32_t kColO = 128;                // 4 x kOCols output columns
+    static constexpr uint32_t kTmem = N == 64 ? 512 : N == 32 ? 512 : 256;
+
+    static constexpr uint32_t kOffV = 0;
+    static constexpr uint32_t kOffR = kOffV + kStages * kVStage;
+    static constexpr uint32_t kOffQV = kOffR + 2 * kRStage;
+    static constexpr uint32_t kOffQR = kOffQV + (N / 8) * kVGroup;
+    static constexpr uint32_t kOffP = kOffQR + ((N / 8) * kRGroup + 1023) / 1024 * 1024;
+    static constexpr uint32_t kOffMask = kOffP + kPBytes;               // [stages][4] words
+    static constexpr uint32_t kOffLim = kOffMask + kStages * 16;        // [2][N] ints
+    static constexpr uint32_t kOffM = kOffLim + 2 * N * 4;              // [N] floats: kBase - m
+    static constexpr uint32_t kOffAlpha = kOffM + N * 4;                // [N]
+    static constexpr uint32_t kOffRed = kOffAlpha + N * 4;              // [4][N]
+    static constexpr uint32_t kOffBar = kOffRed + 4 * N * 4;
+    static constexpr int kBMask = 0;                        // [stages] masks written: 4 producer warps
+    static constexpr int kBReady = kBMask + kStages;        // [stages] rows landed: 128 cp.async arrivals
+    static constexpr int kBVEmpty = kBReady + kStages;      // [stages] values read: MMA commit
+    static constexpr int kBREmpty = kBVEmpty + kStages;     // [2] rotary columns read: MMA commit
+    static constexpr int kBSFull = kBREmpty + 2;            // [2] scores in TMEM: MMA commit
+    static constexpr int kBSFree = kBSFull + 2;             // [2] scores read: softmax warps
+    static constexpr int kBPFull = kBSFree + 2;             // [2] P written, O rescaled: softmax warps
+    static constexpr int kBPEmpty = kBPFull + 2;            // [2] P read: MMA commit
+    static constexpr int kBQEmpty = kBPEmpty + 2;           // queries read: MMA commit
+    static constexpr int kBDrain = kBQEmpty + 1;
+    static constexpr int kBars = kBDrain + 1;
+    static constexpr uint32_t kOffMisc = kOffBar + kBars * 8;
+    static constexpr uint32_t kSmem = kOffMisc + 16;
+    static_assert(kSmem + 1024 <= 232448, "shared memory, with the static arrays below it");
+    static_assert(kOffP % 1024 == 0 && kOffBar % 8 == 0, "alignment");
+
+    static constexpr uint32_t kIdescQK = idesc_e4m3_f32(128, N);
+    // A and B MN-major (bits 15 and 16)
+    static constexpr uint32_t kIdescPV = idesc_e4m3_f32(128, kOCols) | kIdescAMnMajor | (1u << 16);
+};
+
+// Shared-memory matrix descriptor, MN-major with the 64-byte swizzle: one row of 64
+// bytes per K index, 16-byte chunk c of row k at chunk c ^ ((k >> 1) & 3), groups of
+// 8 rows 512 bytes apart; up to 64 elements along N.
+__device__ __forceinline__ uint64_t sw64_mnmajor_desc(uint32_t smem_addr)
+{
+    return sw64_kmajor_desc(smem_addr, 512u);
+}
+
+// Sums or maxima of NR values over the warp's lanes: lane gets the result of value
+// lane (NR = 32) or lane >> 1 (NR = 16).
+template <bool MAX, int NR>
+__device__ __forceinline__ float reduce_scatter(float (&v)[NR], int lane)
+{
+    auto op = [](float x, float y) { return MAX ? fmaxf(x, y) : x + y; };
+    int bit = 16;
+#pragma unroll
+    for (int n = NR / 2; n > 0; n >>= 1) {
+        const bool up = (lane & bit) != 0;
+#pragma unroll
+        for (int k = 0; k < n; ++k) {
+            const float send = up ? v[k] : v[k + n], keep = up ? v[k + n] : v[k];
+            v[k] = op(keep, __shfl_xor_sync(kFull, send, bit));
+        }
+        bit >>= 1;
+    }
+    return NR == 32 ? v[0] : op(v[0], __shfl_xor_sync(kFull, v[0], 1));
+}
+
+__device__ __forceinline__ uint32_t e4m3x2_of_f16x2(uint32_t h2)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t b)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)b));
+    return r;
+}
+
+// Two weights as their terms (bytes 0 and 1): the f16 value of p is off by 2^-11 at
+// most, its difference from the first term exact.
+template <bool UP>
+__device__ __forceinline__ void split2(float p0, float p1, uint32_t &hi, uint32_t &lo)
+{
+    const uint32_t p = cache::pack_f16x2(p0, p1);
+    hi = e4m3x2_of_f16x2(p);
+    uint32_t d = f16x2_of_e4m3x2(hi);
+    asm("sub.rn.f16x2 %0, %1, %0;" : "+r"(d) : "r"(p));
+    if (UP)
+        asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(d) : "r"(0x4C004C00u));  // 16
+    lo = e4m3x2_of_f16x2(d);
+}
+
+// Four codes, NaN (0x7F, 0xFF) replaced by 0.
+__device__ __forceinline__ uint32_t without_nan(uint32_t x)
+{
+    const uint32_t is = ((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+    return x & ~((is >> 7) * 0xFFu);
+}
+
+template <int N>
+__global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const __grid_constant__ Args a)
+{
+    using K = Cfg<N>;
+    constexpr int RG = K::kRowsG;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ Range s_range;
+    const uint32_t sbase = smem_u32(smem);
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(kFull, tid >> 5, 0);
+    const int g = blockIdx.x / a.hb, hs = blockIdx.x - g * a.hb;
+
+    if (hs == 0 && tid == 0)
+        a.meta[g] = make_int4(0, 0, 0, 0);
+    find_range<K::kThreads>(a, g, &s_range);
+    griddep_launch_dependents();
+    if (!s_range.any)
+        return;  // the same for the whole CTA
+    if (sbase & 1023u) {
+        if (tid == 0)
+            atomicOr(a.c.status, (uint32_t)PMQA_DEV_INTERNAL);
+        return;
+    }
+    const long long x0 = s_range.x0, x1 = s_range.x1;
+
+    uint64_t *const bar = reinterpret_cast<uint64_t *>(smem + K::kOffBar);
+    uint32_t *const misc = reinterpret_cast<uint32_t *>(smem + K::kOffMisc);
+    volatile int *const abort_flag = reinterpret_cast<volatile int *>(misc + 1);
+    if (tid == 0) {
+        for (int s = 0; s < K::kStages; ++s) {
+            mbar_init(&bar[K::kBMask + s], 4);
+            mbar_init(&bar[K::kBReady + s], 128);
+            mbar_init(&bar[K::kBVEmpty + s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&bar[K::kBREmpty + s], 1);
+            mbar_init(&bar[K::kBSFull + s], 1);
+            mbar_init(&bar[K::kBSFree + s], 4 * K::kGroups);
+            mbar_init(&bar[K::kBPFull + s], 4 * K::kGroups);
+            mbar_init(&bar[K::kBPEmpty + s], 1);
+        }
+        mbar_init(&bar[K::kBQEmpty], 1);
+        mbar_init(&bar[K::kBDrain], 1);
+        misc[1] = 0;
+        mbar_init_fence();
+    }
+    if (warp == K::kMmaWarp)
+        tmem_alloc(misc, K::kTmem);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = misc[0];
+    auto fail = [&]() {
+        atomicOr(a.c.status, (uint32_t)PMQA_DEV_TIMEOUT);
+        *abort_flag = 1;
+    };
+
+    if (warp < 4) {
+        // ------------------------------------------------------------ producer
+        // Thread tid owns token tid of every tile; warp w copies the rows of tokens
+        // 32 w .. 32 w + 31, one row per instruction (lane = 16-byte chunk). The
+        // table entries of the next tile load while this one is issued.
+        Cursor c = s_range.at, d = c;
+        bool more = true;
+        auto look_up = [&](const Cursor &u) -> int {
+            const int tok = u.t * kTile + tid;
+            const Block b = block_of(a, u, hs, N);
+            return tok < b.end ? __ldg(a.c.bt + (long long)u.i * a.c.W + a.c.page_of(tok)) : -1;
+        };
+        int page = look_up(c);
+        int vs = 0, seg = -1, it = 0;
+        uint32_t vph = 0;
+        for (;; ++it) {
+            const int rs = it & 1;
+            const uint32_t rph = (uint32_t)(it >> 1) & 1u;
+            const Block b = block_of(a, c, hs, N);
+            const bool first = it == 0 || c.t == 0;
+            d = c;
+            more = next_tile(a, d, x1);
+            const int page_next = more ? look_up(d) : -1;
+            // pool row of this thread's token
+            const int tok = c.t * kTile + tid;
+            uint32_t srow = paged::kNoRow;
+            if (tok < b.end) {
+                if (page < 0 || (long long)page >= a.c.nb)
+                    atomicOr(a.c.status, (uint32_t)PMQA_DEV_BAD_BLOCK_ID);
+                else
+                    srow = (uint32_t)page * (uint32_t)a.c.P + (uint32_t)(tok - a.c.page_of(tok) * a.c.P);
+            }
+            page = page_next;
+            if (first) {
+                // one query buffer: free once the last scores of the block before are done
+                ++seg;
+                if (!__all_sync(kFull, mbar_wait(&bar[K::kBQEmpty], ((uint32_t)seg & 1u) ^ 1u, abort_flag))) {
+                    fail();
+                    break;
+                }
+                const uint8_t *const src = a.q + b.first * kDim;
+                for (int k = tid; k < N * kChunks; k += 128) {
+                    const int r = k / kChunks, ch = k - r * kChunks;
+                    const uint32_t dst = ch < 32 ? sbase + K::kOffQV + v_offset(r, ch)
+                                                 : sbase + K::kOffQR + r_offset(r, ch - 32);
+                    cp_async_16(dst, src + (r < b.rows ? r * kDim + ch * 16 : 0), r < b.rows ? 16u : 0u);
+                }
+            }
+            if (!__all_sync(kFull, mbar_wait(&bar[K::kBVEmpty + vs], vph ^ 1u, abort_flag) &&
+                                       mbar_wait(&bar[K::kBREmpty + rs], rph ^ 1u, abort_flag))) {
+                fail();
+                break;
+            }
+            const uint32_t have = __ballot_sync(kFull, srow != paged::kNoRow);
+            if (lane == 0) {
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(sbase + K::kOffMask + (uint32_t)vs * 16u + 4u * warp),
+                             "r"(have) : "memory");
+                mbar_arrive(&bar[K::kBMask + vs]);
+            }
+            const uint32_t vdst = sbase + K::kOffV + (uint32_t)vs * kVStage;
+            const uint32_t rdst = sbase + K::kOffR + (uint32_t)rs * kRStage;
+#pragma unroll 4
+            for (int tt = 0; tt < 32; ++tt) {
+                const uint32_t sr = __shfl_sync(kFull, srow, tt);
+                const bool is = sr != paged::kNoRow;
+                cp_async_16(vdst + v_offset(warp * 32 + tt, lane), a.kv + (is ? (unsigned long long)sr * kDim : 0ull) + 16 * lane,
+                            is ? 16u : 0u);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int tt = k * 8 + (lane >> 2), cc = lane & 3;
+                const uint32_t sr = __shfl_sync(kFull, srow, tt);
+                const bool is = sr != paged::kNoRow;
+                cp_async_16(rdst + r_offset(warp * 32 + tt, cc),
+                            a.kv + (is ? (unsigned long long)sr * kDim : 0ull) + kVDim + 16 * cc, is ? 16u : 0u);
+            }
+            cp_async_arrive_noinc(&bar[K::kBReady + vs]);
+            if (++vs == K::kStages) {
+                vs = 0;
+                vph ^= 1u;
+            }
+            if (!more)
+                break;
+            c = d;
+        }
+        cp_async_wait_all();
+        if (hs == 0 && tid == 0) {
+            // the last unit goes on in later ranges and starts in this one: to be joined
+            const long long xs = c.x - c.t, xe = xs + c.T;
+            if (!a.whole && xs >= x0 && xe > x1)
+                a.meta[g] = make_int4(c.i, c.u, range_of(s_range.total, s_range.C, xe - 1) - g + 1, 0);
+        }
+    } else if (warp < K::kMmaWarp) {
+        // ------------------------------------------------------------ softmax
+        // Thread s of a group owns token s (TMEM lane s) and the group's RG packed
+        // rows. Exits are uniform over the group: a failed wait clears `ok`, and the
+        // group leaves together at its next barrier.
+        const int wg = (warp - 4) >> 2, s = (tid - 128) & 127, w4 = s >> 5;
+        const uint32_t lane_off = (uint32_t)(w4 * 32) << 16;
+        const uint32_t barrier = 1u + wg;
+        float *const mneg = reinterpret_cast<float *>(smem + K::kOffM) + wg * RG;
+        float *const alpha = reinterpret_cast<float *>(smem + K::kOffAlpha) + wg * RG;
+        float *const red = reinterpret_cast<float *>(smem + K::kOffRed) + wg * RG;  // [4][N]
+        int *const lims = reinterpret_cast<int *>(smem + K::kOffLim) + wg * RG;     // [2][N]
+        Cursor c = s_range.at;
+        float l[RG];
+        int seg = -1, vs = 0;
+        uint32_t vph = 0;
+        bool ok = true;
+        for (int it = 0;; ++it) {
+            const int stage = it & 1;
+            const uint32_t kph = (uint32_t)(it >> 1) & 1u;
+            const Block b = block_of(a, c, hs, N);
+            const bool first = it == 0 || c.t == 0;
+            Cursor d = c;
+            const bool more = next_tile(a, d, x1);
+            const bool last = !more || d.t == 0;
+            if (first) {
+                ++seg;
+#pragma unroll
+                for (int h = 0; h < RG; ++h)
+                    l[h] = 0.0f;
+                if (s < RG) {
+                    const int r = wg * RG + s;
+                    mneg[s] = kUnseen;
+                    // rows that do not exist see everything: no mask for their sake
+                    lims[(seg & 1) * N + s] = r < b.rows ? b.last + (a.hb > 1 ? 0 : r / a.heads) : 0x7FFFFFFF;
+                }
+                named_bar_sync(barrier, 128);
+            }
+            ok = ok && mbar_wait(&bar[K::kBSFull + stage], kph, abort_flag) &&
+                 mbar_wait(&bar[K::kBMask + vs], vph, abort_flag) &&
+                 mbar_wait(&bar[K::kBPEmpty + stage], kph ^ 1u, abort_flag);
+            ok = __all_sync(kFull, ok);
+            uint32_t sr[RG];
+            if (ok) {
+                tc_fence_after_sync();
+                tmem_ld_cols<RG>(tmem + K::kColS + (uint32_t)(stage * N + wg * RG) + lane_off, sr);
+                tmem_ld_wait();
+                reg_fence_cols<RG>(sr);
+                tc_fence_before_sync();
+            } else {
+#pragma unroll
+                for (int h = 0; h < RG; ++h)
+                    sr[h] = 0u;
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&bar[K::kBSFree + stage]);
+            const uint4 have = lds128(sbase + K::kOffMask + (uint32_t)vs * 16u);
+            const int tok = c.t * kTile + s;
+            const bool masked = (have.x & have.y & have.z & have.w) != kFull || c.t * kTile + kTile - 1 > b.last;
+            if (masked) {
+                const bool there = lds32(sbase + K::kOffMask + (uint32_t)vs * 16u + 4u * w4) >> lane & 1u;
+                const int *const lim = lims + (seg & 1) * N;
+                bool nan = false;
+                const uint32_t never = __float_as_uint(a.c_log2 > 0.0f ? -INFINITY : INFINITY);
+#pragma unroll
+                for (int h = 0; h < RG; ++h) {
+                    const float x = __uint_as_float(sr[h]);
+                    nan |= x != x;
+                    sr[h] = there && tok <= lim[h] ? sr[h] : never;
+                }
+                if (nan) {
+                    // in the queries, or in the token's row: then out of its values
+                    const uint32_t v = sbase + K::kOffV + (uint32_t)vs * kVStage;
+                    for (int ch = 0; ch < 32; ++ch) {
+                        const uint4 u = lds128(v + v_offset(s, ch));
+                        sts128(v + v_offset(s, ch), without_nan(u.x), without_nan(u.y), without_nan(u.z), without_nan(u.w));
+                    }
+                }
+            }
+            auto value = [&](int h, float m) -> float { return __uint_as_float(sr[h]) * a.c_log2 + m; };
+            float top = -INFINITY;
+#pragma unroll
+            for (int h = 0; h < RG; h += 4) {
+                const float4 m4 = *reinterpret_cast<const float4 *>(mneg + h);
+                top = fmaxf(top, fmaxf(fmaxf(value(h, m4.x), value(h + 1, m4.y)),
+                                       fmaxf(value(h + 2, m4.z), value(h + 3, m4.w))));
+            }
+            bool resc = false;
+            if (named_bar_or(barrier, 128, !ok || top > kTop)) {
+                float v[RG];
+#pragma unroll
+                for (int h = 0; h < RG; ++h)
+                    v[h] = value(h, 0.0f);
+                const float wmax = reduce_scatter<true, RG>(v, lane);
+                const int row = RG == 32 ? lane : lane >> 1;
+                red[w4 * N + row] = wmax;
+                if (!named_bar_and(barrier, 128, ok)) {
+                    fail();
+                    break;
+                }
+                if (w4 == 0 && lane < RG) {
+                    const float x = fmaxf(fmaxf(red[lane], red[N + lane]), fmaxf(red[2 * N + lane], red[3 * N + lane]));
+                    const float m = mneg[lane];
+                    float f = 1.0f;
+                    if (x + m > kTop) {
+                        const float to = kBase - x;
+                        f = ex2_approx(to - m);  // 0 where no score was seen before
+                        mneg[lane] = to;
+                    }
+                    alpha[lane] = f;
+                }
+                named_bar_sync(barrier, 128);
+                resc = true;
+#pragma unroll
+                for (int h = 0; h < RG; ++h)
+                    l[h] *= alpha[h];
+            }
+            // weights, their sum and their two terms
+            uint32_t hi[RG / 4], lo[RG / 4];
+#pragma unroll
+            for (int h = 0; h < RG; h += 4) {
+                const float4 m4 = *reinterpret_cast<const float4 *>(mneg + h);
+                float p[4] = {value(h, m4.x), value(h + 1, m4.y), value(h + 2, m4.z), value(h + 3, m4.w)};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    p[e] = ex2_approx(p[e]);
+                    l[h + e] += p[e];
+                }
+                uint32_t h0, l0, h1, l1;
+                split2<N != 64>(p[0], p[1], h0, l0);
+                split2<N != 64>(p[2], p[3], h1, l1);
+                hi[h / 4] = h0 | h1 << 16;
+                lo[h / 4] = l0 | l1 << 16;
+            }
+            {
+                // token s: one row of 64 bytes, 64-byte swizzle
+                const uint32_t pb = sbase + K::kOffP + (N == 16 ? 0u : (uint32_t)stage * K::kPStage) + (uint32_t)s * 64u;
+                const uint32_t x = (uint32_t)(s >> 1) & 3u;
+#pragma unroll
+                for (int k = 0; k < RG / 16; ++k) {
+                    const uint32_t ch = (uint32_t)((N == 64 ? 2 * wg : N == 16 ? 2 * stage : 0) + k);
+                    const uint32_t cl = N == 64 ? ch : ch + RG / 16;
+                    sts128(pb + ((ch ^ x) << 4), hi[4 * k], hi[4 * k + 1], hi[4 * k + 2], hi[4 * k + 3]);
+                    sts128(pb + (N == 64 ? K::kPTerm : 0u) + ((cl ^ x) << 4), lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
+                }
+            }
+            if (resc && !first) {
+                // O holds the block's earlier tiles, up to it - 1
+                ok = ok && mbar_wait(&bar[K::kBPEmpty + (stage ^ 1)], (uint32_t)((it - 1) >> 1) & 1u, abort_flag);
+                ok = __all_sync(kFull, ok);
+                if (ok) {
+                    tc_fence_after_sync();
+#pragma unroll 1
+                    for (int k = 0; k < 4; ++k) {
+#pragma unroll 1
+                        for (int half = 0; half < (N == 32 ? 2 : 1); ++half) {
+                            uint32_t o[32];
+                            const uint32_t ta = tmem + K::kColO + (uint32_t)(k * K::kOCols + (N == 64 ? 32 * wg : 32 * half)) + lane_off;
+                            tmem_ld32(ta, o);
+                            tmem_ld_wait();
+                            reg_fence_cols<32>(o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha[e & (RG - 1)]);
+                            tmem_st32(ta, o);
+                        }
+                    }
+                    tmem_st_wait();
+                }
+            }
+            fence_proxy_async_smem();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&bar[K::kBPFull + stage]);
+            if (++vs == K::kStages) {
+                vs = 0;
+                vph ^= 1u;
+            }
+            if (!last) {
+                c = d;
+                continue;
+            }
+
+            // ------------------------------------------------ end of a block
+            ok = ok && mbar_wait(&bar[K::kBPEmpty + stage], kph, abort_flag);
+            ok = __all_sync(kFull, ok);
+            const float wl = reduce_scatter<false, RG>(l, lane);
+            red[w4 * N + (RG == 32 ? lane : lane >> 1)] = wl;
+            if (!named_bar_and(barrier, 128, ok)) {
+                fail();
+                break;
+            }
+            tc_fence_after_sync();
+            const long long xs = c.x - c.t, xe = xs + c.T;
+            const bool sole = a.whole || (xs >= x0 && xe <= x1);
+            const int slot = (2 * g + (xs >= x0 ? 1 : 0)) * a.hb + hs;
+            float *const pp = a.part + (long long)slot * N * kVDim;
+            const int rows = b.rows - wg * RG;  // of this group
+            if (s < RG && s < rows) {
+                const float L = (red[s] + red[N + s]) + (red[2 * N + s] + red[3 * N + s]);
+                if (sole) {
+                    if (a.lse)
+                        a.lse[b.first + wg * RG + s] = L == 0.0f ? -INFINITY : (log2f(L) - mneg[s]) * cache::kLn2;
+                } else {
+                    __stcg(a.ml + ((long long)slot * N + wg * RG + s) * 2, -mneg[s]);
+                    __stcg(a.ml + ((long long)slot * N + wg * RG + s) * 2 + 1, L);
+                }
+                alpha[s] = L == 0.0f ? 0.0f : a.kv_scale / L;
+            }
+            named_bar_sync(barrier, 128);
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+                uint32_t o[32], o2[32];
+                tmem_ld32(tmem + K::kColO + (uint32_t)(k * K::kOCols + (N == 64 ? 32 * wg : 0)) + lane_off, o);
+                if (N == 32)
+                    tmem_ld32(tmem + K::kColO + (uint32_t)(k * K::kOCols + 32) + lane_off, o2);
+                tmem_ld_wait();
+                reg_fence_cols<32>(o);
+                if (N == 32)
+                    reg_fence_cols<32>(o2);
+#pragma unroll
+                for (int h = 0; h < RG; ++h) {
+                    float y = __uint_as_float(o[h]);
+                    if (N == 32)
+                        y += __uint_as_float(o2[h]) * (1.0f / K::kLo);
+                    if (N == 16)
+                        y += __uint_as_float(o[(h + 16) & 31]) * (1.0f / K::kLo);
+                    if (h < rows) {
+                        if (sole)
+                            a.out[(b.first + wg * RG + h) * kVDim + k * 128 + s] =
+                                __bfloat16_as_ushort(__float2bfloat16_rn(alpha[h] == 0.0f ? 0.0f : y * alpha[h]));
+                        else
+                            __stcg(pp + (wg * RG + h) * kVDim + k * 128 + s, y);
+                    }
+                }
+            }
+            tc_fence_before_sync();
+            if (!more)
+                break;
+            c = d;
+            // mneg and alpha are written anew only after every thread read them
+            named_bar_sync(barrier, 128);
+        }
+    } else if (lane == 0) {
+        // ------------------------------------------------------------ products
+        // Two streams, each issued as soon as its inputs are ready (polled without
+        // suspending): the scores of tile nq and the output update of tile np.
+        Cursor cq = s_range.at, cp = cq;
+        int nq = 0, np = 0, idle = 0;
+        bool more_q = true, more_p = true;
+        int qv = 0, pv = 0;  // value slots of tiles nq and np
+        uint32_t qvph = 0;
+        uint64_t idle_since = 0;
+        bool ok = true;
+        while (more_p) {
+            bool prog = false;
+            if (np < nq) {
+                const int sb = np & 1;
+                if (mbar_test(&bar[K::kBPFull + sb], (uint32_t)(np >> 1) & 1u)) {
+                    const bool first = np == 0 || cp.t == 0;
+                    tc_fence_after_sync();
+                    const uint32_t vb = sbase + K::kOffV + (uint32_t)pv * kVStage;
+                    const uint32_t pb = sbase + K::kOffP + (uint32_t)sb * K::kPStage;
+#pragma unroll
+                    for (int kb = 0; kb < 4; ++kb)
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks) {
+                            const uint64_t av = sw128_mnmajor_desc(vb + (uint32_t)kb * 1024u + (uint32_t)ks * 4u * kVGroup,
+                                                                   1024u, kVGroup);
+#pragma unroll
+                            for (int term = 0; term < (N == 64 ? 2 : 1); ++term)
+                                umma_e4m3(tmem + K::kColO + (uint32_t)(kb * K::kOCols), av,
+                                          sw64_mnmajor_desc(pb + (uint32_t)term * K::kPTerm + (uint32_t)ks * 2048u),
+                                          K::kIdescPV, (first && ks == 0 && term == 0) ? 0u : 1u);
+                        }
+                    umma_commit(&bar[K::kBVEmpty + pv]);
+                    umma_commit(&bar[K::kBPEmpty + sb]);
+                    if (++pv == K::kStages)
+                        pv = 0;
+                    ++np;
+                    more_p = next_tile(a, cp, x1);
+                    prog = true;
+                }
+            }
+            if (more_q) {
+                const int sb = nq & 1;
+                const uint32_t ph = (uint32_t)(nq >> 1) & 1u;
+                if (mbar_test(&bar[K::kBReady + qv], qvph) && mbar_test(&bar[K::kBSFree + sb], ph ^ 1u)) {
+                    fence_proxy_async_smem();  // cp.async writes -> tensor-core reads
+                    tc_fence_after_sync();
+                    const uint32_t vb = sbase + K::kOffV + (uint32_t)qv * kVStage;
+                    const uint32_t rb = sbase + K::kOffR + (uint32_t)sb * kRStage;
+                    const uint32_t qvb = sbase + K::kOffQV, qrb = sbase + K::kOffQR;
+                    const uint32_t dS = tmem + K::kColS + (uint32_t)(sb * N);
+#pragma unroll
+                    for (int kb = 0; kb < 4; ++kb)
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            umma_e4m3(dS, sw128_kmajor_desc_sbo(vb + (uint32_t)kb * 1024u + (uint32_t)ks * 32u, kVGroup),
+                                      sw128_kmajor_desc_sbo(qvb + (uint32_t)kb * 1024u + (uint32_t)ks * 32u, kVGroup),
+                                      K::kIdescQK, (kb | ks) != 0 ? 1u : 0u);
+#pragma unroll
+                    for (int ks = 0; ks < 2; ++ks)
+                        umma_e4m3(dS, sw64_kmajor_desc(rb + (uint32_t)ks * 32u, kRGroup),
+                                  sw64_kmajor_desc(qrb + (uint32_t)ks * 32u, kRGroup), K::kIdescQK, 1u);
+                    umma_commit(&bar[K::kBSFull + sb]);
+                    umma_commit(&bar[K::kBREmpty + sb]);
+                    ++nq;
+                    more_q = next_tile(a, cq, x1);
+                    if (!more_q || cq.t == 0)
+                        umma_commit(&bar[K::kBQEmpty]);
+                    if (++qv == K::kStages) {
+                        qv = 0;
+                        qvph ^= 1u;
+                    }
+                    prog = true;
+                }
+            }
+            if (prog) {
+                idle = 0;
+                idle_since = 0;
+                continue;
+            }
+            // nothing ready: every 64 empty polls, the abort flag and the clock
+            if (++idle < 64)
+                continue;
+            idle = 0;
+            const uint64_t now = global_timer_ns();
+            if (idle_since == 0) {
+                idle_since = now;
+            } else if (*abort_flag || now - idle_since > kWaitLimitNs) {
+                ok = false;
+                break;
+            }
+        }
+        if (!ok)
+            fail();
+        umma_commit(&bar[K::kBDrain]);
+        if (!mbar_wait(&bar[K::kBDrain], 0u, nullptr))
+            atomicOr(a.c.status, (uint32_t)PMQA_DEV_TIMEOUT);
+    }
+    __syncwarp();
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == K::kMmaWarp) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, K::kTmem);
+    }
+}
+
+// The parts of every unit that was cut, joined: block (g, y) takes packed row y of
+// the unit that range g begins and later ranges go on with; a thread four columns.
+template <int N>
+__global__ void __launch_bounds__(128) latent_join_kernel(const __grid_constant__ Args a)
+{
+    griddep_wait();
+    const int g = blockIdx.x, hs = blockIdx.y / N, row = blockIdx.y % N;
+    const int4 m = __ldcg(a.meta + g);
+    if (m.z < 2)
+        return;
+    Cursor c;
+    c.i = m.x;
+    c.u = m.y;
+    c.r = load_req(a, c.i, false);
+    const Block b = block_of(a, c, hs, N);
+    if (row >= b.rows)
+        return;
+    auto slot = [&](int k) -> long long {
+        return ((long long)(2 * (g + k) + (k == 0 ? 1 : 0)) * a.hb + hs) * N + row;
+    };
+    float M = -INFINITY;
+    for (int k = 0; k < m.z; ++k)
+        M = fmaxf(M, __ldcg(a.ml + slot(k) * 2));
+    float L = 0.0f;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int k = 0; k < m.z; ++k) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.ml + slot(k) * 2));
+        const float4 o = __ldcg(reinterpret_cast<const float4 *>(a.part + slot(k) * kVDim) + threadIdx.x);
+        const float w = ex2_approx(ml.x - M);
+        L += w * ml.y;
+        acc.x += w * o.x;
+        acc.y += w * o.y;
+        acc.z += w * o.z;
+        acc.w += w * o.w;
+    }
+    const float f = L == 0.0f ? 0.0f : a.kv_scale / L;
+    const float y[4] = {acc.x, acc.y, acc.z, acc.w};
+    uint32_t o[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        o[k] = __bfloat16_as_ushort(__float2bfloat16_rn(f == 0.0f ? 0.0f : y[2 * k] * f)) |
+               (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(f == 0.0f ? 0.0f : y[2 * k + 1] * f)) << 16;
+    *reinterpret_cast<uint2 *>(a.out + (b.first + row) * kVDim + 4 * threadIdx.x) = make_uint2(o[0], o[1]);
+    if (a.lse && threadIdx.x == 0)
+        a.lse[b.first + row] = L == 0.0f ? -INFINITY : (M + log2f(L)) * cache::kLn2;
+}
+
+template <int N>
+cudaError_t launch(Args &a, int sms, cudaStream_t st)
+{
+    a.hb = (a.heads + N - 1) / N;
+    a.toks = 1;
+    while (a.hb == 1 && 2 * a.toks * a.heads <= N)
+        a.toks *= 2;
+    a.ranges = std::max(1, std::min(sms, kMaxCtas) / a.hb);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = cache::allow_smem(latent_attn_kernel<N>, (int)Cfg<N>::kSmem, done);
+    if (e != cudaSuccess)
+        return e;
+    latent_attn_kernel<N><<<(unsigned)(a.ranges * a.hb), Cfg<N>::kThreads, Cfg<N>::kSmem, st>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || a.whole)
+        return e;
+    return cache::launch_early(latent_join_kernel<N>, dim3((unsigned)a.ranges, (unsigned)(a.hb * N)), 128, 0, true, st, a);
+}
+
+}  // namespace latent
+}  // namespace pmqa
+
+using namespace pmqa;
+using namespace pmqa::latent;
+
+extern "C" size_t pmqa_latent_workspace_bytes(void) { return kWorkspace; }
+
+extern "C" int pmqa_latent_attention(const pmqa_paged_rows *p, const void *q, const void *kv_cache, int32_t heads,
+                                     float q_scale, float kv_scale, float sm_scale, void *out, float *lse, void *ws,
+                                     size_t ws_bytes, pmqa_stream_t stream)
+{
+    int rc = paged::check_rows(p, true, ws, ws_bytes, kWorkspace);
+    if (rc != PMQA_OK)
+        return rc;
+    const double factor = (double)sm_scale * (double)q_scale * (double)kv_scale * 1.4426950408889634;
+    if (heads < 1 || !std::isfinite(kv_scale) || !std::isfinite(factor))
+        return PMQA_ERR_INVALID_ARG;
+    if (std::fabs(factor) > kMaxFactor)
+        return PMQA_ERR_UNSUPPORTED;
+    if (heads > kMaxHeads || (long long)p->rows * heads > 0x7FFFFFFFll)
+        return PMQA_ERR_UNSUPPORTED;
+    if (p->bs == 0 || p->rows == 0)
+        return PMQA_OK;
+    if (cache::missing(q, 16) || cache::missing(kv_cache, 16) || cache::missing(out, 16) || !cache::aligned(lse, 4))
+        return PMQA_ERR_INVALID_ARG;
+    int sms = 0;
+    if ((rc = cache::sm_count(&sms)) != PMQA_OK)
+        return rc;
+    Args a{};
+    a.c = paged::view(p, ws);
+    a.q = static_cast<const uint8_t *>(q);
+    a.kv = static_cast<const uint8_t *>(kv_cache);
+    a.out = static_cast<uint16_t *>(out);
+    a.lse = lse;
+    // 0: all scores alike; the kernel's masks need a factor that an infinity keeps
+    a.c_log2 = std::fabs(factor) < 1e-37 ? 1e-37f : (float)factor;
+    a.kv_scale = kv_scale;
+    a.heads = heads;
+    a.whole = (long long)p->block_size * p->max_blocks_per_seq <= kWhole ? 1 : 0;
+    uint8_t *const wsb = static_cast<uint8_t *>(ws);
+    a.meta = reinterpret_cast<int4 *>(wsb + kWsMeta);
+    a.ml = reinterpret_cast<float *>(wsb + kWsMl);
+    a.part = reinterpret_cast<float *>(wsb + kWsPart);
+    // packed rows of a block: as many as a request can have, up to 64
+    const long long most = std::min<long long>(p->max_rows, p->rows) * heads;
+    const cudaStream_t st = cache::cuda(stream);
+    const cudaError_t e = most <= 16   ? launch<16>(a, sms, st)
+                          : most <= 32 ? launch<32>(a, sms, st)
+                                       : launch<64>(a, sms, st);
+    return cache::code_of(e);
+}

@@ -46,20 +46,14 @@
 #include <cstdint>
 
 #include "../../include/pmqa.h"
+#include "pmqa_latent.cuh"
 #include "pmqa_mla_ptx.cuh"
 
 namespace pmqa {
 namespace mla {
 
-constexpr int kDim = 576;    // latent row: 512 value columns + 64 rotary columns
-constexpr int kVDim = 512;   // value columns
 constexpr int kHeads = 16;   // query heads per latent KV head
 constexpr int kTile = 128;   // listed positions per tile (the first product's M)
-constexpr int kChunks = kDim / 16;
-constexpr uint32_t kVGroup = 4u * 1024u;          // 8 rows x 4 value blocks of 128 bytes
-constexpr uint32_t kVStage = 16u * kVGroup;       // 128 rows of value columns (64 KB)
-constexpr uint32_t kRGroup = 512u;                // 8 rows x 64 rotary bytes
-constexpr uint32_t kRStage = 16u * kRGroup;       // 128 rows of rotary columns (8 KB)
 constexpr int kVStages = 3;                       // value ring
 constexpr int kRStages = 2;                       // rotary ring (free once the scores are done)
 constexpr uint32_t kPBytes = 32u * 128u;          // 32 rows (hi, lo) x 128 positions
@@ -107,22 +101,6 @@ static_assert(kOffR % 1024 == 0 && kOffQV % 1024 == 0 && kOffP % 1024 == 0, "ato
 
 constexpr uint32_t kIdescQK = idesc_e4m3_f32(128, kHeads);
 constexpr uint32_t kIdescPV = idesc_e4m3_f32(128, 2 * kHeads) | kIdescAMnMajor;
-
-// Byte offset of value chunk c (0..31) of row t: groups of 8 rows 4096 bytes
-// apart, four 1024-byte blocks of 8 rows x 128 bytes, 128-byte swizzle.
-__host__ __device__ constexpr uint32_t v_offset(int t, int c)
-{
-    return (uint32_t)(t >> 3) * kVGroup + (uint32_t)(c >> 3) * 1024u + (uint32_t)(t & 7) * 128u +
-           ((uint32_t)((c & 7) ^ (t & 7)) << 4);
-}
-
-// Byte offset of rotary chunk c (0..3) of row t: groups of 8 rows x 64 bytes,
-// 64-byte swizzle (chunk c of row r at c ^ (r >> 1)).
-__host__ __device__ constexpr uint32_t r_offset(int t, int c)
-{
-    return (uint32_t)(t >> 3) * kRGroup + (uint32_t)(t & 7) * 64u +
-           ((uint32_t)((c ^ ((t & 7) >> 1)) & 3) << 4);
-}
 
 struct Args {
     const uint8_t *q;     // [R, 16, 576]

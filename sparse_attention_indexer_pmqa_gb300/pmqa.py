@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+from typing import NamedTuple
 
 from . import build as _build
 
@@ -32,6 +33,14 @@ PMQA_OP_TOPK = 1
 PMQA_OP_LOGITS_TOPK = 2
 PMQA_OP_MQA_LOGITS = 3
 
+PMQA_ROPE_PLAIN = 0
+PMQA_ROPE_LINEAR = 1
+PMQA_ROPE_PARTS = 2
+
+PMQA_NORM_NONE = 0
+PMQA_NORM_LAYER = 1
+PMQA_NORM_RMS = 2
+
 PMQA_STAGE_SCORE = 1
 PMQA_STAGE_SELECT = 2
 
@@ -43,6 +52,8 @@ EXPORTED = (
     "pmqa_sparse_mla_decode", "pmqa_sparse_mla_decode_range", "pmqa_sparse_mla_merge",
     "pmqa_cache_workspace_bytes", "pmqa_cache_append", "pmqa_cache_attention",
     "pmqa_cache_weigh", "pmqa_cache_evict",
+    "pmqa_rope_frequencies", "pmqa_rope", "pmqa_index_append", "pmqa_index_read",
+    "pmqa_latent_append", "pmqa_latent_workspace_bytes", "pmqa_latent_attention",
     "pmqa_gather_probe", "pmqa_read_device_status", "pmqa_status_string", "pmqa_version",
 )
 
@@ -135,6 +146,121 @@ class CacheProblem(ctypes.Structure):
     ]
 
 
+class PagedRows(ctypes.Structure):
+    """Mirror of struct pmqa_paged_rows."""
+
+    _fields_ = [
+        ("block_tables", ctypes.c_void_p),
+        ("context_lens", ctypes.c_void_p),
+        ("row_begin", ctypes.c_void_p),
+        ("bs", ctypes.c_int32),
+        ("block_size", ctypes.c_int32),
+        ("max_blocks_per_seq", ctypes.c_int32),
+        ("rows", ctypes.c_int32),
+        ("max_rows", ctypes.c_int32),
+        ("num_blocks", ctypes.c_int64),
+    ]
+
+
+class RotaryArgs(ctypes.Structure):
+    """Mirror of struct pmqa_rotary."""
+
+    _fields_ = [
+        ("inv_freq", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p),
+        ("dim", ctypes.c_int32),
+        ("begin", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
+class Heads(ctypes.Structure):
+    """Mirror of struct pmqa_heads."""
+
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("x_row", ctypes.c_int64),
+        ("x_head", ctypes.c_int64),
+        ("out_row", ctypes.c_int64),
+        ("out_head", ctypes.c_int64),
+        ("heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+    ]
+
+
+class NormArgs(ctypes.Structure):
+    """Mirror of struct pmqa_norm."""
+
+    _fields_ = [
+        ("kind", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("weight", ctypes.c_void_p),
+        ("bias", ctypes.c_void_p),
+    ]
+
+
+class IndexRows(ctypes.Structure):
+    """Mirror of struct pmqa_index_rows."""
+
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("q", ctypes.c_void_p),
+        ("weights", ctypes.c_void_p),
+        ("q_out", ctypes.c_void_p),
+        ("weights_out", ctypes.c_void_p),
+        ("k_row", ctypes.c_int64),
+        ("q_row", ctypes.c_int64),
+        ("q_head", ctypes.c_int64),
+        ("weights_row", ctypes.c_int64),
+        ("heads", ctypes.c_int32),
+        ("weights_bf16", ctypes.c_int32),
+        ("weight_scale", ctypes.c_float),
+    ]
+
+
+class LatentRows(ctypes.Structure):
+    """Mirror of struct pmqa_latent_rows."""
+
+    _fields_ = [
+        ("c", ctypes.c_void_p),
+        ("k_pe", ctypes.c_void_p),
+        ("q_c", ctypes.c_void_p),
+        ("q_pe", ctypes.c_void_p),
+        ("q_out", ctypes.c_void_p),
+        ("c_row", ctypes.c_int64),
+        ("pe_row", ctypes.c_int64),
+        ("q_c_row", ctypes.c_int64),
+        ("q_c_head", ctypes.c_int64),
+        ("q_pe_row", ctypes.c_int64),
+        ("q_pe_head", ctypes.c_int64),
+        ("heads", ctypes.c_int32),
+        ("kv_scale", ctypes.c_float),
+        ("q_scale", ctypes.c_float),
+    ]
+
+
+class Rotary(NamedTuple):
+    """Rotary positions of the values begin .. begin + dim of a head: inv_freq is a
+    float64 tensor [dim / 2] on the device (see rope_frequencies)."""
+
+    inv_freq: object
+    begin: int = 0
+    interleaved: bool = False
+    scale: float = 1.0
+
+
+class Norm(NamedTuple):
+    """Normalisation of a row: kind PMQA_NORM_*, weight and bias float32 tensors of
+    the row's width or None."""
+
+    kind: int
+    weight: object = None
+    bias: object = None
+    eps: float = 1e-6
+
+
 _lib = None
 _torch_names = ()
 
@@ -158,7 +284,9 @@ def load(path: str | None = None) -> ctypes.CDLL:
     PM = ctypes.POINTER(MqaProblem)
     PL = ctypes.POINTER(MlaProblem)
     PC = ctypes.POINTER(CacheProblem)
-    F32 = ctypes.c_float
+    PR, PO = ctypes.POINTER(PagedRows), ctypes.POINTER(RotaryArgs)
+    PH, PN = ctypes.POINTER(Heads), ctypes.POINTER(NormArgs)
+    F32, F64 = ctypes.c_float, ctypes.c_double
     sig = {
         "pmqa_workspace_bytes": ([I32, I32, I32, I32, ctypes.c_int], SZ),
         "pmqa_workspace_init": ([V, SZ, V], ctypes.c_int),
@@ -180,6 +308,15 @@ def load(path: str | None = None) -> ctypes.CDLL:
         "pmqa_cache_weigh": ([PC, V, I32, F32, V, V, V, I64, V, SZ, V], ctypes.c_int),
         "pmqa_cache_evict": ([PC, V, I64, I32, I32, I32, V, I32, V, V, V, V, SZ, V],
                              ctypes.c_int),
+        "pmqa_rope_frequencies": ([I32, F64, ctypes.c_int, F64, F64, F64, F64,
+                                   ctypes.POINTER(F64), ctypes.POINTER(F32)], ctypes.c_int),
+        "pmqa_rope": ([PO, I32, PH, PH, V], ctypes.c_int),
+        "pmqa_index_append": ([PR, V, ctypes.POINTER(IndexRows), PN, PO, V, SZ, V], ctypes.c_int),
+        "pmqa_index_read": ([PR, V, V, V, V, V, SZ, V], ctypes.c_int),
+        "pmqa_latent_append": ([PR, V, ctypes.POINTER(LatentRows), PN, PO, V, SZ, V],
+                               ctypes.c_int),
+        "pmqa_latent_workspace_bytes": ([], SZ),
+        "pmqa_latent_attention": ([PR, V, V, I32, F32, F32, F32, V, V, V, SZ, V], ctypes.c_int),
         "pmqa_gather_probe": ([V, ctypes.c_uint64, V, I64, I32, I32, V, V], ctypes.c_int),
         "pmqa_read_device_status": ([V, V], ctypes.c_int),
         "pmqa_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -495,7 +632,7 @@ def make_cache_problem(k_cache, v_cache, k_scale, v_scale, block_tables, context
     num_blocks, kv_heads, block_size, head_dim = pool = k_cache.shape
     bs, width = block_tables.shape
     dev = k_cache.get_device()
-    f32, i32, _, _, _, codes = _torch()
+    f32, i32, _, _, _, codes, _ = _torch()
     code = k_cache.dtype
     if code not in codes or not k_cache.is_contiguous():
         raise AssertionError(f"expected contiguous float8_e4m3fn (or uint8) pools, got {code}")
@@ -532,19 +669,20 @@ def cache_workspace(device=None, stream=None):
 
 def _torch():
     """torch's float32, int32 and bfloat16, the calls that name the current device
-    and its stream's handle, and the pools' types (torch is imported on first use)."""
+    and its stream's handle, the pools' types and float64 (torch is imported on first
+    use)."""
     global _torch_names
     if not _torch_names:
         import torch
 
         _torch_names = (torch.float32, torch.int32, torch.bfloat16, torch._C._cuda_getDevice,
                         torch._C._cuda_getCurrentRawStream,
-                        (torch.float8_e4m3fn, torch.uint8))
+                        (torch.float8_e4m3fn, torch.uint8), torch.float64)
     return _torch_names
 
 
 def _like(t, dev: int, dtype, shape) -> None:
-    """What every operand of a pmqa_cache_* call must be: on the cache's
+    """What every operand of a call on a cache must be: on the cache's
     device, of the documented type and shape, contiguous."""
     if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
         raise AssertionError(f"expected a contiguous {dtype} tensor of shape {tuple(shape)} on the "
@@ -691,6 +829,315 @@ def pmqa_cache_evict(k_cache, v_cache, k_scale, v_scale, block_tables, context_l
                 recent, new_tables.data_ptr(), new_tables.shape[-1], kept.data_ptr(),
                 lens_out.data_ptr(), mass_out.data_ptr())
     return kept, lens_out, mass_out
+
+
+def rope_frequencies(dim: int, base: float = 10000.0, *, kind: int = PMQA_ROPE_PLAIN,
+                     factor: float = 1.0, trained: float = 4096.0, slow_turns: float = 1.0,
+                     fast_turns: float = 32.0, device=None):
+    """Radians per position of the dim / 2 pairs of a rotated head, scaled for contexts
+    `factor` times as long as `trained`, as a float64 tensor on the device, and the
+    scale that goes with them: what Rotary takes."""
+    import torch
+
+    if dim < 2 or dim % 2:
+        raise PmqaError(PMQA_ERR_INVALID_ARG, "pmqa_rope_frequencies")
+    out, scale = (ctypes.c_double * (dim // 2))(), ctypes.c_float()
+    _check(load().pmqa_rope_frequencies(dim, base, kind, factor, trained, slow_turns, fast_turns,
+                                        out, ctypes.byref(scale)), "pmqa_rope_frequencies")
+    return torch.tensor(list(out), dtype=torch.float64, device=device or "cuda"), scale.value
+
+
+def _rotary(rotary, positions, rows: int, dev: int):
+    """A pmqa_rotary, or None for none."""
+    if rotary is None:
+        return None
+    _, i32, _, _, _, _, f64 = _torch()
+    f = rotary.inv_freq
+    _like(f, dev, f64, (f.numel(),))
+    if positions is not None:
+        _like(positions, dev, i32, (rows,))
+    return RotaryArgs(f.data_ptr(), None if positions is None else positions.data_ptr(),
+                      2 * f.numel(), rotary.begin, int(bool(rotary.interleaved)), rotary.scale)
+
+
+def _norm(norm, width: int, dev: int):
+    """A pmqa_norm, or None for none."""
+    if norm is None or norm.kind == PMQA_NORM_NONE:
+        return None
+    f32 = _torch()[0]
+    for t in (norm.weight, norm.bias):
+        if t is not None:
+            _like(t, dev, f32, (width,))
+    return NormArgs(norm.kind, norm.eps, None if norm.weight is None else norm.weight.data_ptr(),
+                    None if norm.bias is None else norm.bias.data_ptr())
+
+
+def _strided(t, dev: int, shape) -> None:
+    """An operand of bf16 rows: on the cache's device, of the documented shape, its last
+    dimension contiguous (the others may be strided)."""
+    bf16 = _torch()[2]
+    if t.shape != shape or t.dtype is not bf16 or t.get_device() != dev or t.stride(-1) != 1:
+        raise AssertionError(f"expected a {bf16} tensor of shape {tuple(shape)} with a contiguous last "
+                             f"dimension on the cache's device ({dev}), got {tuple(t.shape)} {t.dtype} "
+                             f"with strides {t.stride()} on {t.device}")
+
+
+def _step(t, d: int) -> int:
+    """The stride of dimension d (of one entry: none)."""
+    return t.stride(d) if t.shape[d] > 1 else 0
+
+
+def _heads(x, out) -> Heads:
+    """A pmqa_heads of x and out, [rows, heads, head_dim]."""
+    return Heads(x.data_ptr(), out.data_ptr(), _step(x, 0), _step(x, 1), _step(out, 0), _step(out, 1),
+                 x.shape[1], x.shape[2])
+
+
+@_on_stream
+def pmqa_rope(x, positions, rotary: Rotary, *, other=None, out=None, other_out=None, stream=None):
+    """Rotate the heads of x (bf16 [rows, heads, head_dim], the last dimension
+    contiguous) at positions (int32 [rows]) into `out` (a new tensor unless given; x
+    itself rotates in place). `other`: a second tensor of the same rows (the keys
+    beside the queries), rotated by the same launch into other_out; then both results
+    are returned."""
+    import torch
+
+    rows, dev = x.shape[0], x.get_device()
+    pairs = []
+    for t, o in ((x, out), (other, other_out)):
+        if t is None:
+            continue
+        _strided(t, dev, (rows, *t.shape[1:]))
+        if t.dim() != 3:
+            raise AssertionError(f"expected [rows, heads, head_dim], got shape {tuple(t.shape)}")
+        if o is None:
+            o = torch.empty(t.shape, dtype=t.dtype, device=t.device)
+        else:
+            _strided(o, dev, t.shape)
+        pairs.append((t, o))
+    r = _rotary(rotary, positions, rows, dev)
+    a = [_heads(t, o) for t, o in pairs]
+    _device_call("pmqa_rope", dev, stream, r, rows, a[0], a[1] if len(a) > 1 else None)
+    return pairs[0][1] if other is None else (pairs[0][1], pairs[1][1])
+
+
+def _device_call(name: str, dev: int, stream, *args) -> None:
+    """Call a function of the library with device `dev` current, on its current stream
+    unless one is given."""
+    if dev < 0:
+        raise AssertionError(f"{name} takes cuda tensors")
+    current_device, raw_stream = _torch()[3:5]
+    if dev != current_device():
+        import torch
+
+        with torch.cuda.device(dev):
+            return _device_call(name, dev, stream, *args)
+    rc = getattr(_lib or load(), name)(*args, raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc != PMQA_OK:
+        raise PmqaError(rc, name)
+
+
+def _paged_call(name: str, dev: int, stream, ws, size, *args) -> None:
+    """A call that ends with a workspace (made by `size` unless given) and a stream."""
+    if dev < 0:
+        raise AssertionError(f"{name} takes cuda tensors")
+    if ws is None:
+        ws = size(f"cuda:{dev}", stream)
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise AssertionError("expected a contiguous workspace on the cache's device")
+    _device_call(name, dev, stream, *args, ws.data_ptr(), ws.nbytes)
+
+
+def make_paged_rows(kv_cache, width: int, block_tables, context_lens, row_begin, rows: int,
+                    max_rows: int) -> PagedRows:
+    """Fill a pmqa_paged_rows for a pool [num_blocks, block_size, width] of bytes or
+    e4m3 values (context_lens None where the call has none)."""
+    _, i32, _, _, _, codes, _ = _torch()
+    if kv_cache.dim() != 3 or kv_cache.shape[2] != width or kv_cache.dtype not in codes or \
+            not kv_cache.is_contiguous():
+        raise AssertionError(f"expected a contiguous pool [num_blocks, block_size, {width}] of uint8 or "
+                             f"float8_e4m3fn, got {tuple(kv_cache.shape)} {kv_cache.dtype}")
+    dev = kv_cache.get_device()
+    bs, blocks = block_tables.shape
+    _like(block_tables, dev, i32, (bs, blocks))
+    if context_lens is not None:
+        _like(context_lens, dev, i32, (bs,))
+    _like(row_begin, dev, i32, (bs + 1,))
+    return PagedRows(block_tables.data_ptr(), None if context_lens is None else context_lens.data_ptr(),
+                     row_begin.data_ptr(), bs, kv_cache.shape[1], blocks, rows, max_rows,
+                     kv_cache.shape[0])
+
+
+def _status_workspace(device=None, stream=None):
+    """The smallest workspace: a status word."""
+    import torch
+
+    with torch.cuda.stream(stream):
+        ws = torch.empty(256, dtype=torch.uint8, device=device or "cuda")
+        with torch.cuda.device(ws.device):
+            pmqa_workspace_init(ws, stream=stream)
+    return ws
+
+
+def pmqa_latent_workspace_bytes() -> int:
+    return int(load().pmqa_latent_workspace_bytes())
+
+
+def latent_workspace(device=None, stream=None):
+    """A zero-initialised workspace for pmqa_latent_attention (and every other call on
+    the indexer's and the latent cache). With a `stream` the memory is that stream's too."""
+    import torch
+
+    with torch.cuda.stream(stream):
+        ws = torch.empty(pmqa_latent_workspace_bytes(), dtype=torch.uint8, device=device or "cuda")
+        with torch.cuda.device(ws.device):
+            pmqa_workspace_init(ws, stream=stream)
+    return ws
+
+
+@_on_stream
+def pmqa_index_append(k, kv_cache, block_tables, context_lens, row_begin, max_rows: int, *, q=None,
+                      weights=None, weight_scale: float = 1.0, norm: Norm | None = None,
+                      rotary: Rotary | None = None, positions=None, q_out=None, weights_out=None,
+                      ws=None, stream=None):
+    """Normalise, rotate and quantise a step's indexer keys k (bf16 [rows, 128], or None)
+    into their slots of kv_cache, and its queries q (bf16 [rows, heads, 128]) with their
+    head weights (float32 or bfloat16 [rows, heads]) into what the logits calls take:
+    returns (q_out fp8 [rows, heads, 128], weights_out float32 [rows, heads]) where q
+    is given. positions: int32 [rows], the rows' slots unless given."""
+    import torch
+
+    if k is None and q is None:
+        raise AssertionError("expected keys, queries or both")
+    rows, dev = (k if q is None else q).shape[0], kv_cache.get_device()
+    p = make_paged_rows(kv_cache, 132, block_tables, context_lens, row_begin, rows, max_rows)
+    x = IndexRows()
+    if k is not None:
+        _strided(k, dev, (rows, 128))
+        x.k, x.k_row = k.data_ptr(), _step(k, 0)
+    if q is not None:
+        heads = q.shape[1]
+        _strided(q, dev, (rows, heads, 128))
+        if weights.shape != (rows, heads) or weights.dtype not in (torch.float32, torch.bfloat16) or \
+                weights.get_device() != dev or _step(weights, 1) > 1:
+            raise AssertionError(f"expected float32 or bfloat16 weights of shape {(rows, heads)} with a "
+                                 f"contiguous last dimension, got {tuple(weights.shape)} {weights.dtype}")
+        if q_out is None:
+            q_out = torch.empty((rows, heads, 128), dtype=torch.float8_e4m3fn, device=q.device)
+        else:
+            _codes_like(q_out, dev, (rows, heads, 128))
+        if weights_out is None:
+            weights_out = torch.empty((rows, heads), dtype=torch.float32, device=q.device)
+        else:
+            _like(weights_out, dev, torch.float32, (rows, heads))
+        x.q, x.q_row, x.q_head = q.data_ptr(), _step(q, 0), _step(q, 1)
+        x.weights, x.weights_row = weights.data_ptr(), _step(weights, 0)
+        x.weights_bf16 = int(weights.dtype is torch.bfloat16)
+        x.q_out, x.weights_out = q_out.data_ptr(), weights_out.data_ptr()
+        x.heads, x.weight_scale = heads, weight_scale
+    _paged_call("pmqa_index_append", dev, stream, ws, _status_workspace, p, kv_cache.data_ptr(), x,
+                _norm(norm, 128, dev), _rotary(rotary, positions, rows, dev))
+    return None if q is None else (q_out, weights_out)
+
+
+def _codes_like(t, dev: int, shape) -> None:
+    """An output of e4m3 codes."""
+    codes = _torch()[5]
+    if t.shape != shape or t.dtype not in codes or t.get_device() != dev or not t.is_contiguous():
+        raise AssertionError(f"expected a contiguous float8_e4m3fn (or uint8) tensor of shape {tuple(shape)} "
+                             f"on the cache's device ({dev}), got {tuple(t.shape)} {t.dtype} on {t.device}")
+
+
+@_on_stream
+def pmqa_index_read(kv_cache, block_tables, row_begin, rows: int, *, start=None, k=None,
+                    k_scale=None, ws=None, stream=None):
+    """Cached indexer keys as contiguous rows: row row_begin[i] + j of (k fp8 [rows, 128],
+    k_scale float32 [rows]) is the token at slot start[i] + j of request i (start: int32
+    [bs], zeros unless given)."""
+    import torch
+
+    dev = kv_cache.get_device()
+    p = make_paged_rows(kv_cache, 132, block_tables, None, row_begin, rows, 0)
+    if start is not None:
+        _like(start, dev, torch.int32, (p.bs,))
+    if k is None:
+        k = torch.empty((max(rows, 0), 128), dtype=torch.float8_e4m3fn, device=kv_cache.device)
+    else:
+        _codes_like(k, dev, (rows, 128))
+    if k_scale is None:
+        k_scale = torch.empty(max(rows, 0), dtype=torch.float32, device=kv_cache.device)
+    else:
+        _like(k_scale, dev, torch.float32, (rows,))
+    _paged_call("pmqa_index_read", dev, stream, ws, _status_workspace, p, kv_cache.data_ptr(), _addr(start),
+                k.data_ptr(), k_scale.data_ptr())
+    return k, k_scale
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+@_on_stream
+def pmqa_latent_append(c, k_pe, kv_cache, block_tables, context_lens, row_begin, max_rows: int,
+                       kv_scale: float, *, q_c=None, q_pe=None, q_scale: float = 1.0,
+                       norm: Norm | None = None, rotary: Rotary | None = None, positions=None,
+                       q_out=None, ws=None, stream=None):
+    """Quantise a step's latent rows (c bf16 [rows, 512], normalised; k_pe bf16
+    [rows, 64], rotated; both or neither None) into their slots of the latent cache, and
+    its queries (q_c bf16 [rows, heads, 512], q_pe bf16 [rows, heads, 64]) into q_out fp8
+    [rows, heads, 576], which is returned where q_c is given."""
+    import torch
+
+    if c is None and q_c is None:
+        raise AssertionError("expected latent rows, queries or both")
+    rows, dev = (c if q_c is None else q_c).shape[0], kv_cache.get_device()
+    p = make_paged_rows(kv_cache, 576, block_tables, context_lens, row_begin, rows, max_rows)
+    x = LatentRows(kv_scale=kv_scale, q_scale=q_scale)
+    if c is not None:
+        _strided(c, dev, (rows, 512))
+        _strided(k_pe, dev, (rows, 64))
+        x.c, x.c_row, x.k_pe, x.pe_row = c.data_ptr(), _step(c, 0), k_pe.data_ptr(), _step(k_pe, 0)
+    if q_c is not None:
+        heads = q_c.shape[1]
+        _strided(q_c, dev, (rows, heads, 512))
+        _strided(q_pe, dev, (rows, heads, 64))
+        if q_out is None:
+            q_out = torch.empty((rows, heads, 576), dtype=torch.float8_e4m3fn, device=q_c.device)
+        else:
+            _codes_like(q_out, dev, (rows, heads, 576))
+        x.q_c, x.q_c_row, x.q_c_head = q_c.data_ptr(), _step(q_c, 0), _step(q_c, 1)
+        x.q_pe, x.q_pe_row, x.q_pe_head = q_pe.data_ptr(), _step(q_pe, 0), _step(q_pe, 1)
+        x.q_out, x.heads = q_out.data_ptr(), heads
+    _paged_call("pmqa_latent_append", dev, stream, ws, _status_workspace, p, kv_cache.data_ptr(), x,
+                _norm(norm, 512, dev), _rotary(rotary, positions, rows, dev))
+    return q_out
+
+
+@_on_stream
+def pmqa_latent_attention(q, kv_cache, block_tables, context_lens, row_begin, max_rows: int,
+                          q_scale: float, kv_scale: float, sm_scale: float, *, out=None, lse=None,
+                          want_lse: bool = False, ws=None, stream=None):
+    """Attention of q (fp8 [rows, heads, 576]) to all the latent tokens that its rows
+    see: bf16 out [rows, heads, 512] (and float32 lse [rows, heads] when asked for or
+    given)."""
+    import torch
+
+    rows, heads = q.shape[:2]
+    dev = kv_cache.get_device()
+    p = make_paged_rows(kv_cache, 576, block_tables, context_lens, row_begin, rows, max_rows)
+    f32, _, bf16 = _torch()[:3]
+    _codes_like(q, dev, (rows, heads, 576))
+    if out is None:
+        out = torch.empty((rows, heads, 512), dtype=bf16, device=q.device)
+    else:
+        _like(out, dev, bf16, (rows, heads, 512))
+    if lse is None:
+        lse = torch.empty((rows, heads), dtype=f32, device=q.device) if want_lse else None
+    else:
+        _like(lse, dev, f32, (rows, heads))
+    _paged_call("pmqa_latent_attention", dev, stream, ws, latent_workspace, p, q.data_ptr(), kv_cache.data_ptr(),
+                heads, q_scale, kv_scale, sm_scale, out.data_ptr(), _addr(lse))
+    return out if lse is None else (out, lse)
 
 
 def pmqa_gather_probe(pool, rows, row_pitch, method, *, out=None, stream=None):
