@@ -250,21 +250,21 @@ extern "C" int pmqa_index_append(const pmqa_paged_rows *p, void *kv_cache, const
     IndexArgs a{};
     if (!x || (rc = check_norm(norm, &a.n)) != PMQA_OK || (rc = check_rotary(rotary, kDimI, false, &a.r)) != PMQA_OK)
         return x ? rc : PMQA_ERR_INVALID_ARG;
-    if (x->q && (x->heads < 1 || !std::isfinite(x->weight_scale) || x->weights_row < 0))
+    if (x->q && (x->heads < 1 || !std::isfinite(x->weight_scale) || (x->weights_row < 0 && p->rows > 1)))
         return PMQA_ERR_INVALID_ARG;
     if (x->q && (long long)x->heads * p->rows > 0x7FFFFFFFll)
         return PMQA_ERR_UNSUPPORTED;
     if (p->bs == 0 || p->rows == 0 || (!x->k && !x->q))
         return PMQA_OK;
-    if (x->k && (cache::missing(kv_cache, 4) || bad_rows(x->k, 16, x->k_row)))
+    if (x->k && (cache::missing(kv_cache, 4) || bad_rows(x->k, 16, p->rows, x->k_row)))
         return PMQA_ERR_INVALID_ARG;
     if (x->q) {
         const long long n = (long long)p->rows * x->heads;
-        if (bad_rows(x->q, 16, x->q_row, x->q_head) || cache::missing(x->q_out, 8) ||
+        if (bad_rows(x->q, 16, p->rows, x->q_row, x->heads, x->q_head) || cache::missing(x->q_out, 8) ||
             cache::missing(x->weights, x->weights_bf16 ? 2 : 4) || cache::missing(x->weights_out, 4))
             return PMQA_ERR_INVALID_ARG;
         // weights in place, or apart
-        const long long in = ((p->rows - 1ll) * x->weights_row + x->heads) * (x->weights_bf16 ? 2 : 4);
+        const long long in = ((p->rows > 1 ? (p->rows - 1ll) * x->weights_row : 0ll) + x->heads) * (x->weights_bf16 ? 2 : 4);
         const bool same = x->weights == x->weights_out && !x->weights_bf16 &&
                           (x->weights_row == x->heads || p->rows == 1);
         if (!same && cache::overlap(x->weights, in, x->weights_out, 4 * n))

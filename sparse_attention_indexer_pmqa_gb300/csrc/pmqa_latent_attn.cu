@@ -46,9 +46,8 @@ constexpr int kMaxCtas = 160;   // workspace parts: 2 per CTA
 constexpr int kPad = 2;         // tiles' worth of starting and ending a block
 constexpr int kLeast = 2;       // fewest tiles that a CTA takes
 constexpr int kWhole = 512;     // tables of up to so many tokens: blocks are not cut
-constexpr float kBase = 4.0f;   // p = 2^(x - m + kBase)
-constexpr float kTop = 8.0f;    // m moves when a p passes 2^kTop
-constexpr float kUnseen = 1e30f;   // kBase - m of a row that has seen no score: above every |x|
+constexpr float kTop = 8.0f;    // p = 2^(x - m); m moves when a p passes 2^kTop
+constexpr float kUnseen = 1e30f;   // -m of a row that has seen no score: above every |x|
 constexpr double kMaxFactor = 1e20;  // |c_log2|: times a product of two rows (1.2e8) well below kUnseen
 
 constexpr size_t kWsMeta = cache::kStatusBytes;
@@ -310,14 +309,14 @@ struct Cfg {
     static constexpr uint32_t kOffP = kOffQR + ((N / 8) * kRGroup + 1023) / 1024 * 1024;
     static constexpr uint32_t kOffMask = kOffP + kPBytes;               // [stages][4] words
     static constexpr uint32_t kOffLim = kOffMask + kStages * 16;        // [2][N] ints
-    static constexpr uint32_t kOffM = kOffLim + 2 * N * 4;              // [N] floats: kBase - m
+    static constexpr uint32_t kOffM = kOffLim + 2 * N * 4;              // [N] floats: -m       
     static constexpr uint32_t kOffAlpha = kOffM + N * 4;                // [N]
     static constexpr uint32_t kOffRed = kOffAlpha + N * 4;              // [4][N]
     static constexpr uint32_t kOffBar = kOffRed + 4 * N * 4;
     static constexpr int kBMask = 0;                        // [stages] masks written: 4 producer warps
     static constexpr int kBReady = kBMask + kStages;        // [stages] rows landed: 128 cp.async arrivals
-    static constexpr int kBVEmpty = kBReady + kStages;      // [stages] values read: MMA commit
-    static constexpr int kBREmpty = kBVEmpty + kStages;     // [2] rotary columns read: MMA commit
+    static constexpr int kBVEmpty = kBReady + kStages;      // [stages][4] values of 32 tokens read: MMA commit
+    static constexpr int kBREmpty = kBVEmpty + 4 * kStages;    // [2] rotary columns read: MMA commit
     static constexpr int kBSFull = kBREmpty + 2;            // [2] scores in TMEM: MMA commit
     static constexpr int kBSFree = kBSFull + 2;             // [2] scores read: softmax warps
     static constexpr int kBPFull = kBSFree + 2;             // [2] P written, O rescaled: softmax warps
@@ -333,6 +332,7 @@ struct Cfg {
     static constexpr uint32_t kIdescQK = idesc_e4m3_f32(128, N);
     // A and B MN-major (bits 15 and 16)
     static constexpr uint32_t kIdescPV = idesc_e4m3_f32(128, kOCols) | kIdescAMnMajor | (1u << 16);
+    static constexpr uint32_t kIdescPVLo = kIdescPV | cache::kIdescBE5m2;  // N = 64
 };
 
 // Shared-memory matrix descriptor, MN-major with the 64-byte swizzle: one row of 64
@@ -377,18 +377,30 @@ __device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t b)
     return r;
 }
 
+__device__ __forceinline__ uint32_t e5m2x2_of_f16x2(uint32_t h2)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
+    return r;
+}
+
 // Two weights as their terms (bytes 0 and 1): the f16 value of p is off by 2^-11 at
-// most, its difference from the first term exact.
-template <bool UP>
+// most, its difference from the first term exact. SAME: both terms go into one
+// accumulator, so the second has the first's unit: e5m2, which reaches down to 2^-17.
+// Otherwise it is e4m3 of 16 times the difference.
+template <bool SAME>
 __device__ __forceinline__ void split2(float p0, float p1, uint32_t &hi, uint32_t &lo)
 {
     const uint32_t p = cache::pack_f16x2(p0, p1);
     hi = e4m3x2_of_f16x2(p);
     uint32_t d = f16x2_of_e4m3x2(hi);
     asm("sub.rn.f16x2 %0, %1, %0;" : "+r"(d) : "r"(p));
-    if (UP)
+    if (SAME) {
+        lo = e5m2x2_of_f16x2(d);
+    } else {
         asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(d) : "r"(0x4C004C00u));  // 16
-    lo = e4m3x2_of_f16x2(d);
+        lo = e4m3x2_of_f16x2(d);
+    }
 }
 
 // Four codes, NaN (0x7F, 0xFF) replaced by 0.
@@ -430,7 +442,8 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
         for (int s = 0; s < K::kStages; ++s) {
             mbar_init(&bar[K::kBMask + s], 4);
             mbar_init(&bar[K::kBReady + s], 128);
-            mbar_init(&bar[K::kBVEmpty + s], 1);
+            for (int w = 0; w < 4; ++w)
+                mbar_init(&bar[K::kBVEmpty + 4 * s + w], 1);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bar[K::kBREmpty + s], 1);
@@ -503,7 +516,8 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
                     cp_async_16(dst, src + (r < b.rows ? r * kDim + ch * 16 : 0), r < b.rows ? 16u : 0u);
                 }
             }
-            if (!__all_sync(kFull, mbar_wait(&bar[K::kBVEmpty + vs], vph ^ 1u, abort_flag) &&
+            // this warp's 32 tokens of the slot
+            if (!__all_sync(kFull, mbar_wait(&bar[K::kBVEmpty + 4 * vs + warp], vph ^ 1u, abort_flag) &&
                                        mbar_wait(&bar[K::kBREmpty + rs], rph ^ 1u, abort_flag))) {
                 fail();
                 break;
@@ -516,7 +530,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
             }
             const uint32_t vdst = sbase + K::kOffV + (uint32_t)vs * kVStage;
             const uint32_t rdst = sbase + K::kOffR + (uint32_t)rs * kRStage;
-#pragma unroll 4
+#pragma unroll 8
             for (int tt = 0; tt < 32; ++tt) {
                 const uint32_t sr = __shfl_sync(kFull, srow, tt);
                 const bool is = sr != paged::kNoRow;
@@ -653,7 +667,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
                     const float m = mneg[lane];
                     float f = 1.0f;
                     if (x + m > kTop) {
-                        const float to = kBase - x;
+                        const float to = -x;
                         f = ex2_approx(to - m);  // 0 where no score was seen before
                         mneg[lane] = to;
                     }
@@ -677,8 +691,8 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
                     l[h + e] += p[e];
                 }
                 uint32_t h0, l0, h1, l1;
-                split2<N != 64>(p[0], p[1], h0, l0);
-                split2<N != 64>(p[2], p[3], h1, l1);
+                split2<N == 64>(p[0], p[1], h0, l0);
+                split2<N == 64>(p[2], p[3], h1, l1);
                 hi[h / 4] = h0 | h1 << 16;
                 lo[h / 4] = l0 | l1 << 16;
             }
@@ -792,10 +806,13 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
             // mneg and alpha are written anew only after every thread read them
             named_bar_sync(barrier, 128);
         }
-    } else if (lane == 0) {
+    } else {
         // ------------------------------------------------------------ products
         // Two streams, each issued as soon as its inputs are ready (polled without
-        // suspending): the scores of tile nq and the output update of tile np.
+        // suspending): the scores of tile nq and the output update of tile np. The
+        // whole warp walks them, so that descriptors stay in uniform registers; one
+        // elected lane issues. The update goes 32 tokens at a time over all value
+        // columns, and each 32 tokens' values are free for the loads when it is done.
         Cursor cq = s_range.at, cp = cq;
         int nq = 0, np = 0, idle = 0;
         bool more_q = true, more_p = true;
@@ -803,29 +820,33 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
         uint32_t qvph = 0;
         uint64_t idle_since = 0;
         bool ok = true;
+        const uint64_t kd = sw128_kmajor_desc_sbo(sbase, kVGroup) , vd = sw128_mnmajor_desc(sbase, 1024u, kVGroup);
+        const uint64_t rd = sw64_kmajor_desc(sbase, kRGroup), pd = sw64_mnmajor_desc(sbase);
         while (more_p) {
             bool prog = false;
             if (np < nq) {
                 const int sb = np & 1;
-                if (mbar_test(&bar[K::kBPFull + sb], (uint32_t)(np >> 1) & 1u)) {
+                if (__all_sync(kFull, mbar_test(&bar[K::kBPFull + sb], (uint32_t)(np >> 1) & 1u))) {
                     const bool first = np == 0 || cp.t == 0;
                     tc_fence_after_sync();
-                    const uint32_t vb = sbase + K::kOffV + (uint32_t)pv * kVStage;
-                    const uint32_t pb = sbase + K::kOffP + (uint32_t)sb * K::kPStage;
-#pragma unroll
-                    for (int kb = 0; kb < 4; ++kb)
+                    const uint64_t av = vd + ((K::kOffV + (uint32_t)pv * kVStage) >> 4);
+                    const uint64_t bv = pd + ((K::kOffP + (uint32_t)sb * K::kPStage) >> 4);
+                    if (elect_one()) {
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks) {
-                            const uint64_t av = sw128_mnmajor_desc(vb + (uint32_t)kb * 1024u + (uint32_t)ks * 4u * kVGroup,
-                                                                   1024u, kVGroup);
 #pragma unroll
-                            for (int term = 0; term < (N == 64 ? 2 : 1); ++term)
-                                umma_e4m3(tmem + K::kColO + (uint32_t)(kb * K::kOCols), av,
-                                          sw64_mnmajor_desc(pb + (uint32_t)term * K::kPTerm + (uint32_t)ks * 2048u),
-                                          K::kIdescPV, (first && ks == 0 && term == 0) ? 0u : 1u);
+                            for (int kb = 0; kb < 4; ++kb)
+#pragma unroll
+                                for (int term = 0; term < (N == 64 ? 2 : 1); ++term)
+                                    umma_e4m3(tmem + K::kColO + (uint32_t)(kb * K::kOCols),
+                                              av + (((uint32_t)kb * 1024u + (uint32_t)ks * 4u * kVGroup) >> 4),
+                                              bv + (((uint32_t)term * K::kPTerm + (uint32_t)ks * 2048u) >> 4),
+                                              term ? K::kIdescPVLo : K::kIdescPV, (first && ks == 0 && term == 0) ? 0u : 1u);
+                            umma_commit(&bar[K::kBVEmpty + 4 * pv + ks]);
                         }
-                    umma_commit(&bar[K::kBVEmpty + pv]);
-                    umma_commit(&bar[K::kBPEmpty + sb]);
+                        umma_commit(&bar[K::kBPEmpty + sb]);
+                    }
+                    __syncwarp();
                     if (++pv == K::kStages)
                         pv = 0;
                     ++np;
@@ -836,30 +857,31 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
             if (more_q) {
                 const int sb = nq & 1;
                 const uint32_t ph = (uint32_t)(nq >> 1) & 1u;
-                if (mbar_test(&bar[K::kBReady + qv], qvph) && mbar_test(&bar[K::kBSFree + sb], ph ^ 1u)) {
+                if (__all_sync(kFull, mbar_test(&bar[K::kBReady + qv], qvph) && mbar_test(&bar[K::kBSFree + sb], ph ^ 1u))) {
                     fence_proxy_async_smem();  // cp.async writes -> tensor-core reads
                     tc_fence_after_sync();
-                    const uint32_t vb = sbase + K::kOffV + (uint32_t)qv * kVStage;
-                    const uint32_t rb = sbase + K::kOffR + (uint32_t)sb * kRStage;
-                    const uint32_t qvb = sbase + K::kOffQV, qrb = sbase + K::kOffQR;
+                    const uint64_t av = kd + ((K::kOffV + (uint32_t)qv * kVStage) >> 4), bv = kd + (K::kOffQV >> 4);
+                    const uint64_t ar = rd + ((K::kOffR + (uint32_t)sb * kRStage) >> 4), br = rd + (K::kOffQR >> 4);
                     const uint32_t dS = tmem + K::kColS + (uint32_t)(sb * N);
-#pragma unroll
-                    for (int kb = 0; kb < 4; ++kb)
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            umma_e4m3(dS, sw128_kmajor_desc_sbo(vb + (uint32_t)kb * 1024u + (uint32_t)ks * 32u, kVGroup),
-                                      sw128_kmajor_desc_sbo(qvb + (uint32_t)kb * 1024u + (uint32_t)ks * 32u, kVGroup),
-                                      K::kIdescQK, (kb | ks) != 0 ? 1u : 0u);
-#pragma unroll
-                    for (int ks = 0; ks < 2; ++ks)
-                        umma_e4m3(dS, sw64_kmajor_desc(rb + (uint32_t)ks * 32u, kRGroup),
-                                  sw64_kmajor_desc(qrb + (uint32_t)ks * 32u, kRGroup), K::kIdescQK, 1u);
-                    umma_commit(&bar[K::kBSFull + sb]);
-                    umma_commit(&bar[K::kBREmpty + sb]);
                     ++nq;
                     more_q = next_tile(a, cq, x1);
-                    if (!more_q || cq.t == 0)
-                        umma_commit(&bar[K::kBQEmpty]);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kb = 0; kb < 4; ++kb)
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks)
+                                umma_e4m3(dS, av + (((uint32_t)kb * 1024u + (uint32_t)ks * 32u) >> 4),
+                                          bv + (((uint32_t)kb * 1024u + (uint32_t)ks * 32u) >> 4), K::kIdescQK,
+                                          (kb | ks) != 0 ? 1u : 0u);
+#pragma unroll
+                        for (int ks = 0; ks < 2; ++ks)
+                            umma_e4m3(dS, ar + 2u * ks, br + 2u * ks, K::kIdescQK, 1u);
+                        umma_commit(&bar[K::kBSFull + sb]);
+                        umma_commit(&bar[K::kBREmpty + sb]);
+                        if (!more_q || cq.t == 0)
+                            umma_commit(&bar[K::kBQEmpty]);
+                    }
+                    __syncwarp();
                     if (++qv == K::kStages) {
                         qv = 0;
                         qvph ^= 1u;
@@ -876,19 +898,21 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
             if (++idle < 64)
                 continue;
             idle = 0;
-            const uint64_t now = global_timer_ns();
+            const uint64_t now = __shfl_sync(kFull, global_timer_ns(), 0);
             if (idle_since == 0) {
                 idle_since = now;
-            } else if (*abort_flag || now - idle_since > kWaitLimitNs) {
+            } else if (__any_sync(kFull, *abort_flag != 0) || now - idle_since > kWaitLimitNs) {
                 ok = false;
                 break;
             }
         }
         if (!ok)
             fail();
-        umma_commit(&bar[K::kBDrain]);
-        if (!mbar_wait(&bar[K::kBDrain], 0u, nullptr))
-            atomicOr(a.c.status, (uint32_t)PMQA_DEV_TIMEOUT);
+        if (elect_one()) {
+            umma_commit(&bar[K::kBDrain]);
+            if (!mbar_wait(&bar[K::kBDrain], 0u, nullptr))
+                atomicOr(a.c.status, (uint32_t)PMQA_DEV_TIMEOUT);
+        }
     }
     __syncwarp();
     tc_fence_before_sync();

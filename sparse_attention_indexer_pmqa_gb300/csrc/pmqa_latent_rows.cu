@@ -177,9 +177,10 @@ extern "C" int pmqa_latent_append(const pmqa_paged_rows *p, void *kv_cache, cons
         return PMQA_ERR_UNSUPPORTED;
     if (p->bs == 0 || p->rows == 0 || (!x->c && !x->q_c))
         return PMQA_OK;
-    if (x->c && (cache::missing(kv_cache, 8) || bad_rows(x->c, 16, x->c_row) || bad_rows(x->k_pe, 16, x->pe_row)))
+    if (x->c && (cache::missing(kv_cache, 8) || bad_rows(x->c, 16, p->rows, x->c_row) || bad_rows(x->k_pe, 16, p->rows, x->pe_row)))
         return PMQA_ERR_INVALID_ARG;
-    if (x->q_c && (bad_rows(x->q_c, 16, x->q_c_row, x->q_c_head) || bad_rows(x->q_pe, 16, x->q_pe_row, x->q_pe_head) ||
+    if (x->q_c && (bad_rows(x->q_c, 16, p->rows, x->q_c_row, x->heads, x->q_c_head) ||
+                   bad_rows(x->q_pe, 16, p->rows, x->q_pe_row, x->heads, x->q_pe_head) ||
                    cache::missing(x->q_out, 8)))
         return PMQA_ERR_INVALID_ARG;
     a.c = view(p, ws);

@@ -138,6 +138,18 @@ __device__ __forceinline__ void e4m3x2_to_f32x2(uint32_t b, float &lo, float &hi
     hi = __half2float(__ushort_as_half((unsigned short)(h2 >> 16)));
 }
 
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // Named barrier that also returns whether `pred` held in any participating
 // thread.
 __device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t count, bool pred)

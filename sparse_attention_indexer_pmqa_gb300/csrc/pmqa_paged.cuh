@@ -97,10 +97,12 @@ inline int check_norm(const pmqa_norm *n, Norm *out)
     return PMQA_OK;
 }
 
-// a tensor read or written 8 elements at a time: its address and strides
-inline bool bad_rows(const void *p, uintptr_t align, long long row, long long head = 0)
+// A tensor read or written 8 elements at a time: its address and strides (that of a
+// dimension of one entry does not count).
+inline bool bad_rows(const void *p, uintptr_t align, int rows, long long row, int heads = 1, long long head = 0)
 {
-    return cache::missing(p, align) || row < 0 || head < 0 || row % 8 != 0 || head % 8 != 0;
+    return cache::missing(p, align) || (rows > 1 && (row < 0 || row % 8 != 0)) ||
+           (heads > 1 && (head < 0 || head % 8 != 0));
 }
 
 // ------------------------------------------------------------------ device

@@ -132,32 +132,30 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     }
 }
 
-// Sizes, strides and addresses of one tensor; the extent check is that of the
-// rows and heads that are there.
+// Sizes, strides and addresses of one tensor (the stride of a dimension of one
+// entry does not count).
 int check_heads(const pmqa_heads *h, int rows)
 {
-    if (h->heads < 0 || h->head_dim < 1 || h->x_row < 0 || h->x_head < 0 || h->out_row < 0 || h->out_head < 0)
+    if (h->heads < 0 || h->head_dim < 1)
         return PMQA_ERR_INVALID_ARG;
     if (h->head_dim % 8 != 0 || h->head_dim > kMaxRotary)
         return PMQA_ERR_UNSUPPORTED;
     if (rows == 0 || h->heads == 0)
         return PMQA_OK;
-    if (bad_rows(h->x, 16, h->x_row, h->x_head) || bad_rows(h->out, 16, h->out_row, h->out_head))
+    if (bad_rows(h->x, 16, rows, h->x_row, h->heads, h->x_head) ||
+        bad_rows(h->out, 16, rows, h->out_row, h->heads, h->out_head))
+        return PMQA_ERR_INVALID_ARG;
+    const long long n = h->heads, d = h->head_dim, reach = 1ll << 60;
+    const long long xr = rows > 1 ? h->x_row : 0, xh = n > 1 ? h->x_head : 0;
+    const long long yr = rows > 1 ? h->out_row : 0, yh = n > 1 ? h->out_head : 0;
+    if (xr > reach / rows || yr > reach / rows || xh > reach / n || yh > reach / n)
         return PMQA_ERR_INVALID_ARG;
     // results of different rows and heads are apart
-    const long long n = h->heads, d = h->head_dim;
-    const long long reach = 1ll << 60;
-    if (h->x_row > reach / rows || h->out_row > reach / rows || h->x_head > reach / n || h->out_head > reach / n)
+    if ((n > 1 && yh < d) || (rows > 1 && yr < d) ||
+        (n > 1 && rows > 1 && yr < (n - 1) * yh + d && yh < (rows - 1ll) * yr + d))
         return PMQA_ERR_INVALID_ARG;
-    const bool apart = (n == 1 || h->out_head >= d) && (rows == 1 || h->out_row >= d) &&
-                       (n == 1 || rows == 1 || h->out_row >= (n - 1) * h->out_head + d ||
-                        h->out_head >= (rows - 1ll) * h->out_row + d);
-    if (!apart)
-        return PMQA_ERR_INVALID_ARG;
-    const long long xs = 2 * ((rows - 1ll) * h->x_row + (n - 1) * h->x_head + d);
-    const long long os = 2 * ((rows - 1ll) * h->out_row + (n - 1) * h->out_head + d);
-    if (h->x == h->out ? (h->x_row != h->out_row && rows > 1) || (h->x_head != h->out_head && n > 1)
-                       : cache::overlap(h->x, xs, h->out, os))
+    const long long xs = 2 * ((rows - 1ll) * xr + (n - 1) * xh + d), os = 2 * ((rows - 1ll) * yr + (n - 1) * yh + d);
+    if (h->x == h->out ? xr != yr || xh != yh : cache::overlap(h->x, xs, h->out, os))
         return PMQA_ERR_INVALID_ARG;
     return PMQA_OK;
 }

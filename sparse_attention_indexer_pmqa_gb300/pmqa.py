@@ -632,7 +632,7 @@ def make_cache_problem(k_cache, v_cache, k_scale, v_scale, block_tables, context
     num_blocks, kv_heads, block_size, head_dim = pool = k_cache.shape
     bs, width = block_tables.shape
     dev = k_cache.get_device()
-    f32, i32, _, _, _, codes, _ = _torch()
+    f32, i32, _, _, _, codes, _, _ = _torch()
     code = k_cache.dtype
     if code not in codes or not k_cache.is_contiguous():
         raise AssertionError(f"expected contiguous float8_e4m3fn (or uint8) pools, got {code}")
@@ -669,15 +669,15 @@ def cache_workspace(device=None, stream=None):
 
 def _torch():
     """torch's float32, int32 and bfloat16, the calls that name the current device
-    and its stream's handle, the pools' types and float64 (torch is imported on first
-    use)."""
+    and its stream's handle, the pools' types, float64 and torch.empty (torch is
+    imported on first use)."""
     global _torch_names
     if not _torch_names:
         import torch
 
         _torch_names = (torch.float32, torch.int32, torch.bfloat16, torch._C._cuda_getDevice,
                         torch._C._cuda_getCurrentRawStream,
-                        (torch.float8_e4m3fn, torch.uint8), torch.float64)
+                        (torch.float8_e4m3fn, torch.uint8), torch.float64, torch.empty)
     return _torch_names
 
 
@@ -847,50 +847,95 @@ def rope_frequencies(dim: int, base: float = 10000.0, *, kind: int = PMQA_ROPE_P
     return torch.tensor(list(out), dtype=torch.float64, device=device or "cuda"), scale.value
 
 
+# The calls below are made once per layer and step, most of them on a few rows: what
+# they check and marshal is written out to cost little (a tensor attribute takes about
+# 0.1 us, a Python call 0.3, torch.empty 1.7, the launch 2).
+
 def _rotary(rotary, positions, rows: int, dev: int):
     """A pmqa_rotary, or None for none."""
     if rotary is None:
         return None
-    _, i32, _, _, _, _, f64 = _torch()
-    f = rotary.inv_freq
-    _like(f, dev, f64, (f.numel(),))
+    names = _torch()
+    f, begin, interleaved, scale = rotary
+    n = f.numel()
+    if f.dtype is not names[6] or f.dim() != 1 or f.get_device() != dev or not f.is_contiguous():
+        _like(f, dev, names[6], (n,))
     if positions is not None:
-        _like(positions, dev, i32, (rows,))
-    return RotaryArgs(f.data_ptr(), None if positions is None else positions.data_ptr(),
-                      2 * f.numel(), rotary.begin, int(bool(rotary.interleaved)), rotary.scale)
+        _like(positions, dev, names[1], (rows,))
+        positions = positions.data_ptr()
+    return RotaryArgs(f.data_ptr(), positions, 2 * n, begin, 1 if interleaved else 0, scale)
 
 
 def _norm(norm, width: int, dev: int):
     """A pmqa_norm, or None for none."""
-    if norm is None or norm.kind == PMQA_NORM_NONE:
+    if norm is None or norm[0] == PMQA_NORM_NONE:
         return None
-    f32 = _torch()[0]
-    for t in (norm.weight, norm.bias):
-        if t is not None:
-            _like(t, dev, f32, (width,))
-    return NormArgs(norm.kind, norm.eps, None if norm.weight is None else norm.weight.data_ptr(),
-                    None if norm.bias is None else norm.bias.data_ptr())
+    kind, weight, bias, eps = norm
+    if weight is not None:
+        _like(weight, dev, _torch()[0], (width,))
+        weight = weight.data_ptr()
+    if bias is not None:
+        _like(bias, dev, _torch()[0], (width,))
+        bias = bias.data_ptr()
+    return NormArgs(kind, eps, weight, bias)
 
 
-def _strided(t, dev: int, shape) -> None:
-    """An operand of bf16 rows: on the cache's device, of the documented shape, its last
-    dimension contiguous (the others may be strided)."""
-    bf16 = _torch()[2]
-    if t.shape != shape or t.dtype is not bf16 or t.get_device() != dev or t.stride(-1) != 1:
-        raise AssertionError(f"expected a {bf16} tensor of shape {tuple(shape)} with a contiguous last "
+def _strided(t, dev: int, shape):
+    """The strides of an operand of bf16 rows: on the cache's device, of the documented
+    shape, its last dimension contiguous (the others may be strided)."""
+    strides = t.stride()
+    if t.shape != shape or t.dtype is not _torch()[2] or strides[-1] != 1 or t.get_device() != dev:
+        raise AssertionError(f"expected a bfloat16 tensor of shape {tuple(shape)} with a contiguous last "
                              f"dimension on the cache's device ({dev}), got {tuple(t.shape)} {t.dtype} "
                              f"with strides {t.stride()} on {t.device}")
+    return strides
 
 
-def _step(t, d: int) -> int:
-    """The stride of dimension d (of one entry: none)."""
-    return t.stride(d) if t.shape[d] > 1 else 0
+def _codes_like(t, dev: int, shape) -> None:
+    """A tensor of e4m3 codes."""
+    if t.shape != shape or t.dtype not in _torch()[5] or t.get_device() != dev or not t.is_contiguous():
+        raise AssertionError(f"expected a contiguous float8_e4m3fn (or uint8) tensor of shape {tuple(shape)} "
+                             f"on the cache's device ({dev}), got {tuple(t.shape)} {t.dtype} on {t.device}")
 
 
-def _heads(x, out) -> Heads:
-    """A pmqa_heads of x and out, [rows, heads, head_dim]."""
-    return Heads(x.data_ptr(), out.data_ptr(), _step(x, 0), _step(x, 1), _step(out, 0), _step(out, 1),
-                 x.shape[1], x.shape[2])
+def _device_call(fn, dev: int, stream, *args) -> None:
+    """Call a function of the library with device `dev` current, on its current stream
+    unless one is given."""
+    if dev < 0:
+        raise AssertionError(f"{fn.__name__} takes cuda tensors")
+    names = _torch()
+    if dev != names[3]():
+        import torch
+
+        with torch.cuda.device(dev):
+            return _device_call(fn, dev, stream, *args)
+    rc = fn(*args, names[4](dev) if stream is None else stream.cuda_stream)
+    if rc != PMQA_OK:
+        raise PmqaError(rc, fn.__name__)
+
+
+def _paged_call(fn, dev: int, stream, ws, make, *args) -> None:
+    """A call that ends with a workspace (`make` makes it unless given) and a stream."""
+    if dev < 0:
+        raise AssertionError(f"{fn.__name__} takes cuda tensors")
+    if ws is None:
+        ws = make(f"cuda:{dev}", stream)
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise AssertionError("expected a contiguous workspace on the cache's device")
+    _device_call(fn, dev, stream, *args, ws.data_ptr(), ws.nbytes)
+
+
+def _heads(x, dev: int, rows: int, out):
+    """A pmqa_heads of x, [rows, heads, head_dim], and its result (a new tensor unless
+    given)."""
+    _, heads, width = x.shape
+    shape = (rows, heads, width)
+    xr, xh, _ = _strided(x, dev, shape)
+    if out is None:
+        out = _torch()[7](shape, dtype=x.dtype, device=x.device)
+        return Heads(x.data_ptr(), out.data_ptr(), xr, xh, heads * width, width, heads, width), out
+    o_r, oh, _ = _strided(out, dev, shape)
+    return Heads(x.data_ptr(), out.data_ptr(), xr, xh, o_r, oh, heads, width), out
 
 
 @_on_stream
@@ -900,72 +945,35 @@ def pmqa_rope(x, positions, rotary: Rotary, *, other=None, out=None, other_out=N
     itself rotates in place). `other`: a second tensor of the same rows (the keys
     beside the queries), rotated by the same launch into other_out; then both results
     are returned."""
-    import torch
-
-    rows, dev = x.shape[0], x.get_device()
-    pairs = []
-    for t, o in ((x, out), (other, other_out)):
-        if t is None:
-            continue
-        _strided(t, dev, (rows, *t.shape[1:]))
-        if t.dim() != 3:
-            raise AssertionError(f"expected [rows, heads, head_dim], got shape {tuple(t.shape)}")
-        if o is None:
-            o = torch.empty(t.shape, dtype=t.dtype, device=t.device)
-        else:
-            _strided(o, dev, t.shape)
-        pairs.append((t, o))
+    fn, rows, dev = (_lib or load()).pmqa_rope, x.shape[0], x.get_device()
+    a, out = _heads(x, dev, rows, out)
     r = _rotary(rotary, positions, rows, dev)
-    a = [_heads(t, o) for t, o in pairs]
-    _device_call("pmqa_rope", dev, stream, r, rows, a[0], a[1] if len(a) > 1 else None)
-    return pairs[0][1] if other is None else (pairs[0][1], pairs[1][1])
-
-
-def _device_call(name: str, dev: int, stream, *args) -> None:
-    """Call a function of the library with device `dev` current, on its current stream
-    unless one is given."""
-    if dev < 0:
-        raise AssertionError(f"{name} takes cuda tensors")
-    current_device, raw_stream = _torch()[3:5]
-    if dev != current_device():
-        import torch
-
-        with torch.cuda.device(dev):
-            return _device_call(name, dev, stream, *args)
-    rc = getattr(_lib or load(), name)(*args, raw_stream(dev) if stream is None else stream.cuda_stream)
-    if rc != PMQA_OK:
-        raise PmqaError(rc, name)
-
-
-def _paged_call(name: str, dev: int, stream, ws, size, *args) -> None:
-    """A call that ends with a workspace (made by `size` unless given) and a stream."""
-    if dev < 0:
-        raise AssertionError(f"{name} takes cuda tensors")
-    if ws is None:
-        ws = size(f"cuda:{dev}", stream)
-    if ws.get_device() != dev or not ws.is_contiguous():
-        raise AssertionError("expected a contiguous workspace on the cache's device")
-    _device_call(name, dev, stream, *args, ws.data_ptr(), ws.nbytes)
+    if other is None:
+        _device_call(fn, dev, stream, r, rows, a, None)
+        return out
+    b, other_out = _heads(other, dev, rows, other_out)
+    _device_call(fn, dev, stream, r, rows, a, b)
+    return out, other_out
 
 
 def make_paged_rows(kv_cache, width: int, block_tables, context_lens, row_begin, rows: int,
                     max_rows: int) -> PagedRows:
     """Fill a pmqa_paged_rows for a pool [num_blocks, block_size, width] of bytes or
     e4m3 values (context_lens None where the call has none)."""
-    _, i32, _, _, _, codes, _ = _torch()
-    if kv_cache.dim() != 3 or kv_cache.shape[2] != width or kv_cache.dtype not in codes or \
-            not kv_cache.is_contiguous():
+    names = _torch()
+    shape = kv_cache.shape
+    if len(shape) != 3 or shape[2] != width or kv_cache.dtype not in names[5] or not kv_cache.is_contiguous():
         raise AssertionError(f"expected a contiguous pool [num_blocks, block_size, {width}] of uint8 or "
                              f"float8_e4m3fn, got {tuple(kv_cache.shape)} {kv_cache.dtype}")
-    dev = kv_cache.get_device()
+    dev, i32 = kv_cache.get_device(), names[1]
     bs, blocks = block_tables.shape
     _like(block_tables, dev, i32, (bs, blocks))
     if context_lens is not None:
         _like(context_lens, dev, i32, (bs,))
+        context_lens = context_lens.data_ptr()
     _like(row_begin, dev, i32, (bs + 1,))
-    return PagedRows(block_tables.data_ptr(), None if context_lens is None else context_lens.data_ptr(),
-                     row_begin.data_ptr(), bs, kv_cache.shape[1], blocks, rows, max_rows,
-                     kv_cache.shape[0])
+    return PagedRows(block_tables.data_ptr(), context_lens, row_begin.data_ptr(), bs, shape[1], blocks, rows,
+                     max_rows, shape[0])
 
 
 def _status_workspace(device=None, stream=None):
@@ -1005,47 +1013,39 @@ def pmqa_index_append(k, kv_cache, block_tables, context_lens, row_begin, max_ro
     head weights (float32 or bfloat16 [rows, heads]) into what the logits calls take:
     returns (q_out fp8 [rows, heads, 128], weights_out float32 [rows, heads]) where q
     is given. positions: int32 [rows], the rows' slots unless given."""
-    import torch
-
+    f32, _, bf16, _, _, codes, _, empty = _torch()
     if k is None and q is None:
         raise AssertionError("expected keys, queries or both")
     rows, dev = (k if q is None else q).shape[0], kv_cache.get_device()
     p = make_paged_rows(kv_cache, 132, block_tables, context_lens, row_begin, rows, max_rows)
-    x = IndexRows()
+    k_addr, k_row = None, 0
     if k is not None:
-        _strided(k, dev, (rows, 128))
-        x.k, x.k_row = k.data_ptr(), _step(k, 0)
-    if q is not None:
+        k_row = _strided(k, dev, (rows, 128))[0]
+        k_addr = k.data_ptr()
+    if q is None:
+        x = IndexRows(k_addr, None, None, None, None, k_row)
+    else:
         heads = q.shape[1]
-        _strided(q, dev, (rows, heads, 128))
-        if weights.shape != (rows, heads) or weights.dtype not in (torch.float32, torch.bfloat16) or \
-                weights.get_device() != dev or _step(weights, 1) > 1:
-            raise AssertionError(f"expected float32 or bfloat16 weights of shape {(rows, heads)} with a "
+        shape, pair = (rows, heads, 128), (rows, heads)
+        q_row, q_head, _ = _strided(q, dev, shape)
+        w_row, w_step = weights.stride()
+        if weights.shape != pair or weights.dtype not in (f32, bf16) or w_step != 1 and heads > 1 or \
+                weights.get_device() != dev:
+            raise AssertionError(f"expected float32 or bfloat16 weights of shape {pair} with a "
                                  f"contiguous last dimension, got {tuple(weights.shape)} {weights.dtype}")
         if q_out is None:
-            q_out = torch.empty((rows, heads, 128), dtype=torch.float8_e4m3fn, device=q.device)
+            q_out = empty(shape, dtype=codes[0], device=q.device)
         else:
-            _codes_like(q_out, dev, (rows, heads, 128))
+            _codes_like(q_out, dev, shape)
         if weights_out is None:
-            weights_out = torch.empty((rows, heads), dtype=torch.float32, device=q.device)
+            weights_out = empty(pair, dtype=f32, device=q.device)
         else:
-            _like(weights_out, dev, torch.float32, (rows, heads))
-        x.q, x.q_row, x.q_head = q.data_ptr(), _step(q, 0), _step(q, 1)
-        x.weights, x.weights_row = weights.data_ptr(), _step(weights, 0)
-        x.weights_bf16 = int(weights.dtype is torch.bfloat16)
-        x.q_out, x.weights_out = q_out.data_ptr(), weights_out.data_ptr()
-        x.heads, x.weight_scale = heads, weight_scale
-    _paged_call("pmqa_index_append", dev, stream, ws, _status_workspace, p, kv_cache.data_ptr(), x,
+            _like(weights_out, dev, f32, pair)
+        x = IndexRows(k_addr, q.data_ptr(), weights.data_ptr(), q_out.data_ptr(), weights_out.data_ptr(), k_row,
+                      q_row, q_head, w_row, heads, 1 if weights.dtype is bf16 else 0, weight_scale)
+    _paged_call((_lib or load()).pmqa_index_append, dev, stream, ws, _status_workspace, p, kv_cache.data_ptr(), x,
                 _norm(norm, 128, dev), _rotary(rotary, positions, rows, dev))
     return None if q is None else (q_out, weights_out)
-
-
-def _codes_like(t, dev: int, shape) -> None:
-    """An output of e4m3 codes."""
-    codes = _torch()[5]
-    if t.shape != shape or t.dtype not in codes or t.get_device() != dev or not t.is_contiguous():
-        raise AssertionError(f"expected a contiguous float8_e4m3fn (or uint8) tensor of shape {tuple(shape)} "
-                             f"on the cache's device ({dev}), got {tuple(t.shape)} {t.dtype} on {t.device}")
 
 
 @_on_stream
@@ -1054,27 +1054,23 @@ def pmqa_index_read(kv_cache, block_tables, row_begin, rows: int, *, start=None,
     """Cached indexer keys as contiguous rows: row row_begin[i] + j of (k fp8 [rows, 128],
     k_scale float32 [rows]) is the token at slot start[i] + j of request i (start: int32
     [bs], zeros unless given)."""
-    import torch
-
+    f32, i32, _, _, _, codes, _, empty = _torch()
     dev = kv_cache.get_device()
     p = make_paged_rows(kv_cache, 132, block_tables, None, row_begin, rows, 0)
     if start is not None:
-        _like(start, dev, torch.int32, (p.bs,))
+        _like(start, dev, i32, (p.bs,))
+        start = start.data_ptr()
     if k is None:
-        k = torch.empty((max(rows, 0), 128), dtype=torch.float8_e4m3fn, device=kv_cache.device)
+        k = empty((max(rows, 0), 128), dtype=codes[0], device=kv_cache.device)
     else:
         _codes_like(k, dev, (rows, 128))
     if k_scale is None:
-        k_scale = torch.empty(max(rows, 0), dtype=torch.float32, device=kv_cache.device)
+        k_scale = empty(max(rows, 0), dtype=f32, device=kv_cache.device)
     else:
-        _like(k_scale, dev, torch.float32, (rows,))
-    _paged_call("pmqa_index_read", dev, stream, ws, _status_workspace, p, kv_cache.data_ptr(), _addr(start),
+        _like(k_scale, dev, f32, (rows,))
+    _paged_call((_lib or load()).pmqa_index_read, dev, stream, ws, _status_workspace, p, kv_cache.data_ptr(), start,
                 k.data_ptr(), k_scale.data_ptr())
     return k, k_scale
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
 
 
 @_on_stream
@@ -1086,29 +1082,29 @@ def pmqa_latent_append(c, k_pe, kv_cache, block_tables, context_lens, row_begin,
     [rows, 64], rotated; both or neither None) into their slots of the latent cache, and
     its queries (q_c bf16 [rows, heads, 512], q_pe bf16 [rows, heads, 64]) into q_out fp8
     [rows, heads, 576], which is returned where q_c is given."""
-    import torch
-
+    _, _, _, _, _, codes, _, empty = _torch()
     if c is None and q_c is None:
         raise AssertionError("expected latent rows, queries or both")
     rows, dev = (c if q_c is None else q_c).shape[0], kv_cache.get_device()
     p = make_paged_rows(kv_cache, 576, block_tables, context_lens, row_begin, rows, max_rows)
-    x = LatentRows(kv_scale=kv_scale, q_scale=q_scale)
+    c_addr, pe_addr, c_row, pe_row = None, None, 0, 0
     if c is not None:
-        _strided(c, dev, (rows, 512))
-        _strided(k_pe, dev, (rows, 64))
-        x.c, x.c_row, x.k_pe, x.pe_row = c.data_ptr(), _step(c, 0), k_pe.data_ptr(), _step(k_pe, 0)
-    if q_c is not None:
+        c_row, pe_row = _strided(c, dev, (rows, 512))[0], _strided(k_pe, dev, (rows, 64))[0]
+        c_addr, pe_addr = c.data_ptr(), k_pe.data_ptr()
+    if q_c is None:
+        x = LatentRows(c_addr, pe_addr, None, None, None, c_row, pe_row, 0, 0, 0, 0, 0, kv_scale, q_scale)
+    else:
         heads = q_c.shape[1]
-        _strided(q_c, dev, (rows, heads, 512))
-        _strided(q_pe, dev, (rows, heads, 64))
+        shape = (rows, heads, 576)
+        qc_row, qc_head, _ = _strided(q_c, dev, (rows, heads, 512))
+        qp_row, qp_head, _ = _strided(q_pe, dev, (rows, heads, 64))
         if q_out is None:
-            q_out = torch.empty((rows, heads, 576), dtype=torch.float8_e4m3fn, device=q_c.device)
+            q_out = empty(shape, dtype=codes[0], device=q_c.device)
         else:
-            _codes_like(q_out, dev, (rows, heads, 576))
-        x.q_c, x.q_c_row, x.q_c_head = q_c.data_ptr(), _step(q_c, 0), _step(q_c, 1)
-        x.q_pe, x.q_pe_row, x.q_pe_head = q_pe.data_ptr(), _step(q_pe, 0), _step(q_pe, 1)
-        x.q_out, x.heads = q_out.data_ptr(), heads
-    _paged_call("pmqa_latent_append", dev, stream, ws, _status_workspace, p, kv_cache.data_ptr(), x,
+            _codes_like(q_out, dev, shape)
+        x = LatentRows(c_addr, pe_addr, q_c.data_ptr(), q_pe.data_ptr(), q_out.data_ptr(), c_row, pe_row, qc_row,
+                       qc_head, qp_row, qp_head, heads, kv_scale, q_scale)
+    _paged_call((_lib or load()).pmqa_latent_append, dev, stream, ws, _status_workspace, p, kv_cache.data_ptr(), x,
                 _norm(norm, 512, dev), _rotary(rotary, positions, rows, dev))
     return q_out
 
@@ -1120,23 +1116,22 @@ def pmqa_latent_attention(q, kv_cache, block_tables, context_lens, row_begin, ma
     """Attention of q (fp8 [rows, heads, 576]) to all the latent tokens that its rows
     see: bf16 out [rows, heads, 512] (and float32 lse [rows, heads] when asked for or
     given)."""
-    import torch
-
+    f32, _, bf16, _, _, _, _, empty = _torch()
     rows, heads = q.shape[:2]
-    dev = kv_cache.get_device()
+    dev, pair = kv_cache.get_device(), (rows, heads)
     p = make_paged_rows(kv_cache, 576, block_tables, context_lens, row_begin, rows, max_rows)
-    f32, _, bf16 = _torch()[:3]
     _codes_like(q, dev, (rows, heads, 576))
     if out is None:
-        out = torch.empty((rows, heads, 512), dtype=bf16, device=q.device)
+        out = empty((rows, heads, 512), dtype=bf16, device=q.device)
     else:
         _like(out, dev, bf16, (rows, heads, 512))
-    if lse is None:
-        lse = torch.empty((rows, heads), dtype=f32, device=q.device) if want_lse else None
-    else:
-        _like(lse, dev, f32, (rows, heads))
-    _paged_call("pmqa_latent_attention", dev, stream, ws, latent_workspace, p, q.data_ptr(), kv_cache.data_ptr(),
-                heads, q_scale, kv_scale, sm_scale, out.data_ptr(), _addr(lse))
+    if lse is not None:
+        _like(lse, dev, f32, pair)
+    elif want_lse:
+        lse = empty(pair, dtype=f32, device=q.device)
+    _paged_call((_lib or load()).pmqa_latent_attention, dev, stream, ws, latent_workspace, p, q.data_ptr(),
+                kv_cache.data_ptr(), heads, q_scale, kv_scale, sm_scale, out.data_ptr(),
+                None if lse is None else lse.data_ptr())
     return out if lse is None else (out, lse)
 
 
