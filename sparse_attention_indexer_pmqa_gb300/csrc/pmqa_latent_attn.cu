@@ -5,18 +5,20 @@
 //
 // Rows of one request are packed as (query token, head), up to N = 16, 32 or 64 to
 // a block. A CTA walks the token tiles (128 tokens) of its blocks:
-//   * four warps look up the tokens in the block table and copy the latent rows (576
-//     bytes) by cp.async straight into the operand layout (pmqa_latent.cuh);
+//   * one warp walks the tiles ahead of the others, looks their tokens up in the block
+//     table and says what each tile is (Tile, Piece);
+//   * four warps copy the latent rows (576 bytes) by cp.async straight into the operand
+//     layout (pmqa_latent.cuh);
 //   * one thread issues S^T = K Q^T (kind::f8f6f4, M = 128 tokens, N packed rows,
 //     K = 576) into TMEM;
-//   * the softmax threads, one per token and 32 packed rows, form p = 2^(x - m + 4)
+//   * the softmax threads, one per token and 16 or 32 packed rows, form p = 2^(x - m)
 //     with a row maximum m that moves only when a weight passes 2^8, and write p as
-//     two e4m3 terms, p_hi = e4m3(p) and p_lo = e4m3(p - p_hi);
+//     two 8-bit terms, p_hi = e4m3(p) and p_lo, the remainder;
 //   * the thread issues O^T += V^T P^T (M = 128 value columns, four blocks, K = 128
 //     tokens) from the SAME tile as an MN-major operand. With N = 64 both terms add
-//     into one accumulator (the products cost 576 + 2 * 512 fp8 multiplications a
-//     row and token); with fewer rows the terms are N more columns, p_lo times 16,
-//     since there the cost is the read of V.
+//     into one accumulator (576 + 2 * 512 fp8 multiplications a row and token; p_lo is
+//     e5m2); with fewer rows p_lo is e4m3 times 16 in N more columns, since there the
+//     cost is the read of V.
 // The flattened sequence of (block, tile) is split evenly over the CTAs; a block
 // that is cut leaves its parts (O, m, l) in the workspace and a second kernel joins
 // them. Where a query token has more than 64 heads, neighbouring CTAs take its heads
@@ -45,6 +47,7 @@ constexpr int kMaxHeads = 128;
 constexpr int kMaxCtas = 160;   // workspace parts: 2 per CTA
 constexpr int kPad = 2;         // tiles' worth of starting and ending a block
 constexpr int kLeast = 2;       // fewest tiles that a CTA takes
+constexpr int kNoPage = (int)0x80000000;  // no token there (a table entry is negative where it is bad)
 constexpr int kWhole = 512;     // tables of up to so many tokens: blocks are not cut
 constexpr float kTop = 8.0f;    // p = 2^(x - m); m moves when a p passes 2^kTop
 constexpr float kUnseen = 1e30f;   // -m of a row that has seen no score: above every |x|
@@ -151,11 +154,12 @@ __device__ __forceinline__ int range_of(long long total, int C, long long x)
     return (int)(((x + 1) * (long long)C - 1) / total);
 }
 
-// Called by the whole CTA; the result is in s_range after the last barrier.
+// Called by the whole CTA; the result is in *s_range after the last barrier. s_sum:
+// THREADS / 16 words.
 template <int THREADS>
-__device__ __forceinline__ void find_range(const Args &a, int g, Range *s_range)
+__device__ __forceinline__ void find_range(const Args &a, int g, long long *s_sum, Range *s_range)
 {
-    __shared__ long long s_sum[THREADS / 32], s_units[THREADS / 32];
+    long long *const s_units = s_sum + THREADS / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     long long sum = 0, units = 0;
     for (int i = tid; i < a.c.bs; i += THREADS) {
@@ -284,14 +288,42 @@ __device__ __forceinline__ Block block_of(const Args &a, const Cursor &c, int hs
 
 // ------------------------------------------------------------- kernel
 
+// What the planner tells the others of a tile, and of its piece of a unit (the tiles of
+// a unit in one range).
+enum { kFirst = 1, kLast = 2, kEnd = 4 };  // tile of its piece, or of the range
+struct Tile {
+    uint32_t have[4];  // a bit per token that is there
+    int tok;           // first token
+    uint32_t flags;
+    uint32_t unused[2];
+};
+struct Piece {
+    long long first;   // row of q and out, in heads
+    int rows;          // packed rows
+    int last;          // last slot that the first row sees
+    int sole;          // the unit lies in this range whole
+    int slot;          // otherwise: of its part
+    int unused[2];
+};
+static_assert(sizeof(Tile) == 32 && sizeof(Piece) == 32, "places in shared memory");
+constexpr int kPieces = 8;
+
 template <int N>
 struct Cfg {
-    static constexpr int kGroups = N == 64 ? 2 : 1;       // softmax warpgroups
+    static constexpr int kGroups = N == 16 ? 1 : 2;       // softmax warpgroups
     static constexpr int kRowsG = N / kGroups;            // packed rows of each
     static constexpr int kStages = N == 16 ? 3 : 2;       // value ring
-    static constexpr int kThreads = 128 + 128 * kGroups + 32;
-    static constexpr int kMmaWarp = 4 + 4 * kGroups;
-    static constexpr int kOCols = N == 64 ? 64 : 2 * N;   // output columns of a value block
+    // N = 64: two idle warps complete the products' warpgroup, so that registers can
+    // move to the softmax (2 x 192 + 64 + 64 = 4 x 128). Spilled registers cost more than
+    // their instructions: the L1 cache beside so much shared memory holds 28 KB, and rows
+    // pass through it (80 registers, 16 rows a thread: 434 us against 288).
+    static constexpr bool kSplit = N == 64;
+    static constexpr int kThreads = 128 + 128 * kGroups + (kSplit ? 128 : 64);
+    static constexpr int kAhead = N == 16 ? 1 : 2;        // tiles that the planner is ahead of the producers
+    static constexpr int kTiles = kStages + kAhead;       // tiles that are described at a time
+    static constexpr int kMmaWarp = 4 + 4 * kGroups, kPlanWarp = kMmaWarp + 1;
+    static constexpr int kTerms = N == 64 ? 1 : 2;        // accumulators of a value block
+    static constexpr int kOCols = kTerms * N;             // its output columns
     static constexpr float kLo = N == 64 ? 1.0f : 16.0f;  // p_lo holds kLo (p - p_hi)
     // P: a row of 64 bytes per token, two terms of N rows. N = 64: a buffer of 128 rows for
     // each term; N = 16: both stages share a row, 32 bytes each.
@@ -307,14 +339,20 @@ struct Cfg {
     static constexpr uint32_t kOffQV = kOffR + 2 * kRStage;
     static constexpr uint32_t kOffQR = kOffQV + (N / 8) * kVGroup;
     static constexpr uint32_t kOffP = kOffQR + ((N / 8) * kRGroup + 1023) / 1024 * 1024;
-    static constexpr uint32_t kOffMask = kOffP + kPBytes;               // [stages][4] words
-    static constexpr uint32_t kOffLim = kOffMask + kStages * 16;        // [2][N] ints
-    static constexpr uint32_t kOffM = kOffLim + 2 * N * 4;              // [N] floats: -m       
+    // 1 KB for each softmax warp's output; N = 16 has room for it only where P was
+    static constexpr uint32_t kOffOut = N == 16 ? kOffP : kOffP + kPBytes;
+    static constexpr uint32_t kOffRows = N == 16 ? kOffP + kPBytes : kOffOut + 4096 * kGroups;  // [kAhead][128]
+    static constexpr uint32_t kOffInfo = kOffRows + kAhead * 512;       // [kTiles] Tile
+    static constexpr uint32_t kOffPiece = kOffInfo + kTiles * 32;       // [kPieces] Piece
+    static constexpr uint32_t kOffRange = kOffPiece + kPieces * 32;     // Range
+    static constexpr uint32_t kOffLim = kOffRange + 128;                // [N] ints
+    static constexpr uint32_t kOffM = kOffLim + N * 4;                  // [N] floats: -m       
     static constexpr uint32_t kOffAlpha = kOffM + N * 4;                // [N]
     static constexpr uint32_t kOffRed = kOffAlpha + N * 4;              // [4][N]
     static constexpr uint32_t kOffBar = kOffRed + 4 * N * 4;
-    static constexpr int kBMask = 0;                        // [stages] masks written: 4 producer warps
-    static constexpr int kBReady = kBMask + kStages;        // [stages] rows landed: 128 cp.async arrivals
+    static constexpr int kBInfo = 0;                        // [kTiles] tile described: the planner
+    static constexpr int kBUsed = kBInfo + kTiles;          // [kTiles] its slot is free, its rows read: 4 producer warps
+    static constexpr int kBReady = kBUsed + kTiles;        // [stages] rows landed: 128 cp.async arrivals
     static constexpr int kBVEmpty = kBReady + kStages;      // [stages][4] values of 32 tokens read: MMA commit
     static constexpr int kBREmpty = kBVEmpty + 4 * kStages;    // [2] rotary columns read: MMA commit
     static constexpr int kBSFull = kBREmpty + 2;            // [2] scores in TMEM: MMA commit
@@ -326,7 +364,7 @@ struct Cfg {
     static constexpr int kBars = kBDrain + 1;
     static constexpr uint32_t kOffMisc = kOffBar + kBars * 8;
     static constexpr uint32_t kSmem = kOffMisc + 16;
-    static_assert(kSmem + 1024 <= 232448, "shared memory, with the static arrays below it");
+    static_assert(kSmem <= 232448 && sizeof(Range) <= 128, "shared memory");
     static_assert(kOffP % 1024 == 0 && kOffBar % 8 == 0, "alignment");
 
     static constexpr uint32_t kIdescQK = idesc_e4m3_f32(128, N);
@@ -384,14 +422,13 @@ __device__ __forceinline__ uint32_t e5m2x2_of_f16x2(uint32_t h2)
     return r;
 }
 
-// Two weights as their terms (bytes 0 and 1): the f16 value of p is off by 2^-11 at
-// most, its difference from the first term exact. SAME: both terms go into one
+// Two weights, an f16 pair, as their terms (bytes 0 and 1): the f16 value of p is off
+// by 2^-11 at most, its difference from the first term exact. SAME: both terms go into one
 // accumulator, so the second has the first's unit: e5m2, which reaches down to 2^-17.
 // Otherwise it is e4m3 of 16 times the difference.
 template <bool SAME>
-__device__ __forceinline__ void split2(float p0, float p1, uint32_t &hi, uint32_t &lo)
+__device__ __forceinline__ void split2(uint32_t p, uint32_t &hi, uint32_t &lo)
 {
-    const uint32_t p = cache::pack_f16x2(p0, p1);
     hi = e4m3x2_of_f16x2(p);
     uint32_t d = f16x2_of_e4m3x2(hi);
     asm("sub.rn.f16x2 %0, %1, %0;" : "+r"(d) : "r"(p));
@@ -401,6 +438,19 @@ __device__ __forceinline__ void split2(float p0, float p1, uint32_t &hi, uint32_
         asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(d) : "r"(0x4C004C00u));  // 16
         lo = e4m3x2_of_f16x2(d);
     }
+}
+
+// (d0, d1) = (a0, a1) * (b, b) + (c0, c1): one packed fp32x2 multiply-add.
+__device__ __forceinline__ void ffma2_of(float &d0, float &d1, uint32_t a0, uint32_t a1, float b, float c0, float c1)
+{
+    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\t"
+        "mov.b64 rb, {%4, %4};\n\t"
+        "mov.b64 rc, {%5, %6};\n\t"
+        "fma.rn.f32x2 rd, ra, rb, rc;\n\t"
+        "mov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "r"(a0), "r"(a1), "f"(b), "f"(c0), "f"(c1));
 }
 
 // Four codes, NaN (0x7F, 0xFF) replaced by 0.
@@ -416,7 +466,6 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
     using K = Cfg<N>;
     constexpr int RG = K::kRowsG;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ Range s_range;
     const uint32_t sbase = smem_u32(smem);
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(kFull, tid >> 5, 0);
@@ -424,26 +473,30 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
 
     if (hs == 0 && tid == 0)
         a.meta[g] = make_int4(0, 0, 0, 0);
-    find_range<K::kThreads>(a, g, &s_range);
+    Range *const range = reinterpret_cast<Range *>(smem + K::kOffRange);
+    find_range<K::kThreads>(a, g, reinterpret_cast<long long *>(smem), range);
     griddep_launch_dependents();
-    if (!s_range.any)
+    if (!range->any)
         return;  // the same for the whole CTA
     if (sbase & 1023u) {
         if (tid == 0)
             atomicOr(a.c.status, (uint32_t)PMQA_DEV_INTERNAL);
         return;
     }
-    const long long x0 = s_range.x0, x1 = s_range.x1;
+    const long long x0 = range->x0, x1 = range->x1;
 
     uint64_t *const bar = reinterpret_cast<uint64_t *>(smem + K::kOffBar);
     uint32_t *const misc = reinterpret_cast<uint32_t *>(smem + K::kOffMisc);
     volatile int *const abort_flag = reinterpret_cast<volatile int *>(misc + 1);
     if (tid == 0) {
         for (int s = 0; s < K::kStages; ++s) {
-            mbar_init(&bar[K::kBMask + s], 4);
             mbar_init(&bar[K::kBReady + s], 128);
             for (int w = 0; w < 4; ++w)
                 mbar_init(&bar[K::kBVEmpty + 4 * s + w], 1);
+        }
+        for (int s = 0; s < K::kTiles; ++s) {
+            mbar_init(&bar[K::kBInfo + s], 1);
+            mbar_init(&bar[K::kBUsed + s], 4);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bar[K::kBREmpty + s], 1);
@@ -470,50 +523,36 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
 
     if (warp < 4) {
         // ------------------------------------------------------------ producer
-        // Thread tid owns token tid of every tile; warp w copies the rows of tokens
-        // 32 w .. 32 w + 31, one row per instruction (lane = 16-byte chunk). The
-        // table entries of the next tile load while this one is issued.
-        Cursor c = s_range.at, d = c;
-        bool more = true;
-        auto look_up = [&](const Cursor &u) -> int {
-            const int tok = u.t * kTile + tid;
-            const Block b = block_of(a, u, hs, N);
-            return tok < b.end ? __ldg(a.c.bt + (long long)u.i * a.c.W + a.c.page_of(tok)) : -1;
-        };
-        int page = look_up(c);
-        int vs = 0, seg = -1, it = 0;
-        uint32_t vph = 0;
-        for (;; ++it) {
+        if constexpr (K::kSplit)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        // Warp w copies the rows of tokens 32 w .. 32 w + 31, one row per instruction
+        // (lane = 16-byte chunk).
+        int vs = 0, seg = -1, e = 0;
+        uint32_t vph = 0, eph = 0;
+        for (int it = 0;; ++it) {
             const int rs = it & 1;
             const uint32_t rph = (uint32_t)(it >> 1) & 1u;
-            const Block b = block_of(a, c, hs, N);
-            const bool first = it == 0 || c.t == 0;
-            d = c;
-            more = next_tile(a, d, x1);
-            const int page_next = more ? look_up(d) : -1;
-            // pool row of this thread's token
-            const int tok = c.t * kTile + tid;
-            uint32_t srow = paged::kNoRow;
-            if (tok < b.end) {
-                if (page < 0 || (long long)page >= a.c.nb)
-                    atomicOr(a.c.status, (uint32_t)PMQA_DEV_BAD_BLOCK_ID);
-                else
-                    srow = (uint32_t)page * (uint32_t)a.c.P + (uint32_t)(tok - a.c.page_of(tok) * a.c.P);
+            if (!__all_sync(kFull, mbar_wait(&bar[K::kBInfo + e], eph, abort_flag))) {
+                fail();
+                break;
             }
-            page = page_next;
-            if (first) {
+            const Tile *const tile = reinterpret_cast<const Tile *>(smem + K::kOffInfo) + e;
+            const uint32_t flags = tile->flags, srow = reinterpret_cast<const uint32_t *>(smem + K::kOffRows)[it % K::kAhead * 128 + tid];
+            if (flags & kFirst) {
                 // one query buffer: free once the last scores of the block before are done
                 ++seg;
                 if (!__all_sync(kFull, mbar_wait(&bar[K::kBQEmpty], ((uint32_t)seg & 1u) ^ 1u, abort_flag))) {
                     fail();
                     break;
                 }
-                const uint8_t *const src = a.q + b.first * kDim;
+                const Piece *const piece = reinterpret_cast<const Piece *>(smem + K::kOffPiece) + seg % kPieces;
+                const uint8_t *const src = a.q + piece->first * kDim;
+                const int rows = piece->rows;
                 for (int k = tid; k < N * kChunks; k += 128) {
                     const int r = k / kChunks, ch = k - r * kChunks;
                     const uint32_t dst = ch < 32 ? sbase + K::kOffQV + v_offset(r, ch)
                                                  : sbase + K::kOffQR + r_offset(r, ch - 32);
-                    cp_async_16(dst, src + (r < b.rows ? r * kDim + ch * 16 : 0), r < b.rows ? 16u : 0u);
+                    cp_async_16(dst, src + (r < rows ? r * kDim + ch * 16 : 0), r < rows ? 16u : 0u);
                 }
             }
             // this warp's 32 tokens of the slot
@@ -522,12 +561,8 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
                 fail();
                 break;
             }
-            const uint32_t have = __ballot_sync(kFull, srow != paged::kNoRow);
-            if (lane == 0) {
-                asm volatile("st.shared.b32 [%0], %1;" ::"r"(sbase + K::kOffMask + (uint32_t)vs * 16u + 4u * warp),
-                             "r"(have) : "memory");
-                mbar_arrive(&bar[K::kBMask + vs]);
-            }
+            if (lane == 0)
+                mbar_arrive(&bar[K::kBUsed + e]);
             const uint32_t vdst = sbase + K::kOffV + (uint32_t)vs * kVStage;
             const uint32_t rdst = sbase + K::kOffR + (uint32_t)rs * kRStage;
 #pragma unroll 8
@@ -546,23 +581,22 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
                             a.kv + (is ? (unsigned long long)sr * kDim : 0ull) + kVDim + 16 * cc, is ? 16u : 0u);
             }
             cp_async_arrive_noinc(&bar[K::kBReady + vs]);
+            if (flags & kEnd)
+                break;
             if (++vs == K::kStages) {
                 vs = 0;
                 vph ^= 1u;
             }
-            if (!more)
-                break;
-            c = d;
+            if (++e == K::kTiles) {
+                e = 0;
+                eph ^= 1u;
+            }
         }
         cp_async_wait_all();
-        if (hs == 0 && tid == 0) {
-            // the last unit goes on in later ranges and starts in this one: to be joined
-            const long long xs = c.x - c.t, xe = xs + c.T;
-            if (!a.whole && xs >= x0 && xe > x1)
-                a.meta[g] = make_int4(c.i, c.u, range_of(s_range.total, s_range.C, xe - 1) - g + 1, 0);
-        }
     } else if (warp < K::kMmaWarp) {
         // ------------------------------------------------------------ softmax
+        if constexpr (K::kSplit)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         // Thread s of a group owns token s (TMEM lane s) and the group's RG packed
         // rows. Exits are uniform over the group: a failed wait clears `ok`, and the
         // group leaves together at its next barrier.
@@ -572,92 +606,106 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
         float *const mneg = reinterpret_cast<float *>(smem + K::kOffM) + wg * RG;
         float *const alpha = reinterpret_cast<float *>(smem + K::kOffAlpha) + wg * RG;
         float *const red = reinterpret_cast<float *>(smem + K::kOffRed) + wg * RG;  // [4][N]
-        int *const lims = reinterpret_cast<int *>(smem + K::kOffLim) + wg * RG;     // [2][N]
-        Cursor c = s_range.at;
+        int *const lims = reinterpret_cast<int *>(smem + K::kOffLim) + wg * RG;
         float l[RG];
-        int seg = -1, vs = 0;
-        uint32_t vph = 0;
+        int seg = -1, vs = 0, e = 0, seen_by_all = 0;  // last slot that every row of the block sees
+        uint32_t eph = 0;
         bool ok = true;
         for (int it = 0;; ++it) {
             const int stage = it & 1;
             const uint32_t kph = (uint32_t)(it >> 1) & 1u;
-            const Block b = block_of(a, c, hs, N);
-            const bool first = it == 0 || c.t == 0;
-            Cursor d = c;
-            const bool more = next_tile(a, d, x1);
-            const bool last = !more || d.t == 0;
+            ok = ok && mbar_wait(&bar[K::kBInfo + e], eph, abort_flag);
+            ok = __all_sync(kFull, ok);
+            const Tile *const tile = reinterpret_cast<const Tile *>(smem + K::kOffInfo) + e;
+            const uint32_t flags = ok ? tile->flags : 0u;
+            const bool first = flags & kFirst;
             if (first) {
+                // every warp writes the same (no barrier: a failed wait must not part them)
                 ++seg;
 #pragma unroll
                 for (int h = 0; h < RG; ++h)
                     l[h] = 0.0f;
-                if (s < RG) {
-                    const int r = wg * RG + s;
-                    mneg[s] = kUnseen;
+                const Piece *const piece = reinterpret_cast<const Piece *>(smem + K::kOffPiece) + seg % kPieces;
+                seen_by_all = piece->last;
+                if (lane < RG) {
+                    const int r = wg * RG + lane;
+                    mneg[lane] = kUnseen;
                     // rows that do not exist see everything: no mask for their sake
-                    lims[(seg & 1) * N + s] = r < b.rows ? b.last + (a.hb > 1 ? 0 : r / a.heads) : 0x7FFFFFFF;
+                    lims[lane] = r < piece->rows ? seen_by_all + (a.hb > 1 ? 0 : r / a.heads) : 0x7FFFFFFF;
                 }
-                named_bar_sync(barrier, 128);
+                __syncwarp();
             }
             ok = ok && mbar_wait(&bar[K::kBSFull + stage], kph, abort_flag) &&
-                 mbar_wait(&bar[K::kBMask + vs], vph, abort_flag) &&
                  mbar_wait(&bar[K::kBPEmpty + stage], kph ^ 1u, abort_flag);
             ok = __all_sync(kFull, ok);
+            const bool masked = (tile->have[0] & tile->have[1] & tile->have[2] & tile->have[3]) != kFull ||
+                                tile->tok + kTile - 1 > seen_by_all;
+            // the token's scores; those of rows that do not see it become what c_log2
+            // turns into -inf
             uint32_t sr[RG];
-            if (ok) {
-                tc_fence_after_sync();
+            auto load_scores = [&]() {
                 tmem_ld_cols<RG>(tmem + K::kColS + (uint32_t)(stage * N + wg * RG) + lane_off, sr);
                 tmem_ld_wait();
                 reg_fence_cols<RG>(sr);
-                tc_fence_before_sync();
-            } else {
+                if (masked) {
+                    const bool there = tile->have[w4] >> lane & 1u;
+                    const int tok = tile->tok + s;
+                    const uint32_t never = __float_as_uint(a.c_log2 > 0.0f ? -INFINITY : INFINITY);
+                    bool nan = false;
 #pragma unroll
-                for (int h = 0; h < RG; ++h)
-                    sr[h] = 0u;
-            }
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&bar[K::kBSFree + stage]);
-            const uint4 have = lds128(sbase + K::kOffMask + (uint32_t)vs * 16u);
-            const int tok = c.t * kTile + s;
-            const bool masked = (have.x & have.y & have.z & have.w) != kFull || c.t * kTile + kTile - 1 > b.last;
-            if (masked) {
-                const bool there = lds32(sbase + K::kOffMask + (uint32_t)vs * 16u + 4u * w4) >> lane & 1u;
-                const int *const lim = lims + (seg & 1) * N;
-                bool nan = false;
-                const uint32_t never = __float_as_uint(a.c_log2 > 0.0f ? -INFINITY : INFINITY);
-#pragma unroll
-                for (int h = 0; h < RG; ++h) {
-                    const float x = __uint_as_float(sr[h]);
-                    nan |= x != x;
-                    sr[h] = there && tok <= lim[h] ? sr[h] : never;
-                }
-                if (nan) {
-                    // in the queries, or in the token's row: then out of its values
-                    const uint32_t v = sbase + K::kOffV + (uint32_t)vs * kVStage;
-                    for (int ch = 0; ch < 32; ++ch) {
-                        const uint4 u = lds128(v + v_offset(s, ch));
-                        sts128(v + v_offset(s, ch), without_nan(u.x), without_nan(u.y), without_nan(u.z), without_nan(u.w));
+                    for (int h = 0; h < RG; ++h) {
+                        const float x = __uint_as_float(sr[h]);
+                        nan |= x != x;
+                        sr[h] = there && tok <= lims[h] ? sr[h] : never;
+                    }
+                    if (nan) {
+                        // in the queries, or in the token's row: then out of its values
+                        const uint32_t v = sbase + K::kOffV + (uint32_t)vs * kVStage;
+#pragma unroll 1
+                        for (int ch = 0; ch < 32; ++ch) {
+                            const uint4 u = lds128(v + v_offset(s, ch));
+                            sts128(v + v_offset(s, ch), without_nan(u.x), without_nan(u.y), without_nan(u.z), without_nan(u.w));
+                        }
                     }
                 }
-            }
-            auto value = [&](int h, float m) -> float { return __uint_as_float(sr[h]) * a.c_log2 + m; };
-            float top = -INFINITY;
+            };
+            // the weights, in fp32 and as f16 pairs; returns whether one passes 2^kTop
+            float p[RG];
+            uint32_t ph[RG / 2];
+            auto weights = [&]() -> bool {
+                uint32_t top = 0u;
 #pragma unroll
-            for (int h = 0; h < RG; h += 4) {
-                const float4 m4 = *reinterpret_cast<const float4 *>(mneg + h);
-                top = fmaxf(top, fmaxf(fmaxf(value(h, m4.x), value(h + 1, m4.y)),
-                                       fmaxf(value(h + 2, m4.z), value(h + 3, m4.w))));
+                for (int h = 0; h < RG; h += 4) {
+                    const float4 m4 = *reinterpret_cast<const float4 *>(mneg + h);
+                    ffma2_of(p[h], p[h + 1], sr[h], sr[h + 1], a.c_log2, m4.x, m4.y);
+                    ffma2_of(p[h + 2], p[h + 3], sr[h + 2], sr[h + 3], a.c_log2, m4.z, m4.w);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        p[h + e] = ex2_approx(p[h + e]);
+                    ph[h / 2] = cache::pack_f16x2(p[h], p[h + 1]);
+                    ph[h / 2 + 1] = cache::pack_f16x2(p[h + 2], p[h + 3]);
+                    asm("max.f16x2 %0, %0, %1;" : "+r"(top) : "r"(ph[h / 2]));
+                    asm("max.f16x2 %0, %0, %1;" : "+r"(top) : "r"(ph[h / 2 + 1]));
+                }
+                // halves compare as whole numbers: none is negative (0x5C00: 2^8)
+                return (top & 0xFFFFu) > 0x5C00u || (top >> 16) > 0x5C00u;
+            };
+            bool over = true;
+            if (ok) {
+                tc_fence_after_sync();
+                load_scores();
+                over = weights();
             }
             bool resc = false;
-            if (named_bar_or(barrier, 128, !ok || top > kTop)) {
-                float v[RG];
+            if (named_bar_or(barrier, 128, over)) {
+                if (ok) {
+                    load_scores();
+                    float v[RG];
 #pragma unroll
-                for (int h = 0; h < RG; ++h)
-                    v[h] = value(h, 0.0f);
-                const float wmax = reduce_scatter<true, RG>(v, lane);
-                const int row = RG == 32 ? lane : lane >> 1;
-                red[w4 * N + row] = wmax;
+                    for (int h = 0; h < RG; ++h)
+                        v[h] = __uint_as_float(sr[h]) * a.c_log2;
+                    red[w4 * N + (RG == 32 ? lane : lane >> 1)] = reduce_scatter<true, RG>(v, lane);
+                }
                 if (!named_bar_and(barrier, 128, ok)) {
                     fail();
                     break;
@@ -667,9 +715,8 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
                     const float m = mneg[lane];
                     float f = 1.0f;
                     if (x + m > kTop) {
-                        const float to = -x;
-                        f = ex2_approx(to - m);  // 0 where no score was seen before
-                        mneg[lane] = to;
+                        f = ex2_approx(-x - m);  // 0 where no score was seen before
+                        mneg[lane] = -x;
                     }
                     alpha[lane] = f;
                 }
@@ -678,21 +725,21 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
 #pragma unroll
                 for (int h = 0; h < RG; ++h)
                     l[h] *= alpha[h];
+                weights();
             }
-            // weights, their sum and their two terms
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&bar[K::kBSFree + stage]);
+            // their sum and their two terms
             uint32_t hi[RG / 4], lo[RG / 4];
 #pragma unroll
             for (int h = 0; h < RG; h += 4) {
-                const float4 m4 = *reinterpret_cast<const float4 *>(mneg + h);
-                float p[4] = {value(h, m4.x), value(h + 1, m4.y), value(h + 2, m4.z), value(h + 3, m4.w)};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    p[e] = ex2_approx(p[e]);
-                    l[h + e] += p[e];
-                }
+                fadd2(l[h], l[h + 1], p[h], p[h + 1]);
+                fadd2(l[h + 2], l[h + 3], p[h + 2], p[h + 3]);
                 uint32_t h0, l0, h1, l1;
-                split2<N == 64>(p[0], p[1], h0, l0);
-                split2<N == 64>(p[2], p[3], h1, l1);
+                split2<N == 64>(ph[h / 2], h0, l0);
+                split2<N == 64>(ph[h / 2 + 1], h1, l1);
                 hi[h / 4] = h0 | h1 << 16;
                 lo[h / 4] = l0 | l1 << 16;
             }
@@ -702,10 +749,11 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
                 const uint32_t x = (uint32_t)(s >> 1) & 3u;
 #pragma unroll
                 for (int k = 0; k < RG / 16; ++k) {
-                    const uint32_t ch = (uint32_t)((N == 64 ? 2 * wg : N == 16 ? 2 * stage : 0) + k);
-                    const uint32_t cl = N == 64 ? ch : ch + RG / 16;
+                    const uint32_t ch = (uint32_t)(N == 64 ? 2 * wg + k : N == 32 ? wg : 2 * stage);
+                    const uint32_t cl = N == 64 ? ch : N == 32 ? ch + 2 : ch + 1;
                     sts128(pb + ((ch ^ x) << 4), hi[4 * k], hi[4 * k + 1], hi[4 * k + 2], hi[4 * k + 3]);
-                    sts128(pb + (N == 64 ? K::kPTerm : 0u) + ((cl ^ x) << 4), lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
+                    sts128(pb + (N == 64 ? K::kPTerm : 0u) + ((cl ^ x) << 4), lo[4 * k], lo[4 * k + 1], lo[4 * k + 2],
+                           lo[4 * k + 3]);
                 }
             }
             if (resc && !first) {
@@ -715,19 +763,19 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
                 if (ok) {
                     tc_fence_after_sync();
 #pragma unroll 1
-                    for (int k = 0; k < 4; ++k) {
-#pragma unroll 1
-                        for (int half = 0; half < (N == 32 ? 2 : 1); ++half) {
-                            uint32_t o[32];
-                            const uint32_t ta = tmem + K::kColO + (uint32_t)(k * K::kOCols + (N == 64 ? 32 * wg : 32 * half)) + lane_off;
-                            tmem_ld32(ta, o);
-                            tmem_ld_wait();
-                            reg_fence_cols<32>(o);
+                    for (int k = 0; k < 4 * K::kTerms; ++k) {
+                        uint32_t o[RG];
+                        const uint32_t ta = tmem + K::kColO + (uint32_t)((k & 3) * K::kOCols + (k >> 2) * N + RG * wg) + lane_off;
+                        tmem_ld_cols<RG>(ta, o);
+                        tmem_ld_wait();
+                        reg_fence_cols<RG>(o);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha[e & (RG - 1)]);
+                        for (int e = 0; e < RG; ++e)
+                            o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha[e]);
+                        if constexpr (RG == 32)
                             tmem_st32(ta, o);
-                        }
+                        else
+                            tmem_st16(ta, o);
                     }
                     tmem_st_wait();
                 }
@@ -737,14 +785,14 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&bar[K::kBPFull + stage]);
-            if (++vs == K::kStages) {
+            if (++vs == K::kStages)
                 vs = 0;
-                vph ^= 1u;
+            if (++e == K::kTiles) {
+                e = 0;
+                eph ^= 1u;
             }
-            if (!last) {
-                c = d;
+            if (!(flags & kLast))
                 continue;
-            }
 
             // ------------------------------------------------ end of a block
             ok = ok && mbar_wait(&bar[K::kBPEmpty + stage], kph, abort_flag);
@@ -756,16 +804,17 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
                 break;
             }
             tc_fence_after_sync();
-            const long long xs = c.x - c.t, xe = xs + c.T;
-            const bool sole = a.whole || (xs >= x0 && xe <= x1);
-            const int slot = (2 * g + (xs >= x0 ? 1 : 0)) * a.hb + hs;
-            float *const pp = a.part + (long long)slot * N * kVDim;
-            const int rows = b.rows - wg * RG;  // of this group
+            const Piece *const piece = reinterpret_cast<const Piece *>(smem + K::kOffPiece) + seg % kPieces;
+            const bool sole = piece->sole != 0;
+            const int slot = piece->slot, rows = piece->rows - wg * RG;  // rows of this group
+            const long long out_row = piece->first + wg * RG;
+            const uint32_t turn = sbase + K::kOffOut + (uint32_t)(warp - 4) * 1024u;
+            float *const pp = a.part + ((long long)slot * N + wg * RG) * kVDim;
             if (s < RG && s < rows) {
                 const float L = (red[s] + red[N + s]) + (red[2 * N + s] + red[3 * N + s]);
                 if (sole) {
                     if (a.lse)
-                        a.lse[b.first + wg * RG + s] = L == 0.0f ? -INFINITY : (log2f(L) - mneg[s]) * cache::kLn2;
+                        a.lse[out_row + s] = L == 0.0f ? -INFINITY : (log2f(L) - mneg[s]) * cache::kLn2;
                 } else {
                     __stcg(a.ml + ((long long)slot * N + wg * RG + s) * 2, -mneg[s]);
                     __stcg(a.ml + ((long long)slot * N + wg * RG + s) * 2 + 1, L);
@@ -775,49 +824,168 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
             named_bar_sync(barrier, 128);
 #pragma unroll 1
             for (int k = 0; k < 4; ++k) {
-                uint32_t o[32], o2[32];
-                tmem_ld32(tmem + K::kColO + (uint32_t)(k * K::kOCols + (N == 64 ? 32 * wg : 0)) + lane_off, o);
-                if (N == 32)
-                    tmem_ld32(tmem + K::kColO + (uint32_t)(k * K::kOCols + 32) + lane_off, o2);
+                uint32_t o[RG], o2[RG];
+                const uint32_t ta = tmem + K::kColO + (uint32_t)(k * K::kOCols + RG * wg) + lane_off;
+                tmem_ld_cols<RG>(ta, o);
+                if (K::kTerms > 1)
+                    tmem_ld_cols<RG>(ta + N, o2);
                 tmem_ld_wait();
-                reg_fence_cols<32>(o);
-                if (N == 32)
-                    reg_fence_cols<32>(o2);
+                reg_fence_cols<RG>(o);
+                if (K::kTerms > 1) {
+                    reg_fence_cols<RG>(o2);
 #pragma unroll
-                for (int h = 0; h < RG; ++h) {
-                    float y = __uint_as_float(o[h]);
-                    if (N == 32)
-                        y += __uint_as_float(o2[h]) * (1.0f / K::kLo);
-                    if (N == 16)
-                        y += __uint_as_float(o[(h + 16) & 31]) * (1.0f / K::kLo);
-                    if (h < rows) {
-                        if (sole)
-                            a.out[(b.first + wg * RG + h) * kVDim + k * 128 + s] =
-                                __bfloat16_as_ushort(__float2bfloat16_rn(alpha[h] == 0.0f ? 0.0f : y * alpha[h]));
-                        else
-                            __stcg(pp + (wg * RG + h) * kVDim + k * 128 + s, y);
+                    for (int h = 0; h < RG; ++h)
+                        o[h] = __float_as_uint(__uint_as_float(o[h]) + __uint_as_float(o2[h]) * (1.0f / K::kLo));
+                }
+                // 32 columns of the warp, turned in its own kilobyte so that 16 bytes are
+                // stored at a time (2-byte stores: 20 cycles each, 21000 a block)
+                if (sole) {
+#pragma unroll
+                    for (int q = 0; q < RG; q += 16) {
+#pragma unroll
+                        for (int h = 0; h < 16; ++h) {
+                            const float f = alpha[q + h], y = f == 0.0f ? 0.0f : __uint_as_float(o[q + h]) * f;
+                            asm volatile("st.shared.u16 [%0], %1;" ::"r"(turn + 64u * h + 2u * lane),
+                                         "h"(__bfloat16_as_ushort(__float2bfloat16_rn(y))) : "memory");
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int j = 0; j < 16; j += 8) {
+                            const int r = j + (lane >> 2);
+                            const uint4 v = lds128(turn + 64u * r + 16u * (lane & 3));
+                            if (q + r < rows)
+                                *reinterpret_cast<uint4 *>(a.out + (out_row + q + r) * kVDim + k * 128 + w4 * 32 + 8 * (lane & 3)) = v;
+                        }
+                        __syncwarp();
+                    }
+                } else {
+#pragma unroll
+                    for (int q = 0; q < RG; q += 8) {
+#pragma unroll
+                        for (int h = 0; h < 8; ++h)
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(turn + 128u * h + 4u * lane), "r"(o[q + h]) : "memory");
+                        __syncwarp();
+#pragma unroll
+                        for (int j = 0; j < 8; j += 4) {
+                            const int r = j + (lane >> 3);
+                            const uint4 v = lds128(turn + 128u * r + 16u * (lane & 7));
+                            if (q + r < rows)
+                                __stcg(reinterpret_cast<uint4 *>(pp + (q + r) * kVDim + k * 128 + w4 * 32 + 4 * (lane & 7)), v);
+                        }
+                        __syncwarp();
                     }
                 }
             }
             tc_fence_before_sync();
-            if (!more)
+            if (flags & kEnd)
                 break;
-            c = d;
-            // mneg and alpha are written anew only after every thread read them
+            // mneg and alpha (and P, where N = 16) are written anew only after every thread read them
             named_bar_sync(barrier, 128);
         }
     } else {
+        if constexpr (K::kSplit)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if (warp == K::kPlanWarp) {
+        // ------------------------------------------------------------ planner
+        // A lane looks up tokens lane, lane + 32, ... of a tile, whose table entries were
+        // asked for a tile earlier. A tile is described once the producers took the tile
+        // kAhead before it, and with it the slot of the tile kTiles before it: so the values
+        // of that one, whose place the description takes, have been read. (A piece's place:
+        // kPieces pieces later, when all outputs but those of the last kTiles tiles are out.)
+        Cursor c = range->at;
+        int page[4], off[4], seg = -1, e = 0;
+        Block b = block_of(a, c, hs, N);
+        auto look_up = [&](const Cursor &f, int end) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int tok = f.t * kTile + 32 * k + lane;
+                page[k] = kNoPage;
+                if (tok < end) {
+                    const int n = a.c.page_of(tok);
+                    page[k] = __ldg(a.c.bt + (long long)f.i * a.c.W + n);
+                    off[k] = tok - n * a.c.P;
+                }
+            }
+        };
+        look_up(c, b.end);
+        for (int it = 0;; ++it) {
+            const bool first = it == 0 || c.t == 0;
+            uint32_t row[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                row[k] = paged::kNoRow;
+                if (page[k] != kNoPage) {
+                    if (page[k] < 0 || (long long)page[k] >= a.c.nb)
+                        atomicOr(a.c.status, (uint32_t)PMQA_DEV_BAD_BLOCK_ID);
+                    else
+                        row[k] = (uint32_t)page[k] * (uint32_t)a.c.P + (uint32_t)off[k];
+                }
+            }
+            Cursor d = c;
+            const bool more = next_tile(a, d, x1), last = !more || d.t == 0;
+            const Block here = b;
+            if (more) {
+                if (last)
+                    b = block_of(a, d, hs, N);
+                look_up(d, b.end);
+            }
+            if (it >= K::kAhead) {
+                const int j = it - K::kAhead;
+                if (!__all_sync(kFull, mbar_wait(&bar[K::kBUsed + j % K::kTiles], (uint32_t)(j / K::kTiles) & 1u, abort_flag))) {
+                    fail();
+                    break;
+                }
+            }
+            Tile *const tile = reinterpret_cast<Tile *>(smem + K::kOffInfo) + e;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t have = __ballot_sync(kFull, row[k] != paged::kNoRow);
+                reinterpret_cast<uint32_t *>(smem + K::kOffRows)[it % K::kAhead * 128 + 32 * k + lane] = row[k];
+                if (lane == k)
+                    tile->have[k] = have;
+            }
+            if (first)
+                ++seg;
+            if (lane == 0) {
+                tile->tok = c.t * kTile;
+                tile->flags = (first ? kFirst : 0) | (last ? kLast : 0) | (more ? 0 : kEnd);
+                if (first) {
+                    const long long xs = c.x - c.t;
+                    const bool starts = xs >= x0;
+                    Piece *const piece = reinterpret_cast<Piece *>(smem + K::kOffPiece) + seg % kPieces;
+                    piece->first = here.first;
+                    piece->rows = here.rows;
+                    piece->last = here.last;
+                    piece->sole = a.whole || (starts && xs + c.T <= x1);
+                    piece->slot = (2 * g + (starts ? 1 : 0)) * a.hb + hs;
+                }
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&bar[K::kBInfo + e]);
+            if (!more)
+                break;
+            c = d;
+            if (++e == K::kTiles)
+                e = 0;
+        }
+        if (hs == 0 && lane == 0) {
+            // the last unit goes on in later ranges and starts in this one: to be joined
+            const long long xs = c.x - c.t, xe = xs + c.T;
+            if (!a.whole && xs >= x0 && xe > x1)
+                a.meta[g] = make_int4(c.i, c.u, range_of(range->total, range->C, xe - 1) - g + 1, 0);
+        }
+        } else if (warp == K::kMmaWarp) {
         // ------------------------------------------------------------ products
-        // Two streams, each issued as soon as its inputs are ready (polled without
-        // suspending): the scores of tile nq and the output update of tile np. The
+        // Two streams, each issued as soon as its inputs are ready: the scores of tile nq and the output update of tile np. The
         // whole warp walks them, so that descriptors stay in uniform registers; one
         // elected lane issues. The update goes 32 tokens at a time over all value
         // columns, and each 32 tokens' values are free for the loads when it is done.
-        Cursor cq = s_range.at, cp = cq;
+        const Tile *const tiles = reinterpret_cast<const Tile *>(smem + K::kOffInfo);
         int nq = 0, np = 0, idle = 0;
         bool more_q = true, more_p = true;
-        int qv = 0, pv = 0;  // value slots of tiles nq and np
-        uint32_t qvph = 0;
+        int qv = 0, pv = 0, qe = 0, pe = 0;  // value slots and descriptions of tiles nq and np
+        uint32_t qvph = 0, qeph = 0;
         uint64_t idle_since = 0;
         bool ok = true;
         const uint64_t kd = sw128_kmajor_desc_sbo(sbase, kVGroup) , vd = sw128_mnmajor_desc(sbase, 1024u, kVGroup);
@@ -827,7 +995,8 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
             if (np < nq) {
                 const int sb = np & 1;
                 if (__all_sync(kFull, mbar_test(&bar[K::kBPFull + sb], (uint32_t)(np >> 1) & 1u))) {
-                    const bool first = np == 0 || cp.t == 0;
+                    const uint32_t flags = tiles[pe].flags;
+                    const bool first = flags & kFirst;
                     tc_fence_after_sync();
                     const uint64_t av = vd + ((K::kOffV + (uint32_t)pv * kVStage) >> 4);
                     const uint64_t bv = pd + ((K::kOffP + (uint32_t)sb * K::kPStage) >> 4);
@@ -849,22 +1018,26 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
                     __syncwarp();
                     if (++pv == K::kStages)
                         pv = 0;
+                    if (++pe == K::kTiles)
+                        pe = 0;
                     ++np;
-                    more_p = next_tile(a, cp, x1);
+                    more_p = !(flags & kEnd);
                     prog = true;
                 }
             }
             if (more_q) {
                 const int sb = nq & 1;
                 const uint32_t ph = (uint32_t)(nq >> 1) & 1u;
-                if (__all_sync(kFull, mbar_test(&bar[K::kBReady + qv], qvph) && mbar_test(&bar[K::kBSFree + sb], ph ^ 1u))) {
+                if (__all_sync(kFull, mbar_test(&bar[K::kBReady + qv], qvph) && mbar_test(&bar[K::kBInfo + qe], qeph) &&
+                                             mbar_test(&bar[K::kBSFree + sb], ph ^ 1u))) {
                     fence_proxy_async_smem();  // cp.async writes -> tensor-core reads
                     tc_fence_after_sync();
                     const uint64_t av = kd + ((K::kOffV + (uint32_t)qv * kVStage) >> 4), bv = kd + (K::kOffQV >> 4);
                     const uint64_t ar = rd + ((K::kOffR + (uint32_t)sb * kRStage) >> 4), br = rd + (K::kOffQR >> 4);
                     const uint32_t dS = tmem + K::kColS + (uint32_t)(sb * N);
+                    const uint32_t flags = tiles[qe].flags;
                     ++nq;
-                    more_q = next_tile(a, cq, x1);
+                    more_q = !(flags & kEnd);
                     if (elect_one()) {
 #pragma unroll
                         for (int kb = 0; kb < 4; ++kb)
@@ -878,13 +1051,17 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
                             umma_e4m3(dS, ar + 2u * ks, br + 2u * ks, K::kIdescQK, 1u);
                         umma_commit(&bar[K::kBSFull + sb]);
                         umma_commit(&bar[K::kBREmpty + sb]);
-                        if (!more_q || cq.t == 0)
+                        if (flags & kLast)
                             umma_commit(&bar[K::kBQEmpty]);
                     }
                     __syncwarp();
                     if (++qv == K::kStages) {
                         qv = 0;
                         qvph ^= 1u;
+                    }
+                    if (++qe == K::kTiles) {
+                        qe = 0;
+                        qeph ^= 1u;
                     }
                     prog = true;
                 }
@@ -894,7 +1071,13 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
                 idle_since = 0;
                 continue;
             }
-            // nothing ready: every 64 empty polls, the abort flag and the clock
+            // nothing ready: sleep on what comes next for a moment, so that the polls
+            // take no issue slots from the softmax; every 64 times the abort flag and
+            // the clock
+            if (np < nq)
+                mbar_try_wait_sleep(&bar[K::kBPFull + (np & 1)], (uint32_t)(np >> 1) & 1u, 64u);
+            else
+                mbar_try_wait_sleep(&bar[K::kBReady + qv], qvph, 64u);
             if (++idle < 64)
                 continue;
             idle = 0;
@@ -912,6 +1095,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
             umma_commit(&bar[K::kBDrain]);
             if (!mbar_wait(&bar[K::kBDrain], 0u, nullptr))
                 atomicOr(a.c.status, (uint32_t)PMQA_DEV_TIMEOUT);
+        }
         }
     }
     __syncwarp();
