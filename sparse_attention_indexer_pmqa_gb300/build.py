@@ -40,6 +40,7 @@ def _sources():
              ("pmqa_index_rows", os.path.join(CSRC, "pmqa_index_rows.cu"), []),
              ("pmqa_latent_rows", os.path.join(CSRC, "pmqa_latent_rows.cu"), []),
              ("pmqa_latent_attn", os.path.join(CSRC, "pmqa_latent_attn.cu"), []),
+             ("pmqa_latent_wide", os.path.join(CSRC, "pmqa_latent_wide.cu"), []),
              ("pmqa_gather_probe", os.path.join(CSRC, "pmqa_gather_probe.cu"), [])]
     for name in ("", "_append", "_attn", "_prompt", "_weigh", "_window", "_evict"):
         units.append((f"pmqa_cache{name}", os.path.join(CSRC, f"pmqa_cache{name}.cu"), []))

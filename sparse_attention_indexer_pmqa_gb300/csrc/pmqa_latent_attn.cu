@@ -31,282 +31,14 @@
 #include <algorithm>
 #include <cmath>
 
-#include "pmqa_latent.cuh"
-#include "pmqa_paged.cuh"
+#include "pmqa_latent_attn.cuh"
 
 namespace pmqa {
 namespace latent {
 
-using cache::Request;
-using cache::View;
-using namespace mla;
-
-constexpr uint32_t kFull = cache::kFull;
 constexpr int kTile = 128;      // tokens per tile
-constexpr int kMaxHeads = 128;
-constexpr int kMaxCtas = 160;   // workspace parts: 2 per CTA
-constexpr int kPad = 2;         // tiles' worth of starting and ending a block
-constexpr int kLeast = 2;       // fewest tiles that a CTA takes
-constexpr int kNoPage = (int)0x80000000;  // no token there (a table entry is negative where it is bad)
-constexpr int kWhole = 512;     // tables of up to so many tokens: blocks are not cut
-constexpr float kTop = 8.0f;    // p = 2^(x - m); m moves when a p passes 2^kTop
-constexpr float kUnseen = 1e30f;   // -m of a row that has seen no score: above every |x|
-constexpr double kMaxFactor = 1e20;  // |c_log2|: times a product of two rows (1.2e8) well below kUnseen
-
-constexpr size_t kWsMeta = cache::kStatusBytes;
-constexpr size_t kWsMl = kWsMeta + kMaxCtas * 16;
-constexpr size_t kWsPart = kWsMl + (size_t)2 * kMaxCtas * 64 * 2 * 4;
-constexpr size_t kWorkspace = kWsPart + (size_t)2 * kMaxCtas * 64 * kVDim * 4;
-
-struct Args {
-    View c;
-    const uint8_t *q;   // [rows, heads, 576]
-    const uint8_t *kv;  // [num_blocks * P, 576]
-    uint16_t *out;
-    float *lse;
-    float c_log2;       // sm_scale * q_scale * kv_scale * log2(e)
-    float kv_scale;
-    int heads;
-    int toks;           // query tokens of a block (a power of two; 1 where hb > 1)
-    int hb;             // blocks of a query token (CTAs that walk the same tokens)
-    int ranges;         // parts that the sequence is cut into at most
-    int whole;          // blocks are not cut
-    int4 *meta;         // [ranges]: (request, unit, parts, 0) of the unit cut at the range's end
-    float *ml;          // [2 ranges hb][N][2]
-    float *part;        // [2 ranges hb][N][512]
-};
-
-// ------------------------------------------------------------- the sequence
-//
-// Request i has units u < U_i = ceil(n_i / toks) of `toks` query tokens; unit u has
-// the tiles up to the slot of its last token, whether or not that token exists:
-//   T = floor((ctx - n + toks u + toks - 1) / 128) + 1 = floor((f + u) / w) + 1,
-// f = ceil((ctx - n) / toks), w = 128 / toks. kPad places without work follow each
-// unit's tiles.
-
-struct Req {
-    Request q;
-    int f, U;
-};
-
-__device__ __forceinline__ Req load_req(const Args &a, int i, bool tell)
-{
-    Req r;
-    r.q = cache::load_request(a.c, i, tell);
-    r.U = (r.q.n + a.toks - 1) / a.toks;
-    r.f = (max(r.q.ctx - r.q.n, 0) + a.toks - 1) / a.toks;
-    return r;
-}
-
-// sum of floor(y / w) over y < x
-__device__ __forceinline__ long long floor_sum(long long x, int w)
-{
-    const long long q = x / w;
-    return (long long)w * (q * (q - 1) / 2) + q * (x - q * w);
-}
-
-// places of the first u units
-__device__ __forceinline__ long long places(const Args &a, const Req &r, int u)
-{
-    const int w = kTile / a.toks;
-    return floor_sum((long long)r.f + u, w) - floor_sum(r.f, w) + (long long)u * (1 + kPad);
-}
-
-// Where a role is: unit u of request i, tile t of T, at place x of the sequence.
-struct Cursor {
-    Req r;
-    int i, u, t, T;
-    long long x;
-
-    __device__ __forceinline__ void set_unit(const Args &a) { T = (r.f + u) / (kTile / a.toks) + 1; }
-
-    // the next unit; false past the last
-    __device__ __forceinline__ bool next_unit(const Args &a)
-    {
-        x += T + kPad - t;
-        t = 0;
-        ++u;
-        while (u >= r.U) {
-            if (++i >= a.c.bs)
-                return false;
-            r = load_req(a, i, false);
-            u = 0;
-        }
-        set_unit(a);
-        return true;
-    }
-};
-
-struct Range {
-    long long x0, x1, total;
-    int C;       // ranges with work
-    Cursor at;   // place x0
-    int any;
-};
-
-__device__ __forceinline__ long long range_start(long long total, int C, long long b)
-{
-    return b * total / C;
-}
-
-__device__ __forceinline__ int range_of(long long total, int C, long long x)
-{
-    return (int)(((x + 1) * (long long)C - 1) / total);
-}
-
-// Called by the whole CTA; the result is in *s_range after the last barrier. s_sum:
-// THREADS / 16 words.
-template <int THREADS>
-__device__ __forceinline__ void find_range(const Args &a, int g, long long *s_sum, Range *s_range)
-{
-    long long *const s_units = s_sum + THREADS / 32;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    long long sum = 0, units = 0;
-    for (int i = tid; i < a.c.bs; i += THREADS) {
-        const Req r = load_req(a, i, blockIdx.x == 0);
-        sum += places(a, r, r.U);
-        units += r.U;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        sum += __shfl_xor_sync(kFull, sum, o);
-        units += __shfl_xor_sync(kFull, units, o);
-    }
-    if (lane == 0) {
-        s_sum[warp] = sum;
-        s_units[warp] = units;
-    }
-    if (tid == 0)
-        s_range->any = 0;
-    __syncthreads();
-    long long total = 0;
-    units = 0;
-    for (int k = 0; k < THREADS / 32; ++k) {
-        total += s_sum[k];
-        units += s_units[k];
-    }
-    // no more ranges than keep kLeast tiles each
-    const int C = (int)min((long long)a.ranges, max(units > 0 ? 1ll : 0ll, (total - units * kPad) / kLeast));
-    const long long x0 = g < C ? range_start(total, C, g) : total;
-    const long long x1 = g < C ? range_start(total, C, g + 1) : total;
-    long long base = 0;
-    for (int i0 = 0; x0 < x1 && i0 < a.c.bs; i0 += THREADS) {
-        const int i = i0 + tid;
-        long long n = 0;
-        Req r{};
-        if (i < a.c.bs) {
-            r = load_req(a, i, false);
-            n = places(a, r, r.U);
-        }
-        long long inc = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(kFull, inc, o);
-            if (lane >= o)
-                inc += y;
-        }
-        __syncthreads();
-        if (lane == 31)
-            s_sum[warp] = inc;
-        __syncthreads();
-        long long lo = base + inc - n, all = 0;
-        for (int k = 0; k < THREADS / 32; ++k) {
-            if (k < warp)
-                lo += s_sum[k];
-            all += s_sum[k];
-        }
-        if (n > 0 && lo <= x0 && x0 < lo + n) {
-            // the unit that holds place x0
-            const long long y = x0 - lo;
-            int ua = 0, ub = r.U;
-            while (ub - ua > 1) {
-                const int mid = ua + (ub - ua) / 2;
-                if (places(a, r, mid) <= y)
-                    ua = mid;
-                else
-                    ub = mid;
-            }
-            Cursor c;
-            c.r = r;
-            c.i = i;
-            c.u = ua;
-            c.t = (int)(y - places(a, r, ua));
-            c.x = x0;
-            c.set_unit(a);
-            // behind the tiles, or (whole) inside a unit: the next one
-            bool any = true;
-            if (c.t >= c.T || (a.whole && c.t > 0))
-                any = c.next_unit(a);
-            s_range->at = c;
-            s_range->any = any && c.x < x1;
-        }
-        base += all;
-        if (base > x0)
-            break;  // the same for every thread
-    }
-    if (tid == 0) {
-        s_range->x0 = x0;
-        s_range->x1 = x1;
-        s_range->total = total;
-        s_range->C = C;
-    }
-    __syncthreads();
-}
-
-// The next tile of a range; false at its end.
-__device__ __forceinline__ bool next_tile(const Args &a, Cursor &c, long long x1)
-{
-    ++c.t;
-    ++c.x;
-    if (c.t < c.T)
-        return a.whole || c.x < x1;
-    return c.next_unit(a) && c.x < x1;
-}
-
-// ------------------------------------------------------------- one block of rows
-
-// The packed rows of a unit that CTA `hs` of its range takes.
-struct Block {
-    long long first;  // row of q and out, in heads
-    int rows;         // packed rows
-    int last;         // last slot that the first row sees
-    int end;          // slots that some row sees
-};
-
-__device__ __forceinline__ Block block_of(const Args &a, const Cursor &c, int hs, int N)
-{
-    Block b;
-    const int j0 = c.u * a.toks;
-    const int n = min(a.toks, c.r.q.n - j0);
-    const int h0 = hs * N;
-    b.rows = a.hb > 1 ? min(N, a.heads - h0) : n * a.heads;
-    b.first = ((long long)c.r.q.r0 + j0) * a.heads + h0;
-    b.last = c.r.q.ctx - c.r.q.n + j0;
-    b.end = min(c.r.q.ctx, max(0, b.last + n));
-    return b;
-}
 
 // ------------------------------------------------------------- kernel
-
-// What the planner tells the others of a tile, and of its piece of a unit (the tiles of
-// a unit in one range).
-enum { kFirst = 1, kLast = 2, kEnd = 4 };  // tile of its piece, or of the range
-struct Tile {
-    uint32_t have[4];  // a bit per token that is there
-    int tok;           // first token
-    uint32_t flags;
-    uint32_t unused[2];
-};
-struct Piece {
-    long long first;   // row of q and out, in heads
-    int rows;          // packed rows
-    int last;          // last slot that the first row sees
-    int sole;          // the unit lies in this range whole
-    int slot;          // otherwise: of its part
-    int unused[2];
-};
-static_assert(sizeof(Tile) == 32 && sizeof(Piece) == 32, "places in shared memory");
-constexpr int kPieces = 8;
 
 template <int N>
 struct Cfg {
@@ -318,6 +50,7 @@ struct Cfg {
     // their instructions: the L1 cache beside so much shared memory holds 28 KB, and rows
     // pass through it (80 registers, 16 rows a thread: 434 us against 288).
     static constexpr bool kSplit = N == 64;
+    static constexpr int kTile = latent::kTile, kPieces = 8;
     static constexpr int kThreads = 128 + 128 * kGroups + (kSplit ? 128 : 64);
     static constexpr int kAhead = N == 16 ? 1 : 2;        // tiles that the planner is ahead of the producers
     static constexpr int kTiles = kStages + kAhead;       // tiles that are described at a time
@@ -401,65 +134,6 @@ __device__ __forceinline__ float reduce_scatter(float (&v)[NR], int lane)
     return NR == 32 ? v[0] : op(v[0], __shfl_xor_sync(kFull, v[0], 1));
 }
 
-__device__ __forceinline__ uint32_t e4m3x2_of_f16x2(uint32_t h2)
-{
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t b)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)b));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t e5m2x2_of_f16x2(uint32_t h2)
-{
-    uint16_t r;
-    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
-    return r;
-}
-
-// Two weights, an f16 pair, as their terms (bytes 0 and 1): the f16 value of p is off
-// by 2^-11 at most, its difference from the first term exact. SAME: both terms go into one
-// accumulator, so the second has the first's unit: e5m2, which reaches down to 2^-17.
-// Otherwise it is e4m3 of 16 times the difference.
-template <bool SAME>
-__device__ __forceinline__ void split2(uint32_t p, uint32_t &hi, uint32_t &lo)
-{
-    hi = e4m3x2_of_f16x2(p);
-    uint32_t d = f16x2_of_e4m3x2(hi);
-    asm("sub.rn.f16x2 %0, %1, %0;" : "+r"(d) : "r"(p));
-    if (SAME) {
-        lo = e5m2x2_of_f16x2(d);
-    } else {
-        asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(d) : "r"(0x4C004C00u));  // 16
-        lo = e4m3x2_of_f16x2(d);
-    }
-}
-
-// (d0, d1) = (a0, a1) * (b, b) + (c0, c1): one packed fp32x2 multiply-add.
-__device__ __forceinline__ void ffma2_of(float &d0, float &d1, uint32_t a0, uint32_t a1, float b, float c0, float c1)
-{
-    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
-        "mov.b64 ra, {%2, %3};\n\t"
-        "mov.b64 rb, {%4, %4};\n\t"
-        "mov.b64 rc, {%5, %6};\n\t"
-        "fma.rn.f32x2 rd, ra, rb, rc;\n\t"
-        "mov.b64 {%0, %1}, rd;\n\t}"
-        : "=f"(d0), "=f"(d1)
-        : "r"(a0), "r"(a1), "f"(b), "f"(c0), "f"(c1));
-}
-
-// Four codes, NaN (0x7F, 0xFF) replaced by 0.
-__device__ __forceinline__ uint32_t without_nan(uint32_t x)
-{
-    const uint32_t is = ((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-    return x & ~((is >> 7) * 0xFFu);
-}
-
 template <int N>
 __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const __grid_constant__ Args a)
 {
@@ -469,7 +143,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
     const uint32_t sbase = smem_u32(smem);
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(kFull, tid >> 5, 0);
-    const int g = blockIdx.x / a.hb, hs = blockIdx.x - g * a.hb;
+    const int g = blockIdx.x / a.peers, hs = blockIdx.x - g * a.peers;
 
     if (hs == 0 && tid == 0)
         a.meta[g] = make_int4(0, 0, 0, 0);
@@ -483,7 +157,6 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
             atomicOr(a.c.status, (uint32_t)PMQA_DEV_INTERNAL);
         return;
     }
-    const long long x0 = range->x0, x1 = range->x1;
 
     uint64_t *const bar = reinterpret_cast<uint64_t *>(smem + K::kOffBar);
     uint32_t *const misc = reinterpret_cast<uint32_t *>(smem + K::kOffMisc);
@@ -516,10 +189,6 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = misc[0];
-    auto fail = [&]() {
-        atomicOr(a.c.status, (uint32_t)PMQA_DEV_TIMEOUT);
-        *abort_flag = 1;
-    };
 
     if (warp < 4) {
         // ------------------------------------------------------------ producer
@@ -533,7 +202,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
             const int rs = it & 1;
             const uint32_t rph = (uint32_t)(it >> 1) & 1u;
             if (!__all_sync(kFull, mbar_wait(&bar[K::kBInfo + e], eph, abort_flag))) {
-                fail();
+                fail(a, abort_flag);
                 break;
             }
             const Tile *const tile = reinterpret_cast<const Tile *>(smem + K::kOffInfo) + e;
@@ -542,10 +211,10 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
                 // one query buffer: free once the last scores of the block before are done
                 ++seg;
                 if (!__all_sync(kFull, mbar_wait(&bar[K::kBQEmpty], ((uint32_t)seg & 1u) ^ 1u, abort_flag))) {
-                    fail();
+                    fail(a, abort_flag);
                     break;
                 }
-                const Piece *const piece = reinterpret_cast<const Piece *>(smem + K::kOffPiece) + seg % kPieces;
+                const Piece *const piece = reinterpret_cast<const Piece *>(smem + K::kOffPiece) + seg % K::kPieces;
                 const uint8_t *const src = a.q + piece->first * kDim;
                 const int rows = piece->rows;
                 for (int k = tid; k < N * kChunks; k += 128) {
@@ -558,7 +227,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
             // this warp's 32 tokens of the slot
             if (!__all_sync(kFull, mbar_wait(&bar[K::kBVEmpty + 4 * vs + warp], vph ^ 1u, abort_flag) &&
                                        mbar_wait(&bar[K::kBREmpty + rs], rph ^ 1u, abort_flag))) {
-                fail();
+                fail(a, abort_flag);
                 break;
             }
             if (lane == 0)
@@ -625,7 +294,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
 #pragma unroll
                 for (int h = 0; h < RG; ++h)
                     l[h] = 0.0f;
-                const Piece *const piece = reinterpret_cast<const Piece *>(smem + K::kOffPiece) + seg % kPieces;
+                const Piece *const piece = reinterpret_cast<const Piece *>(smem + K::kOffPiece) + seg % K::kPieces;
                 seen_by_all = piece->last;
                 if (lane < RG) {
                     const int r = wg * RG + lane;
@@ -707,7 +376,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
                     red[w4 * N + (RG == 32 ? lane : lane >> 1)] = reduce_scatter<true, RG>(v, lane);
                 }
                 if (!named_bar_and(barrier, 128, ok)) {
-                    fail();
+                    fail(a, abort_flag);
                     break;
                 }
                 if (w4 == 0 && lane < RG) {
@@ -800,11 +469,11 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
             const float wl = reduce_scatter<false, RG>(l, lane);
             red[w4 * N + (RG == 32 ? lane : lane >> 1)] = wl;
             if (!named_bar_and(barrier, 128, ok)) {
-                fail();
+                fail(a, abort_flag);
                 break;
             }
             tc_fence_after_sync();
-            const Piece *const piece = reinterpret_cast<const Piece *>(smem + K::kOffPiece) + seg % kPieces;
+            const Piece *const piece = reinterpret_cast<const Piece *>(smem + K::kOffPiece) + seg % K::kPieces;
             const bool sole = piece->sole != 0;
             const int slot = piece->slot, rows = piece->rows - wg * RG;  // rows of this group
             const long long out_row = piece->first + wg * RG;
@@ -886,95 +555,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
         if constexpr (K::kSplit)
             asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == K::kPlanWarp) {
-        // ------------------------------------------------------------ planner
-        // A lane looks up tokens lane, lane + 32, ... of a tile, whose table entries were
-        // asked for a tile earlier. A tile is described once the producers took the tile
-        // kAhead before it, and with it the slot of the tile kTiles before it: so the values
-        // of that one, whose place the description takes, have been read. (A piece's place:
-        // kPieces pieces later, when all outputs but those of the last kTiles tiles are out.)
-        Cursor c = range->at;
-        int page[4], off[4], seg = -1, e = 0;
-        Block b = block_of(a, c, hs, N);
-        auto look_up = [&](const Cursor &f, int end) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int tok = f.t * kTile + 32 * k + lane;
-                page[k] = kNoPage;
-                if (tok < end) {
-                    const int n = a.c.page_of(tok);
-                    page[k] = __ldg(a.c.bt + (long long)f.i * a.c.W + n);
-                    off[k] = tok - n * a.c.P;
-                }
-            }
-        };
-        look_up(c, b.end);
-        for (int it = 0;; ++it) {
-            const bool first = it == 0 || c.t == 0;
-            uint32_t row[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                row[k] = paged::kNoRow;
-                if (page[k] != kNoPage) {
-                    if (page[k] < 0 || (long long)page[k] >= a.c.nb)
-                        atomicOr(a.c.status, (uint32_t)PMQA_DEV_BAD_BLOCK_ID);
-                    else
-                        row[k] = (uint32_t)page[k] * (uint32_t)a.c.P + (uint32_t)off[k];
-                }
-            }
-            Cursor d = c;
-            const bool more = next_tile(a, d, x1), last = !more || d.t == 0;
-            const Block here = b;
-            if (more) {
-                if (last)
-                    b = block_of(a, d, hs, N);
-                look_up(d, b.end);
-            }
-            if (it >= K::kAhead) {
-                const int j = it - K::kAhead;
-                if (!__all_sync(kFull, mbar_wait(&bar[K::kBUsed + j % K::kTiles], (uint32_t)(j / K::kTiles) & 1u, abort_flag))) {
-                    fail();
-                    break;
-                }
-            }
-            Tile *const tile = reinterpret_cast<Tile *>(smem + K::kOffInfo) + e;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t have = __ballot_sync(kFull, row[k] != paged::kNoRow);
-                reinterpret_cast<uint32_t *>(smem + K::kOffRows)[it % K::kAhead * 128 + 32 * k + lane] = row[k];
-                if (lane == k)
-                    tile->have[k] = have;
-            }
-            if (first)
-                ++seg;
-            if (lane == 0) {
-                tile->tok = c.t * kTile;
-                tile->flags = (first ? kFirst : 0) | (last ? kLast : 0) | (more ? 0 : kEnd);
-                if (first) {
-                    const long long xs = c.x - c.t;
-                    const bool starts = xs >= x0;
-                    Piece *const piece = reinterpret_cast<Piece *>(smem + K::kOffPiece) + seg % kPieces;
-                    piece->first = here.first;
-                    piece->rows = here.rows;
-                    piece->last = here.last;
-                    piece->sole = a.whole || (starts && xs + c.T <= x1);
-                    piece->slot = (2 * g + (starts ? 1 : 0)) * a.hb + hs;
-                }
-            }
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&bar[K::kBInfo + e]);
-            if (!more)
-                break;
-            c = d;
-            if (++e == K::kTiles)
-                e = 0;
-        }
-        if (hs == 0 && lane == 0) {
-            // the last unit goes on in later ranges and starts in this one: to be joined
-            const long long xs = c.x - c.t, xe = xs + c.T;
-            if (!a.whole && xs >= x0 && xe > x1)
-                a.meta[g] = make_int4(c.i, c.u, range_of(range->total, range->C, xe - 1) - g + 1, 0);
-        }
+            plan_tiles<K>(a, smem, bar, range, g, hs, hs == 0, abort_flag);
         } else if (warp == K::kMmaWarp) {
         // ------------------------------------------------------------ products
         // Two streams, each issued as soon as its inputs are ready: the scores of tile nq and the output update of tile np. The
@@ -1090,7 +671,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
             }
         }
         if (!ok)
-            fail();
+            fail(a, abort_flag);
         if (elect_one()) {
             umma_commit(&bar[K::kBDrain]);
             if (!mbar_wait(&bar[K::kBDrain], 0u, nullptr))
@@ -1109,11 +690,10 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
 
 // The parts of every unit that was cut, joined: block (g, y) takes packed row y of
 // the unit that range g begins and later ranges go on with; a thread four columns.
-template <int N>
 __global__ void __launch_bounds__(128) latent_join_kernel(const __grid_constant__ Args a)
 {
     griddep_wait();
-    const int g = blockIdx.x, hs = blockIdx.y / N, row = blockIdx.y % N;
+    const int g = blockIdx.x, hs = blockIdx.y / a.N, row = blockIdx.y - hs * a.N;
     const int4 m = __ldcg(a.meta + g);
     if (m.z < 2)
         return;
@@ -1121,11 +701,11 @@ __global__ void __launch_bounds__(128) latent_join_kernel(const __grid_constant_
     c.i = m.x;
     c.u = m.y;
     c.r = load_req(a, c.i, false);
-    const Block b = block_of(a, c, hs, N);
+    const Block b = block_of(a, c, hs);
     if (row >= b.rows)
         return;
     auto slot = [&](int k) -> long long {
-        return ((long long)(2 * (g + k) + (k == 0 ? 1 : 0)) * a.hb + hs) * N + row;
+        return ((long long)(2 * (g + k) + (k == 0 ? 1 : 0)) * a.hb + hs) * a.N + row;
     };
     float M = -INFINITY;
     for (int k = 0; k < m.z; ++k)
@@ -1158,20 +738,21 @@ __global__ void __launch_bounds__(128) latent_join_kernel(const __grid_constant_
 template <int N>
 cudaError_t launch(Args &a, int sms, cudaStream_t st)
 {
-    a.hb = (a.heads + N - 1) / N;
+    a.tile = kTile;
+    a.N = N;
+    a.pad = 2;
+    a.least = 2;
+    a.hb = a.peers = (a.heads + N - 1) / N;
     a.toks = 1;
     while (a.hb == 1 && 2 * a.toks * a.heads <= N)
         a.toks *= 2;
-    a.ranges = std::max(1, std::min(sms, kMaxCtas) / a.hb);
+    a.ranges = std::max(1, std::min(sms, kMaxCtas) / a.peers);
     static std::atomic<uint64_t> done{0};
     cudaError_t e = cache::allow_smem(latent_attn_kernel<N>, (int)Cfg<N>::kSmem, done);
     if (e != cudaSuccess)
         return e;
-    latent_attn_kernel<N><<<(unsigned)(a.ranges * a.hb), Cfg<N>::kThreads, Cfg<N>::kSmem, st>>>(a);
-    e = cudaGetLastError();
-    if (e != cudaSuccess || a.whole)
-        return e;
-    return cache::launch_early(latent_join_kernel<N>, dim3((unsigned)a.ranges, (unsigned)(a.hb * N)), 128, 0, true, st, a);
+    latent_attn_kernel<N><<<(unsigned)(a.ranges * a.peers), Cfg<N>::kThreads, Cfg<N>::kSmem, st>>>(a);
+    return cudaGetLastError();
 }
 
 }  // namespace latent
@@ -1221,8 +802,11 @@ extern "C" int pmqa_latent_attention(const pmqa_paged_rows *p, const void *q, co
     // packed rows of a block: as many as a request can have, up to 64
     const long long most = std::min<long long>(p->max_rows, p->rows) * heads;
     const cudaStream_t st = cache::cuda(stream);
-    const cudaError_t e = most <= 16   ? launch<16>(a, sms, st)
-                          : most <= 32 ? launch<32>(a, sms, st)
-                                       : launch<64>(a, sms, st);
+    cudaError_t e = most <= 16   ? launch<16>(a, sms, st)
+                    : most <= 32 ? launch<32>(a, sms, st)
+                    : most <= 64 ? launch<64>(a, sms, st)
+                                 : launch_wide(a, sms, st);
+    if (e == cudaSuccess && !a.whole)
+        e = cache::launch_early(latent_join_kernel, dim3((unsigned)a.ranges, (unsigned)(a.hb * a.N)), 128, 0, true, st, a);
     return cache::code_of(e);
 }
