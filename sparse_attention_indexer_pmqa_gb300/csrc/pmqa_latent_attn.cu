@@ -569,8 +569,9 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
         uint32_t qvph = 0, qeph = 0;
         uint64_t idle_since = 0;
         bool ok = true;
-        const uint64_t kd = sw128_kmajor_desc_sbo(sbase, kVGroup) , vd = sw128_mnmajor_desc(sbase, 1024u, kVGroup);
-        const uint64_t rd = sw64_kmajor_desc(sbase, kRGroup), pd = sw64_mnmajor_desc(sbase);
+        const uint64_t kd = sw128_kmajor_desc_sbo(sbase + K::kOffV, kVGroup), qd = sw128_kmajor_desc_sbo(sbase + K::kOffQV, kVGroup);
+        const uint64_t rd = sw64_kmajor_desc(sbase + K::kOffR, kRGroup), qrd = sw64_kmajor_desc(sbase + K::kOffQR, kRGroup);
+        const uint64_t vd = sw128_mnmajor_desc(sbase + K::kOffV, 1024u, kVGroup), pd = sw64_mnmajor_desc(sbase + K::kOffP);
         while (more_p) {
             bool prog = false;
             if (np < nq) {
@@ -579,8 +580,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
                     const uint32_t flags = tiles[pe].flags;
                     const bool first = flags & kFirst;
                     tc_fence_after_sync();
-                    const uint64_t av = vd + ((K::kOffV + (uint32_t)pv * kVStage) >> 4);
-                    const uint64_t bv = pd + ((K::kOffP + (uint32_t)sb * K::kPStage) >> 4);
+                    const uint64_t av = vd + (((uint32_t)pv * kVStage) >> 4), bv = pd + (((uint32_t)sb * K::kPStage) >> 4);
                     if (elect_one()) {
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks) {
@@ -613,23 +613,22 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
                                              mbar_test(&bar[K::kBSFree + sb], ph ^ 1u))) {
                     fence_proxy_async_smem();  // cp.async writes -> tensor-core reads
                     tc_fence_after_sync();
-                    const uint64_t av = kd + ((K::kOffV + (uint32_t)qv * kVStage) >> 4), bv = kd + (K::kOffQV >> 4);
-                    const uint64_t ar = rd + ((K::kOffR + (uint32_t)sb * kRStage) >> 4), br = rd + (K::kOffQR >> 4);
-                    const uint32_t dS = tmem + K::kColS + (uint32_t)(sb * N);
                     const uint32_t flags = tiles[qe].flags;
                     ++nq;
                     more_q = !(flags & kEnd);
+                    const uint64_t av = kd + (((uint32_t)qv * kVStage) >> 4), ar = rd + (((uint32_t)sb * kRStage) >> 4);
+                    const uint32_t dS = tmem + K::kColS + (uint32_t)(sb * N);
                     if (elect_one()) {
 #pragma unroll
                         for (int kb = 0; kb < 4; ++kb)
 #pragma unroll
-                            for (int ks = 0; ks < 4; ++ks)
-                                umma_e4m3(dS, av + (((uint32_t)kb * 1024u + (uint32_t)ks * 32u) >> 4),
-                                          bv + (((uint32_t)kb * 1024u + (uint32_t)ks * 32u) >> 4), K::kIdescQK,
-                                          (kb | ks) != 0 ? 1u : 0u);
+                            for (int ks = 0; ks < 4; ++ks) {
+                                const uint32_t k = (uint32_t)kb * 1024u + (uint32_t)ks * 32u;
+                                umma_e4m3(dS, av + (k >> 4), qd + (k >> 4), K::kIdescQK, (kb | ks) != 0 ? 1u : 0u);
+                            }
 #pragma unroll
                         for (int ks = 0; ks < 2; ++ks)
-                            umma_e4m3(dS, ar + 2u * ks, br + 2u * ks, K::kIdescQK, 1u);
+                            umma_e4m3(dS, ar + 2u * ks, qrd + 2u * ks, K::kIdescQK, 1u);
                         umma_commit(&bar[K::kBSFull + sb]);
                         umma_commit(&bar[K::kBREmpty + sb]);
                         if (flags & kLast)

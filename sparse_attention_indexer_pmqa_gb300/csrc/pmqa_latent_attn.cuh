@@ -260,6 +260,18 @@ __device__ __forceinline__ Block block_of(const Args &a, const Cursor &c, int hs
     return b;
 }
 
+// mbar_wait with all but its first try out of line: the roles' loops wait in many
+// places, and their code together should stay in the instruction caches.
+inline __device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity, const volatile int *abort_flag)
+{
+    return mbar_wait(bar, parity, abort_flag);
+}
+
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, const volatile int *abort_flag)
+{
+    return mbar_try_wait(bar, parity) || wait_long(bar, parity, abort_flag);
+}
+
 // A wait that ran out: recorded, and the CTA's other waits end.
 __device__ __forceinline__ void fail(const Args &a, volatile int *abort_flag)
 {
@@ -269,7 +281,7 @@ __device__ __forceinline__ void fail(const Args &a, volatile int *abort_flag)
 
 // What the planner tells the others of a tile, and of its piece of a unit (the tiles of
 // a unit in one range).
-enum { kFirst = 1, kLast = 2, kEnd = 4 };  // tile of its piece, or of the range
+enum { kFirst = 1, kLast = 2, kEnd = 4, kSteady = 8 };  // first or last of its piece, last of the range, two more in the piece
 struct Tile {
     uint32_t have[4];  // a bit per token that is there
     int tok;           // first token
@@ -337,7 +349,7 @@ __device__ __forceinline__ void plan_tiles(const Args &a, uint8_t *smem, uint64_
         }
         if (it >= K::kAhead) {
             const int j = it - K::kAhead;
-            if (!__all_sync(kFull, mbar_wait(&bar[K::kBUsed + j % K::kTiles], (uint32_t)(j / K::kTiles) & 1u, abort_flag))) {
+            if (!__all_sync(kFull, wait_for(&bar[K::kBUsed + j % K::kTiles], (uint32_t)(j / K::kTiles) & 1u, abort_flag))) {
                 fail(a, abort_flag);
                 break;
             }
@@ -354,7 +366,8 @@ __device__ __forceinline__ void plan_tiles(const Args &a, uint8_t *smem, uint64_
             ++seg;
         if (lane == 0) {
             tile->tok = c.t * (32 * W);
-            tile->flags = (first ? kFirst : 0) | (last ? kLast : 0) | (more ? 0 : kEnd);
+            tile->flags = (first ? kFirst : 0) | (last ? kLast : 0) | (more ? 0 : kEnd) |
+                          (c.t + 2 < c.T && (a.whole || c.x + 2 < x1) ? kSteady : 0);
             if (first) {
                 const long long xs = c.x - c.t;
                 const bool starts = xs >= x0;

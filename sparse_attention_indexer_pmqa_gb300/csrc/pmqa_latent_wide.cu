@@ -4,16 +4,18 @@
 // 128 packed rows to a block, tokens in tiles of 64. Two CTAs take a block, each one
 // half of the value columns (a block's output is 128 x 512 fp32, all of one SM's
 // tensor memory):
-//   S = Q K^T    kind::f8f6f4, M = 128 rows, N = 64 tokens, Q (128 x 576) in tensor memory
-//   p = 2^(x - m), one row to a thread pair; two fp8 terms, to tensor memory
+//   S = Q K^T    kind::f8f6f4, M = 128 rows, N = 64 tokens, Q's 512 latent values in tensor
+//                memory (its 64 rotary ones in shared memory: there are no columns left)
+//   p = 2^(x - m), a row to a thread; two fp8 terms, to tensor memory
 //   O += P V     M = 128 rows, N = 256 value columns, both terms into one accumulator
-// Neither Q nor P passes through shared memory, whose 128 bytes a cycle bound the
+// Neither these nor P pass through shared memory, whose 128 bytes a cycle bound the
 // narrow kernel: a tile of 64 tokens costs 36 KB written, 36 read for the scores and
 // 2 x 16 for the output (832 cycles) against 1088 cycles of products. The price is that
 // both CTAs form the scores: 576 + 576 + 2 * 512 fp8 multiplications a row and token.
-// Roles of the 16 warps: 0-3 copy rows (six slots of 64), 4-11 softmax and output, 12
-// issues the products, 13 looks tokens up. S and P have one buffer each: the scores of
-// the next tile are formed while the softmax works on registers.
+// Roles of the 16 warps: 0-3 copy rows (five slots of 64), 4-11 softmax and output, 12
+// and 14 issue the products, 13 looks tokens up. S has one buffer (the scores of the next tile
+// are formed while the softmax works on registers), P two (with one, each output update
+// waited for the one before through four warps: 1830 cycles a tile).
 #include <algorithm>
 
 #include "pmqa_latent_attn.cuh"
@@ -23,37 +25,42 @@ namespace latent {
 
 struct Wide {
     static constexpr int kTile = 64;                      // tokens per tile
-    static constexpr int kStages = 6;                     // slots of a tile's rows
+    static constexpr int kStages = 5;                     // slots of a tile's rows
     static constexpr int kAhead = 2;                      // tiles that the planner is ahead of the producers
-    static constexpr int kTiles = kStages + kAhead, kPieces = 16;
+    static constexpr int kTiles = kStages + kAhead, kPieces = 10;
     static constexpr int kRows = 128, kThreads = 512;
-    static constexpr int kMmaWarp = 12, kPlanWarp = 13;
+    static constexpr int kMmaWarp = 12, kPlanWarp = 13, kOutWarp = 14;
     static constexpr uint32_t kVBytes = kTile / 8 * kVGroup, kRBytes = kTile / 8 * kRGroup;
-    static constexpr uint32_t kColO = 0, kColQ = 256, kColP = 400, kColS = 448;  // tensor memory
+    static constexpr uint32_t kColO = 0, kColQ = 256, kColP = 384, kColS = 448;  // tensor memory, P twice 32
 
     static constexpr uint32_t kOffV = 0;
     static constexpr uint32_t kOffR = kOffV + kStages * kVBytes;
-    static constexpr uint32_t kOffOut = kOffR + kStages * kRBytes;      // 1 KB for each softmax warp's output
+    static constexpr uint32_t kOffQR = kOffR + kStages * kRBytes;       // the queries' rotary part
+    static constexpr uint32_t kOffOut = kOffQR + kRows / 8 * kRGroup;   // 1 KB for each softmax warp's output
     static constexpr uint32_t kOffRows = kOffOut + 8 * 1024;            // [kAhead][64]
     static constexpr uint32_t kOffInfo = kOffRows + kAhead * kTile * 4; // [kTiles] Tile
     static constexpr uint32_t kOffPiece = kOffInfo + kTiles * 32;       // [kPieces] Piece
     static constexpr uint32_t kOffRange = kOffPiece + kPieces * 32;     // Range
     static constexpr uint32_t kOffRed = kOffRange + 128;                // [2][128]
-    static constexpr uint32_t kOffBar = kOffRed + 2 * kRows * 4;
+    static constexpr uint32_t kOffM = kOffRed + 2 * kRows * 4;          // [128]: -m
+    static constexpr uint32_t kOffBar = kOffM + kRows * 4;
     static constexpr int kBInfo = 0;                    // [kTiles] tile described: the planner
     static constexpr int kBUsed = kBInfo + kTiles;      // [kTiles] its slot is free, its rows read: 4 producer warps
     static constexpr int kBReady = kBUsed + kTiles;     // [stages] rows landed: 128 cp.async arrivals
     static constexpr int kBVEmpty = kBReady + kStages;  // [stages] rows read by both products: MMA commit
-    static constexpr int kBSFull = kBVEmpty + kStages;  // scores in tensor memory: MMA commit
-    static constexpr int kBSFree = kBSFull + 1;         // scores read: 8 softmax warps
-    static constexpr int kBPFull = kBSFree + 1;         // P written, O rescaled: 8 softmax warps
-    static constexpr int kBPEmpty = kBPFull + 1;        // P read: MMA commit
-    static constexpr int kBQFull = kBPEmpty + 1;        // a block's queries in tensor memory: 8 softmax warps
-    static constexpr int kBDrain = kBQFull + 1;
-    static constexpr int kBars = kBDrain + 1;
+    // (pairs by the tile's parity: a softmax group waits on every second tile alone)
+    static constexpr int kBSFull = kBVEmpty + kStages;  // [2] scores in tensor memory: MMA commit
+    static constexpr int kBSFree = kBSFull + 2;         // scores read: 4 softmax warps
+    static constexpr int kBPFull = kBSFree + 1;         // [2] P written, O rescaled: 4 softmax warps
+    static constexpr int kBPEmpty = kBPFull + 2;        // [2] P read: MMA commit
+    static constexpr int kBM = kBPEmpty + 2;            // [2] m published: 4 softmax warps
+    static constexpr int kBQFull = kBM + 2;             // a block's queries in tensor memory: 8 softmax warps
+    static constexpr int kBTurn = kBQFull + 1;          // [2] scores issued: the scores' warp
+    static constexpr int kBDrain = kBTurn + 2;
+    static constexpr int kBars = kBDrain + 2;           // both product warps
     static constexpr uint32_t kOffMisc = kOffBar + kBars * 8;
     static constexpr uint32_t kSmem = kOffMisc + 16;
-    static_assert(kSmem <= 232448 && kOffBar % 8 == 0 && sizeof(Range) <= 128, "shared memory");
+    static_assert(kSmem <= 232448 && kOffBar % 8 == 0 && kOffQR % 1024 == 0 && sizeof(Range) <= 128, "shared memory");
 
     static constexpr uint32_t kIdescQK = idesc_e4m3_f32(kRows, kTile);
     static constexpr uint32_t kIdescPV = idesc_e4m3_f32(kRows, 256) | (1u << 16);  // B MN-major
@@ -70,14 +77,6 @@ __device__ __forceinline__ void umma_f8_ts(uint32_t tmem_d, uint32_t tmem_a, uin
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
         "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
-}
-
-// 8 consecutive TMEM columns of this thread's lane from registers.
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r)
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
 }
 
 __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __grid_constant__ Args a)
@@ -113,12 +112,17 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
             mbar_init(&bar[K::kBInfo + s], 1);
             mbar_init(&bar[K::kBUsed + s], 4);
         }
-        mbar_init(&bar[K::kBSFull], 1);
-        mbar_init(&bar[K::kBSFree], 8);
-        mbar_init(&bar[K::kBPFull], 8);
-        mbar_init(&bar[K::kBPEmpty], 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&bar[K::kBSFull + s], 1);
+            mbar_init(&bar[K::kBPFull + s], 4);
+            mbar_init(&bar[K::kBPEmpty + s], 1);
+            mbar_init(&bar[K::kBM + s], 4);
+            mbar_init(&bar[K::kBTurn + s], 1);
+        }
+        mbar_init(&bar[K::kBSFree], 4);
         mbar_init(&bar[K::kBQFull], 8);
         mbar_init(&bar[K::kBDrain], 1);
+        mbar_init(&bar[K::kBDrain + 1], 1);
         misc[1] = 0;
         mbar_init_fence();
     }
@@ -137,14 +141,14 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
         int vs = 0, e = 0;
         uint32_t vph = 0, eph = 0;
         for (int it = 0;; ++it) {
-            if (!__all_sync(kFull, mbar_wait(&bar[K::kBInfo + e], eph, abort_flag))) {
+            if (!__all_sync(kFull, wait_for(&bar[K::kBInfo + e], eph, abort_flag))) {
                 fail(a, abort_flag);
                 break;
             }
             const uint32_t flags = (reinterpret_cast<const Tile *>(smem + K::kOffInfo) + e)->flags;
             const uint32_t srow = reinterpret_cast<const uint32_t *>(
                 smem + K::kOffRows)[it % K::kAhead * K::kTile + warp * 16 + (lane & 15)];
-            if (!__all_sync(kFull, mbar_wait(&bar[K::kBVEmpty + vs], vph ^ 1u, abort_flag))) {
+            if (!__all_sync(kFull, wait_for(&bar[K::kBVEmpty + vs], vph ^ 1u, abort_flag))) {
                 fail(a, abort_flag);
                 break;
             }
@@ -182,144 +186,183 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
         cp_async_wait_all();
     } else if (warp < K::kMmaWarp) {
         // ------------------------------------------------------------ softmax
-        // Thread (group wg, row): the row's scores of tokens 32 wg .. 32 wg + 31. Both
-        // threads of a row hold the same m. Exits are uniform over both groups: a failed
-        // wait clears `ok`, and they leave together at the next barrier.
+        // The two groups take the tiles in turn, a row to a thread, so that one's waits
+        // and conversions run beside the other's (both on every tile, half a row each:
+        // 2400 cycles a tile, most of them waits). m is theirs in common: it goes from tile
+        // to tile, published before a tile's weights are formed. A warp whose wait failed
+        // takes part in one more barrier, at which all leave.
         asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         const int wg = (warp - 4) >> 2, w4 = warp & 3, row = w4 * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(w4 * 32) << 16);
         float *const red = reinterpret_cast<float *>(smem + K::kOffRed);  // [2][128]
+        float *const shared_m = reinterpret_cast<float *>(smem + K::kOffM);  // [128]: -m
         const uint32_t turn = sbase + K::kOffOut + (uint32_t)(warp - 4) * 1024u;
-        float l0 = 0.0f, l1 = 0.0f, mneg = kUnseen;
+        float l = 0.0f, mneg = kUnseen;
         int seg = -1, vs = 0, e = 0, lim = 0;
         uint32_t eph = 0;
-        bool ok = true;
         for (int it = 0;; ++it) {
-            const uint32_t ph = (uint32_t)it & 1u;
-            ok = ok && mbar_wait(&bar[K::kBInfo + e], eph, abort_flag);
-            ok = __all_sync(kFull, ok);
+            const uint32_t now = (uint32_t)it & 1u, was = now ^ 1u;  // parity of this tile and the one before,
+            const uint32_t ph = (uint32_t)(it >> 1) & 1u, wph = (uint32_t)((it - 1) >> 1) & 1u;  // and their phases
+            if (!__all_sync(kFull, mbar_wait(&bar[K::kBInfo + e], eph, abort_flag))) {
+                fail(a, abort_flag);
+                named_bar_and(1, 256, false);
+                break;
+            }
             const Tile *const tile = reinterpret_cast<const Tile *>(smem + K::kOffInfo) + e;
-            const uint32_t flags = ok ? tile->flags : 0u;
+            const uint32_t flags = tile->flags;
             const bool first = flags & kFirst;
             if (first) {
                 // the row's queries, to tensor memory (the scores of the block before are done)
                 ++seg;
                 const Piece *const piece = reinterpret_cast<const Piece *>(smem + K::kOffPiece) + seg % K::kPieces;
                 const bool is = row < piece->rows;
-                const uint4 *const src = reinterpret_cast<const uint4 *>(a.q + (piece->first + (is ? row : 0)) * kDim) + 20 * wg;
-                uint4 u[20];
+                const uint4 *const src = reinterpret_cast<const uint4 *>(a.q + (piece->first + (is ? row : 0)) * kDim);
+                uint4 u[18];
 #pragma unroll
-                for (int k = 0; k < 20; ++k)
-                    u[k] = is && (wg == 0 || k < 16) ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
+                for (int k = 0; k < 18; ++k)
+                    u[k] = is ? __ldg(src + (k < 16 ? 16 * wg + k : 32 + 2 * wg + k - 16)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-                for (int k = 0; k < 5; ++k)
-                    if (wg == 0 || k < 4)
-                        tmem_st16(lanes + K::kColQ + 80u * wg + 16u * k, &u[4 * k].x);
+                for (int k = 0; k < 4; ++k)
+                    tmem_st16(lanes + K::kColQ + 64u * wg + 16u * k, &u[4 * k].x);
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    sts128(sbase + K::kOffQR + r_offset(row, 2 * wg + k), u[16 + k].x, u[16 + k].y, u[16 + k].z, u[16 + k].w);
                 tmem_st_wait();
+                fence_proxy_async_smem();
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(&bar[K::kBQFull]);
-                l0 = l1 = 0.0f;
+                l = 0.0f;
                 mneg = kUnseen;
                 // rows that do not exist see everything: no mask for their sake
                 lim = is ? piece->last + row / a.heads : 0x7FFFFFFF;
             }
-            ok = ok && mbar_wait(&bar[K::kBSFull], ph, abort_flag);
-            ok = __all_sync(kFull, ok);
-            uint32_t sr[32];
-            float p[32];
-            uint32_t q[16];  // the weights as f16 pairs
-            bool cleaned = false;
-            auto weights = [&]() -> bool {
-                uint32_t top = 0u;
-#pragma unroll
-                for (int k = 0; k < 32; k += 2) {
-                    ffma2_of(p[k], p[k + 1], sr[k], sr[k + 1], a.c_log2, mneg, mneg);
-                    p[k] = ex2_approx(p[k]);
-                    p[k + 1] = ex2_approx(p[k + 1]);
-                    q[k / 2] = cache::pack_f16x2(p[k], p[k + 1]);
-                    asm("max.f16x2 %0, %0, %1;" : "+r"(top) : "r"(q[k / 2]));
+            if (now == (uint32_t)wg) {
+                // what does not wait for the scores comes before them: m as the tile before
+                // left it, the tokens that the row sees
+                if (!first && !__all_sync(kFull, mbar_wait(&bar[K::kBM + was], wph, abort_flag))) {
+                    fail(a, abort_flag);
+                    named_bar_and(1, 256, false);
+                    break;
                 }
-                // halves compare as whole numbers: none is negative (0x5C00: 2^8)
-                return (top & 0xFFFFu) > 0x5C00u || (top >> 16) > 0x5C00u;
-            };
-            bool over = true;
-            if (ok) {
+                if (!first) {
+                    const float m = shared_m[row];
+                    if (m != mneg) {
+                        l *= ex2_approx(m - mneg);
+                        mneg = m;
+                    }
+                }
+                uint32_t sees[2];
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int past = lim - tile->tok - 32 * half;
+                    sees[half] = tile->have[half] & (past >= 31 ? kFull : past < 0 ? 0u : (2u << past) - 1u);
+                }
+                const bool whole = __all_sync(kFull, (sees[0] & sees[1]) == kFull);
+                if (!__all_sync(kFull, mbar_wait(&bar[K::kBSFull + now], ph, abort_flag))) {
+                    fail(a, abort_flag);
+                    named_bar_and(1, 256, false);
+                    break;
+                }
+                uint32_t sr[64];
                 tc_fence_after_sync();
-                tmem_ld32(lanes + K::kColS + 32u * wg, sr);
+                tmem_ld32(lanes + K::kColS, sr);
+                tmem_ld32(lanes + K::kColS + 32u, sr + 32);
                 tmem_ld_wait();
-                reg_fence_cols<32>(sr);
+                reg_fence16(sr);
+                reg_fence16(sr + 16);
+                reg_fence16(sr + 32);
+                reg_fence16(sr + 48);
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(&bar[K::kBSFree]);
-                // tokens that are there and that the row sees
-                const int past = lim - tile->tok - 32 * wg;
-                const uint32_t sees = tile->have[wg] & (past >= 31 ? kFull : past < 0 ? 0u : (2u << past) - 1u);
-                if (!__all_sync(kFull, sees == kFull)) {
+                bool cleaned = false;
+                if (!whole) {
                     const uint32_t never = __float_as_uint(a.c_log2 > 0.0f ? -INFINITY : INFINITY);
-                    uint32_t nan = 0u;
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        const float x = __uint_as_float(sr[k]);
-                        nan |= x != x ? 1u << k : 0u;
-                        sr[k] = sees >> k & 1u ? sr[k] : never;
-                    }
-                    nan = __reduce_or_sync(kFull, nan);
-                    cleaned = nan != 0u;
-                    // in the queries, or in a token's row: then out of its values
-                    for (; nan; nan &= nan - 1u) {
-                        const uint32_t v = sbase + K::kOffV + (uint32_t)vs * K::kVBytes + v_offset(32 * wg + __ffs(nan) - 1, lane);
-                        const uint4 w = lds128(v);
-                        sts128(v, without_nan(w.x), without_nan(w.y), without_nan(w.z), without_nan(w.w));
-                    }
-                }
-                over = weights();
-            }
-            float alpha = 1.0f;
-            if (named_bar_or(1, 256, over)) {
-                float x = -INFINITY;
-                if (ok) {
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t nan = 0u;
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        x = fmaxf(x, __uint_as_float(sr[k]) * a.c_log2);
-                    red[wg * K::kRows + row] = x;
+                        for (int k = 0; k < 32; ++k) {
+                            const float x = __uint_as_float(sr[32 * half + k]);
+                            nan |= x != x ? 1u << k : 0u;
+                            sr[32 * half + k] = sees[half] >> k & 1u ? sr[32 * half + k] : never;
+                        }
+                        nan = __reduce_or_sync(kFull, nan);
+                        cleaned |= nan != 0u;
+                        // in the queries, or in a token's row: then out of its values
+                        for (; nan; nan &= nan - 1u) {
+                            const uint32_t v = sbase + K::kOffV + (uint32_t)vs * K::kVBytes + v_offset(32 * half + __ffs(nan) - 1, lane);
+                            const uint4 w = lds128(v);
+                            sts128(v, without_nan(w.x), without_nan(w.y), without_nan(w.z), without_nan(w.w));
+                        }
+                    }
                 }
-                if (!named_bar_and(1, 256, ok)) {
-                    fail(a, abort_flag);
-                    break;
+                // the row's largest score here, and m: moved where a weight would pass 2^kTop
+                float x;
+                {
+                    float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int k = 0; k < 64; k += 8)
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            const float y0 = __uint_as_float(sr[k + 2 * z]), y1 = __uint_as_float(sr[k + 2 * z + 1]);
+                            t[z] = a.c_log2 > 0.0f ? fmaxf(t[z], fmaxf(y0, y1)) : fmaxf(t[z], fmaxf(-y0, -y1));
+                        }
+                    x = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * fabsf(a.c_log2);
                 }
-                x = fmaxf(x, red[(wg ^ 1) * K::kRows + row]);
+                float alpha = 1.0f;
                 if (x + mneg > kTop) {
                     alpha = ex2_approx(-x - mneg);  // 0 where no score was seen before
                     mneg = -x;
-                    l0 *= alpha;
-                    l1 *= alpha;
+                    l *= alpha;
                 }
-                weights();
-            }
-            uint32_t hi[8], lo[8];
+                if (first || alpha != 1.0f)
+                    shared_m[row] = mneg;
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&bar[K::kBM + now]);
+                // the weights, their sum and their two terms
+                uint32_t hi[16], lo[16];
+                float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-                fadd2(l0, l1, p[k], p[k + 1]);
-                fadd2(l0, l1, p[k + 2], p[k + 3]);
-                uint32_t h0, h1, d0, d1;
-                split2<true>(q[k / 2], h0, d0);
-                split2<true>(q[k / 2 + 1], h1, d1);
-                hi[k / 4] = h0 | h1 << 16;
-                lo[k / 4] = d0 | d1 << 16;
-            }
-            // P, and O where m moved: the output of the tile before is done
-            ok = ok && mbar_wait(&bar[K::kBPEmpty], ph ^ 1u, abort_flag);
-            ok = __all_sync(kFull, ok);
-            if (ok) {
-                tc_fence_after_sync();
+                for (int k = 0; k < 16; ++k) {
+                    float p0, p1, p2, p3;
+                    ffma2_of(p0, p1, sr[4 * k], sr[4 * k + 1], a.c_log2, mneg, mneg);
+                    ffma2_of(p2, p3, sr[4 * k + 2], sr[4 * k + 3], a.c_log2, mneg, mneg);
+                    p0 = ex2_approx(p0);
+                    p1 = ex2_approx(p1);
+                    p2 = ex2_approx(p2);
+                    p3 = ex2_approx(p3);
+                    fadd2(s0, s1, p0, p1);
+                    fadd2(s0, s1, p2, p3);
+                    uint32_t h0, h1, d0, d1;
+                    split2<true>(cache::pack_f16x2(p0, p1), h0, d0);
+                    split2<true>(cache::pack_f16x2(p2, p3), h1, d1);
+                    hi[k] = h0 | h1 << 16;
+                    lo[k] = d0 | d1 << 16;
+                }
+                l += s0 + s1;
+                // this buffer of P is free
+                if (!__all_sync(kFull, mbar_wait(&bar[K::kBPEmpty + now], ph ^ 1u, abort_flag))) {
+                    fail(a, abort_flag);
+                    named_bar_and(1, 256, false);
+                    break;
+                }
                 if (!first && __any_sync(kFull, alpha != 1.0f)) {
+                    // O: the output of the tile before is done
+                    if (!__all_sync(kFull, mbar_wait(&bar[K::kBPEmpty + was], wph, abort_flag))) {
+                        fail(a, abort_flag);
+                        named_bar_and(1, 256, false);
+                        break;
+                    }
+                    tc_fence_after_sync();
 #pragma unroll 1
-                    for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < 8; ++k) {
                         uint32_t o[32];
-                        const uint32_t ta = lanes + K::kColO + 128u * wg + 32u * k;
+                        const uint32_t ta = lanes + K::kColO + 32u * k;
                         tmem_ld32(ta, o);
                         tmem_ld_wait();
                         reg_fence_cols<32>(o);
@@ -329,16 +372,17 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
                         tmem_st32(ta, o);
                     }
                 }
-                tmem_st8(lanes + K::kColP + 8u * wg, hi);
-                tmem_st8(lanes + K::kColP + 16u + 8u * wg, lo);
+                tc_fence_after_sync();
+                tmem_st16(lanes + K::kColP + 32u * now, hi);
+                tmem_st16(lanes + K::kColP + 32u * now + 16u, lo);
                 tmem_st_wait();
+                if (cleaned)
+                    fence_proxy_async_smem();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&bar[K::kBPFull + now]);
             }
-            if (cleaned)
-                fence_proxy_async_smem();
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&bar[K::kBPFull]);
             if (++vs == K::kStages)
                 vs = 0;
             if (++e == K::kTiles) {
@@ -349,14 +393,21 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
                 continue;
 
             // ------------------------------------------------ end of a block
-            ok = ok && mbar_wait(&bar[K::kBPEmpty], ph, abort_flag);
-            ok = __all_sync(kFull, ok);
-            red[wg * K::kRows + row] = l0 + l1;
+            // (the update before the last one first: a parity says nothing of the phase before
+            // its own, which this group may not have waited for)
+            const bool ok = __all_sync(kFull, (it == 0 || mbar_wait(&bar[K::kBPEmpty + was], wph, abort_flag)) &&
+                                                  mbar_wait(&bar[K::kBPEmpty + now], ph, abort_flag));
             if (!named_bar_and(1, 256, ok)) {
                 fail(a, abort_flag);
                 break;
             }
             tc_fence_after_sync();
+            {
+                const float m = shared_m[row];
+                red[wg * K::kRows + row] = l * ex2_approx(m - mneg);
+                mneg = m;
+            }
+            named_bar_sync(1, 256);
             const float L = red[row] + red[K::kRows + row];
             const Piece *const piece = reinterpret_cast<const Piece *>(smem + K::kOffPiece) + seg % K::kPieces;
             const bool sole = piece->sole != 0;
@@ -428,103 +479,92 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == K::kPlanWarp) {
             plan_tiles<K>(a, smem, bar, range, g, 0, vh == 0, abort_flag);
-        } else if (warp == K::kMmaWarp) {
+        } else if (warp == K::kMmaWarp || warp == K::kOutWarp) {
             // -------------------------------------------------------- products
-            // The scores of tile nq as soon as its rows are there and the scores before
-            // were read, the output update of tile np as soon as its weights are there;
-            // one elected lane of the converged warp issues.
+            // One warp for the scores, one for the output updates: between two issues a
+            // warp takes 500 to 650 cycles over its waits and its instructions' way past
+            // the softmax's, and one warp's is the other's tensor time (one warp for both:
+            // 1830 cycles a tile). One elected lane of the converged warp issues; the
+            // scores' loop is rolled for the instruction caches' sake.
+            const bool out = warp == K::kOutWarp;
             const Tile *const tiles = reinterpret_cast<const Tile *>(smem + K::kOffInfo);
-            int nq = 0, np = 0, seg = 0, idle = 0;
-            bool more_q = true, more_p = true, ok = true;
-            int qv = 0, pv = 0, qe = 0, pe = 0;  // slots and descriptions of tiles nq and np
-            uint32_t qvph = 0, qeph = 0;
-            uint64_t idle_since = 0;
-            const uint64_t kd = sw128_kmajor_desc_sbo(sbase, kVGroup), vd = sw128_mnmajor_desc(sbase, 1024u, kVGroup);
-            const uint64_t rd = sw64_kmajor_desc(sbase, kRGroup);
-            while (more_p) {
-                bool prog = false;
-                if (np < nq && __all_sync(kFull, mbar_test(&bar[K::kBPFull], (uint32_t)np & 1u))) {
-                    const uint32_t flags = tiles[pe].flags;
-                    const bool first = flags & kFirst;
+            int seg = 0, vs = 0, e = 0;
+            uint32_t vph = 0, eph = 0;
+            bool ok = true;
+            auto wait = [&](int barrier, uint32_t parity) {
+                ok = ok && __all_sync(kFull, wait_for(&bar[barrier], parity, abort_flag));
+                return ok;
+            };
+            const uint64_t kd = sw128_kmajor_desc_sbo(sbase + K::kOffV, kVGroup);
+            const uint64_t vd = sw128_mnmajor_desc(sbase + K::kOffV + (uint32_t)vh * 2048u, 1024u, kVGroup);
+            const uint64_t rd = sw64_kmajor_desc(sbase + K::kOffR, kRGroup), qrd = sw64_kmajor_desc(sbase + K::kOffQR, kRGroup);
+            for (int it = 0;; ++it) {
+                const uint32_t now = (uint32_t)it & 1u;
+                if (!wait(K::kBInfo + e, eph))
+                    break;
+                const uint32_t flags = tiles[e].flags;
+                if (!out) {
+                    if (!wait(K::kBReady + vs, vph) || ((flags & kFirst) && !wait(K::kBQFull, (uint32_t)seg & 1u)) ||
+                        !wait(K::kBSFree, now ^ 1u))
+                        break;
+                    if (flags & kFirst)
+                        ++seg;
+                    fence_proxy_async_smem();  // cp.async writes -> tensor-core reads
                     tc_fence_after_sync();
-                    const uint64_t bv = vd + ((K::kOffV + (uint32_t)pv * K::kVBytes + (uint32_t)vh * 2048u) >> 4);
+                    const uint64_t bk = kd + (((uint32_t)vs * K::kVBytes) >> 4), br = rd + (((uint32_t)vs * K::kRBytes) >> 4);
+                    if (elect_one()) {
+#pragma unroll 1
+                        for (int kb = 0; kb < 4; ++kb)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                umma_f8_ts(tmem + K::kColS, tmem + K::kColQ + 32u * kb + 8u * k, bk + 64u * kb + 2u * k, K::kIdescQK,
+                                           (kb | k) ? 1u : 0u);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            umma_e4m3(tmem + K::kColS, qrd + 2u * k, br + 2u * k, K::kIdescQK, 1u);
+                        umma_commit(&bar[K::kBSFull + now]);
+                    }
+                } else {
+                    // behind the scores of two tiles on, so that these are worked on while S
+                    // waits to be read; a piece's last two tiles do not wait
+                    if (!wait(K::kBPFull + now, (uint32_t)(it >> 1) & 1u) ||
+                        ((flags & kSteady) && !wait(K::kBTurn + now, ((uint32_t)(it >> 1) & 1u) ^ 1u)))
+                        break;
+                    fence_proxy_async_smem();  // cp.async writes -> tensor-core reads
+                    tc_fence_after_sync();
+                    const uint64_t bv = vd + (((uint32_t)vs * K::kVBytes) >> 4);
+                    const uint32_t ap = tmem + K::kColP + 32u * now;
                     if (elect_one()) {
 #pragma unroll
                         for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
                             for (int term = 0; term < 2; ++term)
-                                umma_f8_ts(tmem + K::kColO, tmem + K::kColP + 16u * term + 8u * ks,
-                                           bv + (((uint32_t)ks * 4u * kVGroup) >> 4), term ? K::kIdescPVLo : K::kIdescPV,
-                                           (first && ks == 0 && term == 0) ? 0u : 1u);
-                        umma_commit(&bar[K::kBVEmpty + pv]);
-                        umma_commit(&bar[K::kBPEmpty]);
-                    }
-                    __syncwarp();
-                    if (++pv == K::kStages)
-                        pv = 0;
-                    if (++pe == K::kTiles)
-                        pe = 0;
-                    ++np;
-                    more_p = !(flags & kEnd);
-                    prog = true;
-                }
-                if (more_q && __all_sync(kFull, mbar_test(&bar[K::kBInfo + qe], qeph) && mbar_test(&bar[K::kBReady + qv], qvph) &&
-                                                    mbar_test(&bar[K::kBSFree], ((uint32_t)nq & 1u) ^ 1u))) {
-                    const uint32_t flags = tiles[qe].flags;
-                    if (!(flags & kFirst) || __all_sync(kFull, mbar_test(&bar[K::kBQFull], (uint32_t)seg & 1u))) {
-                        if (flags & kFirst)
-                            ++seg;
-                        fence_proxy_async_smem();  // cp.async writes -> tensor-core reads
-                        tc_fence_after_sync();
-                        const uint64_t bk = kd + ((K::kOffV + (uint32_t)qv * K::kVBytes) >> 4);
-                        const uint64_t br = rd + ((K::kOffR + (uint32_t)qv * K::kRBytes) >> 4);
-                        if (elect_one()) {
-#pragma unroll
-                            for (int k = 0; k < 16; ++k)
-                                umma_f8_ts(tmem + K::kColS, tmem + K::kColQ + 8u * k,
-                                           bk + (((uint32_t)(k >> 2) * 1024u + (uint32_t)(k & 3) * 32u) >> 4), K::kIdescQK,
-                                           k ? 1u : 0u);
-#pragma unroll
-                            for (int k = 0; k < 2; ++k)
-                                umma_f8_ts(tmem + K::kColS, tmem + K::kColQ + 128u + 8u * k, br + 2u * k, K::kIdescQK, 1u);
-                            umma_commit(&bar[K::kBSFull]);
-                        }
-                        __syncwarp();
-                        if (++qv == K::kStages) {
-                            qv = 0;
-                            qvph ^= 1u;
-                        }
-                        if (++qe == K::kTiles) {
-                            qe = 0;
-                            qeph ^= 1u;
-                        }
-                        ++nq;
-                        more_q = !(flags & kEnd);
-                        prog = true;
+                                umma_f8_ts(tmem + K::kColO, ap + 16u * term + 8u * ks, bv + (((uint32_t)ks * 4u * kVGroup) >> 4),
+                                           term ? K::kIdescPVLo : K::kIdescPV, ((flags & kFirst) && ks == 0 && term == 0) ? 0u : 1u);
+                        umma_commit(&bar[K::kBVEmpty + vs]);
+                        umma_commit(&bar[K::kBPEmpty + now]);
                     }
                 }
-                if (prog) {
-                    idle = 0;
-                    idle_since = 0;
-                    continue;
-                }
-                // nothing ready: every 64 polls the abort flag and the clock
-                if (++idle < 64)
-                    continue;
-                idle = 0;
-                const uint64_t now = __shfl_sync(kFull, global_timer_ns(), 0);
-                if (idle_since == 0) {
-                    idle_since = now;
-                } else if (__any_sync(kFull, *abort_flag != 0) || now - idle_since > kWaitLimitNs) {
-                    ok = false;
+                __syncwarp();
+                if (!out && lane == 0)
+                    mbar_arrive(&bar[K::kBTurn + now]);
+                if (flags & kEnd)
                     break;
+                if (++vs == K::kStages) {
+                    vs = 0;
+                    vph ^= 1u;
+                }
+                if (++e == K::kTiles) {
+                    e = 0;
+                    eph ^= 1u;
                 }
             }
             if (!ok)
                 fail(a, abort_flag);
             if (elect_one()) {
-                umma_commit(&bar[K::kBDrain]);
-                if (!mbar_wait(&bar[K::kBDrain], 0u, nullptr))
+                uint64_t *const drain = &bar[K::kBDrain + (out ? 1 : 0)];
+                umma_commit(drain);
+                if (!mbar_wait(drain, 0u, nullptr))
                     atomicOr(a.c.status, (uint32_t)PMQA_DEV_TIMEOUT);
             }
         }
