@@ -55,11 +55,11 @@ __device__ __forceinline__ float half_max(uint32_t mask, float x)
 // The largest finite |y| of the half warp's 128 values, at least 2^-100.
 __device__ __forceinline__ float largest(uint32_t mask, const float (&y)[8])
 {
-    float top = kLeast;
+    float top = fmaxf(kLeast, fabsf(y[0]));
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        top = fmaxf(top, fabsf(y[e]));
-    top = half_max(mask, top);
+    for (int e = 1; e < 7; e += 2)
+        top = fmaxf(top, fmaxf(fabsf(y[e]), fabsf(y[e + 1])));
+    top = half_max(mask, fmaxf(top, fabsf(y[7])));
     if (top == INFINITY) {
         top = kLeast;
 #pragma unroll
@@ -70,10 +70,73 @@ __device__ __forceinline__ float largest(uint32_t mask, const float (&y)[8])
     return top;
 }
 
-template <int ROWS>
+// The rotation of a half warp's vector, whose packed inputs are u.
+template <bool PAIRS>
+__device__ __forceinline__ void rotate_packed(const Rotary &r, const Turn &turn, uint32_t mask, const uint4 &u, float (&y)[8])
+{
+    float other[8];
+    if (!PAIRS && r.dim) {
+        const int from = ((threadIdx.x & 31) + turn.partner) & 31;
+        const uint4 p = make_uint4(__shfl_sync(mask, u.x, from), __shfl_sync(mask, u.y, from),
+                                   __shfl_sync(mask, u.z, from), __shfl_sync(mask, u.w, from));
+        unpack8(p, other);
+    }
+    turn.apply(PAIRS, y, other);
+}
+
+template <bool PAIRS>
+__device__ __forceinline__ void write_index_key(const IndexArgs &a, const Turn &turn, uint32_t mask, long long r, uint32_t dst)
+{
+    const int lane = threadIdx.x & 31, at = lane & 15;
+    const uint4 u = load_once(a.k + r * a.k_row + 8 * at);
+    float y[8], other[8];
+    unpack8(u, y);
+    if (a.n.kind != PMQA_NORM_NONE) {
+        if (a.n.kind == PMQA_NORM_LAYER) {
+            float s = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                s += y[e];
+            const float mean = half_sum(mask, s) * (1.0f / kDimI);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                y[e] -= mean;
+        }
+        float s = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            s += y[e] * y[e];
+        const float f = rsqrtf(half_sum(mask, s) * (1.0f / kDimI) + a.n.eps);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            y[e] = y[e] * f * (a.n.weight ? __ldg(a.n.weight + 8 * at + e) : 1.0f) +
+                   (a.n.bias ? __ldg(a.n.bias + 8 * at + e) : 0.0f);
+        if (!PAIRS && a.r.dim) {
+            const int from = (lane + turn.partner) & 31;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                other[e] = __shfl_sync(mask, y[e], from);
+        }
+        turn.apply(PAIRS, y, other);
+    } else {
+        rotate_packed<PAIRS>(a.r, turn, mask, u, y);
+    }
+    const float top = largest(mask, y);
+    const uint2 code = codes8(y, __fdividef(448.0f, top));
+    if (dst == kNoRow)
+        return;
+    uint32_t *const p = reinterpret_cast<uint32_t *>(a.kv + (unsigned long long)dst * kRowI);
+    p[2 * at] = code.x;
+    p[2 * at + 1] = code.y;
+    if (at == 0)
+        p[kDimI / 4] = __float_as_uint(top / 448.0f);
+}
+
+template <int ROWS, bool PAIRS>
 __global__ void __launch_bounds__(kIndexThreads) index_append_kernel(const __grid_constant__ IndexArgs a)
 {
     __shared__ RowTable<ROWS, kDimI> t;
+    constexpr int kHalves = kIndexThreads / 16, AHEAD = 4;  // vectors whose loads are in flight
     const int tid = threadIdx.x, lane = tid & 31, at = lane & 15;
     const uint32_t mask = 0xFFFFu << (lane & 16);
     const int row0 = blockIdx.x * ROWS;
@@ -81,97 +144,50 @@ __global__ void __launch_bounds__(kIndexThreads) index_append_kernel(const __gri
         cache::report_requests(a.c);
     load_turns(t, a.r);
     load_rows(t, a.c, a.r, row0, a.k != nullptr);
-
-    // vectors of a row: its heads, then its key
-    const int heads = a.heads, all = heads + (a.k ? 1 : 0);
-    const int total = ROWS * all, step = kIndexThreads / 16 * gridDim.y;
-    constexpr int AHEAD = 4;
-    int row_now = -1;
     Turn turn;
-    for (int v0 = (int)blockIdx.y * (kIndexThreads / 16) + (tid >> 4); v0 < total; v0 += AHEAD * step) {
-        uint4 u[AHEAD];
-        int row[AHEAD], h[AHEAD];
+#pragma unroll 1
+    for (int row = 0; row < ROWS; ++row) {
+        if (!t.place[row].valid)
+            continue;
+        const long long r = row0 + row;
+        turn.load(a.r, t.cs[row], at);
+        const int step = kHalves * gridDim.y;
+        const uint16_t *const q = a.q + r * a.q_row + 8 * at;
+        uint8_t *const out = a.q_out + (r * a.heads) * kDimI + 8 * at;
+        for (int h0 = (int)blockIdx.y * kHalves + (tid >> 4); h0 < a.heads; h0 += AHEAD * step) {
+            uint4 u[AHEAD];
+            float w[AHEAD];
 #pragma unroll
-        for (int k = 0; k < AHEAD; ++k) {
-            const int v = v0 + k * step;
-            row[k] = ROWS == 1 ? 0 : v / all;
-            h[k] = v - row[k] * all;
-            const bool key = h[k] == heads;
-            u[k] = make_uint4(0, 0, 0, 0);
-            if (v >= total || !t.place[row[k]].valid) {
-                row[k] = -1;
-                continue;
+            for (int k = 0; k < AHEAD; ++k) {
+                const int h = h0 + k * step;
+                if (h < a.heads) {
+                    u[k] = load_once(q + h * a.q_head);
+                    if (at == 0) {
+                        const long long iw = r * a.w_row + h;
+                        w[k] = a.w_bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t *>(a.w)[iw] << 16)
+                                        : static_cast<const float *>(a.w)[iw];
+                    }
+                }
             }
-            const long long r = row0 + row[k];
-            u[k] = load_once((key ? a.k + r * a.k_row : a.q + r * a.q_row + h[k] * a.q_head) + 8 * at);
-        }
 #pragma unroll
-        for (int k = 0; k < AHEAD; ++k) {
-            if (row[k] < 0)
-                continue;
-            const long long r = row0 + row[k];
-            const bool key = h[k] == heads;
-            if (row[k] != row_now) {
-                row_now = row[k];
-                turn.load(a.r, t.cs[row_now], at);
-            }
-            float y[8], other[8];
-            unpack8(u[k], y);
-            if (key && a.n.kind != PMQA_NORM_NONE) {
-                if (a.n.kind == PMQA_NORM_LAYER) {
-                    float s = 0.0f;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        s += y[e];
-                    const float mean = half_sum(mask, s) * (1.0f / kDimI);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        y[e] -= mean;
-                }
-                float s = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    s += y[e] * y[e];
-                const float f = rsqrtf(half_sum(mask, s) * (1.0f / kDimI) + a.n.eps);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    y[e] = y[e] * f * (a.n.weight ? __ldg(a.n.weight + 8 * at + e) : 1.0f) +
-                           (a.n.bias ? __ldg(a.n.bias + 8 * at + e) : 0.0f);
-                if (a.r.dim && !a.r.interleaved) {
-                    const int from = (lane + turn.partner) & 31;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        other[e] = __shfl_sync(mask, y[e], from);
-                }
-            } else if (a.r.dim && !a.r.interleaved) {
-                const int from = (lane + turn.partner) & 31;
-                const uint4 p = make_uint4(__shfl_sync(mask, u[k].x, from), __shfl_sync(mask, u[k].y, from),
-                                           __shfl_sync(mask, u[k].z, from), __shfl_sync(mask, u[k].w, from));
-                unpack8(p, other);
-            }
-            turn.apply(a.r.interleaved, y, other);
-            const float top = largest(mask, y);
-            const uint2 code = codes8(y, 448.0f / top);
-            if (key) {
-                const uint32_t dst = t.place[row[k]].row;
-                if (dst != kNoRow) {
-                    uint32_t *const p = reinterpret_cast<uint32_t *>(a.kv + (unsigned long long)dst * kRowI);
-                    p[2 * at] = code.x;
-                    p[2 * at + 1] = code.y;
-                    if (at == 0)
-                        p[kDimI / 4] = __float_as_uint(top / 448.0f);
-                }
-            } else {
-                const long long o = r * heads + h[k];
-                *reinterpret_cast<uint2 *>(a.q_out + o * kDimI + 8 * at) = code;
-                if (at == 0) {
-                    const long long iw = r * a.w_row + h[k];
-                    const float w = a.w_bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t *>(a.w)[iw] << 16)
-                                             : static_cast<const float *>(a.w)[iw];
-                    a.w_out[o] = w * (top / 448.0f) * a.w_scale;
-                }
+            for (int k = 0; k < AHEAD; ++k) {
+                const int h = h0 + k * step;
+                if (h >= a.heads)
+                    break;
+                float y[8];
+                unpack8(u[k], y);
+                rotate_packed<PAIRS>(a.r, turn, mask, u[k], y);
+                const float top = largest(mask, y);
+                *reinterpret_cast<uint2 *>(out + h * kDimI) = codes8(y, __fdividef(448.0f, top));
+                if (at == 0)
+                    a.w_out[r * a.heads + h] = w[k] * (top * (1.0f / 448.0f)) * a.w_scale;
             }
         }
+    }
+    // the keys: a half warp each, after the queries
+    if (a.k && blockIdx.y == gridDim.y - 1 && (tid >> 4) < ROWS && t.place[tid >> 4].valid) {
+        turn.load(a.r, t.cs[tid >> 4], at);
+        write_index_key<PAIRS>(a, turn, mask, row0 + (tid >> 4), t.place[tid >> 4].row);
     }
 }
 
@@ -289,11 +305,12 @@ extern "C" int pmqa_index_append(const pmqa_paged_rows *p, void *kv_cache, const
         return rc;
     const int rows = p->rows;
     const cudaStream_t st = cache::cuda(stream);
-    if (rows >= 16 * sms)
-        index_append_kernel<4><<<(rows + 3) / 4, kIndexThreads, 0, st>>>(a);
-    else
-        // few rows: a row's vectors over several CTAs, as many as there are SMs for
-        index_append_kernel<1><<<dim3(rows, std::max(1, std::min((a.heads + 16) / 16, sms / rows))), kIndexThreads, 0, st>>>(a);
+    // many rows: four to a CTA; few: a row's heads over several CTAs, as many as there are SMs for
+    const bool many = rows >= 16 * sms, pairs = a.r.interleaved != 0;
+    const dim3 grid = many ? dim3((unsigned)((rows + 3ll) / 4)) : dim3(rows, std::max(1, std::min((a.heads + 15) / 16, sms / rows)));
+    auto *const kernel = many ? (pairs ? index_append_kernel<4, true> : index_append_kernel<4, false>)
+                              : (pairs ? index_append_kernel<1, true> : index_append_kernel<1, false>);
+    kernel<<<grid, kIndexThreads, 0, st>>>(a);
     return cache::code_of(cudaGetLastError());
 }
 

@@ -23,6 +23,11 @@
 namespace pmqa {
 namespace latent {
 
+// The block of the scores' products behind which the output update may be issued: its
+// warp wakes and issues in 200 cycles, the last six products' time (none before: 261 us
+// for batch decode, after block 1 258, 2 253, 3 253).
+constexpr int kTurnAt = 2;
+
 struct Wide {
     static constexpr int kTile = 64;                      // tokens per tile
     static constexpr int kStages = 5;                     // slots of a tile's rows
@@ -36,8 +41,7 @@ struct Wide {
     static constexpr uint32_t kOffV = 0;
     static constexpr uint32_t kOffR = kOffV + kStages * kVBytes;
     static constexpr uint32_t kOffQR = kOffR + kStages * kRBytes;       // the queries' rotary part
-    static constexpr uint32_t kOffOut = kOffQR + kRows / 8 * kRGroup;   // 1 KB for each softmax warp's output
-    static constexpr uint32_t kOffRows = kOffOut + 8 * 1024;            // [kAhead][64]
+    static constexpr uint32_t kOffRows = kOffQR + kRows / 8 * kRGroup;  // [kAhead][64]
     static constexpr uint32_t kOffInfo = kOffRows + kAhead * kTile * 4; // [kTiles] Tile
     static constexpr uint32_t kOffPiece = kOffInfo + kTiles * 32;       // [kPieces] Piece
     static constexpr uint32_t kOffRange = kOffPiece + kPieces * 32;     // Range
@@ -77,6 +81,23 @@ __device__ __forceinline__ void umma_f8_ts(uint32_t tmem_d, uint32_t tmem_a, uin
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
         "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+// Two 16-byte neighbours u, v of this lane's row (row `lane` from p on, `stride`
+// elements apart) to memory, 32 bytes of a row at a time: neighbouring lanes trade, so
+// that each store of the pair goes to one row.
+template <typename T>
+__device__ __forceinline__ void store_pair(T *p, int stride, int rows, const uint4 &u, const uint4 &v)
+{
+    const int lane = threadIdx.x & 31, odd = lane & 1;
+    const uint4 send = odd ? u : v;
+    const uint4 got = make_uint4(__shfl_xor_sync(kFull, send.x, 1), __shfl_xor_sync(kFull, send.y, 1),
+                                 __shfl_xor_sync(kFull, send.z, 1), __shfl_xor_sync(kFull, send.w, 1));
+    T *const at = p + (long long)(lane & ~1) * stride + odd * (int)(16 / sizeof(T));
+    if ((lane & ~1) < rows)
+        __stcg(reinterpret_cast<uint4 *>(at), odd ? got : u);
+    if ((lane | 1) < rows)
+        __stcg(reinterpret_cast<uint4 *>(at + stride), odd ? v : got);
 }
 
 __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __grid_constant__ Args a)
@@ -196,7 +217,6 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
         const uint32_t lanes = tmem + ((uint32_t)(w4 * 32) << 16);
         float *const red = reinterpret_cast<float *>(smem + K::kOffRed);  // [2][128]
         float *const shared_m = reinterpret_cast<float *>(smem + K::kOffM);  // [128]: -m
-        const uint32_t turn = sbase + K::kOffOut + (uint32_t)(warp - 4) * 1024u;
         float l = 0.0f, mneg = kUnseen;
         int seg = -1, vs = 0, e = 0, lim = 0;
         uint32_t eph = 0;
@@ -431,10 +451,6 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
                 tmem_ld32(lanes + K::kColO + 128u * wg + 32u * k, o);
                 tmem_ld_wait();
                 reg_fence_cols<32>(o);
-                // turned in the warp's kilobyte, so that rows are stored 32 bytes at a time
-                const uint32_t mine = turn + 32u * lane, flip = (uint32_t)(lane >> 2) & 1u;
-                const int r0 = lane >> 1, half = lane & 1;
-                const uint32_t other = turn + 32u * r0 + 16u * ((uint32_t)half ^ ((uint32_t)(r0 >> 2) & 1u));
                 if (sole) {
 #pragma unroll
                     for (int z = 0; z < 32; z += 16) {
@@ -446,29 +462,14 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
                             b[y] = __bfloat16_as_ushort(__float2bfloat16_rn(y0)) |
                                    (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(y1)) << 16;
                         }
-                        sts128(mine + 16u * flip, b[0], b[1], b[2], b[3]);
-                        sts128(mine + 16u * (flip ^ 1u), b[4], b[5], b[6], b[7]);
-                        __syncwarp();
-                        const uint4 v0 = lds128(other), v1 = lds128(other + 512u);
-                        if (r0 < rows)
-                            *reinterpret_cast<uint4 *>(out + r0 * kVDim + 32 * k + z + 8 * half) = v0;
-                        if (r0 + 16 < rows)
-                            *reinterpret_cast<uint4 *>(out + (r0 + 16) * kVDim + 32 * k + z + 8 * half) = v1;
-                        __syncwarp();
+                        store_pair(out + 32 * k + z, kVDim, rows, make_uint4(b[0], b[1], b[2], b[3]),
+                                   make_uint4(b[4], b[5], b[6], b[7]));
                     }
                 } else {
 #pragma unroll
-                    for (int z = 0; z < 32; z += 8) {
-                        sts128(mine + 16u * flip, o[z], o[z + 1], o[z + 2], o[z + 3]);
-                        sts128(mine + 16u * (flip ^ 1u), o[z + 4], o[z + 5], o[z + 6], o[z + 7]);
-                        __syncwarp();
-                        const uint4 v0 = lds128(other), v1 = lds128(other + 512u);
-                        if (r0 < rows)
-                            __stcg(reinterpret_cast<uint4 *>(part + r0 * kVDim + 32 * k + z + 4 * half), v0);
-                        if (r0 + 16 < rows)
-                            __stcg(reinterpret_cast<uint4 *>(part + (r0 + 16) * kVDim + 32 * k + z + 4 * half), v1);
-                        __syncwarp();
-                    }
+                    for (int z = 0; z < 32; z += 8)
+                        store_pair(part + 32 * k + z, kVDim, rows, make_uint4(o[z], o[z + 1], o[z + 2], o[z + 3]),
+                                   make_uint4(o[z + 4], o[z + 5], o[z + 6], o[z + 7]));
                 }
             }
             tc_fence_before_sync();
@@ -514,11 +515,14 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
                     const uint64_t bk = kd + (((uint32_t)vs * K::kVBytes) >> 4), br = rd + (((uint32_t)vs * K::kRBytes) >> 4);
                     if (elect_one()) {
 #pragma unroll 1
-                        for (int kb = 0; kb < 4; ++kb)
+                        for (int kb = 0; kb < 4; ++kb) {
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 umma_f8_ts(tmem + K::kColS, tmem + K::kColQ + 32u * kb + 8u * k, bk + 64u * kb + 2u * k, K::kIdescQK,
                                            (kb | k) ? 1u : 0u);
+                            if (kb == kTurnAt)
+                                mbar_arrive(&bar[K::kBTurn + now]);
+                        }
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
                             umma_e4m3(tmem + K::kColS, qrd + 2u * k, br + 2u * k, K::kIdescQK, 1u);
@@ -546,8 +550,6 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
                     }
                 }
                 __syncwarp();
-                if (!out && lane == 0)
-                    mbar_arrive(&bar[K::kBTurn + now]);
                 if (flags & kEnd)
                     break;
                 if (++vs == K::kStages) {

@@ -178,8 +178,11 @@ __device__ __forceinline__ uint4 load_once(const void *p)
 // 8 values times f as e4m3 codes
 __device__ __forceinline__ uint2 codes8(const float (&y)[8], float f)
 {
-    return make_uint2(cache::f32x4_to_e4m3x4(y[0] * f, y[1] * f, y[2] * f, y[3] * f),
-                      cache::f32x4_to_e4m3x4(y[4] * f, y[5] * f, y[6] * f, y[7] * f));
+    float z[8];
+#pragma unroll
+    for (int e = 0; e < 8; e += 2)
+        fmul2(z[e], z[e + 1], y[e], y[e + 1], f, f);
+    return make_uint2(cache::f32x4_to_e4m3x4(z[0], z[1], z[2], z[3]), cache::f32x4_to_e4m3x4(z[4], z[5], z[6], z[7]));
 }
 
 // A lane's share of the rotation: eight values of a head whose rotated part it may
