@@ -19,7 +19,7 @@ namespace paged {
 
 constexpr int kDimI = 128;       // values of a key or of a query head
 constexpr int kRowI = 132;       // bytes of a cached row
-constexpr int kIndexThreads = 256;
+constexpr int kIndexThreads = 128;
 constexpr float kLeast = 0x1p-100f;
 
 struct IndexArgs {
@@ -88,7 +88,7 @@ template <bool PAIRS>
 __device__ __forceinline__ void write_index_key(const IndexArgs &a, const Turn &turn, uint32_t mask, long long r, uint32_t dst)
 {
     const int lane = threadIdx.x & 31, at = lane & 15;
-    const uint4 u = load_once(a.k + r * a.k_row + 8 * at);
+    const uint4 u = load_input(a.k + r * a.k_row + 8 * at);
     float y[8], other[8];
     unpack8(u, y);
     if (a.n.kind != PMQA_NORM_NONE) {
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kIndexThreads) index_append_kernel(const __gri
             for (int k = 0; k < AHEAD; ++k) {
                 const int h = h0 + k * step;
                 if (h < a.heads) {
-                    u[k] = load_once(q + h * a.q_head);
+                    u[k] = load_input(q + h * a.q_head);
                     if (at == 0) {
                         const long long iw = r * a.w_row + h;
                         w[k] = a.w_bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t *>(a.w)[iw] << 16)
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(128) index_read_kernel(const __grid_constant__
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) {
             const uint32_t row = __shfl_sync(kFull, src, k0 + k);
-            w[k] = row == kNoRow ? 0u : __ldcs(pool + (unsigned long long)row * (kRowI / 4) + lane);
+            w[k] = row == kNoRow ? 0u : __ldg(pool + (unsigned long long)row * (kRowI / 4) + lane);
         }
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k)
@@ -268,7 +268,7 @@ extern "C" int pmqa_index_append(const pmqa_paged_rows *p, void *kv_cache, const
         return x ? rc : PMQA_ERR_INVALID_ARG;
     if (x->q && (x->heads < 1 || !std::isfinite(x->weight_scale) || (x->weights_row < 0 && p->rows > 1)))
         return PMQA_ERR_INVALID_ARG;
-    if (x->q && (long long)x->heads * p->rows > 0x7FFFFFFFll)
+    if (x->q && (x->heads > kMaxHeads || (long long)x->heads * p->rows > 0x7FFFFFFFll))
         return PMQA_ERR_UNSUPPORTED;
     if (p->bs == 0 || p->rows == 0 || (!x->k && !x->q))
         return PMQA_OK;

@@ -19,7 +19,7 @@ using mla::kDim;
 using mla::kVDim;
 
 constexpr int kPe = kDim - kVDim;
-constexpr int kLatentThreads = 256;
+constexpr int kLatentThreads = 128;
 
 struct LatentArgs {
     View c;
@@ -60,8 +60,8 @@ __device__ __forceinline__ void write_key(const LatentArgs &a, const Turn &turn,
 {
     const int lane = threadIdx.x & 31;
     const uint16_t *const src = a.k_c + r * a.c_row + 8 * lane;
-    const uint4 u0 = load_once(src), u1 = load_once(src + 256);
-    const uint4 up = lane < 8 ? load_once(a.k_pe + r * a.pe_row + 8 * lane) : make_uint4(0, 0, 0, 0);
+    const uint4 u0 = load_input(src), u1 = load_input(src + 256);
+    const uint4 up = lane < 8 ? load_input(a.k_pe + r * a.pe_row + 8 * lane) : make_uint4(0, 0, 0, 0);
     float y[2][8], pe[8];
     unpack8(u0, y[0]);
     unpack8(u1, y[1]);
@@ -106,11 +106,11 @@ __device__ __forceinline__ void write_queries(const LatentArgs &a, const Turn &t
     uint8_t *const out = a.q_out + (r * a.heads + h0) * kDim + 8 * lane;
     uint4 u[8], up = make_uint4(0, 0, 0, 0);
     if (lane >> 3 < n)
-        up = load_once(a.q_pe + r * a.q_pe_row + (h0 + (lane >> 3)) * a.q_pe_head + 8 * (lane & 7));
+        up = load_input(a.q_pe + r * a.q_pe_row + (h0 + (lane >> 3)) * a.q_pe_head + 8 * (lane & 7));
 #pragma unroll
     for (int k = 0; k < 8; ++k)
         if (k >> 1 < n)
-            u[k] = load_once(c + (k >> 1) * a.q_c_head + (k & 1) * 256);
+            u[k] = load_input(c + (k >> 1) * a.q_c_head + (k & 1) * 256);
     float y[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k)
@@ -130,14 +130,14 @@ __global__ void __launch_bounds__(kLatentThreads) latent_append_kernel(const __g
     __shared__ RowTable<ROWS, kPe> t;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int row0 = blockIdx.x * ROWS;
-    if (blockIdx.x == 0)
+    if (blockIdx.x == 0 && blockIdx.y == 0)
         cache::report_requests(a.c);
     load_turns(t, a.r);
     load_rows(t, a.c, a.r, row0, a.k_c != nullptr);
     const int groups = (a.heads + 3) / 4, all = groups + (a.k_c ? 1 : 0);
     int row_now = -1;
     Turn turn;
-    for (int v = warp; v < ROWS * all; v += kLatentThreads / 32) {
+    for (int v = (int)blockIdx.y * (kLatentThreads / 32) + warp; v < ROWS * all; v += (int)gridDim.y * (kLatentThreads / 32)) {
         const int row = ROWS == 1 ? 0 : v / all, g = v - row * all;
         if (!t.place[row].valid)
             continue;
@@ -173,7 +173,7 @@ extern "C" int pmqa_latent_append(const pmqa_paged_rows *p, void *kv_cache, cons
     if ((x->c && !(std::isfinite(x->kv_scale) && std::isfinite(a.kv_inv))) ||
         (x->q_c && (x->heads < 1 || !(std::isfinite(x->q_scale) && std::isfinite(a.q_inv)))))
         return PMQA_ERR_INVALID_ARG;
-    if (x->q_c && (long long)x->heads * p->rows > 0x7FFFFFFFll)
+    if (x->q_c && (x->heads > kMaxHeads || (long long)x->heads * p->rows > 0x7FFFFFFFll))
         return PMQA_ERR_UNSUPPORTED;
     if (p->bs == 0 || p->rows == 0 || (!x->c && !x->q_c))
         return PMQA_OK;
@@ -203,8 +203,8 @@ extern "C" int pmqa_latent_append(const pmqa_paged_rows *p, void *kv_cache, cons
     const int rows = p->rows;
     const cudaStream_t st = cache::cuda(stream);
     if (rows >= 16 * sms)
-        latent_append_kernel<4><<<(rows + 3) / 4, kLatentThreads, 0, st>>>(a);
-    else
-        latent_append_kernel<1><<<rows, kLatentThreads, 0, st>>>(a);
+        latent_append_kernel<4><<<(unsigned)((rows + 3ll) / 4), kLatentThreads, 0, st>>>(a);
+    else  // few rows: a row's heads over several CTAs, as many as there are SMs for
+        latent_append_kernel<1><<<dim3(rows, std::max(1, std::min((a.heads + 15) / 16, sms / rows))), kLatentThreads, 0, st>>>(a);
     return cache::code_of(cudaGetLastError());
 }

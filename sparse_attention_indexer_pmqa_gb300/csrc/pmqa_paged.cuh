@@ -54,6 +54,7 @@ inline View view(const pmqa_paged_rows *p, void *ws)
 }
 
 constexpr int kMaxRotary = 1024;  // rotated values of a head at most
+constexpr int kMaxHeads = 65535;  // query heads of a row: a row's values are counted in 32 bits
 
 struct Rotary {
     const double *inv_freq;
@@ -169,10 +170,12 @@ __device__ __forceinline__ void unpack8(const uint4 &u, float (&f)[8])
     }
 }
 
-// 16 bytes that are read once
-__device__ __forceinline__ uint4 load_once(const void *p)
+// 16 bytes of an input that no output overlaps: loads stay in flight over the stores
+// between them (through plain loads, which do not, 15.7 k rows of 64 index heads take 117 us
+// instead of 93).
+__device__ __forceinline__ uint4 load_input(const void *p)
 {
-    return __ldcs(reinterpret_cast<const uint4 *>(p));
+    return __ldg(reinterpret_cast<const uint4 *>(p));
 }
 
 // 8 values times f as e4m3 codes

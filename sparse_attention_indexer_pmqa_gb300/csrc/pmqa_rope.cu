@@ -14,6 +14,7 @@ namespace pmqa {
 namespace paged {
 
 constexpr int kRopeThreads = 256;
+constexpr long long kMaxAll = 1 << 24;  // heads of both tensors
 
 struct RopeArgs {
     Rotary r;
@@ -26,12 +27,18 @@ struct RopeArgs {
     int copies;   // bit t: the values outside tensor t's rotated part are copied
 };
 
-struct Pair16 {
-    uint4 a, b;
-};
+__device__ __forceinline__ uint4 pack8(const float (&f)[8])
+{
+    uint32_t o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        o[e] = __bfloat16_as_ushort(__float2bfloat16_rn(f[2 * e])) |
+               (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(f[2 * e + 1])) << 16;
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
 
-template <int ROWS>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a)
+template <int ROWS, bool PAIRS>
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_constant__ RopeArgs a)
 {
     extern __shared__ __align__(16) uint8_t smem[];
     const int half = a.r.dim / 2, tid = threadIdx.x;
@@ -66,68 +73,54 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
             cb[t] = (a.copies >> t & 1) && n + 1 < left ? 8 * (n + 1 < b8 ? n + 1 : n + 1 + a.r.dim / 8) : -1;
         }
     }
-    for (int row = 0; row < ROWS; ++row) {
-        const long long r = row0 + row;
-        if (r >= a.rows)
-            break;
-        float2 w[8];
-        if (it < turning) {
+    // heads of all rows of the CTA in one sequence, four loads in flight
+    constexpr int AHEAD = 4;
+    const int stride = step * gridDim.y, total = (int)min((long long)ROWS, a.rows - row0) * all;
+    for (int v0 = hv + step * blockIdx.y; v0 < total; v0 += AHEAD * stride) {
+        uint4 ua[AHEAD], ub[AHEAD];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                w[e] = cs[row * half + 8 * it + e];
+        for (int k = 0; k < AHEAD; ++k) {
+            const int v = v0 + k * stride;
+            if (v >= total)
+                continue;
+            const int row = ROWS == 1 ? 0 : v / all, h = v - row * all, t = h >= a.heads[0];
+            const uint16_t *const p = a.x[t] + (row0 + row) * a.x_row[t] + (long long)(h - (t ? a.heads[0] : 0)) * a.x_head[t];
+            const int ka = t ? ca[1] : ca[0], kb = t ? cb[1] : cb[0];
+            if (ka >= 0)
+                ua[k] = __ldcs(reinterpret_cast<const uint4 *>(p + ka));
+            if (kb >= 0)
+                ub[k] = __ldcs(reinterpret_cast<const uint4 *>(p + kb));
         }
-        constexpr int AHEAD = 4;  // heads whose loads are in flight
-        const int stride = step * gridDim.y;
-        for (int v0 = hv + step * blockIdx.y; v0 < all; v0 += AHEAD * stride) {
-            Pair16 u[AHEAD];
 #pragma unroll
-            for (int k = 0; k < AHEAD; ++k) {
-                const int v = v0 + k * stride, t = v >= a.heads[0];
-                if (v >= all)
-                    continue;
-                const uint16_t *const p = a.x[t] + r * a.x_row[t] + (long long)(v - (t ? a.heads[0] : 0)) * a.x_head[t];
-                const int ka = t ? ca[1] : ca[0], kb = t ? cb[1] : cb[0];
-                if (ka >= 0)
-                    u[k].a = load_once(p + ka);
-                if (kb >= 0)
-                    u[k].b = load_once(p + kb);
-            }
+        for (int k = 0; k < AHEAD; ++k) {
+            const int v = v0 + k * stride;
+            if (v >= total)
+                continue;
+            const int row = ROWS == 1 ? 0 : v / all, h = v - row * all, t = h >= a.heads[0];
+            if (it < turning) {
+                float x[8], y[8];
+                unpack8(ua[k], x);
+                unpack8(ub[k], y);
+                const float2 *const w = cs + row * half + 8 * it;
+                // pairs: (x[e], y[e]), or neighbours in x and then in y
 #pragma unroll
-            for (int k = 0; k < AHEAD; ++k) {
-                const int v = v0 + k * stride, t = v >= a.heads[0];
-                if (v >= all)
-                    continue;
-                if (it < turning) {
-                    float x[8], y[8];
-                    unpack8(u[k].a, x);
-                    unpack8(u[k].b, y);
-                    // pairs: (x[e], y[e]), or neighbours in x and then in y
-                    uint32_t o[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float &p0 = a.r.interleaved ? (e < 4 ? x[(2 * e) & 7] : y[(2 * e) & 7]) : x[e];
-                        float &p1 = a.r.interleaved ? (e < 4 ? x[(2 * e + 1) & 7] : y[(2 * e + 1) & 7]) : y[e];
-                        const float f = p0, g = p1;
-                        p0 = f * w[e].x - g * w[e].y;
-                        p1 = g * w[e].x + f * w[e].y;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        o[e] = __bfloat16_as_ushort(__float2bfloat16_rn(x[2 * e])) |
-                               (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(x[2 * e + 1])) << 16;
-                        o[4 + e] = __bfloat16_as_ushort(__float2bfloat16_rn(y[2 * e])) |
-                                   (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(y[2 * e + 1])) << 16;
-                    }
-                    u[k].a = make_uint4(o[0], o[1], o[2], o[3]);
-                    u[k].b = make_uint4(o[4], o[5], o[6], o[7]);
+                for (int e = 0; e < 8; ++e) {
+                    const float2 c = w[e];
+                    float &p0 = PAIRS ? (e < 4 ? x[(2 * e) & 7] : y[(2 * e) & 7]) : x[e];
+                    float &p1 = PAIRS ? (e < 4 ? x[(2 * e + 1) & 7] : y[(2 * e + 1) & 7]) : y[e];
+                    const float f = p0, g = p1;
+                    p0 = f * c.x - g * c.y;
+                    p1 = g * c.x + f * c.y;
                 }
-                uint16_t *const p = a.out[t] + r * a.out_row[t] + (long long)(v - (t ? a.heads[0] : 0)) * a.out_head[t];
-                const int ka = t ? ca[1] : ca[0], kb = t ? cb[1] : cb[0];
-                if (ka >= 0)
-                    *reinterpret_cast<uint4 *>(p + ka) = u[k].a;
-                if (kb >= 0)
-                    *reinterpret_cast<uint4 *>(p + kb) = u[k].b;
+                ua[k] = pack8(x);
+                ub[k] = pack8(y);
             }
+            uint16_t *const p = a.out[t] + (row0 + row) * a.out_row[t] + (long long)(h - (t ? a.heads[0] : 0)) * a.out_head[t];
+            const int ka = t ? ca[1] : ca[0], kb = t ? cb[1] : cb[0];
+            if (ka >= 0)
+                *reinterpret_cast<uint4 *>(p + ka) = ua[k];
+            if (kb >= 0)
+                *reinterpret_cast<uint4 *>(p + kb) = ub[k];
         }
     }
 }
@@ -201,7 +194,7 @@ extern "C" int pmqa_rope(const pmqa_rotary *rotary, int32_t rows, const pmqa_hea
         }
     }
     const long long all = (long long)k.heads[0] + k.heads[1];
-    if (all > 0x3FFFFFFFll)
+    if (all > kMaxAll)  // counted in 32 bits, over the rows of a CTA
         return PMQA_ERR_UNSUPPORTED;
     k.items = k.r.dim / 16 + (k.copies ? (widest - k.r.dim + 15) / 16 : 0);
     if (rows == 0 || all == 0 || k.items == 0)
@@ -217,10 +210,9 @@ extern "C" int pmqa_rope(const pmqa_rotary *rotary, int32_t rows, const pmqa_hea
     const unsigned split = (unsigned)std::max<long long>(1, std::min<long long>(passes, 2 * sms / rows));
     const dim3 grid((unsigned)((rows + (long long)per - 1) / per), split);
     const size_t smem = (size_t)k.r.dim / 2 * 8 * (1 + per);
-    if (per == 4)
-        rope_kernel<4><<<grid, kRopeThreads, smem, cache::cuda(stream)>>>(k);
-    else
-        rope_kernel<1><<<grid, kRopeThreads, smem, cache::cuda(stream)>>>(k);
+    auto *const kernel = per == 4 ? (k.r.interleaved ? rope_kernel<4, true> : rope_kernel<4, false>)
+                                  : (k.r.interleaved ? rope_kernel<1, true> : rope_kernel<1, false>);
+    kernel<<<grid, kRopeThreads, smem, cache::cuda(stream)>>>(k);
     return cache::code_of(cudaGetLastError());
 }
 

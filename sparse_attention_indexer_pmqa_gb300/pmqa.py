@@ -1028,6 +1028,8 @@ def pmqa_index_append(k, kv_cache, block_tables, context_lens, row_begin, max_ro
         heads = q.shape[1]
         shape, pair = (rows, heads, 128), (rows, heads)
         q_row, q_head, _ = _strided(q, dev, shape)
+        if weights is None:
+            raise AssertionError("expected weights beside q")
         w_row, w_step = weights.stride()
         if weights.shape != pair or weights.dtype not in (f32, bf16) or w_step != 1 and heads > 1 or \
                 weights.get_device() != dev:
@@ -1083,8 +1085,8 @@ def pmqa_latent_append(c, k_pe, kv_cache, block_tables, context_lens, row_begin,
     its queries (q_c bf16 [rows, heads, 512], q_pe bf16 [rows, heads, 64]) into q_out fp8
     [rows, heads, 576], which is returned where q_c is given."""
     _, _, _, _, _, codes, _, empty = _torch()
-    if c is None and q_c is None:
-        raise AssertionError("expected latent rows, queries or both")
+    if c is None and q_c is None or (c is None) != (k_pe is None) or (q_c is None) != (q_pe is None):
+        raise AssertionError("expected latent rows with their rotary part, queries with theirs, or both")
     rows, dev = (c if q_c is None else q_c).shape[0], kv_cache.get_device()
     p = make_paged_rows(kv_cache, 576, block_tables, context_lens, row_begin, rows, max_rows)
     c_addr, pe_addr, c_row, pe_row = None, None, 0, 0
