@@ -123,10 +123,14 @@ def attention(p, leave=None):
     pairs that no row attends to.
 
     A score's error: fp32 sums of 576 exact products, one unit of 2^-23 of their absolute
-    sum each, and its scaling. A weight as two e4m3 terms: the second holds the remainder, at
-    most 2^-4 of the weight, to 2^-4, or to 2^-10 where it is below 2^-6, in units in which the
-    row's largest weight is at least 2^4; through f16, 2^-11. exp2 and the sums in fp32: 2^-18.
-    The result is rounded to bf16."""
+    sum each, and its scaling. A weight, in a unit in which the row's largest is at least 1,
+    as an e4m3 term, off by 2^-4 of the weight, or by 2^-10 below 2^-6, and a term for that
+    remainder: e4m3 of 16 times it with up to 32 packed rows (query tokens x heads), off by 2^-4
+    of the remainder, 2^-8 of the weight, or by 2^-10 / 16 = 2^-14; e5m2 with more, off by 2^-3 of
+    it, 2^-7 of the weight or 2^-13 (a remainder of at most 2^-10). Through f16, 2^-11. exp2
+    and the sums in fp32: 2^-18. The result is rounded to bf16."""
+    few = min(p.max_rows, p.total) * p.heads <= 32
+    part, floor = (2.0 ** -8, 2.0 ** -14) if few else (2.0 ** -7, 2.0 ** -13)
     out = torch.full((p.total, p.heads, VALUES), math.nan, dtype=torch.float64)
     lse = torch.full((p.total, p.heads), math.nan, dtype=torch.float64)
     tol, ltol = torch.zeros_like(out), torch.zeros_like(lse)
@@ -154,9 +158,9 @@ def attention(p, leave=None):
         v0 = torch.where(v.isnan(), torch.zeros_like(v), v)
         o = (w.reshape(n * p.heads, c) @ v0).reshape(n, p.heads, VALUES)
         dtop = d.amax(-1, keepdim=True) if c else torch.zeros((n, p.heads, 1), dtype=torch.float64)
-        e = w * (2.0 ** -8 + 2.0 ** -11 + d + dtop)
+        e = w * (part + 2.0 ** -11 + d + dtop)
         if c:
-            e = e + torch.where(seen[:, None], w.amax(-1, keepdim=True) * 2.0 ** -14, torch.zeros_like(w))
+            e = e + torch.where(seen[:, None], w.amax(-1, keepdim=True) * floor, torch.zeros_like(w))
         e = (e.nan_to_num(0.0).reshape(n * p.heads, c) @ v0.abs()).reshape(n, p.heads, VALUES)
         none = ~seen.any(-1)
         o[none], l[none] = 0.0, -math.inf
