@@ -204,7 +204,7 @@ extern "C" int pmqa_latent_append(const pmqa_paged_rows *p, void *kv_cache, cons
     const cudaStream_t st = cache::cuda(stream);
     if (rows >= 16 * sms)
         latent_append_kernel<4><<<(unsigned)((rows + 3ll) / 4), kLatentThreads, 0, st>>>(a);
-    else  // few rows: a row's heads over several CTAs, as many as there are SMs for
-        latent_append_kernel<1><<<dim3(rows, std::max(1, std::min((a.heads + 15) / 16, sms / rows))), kLatentThreads, 0, st>>>(a);
+    else  // few rows: a row's heads over several CTAs, up to 8 per SM
+        latent_append_kernel<1><<<dim3(rows, std::max(1, std::min((a.heads + 15) / 16, 8 * sms / rows))), kLatentThreads, 0, st>>>(a);
     return cache::code_of(cudaGetLastError());
 }

@@ -124,6 +124,22 @@ __device__ __forceinline__ int request_of(const View &c, int r)
     return lo;
 }
 
+// The same for a lane's own row r, from request i on, which begins at or before r: in steps
+// of 1, 2, 4 and so on, and back.
+__device__ __forceinline__ int request_from(const View &c, int i, long long r)
+{
+    const uint32_t bs = c.bs;
+    uint32_t at = i, d = 1;
+    while (at + d < bs && __ldg(c.row_begin + at + d) <= r) {
+        at += d;
+        d *= 2;
+    }
+    for (d /= 2; d > 0; d /= 2)
+        if (at + d < bs && __ldg(c.row_begin + at + d) <= r)
+            at += d;
+    return (int)at;
+}
+
 constexpr uint32_t kNoRow = 0xFFFFFFFFu;
 
 // The pool row of a slot; kNoRow (recorded) where it has none.
@@ -237,22 +253,23 @@ struct Turn {
     }
 };
 
-// Each row's place, found out by one warp a row: slot, pool row, whether it is a
-// row of a request at all, and its position.
+// A row's place: slot, pool row, whether it is a row of a request at all, and its
+// position.
 struct Place {
     uint32_t row;
     int position;
     int valid;
 };
 
-__device__ __forceinline__ Place place_of(const View &c, const Rotary &r, int row, bool keys)
+// i: a request that begins at or before the row
+__device__ __forceinline__ Place place_of(const View &c, const Rotary &r, int i, long long row, bool keys)
 {
     Place o{kNoRow, 0, 0};
     if (row >= c.rows)
         return o;
-    const int i = request_of(c, row);
+    i = request_from(c, i, row);
     const int b = __ldg(c.row_begin + i), e = __ldg(c.row_begin + i + 1);
-    const long long j = (long long)row - b;
+    const long long j = row - b;
     if (j < 0 || row >= e || j >= c.max_rows)
         return o;
     const long long slot = (long long)__ldg(c.ctx + i) - ((long long)e - b) + j;
@@ -284,13 +301,12 @@ __device__ __forceinline__ void load_turns(RowTable<ROWS, DIM> &t, const Rotary 
 template <int ROWS, int DIM>
 __device__ __forceinline__ void load_rows(RowTable<ROWS, DIM> &t, const View &c, const Rotary &r, int row0, bool keys)
 {
-    const int warp = threadIdx.x >> 5;
+    static_assert(ROWS <= 32, "a lane a row");
     __syncthreads();
-    for (int k = warp; k < ROWS; k += blockDim.x >> 5) {
-        // a row past the last would overflow only behind 2^31 - 1 rows
-        const Place p = place_of(c, r, row0 <= 0x7FFFFFFF - k ? row0 + k : 0x7FFFFFFF, keys);
-        if ((threadIdx.x & 31) == 0)
-            t.place[k] = p;
+    if (threadIdx.x < 32) {
+        const int i = request_of(c, row0);
+        if (threadIdx.x < ROWS)
+            t.place[threadIdx.x] = place_of(c, r, i, (long long)row0 + threadIdx.x, keys);
     }
     __syncthreads();
     const int half = r.dim / 2;
