@@ -595,7 +595,8 @@ typedef struct pmqa_heads {
 /*
  * Rotate the heads of a, and of b unless NULL (queries and keys of one step), at
  * rotary->positions; values outside the rotated part are copied. Products and
- * sums in fp32, one rounding to bf16. head_dim a multiple of 8, at most 1024. One
+ * sums in fp32, one rounding to bf16. head_dim a multiple of 8, at most 1024, the
+ * heads of a and b together at most 2^24 (PMQA_ERR_UNSUPPORTED otherwise). One
  * kernel launch.
  */
 int pmqa_rope(const pmqa_rotary *rotary, int32_t rows, const pmqa_heads *a, const pmqa_heads *b,
@@ -620,7 +621,8 @@ typedef struct pmqa_norm {
  *   keys     k: bf16 [rows, 128], row r at k + r * k_row. Normalised (norm),
  *            rotated, and written to the row's slot of kv_cache (pmqa_problem) as 128
  *            codes rne(k' / s) and the fp32 scale s = max(a, 2^-100) / 448, a the
- *            largest finite |k'|; infinite values saturate, NaN stays NaN
+ *            largest finite |k'|; infinite values saturate, NaN stays NaN. (The
+ *            quotient is k' times 448 / a, each to fp32: within 2^-21 of it)
  *   queries  q: bf16 [rows, heads, 128], head h of row r at q + r * q_row + h * q_head;
  *            rotated and quantised alike, each head with its own scale s, which goes
  *            into the head's weight:
@@ -631,7 +633,8 @@ typedef struct pmqa_norm {
  *   q_out    fp8 [rows, heads, 128], weights_out fp32 [rows, heads]
  * k or q may be NULL: then there is no key to write, or there are no queries (and
  * weights, q_out and weights_out are not used). k, q and their strides: 16-byte
- * aligned, multiples of 8 elements; q_out 8-byte aligned. weights_out may be
+ * aligned, multiples of 8 elements; q_out 8-byte aligned; heads at most 65535 and
+ * rows * heads < 2^31 (PMQA_ERR_UNSUPPORTED otherwise). weights_out may be
  * weights (fp32, weights_row = heads); outputs overlap nothing else.
  */
 typedef struct pmqa_index_rows {
@@ -684,7 +687,7 @@ int pmqa_index_read(const pmqa_paged_rows *p, const void *kv_cache, const int32_
  *            rne(x / q_scale), saturated
  * (x / scale is x times the scale's fp32 reciprocal.) c or q_c may be NULL, as in
  * pmqa_index_append. Strides in elements, multiples of 8; inputs 16-byte, outputs
- * 8-byte aligned; the scales finite, with finite reciprocals.
+ * 8-byte aligned; the scales finite, with finite reciprocals; heads as there.
  */
 typedef struct pmqa_latent_rows {
     const void *c;
@@ -722,11 +725,12 @@ size_t pmqa_latent_workspace_bytes(void);
  *   kv_cache  fp8 e4m3fn [num_blocks, block_size, 576], 16-byte aligned
  *   out       bf16 [rows, heads, 512], 16-byte aligned; lse fp32 [rows, heads] or NULL
  * heads 1 to 128, rows * heads < 2^31, |sm_scale * q_scale * kv_scale| * log2(e) at
- * most 1e20 (PMQA_ERR_UNSUPPORTED otherwise); all of them finite. A row that sees no token gives out = 0 and
- * lse = -inf; tokens behind a bad table entry are not attended to. A NaN among a
- * token's values makes the rows that see it NaN, and no other row.
- * The weights are held as two fp8 terms, to 2^-8 of each and 2^-14 of the row's
- * largest (2^-10 of 2^4); they are summed in fp32, unrounded.
+ * most 1e20 (PMQA_ERR_UNSUPPORTED otherwise); all of them finite. A row that sees no
+ * token gives out = 0 and lse = -inf; tokens behind a bad table entry are not attended
+ * to. A NaN among a token's values makes the rows that see it NaN, and no other row.
+ * The weights enter the products as two fp8 terms: to 2^-8 of each or 2^-14 of the
+ * row's largest where min(rows, max_rows) * heads <= 32, and to 2^-7 or 2^-13
+ * otherwise. Their sum is formed in fp32 of the unrounded ones.
  * ws: pmqa_latent_workspace_bytes() bytes, 256-byte aligned, its status word zero
  * before the first use (pmqa_workspace_init). One kernel launch where block_size *
  * max_blocks_per_seq <= 512, else two. Every sum is formed in one order: equal

@@ -418,9 +418,10 @@ __device__ __forceinline__ uint32_t e5m2x2_of_f16x2(uint32_t h2)
 }
 
 // Two weights, an f16 pair, as their terms (bytes 0 and 1): the f16 value of p is off
-// by 2^-11 at most, its difference from the first term exact. SAME: both terms go into one
-// accumulator, so the second has the first's unit: e5m2, which reaches down to 2^-17.
-// Otherwise it is e4m3 of 16 times the difference.
+// by 2^-11 at most, its difference from the first term exact: at most 2^-4 p, or 2^-10 below
+// p = 2^-6. SAME: both terms go into one accumulator, so the second has the first's unit:
+// e5m2, which reaches down to 2^-17 and leaves 2^-7 p or 2^-13. Otherwise it is e4m3 of 16
+// times the difference, which leaves 2^-8 p or 2^-14 (p of the row's largest weight >= 1).
 template <bool SAME>
 __device__ __forceinline__ void split2(uint32_t p, uint32_t &hi, uint32_t &lo)
 {

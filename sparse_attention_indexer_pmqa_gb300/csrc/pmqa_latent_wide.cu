@@ -24,9 +24,9 @@ namespace pmqa {
 namespace latent {
 
 // The block of the scores' products behind which the output update may be issued: its
-// warp wakes and issues in 200 cycles, the last six products' time (none before: 261 us
-// for batch decode, after block 1 258, 2 253, 3 253).
-constexpr int kTurnAt = 2;
+// warp wakes and issues in 200 cycles, about the time until the scores are done (none before: 261 us
+// for batch decode, after block 1 258, 2 and 3 253; prompt chunks 1878 after 2, 1848 after 3).
+constexpr int kTurnAt = 3;
 
 struct Wide {
     static constexpr int kTile = 64;                      // tokens per tile
