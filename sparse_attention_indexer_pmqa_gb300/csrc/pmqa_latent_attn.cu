@@ -21,8 +21,7 @@
 //     cost is the read of V.
 // The flattened sequence of (block, tile) is split evenly over the CTAs; a block
 // that is cut leaves its parts (O, m, l) in the workspace and a second kernel joins
-// them. Where a query token has more than 64 heads, neighbouring CTAs take its heads
-// and walk the same tokens at the same time, so that the second finds them in L2.
+// them. (More packed rows: pmqa_latent_wide.cu.)
 //
 // A NaN in a token's row makes all its scores NaN. Where some rows do not see the
 // token, its thread sets the row's values to zero before they are multiplied by
@@ -143,9 +142,9 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
     const uint32_t sbase = smem_u32(smem);
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(kFull, tid >> 5, 0);
-    const int g = blockIdx.x / a.peers, hs = blockIdx.x - g * a.peers;
+    const int g = blockIdx.x;
 
-    if (hs == 0 && tid == 0)
+    if (tid == 0)
         a.meta[g] = make_int4(0, 0, 0, 0);
     Range *const range = reinterpret_cast<Range *>(smem + K::kOffRange);
     find_range<K::kThreads>(a, g, reinterpret_cast<long long *>(smem), range);
@@ -300,7 +299,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
                     const int r = wg * RG + lane;
                     mneg[lane] = kUnseen;
                     // rows that do not exist see everything: no mask for their sake
-                    lims[lane] = r < piece->rows ? seen_by_all + (a.hb > 1 ? 0 : r / a.heads) : 0x7FFFFFFF;
+                    lims[lane] = r < piece->rows ? seen_by_all + r / a.heads : 0x7FFFFFFF;
                 }
                 __syncwarp();
             }
@@ -555,7 +554,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
         if constexpr (K::kSplit)
             asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == K::kPlanWarp) {
-            plan_tiles<K>(a, smem, bar, range, g, hs, hs == 0, abort_flag);
+            plan_tiles<K>(a, smem, bar, range, g, true, abort_flag);
         } else if (warp == K::kMmaWarp) {
         // ------------------------------------------------------------ products
         // Two streams, each issued as soon as its inputs are ready: the scores of tile nq and the output update of tile np. The
@@ -687,51 +686,60 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
     }
 }
 
-// The parts of every unit that was cut, joined: block (g, y) takes packed row y of
-// the unit that range g begins and later ranges go on with; a thread four columns.
+// The parts of every unit that was cut, joined: block (g, y) takes packed row y of the unit
+// that range g begins and later ranges go on with; a thread four columns. Bound by the
+// latency of a chain of loads (what there is, the parts), about 5 us behind 32 contexts: each
+// step rescales what the steps before gave, so that maxima and values are loaded
+// together (looking the request up and reading the maxima first: batch decode by graph 230 us,
+// now 220 to 226, verify 180 and 178). Two or four rows to a block, or a warp a row: equal.
 __global__ void __launch_bounds__(128) latent_join_kernel(const __grid_constant__ Args a)
 {
     griddep_wait();
-    const int g = blockIdx.x, hs = blockIdx.y / a.N, row = blockIdx.y - hs * a.N;
+    const int g = blockIdx.x, at = threadIdx.x, row = blockIdx.y;
     const int4 m = __ldcg(a.meta + g);
-    if (m.z < 2)
+    if (row >= m.y)
         return;
-    Cursor c;
-    c.i = m.x;
-    c.u = m.y;
-    c.r = load_req(a, c.i, false);
-    const Block b = block_of(a, c, hs);
-    if (row >= b.rows)
-        return;
-    auto slot = [&](int k) -> long long {
-        return ((long long)(2 * (g + k) + (k == 0 ? 1 : 0)) * a.hb + hs) * a.N + row;
-    };
-    float M = -INFINITY;
-    for (int k = 0; k < m.z; ++k)
-        M = fmaxf(M, __ldcg(a.ml + slot(k) * 2));
-    float L = 0.0f;
+    constexpr int U = 4;  // parts of a step
+    float M = -INFINITY, L = 0.0f;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int k = 0; k < m.z; ++k) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.ml + slot(k) * 2));
-        const float4 o = __ldcg(reinterpret_cast<const float4 *>(a.part + slot(k) * kVDim) + threadIdx.x);
-        const float w = ex2_approx(ml.x - M);
-        L += w * ml.y;
-        acc.x += w * o.x;
-        acc.y += w * o.y;
-        acc.z += w * o.z;
-        acc.w += w * o.w;
+#pragma unroll 1
+    for (int k0 = 0; k0 < m.z; k0 += U) {
+        float2 ml[U];
+        float4 o[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            ml[k] = make_float2(-INFINITY, 0.0f);
+            o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (k0 + k < m.z) {
+                const long long slot = (long long)(2 * (g + k0 + k) + (k0 + k == 0 ? 1 : 0)) * a.N + row;
+                ml[k] = __ldcg(reinterpret_cast<const float2 *>(a.ml + slot * 2));
+                o[k] = __ldcg(reinterpret_cast<const float4 *>(a.part + slot * kVDim) + at);
+            }
+        }
+        const float top = fmaxf(M, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x))), old = ex2_approx(M - top);
+        M = top;
+        L *= old;
+        acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const float w = ex2_approx(ml[k].x - top);
+            L += w * ml[k].y;
+            acc.x += w * o[k].x;
+            acc.y += w * o[k].y;
+            acc.z += w * o[k].z;
+            acc.w += w * o[k].w;
+        }
     }
     const float f = L == 0.0f ? 0.0f : a.kv_scale / L;
     const float y[4] = {acc.x, acc.y, acc.z, acc.w};
-    uint32_t o[2];
+    uint32_t b[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k)
-        o[k] = __bfloat16_as_ushort(__float2bfloat16_rn(f == 0.0f ? 0.0f : y[2 * k] * f)) |
+        b[k] = __bfloat16_as_ushort(__float2bfloat16_rn(f == 0.0f ? 0.0f : y[2 * k] * f)) |
                (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(f == 0.0f ? 0.0f : y[2 * k + 1] * f)) << 16;
-    *reinterpret_cast<uint2 *>(a.out + (b.first + row) * kVDim + 4 * threadIdx.x) = make_uint2(o[0], o[1]);
-    if (a.lse && threadIdx.x == 0)
-        a.lse[b.first + row] = L == 0.0f ? -INFINITY : (M + log2f(L)) * cache::kLn2;
+    *reinterpret_cast<uint2 *>(a.out + ((long long)m.x + row) * kVDim + 4 * at) = make_uint2(b[0], b[1]);
+    if (a.lse && at == 0)
+        a.lse[m.x + row] = L == 0.0f ? -INFINITY : (M + log2f(L)) * cache::kLn2;
 }
 
 template <int N>
@@ -741,16 +749,15 @@ cudaError_t launch(Args &a, int sms, cudaStream_t st)
     a.N = N;
     a.pad = 2;
     a.least = 2;
-    a.hb = a.peers = (a.heads + N - 1) / N;
     a.toks = 1;
-    while (a.hb == 1 && 2 * a.toks * a.heads <= N)
+    while (2 * a.toks * a.heads <= N)
         a.toks *= 2;
-    a.ranges = std::max(1, std::min(sms, kMaxCtas) / a.peers);
+    a.ranges = std::max(1, std::min(sms, kMaxCtas));
     static std::atomic<uint64_t> done{0};
     cudaError_t e = cache::allow_smem(latent_attn_kernel<N>, (int)Cfg<N>::kSmem, done);
     if (e != cudaSuccess)
         return e;
-    latent_attn_kernel<N><<<(unsigned)(a.ranges * a.peers), Cfg<N>::kThreads, Cfg<N>::kSmem, st>>>(a);
+    latent_attn_kernel<N><<<(unsigned)a.ranges, Cfg<N>::kThreads, Cfg<N>::kSmem, st>>>(a);
     return cudaGetLastError();
 }
 
@@ -806,6 +813,6 @@ extern "C" int pmqa_latent_attention(const pmqa_paged_rows *p, const void *q, co
                     : most <= 64 ? launch<64>(a, sms, st)
                                  : launch_wide(a, sms, st);
     if (e == cudaSuccess && !a.whole)
-        e = cache::launch_early(latent_join_kernel, dim3((unsigned)a.ranges, (unsigned)(a.hb * a.N)), 128, 0, true, st, a);
+        e = cache::launch_early(latent_join_kernel, dim3((unsigned)a.ranges, (unsigned)a.N), 128, 0, true, st, a);
     return cache::code_of(e);
 }

@@ -38,16 +38,14 @@ struct Args {
     int heads;
     int tile;           // tokens per tile: 128, or 64 (the wide kernel)
     int N;              // packed rows of a block
-    int toks;           // query tokens of a block (a power of two up to the tile's; 1 where hb > 1)
-    int hb;             // blocks of a query token
-    int peers;          // CTAs that walk the same tokens: a query token's blocks, or the value halves of one
+    int toks;           // query tokens of a block (a power of two up to the tile's)
     int pad;            // tiles' worth of starting and ending a block
     int least;          // fewest tiles that a range has
     int ranges;         // parts that the sequence is cut into at most
     int whole;          // blocks are not cut
-    int4 *meta;         // [ranges]: (request, unit, parts, 0) of the unit cut at the range's end
-    float *ml;          // [2 ranges][hb][N][2]
-    float *part;        // [2 ranges][hb][N][512]
+    int4 *meta;         // [ranges]: (first row of q and out, rows, parts, 0) of the unit cut at the range's end
+    float *ml;          // [2 ranges][N][2]
+    float *part;        // [2 ranges][N][512]
 };
 
 // ------------------------------------------------------------- the sequence
@@ -239,7 +237,7 @@ __device__ __forceinline__ bool next_tile(const Args &a, Cursor &c, long long x1
 
 // ------------------------------------------------------------- one block of rows
 
-// The packed rows of block `hs` of a unit.
+// The packed rows of a unit.
 struct Block {
     long long first;  // row of q and out
     int rows;         // packed rows
@@ -247,14 +245,13 @@ struct Block {
     int end;          // slots that some row sees
 };
 
-__device__ __forceinline__ Block block_of(const Args &a, const Cursor &c, int hs)
+__device__ __forceinline__ Block block_of(const Args &a, const Cursor &c)
 {
     Block b;
     const int j0 = c.u * a.toks;
     const int n = min(a.toks, c.r.q.n - j0);
-    const int h0 = hs * a.N;
-    b.rows = a.hb > 1 ? min(a.N, a.heads - h0) : n * a.heads;
-    b.first = ((long long)c.r.q.r0 + j0) * a.heads + h0;
+    b.rows = n * a.heads;
+    b.first = ((long long)c.r.q.r0 + j0) * a.heads;
     b.last = c.r.q.ctx - c.r.q.n + j0;
     b.end = min(c.r.q.ctx, max(0, b.last + n));
     return b;
@@ -305,14 +302,14 @@ static_assert(sizeof(Tile) == 32 && sizeof(Piece) == 32, "places in shared memor
 // place: kPieces > kTiles + 1 pieces later, when the output of the piece there is out.)
 template <class K>
 __device__ __forceinline__ void plan_tiles(const Args &a, uint8_t *smem, uint64_t *bar, const Range *range, int g,
-                                           int hs, bool joins, volatile int *abort_flag)
+                                           bool joins, volatile int *abort_flag)
 {
     constexpr int W = K::kTile / 32;
     Cursor c = range->at;
     const long long x0 = range->x0, x1 = range->x1;
     const int lane = threadIdx.x & 31;
     int page[W], off[W], seg = -1, e = 0;
-    Block b = block_of(a, c, hs);
+    Block b = block_of(a, c);
     auto look_up = [&](const Cursor &f, int end) {
 #pragma unroll
         for (int k = 0; k < W; ++k) {
@@ -344,7 +341,7 @@ __device__ __forceinline__ void plan_tiles(const Args &a, uint8_t *smem, uint64_
         const Block here = b;
         if (more) {
             if (last)
-                b = block_of(a, d, hs);
+                b = block_of(a, d);
             look_up(d, b.end);
         }
         if (it >= K::kAhead) {
@@ -376,7 +373,7 @@ __device__ __forceinline__ void plan_tiles(const Args &a, uint8_t *smem, uint64_
                 piece->rows = here.rows;
                 piece->last = here.last;
                 piece->sole = a.whole || (starts && xs + c.T <= x1);
-                piece->slot = (2 * g + (starts ? 1 : 0)) * a.hb + hs;
+                piece->slot = 2 * g + (starts ? 1 : 0);
             }
         }
         __syncwarp();
@@ -392,7 +389,7 @@ __device__ __forceinline__ void plan_tiles(const Args &a, uint8_t *smem, uint64_
         // the last unit goes on in later ranges and starts in this one: to be joined
         const long long xs = c.x - c.t, xe = xs + c.T;
         if (!a.whole && xs >= x0 && xe > x1)
-            a.meta[g] = make_int4(c.i, c.u, range_of(range->total, range->C, xe - 1) - g + 1, 0);
+            a.meta[g] = make_int4((int)b.first, b.rows, range_of(range->total, range->C, xe - 1) - g + 1, 0);
     }
 }
 

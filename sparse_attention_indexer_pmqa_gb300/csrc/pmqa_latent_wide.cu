@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == K::kPlanWarp) {
-            plan_tiles<K>(a, smem, bar, range, g, 0, vh == 0, abort_flag);
+            plan_tiles<K>(a, smem, bar, range, g, vh == 0, abort_flag);
         } else if (warp == K::kMmaWarp || warp == K::kOutWarp) {
             // -------------------------------------------------------- products
             // One warp for the scores, one for the output updates: between two issues a
@@ -586,17 +586,15 @@ cudaError_t launch_wide(Args &a, int sms, cudaStream_t st)
     a.N = Wide::kRows;
     a.pad = 4;
     a.least = 4;
-    a.hb = 1;
-    a.peers = 2;
     a.toks = 1;
     while (2 * a.toks * a.heads <= Wide::kRows && 2 * a.toks <= Wide::kTile)
         a.toks *= 2;
-    a.ranges = std::max(1, std::min(sms, kMaxCtas) / a.peers);
+    a.ranges = std::max(1, std::min(sms, kMaxCtas) / 2);
     static std::atomic<uint64_t> done{0};
     cudaError_t e = cache::allow_smem(latent_wide_kernel, (int)Wide::kSmem, done);
     if (e != cudaSuccess)
         return e;
-    latent_wide_kernel<<<(unsigned)(a.ranges * a.peers), Wide::kThreads, Wide::kSmem, st>>>(a);
+    latent_wide_kernel<<<(unsigned)(a.ranges * 2), Wide::kThreads, Wide::kSmem, st>>>(a);
     return cudaGetLastError();
 }
 
