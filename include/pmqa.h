@@ -68,6 +68,7 @@ enum {
 #define PMQA_DEV_OVERFLOW 0x8u     /* top-k candidate storage exceeded; results are invalid */
 #define PMQA_DEV_INTERNAL 0x10u    /* a kernel found its shared memory misaligned and did no work;
                                       results are invalid */
+#define PMQA_DEV_SCORE_RANGE 0x20u /* an attention score out of range; its row's result is invalid */
 
 /* Workspace-size selector for pmqa_workspace_bytes. For PMQA_OP_MQA_LOGITS (the
    prefill entry point) bs is the number of query rows m and the other sizes
@@ -578,8 +579,9 @@ int pmqa_rope_frequencies(int32_t dim, double base, int kind, double factor, dou
  * Heads of bf16 values to rotate: element d of head h of row r at
  * x + r * x_row + h * x_head + d (strides in elements, multiples of 8), the result
  * at out likewise; both 16-byte aligned. out may be x (with the same strides: the
- * values outside the rotated part are then not touched), and overlaps it
- * otherwise nowhere; two results never share an element.
+ * values outside the rotated part are then not touched); their spans overlap
+ * otherwise nowhere. Two results never share an element, nor does one tensor's result
+ * with the other's input.
  */
 typedef struct pmqa_heads {
     const void *x;
@@ -728,6 +730,8 @@ size_t pmqa_latent_workspace_bytes(void);
  * most 1e20 (PMQA_ERR_UNSUPPORTED otherwise); all of them finite. A row that sees no
  * token gives out = 0 and lse = -inf; tokens behind a bad table entry are not attended
  * to. A NaN among a token's values makes the rows that see it NaN, and no other row.
+ * A row whose largest score passes 2^23 ln 2 (5.8 million) in magnitude sets
+ * PMQA_DEV_SCORE_RANGE.
  * The weights enter the products as two fp8 terms: to 2^-8 of each or 2^-14 of the
  * row's largest where min(rows, max_rows) * heads <= 32, and to 2^-7 or 2^-13
  * otherwise. Their sum is formed in fp32 of the unrounded ones.

@@ -385,6 +385,8 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
                     if (x + m > kTop) {
                         f = ex2_approx(-x - m);  // 0 where no score was seen before
                         mneg[lane] = -x;
+                        if (fabsf(x) > kFarScore)
+                            atomicOr(a.c.status, (uint32_t)PMQA_DEV_SCORE_RANGE);
                     }
                     alpha[lane] = f;
                 }

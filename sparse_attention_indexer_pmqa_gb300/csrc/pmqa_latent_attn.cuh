@@ -20,6 +20,9 @@ constexpr int kNoPage = (int)0x80000000;  // no token there (a table entry is ne
 constexpr int kWhole = 512;     // tables of up to so many tokens: blocks are not cut
 constexpr float kTop = 8.0f;    // p = 2^(x - m); m moves when a p passes 2^kTop
 constexpr float kUnseen = 1e30f;   // -m of a row that has seen no score: above every |x|
+// m is an fp32 number: past this its step, a factor that all weights of a row have in common,
+// takes them out of the range of their terms (448 = 2^8.8 against 2^kTop).
+constexpr float kFarScore = 0x1p23f;
 constexpr double kMaxFactor = 1e20;  // |c_log2|: times a product of two rows (1.2e8) well below kUnseen
 
 constexpr size_t kWsMeta = cache::kStatusBytes;
@@ -92,14 +95,29 @@ struct Cursor {
 
     __device__ __forceinline__ void set_unit(const Args &a) { T = (r.f + u) / (a.tile / a.toks) + 1; }
 
-    // the next unit; false past the last
-    __device__ __forceinline__ bool next_unit(const Args &a)
+    // the next unit; false where it is not before place x1 (the last one's end is not after
+    // any range's, so the requests behind it are not looked at)
+    __device__ __forceinline__ bool next_unit(const Args &a, long long x1)
     {
         x += T + a.pad - t;
         t = 0;
         ++u;
+        if (x >= x1)
+            return false;
         while (u >= r.U) {
-            if (++i >= a.c.bs)
+            // past requests without rows, eight at a time: each look costs the latency of memory
+            ++i;
+            for (int k = 8; k == 8; i += k) {
+                int b[9];
+#pragma unroll
+                for (int j = 0; j < 9; ++j)
+                    b[j] = __ldg(a.c.row_begin + min(i + j, a.c.bs));
+                k = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    k += k == j && b[j] == b[j + 1] && i + j < a.c.bs ? 1 : 0;
+            }
+            if (i >= a.c.bs)
                 return false;
             r = load_req(a, i, false);
             u = 0;
@@ -208,9 +226,9 @@ __device__ __forceinline__ void find_range(const Args &a, int g, long long *s_su
             // behind the tiles, or (whole) inside a unit: the next one
             bool any = true;
             if (c.t >= c.T || (a.whole && c.t > 0))
-                any = c.next_unit(a);
+                any = c.next_unit(a, x1);
             s_range->at = c;
-            s_range->any = any && c.x < x1;
+            s_range->any = any;
         }
         base += all;
         if (base > x0)
@@ -232,7 +250,7 @@ __device__ __forceinline__ bool next_tile(const Args &a, Cursor &c, long long x1
     ++c.x;
     if (c.t < c.T)
         return a.whole || c.x < x1;
-    return c.next_unit(a) && c.x < x1;
+    return c.next_unit(a, x1);
 }
 
 // ------------------------------------------------------------- one block of rows

@@ -338,6 +338,8 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
                     alpha = ex2_approx(-x - mneg);  // 0 where no score was seen before
                     mneg = -x;
                     l *= alpha;
+                    if (fabsf(x) > kFarScore)
+                        atomicOr(a.c.status, (uint32_t)PMQA_DEV_SCORE_RANGE);
                 }
                 if (first || alpha != 1.0f)
                     shared_m[row] = mneg;

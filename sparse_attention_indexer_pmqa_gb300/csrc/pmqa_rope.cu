@@ -169,6 +169,12 @@ extern "C" int pmqa_rope(const pmqa_rotary *rotary, int32_t rows, const pmqa_hea
         rc = check_heads(b, rows);
     if (rc != PMQA_OK)
         return rc;
+    const long long all = (long long)a->heads + (b ? b->heads : 0);
+    if (all > kMaxAll)  // counted in 32 bits, over the rows of a CTA
+        return PMQA_ERR_UNSUPPORTED;
+    // one tensor's result on the other's (where both begin alike; a fused projection's slices do not)
+    if (b && rows > 0 && a->heads > 0 && b->heads > 0 && (a->out == b->out || a->out == b->x || b->out == a->x))
+        return PMQA_ERR_INVALID_ARG;
     RopeArgs k{};
     const int width = b ? std::min(a->head_dim, b->head_dim) : a->head_dim;
     if ((rc = check_rotary(rotary, width, rows > 0, &k.r)) != PMQA_OK)
@@ -193,9 +199,6 @@ extern "C" int pmqa_rope(const pmqa_rotary *rotary, int32_t rows, const pmqa_hea
             widest = std::max(widest, h->head_dim);
         }
     }
-    const long long all = (long long)k.heads[0] + k.heads[1];
-    if (all > kMaxAll)  // counted in 32 bits, over the rows of a CTA
-        return PMQA_ERR_UNSUPPORTED;
     k.items = k.r.dim / 16 + (k.copies ? (widest - k.r.dim + 15) / 16 : 0);
     if (rows == 0 || all == 0 || k.items == 0)
         return PMQA_OK;

@@ -27,6 +27,7 @@ PMQA_DEV_BAD_CONTEXT = 0x2
 PMQA_DEV_TIMEOUT = 0x4
 PMQA_DEV_OVERFLOW = 0x8
 PMQA_DEV_INTERNAL = 0x10
+PMQA_DEV_SCORE_RANGE = 0x20
 
 PMQA_OP_LOGITS = 0
 PMQA_OP_TOPK = 1

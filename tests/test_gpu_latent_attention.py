@@ -121,6 +121,29 @@ def test_scores_that_rise_along_the_context(cuda_lib, heads, rows):
     assert check(run(cuda_lib, p), ref.attention(p), p) == 0
 
 
+@pytest.mark.parametrize("heads", [8, 16, 64, 128])
+@pytest.mark.parametrize("sm,far", [(60.0, True), (-60.0, True), (0.06, False), (-0.06, False)])
+def test_scores_out_of_range_are_reported(cuda_lib, heads, sm, far):
+    """Equal tokens of the largest values, with unit scales: each score is 0.7 or 700 times the
+    largest of the range; within it all weights are equal."""
+    p = ref.attention_problem([1, 1], [300, 7], heads, 16, seed=4)
+    p.kv[:], p.q[:] = 0x7E, 0x7E
+    p.q_scale, p.kv_scale, p.sm = 1.0, 1.0, sm / 1.44269504 / 1.1561
+    out, _, status = run(cuda_lib, p)
+    if far:
+        assert status == cuda_lib.PMQA_DEV_SCORE_RANGE
+    else:
+        # equal weights: off by a weight's two terms, and one rounding
+        assert status == 0
+        assert bool(((out.double() - 448.0).abs() <= 448.0 * (2.0 ** -7 + 2.0 ** -8 + 2.0 ** -11)).all())
+
+
+def test_without_a_log_sum_exp(cuda_lib):
+    p = ref.attention_problem([1, 2], [700, 90], 16, 16, seed=12)
+    args = [t.cuda() for t in (p.q, p.kv, p.bt, p.ctx, p.rb)] + [p.max_rows, p.q_scale, p.kv_scale, p.sm]
+    assert torch.equal(cuda_lib.pmqa_latent_attention(*args).cpu(), run(cuda_lib, p)[0])
+
+
 def test_lengths_that_break_the_rules_are_clamped(cuda_lib):
     p = ref.attention_problem([2, 2], [40, 64], 16, 16, seed=2)
     want = ref.attention(p)

@@ -437,6 +437,26 @@ def test_many_requests(cuda_lib, heads):
     assert check(run(cuda_lib, p), ref.attention(p), p) == 0
 
 
+@pytest.mark.parametrize("heads", [16, 128])
+def test_a_padded_batch(cuda_lib, heads):
+    """Requests without rows before, between and behind the others, some of them with contexts."""
+    rows, ctx = [0] * 4000, [0] * 4000
+    for i, n, c in ((7, 1, 300), (8, 2, 40), (16, 1, 1000), (1500, 3, 3), (1501, 1, 129), (2700, 1, 700)):
+        rows[i], ctx[i] = n, c
+    for i in (0, 9, 15, 1499, 3999):
+        ctx[i] = 100
+    p = ref.attention_problem(rows, ctx, heads, 16, seed=14, tail=2)
+    assert check(run(cuda_lib, p), ref.attention(p), p) == 0
+    # the table wide enough for contexts to be cut
+    p.bt = torch.cat([p.bt, torch.full((4000, 8), -1, dtype=torch.int32)], 1)
+    assert check(run(cuda_lib, p), ref.attention(p), p) == 0
+
+
+def test_rows_of_no_request_at_all(cuda_lib):
+    p = ref.attention_problem([0, 0], [30, 0], 16, 16, seed=15, lead=3)
+    assert check(run(cuda_lib, p), ref.attention(p), p) == 0
+
+
 # ------------------------------------------------------------- shared, strided, empty
 
 @pytest.mark.parametrize("heads", [16, 64, 128])

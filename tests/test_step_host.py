@@ -148,6 +148,10 @@ def test_rope(lib):
             (dict(x_row=1 << 62), INV), (dict(out_head=1 << 62), INV)]:
         assert rope(lib, a=heads(**kw)) == code, kw
         assert rope(lib, b=heads(**kw)) == code, kw
+    # one tensor's result where the other's begins
+    assert rope(lib, b=heads(x=0x3000000)) == INV
+    assert rope(lib, b=heads(x=0x2000000, out=0x4000000)) == INV
+    assert rope(lib, b=heads(x=0x3000000, out=0x1000000)) == INV
     # narrower heads beside wide ones: the rotated part has to fit both
     assert rope(lib, rotary(dim=128), b=heads(head_dim=64, x=0x3000000, out=0x4000000)) == INV
     # nothing to do
