@@ -624,7 +624,7 @@ typedef struct pmqa_norm {
  *            rotated, and written to the row's slot of kv_cache (pmqa_problem) as 128
  *            codes rne(k' / s) and the fp32 scale s = max(a, 2^-100) / 448, a the
  *            largest finite |k'|; infinite values saturate, NaN stays NaN. (The
- *            quotient is k' times 448 / a, each to fp32: within 2^-21 of it)
+ *            quotient is k' times 448 / a, each in fp32: within 2^-21 of it)
  *   queries  q: bf16 [rows, heads, 128], head h of row r at q + r * q_row + h * q_head;
  *            rotated and quantised alike, each head with its own scale s, which goes
  *            into the head's weight:

@@ -208,6 +208,25 @@ def test_index_append_infinities_nan_and_zeros(cuda_lib):
     assert bool((code[3] == 448).all()) and bool(s[3] == tiny)
 
 
+def test_index_append_at_the_ends_of_the_range(cuda_lib):
+    """The largest finite bf16 values, whose quotient's factor is below 2^-119, and the least."""
+    pmqa = cuda_lib
+    p = index_case([6], [6], 16, 3, seed=8)
+    for t in (p.k, p.q.view(-1, 128)):
+        for r, a in enumerate((3.38e38, 1.2e38, 8.6e37, 1e37, 1e-38, 1e-29)):
+            t[r] = (t[r].float() / t[r].float().abs().amax() * a).to(torch.bfloat16)
+    kv, qo, wo = p.kv.cuda(), *(torch.empty(s, dtype=d, device="cuda") for s, d in (
+        ((6, 3, 128), torch.uint8), ((6, 3), torch.float32)))
+    pmqa.pmqa_index_append(p.k.cuda(), kv, p.bt.cuda(), p.ctx.cuda(), p.rb.cuda(), 6, q=p.q.cuda(),
+                           weights=torch.ones((6, 3)).cuda(), q_out=qo, weights_out=wo)
+    got = kv.cpu().reshape(-1, 132)[ref.places(p, 0, 0, 6)]
+    y = p.k.double()
+    check_codes(ref.value(got[:, :128].contiguous()), got[:, 128:].contiguous().view(torch.float32)[:, 0].double(), y,
+                torch.zeros_like(y))
+    y = p.q.double()
+    check_codes(ref.value(qo.cpu()), wo.cpu().double(), y, torch.zeros_like(y))
+
+
 def test_index_append_bad_places_are_reported(cuda_lib):
     pmqa = cuda_lib
     ws = pmqa.workspace(1, 1, 1, 0, pmqa.PMQA_OP_LOGITS)
