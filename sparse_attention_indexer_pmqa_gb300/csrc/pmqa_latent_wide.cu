@@ -33,6 +33,10 @@ struct Wide {
     static constexpr int kStages = 5;                     // slots of a tile's rows
     static constexpr int kAhead = 2;                      // tiles that the planner is ahead of the producers
     static constexpr int kTiles = kStages + kAhead, kPieces = 10;
+    // The output of tile t waits for the scores of t + 2. Those of t + 6 need the slot of
+    // tile t + 1 and so this wait's end: with four barriers no phase is passed over (two
+    // could be, by the scores of t + 4: they need the slot of t - 1 alone).
+    static constexpr int kTurns = 4;
     static constexpr int kRows = 128, kThreads = 512;
     static constexpr int kMmaWarp = 12, kPlanWarp = 13, kOutWarp = 14;
     static constexpr uint32_t kVBytes = kTile / 8 * kVGroup, kRBytes = kTile / 8 * kRGroup;
@@ -59,8 +63,8 @@ struct Wide {
     static constexpr int kBPEmpty = kBPFull + 2;        // [2] P read: MMA commit
     static constexpr int kBM = kBPEmpty + 2;            // [2] m published: 4 softmax warps
     static constexpr int kBQFull = kBM + 2;             // a block's queries in tensor memory: 8 softmax warps
-    static constexpr int kBTurn = kBQFull + 1;          // [2] scores issued: the scores' warp
-    static constexpr int kBDrain = kBTurn + 2;
+    static constexpr int kBTurn = kBQFull + 1;          // [kTurns] scores issued: the scores' warp
+    static constexpr int kBDrain = kBTurn + kTurns;
     static constexpr int kBars = kBDrain + 2;           // both product warps
     static constexpr uint32_t kOffMisc = kOffBar + kBars * 8;
     static constexpr uint32_t kSmem = kOffMisc + 16;
@@ -138,8 +142,9 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
             mbar_init(&bar[K::kBPFull + s], 4);
             mbar_init(&bar[K::kBPEmpty + s], 1);
             mbar_init(&bar[K::kBM + s], 4);
-            mbar_init(&bar[K::kBTurn + s], 1);
         }
+        for (int s = 0; s < K::kTurns; ++s)
+            mbar_init(&bar[K::kBTurn + s], 1);
         mbar_init(&bar[K::kBSFree], 4);
         mbar_init(&bar[K::kBQFull], 8);
         mbar_init(&bar[K::kBDrain], 1);
@@ -523,7 +528,7 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
                                 umma_f8_ts(tmem + K::kColS, tmem + K::kColQ + 32u * kb + 8u * k, bk + 64u * kb + 2u * k, K::kIdescQK,
                                            (kb | k) ? 1u : 0u);
                             if (kb == kTurnAt)
-                                mbar_arrive(&bar[K::kBTurn + now]);
+                                mbar_arrive(&bar[K::kBTurn + it % K::kTurns]);
                         }
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
@@ -534,7 +539,7 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
                     // behind the scores of two tiles on, so that these are worked on while S
                     // waits to be read; a piece's last two tiles do not wait
                     if (!wait(K::kBPFull + now, (uint32_t)(it >> 1) & 1u) ||
-                        ((flags & kSteady) && !wait(K::kBTurn + now, ((uint32_t)(it >> 1) & 1u) ^ 1u)))
+                        ((flags & kSteady) && !wait(K::kBTurn + (it + 2) % K::kTurns, (uint32_t)((it + 2) / K::kTurns) & 1u)))
                         break;
                     fence_proxy_async_smem();  // cp.async writes -> tensor-core reads
                     tc_fence_after_sync();
