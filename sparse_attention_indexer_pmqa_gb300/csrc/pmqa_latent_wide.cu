@@ -64,7 +64,8 @@ struct Wide {
     static constexpr int kBM = kBPEmpty + 2;            // [2] m published: 4 softmax warps
     static constexpr int kBQFull = kBM + 2;             // a block's queries in tensor memory: 8 softmax warps
     static constexpr int kBTurn = kBQFull + 1;          // [kTurns] scores issued: the scores' warp
-    static constexpr int kBDrain = kBTurn + kTurns;
+    static constexpr int kBRead = kBTurn + kTurns;      // [kTiles] description read by the softmax group of the other tiles: 4 warps
+    static constexpr int kBDrain = kBRead + kTiles;
     static constexpr int kBars = kBDrain + 2;           // both product warps
     static constexpr uint32_t kOffMisc = kOffBar + kBars * 8;
     static constexpr uint32_t kSmem = kOffMisc + 16;
@@ -136,6 +137,7 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
         for (int s = 0; s < K::kTiles; ++s) {
             mbar_init(&bar[K::kBInfo + s], 1);
             mbar_init(&bar[K::kBUsed + s], 4);
+            mbar_init(&bar[K::kBRead + s], 4);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bar[K::kBSFull + s], 1);
@@ -409,6 +411,12 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(&bar[K::kBPFull + now]);
+            }
+            if (now != (uint32_t)wg) {
+                // all that this group reads of the other's tile
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&bar[K::kBRead + e]);
             }
             if (++vs == K::kStages)
                 vs = 0;

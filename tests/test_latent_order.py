@@ -28,6 +28,7 @@ def number(name, default=None):
 STAGES, AHEAD = number("kStages"), number("kAhead")
 TILES = STAGES + AHEAD
 TURNS = number("kTurns", 2)     # barriers of "scores issued"
+READ = re.search(r"mbar_arrive\(&bar\[K::kBRead", source("pmqa_latent_wide.cu")) is not None
 
 
 class Order:
@@ -100,7 +101,7 @@ class Order:
         return past
 
 
-COUNTS = dict(info=1, used=4, ready=4, vempty=1, sfull=1, sfree=4, pfull=4, pempty=1, m=4, qfull=8, turn=1, exit=8)
+COUNTS = dict(info=1, used=4, ready=4, vempty=1, sfull=1, sfree=4, pfull=4, pempty=1, m=4, qfull=8, turn=1, exit=8, seen=4)
 
 
 def of(name, ring, tile):
@@ -118,6 +119,8 @@ def wide(pieces):
         # the planner
         if it >= AHEAD:
             o.wait("plan", *of("used", TILES, it - AHEAD))
+        if READ:
+            o.wait("plan", *of("seen", TILES, it - TILES))
         o.event("plan", ("write", it))
         o.arrive("plan", *of("info", TILES, it))
         # the producers
@@ -145,6 +148,8 @@ def wide(pieces):
                 o.arrive(me, *of("m", 2, it))
                 o.wait(me, *of("pempty", 2, it - 2))
                 o.arrive(me, *of("pfull", 2, it))
+            elif READ:
+                o.arrive(me, *of("seen", TILES, it))
             if last:
                 if it > 0:
                     o.wait(me, *of("pempty", 2, it - 1))
@@ -180,3 +185,19 @@ PIECES = [[20], [1] * 12, [2] * 8, [3] * 6, [1, 9, 2, 7, 1, 1, 3], [5, 6, 4, 5]]
 @pytest.mark.parametrize("pieces", PIECES)
 def test_the_wait_for_later_scores_is_not_lapped(pieces):
     wide(pieces).check(COUNTS, "turn")
+
+
+@pytest.mark.parametrize("pieces", PIECES)
+def test_no_wait_but_for_outputs_is_lapped(pieces):
+    for bar in COUNTS.keys() - {"pempty"}:
+        wide(pieces).check(COUNTS, bar)
+
+
+@pytest.mark.parametrize("pieces", PIECES)
+def test_descriptions_are_read_before_their_place_is_used_again(pieces):
+    o = wide(pieces)
+    _, past = o.close(COUNTS)
+    for it in range(sum(pieces)):
+        for name, ring in (("read", TILES), ("rows", AHEAD)):
+            for written in o.names.get(("write", it + ring), []):
+                assert all(past[written] >> e & 1 for e in o.names[name, it]), (name, it)
