@@ -37,6 +37,11 @@ struct Wide {
     // tile t + 1 and so this wait's end: with four barriers no phase is passed over (two
     // could be, by the scores of t + 4: they need the slot of t - 1 alone).
     static constexpr int kTurns = 4;
+    // A softmax group waits for the output of the tile two before its own, and where m moved, and
+    // at a block's end, for that of the tile it does not work on. Four barriers: each such wait begins
+    // when the phase before its own, four tiles back, is over. With two, that rested on one output's
+    // end being reported before the next one's.
+    static constexpr int kOuts = 4;
     static constexpr int kRows = 128, kThreads = 512;
     static constexpr int kMmaWarp = 12, kPlanWarp = 13, kOutWarp = 14;
     static constexpr uint32_t kVBytes = kTile / 8 * kVGroup, kRBytes = kTile / 8 * kRGroup;
@@ -60,8 +65,8 @@ struct Wide {
     static constexpr int kBSFull = kBVEmpty + kStages;  // [2] scores in tensor memory: MMA commit
     static constexpr int kBSFree = kBSFull + 2;         // scores read: 4 softmax warps
     static constexpr int kBPFull = kBSFree + 1;         // [2] P written, O rescaled: 4 softmax warps
-    static constexpr int kBPEmpty = kBPFull + 2;        // [2] P read: MMA commit
-    static constexpr int kBM = kBPEmpty + 2;            // [2] m published: 4 softmax warps
+    static constexpr int kBPEmpty = kBPFull + 2;        // [kOuts] P read: MMA commit
+    static constexpr int kBM = kBPEmpty + kOuts;        // [2] m published: 4 softmax warps
     static constexpr int kBQFull = kBM + 2;             // a block's queries in tensor memory: 8 softmax warps
     static constexpr int kBTurn = kBQFull + 1;          // [kTurns] scores issued: the scores' warp
     static constexpr int kBRead = kBTurn + kTurns;      // [kTiles] description read by the softmax group of the other tiles: 4 warps
@@ -142,9 +147,10 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bar[K::kBSFull + s], 1);
             mbar_init(&bar[K::kBPFull + s], 4);
-            mbar_init(&bar[K::kBPEmpty + s], 1);
             mbar_init(&bar[K::kBM + s], 4);
         }
+        for (int s = 0; s < K::kOuts; ++s)
+            mbar_init(&bar[K::kBPEmpty + s], 1);
         for (int s = 0; s < K::kTurns; ++s)
             mbar_init(&bar[K::kBTurn + s], 1);
         mbar_init(&bar[K::kBSFree], 4);
@@ -224,6 +230,11 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
         const uint32_t lanes = tmem + ((uint32_t)(w4 * 32) << 16);
         float *const red = reinterpret_cast<float *>(smem + K::kOffRed);  // [2][128]
         float *const shared_m = reinterpret_cast<float *>(smem + K::kOffM);  // [128]: -m
+        // the output of tile t is done
+        auto out_done = [&](int t) {
+            static_assert(K::kOuts == 4, "a shift: tiles before the first have the phase before the first");
+            return mbar_wait(&bar[K::kBPEmpty + (t & (K::kOuts - 1))], (uint32_t)(t >> 2) & 1u, abort_flag);
+        };
         float l = 0.0f, mneg = kUnseen;
         int seg = -1, vs = 0, e = 0, lim = 0;
         uint32_t eph = 0;
@@ -375,14 +386,14 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
                 }
                 l += s0 + s1;
                 // this buffer of P is free
-                if (!__all_sync(kFull, mbar_wait(&bar[K::kBPEmpty + now], ph ^ 1u, abort_flag))) {
+                if (!__all_sync(kFull, out_done(it - 2))) {
                     fail(a, abort_flag);
                     named_bar_and(1, 256, false);
                     break;
                 }
                 if (!first && __any_sync(kFull, alpha != 1.0f)) {
                     // O: the output of the tile before is done
-                    if (!__all_sync(kFull, mbar_wait(&bar[K::kBPEmpty + was], wph, abort_flag))) {
+                    if (!__all_sync(kFull, out_done(it - 1))) {
                         fail(a, abort_flag);
                         named_bar_and(1, 256, false);
                         break;
@@ -428,11 +439,8 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
                 continue;
 
             // ------------------------------------------------ end of a block
-            // (the update before the last one first: a parity says nothing of the phase before
-            // its own, which this group may not have waited for)
-            const bool ok = __all_sync(kFull, (it == 0 || mbar_wait(&bar[K::kBPEmpty + was], wph, abort_flag)) &&
-                                                  mbar_wait(&bar[K::kBPEmpty + now], ph, abort_flag));
-            if (!named_bar_and(1, 256, ok)) {
+            // (the last two tiles': one of them is of the other group)
+            if (!named_bar_and(1, 256, __all_sync(kFull, (it == 0 || out_done(it - 1)) && out_done(it)))) {
                 fail(a, abort_flag);
                 break;
             }
@@ -561,7 +569,7 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
                                 umma_f8_ts(tmem + K::kColO, ap + 16u * term + 8u * ks, bv + (((uint32_t)ks * 4u * kVGroup) >> 4),
                                            term ? K::kIdescPVLo : K::kIdescPV, ((flags & kFirst) && ks == 0 && term == 0) ? 0u : 1u);
                         umma_commit(&bar[K::kBVEmpty + vs]);
-                        umma_commit(&bar[K::kBPEmpty + now]);
+                        umma_commit(&bar[K::kBPEmpty + it % K::kOuts]);
                     }
                 }
                 __syncwarp();

@@ -28,6 +28,7 @@ def number(name, default=None):
 STAGES, AHEAD = number("kStages"), number("kAhead")
 TILES = STAGES + AHEAD
 TURNS = number("kTurns", 2)     # barriers of "scores issued"
+OUTS = number("kOuts", 2)       # of "output done"
 READ = re.search(r"mbar_arrive\(&bar\[K::kBRead", source("pmqa_latent_wide.cu")) is not None
 
 
@@ -108,8 +109,9 @@ def of(name, ring, tile):
     return ((name, tile % ring), tile // ring)
 
 
-def wide(pieces):
-    """The kernel's events over pieces of so many tiles."""
+def wide(pieces, moved=None):
+    """The kernel's events over pieces of so many tiles. moved: (warp, tile) where a softmax warp
+    found a maximum moved and waits for the output of the tile before."""
     o = Order()
     place = [(t, n) for n in pieces for t in range(n)]
     seg = -1
@@ -146,14 +148,16 @@ def wide(pieces):
                 o.wait(me, *of("sfull", 2, it))
                 o.arrive(me, ("sfree", 0), it)
                 o.arrive(me, *of("m", 2, it))
-                o.wait(me, *of("pempty", 2, it - 2))
+                o.wait(me, *of("pempty", OUTS, it - 2))
+                if moved == (w, it) and not first:
+                    o.wait(me, *of("pempty", OUTS, it - 1))
                 o.arrive(me, *of("pfull", 2, it))
             elif READ:
                 o.arrive(me, *of("seen", TILES, it))
             if last:
                 if it > 0:
-                    o.wait(me, *of("pempty", 2, it - 1))
-                o.wait(me, *of("pempty", 2, it))
+                    o.wait(me, *of("pempty", OUTS, it - 1))
+                o.wait(me, *of("pempty", OUTS, it))
                 for k in range(2):
                     o.arrive(me, ("exit", 0), 2 * seg + k)
                     o.wait(me, ("exit", 0), 2 * seg + k)
@@ -174,7 +178,7 @@ def wide(pieces):
         if steady:
             o.wait("out", *of("turn", TURNS, it + 2))
         issued = o.event("out")
-        for name, ring in (("vempty", STAGES), ("pempty", 2)):
+        for name, ring in (("vempty", STAGES), ("pempty", OUTS)):
             o.arrive(None, *of(name, ring, it), after=[issued])
     return o
 
@@ -191,6 +195,13 @@ def test_the_wait_for_later_scores_is_not_lapped(pieces):
 def test_no_wait_but_for_outputs_is_lapped(pieces):
     for bar in COUNTS.keys() - {"pempty"}:
         wide(pieces).check(COUNTS, bar)
+
+
+@pytest.mark.parametrize("pieces", PIECES)
+def test_no_wait_is_lapped_where_a_maximum_moves(pieces):
+    wide(pieces).check(COUNTS)
+    for it in range(sum(pieces)):
+        wide(pieces, (4 * (it % 2) + it // 2 % 4, it)).check(COUNTS)
 
 
 @pytest.mark.parametrize("pieces", PIECES)
