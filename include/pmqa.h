@@ -732,9 +732,11 @@ size_t pmqa_latent_workspace_bytes(void);
  * to. A NaN among a token's values makes the rows that see it NaN, and no other row.
  * A row whose largest score passes 2^23 ln 2 (5.8 million) in magnitude sets
  * PMQA_DEV_SCORE_RANGE.
- * The weights enter the products as two fp8 terms: to 2^-8 of each or 2^-14 of the
- * row's largest where min(rows, max_rows) * heads <= 32, and to 2^-7 or 2^-13
- * otherwise. Their sum is formed in fp32 of the unrounded ones.
+ * The weights enter the products as two fp8 terms, each to 2^-8 of itself where
+ * min(rows, max_rows) * heads <= 32 and to 2^-7 otherwise. What is lost of small ones
+ * beside that is, over all n tiles of 128 tokens that a row sees, at most 2^-7.6 (1 + ln n) of the
+ * row's weight (light tokens behind a heavy one with 80 % of it: 1 % of theirs, measured
+ * up to 128 k tokens). Their sum is formed in fp32 of the unrounded ones.
  * ws: pmqa_latent_workspace_bytes() bytes, 256-byte aligned, its status word zero
  * before the first use (pmqa_workspace_init). One kernel launch where block_size *
  * max_blocks_per_seq <= 512, else two. Every sum is formed in one order: equal

@@ -42,6 +42,7 @@ struct Wide {
     // when the phase before its own, four tiles back, is over. With two, that rested on one output's
     // end being reported before the next one's.
     static constexpr int kOuts = 4;
+    static constexpr float kAim = 0.0f;  // a weight that moves m up (at 1 prompt chunks 1935 us, at 0 1907)
     static constexpr int kRows = 128, kThreads = 512;
     static constexpr int kMmaWarp = 12, kPlanWarp = 13, kOutWarp = 14;
     static constexpr uint32_t kVBytes = kTile / 8 * kVGroup, kRBytes = kTile / 8 * kRGroup;
@@ -235,7 +236,7 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
             static_assert(K::kOuts == 4, "a shift: tiles before the first have the phase before the first");
             return mbar_wait(&bar[K::kBPEmpty + (t & (K::kOuts - 1))], (uint32_t)(t >> 2) & 1u, abort_flag);
         };
-        float l = 0.0f, mneg = kUnseen;
+        float l = 0.0f, mneg = kUnseen, need = 0.0f;
         int seg = -1, vs = 0, e = 0, lim = 0;
         uint32_t eph = 0;
         for (int it = 0;; ++it) {
@@ -273,6 +274,7 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
                     mbar_arrive(&bar[K::kBQFull]);
                 l = 0.0f;
                 mneg = kUnseen;
+                need = 0.0f;
                 // rows that do not exist see everything: no mask for their sake
                 lim = is ? piece->last + row / a.heads : 0x7FFFFFFF;
             }
@@ -338,7 +340,7 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
                         }
                     }
                 }
-                // the row's largest score here, and m: moved where a weight would pass 2^kTop
+                // the row's largest score here, and m (l and need are of this group's tiles)
                 float x;
                 {
                     float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -352,11 +354,14 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
                     x = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * fabsf(a.c_log2);
                 }
                 float alpha = 1.0f;
-                if (x + mneg > kTop) {
-                    alpha = ex2_approx(-x - mneg);  // 0 where no score was seen before
-                    mneg = -x;
+                need += kEnough * K::kTile;
+                if (x + mneg > kTop || l < need) {
+                    bool is_short;
+                    const float to = moved_to(K::kAim, mneg, x, l, need, is_short);
+                    alpha = ex2_approx(to - mneg);  // 0 where no score was seen before
+                    mneg = to;
                     l *= alpha;
-                    if (fabsf(x) > kFarScore)
+                    if (alpha != 1.0f && fabsf(to) > kFarScore)
                         atomicOr(a.c.status, (uint32_t)PMQA_DEV_SCORE_RANGE);
                 }
                 if (first || alpha != 1.0f)
@@ -400,16 +405,21 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
                     }
                     tc_fence_after_sync();
 #pragma unroll 1
-                    for (int k = 0; k < 8; ++k) {
-                        uint32_t o[32];
-                        const uint32_t ta = lanes + K::kColO + 32u * k;
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t o[64];
+                        const uint32_t ta = lanes + K::kColO + 64u * k;
                         tmem_ld32(ta, o);
+                        tmem_ld32(ta + 32u, o + 32);
                         tmem_ld_wait();
-                        reg_fence_cols<32>(o);
+                        reg_fence16(o);
+                        reg_fence16(o + 16);
+                        reg_fence16(o + 32);
+                        reg_fence16(o + 48);
 #pragma unroll
-                        for (int z = 0; z < 32; ++z)
+                        for (int z = 0; z < 64; ++z)
                             o[z] = __float_as_uint(__uint_as_float(o[z]) * alpha);
                         tmem_st32(ta, o);
+                        tmem_st32(ta + 32u, o + 32);
                     }
                 }
                 tc_fence_after_sync();
@@ -544,7 +554,7 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
                                 umma_f8_ts(tmem + K::kColS, tmem + K::kColQ + 32u * kb + 8u * k, bk + 64u * kb + 2u * k, K::kIdescQK,
                                            (kb | k) ? 1u : 0u);
                             if (kb == kTurnAt)
-                                mbar_arrive(&bar[K::kBTurn + it % K::kTurns]);
+                                mbar_arrive(&bar[K::kBTurn + ((uint32_t)it & (K::kTurns - 1u))]);
                         }
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
@@ -555,7 +565,7 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
                     // behind the scores of two tiles on, so that these are worked on while S
                     // waits to be read; a piece's last two tiles do not wait
                     if (!wait(K::kBPFull + now, (uint32_t)(it >> 1) & 1u) ||
-                        ((flags & kSteady) && !wait(K::kBTurn + (it + 2) % K::kTurns, (uint32_t)((it + 2) / K::kTurns) & 1u)))
+                        ((flags & kSteady) && !wait(K::kBTurn + (((uint32_t)it + 2u) & (K::kTurns - 1u)), (((uint32_t)it + 2u) >> 2) & 1u)))
                         break;
                     fence_proxy_async_smem();  // cp.async writes -> tensor-core reads
                     tc_fence_after_sync();
@@ -569,7 +579,7 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
                                 umma_f8_ts(tmem + K::kColO, ap + 16u * term + 8u * ks, bv + (((uint32_t)ks * 4u * kVGroup) >> 4),
                                            term ? K::kIdescPVLo : K::kIdescPV, ((flags & kFirst) && ks == 0 && term == 0) ? 0u : 1u);
                         umma_commit(&bar[K::kBVEmpty + vs]);
-                        umma_commit(&bar[K::kBPEmpty + it % K::kOuts]);
+                        umma_commit(&bar[K::kBPEmpty + ((uint32_t)it & (K::kOuts - 1u))]);
                     }
                 }
                 __syncwarp();
