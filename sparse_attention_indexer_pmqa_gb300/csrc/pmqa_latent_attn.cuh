@@ -84,6 +84,8 @@ __device__ __forceinline__ Req load_req(const Args &a, int i, bool tell)
 {
     Req r;
     r.q = cache::load_request(a.c, i, tell);
+    if (tell && r.q.n > r.q.ctx)  // rows before slot 0
+        atomicOr(a.c.status, (uint32_t)PMQA_DEV_BAD_CONTEXT);
     r.U = (r.q.n + a.toks - 1) / a.toks;
     r.f = (max(r.q.ctx - r.q.n, 0) + a.toks - 1) / a.toks;
     return r;

@@ -142,13 +142,20 @@ __device__ __forceinline__ int request_from(const View &c, int i, long long r)
 
 constexpr uint32_t kNoRow = 0xFFFFFFFFu;
 
+// Whether the table has a slot; recorded where it has not.
+__device__ __forceinline__ bool has_slot(const View &c, long long slot)
+{
+    if (slot >= 0 && slot < (long long)c.P * c.W && slot <= 0x7FFFFFFFll)
+        return true;
+    atomicOr(c.status, (uint32_t)PMQA_DEV_BAD_CONTEXT);
+    return false;
+}
+
 // The pool row of a slot; kNoRow (recorded) where it has none.
 __device__ __forceinline__ uint32_t pool_row(const View &c, int req, long long slot)
 {
-    if (slot < 0 || slot >= (long long)c.P * c.W || slot > 0x7FFFFFFFll) {
-        atomicOr(c.status, (uint32_t)PMQA_DEV_BAD_CONTEXT);
+    if (!has_slot(c, slot))
         return kNoRow;
-    }
     const int b = c.page_of((int)slot), page = __ldg(c.bt + (long long)req * c.W + b);
     if (page < 0 || (long long)page >= c.nb) {
         atomicOr(c.status, (uint32_t)PMQA_DEV_BAD_BLOCK_ID);
@@ -277,6 +284,8 @@ __device__ __forceinline__ Place place_of(const View &c, const Rotary &r, int i,
     o.position = r.positions && r.dim ? __ldg(r.positions + row) : (int)slot;
     if (keys)
         o.row = pool_row(c, i, slot);
+    else
+        has_slot(c, slot);
     return o;
 }
 
