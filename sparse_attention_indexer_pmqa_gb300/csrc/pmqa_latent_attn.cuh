@@ -25,7 +25,8 @@ constexpr int kWhole = 512;     // tables of up to so many tokens: blocks are no
 //   * where a weight would pass 2^kTop, m moves up, so that this weight is 2^aim;
 //   * behind n tiles of the piece the sum is at least kEnough for each of their tokens. Where it
 //     is not, m moves down: the sum then is 2^kSlack of that, and the tile's largest weight at
-//     least 2^0, as far as it stays below 2^kTop and the sum below 2^kReach.
+//     least 2^0, as far as it stays below 2^kTop and the sum below 2^kReach (or, where that is of
+//     some of the tiles, m within kReach of the highest it was: O has to stay in fp32's range).
 // A token loses at most 2^-14 beside its own share, and so the tokens of tile n together at most
 // 2^-14 / (kEnough n) of the row's weight, 2^-14 (1 + ln n) / kEnough over all tiles: 2^-7.6 (1 + ln n).
 // (In earnest far less: the light tokens behind a heavy one are in range a tile or two later, and
@@ -493,7 +494,9 @@ __device__ __forceinline__ void ffma2_of(float &d0, float &d1, uint32_t a0, uint
 
 // -m of a row for a tile whose largest score is x (-inf: it sees none of them), where the weights
 // before it add up to l, and with its own should to `need`; stays_short: they do not.
-__device__ __forceinline__ float moved_to(float aim, float mneg, float x, float l, float need, bool &stays_short)
+// most: what -m may be at most.
+__device__ __forceinline__ float moved_to(float aim, float mneg, float x, float l, float need, bool &stays_short,
+                                          float most = INFINITY)
 {
     const float to = x + mneg > kTop ? aim - x : mneg;
     const float sum = l * ex2_approx(to - mneg) + ex2_approx(x + to);  // the factor: 0 where no score was seen before
@@ -503,7 +506,7 @@ __device__ __forceinline__ float moved_to(float aim, float mneg, float x, float 
     const float bits = __log2f(__fdividef(need, sum)), room = kTop - (x + to);
     const float light = x > -INFINITY ? -(x + to) : 0.0f;
     stays_short = room < bits;
-    return to + fminf(room, fminf(fmaxf(bits + kSlack, light), kReach - __log2f(sum)));
+    return fminf(most, to + fminf(room, fminf(fmaxf(bits + kSlack, light), kReach - __log2f(sum))));
 }
 
 // Four codes, NaN (0x7F, 0xFF) replaced by 0.

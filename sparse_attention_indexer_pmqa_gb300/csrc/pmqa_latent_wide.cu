@@ -57,7 +57,8 @@ struct Wide {
     static constexpr uint32_t kOffRange = kOffPiece + kPieces * 32;     // Range
     static constexpr uint32_t kOffRed = kOffRange + 128;                // [2][128]
     static constexpr uint32_t kOffM = kOffRed + 2 * kRows * 4;          // [128]: -m
-    static constexpr uint32_t kOffBar = kOffM + kRows * 4;
+    static constexpr uint32_t kOffLeast = kOffM + kRows * 4;            // [128]: the least -m of the block so far
+    static constexpr uint32_t kOffBar = kOffLeast + kRows * 4;
     static constexpr int kBInfo = 0;                    // [kTiles] tile described: the planner
     static constexpr int kBUsed = kBInfo + kTiles;      // [kTiles] its slot is free, its rows read: 4 producer warps
     static constexpr int kBReady = kBUsed + kTiles;     // [stages] rows landed: 128 cp.async arrivals
@@ -231,6 +232,7 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
         const uint32_t lanes = tmem + ((uint32_t)(w4 * 32) << 16);
         float *const red = reinterpret_cast<float *>(smem + K::kOffRed);  // [2][128]
         float *const shared_m = reinterpret_cast<float *>(smem + K::kOffM);  // [128]: -m
+        float *const least = reinterpret_cast<float *>(smem + K::kOffLeast);  // [128]
         // the output of tile t is done
         auto out_done = [&](int t) {
             static_assert(K::kOuts == 4, "a shift: tiles before the first have the phase before the first");
@@ -275,6 +277,8 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
                 l = 0.0f;
                 mneg = kUnseen;
                 need = 0.0f;
+                if (now == (uint32_t)wg)
+                    least[row] = kUnseen;
                 // rows that do not exist see everything: no mask for their sake
                 lim = is ? piece->last + row / a.heads : 0x7FFFFFFF;
             }
@@ -357,7 +361,8 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
                 need += kEnough * K::kTile;
                 if (x + mneg > kTop || l < need) {
                     bool is_short;
-                    const float to = moved_to(K::kAim, mneg, x, l, need, is_short);
+                    const float low = least[row], to = moved_to(K::kAim, mneg, x, l, need, is_short, low + kReach);
+                    least[row] = fminf(low, to);
                     alpha = ex2_approx(to - mneg);  // 0 where no score was seen before
                     mneg = to;
                     l *= alpha;

@@ -22,19 +22,20 @@ pytestmark = pytest.mark.gpu
 SM, QS, KS = 192 ** -0.5, 0.05, 0.03
 LIFT = 16       # rotary values that lift a token's scores
 Q_LIFT = 64.0   # the queries' there
-NATS = SM * QS * KS * LIFT * Q_LIFT  # of a token's score for a code of 1
 
 
-def problem(heads, rows, ctx, lift, sigma=1.0, seed=0):
+def problem(heads, rows, ctx, lift, sigma=1.0, seed=0, q_lift=Q_LIFT, zero=True):
     """lift: float [ctx], nats that the tokens' scores lie above the others'; light scores have a
-    standard deviation of about sigma, and values a mean of 1: what is lost does not cancel."""
+    standard deviation of about sigma, and values a mean of 1: what is lost does not cancel. zero: the
+    heavy tokens' values are 0."""
+    nats = SM * QS * KS * LIFT * q_lift  # of a token's score for a code of 1
     g = torch.Generator(device="cuda").manual_seed(seed)
     k = torch.randn((ctx, 576), generator=g, device="cuda") + 1.0
-    k[:, 512:512 + LIFT] = (lift.cuda() / NATS * KS)[:, None]
-    heavy = lift > 0
-    k[heavy.cuda(), :512] = 0.0
+    k[:, 512:512 + LIFT] = (lift.cuda() / nats * KS)[:, None]
+    if zero:
+        k[(lift > 0).cuda(), :512] = 0.0
     q = torch.randn((rows, heads, 576), generator=g, device="cuda") * (sigma * 13.86 / 560 ** 0.5)
-    q[..., 512:512 + LIFT] = Q_LIFT * QS
+    q[..., 512:512 + LIFT] = q_lift * QS
     code = [(x / s).clamp(-448, 448).to(ref.F8) for x, s in ((k, KS), (q, QS))]
     return SimpleNamespace(k=code[0], q=code[1], heads=heads, rows=rows, ctx=ctx)
 
@@ -63,10 +64,11 @@ def units(s, wide, edge):
     """Per row and tile the unit of the weights, as the power of two of its score, by the rule: a
     row's unit moves up where a weight would pass 2^8; the sum of the weights of the n tiles so far is
     to be at least 1.5 n (of 128 tokens), and where it is not the unit moves down until it is twice
-    that and the tile's largest weight 1, as far as that stays below 2^8 and the sum below 2^30. Up to
-    64 packed rows this is looked at for twice the tiles after 1, 2, 4, ... tiles and where a row's
-    unit moves up; with more for every tile, and the sums are those of every second one. s: scores
-    in powers of two [rows, tiles, tokens]; edge: a factor of the sums near 1."""
+    that and the tile's largest weight 1, as far as that stays below 2^8 and the sum below 2^30. Up to 64
+    packed rows this is looked at for twice the tiles after 1, 2, 4, ... tiles and where a row's unit
+    moves up; with more for every tile, the sums are those of every second one, and the unit stays
+    within 2^30 of the largest it was. s: scores in powers of two [rows, tiles, tokens]; edge: a
+    factor of the sums near 1."""
     rows, tiles, tokens = s.shape
     x, sums, l2 = s.amax(-1), s.exp2().sum(-1), [torch.zeros(rows, dtype=torch.float64) for _ in range(2)]
     m, out, look, aim = torch.full((rows,), -1e30, dtype=torch.float64), torch.zeros_like(x), 2, 0.0 if wide else 2.0
@@ -83,6 +85,8 @@ def units(s, wide, edge):
             need = each * nxt
             bits, room = (need / have).log2(), 8 - (x[:, t] - m)
             down = torch.minimum(torch.maximum(bits + 1, m - x[:, t]), 30 - have.log2()).minimum(room)
+            if wide and t > 0:
+                down = torch.minimum(down, m - out[:, :t].amax(-1) + 30)
             short = (have < need) & (have > 0)
             look = t + 2 if bool((short & (room < bits)).any()) else nxt
             m = torch.where(short, m - down, m)
@@ -164,6 +168,16 @@ def test_scores_that_move_along_the_context(cuda_lib, heads, rows, kind):
     g = torch.Generator(device="cuda").manual_seed(3)
     p.k[:, :512] = (torch.randn((ctx, 512), generator=g, device="cuda") + 1.0).div(KS).clamp(-448, 448).to(ref.F8)
     check(cuda_lib, p)
+
+
+@pytest.mark.parametrize("heads,rows", SHAPES)
+@pytest.mark.parametrize("nats", [70.0, 100.0, 200.0, 330.0])
+@pytest.mark.parametrize("at", [[0], [64], [70, 2000], [0, 64, 128, 1999, 2500]])
+def test_tokens_that_outweigh_the_others_by_far(cuda_lib, heads, rows, nats, at):
+    """By more than fp32's range; all weights but theirs are next to nothing."""
+    lift = torch.zeros(3000)
+    lift[at] = nats
+    check(cuda_lib, problem(heads, rows, 3000, lift, q_lift=448.0, zero=False))
 
 
 @pytest.mark.parametrize("heads,rows", [(16, 4), (8, 4), (40, 2), (128, 3)])
