@@ -730,7 +730,7 @@ size_t pmqa_latent_workspace_bytes(void);
  * most 1e20 (PMQA_ERR_UNSUPPORTED otherwise); all of them finite. A row that sees no
  * token gives out = 0 and lse = -inf; tokens behind a bad table entry are not attended
  * to. A NaN among a token's values makes the rows that see it NaN, and no other row.
- * A row whose largest score passes 2^23 ln 2 (5.8 million) in magnitude sets
+ * A row whose largest score passes about 2^23 ln 2 (5.8 million) in magnitude sets
  * PMQA_DEV_SCORE_RANGE.
  * The weights enter the products as two fp8 terms, each to 2^-8 of itself where
  * min(rows, max_rows) * heads <= 32 and to 2^-7 otherwise. What is lost of small ones

@@ -403,8 +403,6 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
                     const float to = moved_to(K::kAim, m, x, L, kEnough * kTile * (float)next_look, is_short);
                     alpha[lane] = ex2_approx(to - m);  // 0 where no score was seen before
                     mneg[lane] = to;
-                    if (to != m && fabsf(to) > kFarScore)
-                        atomicOr(a.c.status, (uint32_t)PMQA_DEV_SCORE_RANGE);
                     is_short = __any_sync(RG == 32 ? kFull : 0xFFFFu, is_short);
                     if (lane == 0)
                         *any_short = is_short;
@@ -415,7 +413,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
                 for (int h = 0; h < RG; ++h) {
                     const float f = alpha[h];
                     resc |= f != 1.0f;
-                    l[h] *= f;
+                    l[h] = finite(l[h]) * f;
                 }
                 if (resc)
                     weights();
@@ -506,11 +504,13 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
             if (s < RG && s < rows) {
                 const float L = (red[s] + red[N + s]) + (red[2 * N + s] + red[3 * N + s]);
                 if (sole) {
+                    if (too_far(mneg[s]))
+                        atomicOr(a.c.status, (uint32_t)PMQA_DEV_SCORE_RANGE);
                     if (a.lse)
                         a.lse[out_row + s] = L == 0.0f ? -INFINITY : (log2f(L) - mneg[s]) * cache::kLn2;
                 } else {
                     __stcg(a.ml + ((long long)slot * N + wg * RG + s) * 2, -mneg[s]);
-                    __stcg(a.ml + ((long long)slot * N + wg * RG + s) * 2 + 1, L);
+                    __stcg(a.ml + ((long long)slot * N + wg * RG + s) * 2 + 1, finite(L));
                 }
                 alpha[s] = L == 0.0f ? 0.0f : a.kv_scale / L;
             }
@@ -763,6 +763,8 @@ __global__ void __launch_bounds__(128) latent_join_kernel(const __grid_constant_
         b[k] = __bfloat16_as_ushort(__float2bfloat16_rn(f == 0.0f ? 0.0f : y[2 * k] * f)) |
                (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(f == 0.0f ? 0.0f : y[2 * k + 1] * f)) << 16;
     *reinterpret_cast<uint2 *>(a.out + ((long long)m.x + row) * kVDim + 4 * at) = make_uint2(b[0], b[1]);
+    if (at == 0 && too_far(-M))
+        atomicOr(a.c.status, (uint32_t)PMQA_DEV_SCORE_RANGE);
     if (a.lse && at == 0)
         a.lse[m.x + row] = L == 0.0f ? -INFINITY : (M + log2f(L)) * cache::kLn2;
 }

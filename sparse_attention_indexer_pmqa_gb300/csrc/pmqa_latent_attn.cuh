@@ -492,6 +492,14 @@ __device__ __forceinline__ void ffma2_of(float &d0, float &d1, uint32_t a0, uint
         : "r"(a0), "r"(a1), "f"(b), "f"(c0), "f"(c1));
 }
 
+// Whether m, of a row that has seen scores (-m is not kUnseen), is past where weights stay in range.
+// Judged when a row is done: an m that a later one leaves behind does no harm.
+__device__ __forceinline__ bool too_far(float mneg) { return fabsf(mneg) > kFarScore && mneg != kUnseen; }
+
+// A sum in another unit. Past kFarScore weights, and so the sum, may be infinite; a factor of 0 leaves
+// nothing of it then either (NaN stays NaN).
+__device__ __forceinline__ float finite(float l) { return l == INFINITY ? 3.402823466e38f : l; }
+
 // -m of a row for a tile whose largest score is x (-inf: it sees none of them), where the weights
 // before it add up to l, and with its own should to `need`; stays_short: they do not.
 // most: what -m may be at most.

@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
                 if (!first) {
                     const float m = shared_m[row];
                     if (m != mneg) {
-                        l *= ex2_approx(m - mneg);
+                        l = finite(l) * ex2_approx(m - mneg);
                         mneg = m;
                     }
                 }
@@ -365,9 +365,7 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
                     least[row] = fminf(low, to);
                     alpha = ex2_approx(to - mneg);  // 0 where no score was seen before
                     mneg = to;
-                    l *= alpha;
-                    if (alpha != 1.0f && fabsf(to) > kFarScore)
-                        atomicOr(a.c.status, (uint32_t)PMQA_DEV_SCORE_RANGE);
+                    l = finite(l) * alpha;
                 }
                 if (first || alpha != 1.0f)
                     shared_m[row] = mneg;
@@ -462,7 +460,7 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
             tc_fence_after_sync();
             {
                 const float m = shared_m[row];
-                red[wg * K::kRows + row] = l * ex2_approx(m - mneg);
+                red[wg * K::kRows + row] = finite(l) * ex2_approx(m - mneg);
                 mneg = m;
             }
             named_bar_sync(1, 256);
@@ -474,9 +472,12 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
             if (wg == 0 && vh == 0 && lane < rows) {
                 if (!sole) {
                     __stcg(a.ml + at * 2, -mneg);
-                    __stcg(a.ml + at * 2 + 1, L);
-                } else if (a.lse) {
-                    a.lse[piece->first + row] = L == 0.0f ? -INFINITY : (log2f(L) - mneg) * cache::kLn2;
+                    __stcg(a.ml + at * 2 + 1, finite(L));
+                } else {
+                    if (too_far(mneg))
+                        atomicOr(a.c.status, (uint32_t)PMQA_DEV_SCORE_RANGE);
+                    if (a.lse)
+                        a.lse[piece->first + row] = L == 0.0f ? -INFINITY : (log2f(L) - mneg) * cache::kLn2;
                 }
             }
             const float f = L == 0.0f ? 0.0f : a.kv_scale / L;

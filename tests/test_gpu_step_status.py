@@ -1,4 +1,5 @@
-"""What the calls around the sparse-MLA step record in the status word: rows without a slot."""
+"""What the calls around the sparse-MLA step record in the status word: rows without a slot, and
+scores out of range where they are a row's largest."""
 
 import math
 
@@ -51,3 +52,40 @@ def test_appends_without_keys_report_rows_without_a_slot(cuda_lib, rows, ctx):
         for x in (q8, q16):
             assert bool((x[:rows] != 7).flatten(1).any(1).all()) and bool((x[rows:] == 7).all())
     assert not bool(kv.any()) and not bool(lat.any())
+
+
+@pytest.mark.parametrize("heads", [1, 16, 24, 64, 128])
+@pytest.mark.parametrize("ctx,block", [(500, 4), (3000, 64)])
+@pytest.mark.parametrize("factor", [10.0, 1e6, -1e12])
+@pytest.mark.parametrize("where", ["first", "last", "some", "but one", "none", "all"])
+def test_far_scores_are_reported_where_they_are_the_largest(cuda_lib, heads, ctx, block, factor, where):
+    """Scores from -3.2e6 factor to -2.3e6 factor (in powers of two) beside scores of 0: these alone have
+    weight, all the same. With one range for a context and many."""
+    lib = cuda_lib
+    p = ref.attention_problem([2], [ctx], heads, block, seed=6)
+    t = torch.arange(ctx)
+    far = dict(first=t < 256, last=t >= ctx - 200, some=t % 37 < 5, none=t < 0, all=t >= 0)
+    far["but one"] = t != 131
+    far = far[where]
+    p.q[:] = 0
+    p.q.view(ref.F8)[..., 512:528] = 448.0
+    k = ref.value(p.kv.reshape(-1, 576)).float().clamp(-2, 2)
+    k[:, 512:] = 0.0
+    at = ref.places(p, 0, 0, ctx)
+    k[at[far], 512:528] = (-math.copysign(1.0, factor) * (448.0 - 32.0 * (t[far] % 5).float()))[:, None]
+    p.kv = k.to(ref.F8).view(torch.uint8).reshape(p.kv.shape)
+    p.q_scale, p.kv_scale, p.sm = 1.0, 1.0, factor / math.log2(math.e)
+    out, lse, status = run(lib, p)
+    if where == "all":
+        assert status == lib.PMQA_DEV_SCORE_RANGE
+        return
+    assert status == 0
+    for j in range(2):
+        light = ~far & (t <= ctx - 2 + j)
+        v = ref.value(p.kv.reshape(-1, 576))[at[light], :512]
+        mean, size = v.mean(0), v.abs().mean(0)
+        # a weight's two terms and f16, sums in fp32; one rounding
+        tol = size * (2.0 ** -7 + 2.0 ** -11 + 2.0 ** -17)
+        tol = tol + (mean.abs() + tol) * 2.0 ** -8
+        assert bool(((out[j].double() - mean).abs() <= tol).all())
+        assert bool(((lse[j].double() - math.log(int(light.sum()))).abs() <= 2.0 ** -17).all())
