@@ -567,7 +567,7 @@ typedef struct pmqa_rotary {
  *   PMQA_ROPE_PARTS   divided where a pair turns fewer than slow_turns times over the
  *                     trained positions, kept where more than fast_turns times, and
  *                     between the two weighted linearly in i (the ends rounded
- *                     outwards to whole i); scale 0.1 ln(factor) + 1
+ *                     outwards to whole i, within 0 to dim - 1); scale 0.1 ln(factor) + 1
  * A host function: no device work. dim even and positive, base > 1; for PARTS
  * trained >= 1 and 0 < slow_turns < fast_turns.
  */

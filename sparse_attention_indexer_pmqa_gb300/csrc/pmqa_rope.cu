@@ -270,7 +270,7 @@ extern "C" int pmqa_rope_frequencies(int32_t dim, double base, int kind, double 
         if (kind == PMQA_ROPE_LINEAR)
             slowed = 1.0;
         else if (kind == PMQA_ROPE_PARTS)
-            slowed = std::min(1.0, std::max(0.0, (i - lo) / std::max(hi - lo, 0.001)));
+            slowed = i >= hi ? 1.0 : i <= lo ? 0.0 : (i - lo) / (hi - lo);
         inv_freq[i] = kind == PMQA_ROPE_PLAIN ? f : f * (1.0 - slowed) + f / factor * slowed;
     }
     *scale = kind == PMQA_ROPE_PARTS ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
