@@ -96,7 +96,6 @@ struct Cfg {
     static constexpr int kBPEmpty = kBPFull + 2;            // [2] P read: MMA commit
     static constexpr int kBQEmpty = kBPEmpty + 2;           // queries read: MMA commit
     static constexpr int kBDrain = kBQEmpty + 1;
-    static constexpr int kBRead = -1;                       // every softmax warp works on every tile
     static constexpr int kBars = kBDrain + 1;
     static constexpr uint32_t kOffMisc = kOffBar + kBars * 8;
     static constexpr uint32_t kSmem = kOffMisc + 16;

@@ -334,11 +334,10 @@ static_assert(sizeof(Tile) == 32 && sizeof(Piece) == 32, "places in shared memor
 
 // The planner's warp. A lane looks up tokens lane, lane + 32, ... of a tile, whose
 // table entries were asked for a tile earlier. A tile is described once the producers
-// took the tile kAhead before it, and with it the slot of the tile kTiles before it: so
-// the values of that one, whose place the description takes, have been read, and the roles
-// that work on it have read its description. Softmax warps that only look at it say so
-// (kBRead; none where it is negative). (A piece's place: kPieces > kTiles + 1 pieces
-// later, when the output of the piece there is out.)
+// took the tile kAhead before it, and with it the slot of the tile kStages before that: so
+// the values of that one, whose place the description takes (or of the next one after it, where
+// kTiles is larger), have been read, and its description by all that work on it. (A piece's
+// place: kPieces > kTiles + 1 pieces later, when the output of the piece there is out.)
 template <class K>
 __device__ __forceinline__ void plan_tiles(const Args &a, uint8_t *smem, uint64_t *bar, const Range *range, int g,
                                            bool joins, volatile int *abort_flag)
@@ -386,13 +385,6 @@ __device__ __forceinline__ void plan_tiles(const Args &a, uint8_t *smem, uint64_
         if (it >= K::kAhead) {
             const int j = it - K::kAhead;
             if (!__all_sync(kFull, wait_for(&bar[K::kBUsed + j % K::kTiles], (uint32_t)(j / K::kTiles) & 1u, abort_flag))) {
-                fail(a, abort_flag);
-                break;
-            }
-        }
-        if constexpr (K::kBRead >= 0) {
-            if (it >= K::kTiles &&
-                !__all_sync(kFull, wait_for(&bar[K::kBRead + e], (uint32_t)(it / K::kTiles - 1) & 1u, abort_flag))) {
                 fail(a, abort_flag);
                 break;
             }

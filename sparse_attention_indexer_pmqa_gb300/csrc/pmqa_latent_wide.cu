@@ -32,7 +32,10 @@ struct Wide {
     static constexpr int kTile = 64;                      // tokens per tile
     static constexpr int kStages = 5;                     // slots of a tile's rows
     static constexpr int kAhead = 2;                      // tiles that the planner is ahead of the producers
-    static constexpr int kTiles = kStages + kAhead, kPieces = 10;
+    // A tile's description is read by both softmax groups, but its output waits for the one that
+    // works on it: the other has read it when the next tile's output, which is its own, is done.
+    static constexpr int kSpare = 1;
+    static constexpr int kTiles = kStages + kAhead + kSpare, kPieces = 10;
     // The output of tile t waits for the scores of t + 2. Those of t + 6 need the slot of
     // tile t + 1 and so this wait's end: with four barriers no phase is passed over (two
     // could be, by the scores of t + 4: they need the slot of t - 1 alone).
@@ -71,8 +74,7 @@ struct Wide {
     static constexpr int kBM = kBPEmpty + kOuts;        // [2] m published: 4 softmax warps
     static constexpr int kBQFull = kBM + 2;             // a block's queries in tensor memory: 8 softmax warps
     static constexpr int kBTurn = kBQFull + 1;          // [kTurns] scores issued: the scores' warp
-    static constexpr int kBRead = kBTurn + kTurns;      // [kTiles] description read by the softmax group of the other tiles: 4 warps
-    static constexpr int kBDrain = kBRead + kTiles;
+    static constexpr int kBDrain = kBTurn + kTurns;
     static constexpr int kBars = kBDrain + 2;           // both product warps
     static constexpr uint32_t kOffMisc = kOffBar + kBars * 8;
     static constexpr uint32_t kSmem = kOffMisc + 16;
@@ -144,7 +146,6 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
         for (int s = 0; s < K::kTiles; ++s) {
             mbar_init(&bar[K::kBInfo + s], 1);
             mbar_init(&bar[K::kBUsed + s], 4);
-            mbar_init(&bar[K::kBRead + s], 4);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bar[K::kBSFull + s], 1);
@@ -435,12 +436,6 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) latent_wide_kernel(const __
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(&bar[K::kBPFull + now]);
-            }
-            if (now != (uint32_t)wg) {
-                // all that this group reads of the other's tile
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&bar[K::kBRead + e]);
             }
             if (++vs == K::kStages)
                 vs = 0;

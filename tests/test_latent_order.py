@@ -26,10 +26,9 @@ def number(name, default=None):
 
 
 STAGES, AHEAD = number("kStages"), number("kAhead")
-TILES = STAGES + AHEAD
+TILES = STAGES + AHEAD + number("kSpare", 0)
 TURNS = number("kTurns", 2)     # barriers of "scores issued"
 OUTS = number("kOuts", 2)       # of "output done"
-READ = re.search(r"mbar_arrive\(&bar\[K::kBRead", source("pmqa_latent_wide.cu")) is not None
 
 
 class Order:
@@ -102,7 +101,7 @@ class Order:
         return past
 
 
-COUNTS = dict(info=1, used=4, ready=4, vempty=1, sfull=1, sfree=4, pfull=4, pempty=1, m=4, qfull=8, turn=1, exit=8, seen=4)
+COUNTS = dict(info=1, used=4, ready=4, vempty=1, sfull=1, sfree=4, pfull=4, pempty=1, m=4, qfull=8, turn=1, exit=8)
 
 
 def of(name, ring, tile):
@@ -121,8 +120,6 @@ def wide(pieces, moved=None):
         # the planner
         if it >= AHEAD:
             o.wait("plan", *of("used", TILES, it - AHEAD))
-        if READ:
-            o.wait("plan", *of("seen", TILES, it - TILES))
         o.event("plan", ("write", it))
         o.arrive("plan", *of("info", TILES, it))
         # the producers
@@ -152,8 +149,6 @@ def wide(pieces, moved=None):
                 if moved == (w, it) and not first:
                     o.wait(me, *of("pempty", OUTS, it - 1))
                 o.arrive(me, *of("pfull", 2, it))
-            elif READ:
-                o.arrive(me, *of("seen", TILES, it))
             if last:
                 if it > 0:
                     o.wait(me, *of("pempty", OUTS, it - 1))
