@@ -13,8 +13,9 @@
 //     K = 576) into TMEM;
 //   * the softmax threads, one per token and 16 or 32 packed rows, form p = 2^(x - m)
 //     with an m for each row that moves when a weight passes 2^8, or when the row's sum (looked
-//     at after 1, 2, 4, ... tiles, and whenever an m moves) is too small for the terms' steps, and write
-//     p as two 8-bit terms, p_hi = e4m3(p) and p_lo, the remainder;
+//     at before tiles 2, 4, 8, ... for those up to the next of them, and where an m moves) is too
+//     small for the terms' steps, and write p as two 8-bit terms, p_hi = e4m3(p) and p_lo, the
+//     remainder;
 //   * the thread issues O^T += V^T P^T (M = 128 value columns, four blocks, K = 128
 //     tokens) from the SAME tile as an MN-major operand. With N = 64 both terms add
 //     into one accumulator (576 + 2 * 512 fp8 multiplications a row and token; p_lo is
@@ -57,7 +58,7 @@ struct Cfg {
     static constexpr int kMmaWarp = 4 + 4 * kGroups, kPlanWarp = kMmaWarp + 1;
     static constexpr int kTerms = N == 64 ? 1 : 2;        // accumulators of a value block
     static constexpr int kOCols = kTerms * N;             // its output columns
-    static constexpr float kAim = 2.0f;                   // first sums reach to the second tile
+    static constexpr float kAim = 1.0f;                   // a weight that moves m up (verify of 64 rows 185 us, at 2 188)
     static constexpr float kLo = N == 64 ? 1.0f : 16.0f;  // p_lo holds kLo (p - p_hi)
     // P: a row of 64 bytes per token, two terms of N rows. N = 64: a buffer of 128 rows for
     // each term; N = 16: both stages share a row, 32 bytes each.
@@ -82,8 +83,8 @@ struct Cfg {
     static constexpr uint32_t kOffLim = kOffRange + 128;                // [N] ints
     static constexpr uint32_t kOffM = kOffLim + N * 4;                  // [N] floats: -m       
     static constexpr uint32_t kOffAlpha = kOffM + N * 4;                // [N]
-    static constexpr uint32_t kOffRed = kOffAlpha + N * 4;              // [4][N] twice
-    static constexpr uint32_t kOffShort = kOffRed + 8 * N * 4;          // [kGroups]
+    static constexpr uint32_t kOffRed = kOffAlpha + N * 4;              // [4][N]
+    static constexpr uint32_t kOffShort = kOffRed + 4 * N * 4;          // [kGroups]
     static constexpr uint32_t kOffBar = kOffShort + 8;
     static constexpr int kBInfo = 0;                        // [kTiles] tile described: the planner
     static constexpr int kBUsed = kBInfo + kTiles;          // [kTiles] its slot is free, its rows read: 4 producer warps
@@ -277,7 +278,6 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
         float *const mneg = reinterpret_cast<float *>(smem + K::kOffM) + wg * RG;
         float *const alpha = reinterpret_cast<float *>(smem + K::kOffAlpha) + wg * RG;
         float *const red = reinterpret_cast<float *>(smem + K::kOffRed) + wg * RG;  // [4][N]
-        float *const red_l = red + 4 * N;
         uint32_t *const any_short = reinterpret_cast<uint32_t *>(smem + K::kOffShort) + wg;
         int *const lims = reinterpret_cast<int *>(smem + K::kOffLim) + wg * RG;
         float l[RG];
@@ -371,51 +371,67 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
             if (ok) {
                 tc_fence_after_sync();
                 load_scores();
-                over = weights() || tiles == look;
+                over = weights();
             }
             bool resc = false;
-            if (named_bar_or(barrier, 128, over)) {
-                if (ok) {
+            over = named_bar_or(barrier, 128, over);
+            const bool due = tiles == look;
+            if (over || due) {
+                // the rows' sums; most often that is all there is to a look
+                if (ok && tiles > 1) {
+                    float v[RG];
+#pragma unroll
+                    for (int h = 0; h < RG; ++h)
+                        v[h] = l[h];
+                    red[w4 * N + (RG == 32 ? lane : lane >> 1)] = reduce_scatter<false, RG>(v, lane);
+                }
+                if (!named_bar_and(barrier, 128, ok)) {
+                    fail(a, abort_flag);
+                    break;
+                }
+                if (due)
+                    look = 2 * tiles;
+                const float need = kEnough * kTile * (float)(look - 1);
+                float L = 0.0f;
+                if (w4 == 0 && lane < RG) {
+                    if (tiles > 1)
+                        L = (red[lane] + red[N + lane]) + (red[2 * N + lane] + red[3 * N + lane]);
+                    const bool is_short = __any_sync(RG == 32 ? kFull : 0xFFFFu, L < need);
+                    if (lane == 0)
+                        *any_short = is_short;
+                }
+                named_bar_sync(barrier, 128);
+                if (over || *any_short) {
                     load_scores();
                     float v[RG];
 #pragma unroll
                     for (int h = 0; h < RG; ++h)
                         v[h] = __uint_as_float(sr[h]) * a.c_log2;
                     red[w4 * N + (RG == 32 ? lane : lane >> 1)] = reduce_scatter<true, RG>(v, lane);
-                    if (tiles > 1) {
-#pragma unroll
-                        for (int h = 0; h < RG; ++h)
-                            v[h] = l[h];
-                        red_l[w4 * N + (RG == 32 ? lane : lane >> 1)] = reduce_scatter<false, RG>(v, lane);
+                    named_bar_sync(barrier, 128);
+                    if (w4 == 0 && lane < RG) {
+                        const float x = fmaxf(fmaxf(red[lane], red[N + lane]), fmaxf(red[2 * N + lane], red[3 * N + lane]));
+                        const float m = mneg[lane];
+                        bool is_short;
+                        const float to = moved_to(K::kAim, m, x, L, need, is_short);
+                        alpha[lane] = ex2_approx(to - m);  // 0 where no score was seen before
+                        mneg[lane] = to;
+                        is_short = __any_sync(RG == 32 ? kFull : 0xFFFFu, is_short);
+                        if (lane == 0)
+                            *any_short = is_short;
                     }
-                }
-                if (!named_bar_and(barrier, 128, ok)) {
-                    fail(a, abort_flag);
-                    break;
-                }
-                const int next_look = tiles == look ? 2 * tiles : look;
-                if (w4 == 0 && lane < RG) {
-                    const float x = fmaxf(fmaxf(red[lane], red[N + lane]), fmaxf(red[2 * N + lane], red[3 * N + lane]));
-                    const float L = tiles == 1 ? 0.0f : (red_l[lane] + red_l[N + lane]) + (red_l[2 * N + lane] + red_l[3 * N + lane]);
-                    const float m = mneg[lane];
-                    bool is_short;
-                    const float to = moved_to(K::kAim, m, x, L, kEnough * kTile * (float)next_look, is_short);
-                    alpha[lane] = ex2_approx(to - m);  // 0 where no score was seen before
-                    mneg[lane] = to;
-                    is_short = __any_sync(RG == 32 ? kFull : 0xFFFFu, is_short);
-                    if (lane == 0)
-                        *any_short = is_short;
-                }
-                named_bar_sync(barrier, 128);
-                look = *any_short ? tiles + 1 : next_look;
+                    named_bar_sync(barrier, 128);
+                    if (*any_short)
+                        look = tiles + 1;
 #pragma unroll
-                for (int h = 0; h < RG; ++h) {
-                    const float f = alpha[h];
-                    resc |= f != 1.0f;
-                    l[h] = finite(l[h]) * f;
+                    for (int h = 0; h < RG; ++h) {
+                        const float f = alpha[h];
+                        resc |= f != 1.0f;
+                        l[h] = finite(l[h]) * f;
+                    }
+                    if (resc)
+                        weights();
                 }
-                if (resc)
-                    weights();
             }
             tc_fence_before_sync();
             __syncwarp();

@@ -65,13 +65,13 @@ def units(s, wide, edge):
     row's unit moves up where a weight would pass 2^8; the sum of the weights of the n tiles so far is
     to be at least 1.5 n (of 128 tokens), and where it is not the unit moves down until it is twice
     that and the tile's largest weight 1, as far as that stays below 2^8 and the sum below 2^30. Up to 64
-    packed rows this is looked at for twice the tiles after 1, 2, 4, ... tiles and where a row's unit
-    moves up; with more for every tile, the sums are those of every second one, and the unit stays
+    packed rows this is looked at before tiles 2, 4, 8, ..., for all up to the next of them, and where a
+    row's unit moves up; with more for every tile, the sums are those of every second one, and the unit stays
     within 2^30 of the largest it was. s: scores in powers of two [rows, tiles, tokens]; edge: a
     factor of the sums near 1."""
     rows, tiles, tokens = s.shape
     x, sums, l2 = s.amax(-1), s.exp2().sum(-1), [torch.zeros(rows, dtype=torch.float64) for _ in range(2)]
-    m, out, look, aim = torch.full((rows,), -1e30, dtype=torch.float64), torch.zeros_like(x), 2, 0.0 if wide else 2.0
+    m, out, look, aim = torch.full((rows,), -1e30, dtype=torch.float64), torch.zeros_like(x), 2, 0.0 if wide else 1.0
     each = 1.5 * tokens / 128 * edge
     for t in range(tiles):
         g = t % 2 if wide else 0
@@ -79,10 +79,10 @@ def units(s, wide, edge):
         up = x[:, t] - m > 8
         at = t + 1 == look
         if wide or at or bool(up.any()):
-            nxt = n if wide else 2 * n if at else look
+            nxt = n + 1 if wide else 2 * n if at else look
             m = torch.where(up, x[:, t] - aim, m)
             have = l2[g] * (-m).exp2() + (x[:, t] - m).exp2()
-            need = each * nxt
+            need = each * (nxt - 1)
             bits, room = (need / have).log2(), 8 - (x[:, t] - m)
             down = torch.minimum(torch.maximum(bits + 1, m - x[:, t]), 30 - have.log2()).minimum(room)
             if wide and t > 0:
