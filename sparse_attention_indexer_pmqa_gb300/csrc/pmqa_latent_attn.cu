@@ -730,8 +730,8 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) latent_attn_kernel(const 
 // that range g begins and later ranges go on with; a thread four columns. Bound by the
 // latency of a chain of loads (what there is, the parts), about 5 us behind 32 contexts: each
 // step rescales what the steps before gave, so that maxima and values are loaded
-// together (looking the request up and reading the maxima first: batch decode by graph 230 us,
-// now 220 to 226, verify 180 and 178). Two or four rows to a block, or a warp a row: equal.
+// together (looking the request up and reading the maxima first: batch decode 6 us more by graph,
+// verify 2). Two or four rows to a block, or a warp a row: equal.
 __global__ void __launch_bounds__(128) latent_join_kernel(const __grid_constant__ Args a)
 {
     griddep_wait();
@@ -790,7 +790,7 @@ cudaError_t launch(Args &a, int sms, cudaStream_t st)
     a.tile = kTile;
     a.N = N;
     a.pad = 2;
-    a.least = 1;  // 500 tokens of one row: 12.8 us by graph, 13.8 with 2
+    a.least = 1;  // 500 tokens of one row by graph: 1 us less than with 2
     a.toks = 1;
     while (2 * a.toks * a.heads <= N)
         a.toks *= 2;

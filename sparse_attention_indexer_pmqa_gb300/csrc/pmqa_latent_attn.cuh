@@ -18,10 +18,9 @@ constexpr int kMaxHeads = 128;
 constexpr int kMaxCtas = 160;   // workspace parts: 2 per CTA, 64 rows of 512 columns or 128 of 256
 constexpr int kNoPage = (int)0x80000000;  // no token there (a table entry is negative where it is bad)
 constexpr int kWhole = 512;     // tables of up to so many tokens: blocks are not cut
-// p = 2^(x - m), and a weight's terms have steps of 2^-13 at least: below 2^-14 a weight is lost. So
-// a row's m is not its largest score (32 k light tokens behind a heavy one with 80 % of the weight
-// lost 92 % of what they add with up to 32 packed rows, 20 % with more), but moves with the sum of
-// its weights, up and down:
+// p = 2^(x - m), and a weight's terms are off by up to 2^-14 however small it is. So
+// a row's m is not its largest score (32 k light tokens behind a heavy one with about 80 % of the weight
+// then lose 90 % of what they add), but moves with the sum of its weights, up and down:
 //   * where a weight would pass 2^kTop, m moves up, so that this weight is 2^aim;
 //   * behind n tiles of the piece the sum is at least kEnough for each of their tokens. Where it
 //     is not, m moves down: the sum then is 2^kSlack of that, and the tile's largest weight at
@@ -31,9 +30,9 @@ constexpr int kWhole = 512;     // tables of up to so many tokens: blocks are no
 // 2^-14 / (kEnough n) of the row's weight, 2^-14 (1 + ln n) / kEnough over all tiles: 2^-7.6 (1 + ln n).
 // (In earnest far less: the light tokens behind a heavy one are in range a tile or two later, and
 // their output is within 1 % from 8 k to 128 k of them.) The price is the moves. Scores with a standard
-// deviation of 2.2: batch decode of 128 heads 243 us, verify of 64 packed rows 191, prompt chunks 1905 (242, 182
-// and 1820 with m at the largest score); with four times the sum 265, 209 and 2103; m moved down wherever a
-// tile's largest weight is below 2, a third more time. Standard deviation 4.4: 298, 234 and 2339.
+// deviation of 2.2, by graph: batch decode of 128 heads 239 us, verify of 64 packed rows 186, prompt chunks
+// 1850 (3, 5 and 3 % less with m at the largest score); with four times the sum 265, 209 and 2103; m moved
+// down wherever a tile's largest weight is below 2, a third more time. Standard deviation 4.4: 297, 230, 2339.
 constexpr float kTop = 8.0f, kSlack = 1.0f, kReach = 30.0f;
 constexpr float kEnough = 1.5f / 128.0f;
 constexpr float kUnseen = 1e30f;   // -m of a row that has seen no score: above every |x|
@@ -456,7 +455,7 @@ __device__ __forceinline__ uint32_t e5m2x2_of_f16x2(uint32_t h2)
 // by 2^-11 at most, its difference from the first term exact: at most 2^-4 p, or 2^-10 below
 // p = 2^-6. SAME: both terms go into one accumulator, so the second has the first's unit:
 // e5m2, which reaches down to 2^-17 and leaves 2^-7 p or 2^-13. Otherwise it is e4m3 of 16
-// times the difference, which leaves 2^-8 p or 2^-14 (p of the row's largest weight >= 1).
+// times the difference, which leaves 2^-8 p or 2^-14.
 template <bool SAME>
 __device__ __forceinline__ void split2(uint32_t p, uint32_t &hi, uint32_t &lo)
 {

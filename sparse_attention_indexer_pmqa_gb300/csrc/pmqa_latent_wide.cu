@@ -24,8 +24,8 @@ namespace pmqa {
 namespace latent {
 
 // The block of the scores' products behind which the output update may be issued: its
-// warp wakes and issues in 200 cycles, about the time until the scores are done (none before: 261 us
-// for batch decode, after block 1 258, 2 and 3 253; prompt chunks 1878 after 2, 1848 after 3).
+// warp wakes and issues in 200 cycles, about the time until the scores are done (by graph batch
+// decode 246 us after block 2, 239 after 3, prompt chunks 1943 and 1888).
 constexpr int kTurnAt = 3;
 
 struct Wide {
