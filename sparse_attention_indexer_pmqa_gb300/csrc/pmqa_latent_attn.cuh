@@ -484,7 +484,7 @@ __device__ __forceinline__ void ffma2_of(float &d0, float &d1, uint32_t a0, uint
 }
 
 // Whether m, of a row that has seen scores (-m is not kUnseen), is past where weights stay in range.
-// Judged when a row is done: an m that a later one leaves behind does no harm.
+// Decided when a row is done: an m that a later one leaves behind does no harm.
 __device__ __forceinline__ bool too_far(float mneg) { return fabsf(mneg) > kFarScore && mneg != kUnseen; }
 
 // A sum in another unit. Past kFarScore weights, and so the sum, may be infinite; a factor of 0 leaves

@@ -1,5 +1,5 @@
-"""The order of the wide latent attention kernel's roles, as a graph of what comes before
-what (CPU only; the numbers of barriers are read from the kernel's source).
+"""The order of the latent attention kernels' roles, as a graph of what comes before what (CPU
+only; the numbers of the wide kernel's barriers are read from its source).
 
 A wait on an mbarrier names a phase by its parity alone. So for a wait on phase k, phase
 k - 1 has to be complete before the wait begins, and phase k + 1 must not complete before
@@ -29,6 +29,7 @@ STAGES, AHEAD = number("kStages"), number("kAhead")
 TILES = STAGES + AHEAD + number("kSpare", 0)
 TURNS = number("kTurns", 2)     # barriers of "scores issued"
 OUTS = number("kOuts", 2)       # of "output done"
+PIECES_KEPT = number("kPieces")
 
 
 class Order:
@@ -121,6 +122,8 @@ def wide(pieces, moved=None):
         if it >= AHEAD:
             o.wait("plan", *of("used", TILES, it - AHEAD))
         o.event("plan", ("write", it))
+        if first:
+            o.event("plan", ("piece", seg))
         o.arrive("plan", *of("info", TILES, it))
         # the producers
         for w in range(4):
@@ -137,6 +140,7 @@ def wide(pieces, moved=None):
             o.wait(me, *of("info", TILES, it))
             o.event(me, ("read", it))
             if first:
+                o.event(me, ("piece read", seg))
                 o.arrive(me, ("qfull", 0), seg)
             if own:
                 if not first:
@@ -156,6 +160,7 @@ def wide(pieces, moved=None):
                 for k in range(2):
                     o.arrive(me, ("exit", 0), 2 * seg + k)
                     o.wait(me, ("exit", 0), 2 * seg + k)
+                o.event(me, ("piece read", seg))
         # the scores
         o.wait("scores", *of("info", TILES, it))
         o.event("scores", ("read", it))
@@ -178,7 +183,67 @@ def wide(pieces, moved=None):
     return o
 
 
-PIECES = [[20], [1] * 12, [2] * 8, [3] * 6, [1, 9, 2, 7, 1, 1, 3], [5, 6, 4, 5]]
+def narrow(pieces, stages, ahead, groups, moved=None):
+    """The same of the kernel for up to 64 packed rows, each softmax group on every tile. Scores and
+    outputs are issued by one warp in either order: here by two, which is less."""
+    o = Order()
+    place = [(t, n) for n in pieces for t in range(n)]
+    ring, seg = stages + ahead, -1
+    for it, (t, n) in enumerate(place):
+        first, last = t == 0, t == n - 1
+        seg += first
+        if it >= ahead:
+            o.wait("plan", *of("used", ring, it - ahead))
+        o.event("plan", ("write", it))
+        if first:
+            o.event("plan", ("piece", seg))
+        o.arrive("plan", *of("info", ring, it))
+        for w in range(4):
+            me = "copy", w
+            o.wait(me, *of("info", ring, it))
+            o.event(me, ("read", it))
+            o.event(me, ("rows", it))
+            if first:
+                o.wait(me, ("qempty", 0), seg - 1)
+                o.event(me, ("piece read", seg))
+            o.wait(me, *of("vempty", stages, it - stages))
+            o.wait(me, *of("rempty", 2, it - 2))
+            o.arrive(me, *of("used", ring, it))
+            o.arrive(None, *of("ready", stages, it), after=[o.event(me)])
+        for w in range(4 * groups):
+            me = "soft", w
+            o.wait(me, *of("info", ring, it))
+            o.event(me, ("read", it))
+            o.wait(me, *of("sfull", 2, it))
+            o.wait(me, *of("pempty", 2, it - 2))
+            o.arrive(me, ("group", w // 4), it)
+            o.wait(me, ("group", w // 4), it)
+            o.arrive(me, *of("sfree", 2, it))
+            if moved == (w, it) and not first:
+                o.wait(me, *of("pempty", 2, it - 1))
+            o.event(me, ("read", it))
+            o.arrive(me, *of("pfull", 2, it))
+            if last:
+                o.wait(me, *of("pempty", 2, it))
+                o.event(me, ("piece read", seg))
+        o.wait("scores", *of("ready", stages, it))
+        o.wait("scores", *of("info", ring, it))
+        o.wait("scores", *of("sfree", 2, it - 2))
+        o.event("scores", ("read", it))
+        issued = o.event("scores")
+        for name in ("sfull", "rempty"):
+            o.arrive(None, *of(name, 2, it), after=[issued])
+        if last:
+            o.arrive(None, ("qempty", 0), seg, after=[issued])
+        o.wait("out", *of("pfull", 2, it))
+        o.event("out", ("read", it))
+        issued = o.event("out", after=[issued])
+        o.arrive(None, *of("vempty", stages, it), after=[issued])
+        o.arrive(None, *of("pempty", 2, it), after=[issued])
+    return o
+
+
+PIECES = [[20], [1] * 24, [2] * 8, [3] * 6, [1, 9, 2, 7, 1, 1, 3], [5, 6, 4, 5]]
 
 
 @pytest.mark.parametrize("pieces", PIECES)
@@ -207,3 +272,29 @@ def test_descriptions_are_read_before_their_place_is_used_again(pieces):
         for name, ring in (("read", TILES), ("rows", AHEAD)):
             for written in o.names.get(("write", it + ring), []):
                 assert all(past[written] >> e & 1 for e in o.names[name, it]), (name, it)
+
+
+@pytest.mark.parametrize("pieces", PIECES)
+def test_pieces_are_read_before_their_place_is_used_again(pieces):
+    o = wide(pieces)
+    _, past = o.close(COUNTS)
+    for seg in range(len(pieces)):
+        for written in o.names.get(("piece", seg + PIECES_KEPT), []):
+            assert all(past[written] >> e & 1 for e in o.names["piece read", seg]), seg
+
+
+@pytest.mark.parametrize("stages,ahead,groups,kept", [(3, 1, 1, 8), (2, 2, 2, 8)])
+@pytest.mark.parametrize("pieces", PIECES)
+def test_the_kernel_of_few_rows(pieces, stages, ahead, groups, kept):
+    counts = dict(COUNTS, sfree=4 * groups, pfull=4 * groups, group=4, qempty=1, rempty=1)
+    for it in range(sum(pieces)):
+        narrow(pieces, stages, ahead, groups, (it % (4 * groups), it)).check(counts)
+    o = narrow(pieces, stages, ahead, groups)
+    past = o.check(counts)
+    for it in range(sum(pieces)):
+        for name, ring in (("read", stages + ahead), ("rows", ahead)):
+            for written in o.names.get(("write", it + ring), []):
+                assert all(past[written] >> e & 1 for e in o.names[name, it]), (name, it)
+    for seg in range(len(pieces)):
+        for written in o.names.get(("piece", seg + kept), []):
+            assert all(past[written] >> e & 1 for e in o.names["piece read", seg]), seg
